@@ -123,6 +123,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.la_fwd_kernel_name.argtypes = [cp]
         lib.la_bwd_kernel_name.restype = ctypes.c_char_p
         lib.la_bwd_kernel_name.argtypes = [cp]
+        layers.declare(lib)
         _lib = lib
     return _lib
 
@@ -456,3 +457,10 @@ def la_status_string(status: int) -> str:
 
 def la_last_error() -> str:
     return load_library().la_last_error().decode()
+
+
+from . import layers  # noqa: E402  (the binding of the layer operators uses the helpers above)
+from .layers import (LA_ACT_NONE, LA_ACT_SILU, ConvConfig, NormConfig, ScanConfig, la_conv_bwd,  # noqa: E402,F401
+                     la_conv_bwd_workspace_bytes, la_conv_fwd, la_conv_step, la_norm_bwd, la_norm_bwd_workspace_bytes,
+                     la_norm_fwd, la_scan_bwd, la_scan_bwd_workspace_bytes, la_scan_fwd, la_scan_step,
+                     la_scan_workspace_bytes)

@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "la_internal.hpp"
+#include "la_layer.hpp"
 
 namespace {
 
@@ -170,6 +171,10 @@ la_status check_kernel(const la_config& c) {
 }
 
 }  // namespace
+
+namespace la {
+la_status report(la_status s, const char* detail) { return s == LA_OK ? ok() : fail(s, "%s", detail); }
+}  // namespace la
 
 extern "C" {
 

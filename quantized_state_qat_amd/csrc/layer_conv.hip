@@ -1,0 +1,466 @@
+// Depthwise causal convolution of width 2..4 with optional SiLU: forward, backward, one token.
+//
+// pre[t] = bias + sum_j w[j] z[t + j] over the rows z = state0 ++ x of a sequence.  A few
+// multiplies and one exponential an element: memory bound.  A lane owns 16 bytes of channels
+// (8 bf16, 4 fp32) and walks a few consecutive tokens with the window in registers, so each
+// row is read once (plus W - 1 rows at the walk's start, which its neighbour has just read);
+// the weights stay in registers.
+#include "la_layer.hpp"
+
+namespace la {
+namespace {
+
+// The channels' weights of one lane, widened.
+template <int E, int W>
+struct Taps {
+    float w[W][E];
+    float bias[E];
+    __device__ __forceinline__ void load(const void* wp, const void* bp, int dtype, int c0) {
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+#pragma unroll
+            for (int j = 0; j < W; j++) w[j][e] = load_elem(wp, static_cast<size_t>(c0 + e) * W + j, dtype);
+            bias[e] = bp ? load_elem(bp, c0 + e, dtype) : 0.0f;
+        }
+    }
+};
+
+template <class T>
+struct ConvGeom {
+    int B, T_, C, ldx, ldy, w_dtype, per, blocks;  // per: tokens a lane walks; blocks: token blocks per sequence
+    const int32_t* cu;
+};
+
+// Row `pos` (>= -(W-1)) of sequence b, from x or from the state before it.
+template <class T, int W>
+__device__ __forceinline__ uv4 conv_row(const T* x, const T* s0, int64_t begin, int pos, int b, int C, int ldx, int c0) {
+    if (pos >= 0) return load16(x + (begin + pos) * ldx + c0);
+    if (!s0) return uv4{0, 0, 0, 0};
+    return load16(s0 + (static_cast<int64_t>(b) * (W - 1) + (pos + W - 1)) * C + c0);
+}
+
+template <class T, int W, int ACT>
+__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvGeom<T> g, const T* __restrict__ x, const void* w,
+                                                       const void* bias, const T* __restrict__ s0, T* __restrict__ y,
+                                                       T* __restrict__ sT, int64_t items, int64_t main_blocks) {
+    constexpr int E = Io<T>::kVec;
+    const int nch = g.C / E;
+    if (blockIdx.x >= main_blocks) {  // the last W - 1 rows of every sequence
+        const int64_t i = (static_cast<int64_t>(blockIdx.x) - main_blocks) * 256 + threadIdx.x;
+        if (i >= static_cast<int64_t>(g.B) * (W - 1) * nch) return;
+        const int c0 = static_cast<int>(i % nch) * E;
+        const int64_t r = i / nch;
+        const int j = static_cast<int>(r % (W - 1)), b = static_cast<int>(r / (W - 1));
+        Span sp{0, g.T_};
+        if (g.cu) sp = packed_span(g.cu, b, g.T_);
+        const int64_t begin = g.cu ? sp.begin : static_cast<int64_t>(b) * g.T_;
+        const int len = sp.end - sp.begin;
+        store16(sT + (static_cast<int64_t>(b) * (W - 1) + j) * g.C + c0,
+                conv_row<T, W>(x, s0, begin, len + j - (W - 1), b, g.C, g.ldx, c0));
+        return;
+    }
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= items) return;
+    const int c0 = static_cast<int>(i % nch) * E;
+    const int64_t tb = i / nch;
+    Taps<E, W> taps;
+    taps.load(w, bias, g.w_dtype, c0);
+
+    auto walk = [&](int64_t begin, int b, int p0, int p1) {  // positions p0 .. p1 - 1 of sequence b
+        float win[W][E];  // rows p - (W - 1) .. p
+#pragma unroll
+        for (int k = 0; k < W - 1; k++) widen(conv_row<T, W>(x, s0, begin, p0 - (W - 1) + k, b, g.C, g.ldx, c0), win[k + 1]);
+        for (int p = p0; p < p1; p += 8) {
+            uv4 rows[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const int q = p + k < p1 ? p + k : p1 - 1;
+                rows[k] = load16(x + (begin + q) * g.ldx + c0);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                if (p + k >= p1) break;
+#pragma unroll
+                for (int j = 0; j < W - 1; j++)
+#pragma unroll
+                    for (int e = 0; e < E; e++) win[j][e] = win[j + 1][e];
+                widen(rows[k], win[W - 1]);
+                float out[E];
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    float s = taps.bias[e];
+#pragma unroll
+                    for (int j = 0; j < W; j++) s = __builtin_fmaf(taps.w[j][e], win[j][e], s);
+                    out[e] = ACT == LA_ACT_SILU ? s * sigmoid_fine(s) : s;
+                }
+                store16(y + (begin + p + k) * g.ldy + c0, narrow(out));
+            }
+        }
+    };
+    if (!g.cu) {
+        const int b = static_cast<int>(tb / g.blocks);
+        const int p0 = static_cast<int>(tb % g.blocks) * g.per;
+        const int p1 = p0 + g.per < g.T_ ? p0 + g.per : g.T_;
+        walk(static_cast<int64_t>(b) * g.T_, b, p0, p1);
+        return;
+    }
+    int t = static_cast<int>(tb) * g.per;
+    const int t1 = g.T_ - t < g.per ? g.T_ : t + g.per;
+    while (t < t1) {
+        const int b = packed_find(g.cu, g.B, t);
+        const Span sp = packed_span(g.cu, b, g.T_);
+        if (t < sp.begin || t >= sp.end) {  // outside every sequence
+            t++;
+            continue;
+        }
+        const int stop = t1 < sp.end ? t1 : sp.end;
+        walk(sp.begin, b, t - sp.begin, stop - sp.begin);
+        t = stop;
+    }
+}
+
+// Backward.  dpre[t] = dy[t] act'(pre[t]); dz[u] = sum_j w[j] dpre[u - j] (+ dstate_T's row),
+// dx the part of dz behind the state, dstate0 the part before; dw[j] = sum_t dpre[t] z[t + j].
+// Work split as in the forward, 32 lanes of channels by 8 token blocks a workgroup; each walk
+// goes W - 1 tokens past its block for dpre there.  dw and dbias are summed over the walk in
+// registers, over the workgroup in LDS, and over workgroups by a second kernel: no atomics.
+template <class T, int W, int ACT>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* __restrict__ x, const void* w,
+                                                       const void* bias, const T* __restrict__ s0,
+                                                       const T* __restrict__ dy, const T* __restrict__ dsT,
+                                                       T* __restrict__ dx, float* __restrict__ part, int64_t token_blocks) {
+    constexpr int E = Io<T>::kVec;
+    const int nch = g.C / E;
+    const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5;
+    const int ch = blockIdx.y * 32 + lane;
+    const int64_t tb = static_cast<int64_t>(blockIdx.x) * 8 + sub;
+    const int c0 = ch * E;
+    float dw[W][E] = {}, db[E] = {};
+    const bool live = ch < nch && tb < token_blocks;
+    if (live) {
+        Taps<E, W> taps;
+        taps.load(w, bias, g.w_dtype, c0);
+        auto walk = [&](int64_t begin, int len, int b, int p0, int p1) {
+            float win[W][E];
+            float dp[W][E] = {};  // dpre of positions p - (W - 1) .. p
+#pragma unroll
+            for (int k = 0; k < W - 1; k++)
+                widen(conv_row<T, W>(x, s0, begin, p0 - (W - 1) + k, b, g.C, g.ldx, c0), win[k + 1]);
+            const int pe = p1 + W - 1;
+            for (int p = p0; p < pe; p += 4) {
+                uv4 rx[4], rd[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const int q = p + k < len ? p + k : len - 1;
+                    rx[k] = load16(x + (begin + q) * g.ldx + c0);
+                    rd[k] = load16(dy + (begin + q) * g.ldy + c0);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const int q = p + k;
+                    if (q >= pe) break;
+#pragma unroll
+                    for (int j = 0; j < W - 1; j++)
+#pragma unroll
+                        for (int e = 0; e < E; e++) {
+                            win[j][e] = win[j + 1][e];
+                            dp[j][e] = dp[j + 1][e];
+                        }
+                    float d[E];
+                    widen(rx[k], win[W - 1]);
+                    widen(rd[k], d);
+                    const bool inside = q < len, mine = q < p1;
+#pragma unroll
+                    for (int e = 0; e < E; e++) {
+                        float s = taps.bias[e];
+#pragma unroll
+                        for (int j = 0; j < W; j++) s = __builtin_fmaf(taps.w[j][e], win[j][e], s);
+                        if (ACT == LA_ACT_SILU) {
+                            const float sg = sigmoid_fine(s);
+                            d[e] *= sg * __builtin_fmaf(s, 1.0f - sg, 1.0f);
+                        }
+                        dp[W - 1][e] = inside ? d[e] : 0.0f;
+                        const float m = mine ? d[e] : 0.0f;
+                        db[e] += m;
+#pragma unroll
+                        for (int j = 0; j < W; j++) dw[j][e] = __builtin_fmaf(m, mine ? win[j][e] : 0.0f, dw[j][e]);
+                    }
+                    const int u = q - (W - 1);  // its dx is now complete
+                    if (u >= p0) {
+                        float out[E] = {};
+                        const int tail = u - len + W - 1;  // its row of the final state
+                        if (dsT && tail >= 0) widen(load16(dsT + (static_cast<int64_t>(b) * (W - 1) + tail) * g.C + c0), out);
+#pragma unroll
+                        for (int e = 0; e < E; e++)
+#pragma unroll
+                            for (int j = 0; j < W; j++)  // dz[u + W - 1 of z] = sum_j w[j] dpre[u + W - 1 - j]
+                                out[e] = __builtin_fmaf(taps.w[j][e], dp[W - 1 - j][e], out[e]);
+                        store16(dx + (begin + u) * g.ldx + c0, narrow(out));
+                    }
+                }
+            }
+        };
+        if (!g.cu) {
+            const int b = static_cast<int>(tb / g.blocks);
+            const int p0 = static_cast<int>(tb % g.blocks) * g.per;
+            const int p1 = g.T_ - p0 < g.per ? g.T_ : p0 + g.per;
+            walk(static_cast<int64_t>(b) * g.T_, g.T_, b, p0, p1);
+        } else {
+            int t = static_cast<int>(tb) * g.per;
+            const int t1 = g.T_ - t < g.per ? g.T_ : t + g.per;
+            while (t < t1) {
+                const int b = packed_find(g.cu, g.B, t);
+                const Span sp = packed_span(g.cu, b, g.T_);
+                if (t < sp.begin || t >= sp.end) {  // outside every sequence: zero gradient
+                    store16(dx + static_cast<int64_t>(t) * g.ldx + c0, uv4{0, 0, 0, 0});
+                    t++;
+                    continue;
+                }
+                const int stop = t1 < sp.end ? t1 : sp.end;
+                walk(sp.begin, sp.end - sp.begin, b, t - sp.begin, stop - sp.begin);
+                t = stop;
+            }
+        }
+    }
+    __shared__ float red[8][32][E + 1];
+#pragma unroll
+    for (int j = 0; j <= W; j++) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < E; e++) red[sub][lane][e] = j < W ? dw[j < W ? j : 0][e] : db[e];
+        __syncthreads();
+        const int tid = threadIdx.x;
+        if (tid < 32 * E) {
+            const int l = tid / E, e = tid % E, c = (blockIdx.y * 32 + l) * E + e;
+            float s = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; k++) s += red[k][l][e];
+            if (c < g.C) {
+                const size_t at = static_cast<size_t>(blockIdx.x) * g.C * (W + 1) + (j < W ? static_cast<size_t>(c) * W + j
+                                                                                          : static_cast<size_t>(g.C) * W + c);
+                part[at] = s;
+            }
+        }
+    }
+}
+
+// dstate0: row j of z before x gets w[jj] dpre[j - jj] for jj <= j, and where the sequence is
+// shorter than j the final state's own row passes through.
+template <class T, int W, int ACT>
+__global__ __launch_bounds__(256) void conv_bwd_state_kernel(ConvGeom<T> g, const T* x, const void* w, const void* bias,
+                                                             const T* s0, const T* dy, const T* dsT, T* ds0) {
+    constexpr int E = Io<T>::kVec;
+    const int nch = g.C / E;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= static_cast<int64_t>(g.B) * nch) return;
+    const int c0 = static_cast<int>(i % nch) * E, b = static_cast<int>(i / nch);
+    Span sp{0, g.T_};
+    if (g.cu) sp = packed_span(g.cu, b, g.T_);
+    const int64_t begin = g.cu ? sp.begin : static_cast<int64_t>(b) * g.T_;
+    const int len = sp.end - sp.begin;
+    Taps<E, W> taps;
+    taps.load(w, bias, g.w_dtype, c0);
+    float dp[W - 1][E];
+#pragma unroll
+    for (int p = 0; p < W - 1; p++) {
+        float s[E], d[E] = {};
+#pragma unroll
+        for (int e = 0; e < E; e++) s[e] = taps.bias[e];
+        if (p < len) {
+#pragma unroll
+            for (int j = 0; j < W; j++) {
+                float r[E];
+                widen(conv_row<T, W>(x, s0, begin, p - (W - 1) + j, b, g.C, g.ldx, c0), r);
+#pragma unroll
+                for (int e = 0; e < E; e++) s[e] = __builtin_fmaf(taps.w[j][e], r[e], s[e]);
+            }
+            widen(load16(dy + (begin + p) * g.ldy + c0), d);
+        }
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            if (ACT == LA_ACT_SILU) {
+                const float sg = sigmoid_fine(s[e]);
+                d[e] *= sg * __builtin_fmaf(s[e], 1.0f - sg, 1.0f);
+            }
+            dp[p][e] = p < len ? d[e] : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; j++) {
+        float out[E] = {};
+        if (dsT && j >= len) widen(load16(dsT + (static_cast<int64_t>(b) * (W - 1) + j - len) * g.C + c0), out);
+#pragma unroll
+        for (int jj = 0; jj <= j; jj++)
+#pragma unroll
+            for (int e = 0; e < E; e++) out[e] = __builtin_fmaf(taps.w[jj][e], dp[j - jj][e], out[e]);
+        store16(ds0 + (static_cast<int64_t>(b) * (W - 1) + j) * g.C + c0, narrow(out));
+    }
+}
+
+template <class T, int W, int ACT>
+__global__ __launch_bounds__(256) void conv_step_kernel(int B, int C, int ldx, int ldy, int w_dtype, const T* x, const void* w,
+                                                        const void* bias, T* state, const int32_t* slots, int n_slots, T* y) {
+    constexpr int E = Io<T>::kVec;
+    const int nch = C / E;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= static_cast<int64_t>(B) * nch) return;
+    const int c0 = static_cast<int>(i % nch) * E, b = static_cast<int>(i / nch);
+    const int slot = slots ? slots[b] : b;
+    if (slots && (slot <= 0 || slot >= n_slots)) {  // padding
+        store16(y + static_cast<int64_t>(b) * ldy + c0, uv4{0, 0, 0, 0});
+        return;
+    }
+    T* st = state + static_cast<int64_t>(slot) * (W - 1) * C + c0;
+    uv4 rows[W];
+#pragma unroll
+    for (int j = 0; j < W - 1; j++) rows[j] = load16(st + static_cast<int64_t>(j) * C);
+    rows[W - 1] = load16(x + static_cast<int64_t>(b) * ldx + c0);
+    Taps<E, W> taps;
+    taps.load(w, bias, w_dtype, c0);
+    float out[E];
+#pragma unroll
+    for (int e = 0; e < E; e++) out[e] = taps.bias[e];
+#pragma unroll
+    for (int j = 0; j < W; j++) {
+        float r[E];
+        widen(rows[j], r);
+#pragma unroll
+        for (int e = 0; e < E; e++) out[e] = __builtin_fmaf(taps.w[j][e], r[e], out[e]);
+    }
+    if (ACT == LA_ACT_SILU) {
+#pragma unroll
+        for (int e = 0; e < E; e++) out[e] *= sigmoid_fine(out[e]);
+    }
+    store16(y + static_cast<int64_t>(b) * ldy + c0, narrow(out));
+#pragma unroll
+    for (int j = 0; j < W - 1; j++) store16(st + static_cast<int64_t>(j) * C, rows[j + 1]);
+}
+
+__global__ __launch_bounds__(256) void reduce_parts_kernel(const float* __restrict__ part, int parts, int cols,
+                                                           float* __restrict__ out, int split, float* __restrict__ out2) {
+    __shared__ float red[4][64];
+    const int l = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int col = blockIdx.x * 64 + l;
+    float s = 0.0f;
+    if (col < cols)
+        for (int p = q; p < parts; p += 4) s += part[static_cast<size_t>(p) * cols + col];
+    red[q][l] = s;
+    __syncthreads();
+    if (q == 0 && col < cols) {
+        s = (red[0][l] + red[1][l]) + (red[2][l] + red[3][l]);
+        if (col < split) out[col] = s;
+        else if (out2) out2[col - split] = s;
+    }
+}
+
+// Tokens a lane walks in the backward: 32 where that still gives every CU several workgroups,
+// fewer for short inputs.
+int conv_bwd_per(const la_conv_config& c) {
+    const int64_t tokens = static_cast<int64_t>(c.B) * c.T;  // an upper bound for a packing
+    const int nch = c.C / (c.x_dtype == LA_BF16 ? 8 : 4);
+    const int64_t lanes = (nch + 31) / 32;
+    int per = 32;
+    while (per > 4 && lanes * (tokens / (8 * per)) < 512) per >>= 1;
+    return per;
+}
+
+struct ConvBlocks {
+    int64_t blocks;  // token blocks of the whole call
+    int per_seq;     // token blocks a sequence (dense)
+};
+ConvBlocks conv_blocks(const la_conv_config& c, bool packed, int per) {
+    const int n = (c.T + per - 1) / per;
+    return {packed ? n : static_cast<int64_t>(n) * c.B, n};
+}
+
+template <class F>
+hipError_t dispatch(const la_conv_config& c, F&& f) {
+    auto act = [&](auto t, auto w) {
+        if (c.act == LA_ACT_SILU) return f(t, w, std::integral_constant<int, LA_ACT_SILU>{});
+        return f(t, w, std::integral_constant<int, LA_ACT_NONE>{});
+    };
+    auto width = [&](auto t) {
+        switch (c.width) {
+            case 2: return act(t, std::integral_constant<int, 2>{});
+            case 3: return act(t, std::integral_constant<int, 3>{});
+            default: return act(t, std::integral_constant<int, 4>{});
+        }
+    };
+    if (c.x_dtype == LA_BF16) return width(uint16_t{});
+    return width(float{});
+}
+
+template <class T>
+ConvGeom<T> geom(const la_conv_config& c, const int32_t* cu, int per, int blocks) {
+    return {c.B, c.T, c.C, c.ld_x ? c.ld_x : c.C, c.ld_y ? c.ld_y : c.C, c.w_dtype, per, blocks, cu};
+}
+
+}  // namespace
+
+hipError_t launch_conv_fwd(const la_conv_config& c, const ConvArgs& a, hipStream_t s) {
+    return dispatch(c, [&](auto t, auto w, auto act) {
+        using T = decltype(t);
+        constexpr int W = decltype(w)::value, ACT = decltype(act)::value;
+        const int nch = c.C / Io<T>::kVec;
+        int per = 16;
+        while (per > 1 && (static_cast<int64_t>(a.cu ? 1 : c.B) * c.T / per) * nch < 65536) per >>= 1;
+        const ConvBlocks nb = conv_blocks(c, a.cu != nullptr, per);
+        const int64_t items = nb.blocks * nch, main_blocks = (items + 255) / 256;
+        const int64_t extra = a.sT ? (static_cast<int64_t>(c.B) * (W - 1) * nch + 255) / 256 : 0;
+        if (main_blocks + extra == 0) return hipSuccess;
+        conv_fwd_kernel<T, W, ACT><<<dim3(static_cast<unsigned>(main_blocks + extra)), 256, 0, s>>>(
+            geom<T>(c, a.cu, per, nb.per_seq), static_cast<const T*>(a.x), a.w, a.bias, static_cast<const T*>(a.s0),
+            static_cast<T*>(a.y), static_cast<T*>(a.sT), items, main_blocks);
+        return hipGetLastError();
+    });
+}
+
+size_t conv_bwd_workspace(const la_conv_config& c) {
+    const int64_t blocks = static_cast<int64_t>((c.T + conv_bwd_per(c) - 1) / conv_bwd_per(c)) * c.B;
+    return static_cast<size_t>((blocks + 7) / 8) * c.C * (c.width + 1) * sizeof(float);
+}
+
+hipError_t launch_conv_bwd(const la_conv_config& c, const ConvArgs& a, hipStream_t s) {
+    return dispatch(c, [&](auto t, auto w, auto act) {
+        using T = decltype(t);
+        constexpr int W = decltype(w)::value, ACT = decltype(act)::value;
+        const int nch = c.C / Io<T>::kVec;
+        const int per = conv_bwd_per(c);
+        const ConvBlocks nb = conv_blocks(c, a.cu != nullptr, per);
+        const ConvGeom<T> g = geom<T>(c, a.cu, per, nb.per_seq);
+        const int64_t gy = (nb.blocks + 7) / 8;
+        if (gy > 0)
+            conv_bwd_kernel<T, W, ACT><<<dim3(static_cast<unsigned>(gy), (nch + 31) / 32), 256, 0, s>>>(
+                g, static_cast<const T*>(a.x), a.w, a.bias, static_cast<const T*>(a.s0), static_cast<const T*>(a.dy),
+                static_cast<const T*>(a.dsT), static_cast<T*>(a.dx), a.part, nb.blocks);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        e = launch_reduce_parts(a.part, static_cast<int>(gy), c.C * (W + 1), a.dw, c.C * W, a.dbias, s);
+        if (e != hipSuccess || !a.ds0 || c.B == 0) return e;
+        conv_bwd_state_kernel<T, W, ACT><<<dim3(static_cast<unsigned>((static_cast<int64_t>(c.B) * nch + 255) / 256)), 256, 0, s>>>(
+            g, static_cast<const T*>(a.x), a.w, a.bias, static_cast<const T*>(a.s0), static_cast<const T*>(a.dy),
+            static_cast<const T*>(a.dsT), static_cast<T*>(a.ds0));
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_conv_step(const la_conv_config& c, const ConvArgs& a, hipStream_t s) {
+    return dispatch(c, [&](auto t, auto w, auto act) {
+        using T = decltype(t);
+        constexpr int W = decltype(w)::value, ACT = decltype(act)::value;
+        const int64_t items = static_cast<int64_t>(c.B) * (c.C / Io<T>::kVec);
+        conv_step_kernel<T, W, ACT><<<dim3(static_cast<unsigned>((items + 255) / 256)), 256, 0, s>>>(
+            c.B, c.C, c.ld_x ? c.ld_x : c.C, c.ld_y ? c.ld_y : c.C, c.w_dtype, static_cast<const T*>(a.x), a.w, a.bias,
+            static_cast<T*>(a.state), a.slots, a.n_slots, static_cast<T*>(a.y));
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_reduce_parts(const float* part, int parts, int cols, float* out, int split, float* out2,
+                               hipStream_t s) {
+    if (cols == 0) return hipSuccess;
+    reduce_parts_kernel<<<dim3((cols + 63) / 64), 256, 0, s>>>(part, parts, cols, out, split, out2);
+    return hipGetLastError();
+}
+
+}  // namespace la

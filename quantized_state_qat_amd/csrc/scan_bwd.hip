@@ -1,0 +1,717 @@
+// Selective scan backward.
+//
+// Two walks leave, for every 64-token chunk, the state S entering it and the gradient dS of the
+// state leaving it (S_end) in the workspace; the gradients of a chunk then need nothing outside
+// it and all chunks run side by side.  With dM = dY X^T, P = G o L o dM and dG = L o Delta o dM:
+//     dX = M^T dY + diag(W) (B dS) + D dY          dS entering = exp(cum_end) dS + C^T diag(exp cum) dY
+//     dC = sum over heads of dG B + diag(exp cum) (dY S^T)
+//     dB = sum over heads of dG^T C + diag(W) (X dS^T)
+//     c_s = column sums of P + tail_s b_s^T dS x_s         (dDelta_s but for the decay's part)
+//     r_t = row sums of P Delta + exp(cum_t) c_t^T S dy_t
+// cum_t enters the chunk's results as exp(cum_t) on the rows and exp(-cum_s) on the columns, so
+// its gradient is r_t - Delta_t c_t, plus for the last token exp(cum_end) <S, dS> + sum_s Delta_s
+// (c_s's part from dS); a log decay's gradient is the suffix sum of those (in double: the terms
+// cancel), and dDelta, dA follow from it.
+#include "la_scan.hpp"
+
+namespace la {
+namespace {
+
+// Chunk slots: dense, b nch + ch; packed, b + begin_b / 64 + ch (disjoint for any packing).
+__device__ __forceinline__ int64_t slot_of(const ScanP& p, int b, int64_t begin, int ch) {
+    if (!p.cu) return static_cast<int64_t>(b) * ((p.T + kQ - 1) / kQ) + ch;
+    return b + begin / kQ + ch;
+}
+int64_t slot_count(const la_scan_config& c) {  // enough for either layout
+    const int64_t dense = static_cast<int64_t>(c.B) * ((c.T + kQ - 1) / kQ);
+    const int64_t packed = static_cast<int64_t>(c.B) + c.T / kQ + 1;
+    return dense > packed ? dense : packed;
+}
+
+template <class T, int N>
+struct WalkLds {
+    T b[kQ * lds_row<T>(N)];
+    T x[kQ * lds_row<T>(kPT)];
+    Decay d;
+};
+
+// One direction of the state's walk for 64 value columns of a head.  Forward: S from b, x and
+// W, the state entering each chunk to `states`.  REV: dS from c, dy and exp(cum), the gradient
+// of the state leaving each chunk to `states`, and dS0.  ONE: a workgroup a chunk, its own
+// contribution from zero and its decay only (joined by walk_join_kernel): for few heads.
+// The state is held transposed (a lane: one row, four consecutive columns of each tile), so
+// that it is stored in 16-byte pieces.
+template <class T, int N, bool REV, bool ONE>
+__global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* rows_x, int64_t ld_x, const float* first,
+                                                        float* states, float* decay, float* last) {
+    using MT = Mat<T>;
+    constexpr int P3 = MT::template parts<3>;
+    constexpr int RB = lds_row<T>(N), RX = lds_row<T>(kPT);
+    __shared__ __align__(16) WalkLds<T, N> lds;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lm = lane & 15, g = lane >> 4;
+
+    const int tiles = p.dv / kPT, nmax = (p.T + kQ - 1) / kQ;
+    int64_t u = die_unit(blockIdx.x, gridDim.x);
+    const int tile = static_cast<int>(u % tiles);
+    u /= tiles;
+    const int h = static_cast<int>(u % p.H);
+    u /= p.H;
+    const int bi = static_cast<int>(ONE ? u / nmax : u);
+    const SeqRange sr = seq_range(p, bi);
+    const int nch = (sr.len + kQ - 1) / kQ;
+    const int only = ONE ? static_cast<int>(u % nmax) : 0;
+    if (ONE && only >= nch) return;
+    const int steps = ONE ? 1 : nch;
+    const int grp = h / (p.H / p.G);
+    const int col = tile * kPT + 16 * wave + 4 * g;  // this lane's four columns
+    const size_t head = static_cast<size_t>(p.dk) * p.dv;
+
+    f4 S[N / 16];
+#pragma unroll
+    for (int i = 0; i < N / 16; i++) {
+        const int n = 16 * i + lm;
+        S[i] = f4{};
+        if (!ONE && first && n < p.dk)
+            S[i] = *reinterpret_cast<const f4*>(first + (static_cast<size_t>(bi) * p.H + h) * head + static_cast<size_t>(n) * p.dv + col);
+    }
+    auto put = [&](float* at) {
+#pragma unroll
+        for (int i = 0; i < N / 16; i++) {
+            const int n = 16 * i + lm;
+            if (n < p.dk) *reinterpret_cast<f4*>(at + static_cast<size_t>(n) * p.dv + col) = S[i];
+        }
+    };
+    const T* xg = rows_x + static_cast<int64_t>(h) * p.dv + tile * kPT;
+    const T* bg = static_cast<const T*>(REV ? p.c : p.b) + static_cast<int64_t>(grp) * p.dk;
+    const int64_t ld_b = REV ? p.ld_c : p.ld_b;
+    const float A = p.A ? p.A[h] : 0.0f;
+    Tile<T, N, 256> tb;
+    Tile<T, kPT, 256> tx;
+    float raw = 0.0f;
+    auto at_step = [&](int i) { return ONE ? only : REV ? nch - 1 - i : i; };
+    auto fetch = [&](int ch) {
+        const int64_t row0 = sr.begin + static_cast<int64_t>(ch) * kQ;
+        const int live = sr.len - ch * kQ;
+        tb.load(bg + row0 * ld_b, ld_b, live, p.dk);
+        tx.load(xg + row0 * ld_x, ld_x, live, kPT);
+        if (wave == 0 && lane < live) raw = raw_dt(p, row0 + lane, h);
+    };
+    if (steps > 0) fetch(at_step(0));
+    for (int i = 0; i < steps; i++) {
+        const int ch = at_step(i);
+        const int live = sr.len - ch * kQ;
+        tb.store(lds.b, RB);
+        tx.store(lds.x, RX);
+        if (wave == 0) make_decay(lds.d, lane < live ? step_of(p, raw, h) : 0.0f, A);
+        __syncthreads();
+        if (i + 1 < steps) fetch(at_step(i + 1));
+        float* slot = states + (static_cast<size_t>(slot_of(p, bi, sr.begin, ch)) * p.H + h) * head;
+        if (!ONE) put(slot);
+        typename MT::Frag wx[2][P3];
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            float v[8];
+            MT::widen8(MT::col8(lds.x, RX, 32 * k, 16 * wave, lane), v);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int t = 32 * k + 8 * g + j;
+                v[j] *= REV ? lds.d.head[t] : lds.d.tail[t] * lds.d.delta[t];
+            }
+            MT::template split<P3>(v, wx[k]);
+        }
+        const float total = lds.d.total;
+#pragma unroll
+        for (int n = 0; n < N / 16; n++) {
+            S[n] *= total;
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                const typename MT::Frag bf = MT::col8(lds.b, RB, 32 * k, 16 * n, lane);
+#pragma unroll
+                for (int q = 0; q < P3; q++) S[n] = MT::mma(wx[k][q], bf, S[n]);
+            }
+        }
+        if (ONE) {
+            put(slot);
+            if (threadIdx.x == 0 && tile == 0) decay[slot_of(p, bi, sr.begin, ch) * p.H + h] = total;
+        }
+        __syncthreads();
+    }
+    if (!ONE && last) put(last + (static_cast<size_t>(bi) * p.H + h) * head);
+}
+
+// The chunks' own contributions to the state that enters each of them (REV: leaves), in place.
+template <bool REV>
+__global__ __launch_bounds__(256) void walk_join_kernel(ScanP p, const float* first, float* states, const float* decay,
+                                                        float* last) {
+    const int per = p.dk * p.dv / 4;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= static_cast<int64_t>(p.B) * p.H * per) return;
+    const int e = static_cast<int>(i % per);
+    const int64_t bh = i / per;
+    const int h = static_cast<int>(bh % p.H), bi = static_cast<int>(bh / p.H);
+    const SeqRange sr = seq_range(p, bi);
+    const int nch = (sr.len + kQ - 1) / kQ;
+    fv4 S = {};
+    if (first) S = reinterpret_cast<const fv4*>(first)[bh * per + e];
+    for (int k = 0; k < nch; k++) {
+        const int64_t at = slot_of(p, bi, sr.begin, REV ? nch - 1 - k : k) * p.H + h;
+        fv4* l = reinterpret_cast<fv4*>(states) + at * per + e;
+        const fv4 own = *l;
+        *l = S;
+        S = S * decay[at] + own;
+    }
+    if (last) reinterpret_cast<fv4*>(last)[bh * per + e] = S;
+}
+
+template <class T, int N>
+struct GradLds {
+    T b[kQ * lds_row<T>(N)];
+    T c[kQ * lds_row<T>(N)];
+    T x[kQ * lds_row<T>(kPT)];
+    T dy[kQ * lds_row<T>(kPT)];
+    T m[Mat<T>::template parts<2>][kQ * lds_row<T>(kQ)];   // M[t][s]
+    T dg[Mat<T>::template parts<2>][kQ * lds_row<T>(kQ)];  // dG[t][s]
+    T ds[sizeof(T) == 2 ? 2 : 1][sizeof(T) == 2 ? N * lds_row<T>(kPT) : 1];  // dS (bf16 parts); FP32 reads it from memory
+    Decay d;
+    float rt[10][16], ct[10][16];  // the tiles' row and column sums
+    float ri[N / 16][kQ], ci[N / 16][kQ];  // sums over 16 state rows
+    float sd[2][8], dd[8];                 // the waves' <S, dS> (by parity of the iteration) and diagonals of dM
+};
+
+__device__ __forceinline__ void lower_tile_of(int k, int& ti, int& si) {
+    ti = k < 1 ? 0 : k < 3 ? 1 : k < 6 ? 2 : 3;
+    si = k - ti * (ti + 1) / 2;
+}
+
+// Gradients of one chunk for one slice of a group's heads, by eight waves.  Pairs: the ten lower
+// tiles over the waves.  dX: a wave 16 columns by 32 tokens.  dC, dB: a wave 16 state rows by all
+// tokens (fewer rows than 128: by a part of them), kept in registers over the heads.  dbp, dcp: FP32 partial sums of db
+// and dc per slice ([slice][row][G][dk]), or null where one slice holds the whole group.
+template <class T, int N>
+__global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, const float* Sin, const float* dSe, void* dx_,
+                                                        void* ddt, void* db_, void* dc_, float* dbp, float* dcp,
+                                                        float* hp, int64_t slots, int slices, int64_t rows) {
+    using MT = Mat<T>;
+    constexpr int P2 = MT::template parts<2>;
+    constexpr int RB = lds_row<T>(N), RX = lds_row<T>(kPT), RM = lds_row<T>(kQ);
+    constexpr int KS = N / 32, NTL = N / 16, PARTS = 8 / NTL, TI = 4 / PARTS;
+    extern __shared__ __align__(16) char raw_lds[];
+    GradLds<T, N>& lds = *reinterpret_cast<GradLds<T, N>*>(raw_lds);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lm = lane & 15, g = lane >> 4;
+    const int n0 = 16 * (wave % NTL), part = wave / NTL;  // state rows and token part of dC, dB
+
+    int64_t u = die_unit(blockIdx.x, gridDim.x);
+    const int slice = static_cast<int>(u % slices);
+    u /= slices;
+    const int grp = static_cast<int>(u % p.G);
+    const int64_t slot = u / p.G;
+    int bi, ch;
+    if (!p.cu) {
+        const int nmax = (p.T + kQ - 1) / kQ;
+        bi = static_cast<int>(slot / nmax);
+        ch = static_cast<int>(slot % nmax);
+        if (bi >= p.B) return;
+    } else {  // the last b with b + begin_b / 64 <= slot
+        int lo = 0, hi = p.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (mid + packed_span(p.cu, mid, p.T).begin / kQ <= slot) lo = mid;
+            else hi = mid - 1;
+        }
+        bi = lo;
+        ch = static_cast<int>(slot - bi - packed_span(p.cu, bi, p.T).begin / kQ);
+    }
+    const SeqRange sr = seq_range(p, bi);
+    if (ch < 0 || ch * static_cast<int64_t>(kQ) >= sr.len) return;
+    const int64_t row0 = sr.begin + static_cast<int64_t>(ch) * kQ;
+    const int live = sr.len - ch * kQ < kQ ? sr.len - ch * kQ : kQ;
+
+    const int hpg = p.H / p.G, per = (hpg + slices - 1) / slices;
+    const int h0 = grp * hpg + slice * per;
+    const int h1 = slice * per + per < hpg ? h0 + per : (grp + 1) * hpg;
+    const int tiles = p.dv / kPT;
+    const size_t head = static_cast<size_t>(p.dk) * p.dv;
+
+    {  // this chunk's b and c, and zeros above the diagonals
+        Tile<T, N, 512> t;
+        t.load(static_cast<const T*>(p.b) + row0 * p.ld_b + static_cast<int64_t>(grp) * p.dk, p.ld_b, live, p.dk);
+        t.store(lds.b, RB);
+        t.load(static_cast<const T*>(p.c) + row0 * p.ld_c + static_cast<int64_t>(grp) * p.dk, p.ld_c, live, p.dk);
+        t.store(lds.c, RB);
+        for (int i = threadIdx.x; i < P2 * kQ * RM; i += 512) {
+            (&lds.m[0][0])[i] = T{};
+            (&lds.dg[0][0])[i] = T{};
+        }
+    }
+    __syncthreads();
+    f4 G[2];  // G^T of this wave's lower tiles: rows s, columns t
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+        const int k = wave + 8 * q;
+        G[q] = f4{};
+        if (k < 10) {
+            int ti, si;
+            lower_tile_of(k, ti, si);
+#pragma unroll
+            for (int ks = 0; ks < KS; ks++)
+                G[q] = MT::mma(MT::row8(lds.b + (16 * si + lm) * RB + 32 * ks + 8 * g),
+                               MT::row8(lds.c + (16 * ti + lm) * RB + 32 * ks + 8 * g), G[q]);
+        }
+    }
+    f4 dC[TI] = {}, dB[TI] = {};  // rows n, columns t (s)
+
+    Tile<T, kPT, 512> tx, ty;
+    float rdt = 0.0f;
+    typename MT::Frag Sf[2][P2], dSf[2][P2];
+    float Sr[2][8], dSr[2][8];
+    auto fetch = [&](int h, int tile) {
+        tx.load(static_cast<const T*>(p.x) + row0 * p.ld_x + static_cast<int64_t>(h) * p.dv + tile * kPT, p.ld_x, live, kPT);
+        ty.load(dyr + (row0 * p.H + h) * p.dv + tile * kPT, static_cast<int64_t>(p.H) * p.dv, live, kPT);
+        if (wave == 0 && lane < live) rdt = raw_dt(p, row0 + lane, h);
+        const size_t at = (static_cast<size_t>(slot) * p.H + h) * head + tile * kPT;
+        const int n = n0 + lm;
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            f4 v[4] = {};
+            if (n < p.dk) {
+                const float* s = Sin + at + static_cast<size_t>(n) * p.dv + 32 * k + 8 * g;
+                const float* d = dSe + at + static_cast<size_t>(n) * p.dv + 32 * k + 8 * g;
+                v[0] = *reinterpret_cast<const f4*>(s);
+                v[1] = *reinterpret_cast<const f4*>(s + 4);
+                v[2] = *reinterpret_cast<const f4*>(d);
+                v[3] = *reinterpret_cast<const f4*>(d + 4);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                Sr[k][j] = v[0][j];
+                Sr[k][4 + j] = v[1][j];
+                dSr[k][j] = v[2][j];
+                dSr[k][4 + j] = v[3][j];
+            }
+        }
+    };
+    float racc = 0.0f, cacc = 0.0f, iacc = 0.0f, sdacc = 0.0f, ddacc = 0.0f;  // wave 0: the head's sums, lane = token
+    float zt = 0.0f;
+    fetch(h0, 0);
+    const int iters = (h1 - h0) * tiles;
+    for (int it = 0; it < iters; it++) {
+        const int h = h0 + it / tiles, tile = it % tiles;
+        const float A = p.A[h];
+        const float Dh = p.D ? p.D[h] : 0.0f;
+        // ---- this head's tiles to LDS
+        tx.store(lds.x, RX);
+        ty.store(lds.dy, RX);
+        if (wave == 0 && tile == 0) {
+            zt = rdt + (p.bias ? p.bias[h] : 0.0f);
+            make_decay(lds.d, lane < live ? (p.softplus ? softplus_fine(zt) : zt) : 0.0f, A);
+        }
+        float sd = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) sd = __builtin_fmaf(Sr[k][j], dSr[k][j], sd);
+            MT::template split<P2>(Sr[k], Sf[k]);
+            MT::template split<P2>(dSr[k], dSf[k]);
+            if constexpr (sizeof(T) == 2) {
+                if (part == 0) {
+#pragma unroll
+                    for (int r = 0; r < P2; r++)
+                        *reinterpret_cast<typename MT::Frag*>(&lds.ds[r][(n0 + lm) * RX + 32 * k + 8 * g]) = dSf[k][r];
+                }
+            }
+        }
+        sd = part == 0 ? wave_sum(sd) : 0.0f;
+        if (lane == 0) lds.sd[it & 1][wave] = sd;  // (wave 0 may still read the last iteration's)
+        __syncthreads();
+        if (it + 1 < iters) fetch(h0 + (it + 1) / tiles, (it + 1) % tiles);
+
+        // ---- pairs: dM^T tiles (rows s, columns t)
+        float diag = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+            const int k = wave + 8 * q;
+            if (k >= 10) continue;
+            int ti, si;
+            lower_tile_of(k, ti, si);
+            f4 acc = {};
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++)
+                acc = MT::mma(MT::row8(lds.x + (16 * si + lm) * RX + 32 * ks + 8 * g),
+                              MT::row8(lds.dy + (16 * ti + lm) * RX + 32 * ks + 8 * g), acc);
+            const int t = 16 * ti + lm, s0 = 16 * si + 4 * g;
+            const float thi = lds.d.hi[t], tlo = lds.d.lo[t];
+            float m[4], dg[4], pc[4], pr = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const int s = s0 + r;
+                const float L = s <= t ? pair_decay(thi, tlo, lds.d.hi[s], lds.d.lo[s]) : 0.0f;
+                const float gl = G[q][r] * L, dl = lds.d.delta[s];
+                m[r] = gl * dl;
+                dg[r] = L * dl * acc[r];
+                pc[r] = gl * acc[r];
+                pr = __builtin_fmaf(pc[r], dl, pr);
+                if (s == t) diag += acc[r];
+            }
+            MT::template put4<P2>(&lds.m[0][t * RM + s0], kQ * RM, m);
+            MT::template put4<P2>(&lds.dg[0][t * RM + s0], kQ * RM, dg);
+            pr = rows_sum(pr);
+            if (g == 0) lds.rt[k][lm] = pr;
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const float s = group_sum<16>(pc[r]);
+                if (lm == 0) lds.ct[k][4 * g + r] = s;
+            }
+        }
+        diag = wave_sum(diag);
+        if (lane == 0) lds.dd[wave] = diag;
+        __syncthreads();
+
+        // ---- dX^T: rows: columns pc + 4 g + r; column: s
+        {
+            const int pc = 16 * (wave & 3), half = wave >> 2;
+            typename MT::Frag dyT[2];
+#pragma unroll
+            for (int k = 0; k < 2; k++) dyT[k] = MT::col8(lds.dy, RX, 32 * k, pc, lane);
+            f4 acc[2] = {};
+#pragma unroll
+            for (int ks = 0; ks < KS; ks++) {
+                typename MT::Frag dsT[P2];
+                if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                    for (int k = 0; k < P2; k++) dsT[k] = MT::col8(lds.ds[k], RX, 32 * ks, pc, lane);
+                } else {
+                    const float* d = dSe + (static_cast<size_t>(slot) * p.H + h) * head + tile * kPT + pc + lm;
+#pragma unroll
+                    for (int j = 0; j < 8; j++) {
+                        const int n = 32 * ks + 8 * g + j;
+                        dsT[0][j] = n < p.dk ? d[static_cast<size_t>(n) * p.dv] : 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    const typename MT::Frag bf = MT::row8(lds.b + (32 * half + 16 * j + lm) * RB + 32 * ks + 8 * g);
+#pragma unroll
+                    for (int k = 0; k < P2; k++) acc[j] = MT::mma(dsT[k], bf, acc[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int s = 32 * half + 16 * j + lm;
+                acc[j] *= lds.d.tail[s] * lds.d.delta[s];
+#pragma unroll
+                for (int ks = 0; ks < 2; ks++) {
+                    if (ks < half) continue;  // tokens before s
+#pragma unroll
+                    for (int k = 0; k < P2; k++)
+                        acc[j] = MT::mma(dyT[ks], MT::col8(lds.m[k], RM, 32 * ks, 32 * half + 16 * j, lane), acc[j]);
+                }
+                float yv[4];
+                MT::get4(lds.dy + s * RX + pc + 4 * g, yv);
+#pragma unroll
+                for (int r = 0; r < 4; r++) acc[j][r] = __builtin_fmaf(Dh, yv[r], acc[j][r]);
+                if (s < live) {
+                    T* o = static_cast<T*>(dx_) + (row0 + s) * p.ld_x + static_cast<int64_t>(h) * p.dv + tile * kPT + pc + 4 * g;
+                    const float v[4] = {acc[j][0], acc[j][1], acc[j][2], acc[j][3]};
+                    MT::template put4<1>(o, 0, v);
+                }
+            }
+        }
+        // ---- dC^T, dB^T: rows n of this wave, columns t, s
+        {
+            typename MT::Frag bT[2], cT[2];
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                bT[k] = MT::col8(lds.b, RB, 32 * k, n0, lane);
+                cT[k] = MT::col8(lds.c, RB, 32 * k, n0, lane);
+            }
+#pragma unroll
+            for (int ii = 0; ii < TI; ii++) {
+                const int i = part * TI + ii, t = 16 * i + lm;
+                f4 a = {}, b = {};
+#pragma unroll
+                for (int ks = 0; ks < 2; ks++) {
+                    const typename MT::Frag yf = MT::row8(lds.dy + t * RX + 32 * ks + 8 * g);
+                    const typename MT::Frag xf = MT::row8(lds.x + t * RX + 32 * ks + 8 * g);
+#pragma unroll
+                    for (int k = 0; k < P2; k++) {
+                        a = MT::mma(Sf[ks][k], yf, a);
+                        b = MT::mma(dSf[ks][k], xf, b);
+                    }
+                }
+                a *= lds.d.head[t];
+                b *= lds.d.tail[t];
+                float cv[4], bv[4], ri = 0.0f, ci = 0.0f;
+                MT::get4(lds.c + t * RB + n0 + 4 * g, cv);
+                MT::get4(lds.b + t * RB + n0 + 4 * g, bv);
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    ri = __builtin_fmaf(a[r], cv[r], ri);
+                    ci = __builtin_fmaf(b[r], bv[r], ci);
+                }
+                ri = rows_sum(ri);
+                ci = rows_sum(ci);
+                if (g == 0) {
+                    lds.ri[wave % NTL][t] = ri;
+                    lds.ci[wave % NTL][t] = ci;
+                }
+                dC[ii] += a;
+                dB[ii] += b * lds.d.delta[t];
+#pragma unroll
+                for (int ks = 0; ks < 2; ks++) {
+                    if (ks <= i / 2) {
+#pragma unroll
+                        for (int k = 0; k < P2; k++)
+                            dC[ii] = MT::mma(bT[ks], MT::row8(&lds.dg[k][t * RM + 32 * ks + 8 * g]), dC[ii]);
+                    }
+                    if (ks >= i / 2) {
+#pragma unroll
+                        for (int k = 0; k < P2; k++)
+                            dB[ii] = MT::mma(cT[ks], MT::col8(lds.dg[k], RM, 32 * ks, 16 * i, lane), dB[ii]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+
+        // ---- the decays' gradients, once a head
+        if (wave == 0) {
+            const int tq = lane >> 4, tl = lane & 15;
+            for (int si = 0; si <= tq; si++) racc += lds.rt[tq * (tq + 1) / 2 + si][tl];
+            for (int ti = tq; ti < 4; ti++) cacc += lds.ct[ti * (ti + 1) / 2 + tq][tl];
+            float inner = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NTL; k++) {
+                racc += lds.ri[k][lane];
+                inner += lds.ci[k][lane];
+            }
+            cacc += inner;
+            iacc += inner;
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                sdacc += lds.sd[it & 1][k];
+                ddacc += lds.dd[k];
+            }
+            if (tile == tiles - 1) {
+                const float delta = lds.d.delta[lane];
+                double v = static_cast<double>(racc) - static_cast<double>(delta) * cacc;
+                const double into = wave_last(wave_prefix(static_cast<double>(delta) * iacc));
+                if (lane == 63) v += static_cast<double>(lds.d.total) * sdacc + into;
+                const double pre = wave_prefix(v);
+                const double rate = wave_last(pre) - pre + v;  // suffix sum: the log decay's gradient
+                const float dd = cacc + A * static_cast<float>(rate);
+                const float dz = lane < live ? (p.softplus ? dd * sigmoid_fine(zt) : dd) : 0.0f;
+                if (lane < live) store_elem(ddt, (row0 + lane) * p.ld_dt + h, p.dt_dtype, dz);
+                const float da = static_cast<float>(wave_last(wave_prefix(rate * delta)));
+                const float db = static_cast<float>(wave_last(wave_prefix(static_cast<double>(dz))));
+                if (lane == 0) {
+                    float* o = hp + static_cast<size_t>(slot) * 3 * p.H + h;
+                    o[0] = da;
+                    o[p.H] = ddacc;
+                    o[2 * p.H] = db;
+                }
+                racc = cacc = iacc = sdacc = ddacc = 0.0f;
+            }
+        }
+    }
+    // ---- db, dc
+    const int n = n0 + 4 * g;
+    if (n >= p.dk) return;
+#pragma unroll
+    for (int ii = 0; ii < TI; ii++) {
+        const int t = 16 * (part * TI + ii) + lm;
+        if (t >= live) continue;
+        const float vb[4] = {dB[ii][0], dB[ii][1], dB[ii][2], dB[ii][3]};
+        const float vc[4] = {dC[ii][0], dC[ii][1], dC[ii][2], dC[ii][3]};
+        if (dbp) {
+            const size_t at = ((static_cast<size_t>(slice) * rows + row0 + t) * p.G + grp) * p.dk + n;
+            *reinterpret_cast<f4*>(dbp + at) = dB[ii];
+            *reinterpret_cast<f4*>(dcp + at) = dC[ii];
+        } else {
+            MT::template put4<1>(static_cast<T*>(db_) + (row0 + t) * p.ld_b + static_cast<int64_t>(grp) * p.dk + n, 0, vb);
+            MT::template put4<1>(static_cast<T*>(dc_) + (row0 + t) * p.ld_c + static_cast<int64_t>(grp) * p.dk + n, 0, vc);
+        }
+    }
+}
+
+// db and dc from the slices' partial sums, in slice order.
+template <class T>
+__global__ __launch_bounds__(256) void join_slices_kernel(ScanP p, const float* dbp, const float* dcp, T* db, T* dc,
+                                                          int slices, int64_t rows) {
+    const int per = p.G * p.dk / 4;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= rows * per) return;
+    const int64_t row = i / per;
+    const int e = static_cast<int>(i % per) * 4;
+    if (p.cu) {  // rows outside every sequence are cleared by their own kernel
+        const int b = packed_find(p.cu, p.B, static_cast<int>(row));
+        const Span s = packed_span(p.cu, b, p.T);
+        if (row < s.begin || row >= s.end) return;
+    }
+    fv4 vb = {}, vc = {};
+    for (int s = 0; s < slices; s++) {
+        vb += *reinterpret_cast<const fv4*>(dbp + (s * rows + row) * per * 4 + e);
+        vc += *reinterpret_cast<const fv4*>(dcp + (s * rows + row) * per * 4 + e);
+    }
+    const float fb[4] = {vb[0], vb[1], vb[2], vb[3]}, fc[4] = {vc[0], vc[1], vc[2], vc[3]};
+    Mat<T>::template put4<1>(db + row * p.ld_b + e, 0, fb);
+    Mat<T>::template put4<1>(dc + row * p.ld_c + e, 0, fc);
+}
+
+// Zero gradients for a packing's tokens outside every sequence.
+template <class T>
+__global__ __launch_bounds__(256) void clear_outside_kernel(ScanP p, T* dx, void* ddt, T* db, T* dc) {
+    const int t = blockIdx.x;
+    const int b = packed_find(p.cu, p.B, t);
+    const Span s = packed_span(p.cu, b, p.T);
+    if (t >= s.begin && t < s.end) return;
+    for (int i = threadIdx.x; i < p.H * p.dv; i += 256) dx[t * p.ld_x + i] = T{};
+    for (int i = threadIdx.x; i < p.G * p.dk; i += 256) {
+        db[t * p.ld_b + i] = T{};
+        dc[t * p.ld_c + i] = T{};
+    }
+    for (int i = threadIdx.x; i < p.H; i += 256) store_elem(ddt, t * p.ld_dt + i, p.dt_dtype, 0.0f);
+}
+
+// The heads' dA, dD and ddt_bias over all chunks (a packing's unused slots hold nothing).
+__global__ __launch_bounds__(256) void head_sums_kernel(ScanP p, const float* hp, int64_t slots, float* dA, float* dD, float* dbias) {
+    __shared__ double red[256];
+    const int h = blockIdx.x % p.H, which = blockIdx.x / p.H;
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < slots; i += 256) {
+        bool used = true;
+        if (p.cu) {
+            int lo = 0, hi = p.B - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (mid + packed_span(p.cu, mid, p.T).begin / kQ <= i) lo = mid;
+                else hi = mid - 1;
+            }
+            const Span sp = packed_span(p.cu, lo, p.T);
+            const int64_t ch = i - lo - sp.begin / kQ;
+            used = ch >= 0 && ch * kQ < sp.end - sp.begin;
+        }
+        if (used) s += hp[i * 3 * p.H + static_cast<int64_t>(which) * p.H + h];
+    }
+    red[threadIdx.x] = s;
+    __syncthreads();
+    for (int n = 128; n > 0; n >>= 1) {
+        if (threadIdx.x < n) red[threadIdx.x] += red[threadIdx.x + n];
+        __syncthreads();
+    }
+    float* out = which == 0 ? dA : which == 1 ? dD : dbias;
+    if (threadIdx.x == 0 && out) out[h] = static_cast<float>(red[0]);
+}
+
+__global__ __launch_bounds__(256) void copy_or_zero_kernel(const float* src, float* dst, int64_t n) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i < n) dst[i] = src ? src[i] : 0.0f;
+}
+
+// Slices of a group's heads: enough workgroups for two a CU.
+int grad_slices(const la_scan_config& c) {
+    const int64_t units = slot_count(c) * c.G;
+    const int hpg = c.H / c.G;
+    if (units == 0 || hpg == 0) return 1;
+    int64_t n = (512 + units - 1) / units;
+    if (n > hpg) n = hpg;
+    const int per = static_cast<int>((hpg + n - 1) / n);
+    return (hpg + per - 1) / per;
+}
+
+struct BwdWs {
+    size_t S, dS, decay, dbp, dcp, hp, total;
+};
+BwdWs bwd_ws(const la_scan_config& c) {
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    const int64_t slots = slot_count(c);
+    const size_t st = up(static_cast<size_t>(slots) * c.H * c.d_k * c.d_v * sizeof(float));
+    const int slices = grad_slices(c);
+    const size_t bc = slices > 1 ? up(static_cast<size_t>(slices) * c.B * c.T * c.G * c.d_k * sizeof(float)) : 0;
+    BwdWs w;
+    w.S = 0;
+    w.dS = w.S + st;
+    w.decay = w.dS + st;
+    w.dbp = w.decay + up(static_cast<size_t>(slots) * c.H * sizeof(float));
+    w.dcp = w.dbp + bc;
+    w.hp = w.dcp + bc;
+    w.total = w.hp + up(static_cast<size_t>(slots) * 3 * c.H * sizeof(float));
+    return w;
+}
+
+template <class T, int N>
+hipError_t launch(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
+    const ScanP p = scan_params(c, a);
+    const BwdWs w = bwd_ws(c);
+    float* S = reinterpret_cast<float*>(a.ws + w.S);
+    float* dS = reinterpret_cast<float*>(a.ws + w.dS);
+    float* decay = reinterpret_cast<float*>(a.ws + w.decay);
+    float* hp = reinterpret_cast<float*>(a.ws + w.hp);
+    const int64_t rows = a.cu ? c.T : static_cast<int64_t>(c.B) * c.T;
+    const int nmax = (c.T + kQ - 1) / kQ;
+    const int64_t slots = a.cu ? static_cast<int64_t>(c.B) + c.T / kQ + 1 : static_cast<int64_t>(c.B) * nmax;
+    const int64_t groups = static_cast<int64_t>(c.B) * c.H * (c.d_v / kPT);
+    const T* x = static_cast<const T*>(a.x);
+    const T* dy = static_cast<const T*>(a.dy);
+    const int64_t ld_y = static_cast<int64_t>(c.H) * c.d_v;
+    // Enough heads: a workgroup walks a sequence.  Fewer than a workgroup a CU: one a chunk
+    // and a joining pass (three times the state traffic, but no walk).
+    if (groups >= 256 || nmax < 8) {
+        scan_walk_kernel<T, N, false, false><<<dim3(static_cast<unsigned>(groups)), 256, 0, s>>>(p, x, p.ld_x, a.S0, S, nullptr, nullptr);
+        scan_walk_kernel<T, N, true, false><<<dim3(static_cast<unsigned>(groups)), 256, 0, s>>>(p, dy, ld_y, a.dST, dS, nullptr, a.dS0);
+    } else {
+        const unsigned grid = static_cast<unsigned>(groups * nmax);
+        const unsigned join = static_cast<unsigned>((static_cast<int64_t>(c.B) * c.H * (c.d_k * c.d_v / 4) + 255) / 256);
+        scan_walk_kernel<T, N, false, true><<<dim3(grid), 256, 0, s>>>(p, x, p.ld_x, nullptr, S, decay, nullptr);
+        walk_join_kernel<false><<<dim3(join), 256, 0, s>>>(p, a.S0, S, decay, nullptr);
+        scan_walk_kernel<T, N, true, true><<<dim3(grid), 256, 0, s>>>(p, dy, ld_y, nullptr, dS, decay, nullptr);
+        walk_join_kernel<true><<<dim3(join), 256, 0, s>>>(p, a.dST, dS, decay, a.dS0);
+    }
+    const int slices = grad_slices(c);
+    float* dbp = slices > 1 ? reinterpret_cast<float*>(a.ws + w.dbp) : nullptr;
+    float* dcp = slices > 1 ? reinterpret_cast<float*>(a.ws + w.dcp) : nullptr;
+    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&scan_grad_kernel<T, N>),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(GradLds<T, N>)));
+    if (e != hipSuccess) return e;
+    scan_grad_kernel<T, N><<<dim3(static_cast<unsigned>(slots * c.G * slices)), 512, sizeof(GradLds<T, N>), s>>>(
+        p, dy, S, dS, a.dx, a.ddt, a.db, a.dc, dbp, dcp, hp, slots, slices, rows);
+    if (slices > 1) {
+        const int64_t items = rows * (c.G * c.d_k / 4);
+        join_slices_kernel<T><<<dim3(static_cast<unsigned>((items + 255) / 256)), 256, 0, s>>>(
+            p, dbp, dcp, static_cast<T*>(a.db), static_cast<T*>(a.dc), slices, rows);
+    }
+    if (a.cu)
+        clear_outside_kernel<T><<<dim3(static_cast<unsigned>(c.T)), 256, 0, s>>>(p, static_cast<T*>(a.dx), a.ddt,
+                                                                                static_cast<T*>(a.db), static_cast<T*>(a.dc));
+    head_sums_kernel<<<dim3(3 * c.H), 256, 0, s>>>(p, hp, slots, a.dA, a.dD, a.dbias);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t scan_bwd_workspace(const la_scan_config& c) { return bwd_ws(c).total; }
+
+hipError_t launch_scan_bwd(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
+    if (c.B == 0 || c.T == 0) {  // no tokens: the state's gradient passes through, the sums are zero
+        for (float* o : {a.dA, a.dD, a.dbias})
+            if (o) copy_or_zero_kernel<<<dim3((c.H + 255) / 256), 256, 0, s>>>(nullptr, o, c.H);
+        const int64_t n = static_cast<int64_t>(c.B) * c.H * c.d_k * c.d_v;
+        if (a.dS0 && n > 0) copy_or_zero_kernel<<<dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, s>>>(a.dST, a.dS0, n);
+        return hipGetLastError();
+    }
+    if (c.x_dtype == LA_BF16) {
+        switch (c.d_k) {
+            case 128: return launch<uint16_t, 128>(c, a, s);
+            case 64: return launch<uint16_t, 64>(c, a, s);
+            default: return launch<uint16_t, 32>(c, a, s);
+        }
+    }
+    switch (c.d_k) {
+        case 128: return launch<float, 128>(c, a, s);
+        case 64: return launch<float, 64>(c, a, s);
+        default: return launch<float, 32>(c, a, s);
+    }
+}
+
+}  // namespace la

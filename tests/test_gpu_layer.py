@@ -1,0 +1,640 @@
+"""The layer operators on the GPU against their 64-bit forms (tests/layer_ref.py).
+
+Tolerances, derived: an output may be off by half a step of its type (bf16 2^-8, fp32 2^-24 of
+the value) plus a share of its magnitude, the sum of its terms' absolute values:
+  convolution   up to 5 FP32 terms (5 x 2^-24) through silu and its derivative, whose slope is
+                at most 1.1 and whose own error is a few 2^-23: 2^-20.
+  scan          operands in two bf16 parts (2^-17 each, two in a product: 2^-16), at most 192
+                terms a sum in FP32 (192 x 2^-24 < 2^-16), decays to a few 2^-22: 2^-14.  The
+                rates' gradients are suffix sums over a chunk of terms that cancel: their
+                magnitude is the chunk's sum of the terms' absolute values.
+  norm          a row's mean and two products in FP32: 2^-19 (d <= 16384 terms, summed in
+                pieces of at most 64 per lane).
+"""
+import numpy as np
+import pytest
+import torch
+
+import quantized_state_qat_amd as la
+from tests import layer_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+CODE = {BF: la.LA_BF16, F32: la.LA_F32}
+HALF = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def draw(g, *shape, dtype=BF, scale=1.0):
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).cuda()
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def close(got, want, mag, share, name, dtype=None):
+    half = HALF[dtype or got.dtype]
+    got = np64(got)
+    assert got.shape == want.shape, (name, got.shape, want.shape)
+    assert np.isfinite(got).all(), name
+    over = np.abs(got - want) - (half * 1.01 * np.abs(want) + share * mag + 1e-30)
+    worst = np.unravel_index(np.argmax(over), over.shape) if over.size else None
+    assert over.size == 0 or over.max() <= 0, (name, worst, got[worst], want[worst], mag[worst] if np.ndim(mag) else mag)
+
+
+def spans(B, T, cu):
+    return [(cu[i], cu[i + 1]) for i in range(B)] if cu is not None else [(i * T, (i + 1) * T) for i in range(B)]
+
+
+def cu_tensor(cu):
+    return None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+
+def strided(g, tokens, width, extra, dtype):
+    """Rows of `width` inside wider rows: (view, ld)."""
+    buf = draw(g, tokens, width + extra, dtype=dtype)
+    return buf[:, 8:8 + width] if extra else buf, width + extra
+
+
+# ------------------------------------------------------------------------------- convolution
+CONV = [
+    # dtype, B, T, cu, C, W, act, extra columns, bias, states, weights' dtype
+    (BF, 2, 37, None, 64, 4, 1, 0, True, True, F32),
+    (F32, 1, 130, None, 24, 3, 1, 16, True, True, F32),
+    (BF, 3, 1, None, 2312, 4, 1, 0, True, True, BF),
+    (BF, 2, 2, None, 72, 4, 0, 24, False, True, F32),
+    (F32, 2, 3, None, 8, 2, 1, 0, True, False, BF),
+    (BF, 6, 200, [3, 3, 40, 41, 43, 150, 190], 136, 4, 1, 8, True, True, F32),
+    (F32, 4, 70, [0, 0, 70, 70, 70], 40, 3, 0, 0, False, True, F32),
+    (BF, 1, 700, None, 264, 2, 1, 0, True, False, F32),
+    (BF, 65, 300, [min(300, 4 * i) for i in range(66)], 16, 4, 1, 0, True, True, F32),
+]
+
+
+@pytest.mark.parametrize("dtype,B,T,cu,C,W,act,extra,bias,states,wt", CONV)
+def test_conv(dtype, B, T, cu, C, W, act, extra, bias, states, wt):
+    g = gen(C + T)
+    tokens = T if cu is not None else B * T
+    x, ld = strided(g, tokens, C, extra, dtype)
+    w = draw(g, C, W, dtype=wt, scale=0.5)
+    bv = draw(g, C, dtype=wt) if bias else None
+    s0 = draw(g, B, W - 1, C, dtype=dtype) if states else None
+    dsT = draw(g, B, W - 1, C, dtype=dtype) if states else None
+    dy = draw(g, tokens, C, dtype=dtype)
+    cfg = la.ConvConfig(B=B, T=T, C=C, width=W, act=act, x_dtype=CODE[dtype], w_dtype=CODE[wt], ld_x=ld if extra else 0)
+    y = torch.full((tokens, C), 7.0, dtype=dtype, device="cuda")
+    sT = torch.full((B, W - 1, C), float("nan"), dtype=dtype, device="cuda")
+    la.la_conv_fwd(cfg, x, w, bv, s0, y, sT, cu_seqlens=cu_tensor(cu))
+    dxb = torch.full((tokens, C + extra), 9.0, dtype=dtype, device="cuda")
+    dx = dxb[:, 8:8 + C] if extra else dxb
+    dw, db = torch.full((C, W), float("nan"), device="cuda"), torch.full((C,), float("nan"), device="cuda")
+    ds0 = torch.full((B, W - 1, C), float("nan"), dtype=dtype, device="cuda")
+    n = la.la_conv_bwd_workspace_bytes(cfg)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    la.la_conv_bwd(cfg, x, w, bv, s0, dy, dsT, dx, dw, db, ds0, ws, n, cu_seqlens=cu_tensor(cu))
+
+    xn, wn, dyn = np64(x), np64(w), np64(dy)
+    bn = np64(bv) if bias else np.zeros(C)
+    zero = np.zeros((B, W - 1, C))
+    s0n, dsn = (np64(s0), np64(dsT)) if states else (zero, zero)
+    yr, ym, dxr, dxm = (np.zeros((tokens, C)) for _ in range(4))
+    yr[:] = 7.0
+    dwr, dwm, dbr, dbm = np.zeros((C, W)), np.zeros((C, W)), np.zeros(C), np.zeros(C)
+    for b, (lo, hi) in enumerate(spans(B, T, cu)):
+        yr[lo:hi], last = R.conv_fwd(xn[lo:hi], wn, bn, s0n[b], act)
+        np.testing.assert_array_equal(np64(sT[b]), last)
+        _, pre = R.conv_pre(xn[lo:hi], wn, bn, s0n[b])
+        _, big = R.conv_pre(np.abs(xn[lo:hi]), np.abs(wn), np.abs(bn), np.abs(s0n[b]))
+        ym[lo:hi] = big
+        a, c, d, e = R.conv_bwd(xn[lo:hi], wn, bn, s0n[b], dyn[lo:hi], dsn[b], act)
+        # the derivative moves with pre by at most half its error
+        scale = (1.0 + big) if act else np.ones_like(big)
+        am, cm, dm, em = R.conv_bwd(np.abs(xn[lo:hi]), np.abs(wn), np.abs(bn), np.abs(s0n[b]), np.abs(dyn[lo:hi]) * scale * 1.1,
+                                    np.abs(dsn[b]), 0)
+        dxr[lo:hi], dxm[lo:hi] = a, am
+        dwr += c
+        dwm += cm
+        dbr += d
+        dbm += dm
+        close(ds0[b], e, em, 2.0 ** -20, f"dstate0[{b}]")
+    close(y, yr, ym, 2.0 ** -20, "y")
+    close(dx, dxr, dxm, 2.0 ** -20, "dx")
+    sums = 2.0 ** -20 + 2.0 ** -24 * min(tokens, 512)  # sums over tokens: 32 a lane, then 8 and the workgroups
+    close(dw, dwr, dwm, sums, "dweight")
+    close(db, dbr, dbm, sums, "dbias")
+    if extra:
+        assert (dxb[:, :8] == 9).all() and (dxb[:, 8 + C:] == 9).all()
+
+
+@pytest.mark.parametrize("dtype,B,C,W,pool", [(BF, 5, 264, 4, True), (F32, 1, 8, 2, True), (BF, 3, 2312, 3, False)])
+def test_conv_step_continues_the_forward(dtype, B, C, W, pool):
+    g = gen(B)
+    T = 6
+    x = draw(g, B, T, C, dtype=dtype)
+    w, bv, s0 = draw(g, C, W, dtype=F32), draw(g, C, dtype=F32), draw(g, B, W - 1, C, dtype=dtype)
+    full = la.ConvConfig(B=B, T=T, C=C, width=W, x_dtype=CODE[dtype])
+    y, sT = torch.empty_like(x), torch.empty_like(s0)
+    la.la_conv_fwd(full, x, w, bv, s0, y, sT)
+    cfg = la.ConvConfig(B=B, T=1, C=C, width=W, x_dtype=CODE[dtype])
+    if pool:
+        state = draw(g, B + 3, W - 1, C, dtype=dtype)
+        before = state.clone()
+        slots = torch.arange(B + 1, 1, -1, dtype=torch.int32, device="cuda")
+        state[slots.long()] = s0
+        if B > 2:
+            slots[1], slots[2] = 0, B + 3  # padding
+    else:
+        state, slots = s0.clone(), None
+    for t in range(T):
+        yt = torch.full((B, C), float("nan"), dtype=dtype, device="cuda")
+        la.la_conv_step(cfg, x[:, t].contiguous(), w, bv, state, yt, slots=slots, n_slots=B + 3 if pool else 0)
+        for b in range(B):
+            if pool and B > 2 and b in (1, 2):
+                assert not yt[b].any()
+            else:
+                assert torch.equal(yt[b], y[b, t]), (b, t)
+    for b in range(B):
+        if pool and B > 2 and b in (1, 2):
+            continue
+        assert torch.equal(state[int(slots[b]) if pool else b], sT[b])
+    if pool:
+        assert torch.equal(state[0], before[0])
+
+
+# -------------------------------------------------------------------------------------- scan
+class Scan:
+    """One case's inputs, in slices of wider rows, and its 64-bit results."""
+
+    def __init__(self, dtype, B, T, H, G, N, P, cu=None, sp=1, seed=0, states=True, params=True, extra=8, dtt=None, rate=4.0,
+                 out=None):
+        g = gen(1000 * T + 10 * H + N + seed)
+        self.dtype, self.B, self.T, self.H, self.G, self.N, self.P, self.cu, self.sp = dtype, B, T, H, G, N, P, cu, sp
+        self.states, self.params, self.out, self.dtt = states, params, out or dtype, dtt or dtype
+        self.tokens = n = T if cu is not None else B * T
+        self.wx, self.wb = H * P, G * N
+        self.ld = self.wx + 2 * self.wb + extra
+        self.buf = draw(g, n, self.ld, dtype=dtype, scale=0.7)
+        self.x, self.b, self.c = self.cut(self.buf)
+        self.dt = draw(g, n, H, dtype=self.dtt) if sp else draw(g, n, H, dtype=self.dtt).abs()
+        self.A = -torch.rand(H, generator=g).cuda() * rate
+        self.D = draw(g, H, dtype=F32) if params else None
+        self.bias = draw(g, H, dtype=F32) - 2.0 if params and sp else None
+        self.S0 = draw(g, B, H, N, P, dtype=F32) if states else None
+        self.dST = draw(g, B, H, N, P, dtype=F32) if states else None
+        self.dy = draw(g, n, H * P, dtype=self.out)
+        self.cfg = la.ScanConfig(B=B, T=T, H=H, G=G, d_k=N, d_v=P, softplus=sp, x_dtype=CODE[dtype], dt_dtype=CODE[self.dtt],
+                                 out_dtype=CODE[self.out], ld_x=self.ld, ld_b=self.ld, ld_c=self.ld)
+
+    def cut(self, buf):
+        return buf[:, :self.wx], buf[:, self.wx:self.wx + self.wb], buf[:, self.wx + self.wb:self.wx + 2 * self.wb]
+
+    def fwd(self, stream=None):
+        y = torch.full((self.tokens, self.H * self.P), 5.0, dtype=self.out, device="cuda")
+        ST = torch.full((self.B, self.H, self.N, self.P), float("nan"), device="cuda")
+        n = la.la_scan_workspace_bytes(self.cfg)
+        ws = torch.full((max(n, 1),), 255, dtype=torch.uint8, device="cuda")
+        la.la_scan_fwd(self.cfg, self.x, self.dt, self.A, self.b, self.c, self.D, self.bias, self.S0, y, ST,
+                       ws if n else None, n, cu_seqlens=cu_tensor(self.cu), stream=stream)
+        return y, ST
+
+    def out_buffers(self):
+        nan = lambda *s: torch.full(s, float("nan"), device="cuda")  # noqa: E731
+        buf = torch.full_like(self.buf, 9.0)
+        dx, db, dc = self.cut(buf)
+        return buf, dict(dx=dx, db=db, dc=dc, ddt=torch.full_like(self.dt, 9.0), dA=nan(self.H), dD=nan(self.H),
+                         ddt_bias=nan(self.H), dS0=nan(self.B, self.H, self.N, self.P))
+
+    def bwd_into(self, bufs):
+        o = bufs[1]
+        n = la.la_scan_bwd_workspace_bytes(self.cfg)
+        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        la.la_scan_bwd(self.cfg, self.x, self.dt, self.A, self.b, self.c, self.D, self.bias, self.S0, self.dy, self.dST, o["dx"],
+                       o["ddt"], o["dA"], o["db"], o["dc"], o["dD"], o["ddt_bias"], o["dS0"], ws, n,
+                       cu_seqlens=cu_tensor(self.cu))
+        return o
+
+    def bwd(self):
+        bufs = self.out_buffers()
+        o = self.bwd_into(bufs)
+        assert (bufs[0][:, self.wx + 2 * self.wb:] == 9).all()
+        return o
+
+    def reference(self, backward):
+        n, H, G, N, P = self.tokens, self.H, self.G, self.N, self.P
+        x, b, c = np64(self.x).reshape(n, H, P), np64(self.b).reshape(n, G, N), np64(self.c).reshape(n, G, N)
+        dy = np64(self.dy).reshape(n, H, P)
+        A = np64(self.A)
+        D = np64(self.D) if self.D is not None else np.zeros(H)
+        z, delta = R.steps(np64(self.dt), np64(self.bias) if self.bias is not None else np.zeros(H), self.sp)
+        zero = np.zeros((self.B, H, N, P))
+        S0, dST = (np64(self.S0), np64(self.dST)) if self.states else (zero, zero)
+        w = dict(y=np.full((n, H, P), 5.0), S_T=zero.copy())
+        m = dict(y=np.zeros((n, H, P)), S_T=zero.copy())
+        if backward:
+            shapes = dict(dx=(n, H, P), db=(n, G, N), dc=(n, G, N), ddt=(n, H), dA=(H,), dD=(H,), ddt_bias=(H,), dS0=zero.shape)
+            for k, s in shapes.items():
+                w[k], m[k] = np.zeros(s), np.zeros(s)
+        a = np.abs
+        for i, (lo, hi) in enumerate(spans(self.B, self.T, self.cu)):
+            r = slice(lo, hi)
+            w["y"][r], w["S_T"][i], _ = R.scan_fwd(x[r], delta[r], A, b[r], c[r], D, S0[i])
+            m["y"][r], m["S_T"][i], _ = R.scan_fwd(a(x[r]), a(delta[r]), A, a(b[r]), a(c[r]), a(D), a(S0[i]))
+            if not backward:
+                continue
+            got, _ = R.scan_bwd(x[r], z[r], delta[r], A, b[r], c[r], D, S0[i], dy[r], dST[i], self.sp)
+            big, _ = R.scan_bwd(a(x[r]), z[r], a(delta[r]), A, a(b[r]), a(c[r]), a(D), a(S0[i]), a(dy[r]), a(dST[i]), self.sp,
+                                A_sum=a(A))
+            # the rates' gradients: suffix sums of y.dy - x.dx (without D) over a chunk, and the state's part at its end
+            T = hi - lo
+            yn, S_end, st = R.scan_fwd(a(x[r]), a(delta[r]), A, a(b[r]), a(c[r]), 0 * D, a(S0[i]))
+            dxn = big["dx"] - a(D)[:, None] * a(dy[r])
+            terms = (yn * a(dy[r])).sum(2) + (dxn * a(x[r])).sum(2)
+            chunk = np.zeros((T, H))
+            for t0 in range(0, T, 64):
+                t1 = min(T, t0 + 64)
+                # <S_end, dS_end> of the chunk: the sums of b, x against the gradient that leaves it
+                endS = st[t1]
+                nxt = R.scan_bwd(a(x[r])[t1:], z[r][t1:], a(delta[r])[t1:], A, a(b[r])[t1:], a(c[r])[t1:], a(D), endS,
+                                 a(dy[r])[t1:], a(dST[i]), self.sp, A_sum=a(A))[0]["dS0"]
+                chunk[t0:t1] = terms[t0:t1].sum(0) + (endS * nxt).sum((1, 2))
+            sg = 1 / (1 + np.exp(-z[r])) if self.sp else 1.0
+            extra = dict(ddt=a(A) * chunk * sg, dA=(a(delta[r]) * chunk).sum(0), ddt_bias=(a(A) * chunk * sg).sum(0))
+            for k in shapes:
+                v, u = got[k], big[k] + extra.get(k, 0.0)
+                if k in ("dA", "dD", "ddt_bias"):
+                    w[k] += v
+                    m[k] += u
+                elif k == "dS0":
+                    w[k][i], m[k][i] = v, u
+                else:
+                    w[k][r], m[k][r] = v, u
+        return w, m
+
+    def check(self, backward=True):
+        w, m = self.reference(backward)
+        y, ST = self.fwd()
+        share = 2.0 ** -14
+        close(y.reshape(w["y"].shape), w["y"], m["y"], share, "y")
+        close(ST, w["S_T"], m["S_T"], share, "S_T")
+        if not backward:
+            return
+        o = self.bwd()
+        for k, t in o.items():
+            if k == "dD" and self.D is None or k == "ddt_bias" and self.bias is None:
+                pass  # written all the same
+            close(t.reshape(w[k].shape), w[k], m[k], share, k)
+
+
+SCAN = [
+    # dtype, B, T, H, G, d_k, d_v, more
+    (BF, 2, 1, 2, 1, 16, 64, {}),
+    (BF, 1, 2, 3, 3, 32, 64, {}),
+    (BF, 2, 63, 4, 2, 64, 64, {}),
+    (BF, 1, 64, 2, 1, 128, 128, {}),
+    (BF, 2, 65, 4, 1, 128, 64, {}),
+    (BF, 1, 130, 5, 1, 64, 192, dict(states=False)),
+    (BF, 1, 200, 2, 2, 16, 64, dict(params=False)),
+    (BF, 1, 100, 2, 1, 128, 64, dict(sp=0, rate=0.5)),
+    (BF, 1, 150, 2, 1, 64, 64, dict(rate=30.0)),
+    (F32, 2, 1, 2, 1, 64, 64, {}),
+    (F32, 1, 65, 4, 2, 16, 64, {}),
+    (F32, 1, 130, 2, 1, 128, 128, {}),
+    (F32, 2, 90, 3, 1, 32, 64, dict(sp=0, rate=0.5, states=False)),
+    (BF, 1, 70, 2, 1, 64, 64, dict(dtt=F32)),
+    (BF, 6, 300, 2, 1, 64, 64, dict(cu=[2, 2, 66, 67, 131, 260, 290])),
+    (F32, 3, 80, 2, 2, 32, 64, dict(cu=[0, 80, 80, 80])),
+    (BF, 3, 200, 4, 1, 128, 128, dict(cu=[0, 0, 129, 200])),
+    (BF, 1, 700, 2, 1, 32, 64, {}),     # few heads: the walks cut into segments / chunks
+    (F32, 1, 1025, 1, 1, 16, 64, {}),
+    (BF, 3, 1200, 1, 1, 16, 64, dict(cu=[0, 900, 900, 1190])),
+    (BF, 4, 70, 64, 2, 16, 64, {}),     # many heads: a workgroup walks a sequence
+]
+
+
+@pytest.mark.parametrize("dtype,B,T,H,G,N,P,more", SCAN)
+def test_scan(dtype, B, T, H, G, N, P, more):
+    Scan(dtype, B, T, H, G, N, P, **more).check()
+
+
+def test_scan_mixed_output_dtypes():
+    Scan(BF, 1, 100, 2, 1, 64, 64, out=F32).check(backward=False)
+    Scan(F32, 1, 100, 2, 1, 64, 64, out=BF).check(backward=False)
+
+
+def test_scan_steps_that_vanish_and_explode():
+    """Delta = 0 leaves the state; a very negative rate empties it within a token."""
+    k = Scan(BF, 1, 130, 2, 1, 64, 64, sp=0)
+    k.dt[:65] = 0
+    k.dt[100] = 200.0
+    k.A[:] = -5.0
+    k.check()
+
+
+def test_scan_without_tokens():
+    for cu, T in ((None, 0), ([0, 0, 0], 4)):
+        k = Scan(BF, 2, max(T, 1), 2, 1, 64, 64, cu=[0, 0, 0])
+        k.cfg.T = T
+        k.cu = cu
+        y, ST = k.fwd()
+        assert torch.equal(ST, k.S0) and (y == 5).all()
+        o = k.bwd()
+        assert torch.equal(o["dS0"], k.dST)
+        for n in ("dA", "dD", "ddt_bias"):
+            assert not o[n].any()
+        if T:
+            assert not o["dx"].any() and not o["ddt"].any() and not o["db"].any() and not o["dc"].any()
+
+
+@pytest.mark.parametrize("B,H,G,N,P,dtype", [(1, 2, 1, 16, 64, BF), (3, 4, 2, 32, 64, F32), (2, 3, 1, 64, 192, BF),
+                                             (5, 16, 1, 128, 128, BF), (40, 16, 1, 64, 64, F32), (70, 16, 2, 16, 128, BF)])
+def test_scan_step(B, H, G, N, P, dtype):
+    g = gen(B + H)
+    cfg = la.ScanConfig(B=B, T=1, H=H, G=G, d_k=N, d_v=P, x_dtype=CODE[dtype], dt_dtype=CODE[dtype], out_dtype=CODE[dtype])
+    x, b, c = draw(g, B, H, P, dtype=dtype), draw(g, B, G, N, dtype=dtype), draw(g, B, G, N, dtype=dtype)
+    dt, A, D, bias = draw(g, B, H, dtype=dtype), -torch.rand(H, generator=g).cuda() * 4, draw(g, H, dtype=F32), draw(g, H, dtype=F32)
+    pool = draw(g, B + 3, H, N, P, dtype=F32)
+    slots = (torch.randperm(B + 2, generator=g)[:B] + 1).to(torch.int32).cuda()
+    if B > 2:
+        slots[1], slots[2] = 0, B + 3
+    before = pool.clone()
+    y = torch.full((B, H, P), float("nan"), dtype=dtype, device="cuda")
+    la.la_scan_step(cfg, x, dt, A, b, c, D, bias, pool, y, slots=slots, n_slots=B + 3)
+    _, delta = R.steps(np64(dt), np64(bias), 1)
+    touched = set()
+    for i in range(B):
+        s = int(slots[i])
+        if s <= 0 or s >= B + 3:
+            assert not y[i].any()
+            continue
+        touched.add(s)
+        want, S, _ = R.scan_fwd(np64(x[i:i + 1]), delta[i:i + 1], np64(A), np64(b[i:i + 1]), np64(c[i:i + 1]), np64(D), np64(before[s]))
+        mag, Sm, _ = R.scan_fwd(*(np.abs(v) for v in (np64(x[i:i + 1]), delta[i:i + 1])), np64(A), np.abs(np64(b[i:i + 1])),
+                                np.abs(np64(c[i:i + 1])), np.abs(np64(D)), np.abs(np64(before[s])))
+        close(y[i], want[0], mag[0], 2.0 ** -17, "y")  # at most 129 FP32 terms
+        close(pool[s], S, Sm, 2.0 ** -21, "S")
+    for s in range(B + 3):
+        if s not in touched:
+            assert torch.equal(pool[s], before[s])
+    if B <= 3:  # without slots: the states in order
+        st = before[:B].clone()
+        y2 = torch.empty_like(y)
+        la.la_scan_step(cfg, x, dt, A, b, c, D, bias, st, y2)
+        i = 0
+        pool2 = before.clone()
+        one = torch.zeros(B, dtype=torch.int32, device="cuda")
+        one[i] = 1
+        pool2[1] = before[0]
+        la.la_scan_step(cfg, x, dt, A, b, c, D, bias, pool2, y, slots=one, n_slots=B + 3)
+        assert torch.equal(y2[0], y[0]) and torch.equal(pool2[1], st[0])
+
+
+# -------------------------------------------------------------------------------------- norm
+NORM = [
+    # dtype, rows, d, codec, group, out, weights, residual
+    (BF, 5, 8, "none", 0, BF, F32, True), (BF, 3, 64, "int8", 0, BF, F32, True), (F32, 7, 96, "int8", 16, F32, F32, True),
+    (BF, 9, 128, "e4m3", 128, BF, BF, True), (BF, 4, 256, "int8", 64, F32, F32, False), (F32, 2, 520, "e4m3", 0, F32, None, True),
+    (BF, 33, 1024, "e4m3", 32, F32, F32, True), (BF, 6, 2048, "int8", 128, BF, F32, True), (BF, 3, 2056, "none", 0, F32, F32, True),
+    (F32, 2, 4096, "int8", 0, F32, BF, True), (BF, 2, 8192, "e4m3", 16, BF, F32, True), (BF, 2, 16384, "none", 0, F32, F32, True),
+    (BF, 1, 16384, "int8", 32, F32, F32, True), (BF, 1000, 72, "none", 0, BF, F32, True),
+]
+
+
+@pytest.mark.parametrize("dtype,rows,d,kind,group,out,wt,residual", NORM)
+def test_norm(dtype, rows, d, kind, group, out, wt, residual):
+    g = gen(rows + d)
+    x = draw(g, rows, d, dtype=dtype)
+    res = draw(g, rows, d, dtype=dtype, scale=3.0) if residual else None
+    w = draw(g, d, dtype=wt) if wt is not None else None
+    x[0] = 0
+    if residual:
+        res[0] = 0  # a row of zeros
+    eps = 1e-5
+    qdq = {"none": la.LA_QDQ_NONE, "int8": la.LA_QDQ_INT8_GROUP, "e4m3": la.LA_QDQ_E4M3_TILE}[kind]
+    cfg = la.NormConfig(rows=rows, d=d, eps=eps, qdq=qdq, group=group, x_dtype=CODE[dtype], w_dtype=CODE[wt or F32],
+                        out_dtype=CODE[out])
+    ro, y = torch.empty_like(x), torch.empty(rows, d, dtype=out, device="cuda")
+    codes = scales = None
+    if kind != "none":
+        codes = torch.empty(rows, d, dtype=torch.int8 if kind == "int8" else torch.float8_e4m3fn, device="cuda")
+        scales = torch.empty(rows, d // (group or d), device="cuda")
+    la.la_norm_fwd(cfg, x, res, w, ro, y, codes, scales)
+    h = (x.float() + res.float()).to(dtype) if residual else x
+    assert torch.equal(ro, h)
+    hn, wn = np64(h), np64(w) if w is not None else np.ones(d)
+    n, _ = R.norm_fwd(hn, wn, eps)
+    tol = 2.0 ** -19
+    if kind == "none":
+        close(y, n, np.abs(n), tol, "y")
+    else:
+        v, s, step = R.codec(n, group, kind)
+        close(scales, s, s, tol, "scales")
+        # a value next to a rounding border may take the neighbouring code: one step, at most one in 2000
+        # (borders are a step apart, the error is below 2^-18 of 127 or 448 steps: 2 x 448 x 2^-18 = 1 in 290 at most)
+        got = np64(y)
+        off = np.abs(got - v) - (HALF[out] * 1.01 * np.abs(v) + 2 * tol * np.abs(v) + 1e-30)
+        assert (off <= 1.01 * step).all() and (off > 0).mean() <= 1 / 290
+        stood = np64(codes.float()) * np.repeat(np64(scales), group or d, 1)
+        np.testing.assert_array_less(np.abs(got - stood), HALF[out] * 1.01 * np.abs(stood) + 2.0 ** -23 * np.abs(stood) + 1e-30)
+    # backward
+    dy, dres = draw(g, rows, d, dtype=out), draw(g, rows, d, dtype=dtype)
+    dx, dw = torch.empty_like(x), torch.full((d,), float("nan"), device="cuda")
+    nb = la.la_norm_bwd_workspace_bytes(cfg)
+    ws = torch.full((nb,), 255, dtype=torch.uint8, device="cuda")
+    la.la_norm_bwd(cfg, h, w, dy, dres, dx, dw, ws, nb)
+    dxr, dwr = R.norm_bwd(hn, wn, eps, np64(dy), np64(dres))
+    a = np.abs
+    r = 1 / np.sqrt((hn * hn).mean(1, keepdims=True) + eps)
+    gm = a(np64(dy) * wn)
+    mag = a(np64(dres)) + r * (gm + a(hn) * r * r * (gm * a(hn)).mean(1, keepdims=True))
+    close(dx, dxr, mag, tol, "dx")
+    close(dw, dwr, (a(np64(dy)) * a(hn) * r).sum(0), tol + rows * 2.0 ** -24, "dweight")
+    # without the optional tensors, in place
+    same = dres.clone()
+    la.la_norm_bwd(cfg, h, w, dy, same, same, None, None, 0)
+    assert torch.equal(same, dx)
+    y2, x2 = torch.empty_like(y), x.clone()
+    la.la_norm_fwd(cfg, x2, res, w, x2, y2)
+    assert torch.equal(x2, ro) and torch.equal(y2, y)
+
+
+def test_norm_keeps_infinities_and_nan_in_their_rows():
+    for qdq in (la.LA_QDQ_NONE, la.LA_QDQ_INT8_GROUP, la.LA_QDQ_E4M3_TILE):
+        x = torch.ones(4, 256, dtype=BF, device="cuda")
+        x[1, 3], x[2, 7] = float("nan"), float("inf")
+        cfg = la.NormConfig(rows=4, d=256, eps=0.0, qdq=qdq, group=0)
+        y = torch.empty_like(x)
+        la.la_norm_fwd(cfg, x, None, None, None, y)
+        ones = torch.ones(256, dtype=BF, device="cuda")
+        assert torch.equal(y[0], ones) and torch.equal(y[3], ones)
+        assert torch.isnan(y[1]).all() and torch.isnan(y[2, 7])
+
+
+# ----------------------------------------------------------------------------- run together
+class Layer:
+    """norm (8-bit) -> projection -> convolution -> scan -> projection, as a hybrid stack runs them."""
+
+    def __init__(self, d=256, H=4, G=1, N=64, P=64, seed=5):
+        g = gen(seed)
+        self.d, self.H, self.G, self.N, self.P = d, H, G, N, P
+        self.C = H * P + 2 * G * N
+        self.W = self.C + 8  # the projection's rows: the convolution's channels, dt, unused (a multiple of 16 bytes)
+        self.w, self.cw, self.cb = 1 + draw(g, d, dtype=F32, scale=0.1), draw(g, self.C, 4, dtype=F32, scale=0.4), draw(g, self.C, dtype=F32, scale=0.1)
+        self.win, self.wout = draw(g, d, self.W, scale=d ** -0.5), draw(g, H * P, d, scale=(H * P) ** -0.5)
+        self.A, self.D, self.bias = -torch.rand(H, generator=g).cuda() * 4, draw(g, H, dtype=F32), draw(g, H, dtype=F32) - 2
+
+    def prefill(self, x, res, B, T, cu=None):
+        n = x.shape[0]
+        h, y = torch.empty_like(x), torch.empty_like(x)
+        codes, scales = torch.empty(n, self.d, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(n, 1, device="cuda")
+        la.la_norm_fwd(la.NormConfig(rows=n, d=self.d, qdq=la.LA_QDQ_E4M3_TILE), x, res, self.w, h, y, codes, scales)
+        proj = y @ self.win
+        z, cs = torch.empty(n, self.C, dtype=BF, device="cuda"), torch.zeros(B, 3, self.C, dtype=BF, device="cuda")
+        la.la_conv_fwd(la.ConvConfig(B=B, T=T, C=self.C, width=4, ld_x=self.W), proj[:, :self.C], self.cw, self.cb, None, z, cs, cu_seqlens=cu)
+        cfg = la.ScanConfig(B=B, T=T, H=self.H, G=self.G, d_k=self.N, d_v=self.P, ld_x=self.C, ld_b=self.C, ld_c=self.C, ld_dt=self.W)
+        o, S = torch.zeros(n, self.H * self.P, dtype=BF, device="cuda"), torch.zeros(B, self.H, self.N, self.P, device="cuda")
+        nb = la.la_scan_workspace_bytes(cfg)
+        ws = torch.empty(max(nb, 1), dtype=torch.uint8, device="cuda")
+        i, j = self.H * self.P, self.H * self.P + self.G * self.N
+        la.la_scan_fwd(cfg, z[:, :i], proj[:, self.C:self.C + self.H], self.A, z[:, i:j], z[:, j:], self.D, self.bias, None, o, S, ws, nb, cu_seqlens=cu)
+        return o @ self.wout, h, cs, S
+
+    def step(self, x, res, cs, S):
+        B = x.shape[0]
+        h, y = torch.empty_like(x), torch.empty_like(x)
+        la.la_norm_fwd(la.NormConfig(rows=B, d=self.d, qdq=la.LA_QDQ_E4M3_TILE), x, res, self.w, h, y)
+        proj = y @ self.win
+        z, o = torch.empty(B, self.C, dtype=BF, device="cuda"), torch.empty(B, self.H * self.P, dtype=BF, device="cuda")
+        la.la_conv_step(la.ConvConfig(B=B, T=1, C=self.C, width=4, ld_x=self.W), proj[:, :self.C], self.cw, self.cb, cs, z)
+        i, j = self.H * self.P, self.H * self.P + self.G * self.N
+        cfg = la.ScanConfig(B=B, T=1, H=self.H, G=self.G, d_k=self.N, d_v=self.P, ld_x=self.C, ld_b=self.C, ld_c=self.C, ld_dt=self.W)
+        la.la_scan_step(cfg, z[:, :i], proj[:, self.C:self.C + self.H], self.A, z[:, i:j], z[:, j:], self.D, self.bias, S, o)
+        return o @ self.wout, h
+
+
+def test_layer_prompt_then_tokens():
+    """A prompt of T tokens followed by single tokens equals one prompt of all of them, dense and packed."""
+    m, g = Layer(), gen(6)
+    B, T, more = 3, 70, 4
+    x, res = draw(g, B, T + more, m.d), draw(g, B, T + more, m.d)
+    full, _, cs_full, S_full = m.prefill(x.reshape(-1, m.d), res.reshape(-1, m.d), B, T + more)
+    full = full.reshape(B, T + more, -1)
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * T
+    px, pr = x[:, :T].reshape(-1, m.d).contiguous(), res[:, :T].reshape(-1, m.d).contiguous()
+    out, _, cs, S = m.prefill(px, pr, B, B * T, cu=cu)
+    # a bf16 result of the same inputs, computed with sums in another order: a step of its type
+    torch.testing.assert_close(out.reshape(B, T, -1), full[:, :T], rtol=2 ** -6, atol=2 ** -6)
+    for t in range(more):
+        o, _ = m.step(x[:, T + t].contiguous(), res[:, T + t].contiguous(), cs, S)
+        torch.testing.assert_close(o, full[:, T + t], rtol=2 ** -6, atol=2 ** -6)
+    # the states hold bf16 roundings of the convolution's outputs, some of them one step apart
+    assert torch.equal(cs, cs_full) or (cs.float() - cs_full.float()).abs().max() < 0.1
+    assert (S - S_full).norm() <= 2 ** -7 * S_full.norm()
+
+
+def test_calls_repeat_bit_for_bit_and_on_other_streams():
+    k = Scan(BF, 1, 700, 2, 1, 32, 64)
+    y, ST = k.fwd()
+    a = k.bwd()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        y1, S1 = k.fwd()
+        b = k.bwd()
+    with torch.cuda.stream(other):
+        y2, S2 = k.fwd()
+        c = k.bwd()
+    torch.cuda.synchronize()
+    assert torch.equal(y, y1) and torch.equal(ST, S1) and torch.equal(y, y2) and torch.equal(ST, S2)
+    for n in a:
+        assert torch.equal(a[n], b[n]) and torch.equal(a[n], c[n]), n
+
+
+def test_captured_layer_replays():
+    m, g = Layer(), gen(8)
+    B = 2
+    x, res = draw(g, B * 130, m.d), draw(g, B * 130, m.d)
+    tx, tr = draw(g, B, m.d), draw(g, B, m.d)
+    _, _, cs0, S0 = m.prefill(x, res, B, 130)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # warm up
+        m.prefill(x, res, B, 130)
+        m.step(tx, tr, cs0.clone(), S0.clone())
+    torch.cuda.current_stream().wait_stream(side)
+    cs, S = cs0.clone(), S0.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, h, cs_p, S_p = m.prefill(x, res, B, 130)
+        o, hs = m.step(tx, tr, cs, S)
+    for i in range(4):
+        x.copy_(draw(gen(20 + i), B * 130, m.d))
+        tx.copy_(draw(gen(30 + i), B, m.d))
+        cs_e, S_e = cs.clone(), S.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        e_out, e_h, e_cs, e_S = m.prefill(x, res, B, 130)
+        e_o, _ = m.step(tx, tr, cs_e, S_e)
+        torch.cuda.synchronize()
+        for a, b in ((out, e_out), (h, e_h), (cs_p, e_cs), (S_p, e_S), (o, e_o), (cs, cs_e), (S, S_e)):
+            assert torch.equal(a, b), i
+
+
+def test_captured_backward_replays():
+    k = Scan(BF, 2, 140, 2, 1, 64, 64)
+    g = gen(9)
+    n, C = 2 * 140, 64
+    x, w, dy = draw(g, n, C), draw(g, C, 4, dtype=F32), draw(g, n, C)
+    cc = la.ConvConfig(B=2, T=140, C=C, width=4)
+    nc = la.NormConfig(rows=n, d=C)
+
+    def run():
+        o = k.bwd_into(k.out_buffers())
+        dx, dw, ds = torch.empty_like(x), torch.empty_like(w), torch.empty(2, 3, C, dtype=BF, device="cuda")
+        b = la.la_conv_bwd_workspace_bytes(cc)
+        la.la_conv_bwd(cc, x, w, None, None, dy, None, dx, dw, None, ds, torch.empty(b, dtype=torch.uint8, device="cuda"), b)
+        nx, nw = torch.empty_like(x), torch.empty(C, device="cuda")
+        b = la.la_norm_bwd_workspace_bytes(nc)
+        la.la_norm_bwd(nc, x, None, dy, None, nx, nw, torch.empty(b, dtype=torch.uint8, device="cuda"), b)
+        return [o[i] for i in sorted(o)] + [dx, dw, ds, nx, nw]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = run()
+    for i in range(3):
+        x.copy_(draw(gen(40 + i), n, C))
+        k.buf.copy_(draw(gen(50 + i), *k.buf.shape))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, run()):
+            assert torch.equal(a, b), i
+
+
+def test_binding_refuses_layouts():
+    x = torch.zeros(2, 8, 64, dtype=BF, device="cuda")
+    w = torch.zeros(64, 4, device="cuda")
+    cfg = la.ConvConfig(B=2, T=8, C=64, width=4)
+    y = torch.empty_like(x)
+    with pytest.raises(ValueError, match="strides"):
+        la.la_conv_fwd(cfg, x.transpose(0, 1), w, None, None, y)
+    with pytest.raises(ValueError, match="holds 512"):
+        la.la_conv_fwd(cfg, x[:1], w, None, None, y)
+    with pytest.raises(ValueError, match="dtype"):
+        la.la_conv_fwd(cfg, x.float(), w, None, None, y)
+    with pytest.raises(ValueError, match="contiguous"):
+        la.la_conv_fwd(cfg, x, torch.zeros(4, 64, device="cuda").t(), None, None, y)
+    wide = torch.zeros(2, 8, 96, dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="strides"):
+        la.la_conv_fwd(cfg, wide[..., :64], w, None, None, y)
+    la.la_conv_fwd(la.ConvConfig(B=2, T=8, C=64, width=4, ld_x=96), wide[..., 8:72], w, None, None, y)
+    with pytest.raises(ValueError, match="GPU"):
+        la.la_conv_fwd(cfg, x, w.cpu(), None, None, y)
