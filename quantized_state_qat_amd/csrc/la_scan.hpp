@@ -19,12 +19,23 @@ namespace la {
 constexpr int kQ = 64;   // tokens a chunk
 constexpr int kPT = 64;  // value columns a workgroup
 
-// LDS row of n elements: strides for which 16 rows fall on different 16-byte bank slots, and,
-// in bf16, the transposed reads' four rows of 32 bytes too.
+// LDS row of n elements.  bf16: 32 bytes over a multiple of 256 or 64 (288, 160, 96) for rows that
+// are read in 16-byte pieces (8.3 cycles a kilobyte against 9.5 at 16 bytes over), 144 bytes for
+// the 64-wide rows that are also written in 8-byte pieces (10 cycles against 17).  Two 8-byte reads
+// or transposed reads take 17 cycles a kilobyte at any of these, so a row operand is always one
+// 16-byte piece a lane.
 template <class T>
 constexpr int lds_row(int n) {
-    return sizeof(T) == 2 ? (n == 128 ? 152 : n == 64 ? 72 : 56) : n + 4;
+    return sizeof(T) == 2 ? (n == 128 ? 144 : n == 64 ? 80 : 48) : n + 4;
 }
+template <class T>
+constexpr int lds_row64() {
+    return sizeof(T) == 2 ? 72 : 68;
+}
+
+// State rows in the accumulators: register r of tile i in lane group g is row state_n(i, 4 g + r),
+// so that two tiles hold the eight consecutive rows of a lane's operand piece.
+__device__ __forceinline__ int state_n(int i, int m) { return 32 * (i >> 1) + 8 * (m >> 2) + 4 * (i & 1) + (m & 3); }
 
 template <class T>
 struct Mat;
@@ -39,20 +50,21 @@ struct Mat<uint16_t> {
     }
     // Row operand: 8 consecutive elements from k (lane group g: k = 32 i + 8 g).
     static __device__ __forceinline__ Frag row8(const uint16_t* p) { return *reinterpret_cast<const bf8*>(p); }
-    // Row operand in the accumulators' order: 4 elements at p and 4 at p + 16 (p at 32 i + 4 g),
-    // as two tiles of a product's result hold them.
-    static __device__ __forceinline__ Frag row44(const uint16_t* p) {
-        const uv2 a = *reinterpret_cast<const uv2*>(p), b = *reinterpret_cast<const uv2*>(p + 16);
-        return __builtin_bit_cast(Frag, uv4{a[0], a[1], b[0], b[1]});
-    }
     // Column operand: rows r0 + 8 g .. + 7 of column c0 + lane % 16, by two transposed reads (in
     // each 16 lanes, lane 4 j + q addresses row j's 8 bytes q and lane i receives column i).
-    static __device__ __forceinline__ Frag col8(const uint16_t* base, int stride, int r0, int c0, int lane) {
-        const int i = lane & 15, g = lane >> 4;
-        const uint16_t* p = base + (r0 + 8 * g + (i >> 2)) * stride + c0 + 4 * (i & 3);
+    static __device__ __forceinline__ Frag tr8(const uint16_t* p, int stride) {
         const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p));
         const s4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + 4 * stride));
         return __builtin_bit_cast(Frag, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    static __device__ __forceinline__ Frag col8(const uint16_t* base, int stride, int r0, int c0, int lane) {
+        const int i = lane & 15, g = lane >> 4;
+        return tr8(base + (r0 + 8 * g + (i >> 2)) * stride + c0 + 4 * (i & 3), stride);
+    }
+    // The same of column state_n(tile, lane % 16).
+    static __device__ __forceinline__ Frag col8_state(const uint16_t* base, int stride, int r0, int tile, int lane) {
+        const int i = lane & 15, g = lane >> 4;
+        return tr8(base + (r0 + 8 * g + (i >> 2)) * stride + state_n(tile, 4 * (i & 3)), stride);
     }
     static __device__ __forceinline__ void widen8(Frag f, float (&v)[8]) { widen(__builtin_bit_cast(uv4, f), v); }
     // x = sum of the P parts (P = 2: to 2^-17 of x; P = 3: exactly).
@@ -114,13 +126,15 @@ struct Mat<float> {
         return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
     }
     static __device__ __forceinline__ Frag row8(const float* p) { return two(p, p + 4); }
-    static __device__ __forceinline__ Frag row44(const float* p) { return two(p, p + 16); }
     static __device__ __forceinline__ Frag col8(const float* base, int stride, int r0, int c0, int lane) {
         const float* p = base + (r0 + 8 * (lane >> 4)) * stride + c0 + (lane & 15);
         Frag f;
 #pragma unroll
         for (int j = 0; j < 8; j++) f[j] = p[j * stride];
         return f;
+    }
+    static __device__ __forceinline__ Frag col8_state(const float* base, int stride, int r0, int tile, int lane) {
+        return col8(base, stride, r0, state_n(tile, lane & 15) - (lane & 15), lane);
     }
     static __device__ __forceinline__ void widen8(Frag f, float (&v)[8]) {
 #pragma unroll
@@ -183,6 +197,7 @@ struct Decay {
     float delta[kQ];       // 0 behind the sequence
     float head[kQ];        // exp(cum_t)
     float tail[kQ];        // exp(cum_end - cum_t)
+    float w[kQ];           // tail Delta
     float total;           // exp(cum_end)
     float pad[3];
 };
@@ -198,9 +213,20 @@ __device__ __forceinline__ double make_decay(Decay& d, float delta, float A) {
     d.lo[t] = lo;
     d.delta[t] = delta;
     d.head[t] = exp2_two(hi, lo);
-    d.tail[t] = exp2_two(rh, rl);
+    const float tail = exp2_two(rh, rl);
+    d.tail[t] = tail;
+    d.w[t] = tail * delta;
     if (t == 63) d.total = exp2_two(hi, lo);
     return end;
+}
+// Eight consecutive values of one of the arrays (16-byte aligned).
+__device__ __forceinline__ void get8(const float* a, float (&v)[8]) {
+    const f4 x = *reinterpret_cast<const f4*>(a), y = *reinterpret_cast<const f4*>(a + 4);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        v[i] = x[i];
+        v[4 + i] = y[i];
+    }
 }
 // exp(cum_t - cum_s)
 __device__ __forceinline__ float pair_decay(float thi, float tlo, float shi, float slo) {
@@ -238,15 +264,32 @@ __device__ __forceinline__ SeqRange seq_range(const ScanP& p, int b) {
     return {s.begin, s.end - s.begin};
 }
 
-// dt of a token as the step Delta.
-__device__ __forceinline__ float raw_dt(const ScanP& p, int64_t row, int h) { return load_elem(p.dt, row * p.ld_dt + h, p.dt_dtype); }
+// dt of a chunk's tokens, lane = token: the word that holds it on its way (no branch around the
+// load and nothing that would wait for it), and the value once it is needed.
+struct DtAhead {
+    uint32_t word = 0, half = 0;
+    __device__ __forceinline__ void fetch(const ScanP& p, int64_t row0, int h, int lane, int live) {
+        const int es = p.dt_dtype == LA_BF16 ? 2 : 4;
+        const int64_t byte = (row0 * p.ld_dt + h) * es;
+        const __amdgpu_buffer_rsrc_t r =
+            make_rsrc(static_cast<const char*>(p.dt) + (byte & ~int64_t{3}), static_cast<size_t>(kQ) * p.ld_dt * es + 4);
+        const uint32_t off = static_cast<uint32_t>((byte & 3) + lane * p.ld_dt * es);
+        half = off & 2;
+        word = __builtin_amdgcn_raw_buffer_load_b32(r, lane < live ? static_cast<int>(off & ~3u) : -4, 0, 0);
+    }
+    __device__ __forceinline__ float value(const ScanP& p) const {
+        return p.dt_dtype == LA_F32 ? __uint_as_float(word) : half ? hi16(word) : lo16(word);
+    }
+};
 __device__ __forceinline__ float step_of(const ScanP& p, float raw, int h) {
     const float z = raw + (p.bias ? p.bias[h] : 0.0f);
     return p.softplus ? softplus_fine(z) : z;
 }
 
 // A [64][COLS] tile of rows `row0 ..` in registers and on its way to LDS: 16-byte pieces, the
-// pieces of a row on neighbouring threads; rows from `live` on and columns from `cols` on are zero.
+// pieces of a row on neighbouring threads; rows from `live` on and columns from `cols` on are
+// zero.  The buffer's bounds give the zeros: no branch around a load, so that the loads stay in
+// flight behind the products of the chunk before.
 template <class T, int COLS, int THREADS>
 struct Tile {
     static constexpr int E = Io<T>::kVec;
@@ -254,12 +297,17 @@ struct Tile {
     static constexpr int K = kQ * PPR / THREADS > 0 ? kQ * PPR / THREADS : 1;
     uv4 r[K];
     __device__ __forceinline__ void load(const T* base, int64_t ld, int live, int cols) {
+        // (the offset of a row from `live` on is at least the buffer's size)
+        const uint32_t bytes = static_cast<uint32_t>((live < kQ ? live : kQ) * ld * static_cast<int>(sizeof(T)));
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, bytes);
 #pragma unroll
         for (int k = 0; k < K; k++) {
             const int i = threadIdx.x + THREADS * k;
             const int row = i / PPR, col = (i % PPR) * E;
-            r[k] = uv4{0, 0, 0, 0};
-            if (row < live && col < cols) r[k] = load16(base + row * ld + col);
+            int off = (row * static_cast<int>(ld) + col) * static_cast<int>(sizeof(T));
+            if (COLS == 32 && col >= cols) off = -16;  // d_k = 16 in a tile of 32
+            if (kQ * PPR < THREADS && row >= kQ) off = -16;
+            r[k] = __builtin_bit_cast(uv4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
         }
     }
     __device__ __forceinline__ void store(T* lds, int stride) const {

@@ -31,32 +31,39 @@ int64_t slot_count(const la_scan_config& c) {  // enough for either layout
 template <class T, int N>
 struct WalkLds {
     T b[kQ * lds_row<T>(N)];
-    T x[kQ * lds_row<T>(kPT)];
+    T x[kQ * lds_row64<T>()];
     Decay d;
 };
 
-// One direction of the state's walk for 64 value columns of a head.  Forward: S from b, x and
-// W, the state entering each chunk to `states`.  REV: dS from c, dy and exp(cum), the gradient
-// of the state leaving each chunk to `states`, and dS0.  ONE: a workgroup a chunk, its own
-// contribution from zero and its decay only (joined by walk_join_kernel): for few heads.
+// Both directions of the state's walk for 64 value columns of a head, a workgroup each in one
+// launch (they are independent, and the chip holds two a CU).  Forward: S from b, x and W, the
+// state entering each chunk to `S`.  Back: dS from c, dy and exp(cum), the gradient of the state
+// leaving each chunk to `dS`, and dS0.  ONE: a workgroup a chunk, its own contribution from zero
+// and its decay only (joined by walk_join_kernel): for few heads.
 // The state is held transposed (a lane: one row, four consecutive columns of each tile), so
 // that it is stored in 16-byte pieces.
-template <class T, int N, bool REV, bool ONE>
-__global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* rows_x, int64_t ld_x, const float* first,
-                                                        float* states, float* decay, float* last) {
+template <class T, int N, bool ONE>
+__global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* dy, const float* S0, const float* dST, float* Sst,
+                                                        float* dSst, float* decay, float* dS0) {
     using MT = Mat<T>;
     constexpr int P3 = MT::template parts<3>;
-    constexpr int RB = lds_row<T>(N), RX = lds_row<T>(kPT);
+    constexpr int RB = lds_row<T>(N), RX = lds_row64<T>();
     __shared__ __align__(16) WalkLds<T, N> lds;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lm = lane & 15, g = lane >> 4;
 
     const int tiles = p.dv / kPT, nmax = (p.T + kQ - 1) / kQ;
     int64_t u = die_unit(blockIdx.x, gridDim.x);
+    const bool rev = u & 1;
+    u >>= 1;
     const int tile = static_cast<int>(u % tiles);
     u /= tiles;
     const int h = static_cast<int>(u % p.H);
     u /= p.H;
+    const float* first = rev ? dST : S0;
+    float* states = rev ? dSst : Sst;
+    float* last = rev ? dS0 : nullptr;
+    const int64_t ld_x = rev ? static_cast<int64_t>(p.H) * p.dv : p.ld_x;
     const int bi = static_cast<int>(ONE ? u / nmax : u);
     const SeqRange sr = seq_range(p, bi);
     const int nch = (sr.len + kQ - 1) / kQ;
@@ -82,20 +89,20 @@ __global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* rows_x
             if (n < p.dk) *reinterpret_cast<f4*>(at + static_cast<size_t>(n) * p.dv + col) = S[i];
         }
     };
-    const T* xg = rows_x + static_cast<int64_t>(h) * p.dv + tile * kPT;
-    const T* bg = static_cast<const T*>(REV ? p.c : p.b) + static_cast<int64_t>(grp) * p.dk;
-    const int64_t ld_b = REV ? p.ld_c : p.ld_b;
+    const T* xg = (rev ? dy : static_cast<const T*>(p.x)) + static_cast<int64_t>(h) * p.dv + tile * kPT;
+    const T* bg = static_cast<const T*>(rev ? p.c : p.b) + static_cast<int64_t>(grp) * p.dk;
+    const int64_t ld_b = rev ? p.ld_c : p.ld_b;
     const float A = p.A ? p.A[h] : 0.0f;
     Tile<T, N, 256> tb;
     Tile<T, kPT, 256> tx;
-    float raw = 0.0f;
-    auto at_step = [&](int i) { return ONE ? only : REV ? nch - 1 - i : i; };
+    DtAhead raw;
+    auto at_step = [&](int i) { return ONE ? only : rev ? nch - 1 - i : i; };
     auto fetch = [&](int ch) {
         const int64_t row0 = sr.begin + static_cast<int64_t>(ch) * kQ;
         const int live = sr.len - ch * kQ;
         tb.load(bg + row0 * ld_b, ld_b, live, p.dk);
         tx.load(xg + row0 * ld_x, ld_x, live, kPT);
-        if (wave == 0 && lane < live) raw = raw_dt(p, row0 + lane, h);
+        if (wave == 0) raw.fetch(p, row0, h, lane, live);
     };
     if (steps > 0) fetch(at_step(0));
     for (int i = 0; i < steps; i++) {
@@ -103,7 +110,7 @@ __global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* rows_x
         const int live = sr.len - ch * kQ;
         tb.store(lds.b, RB);
         tx.store(lds.x, RX);
-        if (wave == 0) make_decay(lds.d, lane < live ? step_of(p, raw, h) : 0.0f, A);
+        if (wave == 0) make_decay(lds.d, lane < live ? step_of(p, raw.value(p), h) : 0.0f, A);
         __syncthreads();
         if (i + 1 < steps) fetch(at_step(i + 1));
         float* slot = states + (static_cast<size_t>(slot_of(p, bi, sr.begin, ch)) * p.H + h) * head;
@@ -113,37 +120,42 @@ __global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* rows_x
         for (int k = 0; k < 2; k++) {
             float v[8];
             MT::widen8(MT::col8(lds.x, RX, 32 * k, 16 * wave, lane), v);
+            float wt[8];
+            get8((rev ? lds.d.head : lds.d.w) + 32 * k + 8 * g, wt);
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const int t = 32 * k + 8 * g + j;
-                v[j] *= REV ? lds.d.head[t] : lds.d.tail[t] * lds.d.delta[t];
-            }
+            for (int j = 0; j < 8; j++) v[j] *= wt[j];
             MT::template split<P3>(v, wx[k]);
         }
         const float total = lds.d.total;
 #pragma unroll
-        for (int n = 0; n < N / 16; n++) {
-            S[n] *= total;
+        for (int n = 0; n < N / 16; n++) S[n] *= total;
 #pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const typename MT::Frag bf = MT::col8(lds.b, RB, 32 * k, 16 * n, lane);
+        for (int k = 0; k < 2; k++) {
+            typename MT::Frag bf[N / 16];
 #pragma unroll
-                for (int q = 0; q < P3; q++) S[n] = MT::mma(wx[k][q], bf, S[n]);
-            }
+            for (int n = 0; n < N / 16; n++) bf[n] = MT::col8(lds.b, RB, 32 * k, 16 * n, lane);
+#pragma unroll
+            for (int q = 0; q < P3; q++)
+#pragma unroll
+                for (int n = 0; n < N / 16; n++) S[n] = MT::mma(wx[k][q], bf[n], S[n]);
         }
         if (ONE) {
             put(slot);
-            if (threadIdx.x == 0 && tile == 0) decay[slot_of(p, bi, sr.begin, ch) * p.H + h] = total;
+            if (threadIdx.x == 0 && tile == 0 && !rev) decay[slot_of(p, bi, sr.begin, ch) * p.H + h] = total;
         }
         __syncthreads();
     }
     if (!ONE && last) put(last + (static_cast<size_t>(bi) * p.H + h) * head);
 }
 
-// The chunks' own contributions to the state that enters each of them (REV: leaves), in place.
-template <bool REV>
-__global__ __launch_bounds__(256) void walk_join_kernel(ScanP p, const float* first, float* states, const float* decay,
-                                                        float* last) {
+// From the chunks' own contributions, in place: the state that enters each of them and (y = 1)
+// the gradient of the state that leaves it.
+__global__ __launch_bounds__(256) void walk_join_kernel(ScanP p, const float* S0, const float* dST, float* Sst, float* dSst,
+                                                        const float* decay, float* dS0) {
+    const bool rev = blockIdx.y != 0;
+    const float* first = rev ? dST : S0;
+    float* states = rev ? dSst : Sst;
+    float* last = rev ? dS0 : nullptr;
     const int per = p.dk * p.dv / 4;
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i >= static_cast<int64_t>(p.B) * p.H * per) return;
@@ -155,7 +167,7 @@ __global__ __launch_bounds__(256) void walk_join_kernel(ScanP p, const float* fi
     fv4 S = {};
     if (first) S = reinterpret_cast<const fv4*>(first)[bh * per + e];
     for (int k = 0; k < nch; k++) {
-        const int64_t at = slot_of(p, bi, sr.begin, REV ? nch - 1 - k : k) * p.H + h;
+        const int64_t at = slot_of(p, bi, sr.begin, rev ? nch - 1 - k : k) * p.H + h;
         fv4* l = reinterpret_cast<fv4*>(states) + at * per + e;
         const fv4 own = *l;
         *l = S;
@@ -168,11 +180,11 @@ template <class T, int N>
 struct GradLds {
     T b[kQ * lds_row<T>(N)];
     T c[kQ * lds_row<T>(N)];
-    T x[kQ * lds_row<T>(kPT)];
-    T dy[kQ * lds_row<T>(kPT)];
-    T m[Mat<T>::template parts<2>][kQ * lds_row<T>(kQ)];   // M[t][s]
-    T dg[Mat<T>::template parts<2>][kQ * lds_row<T>(kQ)];  // dG[t][s]
-    T ds[sizeof(T) == 2 ? 2 : 1][sizeof(T) == 2 ? N * lds_row<T>(kPT) : 1];  // dS (bf16 parts); FP32 reads it from memory
+    T x[kQ * lds_row64<T>()];
+    T dy[kQ * lds_row64<T>()];
+    T m[Mat<T>::template parts<2>][kQ * lds_row64<T>()];   // M[t][s]
+    T dg[Mat<T>::template parts<2>][kQ * lds_row64<T>()];  // dG[t][s]
+    T ds[sizeof(T) == 2 ? 2 : 1][sizeof(T) == 2 ? N * lds_row64<T>() : 1];  // dS (bf16 parts); FP32 reads it from memory
     Decay d;
     float rt[10][16], ct[10][16];  // the tiles' row and column sums
     float ri[N / 16][kQ], ci[N / 16][kQ];  // sums over 16 state rows
@@ -194,7 +206,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                                                         float* hp, int64_t slots, int slices, int64_t rows) {
     using MT = Mat<T>;
     constexpr int P2 = MT::template parts<2>;
-    constexpr int RB = lds_row<T>(N), RX = lds_row<T>(kPT), RM = lds_row<T>(kQ);
+    constexpr int RB = lds_row<T>(N), RX = lds_row64<T>(), RM = lds_row64<T>();
     constexpr int KS = N / 32, NTL = N / 16, PARTS = 8 / NTL, TI = 4 / PARTS;
     extern __shared__ __align__(16) char raw_lds[];
     GradLds<T, N>& lds = *reinterpret_cast<GradLds<T, N>*>(raw_lds);
@@ -263,26 +275,23 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
     f4 dC[TI] = {}, dB[TI] = {};  // rows n, columns t (s)
 
     Tile<T, kPT, 512> tx, ty;
-    float rdt = 0.0f;
+    DtAhead rdt;
     typename MT::Frag Sf[2][P2], dSf[2][P2];
     float Sr[2][8], dSr[2][8];
     auto fetch = [&](int h, int tile) {
         tx.load(static_cast<const T*>(p.x) + row0 * p.ld_x + static_cast<int64_t>(h) * p.dv + tile * kPT, p.ld_x, live, kPT);
         ty.load(dyr + (row0 * p.H + h) * p.dv + tile * kPT, static_cast<int64_t>(p.H) * p.dv, live, kPT);
-        if (wave == 0 && lane < live) rdt = raw_dt(p, row0 + lane, h);
+        if (wave == 0) rdt.fetch(p, row0, h, lane, live);
         const size_t at = (static_cast<size_t>(slot) * p.H + h) * head + tile * kPT;
         const int n = n0 + lm;
+        const __amdgpu_buffer_rsrc_t rS = make_rsrc(Sin + at, head * 4), rD = make_rsrc(dSe + at, head * 4);
 #pragma unroll
         for (int k = 0; k < 2; k++) {
-            f4 v[4] = {};
-            if (n < p.dk) {
-                const float* s = Sin + at + static_cast<size_t>(n) * p.dv + 32 * k + 8 * g;
-                const float* d = dSe + at + static_cast<size_t>(n) * p.dv + 32 * k + 8 * g;
-                v[0] = *reinterpret_cast<const f4*>(s);
-                v[1] = *reinterpret_cast<const f4*>(s + 4);
-                v[2] = *reinterpret_cast<const f4*>(d);
-                v[3] = *reinterpret_cast<const f4*>(d + 4);
-            }
+            const int off = n < p.dk ? (n * p.dv + 32 * k + 8 * g) * 4 : -32;
+            const f4 v[4] = {__builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rS, off, 0, 0)),
+                             __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rS, off, 16, 0)),
+                             __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rD, off, 0, 0)),
+                             __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rD, off, 16, 0))};
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 Sr[k][j] = v[0][j];
@@ -304,7 +313,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         tx.store(lds.x, RX);
         ty.store(lds.dy, RX);
         if (wave == 0 && tile == 0) {
-            zt = rdt + (p.bias ? p.bias[h] : 0.0f);
+            zt = rdt.value(p) + (p.bias ? p.bias[h] : 0.0f);
             make_decay(lds.d, lane < live ? (p.softplus ? softplus_fine(zt) : zt) : 0.0f, A);
         }
         float sd = 0.0f;
@@ -342,12 +351,14 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                               MT::row8(lds.dy + (16 * ti + lm) * RX + 32 * ks + 8 * g), acc);
             const int t = 16 * ti + lm, s0 = 16 * si + 4 * g;
             const float thi = lds.d.hi[t], tlo = lds.d.lo[t];
+            const f4 shi = *reinterpret_cast<const f4*>(lds.d.hi + s0), slo = *reinterpret_cast<const f4*>(lds.d.lo + s0);
+            const f4 sdl = *reinterpret_cast<const f4*>(lds.d.delta + s0);
             float m[4], dg[4], pc[4], pr = 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; r++) {
                 const int s = s0 + r;
-                const float L = s <= t ? pair_decay(thi, tlo, lds.d.hi[s], lds.d.lo[s]) : 0.0f;
-                const float gl = G[q][r] * L, dl = lds.d.delta[s];
+                const float L = s <= t ? pair_decay(thi, tlo, shi[r], slo[r]) : 0.0f;
+                const float gl = G[q][r] * L, dl = sdl[r];
                 m[r] = gl * dl;
                 dg[r] = L * dl * acc[r];
                 pc[r] = gl * acc[r];
@@ -368,6 +379,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         if (lane == 0) lds.dd[wave] = diag;
         __syncthreads();
 
+        __builtin_amdgcn_sched_barrier(0);  // (hoisted loads of later parts would not fit the registers)
         // ---- dX^T: rows: columns pc + 4 g + r; column: s
         {
             const int pc = 16 * (wave & 3), half = wave >> 2;
@@ -399,7 +411,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 const int s = 32 * half + 16 * j + lm;
-                acc[j] *= lds.d.tail[s] * lds.d.delta[s];
+                acc[j] *= lds.d.w[s];
 #pragma unroll
                 for (int ks = 0; ks < 2; ks++) {
                     if (ks < half) continue;  // tokens before s
@@ -418,6 +430,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                 }
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         // ---- dC^T, dB^T: rows n of this wave, columns t, s
         {
             typename MT::Frag bT[2], cT[2];
@@ -429,6 +442,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
 #pragma unroll
             for (int ii = 0; ii < TI; ii++) {
                 const int i = part * TI + ii, t = 16 * i + lm;
+                __builtin_amdgcn_sched_barrier(0);
                 f4 a = {}, b = {};
 #pragma unroll
                 for (int ks = 0; ks < 2; ks++) {
@@ -652,21 +666,16 @@ hipError_t launch(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
     const int nmax = (c.T + kQ - 1) / kQ;
     const int64_t slots = a.cu ? static_cast<int64_t>(c.B) + c.T / kQ + 1 : static_cast<int64_t>(c.B) * nmax;
     const int64_t groups = static_cast<int64_t>(c.B) * c.H * (c.d_v / kPT);
-    const T* x = static_cast<const T*>(a.x);
     const T* dy = static_cast<const T*>(a.dy);
-    const int64_t ld_y = static_cast<int64_t>(c.H) * c.d_v;
     // Enough heads: a workgroup walks a sequence.  Fewer than a workgroup a CU: one a chunk
     // and a joining pass (three times the state traffic, but no walk).
     if (groups >= 256 || nmax < 8) {
-        scan_walk_kernel<T, N, false, false><<<dim3(static_cast<unsigned>(groups)), 256, 0, s>>>(p, x, p.ld_x, a.S0, S, nullptr, nullptr);
-        scan_walk_kernel<T, N, true, false><<<dim3(static_cast<unsigned>(groups)), 256, 0, s>>>(p, dy, ld_y, a.dST, dS, nullptr, a.dS0);
+        scan_walk_kernel<T, N, false><<<dim3(static_cast<unsigned>(2 * groups)), 256, 0, s>>>(p, dy, a.S0, a.dST, S, dS, nullptr, a.dS0);
     } else {
-        const unsigned grid = static_cast<unsigned>(groups * nmax);
+        const unsigned grid = static_cast<unsigned>(2 * groups * nmax);
         const unsigned join = static_cast<unsigned>((static_cast<int64_t>(c.B) * c.H * (c.d_k * c.d_v / 4) + 255) / 256);
-        scan_walk_kernel<T, N, false, true><<<dim3(grid), 256, 0, s>>>(p, x, p.ld_x, nullptr, S, decay, nullptr);
-        walk_join_kernel<false><<<dim3(join), 256, 0, s>>>(p, a.S0, S, decay, nullptr);
-        scan_walk_kernel<T, N, true, true><<<dim3(grid), 256, 0, s>>>(p, dy, ld_y, nullptr, dS, decay, nullptr);
-        walk_join_kernel<true><<<dim3(join), 256, 0, s>>>(p, a.dST, dS, decay, a.dS0);
+        scan_walk_kernel<T, N, true><<<dim3(grid), 256, 0, s>>>(p, dy, nullptr, nullptr, S, dS, decay, nullptr);
+        walk_join_kernel<<<dim3(join, 2), 256, 0, s>>>(p, a.S0, a.dST, S, dS, decay, a.dS0);
     }
     const int slices = grad_slices(c);
     float* dbp = slices > 1 ? reinterpret_cast<float*>(a.ws + w.dbp) : nullptr;
