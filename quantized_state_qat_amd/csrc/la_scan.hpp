@@ -187,9 +187,27 @@ __device__ __forceinline__ double wave_last(double x) {
     return __builtin_bit_cast(double, static_cast<uint64_t>(a) | (static_cast<uint64_t>(b) << 32));
 }
 
-__device__ __forceinline__ float softplus_fine(float z) { return fmaxf(z, 0.0f) + log1pf(expf(-fabsf(z))); }
+// log(1 + exp(z)) = max(z, 0) + log1p(e), e = exp(-|z|) in (0, 1]; log1p(e) = 2 artanh(e / (2 + e)),
+// the argument at most 1/3: its series to the 15th power is within 2^-26 of the sum.  A third of
+// the library functions' instructions; one wave forms it while others wait.
+__device__ __forceinline__ float softplus_fine(float z) {
+    const float e = exp_fine(fmaxf(-fabsf(z), -87.0f));
+    const float d = 2.0f + e, r = __builtin_amdgcn_rcpf(d);
+    const float q = e * r;
+    const float s = __builtin_fmaf(__builtin_fmaf(-d, q, e), r, q);
+    const float x = s * s;
+    float p = 1.0f / 15.0f;
+    p = __builtin_fmaf(p, x, 1.0f / 13.0f);
+    p = __builtin_fmaf(p, x, 1.0f / 11.0f);
+    p = __builtin_fmaf(p, x, 1.0f / 9.0f);
+    p = __builtin_fmaf(p, x, 1.0f / 7.0f);
+    p = __builtin_fmaf(p, x, 1.0f / 5.0f);
+    p = __builtin_fmaf(p, x, 1.0f / 3.0f);
+    const float two_s = s + s;
+    return fmaxf(z, 0.0f) + __builtin_fmaf(two_s * x, p, two_s);
+}
 
-// One chunk's decays, in LDS.  Exponents are in units of log2; the cumulative sums are formed
+// One chunk's decays for a head.  Exponents are in units of log2; the cumulative sums are formed
 // in double and kept as hi + lo floats, so that the difference of two far into a long decay
 // keeps FP32's relative precision.
 struct Decay {
@@ -198,12 +216,13 @@ struct Decay {
     float head[kQ];        // exp(cum_t)
     float tail[kQ];        // exp(cum_end - cum_t)
     float w[kQ];           // tail Delta
-    float total;           // exp(cum_end)
-    float pad[3];
+    float z[kQ];           // dt + dt_bias
+    float total[kQ];       // [0]: exp(cum_end)
 };
-// By one whole wave, lane = token.  Returns cum_end (log2).
-__device__ __forceinline__ double make_decay(Decay& d, float delta, float A) {
+// By one whole wave, lane = token, from z (0 steps from token `live` on).  Returns cum_end (log2).
+__device__ __forceinline__ double make_decay(Decay& d, float z, int softplus, int live, float A) {
     const int t = threadIdx.x & 63;
+    const float delta = t < live ? (softplus ? softplus_fine(z) : z) : 0.0f;
     const double cum = wave_prefix(static_cast<double>(delta) * (static_cast<double>(A) * 1.4426950408889634));
     const double end = wave_last(cum);
     const float hi = static_cast<float>(cum), lo = static_cast<float>(cum - hi);
@@ -216,9 +235,22 @@ __device__ __forceinline__ double make_decay(Decay& d, float delta, float A) {
     const float tail = exp2_two(rh, rl);
     d.tail[t] = tail;
     d.w[t] = tail * delta;
-    if (t == 63) d.total = exp2_two(hi, lo);
+    d.z[t] = z;
+    if (t == 63) d.total[0] = exp2_two(hi, lo);
     return end;
 }
+// A Decay on its way from memory to LDS: 16 bytes a thread, threads first .. first + 127.
+struct DecayAhead {
+    uv4 r;
+    __device__ __forceinline__ void load(const Decay* from, int first) {
+        const __amdgpu_buffer_rsrc_t rs = make_rsrc(from, sizeof(Decay));
+        r = __builtin_bit_cast(uv4, __builtin_amdgcn_raw_buffer_load_b128(rs, (static_cast<int>(threadIdx.x) - first) * 16, 0, 0));
+    }
+    __device__ __forceinline__ void store(Decay& to, int first) const {
+        const int i = static_cast<int>(threadIdx.x) - first;
+        if (i >= 0 && i < static_cast<int>(sizeof(Decay) / 16)) reinterpret_cast<uv4*>(&to)[i] = r;
+    }
+};
 // Eight consecutive values of one of the arrays (16-byte aligned).
 __device__ __forceinline__ void get8(const float* a, float (&v)[8]) {
     const f4 x = *reinterpret_cast<const f4*>(a), y = *reinterpret_cast<const f4*>(a + 4);
@@ -281,11 +313,6 @@ struct DtAhead {
         return p.dt_dtype == LA_F32 ? __uint_as_float(word) : half ? hi16(word) : lo16(word);
     }
 };
-__device__ __forceinline__ float step_of(const ScanP& p, float raw, int h) {
-    const float z = raw + (p.bias ? p.bias[h] : 0.0f);
-    return p.softplus ? softplus_fine(z) : z;
-}
-
 // A [64][COLS] tile of rows `row0 ..` in registers and on its way to LDS: 16-byte pieces, the
 // pieces of a row on neighbouring threads; rows from `live` on and columns from `cols` on are
 // zero.  The buffer's bounds give the zeros: no branch around a load, so that the loads stay in

@@ -28,6 +28,25 @@ int64_t slot_count(const la_scan_config& c) {  // enough for either layout
     return dense > packed ? dense : packed;
 }
 
+// Every chunk's decays, a wave each; read by the walks, the gradients and the rates' gradients.
+__global__ __launch_bounds__(256) void decays_kernel(ScanP p, Decay* out, int nmax) {
+    __shared__ __align__(16) Decay d[4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + wave;  // (b, chunk, h), h fastest
+    const int h = static_cast<int>(unit % p.H), ch = static_cast<int>(unit / p.H % nmax);
+    const int64_t b = unit / p.H / nmax;
+    if (b >= p.B) return;
+    const SeqRange sr = seq_range(p, static_cast<int>(b));
+    const int live = sr.len - ch * kQ;
+    if (live <= 0) return;
+    DtAhead dt;
+    dt.fetch(p, sr.begin + static_cast<int64_t>(ch) * kQ, h, lane, live);
+    make_decay(d[wave], dt.value(p) + (p.bias ? p.bias[h] : 0.0f), p.softplus, live, p.A[h]);
+    uv4* o = reinterpret_cast<uv4*>(out + slot_of(p, static_cast<int>(b), sr.begin, ch) * p.H + h);
+#pragma unroll
+    for (int q = 0; q < 2; q++) o[lane + 64 * q] = reinterpret_cast<const uv4*>(&d[wave])[lane + 64 * q];
+}
+
 template <class T, int N>
 struct WalkLds {
     T b[kQ * lds_row<T>(N)];
@@ -39,12 +58,12 @@ struct WalkLds {
 // launch (they are independent, and the chip holds two a CU).  Forward: S from b, x and W, the
 // state entering each chunk to `S`.  Back: dS from c, dy and exp(cum), the gradient of the state
 // leaving each chunk to `dS`, and dS0.  ONE: a workgroup a chunk, its own contribution from zero
-// and its decay only (joined by walk_join_kernel): for few heads.
+// only (joined by walk_join_kernel): for few heads.
 // The state is held transposed (a lane: one row, four consecutive columns of each tile), so
 // that it is stored in 16-byte pieces.
 template <class T, int N, bool ONE>
 __global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* dy, const float* S0, const float* dST, float* Sst,
-                                                        float* dSst, float* decay, float* dS0) {
+                                                        float* dSst, const Decay* decays, float* dS0) {
     using MT = Mat<T>;
     constexpr int P3 = MT::template parts<3>;
     constexpr int RB = lds_row<T>(N), RX = lds_row64<T>();
@@ -92,25 +111,23 @@ __global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* dy, co
     const T* xg = (rev ? dy : static_cast<const T*>(p.x)) + static_cast<int64_t>(h) * p.dv + tile * kPT;
     const T* bg = static_cast<const T*>(rev ? p.c : p.b) + static_cast<int64_t>(grp) * p.dk;
     const int64_t ld_b = rev ? p.ld_c : p.ld_b;
-    const float A = p.A ? p.A[h] : 0.0f;
     Tile<T, N, 256> tb;
     Tile<T, kPT, 256> tx;
-    DtAhead raw;
+    DecayAhead td;
     auto at_step = [&](int i) { return ONE ? only : rev ? nch - 1 - i : i; };
     auto fetch = [&](int ch) {
         const int64_t row0 = sr.begin + static_cast<int64_t>(ch) * kQ;
         const int live = sr.len - ch * kQ;
         tb.load(bg + row0 * ld_b, ld_b, live, p.dk);
         tx.load(xg + row0 * ld_x, ld_x, live, kPT);
-        if (wave == 0) raw.fetch(p, row0, h, lane, live);
+        td.load(decays + slot_of(p, bi, sr.begin, ch) * p.H + h, 0);
     };
     if (steps > 0) fetch(at_step(0));
     for (int i = 0; i < steps; i++) {
         const int ch = at_step(i);
-        const int live = sr.len - ch * kQ;
         tb.store(lds.b, RB);
         tx.store(lds.x, RX);
-        if (wave == 0) make_decay(lds.d, lane < live ? step_of(p, raw.value(p), h) : 0.0f, A);
+        td.store(lds.d, 0);
         __syncthreads();
         if (i + 1 < steps) fetch(at_step(i + 1));
         float* slot = states + (static_cast<size_t>(slot_of(p, bi, sr.begin, ch)) * p.H + h) * head;
@@ -126,7 +143,7 @@ __global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* dy, co
             for (int j = 0; j < 8; j++) v[j] *= wt[j];
             MT::template split<P3>(v, wx[k]);
         }
-        const float total = lds.d.total;
+        const float total = lds.d.total[0];
 #pragma unroll
         for (int n = 0; n < N / 16; n++) S[n] *= total;
 #pragma unroll
@@ -139,10 +156,7 @@ __global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* dy, co
 #pragma unroll
                 for (int n = 0; n < N / 16; n++) S[n] = MT::mma(wx[k][q], bf[n], S[n]);
         }
-        if (ONE) {
-            put(slot);
-            if (threadIdx.x == 0 && tile == 0 && !rev) decay[slot_of(p, bi, sr.begin, ch) * p.H + h] = total;
-        }
+        if (ONE) put(slot);
         __syncthreads();
     }
     if (!ONE && last) put(last + (static_cast<size_t>(bi) * p.H + h) * head);
@@ -151,7 +165,7 @@ __global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* dy, co
 // From the chunks' own contributions, in place: the state that enters each of them and (y = 1)
 // the gradient of the state that leaves it.
 __global__ __launch_bounds__(256) void walk_join_kernel(ScanP p, const float* S0, const float* dST, float* Sst, float* dSst,
-                                                        const float* decay, float* dS0) {
+                                                        const Decay* decays, float* dS0) {
     const bool rev = blockIdx.y != 0;
     const float* first = rev ? dST : S0;
     float* states = rev ? dSst : Sst;
@@ -171,10 +185,17 @@ __global__ __launch_bounds__(256) void walk_join_kernel(ScanP p, const float* S0
         fv4* l = reinterpret_cast<fv4*>(states) + at * per + e;
         const fv4 own = *l;
         *l = S;
-        S = S * decay[at] + own;
+        S = S * decays[at].total[0] + own;
     }
     if (last) reinterpret_cast<fv4*>(last)[bh * per + e] = S;
 }
+
+// What the decays' gradients of one chunk and head are formed from.
+struct RateSums {
+    float r[kQ], c[kQ], inner[kQ];  // r_t, c_t, and c_t's part from dS
+    float sd, dd;                   // <S, dS>, sum of dy x
+    float pad[2];
+};
 
 template <class T, int N>
 struct GradLds {
@@ -182,13 +203,16 @@ struct GradLds {
     T c[kQ * lds_row<T>(N)];
     T x[kQ * lds_row64<T>()];
     T dy[kQ * lds_row64<T>()];
-    T m[Mat<T>::template parts<2>][kQ * lds_row64<T>()];   // M[t][s]
-    T dg[Mat<T>::template parts<2>][kQ * lds_row64<T>()];  // dG[t][s]
-    T ds[sizeof(T) == 2 ? 2 : 1][sizeof(T) == 2 ? N * lds_row64<T>() : 1];  // dS (bf16 parts); FP32 reads it from memory
+    // M[t][s] and dG[t][s].  bf16: rounded once.  Their share of dX, dB and dC then carries an error
+    // like the bf16 results' own rounding; the decays' gradients, in FP32, are formed before it.
+    T m[kQ * lds_row64<T>()];
+    T dg[kQ * lds_row64<T>()];
+    T ds[sizeof(T) == 2 ? 2 : 1][sizeof(T) == 2 ? N * lds_row64<T>() : 8];  // dS (two bf16 parts); FP32 reads it from memory
     Decay d;
-    float rt[10][16], ct[10][16];  // the tiles' row and column sums
-    float ri[N / 16][kQ], ci[N / 16][kQ];  // sums over 16 state rows
-    float sd[2][8], dd[8];                 // the waves' <S, dS> (by parity of the iteration) and diagonals of dM
+    // partial sums of the decays' gradients, by parity of the iteration (they are joined beside the next)
+    float rt[2][10][16], ct[2][10][16];          // the pair tiles' row and column sums
+    float ri[2][N / 16][kQ], ci[2][N / 16][kQ];  // sums over 16 state rows
+    float sd[2][8], dd[2][8];                    // the waves' <S, dS> and diagonals of dM
 };
 
 __device__ __forceinline__ void lower_tile_of(int k, int& ti, int& si) {
@@ -196,14 +220,17 @@ __device__ __forceinline__ void lower_tile_of(int k, int& ti, int& si) {
     si = k - ti * (ti + 1) / 2;
 }
 
-// Gradients of one chunk for one slice of a group's heads, by eight waves.  Pairs: the ten lower
-// tiles over the waves.  dX: a wave 16 columns by 32 tokens.  dC, dB: a wave 16 state rows by all
-// tokens (fewer rows than 128: by a part of them), kept in registers over the heads.  dbp, dcp: FP32 partial sums of db
-// and dc per slice ([slice][row][G][dk]), or null where one slice holds the whole group.
+// Gradients of one chunk for one slice of a group's heads, by eight waves; a head's 64 value
+// columns an iteration.  Pairs: the ten lower tiles over the waves, and beside them the last
+// iteration's sums for the decays' gradients.  dX: a wave 16 columns by 32 tokens.  dC, dB: a wave 16 state rows by all tokens (fewer rows than 128: by a
+// part of them), kept in registers over the heads.  LDS bandwidth bounds it: what does not change
+// over the heads (b^T, c^T and this wave's pieces of b and c) stays in registers, and the next
+// iteration's loads are issued in three places.  dbp, dcp: FP32 partial sums of db and dc per
+// slice ([slice][row][G][dk]), or null where one slice holds the whole group.
 template <class T, int N>
 __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, const float* Sin, const float* dSe, void* dx_,
-                                                        void* ddt, void* db_, void* dc_, float* dbp, float* dcp,
-                                                        float* hp, int64_t slots, int slices, int64_t rows) {
+                                                        void* db_, void* dc_, float* dbp, float* dcp, const Decay* decays,
+                                                        RateSums* sums, int slices, int64_t rows) {
     using MT = Mat<T>;
     constexpr int P2 = MT::template parts<2>;
     constexpr int RB = lds_row<T>(N), RX = lds_row64<T>(), RM = lds_row64<T>();
@@ -213,6 +240,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lm = lane & 15, g = lane >> 4;
     const int n0 = 16 * (wave % NTL), part = wave / NTL;  // state rows and token part of dC, dB
+    constexpr int kJoin = 7;                              // the wave that joins the sums
 
     int64_t u = die_unit(blockIdx.x, gridDim.x);
     const int slice = static_cast<int>(u % slices);
@@ -245,16 +273,42 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
     const int h1 = slice * per + per < hpg ? h0 + per : (grp + 1) * hpg;
     const int tiles = p.dv / kPT;
     const size_t head = static_cast<size_t>(p.dk) * p.dv;
+    const int iters = (h1 - h0) * tiles;
 
+    Tile<T, kPT, 512> tx, ty;
+    DecayAhead td;
+    float Sr[2][8], dSr[2][8];
+    auto fetch_rows = [&](int it) {
+        const int h = h0 + it / tiles, tile = it % tiles;
+        tx.load(static_cast<const T*>(p.x) + row0 * p.ld_x + static_cast<int64_t>(h) * p.dv + tile * kPT, p.ld_x, live, kPT);
+        ty.load(dyr + (row0 * p.H + h) * p.dv + tile * kPT, static_cast<int64_t>(p.H) * p.dv, live, kPT);
+        td.load(decays + slot * p.H + h, 0);
+    };
+    const int soff = n0 + lm < p.dk ? ((n0 + lm) * p.dv + 8 * g) * 4 : -1024;
+    auto fetch_state = [&](int it, const float* from, float (&to)[2][8]) {
+        const size_t at = (static_cast<size_t>(slot) * p.H + h0 + it / tiles) * head + (it % tiles) * kPT;
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(from + at, head * 4);
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+#pragma unroll
+            for (int q = 0; q < 2; q++) {
+                const f4 v = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, soff, 128 * k + 16 * q, 0));
+#pragma unroll
+                for (int j = 0; j < 4; j++) to[k][4 * q + j] = v[j];
+            }
+    };
+    fetch_rows(0);
+    fetch_state(0, Sin, Sr);
+    fetch_state(0, dSe, dSr);
     {  // this chunk's b and c, and zeros above the diagonals
         Tile<T, N, 512> t;
         t.load(static_cast<const T*>(p.b) + row0 * p.ld_b + static_cast<int64_t>(grp) * p.dk, p.ld_b, live, p.dk);
         t.store(lds.b, RB);
         t.load(static_cast<const T*>(p.c) + row0 * p.ld_c + static_cast<int64_t>(grp) * p.dk, p.ld_c, live, p.dk);
         t.store(lds.c, RB);
-        for (int i = threadIdx.x; i < P2 * kQ * RM; i += 512) {
-            (&lds.m[0][0])[i] = T{};
-            (&lds.dg[0][0])[i] = T{};
+        for (int i = threadIdx.x; i < kQ * RM; i += 512) {
+            lds.m[i] = T{};
+            lds.dg[i] = T{};
         }
     }
     __syncthreads();
@@ -272,50 +326,60 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                                MT::row8(lds.c + (16 * ti + lm) * RB + 32 * ks + 8 * g), G[q]);
         }
     }
+    typename MT::Frag bT[2], cT[2];  // b^T, c^T: row n0 + lm, tokens 32 k + 8 g ..
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        bT[k] = MT::col8(lds.b, RB, 32 * k, n0, lane);
+        cT[k] = MT::col8(lds.c, RB, 32 * k, n0, lane);
+    }
     f4 dC[TI] = {}, dB[TI] = {};  // rows n, columns t (s)
 
-    Tile<T, kPT, 512> tx, ty;
-    DtAhead rdt;
-    typename MT::Frag Sf[2][P2], dSf[2][P2];
-    float Sr[2][8], dSr[2][8];
-    auto fetch = [&](int h, int tile) {
-        tx.load(static_cast<const T*>(p.x) + row0 * p.ld_x + static_cast<int64_t>(h) * p.dv + tile * kPT, p.ld_x, live, kPT);
-        ty.load(dyr + (row0 * p.H + h) * p.dv + tile * kPT, static_cast<int64_t>(p.H) * p.dv, live, kPT);
-        if (wave == 0) rdt.fetch(p, row0, h, lane, live);
-        const size_t at = (static_cast<size_t>(slot) * p.H + h) * head + tile * kPT;
-        const int n = n0 + lm;
-        const __amdgpu_buffer_rsrc_t rS = make_rsrc(Sin + at, head * 4), rD = make_rsrc(dSe + at, head * 4);
+    // kJoin: iteration it's partial sums, added up over a head's tiles; lane = token
+    float racc = 0.0f, cacc = 0.0f, iacc = 0.0f, sdacc = 0.0f, ddacc = 0.0f;
+    auto join = [&](int it) {
+        const int par = it & 1;
+        const int tq = lane >> 4, tl = lane & 15;
 #pragma unroll
-        for (int k = 0; k < 2; k++) {
-            const int off = n < p.dk ? (n * p.dv + 32 * k + 8 * g) * 4 : -32;
-            const f4 v[4] = {__builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rS, off, 0, 0)),
-                             __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rS, off, 16, 0)),
-                             __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rD, off, 0, 0)),
-                             __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rD, off, 16, 0))};
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                Sr[k][j] = v[0][j];
-                Sr[k][4 + j] = v[1][j];
-                dSr[k][j] = v[2][j];
-                dSr[k][4 + j] = v[3][j];
-            }
+        for (int q = 0; q < 4; q++) {
+            const float rt = lds.rt[par][tq * (tq + 1) / 2 + (q <= tq ? q : 0)][tl], ct = lds.ct[par][(q >= tq ? q * (q + 1) / 2 : 0) + tq][tl];
+            racc += q <= tq ? rt : 0.0f;
+            cacc += q >= tq ? ct : 0.0f;
         }
+        float inner = 0.0f;
+#pragma unroll
+        for (int q = 0; q < NTL; q++) {
+            racc += lds.ri[par][q][lane];
+            inner += lds.ci[par][q][lane];
+        }
+        cacc += inner;
+        iacc += inner;
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+            sdacc += lds.sd[par][q];
+            ddacc += lds.dd[par][q];
+        }
+        if (it % tiles != tiles - 1) return;
+        RateSums& o = sums[slot * p.H + h0 + it / tiles];
+        o.r[lane] = racc;
+        o.c[lane] = cacc;
+        o.inner[lane] = iacc;
+        if (lane == 0) {
+            o.sd = sdacc;
+            o.dd = ddacc;
+        }
+        racc = cacc = iacc = sdacc = ddacc = 0.0f;
     };
-    float racc = 0.0f, cacc = 0.0f, iacc = 0.0f, sdacc = 0.0f, ddacc = 0.0f;  // wave 0: the head's sums, lane = token
-    float zt = 0.0f;
-    fetch(h0, 0);
-    const int iters = (h1 - h0) * tiles;
+
     for (int it = 0; it < iters; it++) {
-        const int h = h0 + it / tiles, tile = it % tiles;
-        const float A = p.A[h];
+        const int h = h0 + it / tiles, tile = it % tiles, par = it & 1;
+        const Decay& d = lds.d;
         const float Dh = p.D ? p.D[h] : 0.0f;
-        // ---- this head's tiles to LDS
+        const int next = it + 1 < iters ? it + 1 : it;
+        // ---- this head's tiles to LDS, S and dS as operands (row n0 + lm, columns 32 k + 8 g ..)
         tx.store(lds.x, RX);
         ty.store(lds.dy, RX);
-        if (wave == 0 && tile == 0) {
-            zt = rdt.value(p) + (p.bias ? p.bias[h] : 0.0f);
-            make_decay(lds.d, lane < live ? (p.softplus ? softplus_fine(zt) : zt) : 0.0f, A);
-        }
+        td.store(lds.d, 0);
+        typename MT::Frag Sf[2][P2], dSf[2][P2];
         float sd = 0.0f;
 #pragma unroll
         for (int k = 0; k < 2; k++) {
@@ -332,11 +396,11 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
             }
         }
         sd = part == 0 ? wave_sum(sd) : 0.0f;
-        if (lane == 0) lds.sd[it & 1][wave] = sd;  // (wave 0 may still read the last iteration's)
+        if (lane == 0) lds.sd[par][wave] = sd;
         __syncthreads();
-        if (it + 1 < iters) fetch(h0 + (it + 1) / tiles, (it + 1) % tiles);
 
         // ---- pairs: dM^T tiles (rows s, columns t)
+        if (sizeof(T) == 2) fetch_state(next, Sin, Sr);  // (FP32: no registers to hold it so early)
         float diag = 0.0f;
 #pragma unroll
         for (int q = 0; q < 2; q++) {
@@ -344,15 +408,19 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
             if (k >= 10) continue;
             int ti, si;
             lower_tile_of(k, ti, si);
+            const int t = 16 * ti + lm, s0 = 16 * si + 4 * g;
+            typename MT::Frag xf[2], yf[2];
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++) {
+                xf[ks] = MT::row8(lds.x + (16 * si + lm) * RX + 32 * ks + 8 * g);
+                yf[ks] = MT::row8(lds.dy + t * RX + 32 * ks + 8 * g);
+            }
+            const float thi = d.hi[t], tlo = d.lo[t];
+            const f4 shi = *reinterpret_cast<const f4*>(d.hi + s0), slo = *reinterpret_cast<const f4*>(d.lo + s0);
+            const f4 sdl = *reinterpret_cast<const f4*>(d.delta + s0);
             f4 acc = {};
 #pragma unroll
-            for (int ks = 0; ks < 2; ks++)
-                acc = MT::mma(MT::row8(lds.x + (16 * si + lm) * RX + 32 * ks + 8 * g),
-                              MT::row8(lds.dy + (16 * ti + lm) * RX + 32 * ks + 8 * g), acc);
-            const int t = 16 * ti + lm, s0 = 16 * si + 4 * g;
-            const float thi = lds.d.hi[t], tlo = lds.d.lo[t];
-            const f4 shi = *reinterpret_cast<const f4*>(lds.d.hi + s0), slo = *reinterpret_cast<const f4*>(lds.d.lo + s0);
-            const f4 sdl = *reinterpret_cast<const f4*>(lds.d.delta + s0);
+            for (int ks = 0; ks < 2; ks++) acc = MT::mma(xf[ks], yf[ks], acc);
             float m[4], dg[4], pc[4], pr = 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; r++) {
@@ -365,60 +433,77 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                 pr = __builtin_fmaf(pc[r], dl, pr);
                 if (s == t) diag += acc[r];
             }
-            MT::template put4<P2>(&lds.m[0][t * RM + s0], kQ * RM, m);
-            MT::template put4<P2>(&lds.dg[0][t * RM + s0], kQ * RM, dg);
+            MT::template put4<1>(&lds.m[t * RM + s0], 0, m);
+            MT::template put4<1>(&lds.dg[t * RM + s0], 0, dg);
             pr = rows_sum(pr);
-            if (g == 0) lds.rt[k][lm] = pr;
+            if (g == 0) lds.rt[par][k][lm] = pr;
 #pragma unroll
             for (int r = 0; r < 4; r++) {
                 const float s = group_sum<16>(pc[r]);
-                if (lm == 0) lds.ct[k][4 * g + r] = s;
+                if (lm == 0) lds.ct[par][k][4 * g + r] = s;
             }
         }
         diag = wave_sum(diag);
-        if (lane == 0) lds.dd[wave] = diag;
+        if (lane == 0) lds.dd[par][wave] = diag;
+        if (wave == kJoin && it > 0) join(it - 1);
         __syncthreads();
 
-        __builtin_amdgcn_sched_barrier(0);  // (hoisted loads of later parts would not fit the registers)
         // ---- dX^T: rows: columns pc + 4 g + r; column: s
+        if (sizeof(T) == 2) fetch_state(next, dSe, dSr);
         {
             const int pc = 16 * (wave & 3), half = wave >> 2;
-            typename MT::Frag dyT[2];
-#pragma unroll
-            for (int k = 0; k < 2; k++) dyT[k] = MT::col8(lds.dy, RX, 32 * k, pc, lane);
             f4 acc[2] = {};
 #pragma unroll
-            for (int ks = 0; ks < KS; ks++) {
-                typename MT::Frag dsT[P2];
-                if constexpr (sizeof(T) == 2) {
+            for (int k1 = 0; k1 < KS; k1 += 2) {
+                typename MT::Frag dsT[2][P2], bf[2][2];
 #pragma unroll
-                    for (int k = 0; k < P2; k++) dsT[k] = MT::col8(lds.ds[k], RX, 32 * ks, pc, lane);
-                } else {
-                    const float* d = dSe + (static_cast<size_t>(slot) * p.H + h) * head + tile * kPT + pc + lm;
+                for (int q = 0; q < 2; q++) {
+                    const int ks = k1 + q;
+                    if (ks >= KS) continue;
 #pragma unroll
-                    for (int j = 0; j < 8; j++) {
-                        const int n = 32 * ks + 8 * g + j;
-                        dsT[0][j] = n < p.dk ? d[static_cast<size_t>(n) * p.dv] : 0.0f;
+                    for (int j = 0; j < 2; j++) bf[q][j] = MT::row8(lds.b + (32 * half + 16 * j + lm) * RB + 32 * ks + 8 * g);
+                    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                        for (int k = 0; k < P2; k++) dsT[q][k] = MT::col8(lds.ds[k], RX, 32 * ks, pc, lane);
+                    } else {
+                        const float* src = dSe + (static_cast<size_t>(slot) * p.H + h) * head + tile * kPT + pc + lm;
+#pragma unroll
+                        for (int j = 0; j < 8; j++) {
+                            const int n = 32 * ks + 8 * g + j;
+                            dsT[q][0][j] = n < p.dk ? src[static_cast<size_t>(n) * p.dv] : 0.0f;
+                        }
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    const typename MT::Frag bf = MT::row8(lds.b + (32 * half + 16 * j + lm) * RB + 32 * ks + 8 * g);
+                for (int q = 0; q < 2; q++)
 #pragma unroll
-                    for (int k = 0; k < P2; k++) acc[j] = MT::mma(dsT[k], bf, acc[j]);
-                }
+                    for (int k = 0; k < P2; k++)
+#pragma unroll
+                        for (int j = 0; j < 2; j++)
+                            if (k1 + q < KS) acc[j] = MT::mma(dsT[q][k], bf[q][j], acc[j]);
             }
+            typename MT::Frag dyT[2], mf[2][2];
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++) {
+                dyT[ks] = MT::col8(lds.dy, RX, 32 * ks, pc, lane);
+#pragma unroll
+                for (int j = 0; j < 2; j++) mf[ks][j] = MT::col8(lds.m, RM, 32 * ks, 32 * half + 16 * j, lane);
+            }
+            float w[2];
+#pragma unroll
+            for (int j = 0; j < 2; j++) w[j] = d.w[32 * half + 16 * j + lm];
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < 2; j++) acc[j] *= w[j];
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++)
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+                    if (ks >= half) acc[j] = MT::mma(dyT[ks], mf[ks][j], acc[j]);  // (tokens before s: zero)
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 const int s = 32 * half + 16 * j + lm;
-                acc[j] *= lds.d.w[s];
-#pragma unroll
-                for (int ks = 0; ks < 2; ks++) {
-                    if (ks < half) continue;  // tokens before s
-#pragma unroll
-                    for (int k = 0; k < P2; k++)
-                        acc[j] = MT::mma(dyT[ks], MT::col8(lds.m[k], RM, 32 * ks, 32 * half + 16 * j, lane), acc[j]);
-                }
                 float yv[4];
                 MT::get4(lds.dy + s * RX + pc + 4 * g, yv);
 #pragma unroll
@@ -430,105 +515,61 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                 }
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
         // ---- dC^T, dB^T: rows n of this wave, columns t, s
-        {
-            typename MT::Frag bT[2], cT[2];
+        fetch_rows(next);
 #pragma unroll
-            for (int k = 0; k < 2; k++) {
-                bT[k] = MT::col8(lds.b, RB, 32 * k, n0, lane);
-                cT[k] = MT::col8(lds.c, RB, 32 * k, n0, lane);
+        for (int ii = 0; ii < TI; ii++) {
+            const int i = part * TI + ii, t = 16 * i + lm;
+            __builtin_amdgcn_sched_barrier(0);
+            typename MT::Frag yf[2], xf[2], gr[2], gc[2];
+#pragma unroll
+            for (int ks = 0; ks < 2; ks++) {
+                yf[ks] = MT::row8(lds.dy + t * RX + 32 * ks + 8 * g);
+                xf[ks] = MT::row8(lds.x + t * RX + 32 * ks + 8 * g);
+                gr[ks] = MT::row8(&lds.dg[t * RM + 32 * ks + 8 * g]);
+                gc[ks] = MT::col8(lds.dg, RM, 32 * ks, 16 * i, lane);
             }
+            float cv[4], bv[4], ri = 0.0f, ci = 0.0f;
+            MT::get4(lds.c + t * RB + n0 + 4 * g, cv);
+            MT::get4(lds.b + t * RB + n0 + 4 * g, bv);
+            const float head_t = d.head[t], tail_t = d.tail[t], delta_t = d.delta[t];
+            __builtin_amdgcn_sched_barrier(0);
+            f4 a = {}, b = {};
 #pragma unroll
-            for (int ii = 0; ii < TI; ii++) {
-                const int i = part * TI + ii, t = 16 * i + lm;
-                __builtin_amdgcn_sched_barrier(0);
-                f4 a = {}, b = {};
+            for (int ks = 0; ks < 2; ks++)
 #pragma unroll
-                for (int ks = 0; ks < 2; ks++) {
-                    const typename MT::Frag yf = MT::row8(lds.dy + t * RX + 32 * ks + 8 * g);
-                    const typename MT::Frag xf = MT::row8(lds.x + t * RX + 32 * ks + 8 * g);
-#pragma unroll
-                    for (int k = 0; k < P2; k++) {
-                        a = MT::mma(Sf[ks][k], yf, a);
-                        b = MT::mma(dSf[ks][k], xf, b);
-                    }
+                for (int k = 0; k < P2; k++) {
+                    a = MT::mma(Sf[ks][k], yf[ks], a);
+                    b = MT::mma(dSf[ks][k], xf[ks], b);
                 }
-                a *= lds.d.head[t];
-                b *= lds.d.tail[t];
-                float cv[4], bv[4], ri = 0.0f, ci = 0.0f;
-                MT::get4(lds.c + t * RB + n0 + 4 * g, cv);
-                MT::get4(lds.b + t * RB + n0 + 4 * g, bv);
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    ri = __builtin_fmaf(a[r], cv[r], ri);
-                    ci = __builtin_fmaf(b[r], bv[r], ci);
-                }
-                ri = rows_sum(ri);
-                ci = rows_sum(ci);
-                if (g == 0) {
-                    lds.ri[wave % NTL][t] = ri;
-                    lds.ci[wave % NTL][t] = ci;
-                }
-                dC[ii] += a;
-                dB[ii] += b * lds.d.delta[t];
-#pragma unroll
-                for (int ks = 0; ks < 2; ks++) {
-                    if (ks <= i / 2) {
-#pragma unroll
-                        for (int k = 0; k < P2; k++)
-                            dC[ii] = MT::mma(bT[ks], MT::row8(&lds.dg[k][t * RM + 32 * ks + 8 * g]), dC[ii]);
-                    }
-                    if (ks >= i / 2) {
-#pragma unroll
-                        for (int k = 0; k < P2; k++)
-                            dB[ii] = MT::mma(cT[ks], MT::col8(lds.dg[k], RM, 32 * ks, 16 * i, lane), dB[ii]);
-                    }
-                }
+            for (int ks = 0; ks < 2; ks++) {
+                if (ks <= i / 2) dC[ii] = MT::mma(bT[ks], gr[ks], dC[ii]);
+                if (ks >= i / 2) dB[ii] = MT::mma(cT[ks], gc[ks], dB[ii]);
             }
+            a *= head_t;
+            b *= tail_t;
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                ri = __builtin_fmaf(a[r], cv[r], ri);
+                ci = __builtin_fmaf(b[r], bv[r], ci);
+            }
+            ri = rows_sum(ri);
+            ci = rows_sum(ci);
+            if (g == 0) {
+                lds.ri[par][wave % NTL][t] = ri;
+                lds.ci[par][wave % NTL][t] = ci;
+            }
+            dC[ii] += a;
+            dB[ii] += b * delta_t;
+        }
+        if (sizeof(T) == 4) {
+            fetch_state(next, Sin, Sr);
+            fetch_state(next, dSe, dSr);
         }
         __syncthreads();
-
-        // ---- the decays' gradients, once a head
-        if (wave == 0) {
-            const int tq = lane >> 4, tl = lane & 15;
-            for (int si = 0; si <= tq; si++) racc += lds.rt[tq * (tq + 1) / 2 + si][tl];
-            for (int ti = tq; ti < 4; ti++) cacc += lds.ct[ti * (ti + 1) / 2 + tq][tl];
-            float inner = 0.0f;
-#pragma unroll
-            for (int k = 0; k < NTL; k++) {
-                racc += lds.ri[k][lane];
-                inner += lds.ci[k][lane];
-            }
-            cacc += inner;
-            iacc += inner;
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                sdacc += lds.sd[it & 1][k];
-                ddacc += lds.dd[k];
-            }
-            if (tile == tiles - 1) {
-                const float delta = lds.d.delta[lane];
-                double v = static_cast<double>(racc) - static_cast<double>(delta) * cacc;
-                const double into = wave_last(wave_prefix(static_cast<double>(delta) * iacc));
-                if (lane == 63) v += static_cast<double>(lds.d.total) * sdacc + into;
-                const double pre = wave_prefix(v);
-                const double rate = wave_last(pre) - pre + v;  // suffix sum: the log decay's gradient
-                const float dd = cacc + A * static_cast<float>(rate);
-                const float dz = lane < live ? (p.softplus ? dd * sigmoid_fine(zt) : dd) : 0.0f;
-                if (lane < live) store_elem(ddt, (row0 + lane) * p.ld_dt + h, p.dt_dtype, dz);
-                const float da = static_cast<float>(wave_last(wave_prefix(rate * delta)));
-                const float db = static_cast<float>(wave_last(wave_prefix(static_cast<double>(dz))));
-                if (lane == 0) {
-                    float* o = hp + static_cast<size_t>(slot) * 3 * p.H + h;
-                    o[0] = da;
-                    o[p.H] = ddacc;
-                    o[2 * p.H] = db;
-                }
-                racc = cacc = iacc = sdacc = ddacc = 0.0f;
-            }
-        }
     }
+    if (wave == kJoin) join(iters - 1);
     // ---- db, dc
     const int n = n0 + 4 * g;
     if (n >= p.dk) return;
@@ -588,6 +629,40 @@ __global__ __launch_bounds__(256) void clear_outside_kernel(ScanP p, T* dx, void
     for (int i = threadIdx.x; i < p.H; i += 256) store_elem(ddt, t * p.ld_dt + i, p.dt_dtype, 0.0f);
 }
 
+// The decays' gradients of every chunk, a wave each: the suffix sums of r_t - Delta_t c_t and what
+// the last token gets from the chunk's end, in double (the terms cancel); ddt, and the chunk's
+// share of dA, dD and ddt_bias to hp [slot][3][H].
+__global__ __launch_bounds__(256) void rates_kernel(ScanP p, const Decay* decays, const RateSums* sums, void* ddt, float* hp, int nmax) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + wave;  // (b, chunk, h), h fastest
+    const int h = static_cast<int>(unit % p.H), ch = static_cast<int>(unit / p.H % nmax);
+    const int64_t b = unit / p.H / nmax;
+    if (b >= p.B) return;
+    const SeqRange sr = seq_range(p, static_cast<int>(b));
+    const int live = sr.len - ch * kQ;
+    if (live <= 0) return;
+    const int64_t slot = slot_of(p, static_cast<int>(b), sr.begin, ch);
+    const Decay& d = decays[slot * p.H + h];
+    const RateSums& m = sums[slot * p.H + h];
+    const float delta = d.delta[lane], c = m.c[lane];
+    double v = static_cast<double>(m.r[lane]) - static_cast<double>(delta) * c;
+    const float into = wave_sum(delta * m.inner[lane]);
+    if (lane == 63) v += static_cast<double>(d.total[0]) * m.sd + into;
+    const double pre = wave_prefix(v);
+    const double rate = wave_last(pre) - pre + v;  // the log decay's gradient
+    const float dd = static_cast<float>(c + static_cast<double>(p.A[h]) * rate);
+    const float dz = lane < live ? (p.softplus ? dd * sigmoid_fine(d.z[lane]) : dd) : 0.0f;
+    if (lane < live) store_elem(ddt, (sr.begin + static_cast<int64_t>(ch) * kQ + lane) * p.ld_dt + h, p.dt_dtype, dz);
+    const float da = static_cast<float>(wave_last(wave_prefix(rate * delta)));
+    const float db = wave_sum(dz);
+    if (lane == 0) {
+        float* o = hp + static_cast<size_t>(slot) * 3 * p.H + h;
+        o[0] = da;
+        o[p.H] = m.dd;
+        o[2 * p.H] = db;
+    }
+}
+
 // The heads' dA, dD and ddt_bias over all chunks (a packing's unused slots hold nothing).
 __global__ __launch_bounds__(256) void head_sums_kernel(ScanP p, const float* hp, int64_t slots, float* dA, float* dD, float* dbias) {
     __shared__ double red[256];
@@ -635,7 +710,7 @@ int grad_slices(const la_scan_config& c) {
 }
 
 struct BwdWs {
-    size_t S, dS, decay, dbp, dcp, hp, total;
+    size_t S, dS, decays, sums, dbp, dcp, hp, total;
 };
 BwdWs bwd_ws(const la_scan_config& c) {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
@@ -646,8 +721,9 @@ BwdWs bwd_ws(const la_scan_config& c) {
     BwdWs w;
     w.S = 0;
     w.dS = w.S + st;
-    w.decay = w.dS + st;
-    w.dbp = w.decay + up(static_cast<size_t>(slots) * c.H * sizeof(float));
+    w.decays = w.dS + st;
+    w.sums = w.decays + up(static_cast<size_t>(slots) * c.H * sizeof(Decay));
+    w.dbp = w.sums + up(static_cast<size_t>(slots) * c.H * sizeof(RateSums));
     w.dcp = w.dbp + bc;
     w.hp = w.dcp + bc;
     w.total = w.hp + up(static_cast<size_t>(slots) * 3 * c.H * sizeof(float));
@@ -660,22 +736,25 @@ hipError_t launch(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
     const BwdWs w = bwd_ws(c);
     float* S = reinterpret_cast<float*>(a.ws + w.S);
     float* dS = reinterpret_cast<float*>(a.ws + w.dS);
-    float* decay = reinterpret_cast<float*>(a.ws + w.decay);
+    Decay* decays = reinterpret_cast<Decay*>(a.ws + w.decays);
+    RateSums* sums = reinterpret_cast<RateSums*>(a.ws + w.sums);
     float* hp = reinterpret_cast<float*>(a.ws + w.hp);
     const int64_t rows = a.cu ? c.T : static_cast<int64_t>(c.B) * c.T;
     const int nmax = (c.T + kQ - 1) / kQ;
     const int64_t slots = a.cu ? static_cast<int64_t>(c.B) + c.T / kQ + 1 : static_cast<int64_t>(c.B) * nmax;
     const int64_t groups = static_cast<int64_t>(c.B) * c.H * (c.d_v / kPT);
     const T* dy = static_cast<const T*>(a.dy);
+    const unsigned units = static_cast<unsigned>((static_cast<int64_t>(c.B) * nmax * c.H + 3) / 4);
+    decays_kernel<<<dim3(units), 256, 0, s>>>(p, decays, nmax);
     // Enough heads: a workgroup walks a sequence.  Fewer than a workgroup a CU: one a chunk
     // and a joining pass (three times the state traffic, but no walk).
     if (groups >= 256 || nmax < 8) {
-        scan_walk_kernel<T, N, false><<<dim3(static_cast<unsigned>(2 * groups)), 256, 0, s>>>(p, dy, a.S0, a.dST, S, dS, nullptr, a.dS0);
+        scan_walk_kernel<T, N, false><<<dim3(static_cast<unsigned>(2 * groups)), 256, 0, s>>>(p, dy, a.S0, a.dST, S, dS, decays, a.dS0);
     } else {
         const unsigned grid = static_cast<unsigned>(2 * groups * nmax);
         const unsigned join = static_cast<unsigned>((static_cast<int64_t>(c.B) * c.H * (c.d_k * c.d_v / 4) + 255) / 256);
-        scan_walk_kernel<T, N, true><<<dim3(grid), 256, 0, s>>>(p, dy, nullptr, nullptr, S, dS, decay, nullptr);
-        walk_join_kernel<<<dim3(join, 2), 256, 0, s>>>(p, a.S0, a.dST, S, dS, decay, a.dS0);
+        scan_walk_kernel<T, N, true><<<dim3(grid), 256, 0, s>>>(p, dy, nullptr, nullptr, S, dS, decays, nullptr);
+        walk_join_kernel<<<dim3(join, 2), 256, 0, s>>>(p, a.S0, a.dST, S, dS, decays, a.dS0);
     }
     const int slices = grad_slices(c);
     float* dbp = slices > 1 ? reinterpret_cast<float*>(a.ws + w.dbp) : nullptr;
@@ -684,7 +763,8 @@ hipError_t launch(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
                                        hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(GradLds<T, N>)));
     if (e != hipSuccess) return e;
     scan_grad_kernel<T, N><<<dim3(static_cast<unsigned>(slots * c.G * slices)), 512, sizeof(GradLds<T, N>), s>>>(
-        p, dy, S, dS, a.dx, a.ddt, a.db, a.dc, dbp, dcp, hp, slots, slices, rows);
+        p, dy, S, dS, a.dx, a.db, a.dc, dbp, dcp, decays, sums, slices, rows);
+    rates_kernel<<<dim3(units), 256, 0, s>>>(p, decays, sums, a.ddt, hp, nmax);
     if (slices > 1) {
         const int64_t items = rows * (c.G * c.d_k / 4);
         join_slices_kernel<T><<<dim3(static_cast<unsigned>((items + 255) / 256)), 256, 0, s>>>(

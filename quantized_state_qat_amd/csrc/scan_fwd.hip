@@ -64,7 +64,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
     const int c1 = c0 + cps < nch ? c0 + cps : nch;
     if (c0 >= nch && !(nch == 0 && seg == 0)) return;
     const float A = p.A ? p.A[h] : 0.0f;  // (no tokens: A may be missing)
-    const float Dh = FULL && p.D ? p.D[h] : 0.0f;
+    const float Dh = FULL && p.D ? p.D[h] : 0.0f, bias = p.bias ? p.bias[h] : 0.0f;
 
     if (FULL) {  // the tiles above the diagonal that the products below read stay zero
         for (int q = 0; q < NB; q++)
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
         };
         double cum_seg = 0.0;
         auto decays_of = [&](int ch, const Ahead& r) {  // by one wave
-            cum_seg += make_decay(decays[(ch - c0) % 3], lane < sr.len - ch * kQ ? step_of(p, r.raw.value(p), h) : 0.0f, A);
+            cum_seg += make_decay(decays[(ch - c0) % 3], r.raw.value(p) + bias, p.softplus, sr.len - ch * kQ, A);
         };
         auto stage = [&](Buf& lds, const Ahead& r) {
             r.b.store(lds.b, RB);
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
         }
     };
     auto update = [&](const Buf& lds, const Decay& d, const typename MT::Frag (&wx)[2][P3]) {  // S = total S + B^T (W x)
-        const float total = d.total;
+        const float total = d.total[0];
 #pragma unroll
         for (int k = 0; k < 2; k++) {
             typename MT::Frag bf[N / 16];

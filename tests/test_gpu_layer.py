@@ -7,7 +7,11 @@ the value) plus a share of its magnitude, the sum of its terms' absolute values:
   scan          operands in two bf16 parts (2^-17 each, two in a product: 2^-16), at most 192
                 terms a sum in FP32 (192 x 2^-24 < 2^-16), decays to a few 2^-22: 2^-14.  The
                 rates' gradients are suffix sums over a chunk of terms that cancel: their
-                magnitude is the chunk's sum of the terms' absolute values.
+                magnitude is the chunk's sum of the terms' absolute values.  With bf16 inputs
+                the pair products' factor enters dx, db and dc rounded to bf16 once, half a step
+                of every term: 2^-8 more for these; and as such errors are independent, the
+                2-norm of theirs and of the result's own rounding stays within 2^-8 of the
+                result's (two errors uniform in +-2^-8 of a value: sqrt(2/3) 2^-8).
   norm          a row's mean and two products in FP32: 2^-19 (d <= 16384 terms, summed in
                 pieces of at most 64 per lane).
 """
@@ -287,7 +291,10 @@ class Scan:
         for k, t in o.items():
             if k == "dD" and self.D is None or k == "ddt_bias" and self.bias is None:
                 pass  # written all the same
-            close(t.reshape(w[k].shape), w[k], m[k], share, k)
+            once = 2.0 ** -8 if self.dtype == BF and k in ("dx", "db", "dc") else 0.0
+            close(t.reshape(w[k].shape), w[k], m[k], share + once, k)
+            if once and t.numel() >= 1024:
+                assert np.linalg.norm(np64(t).reshape(w[k].shape) - w[k]) <= 2.0 ** -8 * np.linalg.norm(w[k]), k
 
 
 SCAN = [
