@@ -157,6 +157,12 @@ struct Mat<float> {
     }
 };
 
+// x, as a value that the compiler knows nothing about.
+__device__ __forceinline__ int opaque(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // 2^(hi + lo) for |lo| far below an ulp of hi.
 __device__ __forceinline__ float exp2_two(float hi, float lo) {
     const float r = __builtin_amdgcn_exp2f(hi);
@@ -239,16 +245,19 @@ __device__ __forceinline__ double make_decay(Decay& d, float z, int softplus, in
     if (t == 63) d.total[0] = exp2_two(hi, lo);
     return end;
 }
-// A Decay on its way from memory to LDS: 16 bytes a thread, threads first .. first + 127.
+// A Decay on its way from memory to LDS, a few words a thread.
+template <int THREADS>
 struct DecayAhead {
-    uv4 r;
-    __device__ __forceinline__ void load(const Decay* from, int first) {
+    static constexpr int W = static_cast<int>(sizeof(Decay) / 4) / THREADS;
+    uint32_t r[W];
+    __device__ __forceinline__ void load(const Decay* from) {
         const __amdgpu_buffer_rsrc_t rs = make_rsrc(from, sizeof(Decay));
-        r = __builtin_bit_cast(uv4, __builtin_amdgcn_raw_buffer_load_b128(rs, (static_cast<int>(threadIdx.x) - first) * 16, 0, 0));
+#pragma unroll
+        for (int i = 0; i < W; i++) r[i] = __builtin_amdgcn_raw_buffer_load_b32(rs, static_cast<int>(threadIdx.x) * 4, i * THREADS * 4, 0);
     }
-    __device__ __forceinline__ void store(Decay& to, int first) const {
-        const int i = static_cast<int>(threadIdx.x) - first;
-        if (i >= 0 && i < static_cast<int>(sizeof(Decay) / 16)) reinterpret_cast<uv4*>(&to)[i] = r;
+    __device__ __forceinline__ void store(Decay& to) const {
+#pragma unroll
+        for (int i = 0; i < W; i++) reinterpret_cast<uint32_t*>(&to)[threadIdx.x + i * THREADS] = r[i];
     }
 };
 // Eight consecutive values of one of the arrays (16-byte aligned).
@@ -349,9 +358,16 @@ struct Tile {
 
 // Workgroups go round the eight dies in launch order: unit u of consecutive ones on one die,
 // so that the heads that read the same b and c share its L2.
-__device__ __forceinline__ int64_t die_unit(int64_t block, int64_t blocks) {
-    const int64_t q = blocks / 8, r = blocks % 8, d = block % 8;
+__device__ __forceinline__ uint32_t die_unit(uint32_t block, uint32_t blocks) {
+    const uint32_t q = blocks / 8, r = blocks % 8, d = block % 8;
     return d * q + (d < r ? d : r) + block / 8;
+}
+// u modulo n, u divided by n: the result in scalar registers (the same in every lane).
+__device__ __forceinline__ int take(uint32_t& u, int n) {
+    const uint32_t q = u / static_cast<uint32_t>(n);
+    const int r = __builtin_amdgcn_readfirstlane(static_cast<int>(u - q * n));
+    u = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(q)));
+    return r;
 }
 
 }  // namespace la

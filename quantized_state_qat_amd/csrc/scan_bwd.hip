@@ -72,21 +72,17 @@ __global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* dy, co
     const int lm = lane & 15, g = lane >> 4;
 
     const int tiles = p.dv / kPT, nmax = (p.T + kQ - 1) / kQ;
-    int64_t u = die_unit(blockIdx.x, gridDim.x);
-    const bool rev = u & 1;
-    u >>= 1;
-    const int tile = static_cast<int>(u % tiles);
-    u /= tiles;
-    const int h = static_cast<int>(u % p.H);
-    u /= p.H;
+    uint32_t u = die_unit(blockIdx.x, gridDim.x);
+    const bool rev = take(u, 2) != 0;
+    const int tile = take(u, tiles), h = take(u, p.H);
     const float* first = rev ? dST : S0;
     float* states = rev ? dSst : Sst;
     float* last = rev ? dS0 : nullptr;
     const int64_t ld_x = rev ? static_cast<int64_t>(p.H) * p.dv : p.ld_x;
-    const int bi = static_cast<int>(ONE ? u / nmax : u);
+    const int only = ONE ? take(u, nmax) : 0;
+    const int bi = static_cast<int>(u);
     const SeqRange sr = seq_range(p, bi);
     const int nch = (sr.len + kQ - 1) / kQ;
-    const int only = ONE ? static_cast<int>(u % nmax) : 0;
     if (ONE && only >= nch) return;
     const int steps = ONE ? 1 : nch;
     const int grp = h / (p.H / p.G);
@@ -113,21 +109,21 @@ __global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* dy, co
     const int64_t ld_b = rev ? p.ld_c : p.ld_b;
     Tile<T, N, 256> tb;
     Tile<T, kPT, 256> tx;
-    DecayAhead td;
+    DecayAhead<256> td;
     auto at_step = [&](int i) { return ONE ? only : rev ? nch - 1 - i : i; };
     auto fetch = [&](int ch) {
         const int64_t row0 = sr.begin + static_cast<int64_t>(ch) * kQ;
         const int live = sr.len - ch * kQ;
         tb.load(bg + row0 * ld_b, ld_b, live, p.dk);
         tx.load(xg + row0 * ld_x, ld_x, live, kPT);
-        td.load(decays + slot_of(p, bi, sr.begin, ch) * p.H + h, 0);
+        td.load(decays + slot_of(p, bi, sr.begin, ch) * p.H + h);
     };
     if (steps > 0) fetch(at_step(0));
     for (int i = 0; i < steps; i++) {
         const int ch = at_step(i);
         tb.store(lds.b, RB);
         tx.store(lds.x, RX);
-        td.store(lds.d, 0);
+        td.store(lds.d);
         __syncthreads();
         if (i + 1 < steps) fetch(at_step(i + 1));
         float* slot = states + (static_cast<size_t>(slot_of(p, bi, sr.begin, ch)) * p.H + h) * head;
@@ -239,19 +235,16 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
     GradLds<T, N>& lds = *reinterpret_cast<GradLds<T, N>*>(raw_lds);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lm = lane & 15, g = lane >> 4;
-    const int n0 = 16 * (wave % NTL), part = wave / NTL;  // state rows and token part of dC, dB
+    const int nt = PARTS == 1 ? wave : wave % NTL, n0 = 16 * nt, part = PARTS == 1 ? 0 : wave / NTL;  // state rows and token part of dC, dB
     constexpr int kJoin = 7;                              // the wave that joins the sums
 
-    int64_t u = die_unit(blockIdx.x, gridDim.x);
-    const int slice = static_cast<int>(u % slices);
-    u /= slices;
-    const int grp = static_cast<int>(u % p.G);
-    const int64_t slot = u / p.G;
+    uint32_t u = die_unit(blockIdx.x, gridDim.x);
+    const int slice = take(u, slices), grp = take(u, p.G);
+    const int64_t slot = u;
     int bi, ch;
     if (!p.cu) {
-        const int nmax = (p.T + kQ - 1) / kQ;
-        bi = static_cast<int>(slot / nmax);
-        ch = static_cast<int>(slot % nmax);
+        ch = take(u, (p.T + kQ - 1) / kQ);
+        bi = static_cast<int>(u);
         if (bi >= p.B) return;
     } else {  // the last b with b + begin_b / 64 <= slot
         int lo = 0, hi = p.B - 1;
@@ -268,7 +261,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
     const int64_t row0 = sr.begin + static_cast<int64_t>(ch) * kQ;
     const int live = sr.len - ch * kQ < kQ ? sr.len - ch * kQ : kQ;
 
-    const int hpg = p.H / p.G, per = (hpg + slices - 1) / slices;
+    const int hpg = __builtin_amdgcn_readfirstlane(p.H / p.G), per = __builtin_amdgcn_readfirstlane((hpg + slices - 1) / slices);
     const int h0 = grp * hpg + slice * per;
     const int h1 = slice * per + per < hpg ? h0 + per : (grp + 1) * hpg;
     const int tiles = p.dv / kPT;
@@ -276,25 +269,28 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
     const int iters = (h1 - h0) * tiles;
 
     Tile<T, kPT, 512> tx, ty;
-    DecayAhead td;
+    DecayAhead<512> td;
     float Sr[2][8], dSr[2][8];
     auto fetch_rows = [&](int it) {
-        const int h = h0 + it / tiles, tile = it % tiles;
+        uint32_t q = static_cast<uint32_t>(it);
+        const int tile = take(q, tiles), h = h0 + static_cast<int>(q);
         tx.load(static_cast<const T*>(p.x) + row0 * p.ld_x + static_cast<int64_t>(h) * p.dv + tile * kPT, p.ld_x, live, kPT);
         ty.load(dyr + (row0 * p.H + h) * p.dv + tile * kPT, static_cast<int64_t>(p.H) * p.dv, live, kPT);
-        td.load(decays + slot * p.H + h, 0);
+        td.load(decays + slot * p.H + h);
     };
     const int soff = n0 + lm < p.dk ? ((n0 + lm) * p.dv + 8 * g) * 4 : -1024;
     auto fetch_state = [&](int it, const float* from, float (&to)[2][8]) {
-        const size_t at = (static_cast<size_t>(slot) * p.H + h0 + it / tiles) * head + (it % tiles) * kPT;
+        uint32_t q = static_cast<uint32_t>(it);
+        const int tile = take(q, tiles);
+        const size_t at = (static_cast<size_t>(slot) * p.H + h0 + q) * head + tile * kPT;
         const __amdgpu_buffer_rsrc_t r = make_rsrc(from + at, head * 4);
 #pragma unroll
         for (int k = 0; k < 2; k++)
 #pragma unroll
-            for (int q = 0; q < 2; q++) {
-                const f4 v = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, soff, 128 * k + 16 * q, 0));
+            for (int i = 0; i < 2; i++) {
+                const f4 v = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(r, soff, 128 * k + 16 * i, 0));
 #pragma unroll
-                for (int j = 0; j < 4; j++) to[k][4 * q + j] = v[j];
+                for (int j = 0; j < 4; j++) to[k][4 * i + j] = v[j];
             }
     };
     fetch_rows(0);
@@ -346,41 +342,46 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
             cacc += q >= tq ? ct : 0.0f;
         }
         float inner = 0.0f;
-#pragma unroll
-        for (int q = 0; q < NTL; q++) {
+#pragma unroll 2
+        for (int q = 0; q < NTL; q++) {  // (unrolled whole, its registers would spill others)
             racc += lds.ri[par][q][lane];
             inner += lds.ci[par][q][lane];
         }
         cacc += inner;
         iacc += inner;
-#pragma unroll
-        for (int q = 0; q < 8; q++) {
-            sdacc += lds.sd[par][q];
-            ddacc += lds.dd[par][q];
-        }
-        if (it % tiles != tiles - 1) return;
-        RateSums& o = sums[slot * p.H + h0 + it / tiles];
+        // lane q: wave q's
+        sdacc += lds.sd[par][lane & 7];
+        ddacc += lds.dd[par][lane & 7];
+        uint32_t q = static_cast<uint32_t>(it);
+        if (take(q, tiles) != tiles - 1) return;
+        RateSums& o = sums[slot * p.H + h0 + q];
         o.r[lane] = racc;
         o.c[lane] = cacc;
         o.inner[lane] = iacc;
+        const float sd = group_sum<8>(sdacc), dd = group_sum<8>(ddacc);
         if (lane == 0) {
-            o.sd = sdacc;
-            o.dd = ddacc;
+            o.sd = sd;
+            o.dd = dd;
         }
         racc = cacc = iacc = sdacc = ddacc = 0.0f;
     };
 
     for (int it = 0; it < iters; it++) {
-        const int h = h0 + it / tiles, tile = it % tiles, par = it & 1;
+        uint32_t qh = static_cast<uint32_t>(it);
+        const int tile = take(qh, tiles), h = h0 + static_cast<int>(qh), par = it & 1;
         const Decay& d = lds.d;
         const float Dh = p.D ? p.D[h] : 0.0f;
         const int next = it + 1 < iters ? it + 1 : it;
+        // (The lane's indices are made opaque in every part: addresses formed from them before the
+        // loop would fill the registers.)
         // ---- this head's tiles to LDS, S and dS as operands (row n0 + lm, columns 32 k + 8 g ..)
         tx.store(lds.x, RX);
         ty.store(lds.dy, RX);
-        td.store(lds.d, 0);
+        td.store(lds.d);
         typename MT::Frag Sf[2][P2], dSf[2][P2];
         float sd = 0.0f;
+        {
+        const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
 #pragma unroll
         for (int k = 0; k < 2; k++) {
 #pragma unroll
@@ -397,11 +398,14 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         }
         sd = part == 0 ? wave_sum(sd) : 0.0f;
         if (lane == 0) lds.sd[par][wave] = sd;
+        }
         __syncthreads();
 
         // ---- pairs: dM^T tiles (rows s, columns t)
         if (sizeof(T) == 2) fetch_state(next, Sin, Sr);  // (FP32: no registers to hold it so early)
         float diag = 0.0f;
+        {
+        const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
 #pragma unroll
         for (int q = 0; q < 2; q++) {
             const int k = wave + 8 * q;
@@ -443,6 +447,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                 if (lm == 0) lds.ct[par][k][4 * g + r] = s;
             }
         }
+        }
         diag = wave_sum(diag);
         if (lane == 0) lds.dd[par][wave] = diag;
         if (wave == kJoin && it > 0) join(it - 1);
@@ -451,6 +456,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         // ---- dX^T: rows: columns pc + 4 g + r; column: s
         if (sizeof(T) == 2) fetch_state(next, dSe, dSr);
         {
+            const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
             const int pc = 16 * (wave & 3), half = wave >> 2;
             f4 acc[2] = {};
 #pragma unroll
@@ -464,7 +470,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                     for (int j = 0; j < 2; j++) bf[q][j] = MT::row8(lds.b + (32 * half + 16 * j + lm) * RB + 32 * ks + 8 * g);
                     if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                        for (int k = 0; k < P2; k++) dsT[q][k] = MT::col8(lds.ds[k], RX, 32 * ks, pc, lane);
+                        for (int k = 0; k < P2; k++) dsT[q][k] = MT::col8(lds.ds[k], RX, 32 * ks, pc, ln);
                     } else {
                         const float* src = dSe + (static_cast<size_t>(slot) * p.H + h) * head + tile * kPT + pc + lm;
 #pragma unroll
@@ -486,9 +492,9 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
             typename MT::Frag dyT[2], mf[2][2];
 #pragma unroll
             for (int ks = 0; ks < 2; ks++) {
-                dyT[ks] = MT::col8(lds.dy, RX, 32 * ks, pc, lane);
+                dyT[ks] = MT::col8(lds.dy, RX, 32 * ks, pc, ln);
 #pragma unroll
-                for (int j = 0; j < 2; j++) mf[ks][j] = MT::col8(lds.m, RM, 32 * ks, 32 * half + 16 * j, lane);
+                for (int j = 0; j < 2; j++) mf[ks][j] = MT::col8(lds.m, RM, 32 * ks, 32 * half + 16 * j, ln);
             }
             float w[2];
 #pragma unroll
@@ -519,6 +525,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         fetch_rows(next);
 #pragma unroll
         for (int ii = 0; ii < TI; ii++) {
+            const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
             const int i = part * TI + ii, t = 16 * i + lm;
             __builtin_amdgcn_sched_barrier(0);
             typename MT::Frag yf[2], xf[2], gr[2], gc[2];
@@ -527,7 +534,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                 yf[ks] = MT::row8(lds.dy + t * RX + 32 * ks + 8 * g);
                 xf[ks] = MT::row8(lds.x + t * RX + 32 * ks + 8 * g);
                 gr[ks] = MT::row8(&lds.dg[t * RM + 32 * ks + 8 * g]);
-                gc[ks] = MT::col8(lds.dg, RM, 32 * ks, 16 * i, lane);
+                gc[ks] = MT::col8(lds.dg, RM, 32 * ks, 16 * i, ln);
             }
             float cv[4], bv[4], ri = 0.0f, ci = 0.0f;
             MT::get4(lds.c + t * RB + n0 + 4 * g, cv);
@@ -557,8 +564,8 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
             ri = rows_sum(ri);
             ci = rows_sum(ci);
             if (g == 0) {
-                lds.ri[par][wave % NTL][t] = ri;
-                lds.ci[par][wave % NTL][t] = ci;
+                lds.ri[par][nt][t] = ri;
+                lds.ci[par][nt][t] = ci;
             }
             dC[ii] += a;
             dB[ii] += b * delta_t;

@@ -48,14 +48,12 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
     const int lm = lane & 15, g = lane >> 4;
 
     const int tiles = p.dv / kPT;
-    int64_t u = die_unit(blockIdx.x, gridDim.x);
-    const int tile = static_cast<int>(u % tiles);
-    u /= tiles;
-    const int h = static_cast<int>(u % p.H);
-    u /= p.H;
-    const int seg = static_cast<int>(u % segs);  // segs: segments of this launch
-    const int bi = static_cast<int>(u / segs);
-    const int grp = h / (p.H / p.G);
+    uint32_t u = die_unit(blockIdx.x, gridDim.x);
+    const int tile = take(u, tiles), h = take(u, p.H), seg = take(u, segs);  // segs: segments of this launch
+    const int bi = static_cast<int>(u);
+    uint32_t hu = static_cast<uint32_t>(h);
+    take(hu, p.H / p.G);
+    const int grp = static_cast<int>(hu);
 
     const SeqRange sr = seq_range(p, bi);
     const int nch = (sr.len + kQ - 1) / kQ;
