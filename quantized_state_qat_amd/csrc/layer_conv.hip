@@ -15,12 +15,31 @@ template <int E, int W>
 struct Taps {
     float w[W][E];
     float bias[E];
+    // E W weights from c0 W on and E biases, in 16- or 8-byte pieces (c0 is a multiple of E).
     __device__ __forceinline__ void load(const void* wp, const void* bp, int dtype, int c0) {
+        if (dtype == LA_BF16) load_as<uint16_t>(wp, bp, c0);
+        else load_as<float>(wp, bp, c0);
+    }
+    template <class P>
+    __device__ __forceinline__ void load_as(const void* wp, const void* bp, int c0) {
+        constexpr int V = 8 / sizeof(P);  // elements of 8 bytes
+        const uv2* w8 = reinterpret_cast<const uv2*>(static_cast<const P*>(wp) + static_cast<size_t>(c0) * W);
+        uv2 raw[E * W / V], rb[E / V] = {};
+#pragma unroll
+        for (int i = 0; i < E * W / V; i++) raw[i] = w8[i];
+        if (bp) {
+#pragma unroll
+            for (int i = 0; i < E / V; i++) rb[i] = reinterpret_cast<const uv2*>(static_cast<const P*>(bp) + c0)[i];
+        }
+        auto at = [](const uv2* r, int i) {
+            if constexpr (sizeof(P) == 4) return __uint_as_float(r[i / 2][i % 2]);
+            else return (i & 1) ? hi16(r[i / 4][i % 4 / 2]) : lo16(r[i / 4][i % 4 / 2]);
+        };
 #pragma unroll
         for (int e = 0; e < E; e++) {
 #pragma unroll
-            for (int j = 0; j < W; j++) w[j][e] = load_elem(wp, static_cast<size_t>(c0 + e) * W + j, dtype);
-            bias[e] = bp ? load_elem(bp, c0 + e, dtype) : 0.0f;
+            for (int j = 0; j < W; j++) w[j][e] = at(raw, e * W + j);
+            bias[e] = at(rb, e);
         }
     }
 };
@@ -31,7 +50,38 @@ struct ConvGeom {
     const int32_t* cu;
 };
 
+// E elements of a row: 16 bytes, or 8 for four bf16.
+template <class T, int E>
+struct Piece {
+    using Raw = std::conditional_t<sizeof(T) * E == 16, uv4, uv2>;
+    static __device__ __forceinline__ Raw load(const T* p) { return *reinterpret_cast<const Raw*>(p); }
+    static __device__ __forceinline__ void widen(Raw r, float (&v)[E]) {
+        if constexpr (sizeof(T) * E == 16) {
+            la::widen(r, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                v[2 * i] = lo16(r[i]);
+                v[2 * i + 1] = hi16(r[i]);
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(T* p, const float (&v)[E]) {
+        if constexpr (sizeof(T) * E == 16) store16(p, narrow(v));
+        else *reinterpret_cast<uv2*>(p) = uv2{pack16(v[0], v[1]), pack16(v[2], v[3])};
+    }
+};
+
 // Row `pos` (>= -(W-1)) of sequence b, from x or from the state before it.
+template <class T, int W, int E>
+__device__ __forceinline__ void conv_row_e(const T* x, const T* s0, int64_t begin, int pos, int b, int C, int ldx, int c0, float (&v)[E]) {
+    if (pos >= 0) Piece<T, E>::widen(Piece<T, E>::load(x + (begin + pos) * ldx + c0), v);
+    else if (s0) Piece<T, E>::widen(Piece<T, E>::load(s0 + (static_cast<int64_t>(b) * (W - 1) + (pos + W - 1)) * C + c0), v);
+    else {
+#pragma unroll
+        for (int e = 0; e < E; e++) v[e] = 0.0f;
+    }
+}
 template <class T, int W>
 __device__ __forceinline__ uv4 conv_row(const T* x, const T* s0, int64_t begin, int pos, int b, int C, int ldx, int c0) {
     if (pos >= 0) return load16(x + (begin + pos) * ldx + c0);
@@ -119,22 +169,78 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvGeom<T> g, const T* _
     }
 }
 
+// dstate0: row j of z before x gets w[jj] dpre[j - jj] for jj <= j, and where the sequence is
+// shorter than j the final state's own row passes through.
+template <class T, int W, int ACT, int E>
+__device__ __forceinline__ void conv_bwd_state(const ConvGeom<T>& g, const T* x, const void* w, const void* bias, const T* s0,
+                                               const T* dy, const T* dsT, T* ds0, int b, int c0) {
+    using Pc = Piece<T, E>;
+    Span sp{0, g.T_};
+    if (g.cu) sp = packed_span(g.cu, b, g.T_);
+    const int64_t begin = g.cu ? sp.begin : static_cast<int64_t>(b) * g.T_;
+    const int len = sp.end - sp.begin;
+    Taps<E, W> taps;
+    taps.load(w, bias, g.w_dtype, c0);
+    float dp[W - 1][E];
+#pragma unroll
+    for (int p = 0; p < W - 1; p++) {
+        float s[E], d[E] = {};
+#pragma unroll
+        for (int e = 0; e < E; e++) s[e] = taps.bias[e];
+        if (p < len) {
+#pragma unroll
+            for (int j = 0; j < W; j++) {
+                float r[E];
+                conv_row_e<T, W>(x, s0, begin, p - (W - 1) + j, b, g.C, g.ldx, c0, r);
+#pragma unroll
+                for (int e = 0; e < E; e++) s[e] = __builtin_fmaf(taps.w[j][e], r[e], s[e]);
+            }
+            Pc::widen(Pc::load(dy + (begin + p) * g.ldy + c0), d);
+        }
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            if (ACT == LA_ACT_SILU) {
+                const float sg = sigmoid_fine(s[e]);
+                d[e] *= sg * __builtin_fmaf(s[e], 1.0f - sg, 1.0f);
+            }
+            dp[p][e] = p < len ? d[e] : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; j++) {
+        float out[E] = {};
+        if (dsT && j >= len) Pc::widen(Pc::load(dsT + (static_cast<int64_t>(b) * (W - 1) + j - len) * g.C + c0), out);
+#pragma unroll
+        for (int jj = 0; jj <= j; jj++)
+#pragma unroll
+            for (int e = 0; e < E; e++) out[e] = __builtin_fmaf(taps.w[jj][e], dp[j - jj][e], out[e]);
+        Pc::store(ds0 + (static_cast<int64_t>(b) * (W - 1) + j) * g.C + c0, out);
+    }
+}
+
 // Backward.  dpre[t] = dy[t] act'(pre[t]); dz[u] = sum_j w[j] dpre[u - j] (+ dstate_T's row),
 // dx the part of dz behind the state, dstate0 the part before; dw[j] = sum_t dpre[t] z[t + j].
-// Work split as in the forward, 32 lanes of channels by 8 token blocks a workgroup; each walk
+// Work split as in the forward, 32 lanes of four channels by 8 token blocks a workgroup; each walk
 // goes W - 1 tokens past its block for dpre there.  dw and dbias are summed over the walk in
 // registers, over the workgroup in LDS, and over workgroups by a second kernel: no atomics.
 template <class T, int W, int ACT>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* __restrict__ x, const void* w,
                                                        const void* bias, const T* __restrict__ s0,
                                                        const T* __restrict__ dy, const T* __restrict__ dsT,
-                                                       T* __restrict__ dx, float* __restrict__ part, int64_t token_blocks) {
-    constexpr int E = Io<T>::kVec;
+                                                       T* __restrict__ dx, float* __restrict__ part, int64_t token_blocks,
+                                                       T* ds0, int64_t main_blocks) {
+    constexpr int E = 4;  // (with 8 bf16 a lane 232 registers left two waves a SIMD)
+    using Pc = Piece<T, E>;
     const int nch = g.C / E;
     const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5;
     const int ch = blockIdx.y * 32 + lane;
     const int64_t tb = static_cast<int64_t>(blockIdx.x) * 8 + sub;
     const int c0 = ch * E;
+    if (blockIdx.x >= main_blocks) {  // the initial states' gradients
+        const int64_t b = (blockIdx.x - main_blocks) * 8 + sub;
+        if (b < g.B && ch < nch) conv_bwd_state<T, W, ACT, E>(g, x, w, bias, s0, dy, dsT, ds0, static_cast<int>(b), c0);
+        return;
+    }
     float dw[W][E] = {}, db[E] = {};
     const bool live = ch < nch && tb < token_blocks;
     if (live) {
@@ -145,20 +251,22 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* _
             float dp[W][E] = {};  // dpre of positions p - (W - 1) .. p
 #pragma unroll
             for (int k = 0; k < W - 1; k++)
-                widen(conv_row<T, W>(x, s0, begin, p0 - (W - 1) + k, b, g.C, g.ldx, c0), win[k + 1]);
+                conv_row_e<T, W>(x, s0, begin, p0 - (W - 1) + k, b, g.C, g.ldx, c0, win[k + 1]);
             const int pe = p1 + W - 1;
-            for (int p = p0; p < pe; p += 4) {
-                uv4 rx[4], rd[4];
+            // four tokens; EDGE: some of them behind the block or the sequence
+            auto four = [&](int p, auto edge) {
+                constexpr bool EDGE = decltype(edge)::value;
+                typename Pc::Raw rx[4], rd[4];
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    const int q = p + k < len ? p + k : len - 1;
-                    rx[k] = load16(x + (begin + q) * g.ldx + c0);
-                    rd[k] = load16(dy + (begin + q) * g.ldy + c0);
+                    const int q = !EDGE || p + k < len ? p + k : len - 1;
+                    rx[k] = Pc::load(x + (begin + q) * g.ldx + c0);
+                    rd[k] = Pc::load(dy + (begin + q) * g.ldy + c0);
                 }
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
                     const int q = p + k;
-                    if (q >= pe) break;
+                    if (EDGE && q >= pe) break;
 #pragma unroll
                     for (int j = 0; j < W - 1; j++)
 #pragma unroll
@@ -167,9 +275,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* _
                             dp[j][e] = dp[j + 1][e];
                         }
                     float d[E];
-                    widen(rx[k], win[W - 1]);
-                    widen(rd[k], d);
-                    const bool inside = q < len, mine = q < p1;
+                    Pc::widen(rx[k], win[W - 1]);
+                    Pc::widen(rd[k], d);
+                    const bool inside = !EDGE || q < len, mine = !EDGE || q < p1;
 #pragma unroll
                     for (int e = 0; e < E; e++) {
                         float s = taps.bias[e];
@@ -189,16 +297,20 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* _
                     if (u >= p0) {
                         float out[E] = {};
                         const int tail = u - len + W - 1;  // its row of the final state
-                        if (dsT && tail >= 0) widen(load16(dsT + (static_cast<int64_t>(b) * (W - 1) + tail) * g.C + c0), out);
+                        if (EDGE && dsT && tail >= 0)
+                            Pc::widen(Pc::load(dsT + (static_cast<int64_t>(b) * (W - 1) + tail) * g.C + c0), out);
 #pragma unroll
                         for (int e = 0; e < E; e++)
 #pragma unroll
                             for (int j = 0; j < W; j++)  // dz[u + W - 1 of z] = sum_j w[j] dpre[u + W - 1 - j]
                                 out[e] = __builtin_fmaf(taps.w[j][e], dp[W - 1 - j][e], out[e]);
-                        store16(dx + (begin + u) * g.ldx + c0, narrow(out));
+                        Pc::store(dx + (begin + u) * g.ldx + c0, out);
                     }
                 }
-            }
+            };
+            int p = p0;
+            for (; p + 4 <= p1 && p + 4 <= len; p += 4) four(p, std::false_type{});
+            for (; p < pe; p += 4) four(p, std::true_type{});
         };
         if (!g.cu) {
             const int b = static_cast<int>(tb / g.blocks);
@@ -212,7 +324,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* _
                 const int b = packed_find(g.cu, g.B, t);
                 const Span sp = packed_span(g.cu, b, g.T_);
                 if (t < sp.begin || t >= sp.end) {  // outside every sequence: zero gradient
-                    store16(dx + static_cast<int64_t>(t) * g.ldx + c0, uv4{0, 0, 0, 0});
+                    const float zero[E] = {};
+                    Pc::store(dx + static_cast<int64_t>(t) * g.ldx + c0, zero);
                     t++;
                     continue;
                 }
@@ -241,59 +354,6 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* _
                 part[at] = s;
             }
         }
-    }
-}
-
-// dstate0: row j of z before x gets w[jj] dpre[j - jj] for jj <= j, and where the sequence is
-// shorter than j the final state's own row passes through.
-template <class T, int W, int ACT>
-__global__ __launch_bounds__(256) void conv_bwd_state_kernel(ConvGeom<T> g, const T* x, const void* w, const void* bias,
-                                                             const T* s0, const T* dy, const T* dsT, T* ds0) {
-    constexpr int E = Io<T>::kVec;
-    const int nch = g.C / E;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= static_cast<int64_t>(g.B) * nch) return;
-    const int c0 = static_cast<int>(i % nch) * E, b = static_cast<int>(i / nch);
-    Span sp{0, g.T_};
-    if (g.cu) sp = packed_span(g.cu, b, g.T_);
-    const int64_t begin = g.cu ? sp.begin : static_cast<int64_t>(b) * g.T_;
-    const int len = sp.end - sp.begin;
-    Taps<E, W> taps;
-    taps.load(w, bias, g.w_dtype, c0);
-    float dp[W - 1][E];
-#pragma unroll
-    for (int p = 0; p < W - 1; p++) {
-        float s[E], d[E] = {};
-#pragma unroll
-        for (int e = 0; e < E; e++) s[e] = taps.bias[e];
-        if (p < len) {
-#pragma unroll
-            for (int j = 0; j < W; j++) {
-                float r[E];
-                widen(conv_row<T, W>(x, s0, begin, p - (W - 1) + j, b, g.C, g.ldx, c0), r);
-#pragma unroll
-                for (int e = 0; e < E; e++) s[e] = __builtin_fmaf(taps.w[j][e], r[e], s[e]);
-            }
-            widen(load16(dy + (begin + p) * g.ldy + c0), d);
-        }
-#pragma unroll
-        for (int e = 0; e < E; e++) {
-            if (ACT == LA_ACT_SILU) {
-                const float sg = sigmoid_fine(s[e]);
-                d[e] *= sg * __builtin_fmaf(s[e], 1.0f - sg, 1.0f);
-            }
-            dp[p][e] = p < len ? d[e] : 0.0f;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < W - 1; j++) {
-        float out[E] = {};
-        if (dsT && j >= len) widen(load16(dsT + (static_cast<int64_t>(b) * (W - 1) + j - len) * g.C + c0), out);
-#pragma unroll
-        for (int jj = 0; jj <= j; jj++)
-#pragma unroll
-            for (int e = 0; e < E; e++) out[e] = __builtin_fmaf(taps.w[jj][e], dp[j - jj][e], out[e]);
-        store16(ds0 + (static_cast<int64_t>(b) * (W - 1) + j) * g.C + c0, narrow(out));
     }
 }
 
@@ -336,18 +396,22 @@ __global__ __launch_bounds__(256) void conv_step_kernel(int B, int C, int ldx, i
     for (int j = 0; j < W - 1; j++) store16(st + static_cast<int64_t>(j) * C, rows[j + 1]);
 }
 
-__global__ __launch_bounds__(256) void reduce_parts_kernel(const float* __restrict__ part, int parts, int cols,
-                                                           float* __restrict__ out, int split, float* __restrict__ out2) {
-    __shared__ float red[4][64];
-    const int l = threadIdx.x & 63, q = threadIdx.x >> 6;
-    const int col = blockIdx.x * 64 + l;
+__global__ __launch_bounds__(1024) void reduce_parts_kernel(const float* __restrict__ part, int parts, int cols,
+                                                            float* __restrict__ out, int split, float* __restrict__ out2) {
+    __shared__ float red[32][33];
+    const int l = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const int col = blockIdx.x * 32 + l;
     float s = 0.0f;
-    if (col < cols)
-        for (int p = q; p < parts; p += 4) s += part[static_cast<size_t>(p) * cols + col];
+    if (col < cols) {
+#pragma unroll 4
+        for (int p = q; p < parts; p += 32) s += part[static_cast<size_t>(p) * cols + col];
+    }
     red[q][l] = s;
     __syncthreads();
     if (q == 0 && col < cols) {
-        s = (red[0][l] + red[1][l]) + (red[2][l] + red[3][l]);
+        s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 32; k++) s += red[k][l];
         if (col < split) out[col] = s;
         else if (out2) out2[col - split] = s;
     }
@@ -357,8 +421,7 @@ __global__ __launch_bounds__(256) void reduce_parts_kernel(const float* __restri
 // fewer for short inputs.
 int conv_bwd_per(const la_conv_config& c) {
     const int64_t tokens = static_cast<int64_t>(c.B) * c.T;  // an upper bound for a packing
-    const int nch = c.C / (c.x_dtype == LA_BF16 ? 8 : 4);
-    const int64_t lanes = (nch + 31) / 32;
+    const int64_t lanes = (c.C / 4 + 31) / 32;
     int per = 32;
     while (per > 4 && lanes * (tokens / (8 * per)) < 512) per >>= 1;
     return per;
@@ -424,23 +487,17 @@ hipError_t launch_conv_bwd(const la_conv_config& c, const ConvArgs& a, hipStream
     return dispatch(c, [&](auto t, auto w, auto act) {
         using T = decltype(t);
         constexpr int W = decltype(w)::value, ACT = decltype(act)::value;
-        const int nch = c.C / Io<T>::kVec;
         const int per = conv_bwd_per(c);
         const ConvBlocks nb = conv_blocks(c, a.cu != nullptr, per);
         const ConvGeom<T> g = geom<T>(c, a.cu, per, nb.per_seq);
-        const int64_t gy = (nb.blocks + 7) / 8;
-        if (gy > 0)
-            conv_bwd_kernel<T, W, ACT><<<dim3(static_cast<unsigned>(gy), (nch + 31) / 32), 256, 0, s>>>(
+        const int64_t gy = (nb.blocks + 7) / 8, extra = a.ds0 ? (c.B + 7) / 8 : 0;
+        if (gy + extra > 0)
+            conv_bwd_kernel<T, W, ACT><<<dim3(static_cast<unsigned>(gy + extra), (c.C / 4 + 31) / 32), 256, 0, s>>>(
                 g, static_cast<const T*>(a.x), a.w, a.bias, static_cast<const T*>(a.s0), static_cast<const T*>(a.dy),
-                static_cast<const T*>(a.dsT), static_cast<T*>(a.dx), a.part, nb.blocks);
-        hipError_t e = hipGetLastError();
+                static_cast<const T*>(a.dsT), static_cast<T*>(a.dx), a.part, nb.blocks, static_cast<T*>(a.ds0), gy);
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        e = launch_reduce_parts(a.part, static_cast<int>(gy), c.C * (W + 1), a.dw, c.C * W, a.dbias, s);
-        if (e != hipSuccess || !a.ds0 || c.B == 0) return e;
-        conv_bwd_state_kernel<T, W, ACT><<<dim3(static_cast<unsigned>((static_cast<int64_t>(c.B) * nch + 255) / 256)), 256, 0, s>>>(
-            g, static_cast<const T*>(a.x), a.w, a.bias, static_cast<const T*>(a.s0), static_cast<const T*>(a.dy),
-            static_cast<const T*>(a.dsT), static_cast<T*>(a.ds0));
-        return hipGetLastError();
+        return launch_reduce_parts(a.part, static_cast<int>(gy), c.C * (W + 1), a.dw, c.C * W, a.dbias, s);
     });
 }
 
@@ -459,7 +516,7 @@ hipError_t launch_conv_step(const la_conv_config& c, const ConvArgs& a, hipStrea
 hipError_t launch_reduce_parts(const float* part, int parts, int cols, float* out, int split, float* out2,
                                hipStream_t s) {
     if (cols == 0) return hipSuccess;
-    reduce_parts_kernel<<<dim3((cols + 63) / 64), 256, 0, s>>>(part, parts, cols, out, split, out2);
+    reduce_parts_kernel<<<dim3((cols + 31) / 32), 1024, 0, s>>>(part, parts, cols, out, split, out2);
     return hipGetLastError();
 }
 

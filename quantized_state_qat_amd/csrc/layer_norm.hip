@@ -228,7 +228,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwd p) {
     float dw[CH][8] = {};
     for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPW + sub; row < p.rows; row += static_cast<int64_t>(gridDim.x) * RPW) {
         const size_t base = static_cast<size_t>(row) * p.d;
-        float h[CH][8], dy[CH][8];
+        float h[CH][8], dy[CH][8], up[CH][8] = {};
         float ss = 0.0f, gh = 0.0f;
 #pragma unroll
         for (int c = 0; c < CH; c++) {
@@ -238,6 +238,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwd p) {
                 load8(static_cast<const T*>(p.h) + base + col, h[c]);
                 load8(static_cast<const O*>(p.dy) + base + col, dy[c]);
                 load_w(p.w, p.w_dtype, col, w);
+                if (p.dres) load8(static_cast<const T*>(p.dres) + base + col, up[c]);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; e++) h[c][e] = dy[c][e] = w[e] = 0.0f;
@@ -255,16 +256,15 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwd p) {
         for (int c = 0; c < CH; c++) {
             const int col = (c * LANES + l) * kPiece;
             if (col >= p.d) continue;
-            float w[8], out[8] = {};
+            float w[8];
             load_w(p.w, p.w_dtype, col, w);
-            if (p.dres) load8(static_cast<const T*>(p.dres) + base + col, out);
 #pragma unroll
             for (int e = 0; e < 8; e++) {
                 const float hr = h[c][e] * r;
                 dw[c][e] = __builtin_fmaf(dy[c][e], hr, dw[c][e]);
-                out[e] = __builtin_fmaf(r, __builtin_fmaf(dy[c][e], w[e], -h[c][e] * k), out[e]);
+                up[c][e] = __builtin_fmaf(r, __builtin_fmaf(dy[c][e], w[e], -h[c][e] * k), up[c][e]);
             }
-            store8(static_cast<T*>(p.dx) + base + col, out);
+            store8(static_cast<T*>(p.dx) + base + col, up[c]);
         }
     }
     if (!p.part) return;
@@ -313,12 +313,12 @@ int norm_lanes(int d) {
     const int pieces = d / kPiece;
     return pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : pieces <= 256 ? 64 : 256;
 }
-// Workgroups of the backward: up to four a CU, so that the partial sums stay a small part of
+// Workgroups of the backward: up to two a CU, so that the partial sums stay a small part of
 // the traffic.
 int norm_bwd_groups(const la_norm_config& c) {
     const int rpw = 256 / norm_lanes(c.d);
     const int need = (c.rows + rpw - 1) / rpw;
-    return need < 1024 ? need : 1024;
+    return need < 512 ? need : 512;
 }
 
 }  // namespace
