@@ -65,90 +65,112 @@ def declare(lib) -> None:
         f.restype, f.argtypes = sz, [ctypes.POINTER(cfg)]
 
 
-class _Call:
-    """Checks the tensors of one call and makes it on their GPU."""
+_torch = None   # set by the first call: the package imports torch with the library
+_types = ()     # torch dtypes by la_dtype
+_current = None  # GPU index -> its current stream's handle
 
-    def __init__(self, stream):
+
+def _library():
+    global _torch, _types, _current
+    lib = _la.load_library()
+    if _torch is None:
         import torch
-        self.torch, self.stream, self.device = torch, stream, None
-        self.types = {_F32: torch.float32, _BF16: torch.bfloat16}
+        _torch, _types = torch, (torch.float32, torch.bfloat16)
+        # (a stream object costs a microsecond a call, a fifth of a short one)
+        _current = getattr(torch._C, "_cuda_getCurrentRawStream", lambda gpu: torch.cuda.current_stream(gpu).cuda_stream)
+    return lib
 
-    def _same_gpu(self, t, name):
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a GPU tensor (got device {t.device})")
-        at = t.device.index
-        if self.device is None:
-            self.device = at
-        elif at != self.device:
-            raise ValueError(f"{name} is on GPU {at}, an earlier argument on GPU {self.device}")
 
-    def tight(self, t, name, numel, *dtypes):
-        """Address of a contiguous tensor of at least `numel` elements."""
-        if t is None or isinstance(t, int):
-            return t
-        self._same_gpu(t, name)
-        if t.dtype not in dtypes:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-        if t.numel() < numel:
-            raise ValueError(f"{name} holds {t.numel()} elements, the configuration needs {numel}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _dtype(code):
+    return _types[code] if code in (_F32, _BF16) else _types[_F32]  # (an unknown code is refused by the library)
+
+
+def _gpu(*tensors):
+    """The GPU of the first tensor among the arguments; None when it is on the host or all are
+    raw addresses."""
+    for t in tensors:
+        if t is not None and t.__class__ is not int:
+            return t.get_device() if t.is_cuda else None
+    return None
+
+
+def _elsewhere(t, name, gpu):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (got device {t.device})")
+    raise ValueError(f"{name} is on GPU {t.get_device()}, the first tensor on {'the host' if gpu is None else f'GPU {gpu}'}")
+
+
+def _tight(gpu, t, name, numel, dtype):
+    """Address of a contiguous tensor of at least `numel` elements."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.get_device() != gpu:
+        _elsewhere(t, name, gpu)
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.numel() < numel:
+        raise ValueError(f"{name} holds {t.numel()} elements, the configuration needs {numel}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(gpu, t, name, tokens, width, ld, dtype):
+    """Address of `tokens` rows of `width` contiguous elements, `ld` (0: width) elements apart."""
+    if t is None or t.__class__ is int:
+        return t
+    if t.get_device() != gpu:
+        _elsewhere(t, name, gpu)
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.numel() < tokens * width:
+        raise ValueError(f"{name} holds {t.numel()} elements, the configuration needs {tokens * width}")
+    if (ld == 0 or ld == width) and t.is_contiguous():
         return t.data_ptr()
-
-    def rows(self, t, name, tokens, width, ld, dtype):
-        """Address of `tokens` rows of `width` contiguous elements, `ld` (0: width) elements apart."""
-        if t is None or isinstance(t, int):
-            return t
-        self._same_gpu(t, name)
-        if t.dtype != dtype:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-        ld = ld or width
-        if t.numel() < tokens * width:
-            raise ValueError(f"{name} holds {t.numel()} elements, the configuration needs {tokens * width}")
-        if ld == width and t.is_contiguous():
-            return t.data_ptr()
-        inner, want = 1, 1  # elements of the row walked so far, the stride the next dimension must have
-        for n, step in zip(reversed(t.shape), reversed(t.stride())):
-            if n != 1 and step != want:
-                raise ValueError(f"{name} has strides {t.stride()}: rows of {width} contiguous elements, {ld} apart, "
-                                 "are needed")
-            if inner < width:
-                inner *= n
-                want = ld if inner == width else inner
-                if inner > width:
-                    raise ValueError(f"{name} has shape {tuple(t.shape)}: its last dimensions must make up a row of {width}")
-            else:
-                want *= n
+    ld = ld or width
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 3 and strides == (ld, shape[2], 1) and shape[1] * shape[2] == width:  # tokens of heads or groups
         return t.data_ptr()
-
-    def __call__(self, fn, *args):
-        torch = self.torch
-        if self.device is None or self.device == torch.cuda.current_device():
-            status = fn(*args, self._stream())
+    inner = want = 1  # elements of the row walked so far, the stride the next dimension must have
+    for n, step in zip(shape[::-1], strides[::-1]):
+        if step != want and n != 1:
+            raise ValueError(f"{name} has strides {strides}: rows of {width} contiguous elements, {ld} apart, are needed")
+        if inner < width:
+            inner *= n
+            if inner > width:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}: its last dimensions must make up a row of {width}")
+            want = ld if inner == width else inner
         else:
-            with torch.cuda.device(self.device):
-                status = fn(*args, self._stream())
-        if status:
-            _la._check(status)
-
-    def _stream(self):
-        s = self.stream
-        if s is None:
-            return self.torch.cuda.current_stream(self.device).cuda_stream
-        if isinstance(s, int):
-            return s
-        if self.device is not None and s.device.index != self.device:
-            raise ValueError(f"stream is on GPU {s.device.index}, the tensors on GPU {self.device}")
-        return s.cuda_stream
+            want *= n
+    return t.data_ptr()
 
 
-def _workspace(call, workspace, ws_bytes):
-    if workspace is None or isinstance(workspace, int):
+def _workspace(gpu, workspace, ws_bytes):
+    if workspace is None or workspace.__class__ is int:
         return workspace
-    call._same_gpu(workspace, "workspace")
-    if workspace.numel() * workspace.element_size() < int(ws_bytes):
+    if workspace.get_device() != gpu:
+        _elsewhere(workspace, "workspace", gpu)
+    if workspace.numel() * workspace.element_size() < ws_bytes:
         raise ValueError(f"workspace holds fewer than the {int(ws_bytes)} bytes passed as ws_bytes")
     return _la._ptr(workspace)
+
+
+def _call(gpu, stream, fn, *args):
+    """The call on its tensors' GPU and that GPU's current stream, or `stream`."""
+    cuda = _torch.cuda
+    if stream is None:
+        stream = _current(cuda.current_device() if gpu is None else gpu)
+    elif stream.__class__ is not int:
+        if gpu is not None and stream.device.index != gpu:
+            raise ValueError(f"stream is on GPU {stream.device.index}, the tensors on GPU {gpu}")
+        stream = stream.cuda_stream
+    if gpu is None or gpu == cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with cuda.device(gpu):
+            status = fn(*args, stream)
+    if status:
+        _la._check(status)
 
 
 def _tokens(cfg, cu_seqlens):
@@ -158,12 +180,15 @@ def _tokens(cfg, cu_seqlens):
 # ------------------------------------------------------------------ short causal convolution
 def la_conv_fwd(cfg: ConvConfig, x, weight, bias, state0, y, state_T=None, cu_seqlens=None, stream=None) -> None:
     """y = act(causal depthwise convolution of state0 ++ x); state_T = its last rows."""
-    lib, k = _la.load_library(), _Call(stream)
-    xt, wt, n = k.types.get(cfg.x_dtype, k.torch.float32), k.types.get(cfg.w_dtype, k.torch.float32), _tokens(cfg, cu_seqlens)
+    lib = _library()
+    gpu = _gpu(x, weight, y)
+    xt, wt, n = _dtype(cfg.x_dtype), _dtype(cfg.w_dtype), _tokens(cfg, cu_seqlens)
     st = cfg.B * (cfg.width - 1) * cfg.C
-    k(lib.la_conv_fwd, cfg, k.tight(cu_seqlens, "cu_seqlens", cfg.B + 1, k.torch.int32), k.rows(x, "x", n, cfg.C, cfg.ld_x, xt),
-      k.tight(weight, "weight", cfg.C * cfg.width, wt), k.tight(bias, "bias", cfg.C, wt), k.tight(state0, "state0", st, xt),
-      k.rows(y, "y", n, cfg.C, cfg.ld_y, xt), k.tight(state_T, "state_T", st, xt))
+    _call(gpu, stream, lib.la_conv_fwd, cfg,
+          _tight(gpu, cu_seqlens, "cu_seqlens", cfg.B + 1, _torch.int32), _rows(gpu, x, "x", n, cfg.C, cfg.ld_x, xt),
+          _tight(gpu, weight, "weight", cfg.C * cfg.width, wt), _tight(gpu, bias, "bias", cfg.C, wt),
+          _tight(gpu, state0, "state0", st, xt),
+          _rows(gpu, y, "y", n, cfg.C, cfg.ld_y, xt), _tight(gpu, state_T, "state_T", st, xt))
 
 
 def la_conv_bwd_workspace_bytes(cfg: ConvConfig) -> int:
@@ -173,34 +198,39 @@ def la_conv_bwd_workspace_bytes(cfg: ConvConfig) -> int:
 def la_conv_bwd(cfg: ConvConfig, x, weight, bias, state0, dy, dstate_T, dx, dweight, dbias, dstate0, workspace,
                 ws_bytes: int, cu_seqlens=None, stream=None) -> None:
     """Gradients of la_conv_fwd (dweight and dbias float32)."""
-    lib, k = _la.load_library(), _Call(stream)
-    xt, wt, n = k.types.get(cfg.x_dtype, k.torch.float32), k.types.get(cfg.w_dtype, k.torch.float32), _tokens(cfg, cu_seqlens)
-    st, f32 = cfg.B * (cfg.width - 1) * cfg.C, k.torch.float32
-    k(lib.la_conv_bwd, cfg, k.tight(cu_seqlens, "cu_seqlens", cfg.B + 1, k.torch.int32), k.rows(x, "x", n, cfg.C, cfg.ld_x, xt),
-      k.tight(weight, "weight", cfg.C * cfg.width, wt), k.tight(bias, "bias", cfg.C, wt), k.tight(state0, "state0", st, xt),
-      k.rows(dy, "dy", n, cfg.C, cfg.ld_y, xt), k.tight(dstate_T, "dstate_T", st, xt),
-      k.rows(dx, "dx", n, cfg.C, cfg.ld_x, xt), k.tight(dweight, "dweight", cfg.C * cfg.width, f32),
-      k.tight(dbias, "dbias", cfg.C, f32), k.tight(dstate0, "dstate0", st, xt), _workspace(k, workspace, ws_bytes),
-      int(ws_bytes))
+    lib = _library()
+    gpu = _gpu(x, weight, dy, dx)
+    xt, wt, n = _dtype(cfg.x_dtype), _dtype(cfg.w_dtype), _tokens(cfg, cu_seqlens)
+    st, f32 = cfg.B * (cfg.width - 1) * cfg.C, _torch.float32
+    _call(gpu, stream, lib.la_conv_bwd, cfg,
+          _tight(gpu, cu_seqlens, "cu_seqlens", cfg.B + 1, _torch.int32), _rows(gpu, x, "x", n, cfg.C, cfg.ld_x, xt),
+          _tight(gpu, weight, "weight", cfg.C * cfg.width, wt), _tight(gpu, bias, "bias", cfg.C, wt),
+          _tight(gpu, state0, "state0", st, xt),
+          _rows(gpu, dy, "dy", n, cfg.C, cfg.ld_y, xt), _tight(gpu, dstate_T, "dstate_T", st, xt),
+          _rows(gpu, dx, "dx", n, cfg.C, cfg.ld_x, xt), _tight(gpu, dweight, "dweight", cfg.C * cfg.width, f32),
+          _tight(gpu, dbias, "dbias", cfg.C, f32), _tight(gpu, dstate0, "dstate0", st, xt), _workspace(gpu, workspace, ws_bytes),
+          int(ws_bytes))
 
 
 def la_conv_step(cfg: ConvConfig, x, weight, bias, state, y, slots=None, n_slots: int = 0, stream=None) -> None:
     """One token; the state (or its slot of the pool) is shifted in place."""
-    lib, k = _la.load_library(), _Call(stream)
-    xt, wt = k.types.get(cfg.x_dtype, k.torch.float32), k.types.get(cfg.w_dtype, k.torch.float32)
+    lib = _library()
+    gpu = _gpu(x, weight, state, y)
+    xt, wt = _dtype(cfg.x_dtype), _dtype(cfg.w_dtype)
     units = max(int(n_slots), 0) if slots is not None else cfg.B
-    k(lib.la_conv_step, cfg, k.rows(x, "x", cfg.B, cfg.C, cfg.ld_x, xt), k.tight(weight, "weight", cfg.C * cfg.width, wt),
-      k.tight(bias, "bias", cfg.C, wt), k.tight(state, "state", units * (cfg.width - 1) * cfg.C, xt),
-      k.tight(slots, "slots", cfg.B, k.torch.int32), int(n_slots), k.rows(y, "y", cfg.B, cfg.C, cfg.ld_y, xt))
+    _call(gpu, stream, lib.la_conv_step, cfg,
+          _rows(gpu, x, "x", cfg.B, cfg.C, cfg.ld_x, xt), _tight(gpu, weight, "weight", cfg.C * cfg.width, wt),
+          _tight(gpu, bias, "bias", cfg.C, wt), _tight(gpu, state, "state", units * (cfg.width - 1) * cfg.C, xt),
+          _tight(gpu, slots, "slots", cfg.B, _torch.int32), int(n_slots), _rows(gpu, y, "y", cfg.B, cfg.C, cfg.ld_y, xt))
 
 
 # ----------------------------------------------------------------------------- selective scan
-def _scan_inputs(k, cfg, n, x, dt, A, b, c, D, dt_bias):
-    xt, f32 = k.types.get(cfg.x_dtype, k.torch.float32), k.torch.float32
-    return (k.rows(x, "x", n, cfg.H * cfg.d_v, cfg.ld_x, xt), k.rows(dt, "dt", n, cfg.H, cfg.ld_dt, k.types.get(cfg.dt_dtype, k.torch.float32)),
-            k.tight(A, "A", cfg.H, f32), k.rows(b, "b", n, cfg.G * cfg.d_k, cfg.ld_b, xt),
-            k.rows(c, "c", n, cfg.G * cfg.d_k, cfg.ld_c, xt), k.tight(D, "D", cfg.H, f32),
-            k.tight(dt_bias, "dt_bias", cfg.H, f32))
+def _scan_inputs(gpu, cfg, n, x, dt, A, b, c, D, dt_bias):
+    xt, f32 = _dtype(cfg.x_dtype), _torch.float32
+    return (_rows(gpu, x, "x", n, cfg.H * cfg.d_v, cfg.ld_x, xt), _rows(gpu, dt, "dt", n, cfg.H, cfg.ld_dt, _dtype(cfg.dt_dtype)),
+            _tight(gpu, A, "A", cfg.H, f32), _rows(gpu, b, "b", n, cfg.G * cfg.d_k, cfg.ld_b, xt),
+            _rows(gpu, c, "c", n, cfg.G * cfg.d_k, cfg.ld_c, xt), _tight(gpu, D, "D", cfg.H, f32),
+            _tight(gpu, dt_bias, "dt_bias", cfg.H, f32))
 
 
 def la_scan_workspace_bytes(cfg: ScanConfig) -> int:
@@ -210,12 +240,14 @@ def la_scan_workspace_bytes(cfg: ScanConfig) -> int:
 def la_scan_fwd(cfg: ScanConfig, x, dt, A, b, c, D, dt_bias, S0, y, S_T, workspace, ws_bytes: int, cu_seqlens=None,
                 stream=None) -> None:
     """S <- exp(Delta A) S + Delta b x^T, y = S^T c + D x over every sequence."""
-    lib, k = _la.load_library(), _Call(stream)
-    n, st, f32 = _tokens(cfg, cu_seqlens), cfg.B * cfg.H * cfg.d_k * cfg.d_v, k.torch.float32
-    k(lib.la_scan_fwd, cfg, k.tight(cu_seqlens, "cu_seqlens", cfg.B + 1, k.torch.int32),
-      *_scan_inputs(k, cfg, n, x, dt, A, b, c, D, dt_bias), k.tight(S0, "S0", st, f32),
-      k.tight(y, "y", n * cfg.H * cfg.d_v, k.types.get(cfg.out_dtype, k.torch.float32)), k.tight(S_T, "S_T", st, f32),
-      _workspace(k, workspace, ws_bytes), int(ws_bytes))
+    lib = _library()
+    gpu = _gpu(x, dt, A, b, c, y)
+    n, st, f32 = _tokens(cfg, cu_seqlens), cfg.B * cfg.H * cfg.d_k * cfg.d_v, _torch.float32
+    _call(gpu, stream, lib.la_scan_fwd, cfg,
+          _tight(gpu, cu_seqlens, "cu_seqlens", cfg.B + 1, _torch.int32),
+          *_scan_inputs(gpu, cfg, n, x, dt, A, b, c, D, dt_bias), _tight(gpu, S0, "S0", st, f32),
+          _tight(gpu, y, "y", n * cfg.H * cfg.d_v, _dtype(cfg.out_dtype)), _tight(gpu, S_T, "S_T", st, f32),
+          _workspace(gpu, workspace, ws_bytes), int(ws_bytes))
 
 
 def la_scan_bwd_workspace_bytes(cfg: ScanConfig) -> int:
@@ -225,38 +257,45 @@ def la_scan_bwd_workspace_bytes(cfg: ScanConfig) -> int:
 def la_scan_bwd(cfg: ScanConfig, x, dt, A, b, c, D, dt_bias, S0, dy, dS_T, dx, ddt, dA, db, dc, dD, ddt_bias, dS0,
                 workspace, ws_bytes: int, cu_seqlens=None, stream=None) -> None:
     """Gradients of la_scan_fwd."""
-    lib, k = _la.load_library(), _Call(stream)
-    n, st, f32 = _tokens(cfg, cu_seqlens), cfg.B * cfg.H * cfg.d_k * cfg.d_v, k.torch.float32
-    xt = k.types.get(cfg.x_dtype, k.torch.float32)
-    k(lib.la_scan_bwd, cfg, k.tight(cu_seqlens, "cu_seqlens", cfg.B + 1, k.torch.int32),
-      *_scan_inputs(k, cfg, n, x, dt, A, b, c, D, dt_bias), k.tight(S0, "S0", st, f32),
-      k.tight(dy, "dy", n * cfg.H * cfg.d_v, k.types.get(cfg.out_dtype, k.torch.float32)), k.tight(dS_T, "dS_T", st, f32),
-      k.rows(dx, "dx", n, cfg.H * cfg.d_v, cfg.ld_x, xt), k.rows(ddt, "ddt", n, cfg.H, cfg.ld_dt, k.types.get(cfg.dt_dtype, k.torch.float32)),
-      k.tight(dA, "dA", cfg.H, f32), k.rows(db, "db", n, cfg.G * cfg.d_k, cfg.ld_b, xt),
-      k.rows(dc, "dc", n, cfg.G * cfg.d_k, cfg.ld_c, xt), k.tight(dD, "dD", cfg.H, f32),
-      k.tight(ddt_bias, "ddt_bias", cfg.H, f32), k.tight(dS0, "dS0", st, f32), _workspace(k, workspace, ws_bytes),
-      int(ws_bytes))
+    lib = _library()
+    gpu = _gpu(x, dt, A, b, c, dy, dx)
+    n, st, f32 = _tokens(cfg, cu_seqlens), cfg.B * cfg.H * cfg.d_k * cfg.d_v, _torch.float32
+    xt = _dtype(cfg.x_dtype)
+    _call(gpu, stream, lib.la_scan_bwd, cfg,
+          _tight(gpu, cu_seqlens, "cu_seqlens", cfg.B + 1, _torch.int32),
+          *_scan_inputs(gpu, cfg, n, x, dt, A, b, c, D, dt_bias), _tight(gpu, S0, "S0", st, f32),
+          _tight(gpu, dy, "dy", n * cfg.H * cfg.d_v, _dtype(cfg.out_dtype)), _tight(gpu, dS_T, "dS_T", st, f32),
+          _rows(gpu, dx, "dx", n, cfg.H * cfg.d_v, cfg.ld_x, xt), _rows(gpu, ddt, "ddt", n, cfg.H, cfg.ld_dt, _dtype(cfg.dt_dtype)),
+          _tight(gpu, dA, "dA", cfg.H, f32), _rows(gpu, db, "db", n, cfg.G * cfg.d_k, cfg.ld_b, xt),
+          _rows(gpu, dc, "dc", n, cfg.G * cfg.d_k, cfg.ld_c, xt), _tight(gpu, dD, "dD", cfg.H, f32),
+          _tight(gpu, ddt_bias, "ddt_bias", cfg.H, f32), _tight(gpu, dS0, "dS0", st, f32), _workspace(gpu, workspace, ws_bytes),
+          int(ws_bytes))
 
 
 def la_scan_step(cfg: ScanConfig, x, dt, A, b, c, D, dt_bias, S, y, slots=None, n_slots: int = 0, stream=None) -> None:
     """One token; the state (or its slot of the pool) is advanced in place."""
-    lib, k = _la.load_library(), _Call(stream)
+    lib = _library()
+    gpu = _gpu(x, dt, A, b, c, S, y)
     units = max(int(n_slots), 0) if slots is not None else cfg.B
-    k(lib.la_scan_step, cfg, *_scan_inputs(k, cfg, cfg.B, x, dt, A, b, c, D, dt_bias),
-      k.tight(S, "S", units * cfg.H * cfg.d_k * cfg.d_v, k.torch.float32), k.tight(slots, "slots", cfg.B, k.torch.int32),
-      int(n_slots), k.tight(y, "y", cfg.B * cfg.H * cfg.d_v, k.types.get(cfg.out_dtype, k.torch.float32)))
+    _call(gpu, stream, lib.la_scan_step, cfg,
+          *_scan_inputs(gpu, cfg, cfg.B, x, dt, A, b, c, D, dt_bias),
+          _tight(gpu, S, "S", units * cfg.H * cfg.d_k * cfg.d_v, _torch.float32), _tight(gpu, slots, "slots", cfg.B, _torch.int32),
+          int(n_slots), _tight(gpu, y, "y", cfg.B * cfg.H * cfg.d_v, _dtype(cfg.out_dtype)))
 
 
 # -------------------------------------------------- RMS norm with the residual's addition
 def la_norm_fwd(cfg: NormConfig, x, residual, weight, res_out, y, codes=None, scales=None, stream=None) -> None:
     """res_out = x + residual, y = its RMS norm, and with a quantizer its codes and scales."""
-    lib, k = _la.load_library(), _Call(stream)
-    t, n, xt = k.torch, cfg.rows * cfg.d, k.types.get(cfg.x_dtype, k.torch.float32)
-    eight = (t.int8, t.uint8, t.float8_e4m3fn)
-    k(lib.la_norm_fwd, cfg, k.tight(x, "x", n, xt), k.tight(residual, "residual", n, xt),
-      k.tight(weight, "weight", cfg.d, k.types.get(cfg.w_dtype, k.torch.float32)), k.tight(res_out, "res_out", n, xt),
-      k.tight(y, "y", n, k.types.get(cfg.out_dtype, k.torch.float32)), k.tight(codes, "codes", n, *eight),
-      k.tight(scales, "scales", n // (cfg.group or cfg.d) if cfg.d > 0 else 0, t.float32))
+    lib = _library()
+    gpu = _gpu(x, residual, weight, res_out, y)
+    n, xt, eight = cfg.rows * cfg.d, _dtype(cfg.x_dtype), _torch.uint8
+    if codes is not None and codes.__class__ is not int and codes.dtype in (_torch.int8, _torch.float8_e4m3fn):
+        eight = codes.dtype
+    _call(gpu, stream, lib.la_norm_fwd, cfg,
+          _tight(gpu, x, "x", n, xt), _tight(gpu, residual, "residual", n, xt),
+          _tight(gpu, weight, "weight", cfg.d, _dtype(cfg.w_dtype)), _tight(gpu, res_out, "res_out", n, xt),
+          _tight(gpu, y, "y", n, _dtype(cfg.out_dtype)), _tight(gpu, codes, "codes", n, eight),
+          _tight(gpu, scales, "scales", n // (cfg.group or cfg.d) if cfg.d > 0 else 0, _torch.float32))
 
 
 def la_norm_bwd_workspace_bytes(cfg: NormConfig) -> int:
@@ -265,8 +304,10 @@ def la_norm_bwd_workspace_bytes(cfg: NormConfig) -> int:
 
 def la_norm_bwd(cfg: NormConfig, h, weight, dy, dres, dx, dweight, workspace, ws_bytes: int, stream=None) -> None:
     """Gradients of la_norm_fwd from its res_out (straight through the codec)."""
-    lib, k = _la.load_library(), _Call(stream)
-    n, xt = cfg.rows * cfg.d, k.types.get(cfg.x_dtype, k.torch.float32)
-    k(lib.la_norm_bwd, cfg, k.tight(h, "h", n, xt), k.tight(weight, "weight", cfg.d, k.types.get(cfg.w_dtype, k.torch.float32)),
-      k.tight(dy, "dy", n, k.types.get(cfg.out_dtype, k.torch.float32)), k.tight(dres, "dres", n, xt), k.tight(dx, "dx", n, xt),
-      k.tight(dweight, "dweight", cfg.d, k.torch.float32), _workspace(k, workspace, ws_bytes), int(ws_bytes))
+    lib = _library()
+    gpu = _gpu(h, weight, dy, dres, dx)
+    n, xt = cfg.rows * cfg.d, _dtype(cfg.x_dtype)
+    _call(gpu, stream, lib.la_norm_bwd, cfg,
+          _tight(gpu, h, "h", n, xt), _tight(gpu, weight, "weight", cfg.d, _dtype(cfg.w_dtype)),
+          _tight(gpu, dy, "dy", n, _dtype(cfg.out_dtype)), _tight(gpu, dres, "dres", n, xt), _tight(gpu, dx, "dx", n, xt),
+          _tight(gpu, dweight, "dweight", cfg.d, _torch.float32), _workspace(gpu, workspace, ws_bytes), int(ws_bytes))
