@@ -163,6 +163,18 @@ __device__ __forceinline__ int opaque(int x) {
     return x;
 }
 
+// Four values summed over the four rows of 16 lanes, lane row g left with value g's sum: three
+// exchanges for what four whole sums take eight for.
+__device__ __forceinline__ float rows_scatter4(const float (&v)[4]) {
+    auto half = [](float a, float b) {  // lanes 0..31: a's sum over lane and lane + 32, lanes 32..63: b's
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    };
+    const float x = half(v[0], v[2]), y = half(v[1], v[3]);
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
 // 2^(hi + lo) for |lo| far below an ulp of hi.
 __device__ __forceinline__ float exp2_two(float hi, float lo) {
     const float r = __builtin_amdgcn_exp2f(hi);

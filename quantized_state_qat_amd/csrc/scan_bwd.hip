@@ -228,7 +228,9 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                                                         void* db_, void* dc_, float* dbp, float* dcp, const Decay* decays,
                                                         RateSums* sums, int slices, int64_t rows) {
     using MT = Mat<T>;
-    constexpr int P2 = MT::template parts<2>;
+    // S and dS as operands: three bf16 parts (exact) where the decays' gradients come from them,
+    // two of dS for dX
+    constexpr int P2 = MT::template parts<2>, P3 = MT::template parts<3>;
     constexpr int RB = lds_row<T>(N), RX = lds_row64<T>(), RM = lds_row64<T>();
     constexpr int KS = N / 32, NTL = N / 16, PARTS = 8 / NTL, TI = 4 / PARTS;
     extern __shared__ __align__(16) char raw_lds[];
@@ -378,7 +380,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         tx.store(lds.x, RX);
         ty.store(lds.dy, RX);
         td.store(lds.d);
-        typename MT::Frag Sf[2][P2], dSf[2][P2];
+        typename MT::Frag Sf[2][P3], dSf[2][P3];
         float sd = 0.0f;
         {
         const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
@@ -386,8 +388,8 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         for (int k = 0; k < 2; k++) {
 #pragma unroll
             for (int j = 0; j < 8; j++) sd = __builtin_fmaf(Sr[k][j], dSr[k][j], sd);
-            MT::template split<P2>(Sr[k], Sf[k]);
-            MT::template split<P2>(dSr[k], dSf[k]);
+            MT::template split<P3>(Sr[k], Sf[k]);
+            MT::template split<P3>(dSr[k], dSf[k]);
             if constexpr (sizeof(T) == 2) {
                 if (part == 0) {
 #pragma unroll
@@ -496,6 +498,9 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
 #pragma unroll
                 for (int j = 0; j < 2; j++) mf[ks][j] = MT::col8(lds.m, RM, 32 * ks, 32 * half + 16 * j, ln);
             }
+            // (rows behind the sequence lie behind the buffer's end)
+            const __amdgpu_buffer_rsrc_t rdx =
+                make_rsrc(static_cast<T*>(dx_) + row0 * p.ld_x + static_cast<int64_t>(h) * p.dv + tile * kPT, live * p.ld_x * sizeof(T));
             float w[2];
 #pragma unroll
             for (int j = 0; j < 2; j++) w[j] = d.w[32 * half + 16 * j + lm];
@@ -514,61 +519,73 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                 MT::get4(lds.dy + s * RX + pc + 4 * g, yv);
 #pragma unroll
                 for (int r = 0; r < 4; r++) acc[j][r] = __builtin_fmaf(Dh, yv[r], acc[j][r]);
-                if (s < live) {
-                    T* o = static_cast<T*>(dx_) + (row0 + s) * p.ld_x + static_cast<int64_t>(h) * p.dv + tile * kPT + pc + 4 * g;
-                    const float v[4] = {acc[j][0], acc[j][1], acc[j][2], acc[j][3]};
-                    MT::template put4<1>(o, 0, v);
-                }
+                const int off = (s * static_cast<int>(p.ld_x) + pc + 4 * g) * static_cast<int>(sizeof(T));
+                if constexpr (sizeof(T) == 2)
+                    __builtin_amdgcn_raw_buffer_store_b64(uv2{pack16(acc[j][0], acc[j][1]), pack16(acc[j][2], acc[j][3])}, rdx, off, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uv4, acc[j]), rdx, off, 0, 0);
             }
         }
         // ---- dC^T, dB^T: rows n of this wave, columns t, s
         fetch_rows(next);
-#pragma unroll
-        for (int ii = 0; ii < TI; ii++) {
+        {
             const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
-            const int i = part * TI + ii, t = 16 * i + lm;
-            __builtin_amdgcn_sched_barrier(0);
-            typename MT::Frag yf[2], xf[2], gr[2], gc[2];
+            float ri[TI], ci[TI];
 #pragma unroll
-            for (int ks = 0; ks < 2; ks++) {
-                yf[ks] = MT::row8(lds.dy + t * RX + 32 * ks + 8 * g);
-                xf[ks] = MT::row8(lds.x + t * RX + 32 * ks + 8 * g);
-                gr[ks] = MT::row8(&lds.dg[t * RM + 32 * ks + 8 * g]);
-                gc[ks] = MT::col8(lds.dg, RM, 32 * ks, 16 * i, ln);
-            }
-            float cv[4], bv[4], ri = 0.0f, ci = 0.0f;
-            MT::get4(lds.c + t * RB + n0 + 4 * g, cv);
-            MT::get4(lds.b + t * RB + n0 + 4 * g, bv);
-            const float head_t = d.head[t], tail_t = d.tail[t], delta_t = d.delta[t];
-            __builtin_amdgcn_sched_barrier(0);
-            f4 a = {}, b = {};
+            for (int ii = 0; ii < TI; ii++) {
+                const int i = part * TI + ii, t = 16 * i + lm;
+                __builtin_amdgcn_sched_barrier(0);
+                typename MT::Frag yf[2], xf[2], gr[2], gc[2];
 #pragma unroll
-            for (int ks = 0; ks < 2; ks++)
-#pragma unroll
-                for (int k = 0; k < P2; k++) {
-                    a = MT::mma(Sf[ks][k], yf[ks], a);
-                    b = MT::mma(dSf[ks][k], xf[ks], b);
+                for (int ks = 0; ks < 2; ks++) {
+                    yf[ks] = MT::row8(lds.dy + t * RX + 32 * ks + 8 * g);
+                    xf[ks] = MT::row8(lds.x + t * RX + 32 * ks + 8 * g);
+                    gr[ks] = MT::row8(&lds.dg[t * RM + 32 * ks + 8 * g]);
+                    gc[ks] = MT::col8(lds.dg, RM, 32 * ks, 16 * i, ln);
                 }
+                float cv[4], bv[4];
+                MT::get4(lds.c + t * RB + n0 + 4 * g, cv);
+                MT::get4(lds.b + t * RB + n0 + 4 * g, bv);
+                const float head_t = d.head[t], tail_t = d.tail[t], w_t = d.w[t];
+                __builtin_amdgcn_sched_barrier(0);
+                f4 a = {}, b = {};
 #pragma unroll
-            for (int ks = 0; ks < 2; ks++) {
-                if (ks <= i / 2) dC[ii] = MT::mma(bT[ks], gr[ks], dC[ii]);
-                if (ks >= i / 2) dB[ii] = MT::mma(cT[ks], gc[ks], dB[ii]);
-            }
-            a *= head_t;
-            b *= tail_t;
+                for (int ks = 0; ks < 2; ks++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                ri = __builtin_fmaf(a[r], cv[r], ri);
-                ci = __builtin_fmaf(b[r], bv[r], ci);
+                    for (int k = 0; k < P3; k++) {
+                        a = MT::mma(Sf[ks][k], yf[ks], a);
+                        b = MT::mma(dSf[ks][k], xf[ks], b);
+                    }
+#pragma unroll
+                for (int ks = 0; ks < 2; ks++) {
+                    if (ks <= i / 2) dC[ii] = MT::mma(bT[ks], gr[ks], dC[ii]);
+                    if (ks >= i / 2) dB[ii] = MT::mma(cT[ks], gc[ks], dB[ii]);
+                }
+                ri[ii] = ci[ii] = 0.0f;
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    ri[ii] = __builtin_fmaf(a[r], cv[r], ri[ii]);
+                    ci[ii] = __builtin_fmaf(b[r], bv[r], ci[ii]);
+                    dC[ii][r] = __builtin_fmaf(a[r], head_t, dC[ii][r]);
+                    dB[ii][r] = __builtin_fmaf(b[r], w_t, dB[ii][r]);
+                }
+                ri[ii] *= head_t;
+                ci[ii] *= tail_t;
             }
-            ri = rows_sum(ri);
-            ci = rows_sum(ci);
-            if (g == 0) {
-                lds.ri[par][nt][t] = ri;
-                lds.ci[par][nt][t] = ci;
+            if constexpr (TI == 4) {  // lane group g is left with the sums of tile g
+                const float r = rows_scatter4(ri), c = rows_scatter4(ci);
+                lds.ri[par][nt][16 * g + lm] = r;
+                lds.ci[par][nt][16 * g + lm] = c;
+            } else {
+#pragma unroll
+                for (int ii = 0; ii < TI; ii++) {
+                    const float r = rows_sum(ri[ii]), c = rows_sum(ci[ii]);
+                    if (g == 0) {
+                        lds.ri[par][nt][16 * (part * TI + ii) + lm] = r;
+                        lds.ci[par][nt][16 * (part * TI + ii) + lm] = c;
+                    }
+                }
             }
-            dC[ii] += a;
-            dB[ii] += b * delta_t;
         }
         if (sizeof(T) == 4) {
             fetch_state(next, Sin, Sr);
