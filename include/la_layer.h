@@ -46,7 +46,7 @@ typedef enum { LA_ACT_NONE = 0, LA_ACT_SILU = 1 } la_act;
  * Sums are FP32.
  */
 typedef struct la_conv_config {
-    int32_t B, T, C;  /* C a multiple of 8 */
+    int32_t B, T, C;  /* B up to 65535; T up to 2^30; C a multiple of 8 up to 2^20 */
     int32_t width;    /* 2, 3 or 4 */
     int32_t act;      /* la_act */
     int32_t x_dtype;  /* la_dtype of x, y, the states and their gradients */
@@ -87,15 +87,17 @@ la_status la_conv_step(const la_conv_config* cfg, const void* x, const void* wei
  *     y_t     = S_t^T c_t + D_h x_t
  * The recurrence of la.h with the scalar gate g = Delta A, k = b, q = c and delta = Delta x.
  * Rates Delta A above zero grow the state; cumulated over 64 tokens they must stay below 88.
+ * An infinity or NaN in x reaches the outputs of its whole block of 64 tokens of the sequence
+ * (earlier ones too), as one in dt, b or c those from its own token on, and every later one.
  */
 typedef struct la_scan_config {
-    int32_t B, T, H, G;    /* G divides H */
-    int32_t d_k, d_v;      /* d_k 16, 32, 64 or 128; d_v a multiple of 64 up to 4096 */
+    int32_t B, T, H, G;    /* B and H up to 65535; T up to 2^30; G divides H */
+    int32_t d_k, d_v;      /* d_k 16, 32, 64 or 128; d_v a multiple of 64 up to 4096; H d_v up to 2^23 */
     int32_t softplus;      /* 0 | 1 */
     int32_t x_dtype;       /* la_dtype of x, b, c and their gradients */
     int32_t dt_dtype;      /* la_dtype of dt and ddt */
     int32_t out_dtype;     /* la_dtype of y and dy */
-    int32_t ld_x;          /* row strides of x and dx (0 = H d_v), */
+    int32_t ld_x;          /* row strides, up to 2^23, of x and dx (0 = H d_v), */
     int32_t ld_b, ld_c;    /* b and db, c and dc (0 = G d_k), */
     int32_t ld_dt;         /* dt and ddt (0 = H; any value >= H) */
 } la_scan_config;
@@ -103,7 +105,8 @@ typedef struct la_scan_config {
 /* x [B][T][H][d_v], dt [B][T][H], b and c [B][T][G][d_k], y [B][T][H][d_v] (tight); A, D,
  * dt_bias float [H] (D and dt_bias may be NULL: zeros); S0, S_T float [B][H][d_k][d_v], each
  * may be NULL (zeros; not written).  S_T must not overlap S0 nor y the inputs.  Workspace: at
- * least la_scan_workspace_bytes(cfg) bytes (0 for many shapes: then NULL will do). */
+ * least la_scan_workspace_bytes(cfg) bytes (0 for many shapes: then NULL will do).
+ * B H d_v / 64 must be below 2^23. */
 la_status la_scan_fwd(const la_scan_config* cfg, const int32_t* cu_seqlens, const void* x, const void* dt,
                       const float* A, const void* b, const void* c, const float* D, const float* dt_bias,
                       const float* S0, void* y, float* S_T, void* workspace, size_t ws_bytes, void* stream);
@@ -111,14 +114,17 @@ size_t la_scan_workspace_bytes(const la_scan_config* cfg);
 
 /* Gradients for the upstream gradients dy and dS_T (NULL = zero): dx, ddt, db, dc laid out and
  * typed as their inputs; dA, dD, ddt_bias float [H] (dD and ddt_bias may be NULL); dS0 (may be
- * NULL).  db and dc are summed over the group's heads.  out_dtype must equal x_dtype.  Workspace: at
- * least la_scan_bwd_workspace_bytes(cfg) bytes. */
+ * NULL).  db and dc are summed over the group's heads.  out_dtype must equal x_dtype.  A call
+ * takes below 2^23 heads of 64-token chunks.  Workspace (the state and its gradient at every
+ * 64th token, and more): at least la_scan_bwd_workspace_bytes(cfg) bytes; for packed sequences
+ * la_scan_bwd_varlen_workspace_bytes(cfg), up to B times less, is enough. */
 la_status la_scan_bwd(const la_scan_config* cfg, const int32_t* cu_seqlens, const void* x, const void* dt,
                       const float* A, const void* b, const void* c, const float* D, const float* dt_bias,
                       const float* S0, const void* dy, const float* dS_T, void* dx, void* ddt, float* dA, void* db,
                       void* dc, float* dD, float* ddt_bias, float* dS0, void* workspace, size_t ws_bytes,
                       void* stream);
 size_t la_scan_bwd_workspace_bytes(const la_scan_config* cfg);
+size_t la_scan_bwd_varlen_workspace_bytes(const la_scan_config* cfg);
 
 /* One token (cfg->T must be 1): the state is updated in place.  slots and n_slots as in
  * la_conv_step, over a pool float [n_slots][H][d_k][d_v]. */

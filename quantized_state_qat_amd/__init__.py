@@ -462,5 +462,6 @@ def la_last_error() -> str:
 from . import layers  # noqa: E402  (the binding of the layer operators uses the helpers above)
 from .layers import (LA_ACT_NONE, LA_ACT_SILU, ConvConfig, NormConfig, ScanConfig, la_conv_bwd,  # noqa: E402,F401
                      la_conv_bwd_workspace_bytes, la_conv_fwd, la_conv_step, la_norm_bwd, la_norm_bwd_workspace_bytes,
-                     la_norm_fwd, la_scan_bwd, la_scan_bwd_workspace_bytes, la_scan_fwd, la_scan_step,
+                     la_norm_fwd, la_scan_bwd, la_scan_bwd_varlen_workspace_bytes, la_scan_bwd_workspace_bytes,
+                     la_scan_fwd, la_scan_step,
                      la_scan_workspace_bytes)

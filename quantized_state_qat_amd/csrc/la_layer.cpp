@@ -61,17 +61,16 @@ la_status check_slots(const int32_t* slots, int32_t n_slots) {
     return check_ptr(slots, "slots", false);
 }
 
-// Workgroups of one launch stay below 2^31; every kernel here uses at most one workgroup for
-// 256 accesses of 16 bytes.
-constexpr int64_t kMaxItems = static_cast<int64_t>(1) << 38;
+constexpr int32_t kMaxT = 1 << 30;
 
 // ------------------------------------------------------------------------------ convolution
-la_status check_conv(const la_conv_config* c, bool step) {
+la_status check_conv(const la_conv_config* c, bool step, bool packed) {
     if (!c) return fail(LA_ERR_INVALID_ARG, "cfg is NULL");
     if (c->B < 0 || c->T < 0 || c->C <= 0)
         return fail(LA_ERR_INVALID_ARG, "negative or zero size (B=%d T=%d C=%d)", c->B, c->T, c->C);
     if (step && c->T != 1) return fail(LA_ERR_INVALID_ARG, "one token needs T == 1 (T=%d)", c->T);
     if (c->C % 8 != 0) return fail(LA_ERR_UNSUPPORTED, "C must be a multiple of 8 (C=%d)", c->C);
+    if (c->T > kMaxT) return fail(LA_ERR_UNSUPPORTED, "T must be at most 2^30 (T=%d)", c->T);
     if (c->C > (1 << 20)) return fail(LA_ERR_UNSUPPORTED, "C must be at most 2^20 (C=%d)", c->C);
     if (c->width < 2 || c->width > 4) return fail(LA_ERR_UNSUPPORTED, "width must be 2, 3 or 4 (width=%d)", c->width);
     if (c->act != LA_ACT_NONE && c->act != LA_ACT_SILU) return fail(LA_ERR_INVALID_ARG, "unknown act %d", c->act);
@@ -79,8 +78,11 @@ la_status check_conv(const la_conv_config* c, bool step) {
     CHECK(check_dtype(c->w_dtype, "w_dtype"));
     CHECK(check_ld(c->ld_x, c->C, c->x_dtype, "ld_x"));
     CHECK(check_ld(c->ld_y, c->C, c->x_dtype, "ld_y"));
-    if (static_cast<int64_t>(c->B) * (c->T + 4LL) * (c->C / 4) > kMaxItems)
+    // grids stay below 2^32 threads
+    const int64_t tokens = packed ? c->T : static_cast<int64_t>(c->B) * c->T;
+    if (tokens * c->C > (int64_t{1} << 36) || static_cast<int64_t>(c->B) * c->C > (int64_t{1} << 32))
         return fail(LA_ERR_UNSUPPORTED, "too many elements (B=%d T=%d C=%d)", c->B, c->T, c->C);
+    if (c->B > 65535) return fail(LA_ERR_UNSUPPORTED, "B must be <= 65535 (B=%d)", c->B);
     return LA_OK;
 }
 
@@ -107,11 +109,21 @@ la_status check_scan(const la_scan_config* c, bool step) {
     CHECK(check_ld(c->ld_c, static_cast<int64_t>(c->G) * c->d_k, c->x_dtype, "ld_c"));
     if (c->ld_dt != 0 && c->ld_dt < c->H)
         return fail(LA_ERR_INVALID_ARG, "ld_dt = %d is shorter than the row (%d)", c->ld_dt, c->H);
-    // one workgroup a sequence, head and 32 or 64 columns, or a 64-token chunk of that
-    const int64_t tiles = static_cast<int64_t>(c->B) * c->H * (c->d_v / 32);
-    const int64_t chunks = (static_cast<int64_t>(c->T) + 63) / 64 + 1;
-    if (tiles > INT32_MAX || tiles * chunks > (static_cast<int64_t>(1) << 40))
-        return fail(LA_ERR_UNSUPPORTED, "too many heads and tokens (B=%d T=%d H=%d)", c->B, c->T, c->H);
+    // byte offsets within 64 rows stay below 2^31
+    const int64_t row = static_cast<int64_t>(c->H) * c->d_v;
+    if (row > (1 << 23) || c->ld_x > (1 << 23) || c->ld_b > (1 << 23) || c->ld_c > (1 << 23) || c->ld_dt > (1 << 23))
+        return fail(LA_ERR_UNSUPPORTED, "rows and row strides must be at most 2^23 elements (H=%d d_v=%d)", c->H, c->d_v);
+    if (c->T > kMaxT) return fail(LA_ERR_UNSUPPORTED, "T must be at most 2^30 (T=%d)", c->T);
+    // a workgroup a sequence, head and 64 columns
+    if (c->B * (row / 64) >= la::kMaxUnits)
+        return fail(LA_ERR_UNSUPPORTED, "too many heads: B H d_v / 64 must be below 2^23 (B=%d H=%d d_v=%d)", c->B, c->H, c->d_v);
+    return LA_OK;
+}
+// The backward: a workgroup a chunk and group, a wave a chunk and head.
+la_status check_scan_bwd(const la_scan_config* c, bool packed) {
+    CHECK(check_scan(c, false));
+    if (la::scan_bwd_slots(*c, packed) * c->H >= la::kMaxUnits)
+        return fail(LA_ERR_UNSUPPORTED, "too many tokens: the backward takes below 2^23 heads of 64-token chunks (B=%d T=%d H=%d)", c->B, c->T, c->H);
     return LA_OK;
 }
 
@@ -152,7 +164,7 @@ extern "C" {
 
 la_status la_conv_fwd(const la_conv_config* cfg, const int32_t* cu_seqlens, const void* x, const void* weight,
                       const void* bias, const void* state0, void* y, void* state_T, void* stream) {
-    CHECK(check_conv(cfg, false));
+    CHECK(check_conv(cfg, false, cu_seqlens != nullptr));
     const la_conv_config& c = *cfg;
     const bool work = c.B > 0 && c.T > 0;
     CHECK(check_ptr(cu_seqlens, "cu_seqlens", false));
@@ -170,14 +182,14 @@ la_status la_conv_fwd(const la_conv_config* cfg, const int32_t* cu_seqlens, cons
 }
 
 size_t la_conv_bwd_workspace_bytes(const la_conv_config* cfg) {
-    if (check_conv(cfg, false) != LA_OK) return 0;
+    if (check_conv(cfg, false, true) != LA_OK) return 0;
     return la::conv_bwd_workspace(*cfg);
 }
 
 la_status la_conv_bwd(const la_conv_config* cfg, const int32_t* cu_seqlens, const void* x, const void* weight,
                       const void* bias, const void* state0, const void* dy, const void* dstate_T, void* dx,
                       float* dweight, float* dbias, void* dstate0, void* workspace, size_t ws_bytes, void* stream) {
-    CHECK(check_conv(cfg, false));
+    CHECK(check_conv(cfg, false, cu_seqlens != nullptr));
     const la_conv_config& c = *cfg;
     const bool work = c.B > 0 && c.T > 0;
     CHECK(check_ptr(cu_seqlens, "cu_seqlens", false));
@@ -200,7 +212,7 @@ la_status la_conv_bwd(const la_conv_config* cfg, const int32_t* cu_seqlens, cons
 
 la_status la_conv_step(const la_conv_config* cfg, const void* x, const void* weight, const void* bias, void* state,
                        const int32_t* slots, int32_t n_slots, void* y, void* stream) {
-    CHECK(check_conv(cfg, true));
+    CHECK(check_conv(cfg, true, false));
     const la_conv_config& c = *cfg;
     const bool work = c.B > 0;
     CHECK(check_slots(slots, n_slots));
@@ -240,9 +252,15 @@ la_status la_scan_fwd(const la_scan_config* cfg, const int32_t* cu_seqlens, cons
     return done(la::launch_scan_fwd(*cfg, a, static_cast<hipStream_t>(stream)), "la_scan_fwd launch");
 }
 
-size_t la_scan_bwd_workspace_bytes(const la_scan_config* cfg) {
-    if (check_scan(cfg, false) != LA_OK) return 0;
-    return la::scan_bwd_workspace(*cfg);
+size_t la_scan_bwd_workspace_bytes(const la_scan_config* cfg) {  // enough for either layout
+    if (check_scan_bwd(cfg, true) != LA_OK || check_scan_bwd(cfg, false) != LA_OK) return 0;
+    const size_t dense = la::scan_bwd_workspace(*cfg, false), packed = la::scan_bwd_workspace(*cfg, true);
+    return dense > packed ? dense : packed;
+}
+
+size_t la_scan_bwd_varlen_workspace_bytes(const la_scan_config* cfg) {
+    if (check_scan_bwd(cfg, true) != LA_OK) return 0;
+    return la::scan_bwd_workspace(*cfg, true);
 }
 
 la_status la_scan_bwd(const la_scan_config* cfg, const int32_t* cu_seqlens, const void* x, const void* dt,
@@ -250,7 +268,7 @@ la_status la_scan_bwd(const la_scan_config* cfg, const int32_t* cu_seqlens, cons
                       const float* S0, const void* dy, const float* dS_T, void* dx, void* ddt, float* dA, void* db,
                       void* dc, float* dD, float* ddt_bias, float* dS0, void* workspace, size_t ws_bytes,
                       void* stream) {
-    CHECK(check_scan(cfg, false));
+    CHECK(check_scan_bwd(cfg, cu_seqlens != nullptr));
     if (cfg->out_dtype != cfg->x_dtype)
         return fail(LA_ERR_UNSUPPORTED, "the backward takes dy in the inputs' dtype (out_dtype must equal x_dtype)");
     const bool units = cfg->B > 0 && cfg->H > 0;
@@ -269,7 +287,8 @@ la_status la_scan_bwd(const la_scan_config* cfg, const int32_t* cu_seqlens, cons
     CHECK(check_ptr(ddt_bias, "ddt_bias", false));
     CHECK(check_ptr(dS0, "dS0", false));
     if (dS0 && dS0 == dS_T) return fail(LA_ERR_INVALID_ARG, "dS0 must not be dS_T");
-    CHECK(check_workspace(workspace, ws_bytes, la::scan_bwd_workspace(*cfg)));
+    CHECK(check_workspace(workspace, ws_bytes, cu_seqlens ? la_scan_bwd_varlen_workspace_bytes(cfg)
+                                                          : la_scan_bwd_workspace_bytes(cfg)));
     if (cfg->H == 0) return ok();
     la::ScanArgs a;
     a.cu = cu_seqlens, a.x = x, a.dt = dt, a.A = A, a.b = b, a.c = c, a.D = D, a.bias = dt_bias, a.S0 = S0, a.dy = dy;

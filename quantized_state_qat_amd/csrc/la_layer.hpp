@@ -89,7 +89,10 @@ hipError_t launch_scan_fwd(const la_scan_config& c, const ScanArgs& a, hipStream
 hipError_t launch_scan_bwd(const la_scan_config& c, const ScanArgs& a, hipStream_t s);
 hipError_t launch_scan_step(const la_scan_config& c, const ScanArgs& a, hipStream_t s);
 size_t scan_fwd_workspace(const la_scan_config& c);
-size_t scan_bwd_workspace(const la_scan_config& c);
+size_t scan_bwd_workspace(const la_scan_config& c, bool packed);
+int64_t scan_bwd_slots(const la_scan_config& c, bool packed);  // chunks of 64 tokens in its workspace
+// Workgroups of a launch of 512 threads, and half of those of one of 256: a grid has below 2^32 threads.
+constexpr int64_t kMaxUnits = static_cast<int64_t>(1) << 23;
 
 // out[i] = sum over p < parts of part[p cols + i], p in order within each of four interleaved
 // partial sums (a fixed order: the result does not depend on scheduling).  Columns from

@@ -222,7 +222,7 @@ __device__ __forceinline__ float softplus_fine(float z) {
     p = __builtin_fmaf(p, x, 1.0f / 5.0f);
     p = __builtin_fmaf(p, x, 1.0f / 3.0f);
     const float two_s = s + s;
-    return fmaxf(z, 0.0f) + __builtin_fmaf(two_s * x, p, two_s);
+    return (z < 0.0f ? 0.0f : z) + __builtin_fmaf(two_s * x, p, two_s);  // (NaN stays NaN)
 }
 
 // One chunk's decays for a head.  Exponents are in units of log2; the cumulative sums are formed

@@ -221,7 +221,7 @@ __device__ __forceinline__ void conv_bwd_state(const ConvGeom<T>& g, const T* x,
 // Backward.  dpre[t] = dy[t] act'(pre[t]); dz[u] = sum_j w[j] dpre[u - j] (+ dstate_T's row),
 // dx the part of dz behind the state, dstate0 the part before; dw[j] = sum_t dpre[t] z[t + j].
 // Work split as in the forward, 32 lanes of four channels by 8 token blocks a workgroup; each walk
-// goes W - 1 tokens past its block for dpre there.  dw and dbias are summed over the walk in
+// goes W - 1 tokens past its block for dpre there.  dw and dbias are summed over a lane's walks in
 // registers, over the workgroup in LDS, and over workgroups by a second kernel: no atomics.
 template <class T, int W, int ACT>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* __restrict__ x, const void* w,
@@ -234,7 +234,6 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* _
     const int nch = g.C / E;
     const int lane = threadIdx.x & 31, sub = threadIdx.x >> 5;
     const int ch = blockIdx.y * 32 + lane;
-    const int64_t tb = static_cast<int64_t>(blockIdx.x) * 8 + sub;
     const int c0 = ch * E;
     if (blockIdx.x >= main_blocks) {  // the initial states' gradients
         const int64_t b = (blockIdx.x - main_blocks) * 8 + sub;
@@ -242,8 +241,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* _
         return;
     }
     float dw[W][E] = {}, db[E] = {};
-    const bool live = ch < nch && tb < token_blocks;
-    if (live) {
+    if (ch < nch) {
         Taps<E, W> taps;
         taps.load(w, bias, g.w_dtype, c0);
         auto walk = [&](int64_t begin, int len, int b, int p0, int p1) {
@@ -312,12 +310,14 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* _
             for (; p + 4 <= p1 && p + 4 <= len; p += 4) four(p, std::false_type{});
             for (; p < pe; p += 4) four(p, std::true_type{});
         };
-        if (!g.cu) {
-            const int b = static_cast<int>(tb / g.blocks);
-            const int p0 = static_cast<int>(tb % g.blocks) * g.per;
-            const int p1 = g.T_ - p0 < g.per ? g.T_ : p0 + g.per;
-            walk(static_cast<int64_t>(b) * g.T_, g.T_, b, p0, p1);
-        } else {
+        for (int64_t tb = static_cast<int64_t>(blockIdx.x) * 8 + sub; tb < token_blocks; tb += main_blocks * 8) {
+            if (!g.cu) {
+                const int b = static_cast<int>(tb / g.blocks);
+                const int p0 = static_cast<int>(tb % g.blocks) * g.per;
+                const int p1 = g.T_ - p0 < g.per ? g.T_ : p0 + g.per;
+                walk(static_cast<int64_t>(b) * g.T_, g.T_, b, p0, p1);
+                continue;
+            }
             int t = static_cast<int>(tb) * g.per;
             const int t1 = g.T_ - t < g.per ? g.T_ : t + g.per;
             while (t < t1) {
@@ -478,9 +478,16 @@ hipError_t launch_conv_fwd(const la_conv_config& c, const ConvArgs& a, hipStream
     });
 }
 
-size_t conv_bwd_workspace(const la_conv_config& c) {
-    const int64_t blocks = static_cast<int64_t>((c.T + conv_bwd_per(c) - 1) / conv_bwd_per(c)) * c.B;
-    return static_cast<size_t>((blocks + 7) / 8) * c.C * (c.width + 1) * sizeof(float);
+// Workgroups along the tokens, each with its partial sums: one for eight token blocks, and no more
+// than 8192 over all channels (32 a CU), beyond which each takes several.
+int64_t conv_bwd_parts(const la_conv_config& c, int64_t blocks) {
+    const int64_t lanes = (c.C / 4 + 31) / 32, cap = 8192 / lanes > 1 ? 8192 / lanes : 1;
+    return (blocks + 7) / 8 < cap ? (blocks + 7) / 8 : cap;
+}
+
+size_t conv_bwd_workspace(const la_conv_config& c) {  // (a packing has fewer blocks)
+    const int64_t parts = conv_bwd_parts(c, conv_blocks(c, false, conv_bwd_per(c)).blocks);
+    return static_cast<size_t>(parts) * c.C * (c.width + 1) * sizeof(float);
 }
 
 hipError_t launch_conv_bwd(const la_conv_config& c, const ConvArgs& a, hipStream_t s) {
@@ -490,7 +497,8 @@ hipError_t launch_conv_bwd(const la_conv_config& c, const ConvArgs& a, hipStream
         const int per = conv_bwd_per(c);
         const ConvBlocks nb = conv_blocks(c, a.cu != nullptr, per);
         const ConvGeom<T> g = geom<T>(c, a.cu, per, nb.per_seq);
-        const int64_t gy = (nb.blocks + 7) / 8, extra = a.ds0 ? (c.B + 7) / 8 : 0;
+        // (no sequences, or no tokens: no parts, and the sums below are zero)
+        const int64_t gy = c.B > 0 ? conv_bwd_parts(c, nb.blocks) : 0, extra = a.ds0 ? (c.B + 7) / 8 : 0;
         if (gy + extra > 0)
             conv_bwd_kernel<T, W, ACT><<<dim3(static_cast<unsigned>(gy + extra), (c.C / 4 + 31) / 32), 256, 0, s>>>(
                 g, static_cast<const T*>(a.x), a.w, a.bias, static_cast<const T*>(a.s0), static_cast<const T*>(a.dy),

@@ -22,27 +22,59 @@ __device__ __forceinline__ int64_t slot_of(const ScanP& p, int b, int64_t begin,
     if (!p.cu) return static_cast<int64_t>(b) * ((p.T + kQ - 1) / kQ) + ch;
     return b + begin / kQ + ch;
 }
-int64_t slot_count(const la_scan_config& c) {  // enough for either layout
-    const int64_t dense = static_cast<int64_t>(c.B) * ((c.T + kQ - 1) / kQ);
-    const int64_t packed = static_cast<int64_t>(c.B) + c.T / kQ + 1;
-    return dense > packed ? dense : packed;
+int64_t slot_count(const la_scan_config& c, bool packed) {
+    return packed ? static_cast<int64_t>(c.B) + c.T / kQ + 1 : static_cast<int64_t>(c.B) * ((c.T + kQ - 1) / kQ);
+}
+// The chunk of a slot; a packing leaves some slots without one.
+struct ChunkAt {
+    int b, ch;
+    SeqRange sr;
+    bool used;
+};
+__device__ __forceinline__ ChunkAt chunk_at(const ScanP& p, uint32_t slot) {
+    ChunkAt c;
+    if (!p.cu) {
+        uint32_t u = slot;
+        c.ch = take(u, (p.T + kQ - 1) / kQ);
+        c.b = static_cast<int>(u);
+    } else {  // the last b with b + begin_b / 64 <= slot, eight boundaries a step
+        int lo = 0, n = p.B;
+        while (n > 1) {
+            const int step = (n + 7) / 8;
+            uint32_t at[7];
+            int k = 0;
+#pragma unroll
+            for (int i = 0; i < 7; i++) {
+                const int b = lo + (step * (i + 1) < n ? step * (i + 1) : 0);
+                at[i] = static_cast<uint32_t>(b + packed_span(p.cu, b, p.T).begin / kQ);
+            }
+#pragma unroll
+            for (int i = 0; i < 7; i++) k = step * (i + 1) < n && at[i] <= slot ? i + 1 : k;
+            lo += k * step;
+            n = n - k * step < step ? n - k * step : step;
+        }
+        c.b = lo;
+        c.ch = static_cast<int>(slot) - lo - packed_span(p.cu, lo, p.T).begin / kQ;
+    }
+    c.sr = c.b < p.B ? seq_range(p, c.b) : SeqRange{0, 0};
+    c.used = c.ch >= 0 && c.ch < (c.sr.len + kQ - 1) / kQ;
+    return c;
 }
 
 // Every chunk's decays, a wave each; read by the walks, the gradients and the rates' gradients.
-__global__ __launch_bounds__(256) void decays_kernel(ScanP p, Decay* out, int nmax) {
+__global__ __launch_bounds__(256) void decays_kernel(ScanP p, Decay* out, uint32_t slots) {
     __shared__ __align__(16) Decay d[4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + wave;  // (b, chunk, h), h fastest
-    const int h = static_cast<int>(unit % p.H), ch = static_cast<int>(unit / p.H % nmax);
-    const int64_t b = unit / p.H / nmax;
-    if (b >= p.B) return;
-    const SeqRange sr = seq_range(p, static_cast<int>(b));
-    const int live = sr.len - ch * kQ;
-    if (live <= 0) return;
+    uint32_t slot = blockIdx.x * 4u + wave;
+    const int h = take(slot, p.H);
+    if (slot >= slots) return;
+    const ChunkAt at = chunk_at(p, slot);
+    if (!at.used) return;
+    const int live = at.sr.len - at.ch * kQ;
     DtAhead dt;
-    dt.fetch(p, sr.begin + static_cast<int64_t>(ch) * kQ, h, lane, live);
+    dt.fetch(p, at.sr.begin + static_cast<int64_t>(at.ch) * kQ, h, lane, live);
     make_decay(d[wave], dt.value(p) + (p.bias ? p.bias[h] : 0.0f), p.softplus, live, p.A[h]);
-    uv4* o = reinterpret_cast<uv4*>(out + slot_of(p, static_cast<int>(b), sr.begin, ch) * p.H + h);
+    uv4* o = reinterpret_cast<uv4*>(out + static_cast<int64_t>(slot) * p.H + h);
 #pragma unroll
     for (int q = 0; q < 2; q++) o[lane + 64 * q] = reinterpret_cast<const uv4*>(&d[wave])[lane + 64 * q];
 }
@@ -71,7 +103,7 @@ __global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* dy, co
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lm = lane & 15, g = lane >> 4;
 
-    const int tiles = p.dv / kPT, nmax = (p.T + kQ - 1) / kQ;
+    const int tiles = p.dv / kPT;
     uint32_t u = die_unit(blockIdx.x, gridDim.x);
     const bool rev = take(u, 2) != 0;
     const int tile = take(u, tiles), h = take(u, p.H);
@@ -79,11 +111,16 @@ __global__ __launch_bounds__(256) void scan_walk_kernel(ScanP p, const T* dy, co
     float* states = rev ? dSst : Sst;
     float* last = rev ? dS0 : nullptr;
     const int64_t ld_x = rev ? static_cast<int64_t>(p.H) * p.dv : p.ld_x;
-    const int only = ONE ? take(u, nmax) : 0;
-    const int bi = static_cast<int>(u);
-    const SeqRange sr = seq_range(p, bi);
+    int bi = static_cast<int>(u), only = 0;  // (ONE: u is a slot)
+    SeqRange sr;
+    if constexpr (ONE) {
+        const ChunkAt at = chunk_at(p, u);
+        if (!at.used) return;
+        bi = at.b, only = at.ch, sr = at.sr;
+    } else {
+        sr = seq_range(p, bi);
+    }
     const int nch = (sr.len + kQ - 1) / kQ;
-    if (ONE && only >= nch) return;
     const int steps = ONE ? 1 : nch;
     const int grp = h / (p.H / p.G);
     const int col = tile * kPT + 16 * wave + 4 * g;  // this lane's four columns
@@ -242,26 +279,12 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
 
     uint32_t u = die_unit(blockIdx.x, gridDim.x);
     const int slice = take(u, slices), grp = take(u, p.G);
-    const int64_t slot = u;
-    int bi, ch;
-    if (!p.cu) {
-        ch = take(u, (p.T + kQ - 1) / kQ);
-        bi = static_cast<int>(u);
-        if (bi >= p.B) return;
-    } else {  // the last b with b + begin_b / 64 <= slot
-        int lo = 0, hi = p.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (mid + packed_span(p.cu, mid, p.T).begin / kQ <= slot) lo = mid;
-            else hi = mid - 1;
-        }
-        bi = lo;
-        ch = static_cast<int>(slot - bi - packed_span(p.cu, bi, p.T).begin / kQ);
-    }
-    const SeqRange sr = seq_range(p, bi);
-    if (ch < 0 || ch * static_cast<int64_t>(kQ) >= sr.len) return;
-    const int64_t row0 = sr.begin + static_cast<int64_t>(ch) * kQ;
-    const int live = sr.len - ch * kQ < kQ ? sr.len - ch * kQ : kQ;
+    const uint32_t slot = u;
+    const ChunkAt at = chunk_at(p, slot);
+    if (!at.used) return;
+    const SeqRange sr = at.sr;
+    const int64_t row0 = sr.begin + static_cast<int64_t>(at.ch) * kQ;
+    const int live = sr.len - at.ch * kQ < kQ ? sr.len - at.ch * kQ : kQ;
 
     const int hpg = __builtin_amdgcn_readfirstlane(p.H / p.G), per = __builtin_amdgcn_readfirstlane((hpg + slices - 1) / slices);
     const int h0 = grp * hpg + slice * per;
@@ -278,7 +301,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         const int tile = take(q, tiles), h = h0 + static_cast<int>(q);
         tx.load(static_cast<const T*>(p.x) + row0 * p.ld_x + static_cast<int64_t>(h) * p.dv + tile * kPT, p.ld_x, live, kPT);
         ty.load(dyr + (row0 * p.H + h) * p.dv + tile * kPT, static_cast<int64_t>(p.H) * p.dv, live, kPT);
-        td.load(decays + slot * p.H + h);
+        td.load(decays + static_cast<int64_t>(slot) * p.H + h);
     };
     const int soff = n0 + lm < p.dk ? ((n0 + lm) * p.dv + 8 * g) * 4 : -1024;
     auto fetch_state = [&](int it, const float* from, float (&to)[2][8]) {
@@ -638,34 +661,48 @@ __global__ __launch_bounds__(256) void join_slices_kernel(ScanP p, const float* 
     Mat<T>::template put4<1>(dc + row * p.ld_c + e, 0, fc);
 }
 
-// Zero gradients for a packing's tokens outside every sequence.
+// Zero gradients for a packing's tokens outside every sequence, 256 tokens a workgroup.
 template <class T>
 __global__ __launch_bounds__(256) void clear_outside_kernel(ScanP p, T* dx, void* ddt, T* db, T* dc) {
-    const int t = blockIdx.x;
-    const int b = packed_find(p.cu, p.B, t);
-    const Span s = packed_span(p.cu, b, p.T);
-    if (t >= s.begin && t < s.end) return;
-    for (int i = threadIdx.x; i < p.H * p.dv; i += 256) dx[t * p.ld_x + i] = T{};
-    for (int i = threadIdx.x; i < p.G * p.dk; i += 256) {
-        db[t * p.ld_b + i] = T{};
-        dc[t * p.ld_c + i] = T{};
+    __shared__ bool outside[256];
+    const int t0 = static_cast<int>(blockIdx.x) * 256, tid = threadIdx.x;
+    const int n = p.T - t0 < 256 ? p.T - t0 : 256;
+    bool out = false;
+    if (tid < n) {
+        const Span s = packed_span(p.cu, packed_find(p.cu, p.B, t0 + tid), p.T);
+        out = t0 + tid < s.begin || t0 + tid >= s.end;
     }
-    for (int i = threadIdx.x; i < p.H; i += 256) store_elem(ddt, t * p.ld_dt + i, p.dt_dtype, 0.0f);
+    outside[tid] = out;
+    if (__syncthreads_count(out) == 0) return;
+    for (int k = 0; k < n; k++) {
+        if (!outside[k]) continue;
+        const int64_t t = t0 + k;
+        for (int i = tid; i < p.H * p.dv; i += 256) dx[t * p.ld_x + i] = T{};
+        for (int i = tid; i < p.G * p.dk; i += 256) {
+            db[t * p.ld_b + i] = T{};
+            dc[t * p.ld_c + i] = T{};
+        }
+        for (int i = tid; i < p.H; i += 256) store_elem(ddt, t * p.ld_dt + i, p.dt_dtype, 0.0f);
+    }
 }
 
 // The decays' gradients of every chunk, a wave each: the suffix sums of r_t - Delta_t c_t and what
 // the last token gets from the chunk's end, in double (the terms cancel); ddt, and the chunk's
 // share of dA, dD and ddt_bias to hp [slot][3][H].
-__global__ __launch_bounds__(256) void rates_kernel(ScanP p, const Decay* decays, const RateSums* sums, void* ddt, float* hp, int nmax) {
+__global__ __launch_bounds__(256) void rates_kernel(ScanP p, const Decay* decays, const RateSums* sums, void* ddt, float* hp, uint32_t slots) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + wave;  // (b, chunk, h), h fastest
-    const int h = static_cast<int>(unit % p.H), ch = static_cast<int>(unit / p.H % nmax);
-    const int64_t b = unit / p.H / nmax;
-    if (b >= p.B) return;
-    const SeqRange sr = seq_range(p, static_cast<int>(b));
-    const int live = sr.len - ch * kQ;
-    if (live <= 0) return;
-    const int64_t slot = slot_of(p, static_cast<int>(b), sr.begin, ch);
+    uint32_t su = blockIdx.x * 4u + wave;
+    const int h = take(su, p.H);
+    if (su >= slots) return;
+    const int64_t slot = su;
+    float* o = hp + slot * 3 * p.H + h;
+    const ChunkAt at = chunk_at(p, su);
+    if (!at.used) {
+        if (lane < 3) o[lane * p.H] = 0.0f;
+        return;
+    }
+    const SeqRange sr = at.sr;
+    const int ch = at.ch, live = sr.len - ch * kQ;
     const Decay& d = decays[slot * p.H + h];
     const RateSums& m = sums[slot * p.H + h];
     const float delta = d.delta[lane], c = m.c[lane];
@@ -680,33 +717,18 @@ __global__ __launch_bounds__(256) void rates_kernel(ScanP p, const Decay* decays
     const float da = static_cast<float>(wave_last(wave_prefix(rate * delta)));
     const float db = wave_sum(dz);
     if (lane == 0) {
-        float* o = hp + static_cast<size_t>(slot) * 3 * p.H + h;
         o[0] = da;
         o[p.H] = m.dd;
         o[2 * p.H] = db;
     }
 }
 
-// The heads' dA, dD and ddt_bias over all chunks (a packing's unused slots hold nothing).
+// The heads' dA, dD and ddt_bias over all chunks (a packing's unused slots hold zeros).
 __global__ __launch_bounds__(256) void head_sums_kernel(ScanP p, const float* hp, int64_t slots, float* dA, float* dD, float* dbias) {
     __shared__ double red[256];
     const int h = blockIdx.x % p.H, which = blockIdx.x / p.H;
     double s = 0.0;
-    for (int64_t i = threadIdx.x; i < slots; i += 256) {
-        bool used = true;
-        if (p.cu) {
-            int lo = 0, hi = p.B - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (mid + packed_span(p.cu, mid, p.T).begin / kQ <= i) lo = mid;
-                else hi = mid - 1;
-            }
-            const Span sp = packed_span(p.cu, lo, p.T);
-            const int64_t ch = i - lo - sp.begin / kQ;
-            used = ch >= 0 && ch * kQ < sp.end - sp.begin;
-        }
-        if (used) s += hp[i * 3 * p.H + static_cast<int64_t>(which) * p.H + h];
-    }
+    for (int64_t i = threadIdx.x; i < slots; i += 256) s += hp[i * 3 * p.H + static_cast<int64_t>(which) * p.H + h];
     red[threadIdx.x] = s;
     __syncthreads();
     for (int n = 128; n > 0; n >>= 1) {
@@ -723,8 +745,8 @@ __global__ __launch_bounds__(256) void copy_or_zero_kernel(const float* src, flo
 }
 
 // Slices of a group's heads: enough workgroups for two a CU.
-int grad_slices(const la_scan_config& c) {
-    const int64_t units = slot_count(c) * c.G;
+int grad_slices(const la_scan_config& c, bool packed) {
+    const int64_t units = slot_count(c, packed) * c.G;
     const int hpg = c.H / c.G;
     if (units == 0 || hpg == 0) return 1;
     int64_t n = (512 + units - 1) / units;
@@ -736,12 +758,12 @@ int grad_slices(const la_scan_config& c) {
 struct BwdWs {
     size_t S, dS, decays, sums, dbp, dcp, hp, total;
 };
-BwdWs bwd_ws(const la_scan_config& c) {
+BwdWs bwd_ws(const la_scan_config& c, bool packed) {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-    const int64_t slots = slot_count(c);
+    const int64_t slots = slot_count(c, packed), rows = packed ? c.T : static_cast<int64_t>(c.B) * c.T;
     const size_t st = up(static_cast<size_t>(slots) * c.H * c.d_k * c.d_v * sizeof(float));
-    const int slices = grad_slices(c);
-    const size_t bc = slices > 1 ? up(static_cast<size_t>(slices) * c.B * c.T * c.G * c.d_k * sizeof(float)) : 0;
+    const int slices = grad_slices(c, packed);
+    const size_t bc = slices > 1 ? up(static_cast<size_t>(slices) * rows * c.G * c.d_k * sizeof(float)) : 0;
     BwdWs w;
     w.S = 0;
     w.dS = w.S + st;
@@ -757,30 +779,29 @@ BwdWs bwd_ws(const la_scan_config& c) {
 template <class T, int N>
 hipError_t launch(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
     const ScanP p = scan_params(c, a);
-    const BwdWs w = bwd_ws(c);
+    const bool packed = a.cu != nullptr;
+    const BwdWs w = bwd_ws(c, packed);
     float* S = reinterpret_cast<float*>(a.ws + w.S);
     float* dS = reinterpret_cast<float*>(a.ws + w.dS);
     Decay* decays = reinterpret_cast<Decay*>(a.ws + w.decays);
     RateSums* sums = reinterpret_cast<RateSums*>(a.ws + w.sums);
     float* hp = reinterpret_cast<float*>(a.ws + w.hp);
     const int64_t rows = a.cu ? c.T : static_cast<int64_t>(c.B) * c.T;
-    const int nmax = (c.T + kQ - 1) / kQ;
-    const int64_t slots = a.cu ? static_cast<int64_t>(c.B) + c.T / kQ + 1 : static_cast<int64_t>(c.B) * nmax;
-    const int64_t groups = static_cast<int64_t>(c.B) * c.H * (c.d_v / kPT);
+    const int64_t slots = slot_count(c, packed), tiles = c.d_v / kPT;
+    const int64_t groups = static_cast<int64_t>(c.B) * c.H * tiles, chunks = slots * c.H * tiles;
     const T* dy = static_cast<const T*>(a.dy);
-    const unsigned units = static_cast<unsigned>((static_cast<int64_t>(c.B) * nmax * c.H + 3) / 4);
-    decays_kernel<<<dim3(units), 256, 0, s>>>(p, decays, nmax);
+    const unsigned units = static_cast<unsigned>((slots * c.H + 3) / 4);
+    decays_kernel<<<dim3(units), 256, 0, s>>>(p, decays, static_cast<uint32_t>(slots));
     // Enough heads: a workgroup walks a sequence.  Fewer than a workgroup a CU: one a chunk
     // and a joining pass (three times the state traffic, but no walk).
-    if (groups >= 256 || nmax < 8) {
+    if (groups >= 256 || c.T <= 7 * kQ || chunks >= kMaxUnits) {
         scan_walk_kernel<T, N, false><<<dim3(static_cast<unsigned>(2 * groups)), 256, 0, s>>>(p, dy, a.S0, a.dST, S, dS, decays, a.dS0);
     } else {
-        const unsigned grid = static_cast<unsigned>(2 * groups * nmax);
         const unsigned join = static_cast<unsigned>((static_cast<int64_t>(c.B) * c.H * (c.d_k * c.d_v / 4) + 255) / 256);
-        scan_walk_kernel<T, N, true><<<dim3(grid), 256, 0, s>>>(p, dy, nullptr, nullptr, S, dS, decays, nullptr);
+        scan_walk_kernel<T, N, true><<<dim3(static_cast<unsigned>(2 * chunks)), 256, 0, s>>>(p, dy, nullptr, nullptr, S, dS, decays, nullptr);
         walk_join_kernel<<<dim3(join, 2), 256, 0, s>>>(p, a.S0, a.dST, S, dS, decays, a.dS0);
     }
-    const int slices = grad_slices(c);
+    const int slices = grad_slices(c, packed);
     float* dbp = slices > 1 ? reinterpret_cast<float*>(a.ws + w.dbp) : nullptr;
     float* dcp = slices > 1 ? reinterpret_cast<float*>(a.ws + w.dcp) : nullptr;
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&scan_grad_kernel<T, N>),
@@ -788,14 +809,14 @@ hipError_t launch(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     scan_grad_kernel<T, N><<<dim3(static_cast<unsigned>(slots * c.G * slices)), 512, sizeof(GradLds<T, N>), s>>>(
         p, dy, S, dS, a.dx, a.db, a.dc, dbp, dcp, decays, sums, slices, rows);
-    rates_kernel<<<dim3(units), 256, 0, s>>>(p, decays, sums, a.ddt, hp, nmax);
+    rates_kernel<<<dim3(units), 256, 0, s>>>(p, decays, sums, a.ddt, hp, static_cast<uint32_t>(slots));
     if (slices > 1) {
         const int64_t items = rows * (c.G * c.d_k / 4);
         join_slices_kernel<T><<<dim3(static_cast<unsigned>((items + 255) / 256)), 256, 0, s>>>(
             p, dbp, dcp, static_cast<T*>(a.db), static_cast<T*>(a.dc), slices, rows);
     }
-    if (a.cu)
-        clear_outside_kernel<T><<<dim3(static_cast<unsigned>(c.T)), 256, 0, s>>>(p, static_cast<T*>(a.dx), a.ddt,
+    if (packed)
+        clear_outside_kernel<T><<<dim3(static_cast<unsigned>((c.T + 255) / 256)), 256, 0, s>>>(p, static_cast<T*>(a.dx), a.ddt,
                                                                                 static_cast<T*>(a.db), static_cast<T*>(a.dc));
     head_sums_kernel<<<dim3(3 * c.H), 256, 0, s>>>(p, hp, slots, a.dA, a.dD, a.dbias);
     return hipGetLastError();
@@ -803,7 +824,8 @@ hipError_t launch(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
 
 }  // namespace
 
-size_t scan_bwd_workspace(const la_scan_config& c) { return bwd_ws(c).total; }
+size_t scan_bwd_workspace(const la_scan_config& c, bool packed) { return bwd_ws(c, packed).total; }
+int64_t scan_bwd_slots(const la_scan_config& c, bool packed) { return slot_count(c, packed); }
 
 hipError_t launch_scan_bwd(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
     if (c.B == 0 || c.T == 0) {  // no tokens: the state's gradient passes through, the sums are zero

@@ -60,7 +60,8 @@ def declare(lib) -> None:
         f = getattr(lib, name)
         f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(cfg)] + args
     for name, cfg in (("la_conv_bwd_workspace_bytes", ConvConfig), ("la_scan_workspace_bytes", ScanConfig),
-                      ("la_scan_bwd_workspace_bytes", ScanConfig), ("la_norm_bwd_workspace_bytes", NormConfig)):
+                      ("la_scan_bwd_workspace_bytes", ScanConfig), ("la_scan_bwd_varlen_workspace_bytes", ScanConfig),
+                      ("la_norm_bwd_workspace_bytes", NormConfig)):
         f = getattr(lib, name)
         f.restype, f.argtypes = sz, [ctypes.POINTER(cfg)]
 
@@ -252,6 +253,11 @@ def la_scan_fwd(cfg: ScanConfig, x, dt, A, b, c, D, dt_bias, S0, y, S_T, workspa
 
 def la_scan_bwd_workspace_bytes(cfg: ScanConfig) -> int:
     return _la.load_library().la_scan_bwd_workspace_bytes(cfg)
+
+
+def la_scan_bwd_varlen_workspace_bytes(cfg: ScanConfig) -> int:
+    """What la_scan_bwd needs with cu_seqlens (la_scan_bwd_workspace_bytes is enough too)."""
+    return _la.load_library().la_scan_bwd_varlen_workspace_bytes(cfg)
 
 
 def la_scan_bwd(cfg: ScanConfig, x, dt, A, b, c, D, dt_bias, S0, dy, dS_T, dx, ddt, dA, db, dc, dD, ddt_bias, dS0,

@@ -135,6 +135,47 @@ def test_conv(dtype, B, T, cu, C, W, act, extra, bias, states, wt):
         assert (dxb[:, :8] == 9).all() and (dxb[:, 8 + C:] == 9).all()
 
 
+@pytest.mark.parametrize("cu", [None, [0, 7000, 7001, 9000]])
+def test_conv_gradients_over_more_blocks_than_workgroups(cu):
+    """9000 tokens by 32768 channels: a workgroup takes several of the token blocks."""
+    g = gen(2)
+    T, C, W = 9000, 32768, 4
+    B = 1 if cu is None else 3
+    x, dy, w = draw(g, T, 256, dtype=BF), draw(g, T, 256, dtype=BF), draw(g, 256, W, dtype=F32)
+    wide = lambda t: t.repeat(1, C // 256).contiguous()  # noqa: E731
+    cfg = la.ConvConfig(B=B, T=T, C=C, width=W, x_dtype=CODE[BF])
+    n = la.la_conv_bwd_workspace_bytes(cfg)
+    assert n <= 32 * C * (W + 1) * 4
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    dx = torch.empty(T, C, dtype=BF, device="cuda")
+    dw, db = torch.empty(C, W, device="cuda"), torch.empty(C, device="cuda")
+    la.la_conv_bwd(cfg, wide(x), w.repeat(C // 256, 1), None, None, wide(dy), None, dx, dw, db, None, ws, n,
+                   cu_seqlens=cu_tensor(cu))
+    for t in (dx.view(T, -1, 256).transpose(0, 1), dw.view(-1, 256, W), db.view(-1, 256)):
+        assert torch.equal(t, t[:1].expand_as(t))  # the repeated channels agree in every bit
+    xn, dyn, wn, zero = np64(x), np64(dy), np64(w), np.zeros((W - 1, 256))
+    dwr, dwm, dbr, dbm = np.zeros((256, W)), np.zeros((256, W)), np.zeros(256), np.zeros(256)
+    for lo, hi in spans(B, T, cu):
+        dxr, c, d, _ = R.conv_bwd(xn[lo:hi], wn, np.zeros(256), zero, dyn[lo:hi], zero, 1)
+        _, big = R.conv_pre(np.abs(xn[lo:hi]), np.abs(wn), np.zeros(256), zero)
+        dxm, cm, dm, _ = R.conv_bwd(np.abs(xn[lo:hi]), np.abs(wn), np.zeros(256), zero, np.abs(dyn[lo:hi]) * (1.0 + big) * 1.1,
+                                    zero, 0)
+        close(dx[lo:hi, :256], dxr, dxm, 2.0 ** -20, "dx")
+        dwr, dwm, dbr, dbm = dwr + c, dwm + cm, dbr + d, dbm + dm
+    sums = 2.0 ** -20 + 2.0 ** -24 * 512
+    close(dw[:256], dwr, dwm, sums, "dweight")
+    close(db[:256], dbr, dbm, sums, "dbias")
+
+
+def test_conv_gradients_of_no_sequences():
+    cfg = la.ConvConfig(B=0, T=50, C=64, width=4)
+    dw, db = torch.full((64, 4), 3.0, device="cuda"), torch.full((64,), 3.0, device="cuda")
+    w = torch.ones(64, 4, device="cuda")
+    la.la_conv_bwd(cfg, None, w, None, None, None, None, None, dw, db, None, None, 0,
+                   cu_seqlens=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    assert not dw.any() and not db.any()
+
+
 @pytest.mark.parametrize("dtype,B,C,W,pool", [(BF, 5, 264, 4, True), (F32, 1, 8, 2, True), (BF, 3, 2312, 3, False)])
 def test_conv_step_continues_the_forward(dtype, B, C, W, pool):
     g = gen(B)
@@ -215,7 +256,7 @@ class Scan:
 
     def bwd_into(self, bufs):
         o = bufs[1]
-        n = la.la_scan_bwd_workspace_bytes(self.cfg)
+        n = (la.la_scan_bwd_varlen_workspace_bytes if self.cu is not None else la.la_scan_bwd_workspace_bytes)(self.cfg)
         ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
         la.la_scan_bwd(self.cfg, self.x, self.dt, self.A, self.b, self.c, self.D, self.bias, self.S0, self.dy, self.dST, o["dx"],
                        o["ddt"], o["dA"], o["db"], o["dc"], o["dD"], o["ddt_bias"], o["dS0"], ws, n,
@@ -321,6 +362,24 @@ SCAN = [
     (BF, 3, 1200, 1, 1, 16, 64, dict(cu=[0, 900, 900, 1190])),
     (BF, 4, 70, 64, 2, 16, 64, {}),     # many heads: a workgroup walks a sequence
 ]
+
+
+@pytest.mark.parametrize("H", [2, 1])
+def test_scan_of_many_short_sequences(H):
+    """200 ragged sequences, some empty, tokens before and behind them (H = 1: a workgroup a chunk)."""
+    lens = torch.randint(0, 41, (200,), generator=gen(7)).tolist()
+    lens[17], lens[18], lens[199] = 130, 0, 64
+    cu = np.concatenate([[5], 5 + np.cumsum(lens)]).tolist()
+    Scan(BF, 200, cu[-1] + 300, H, 1, 16, 64, cu=cu).check()
+
+
+def test_scan_nan_step_reaches_its_own_head_from_its_token_on():
+    s = Scan(BF, 1, 200, 2, 1, 64, 64)
+    s.dt[70, 1] = float("nan")
+    y, ST = s.fwd()
+    y = y.view(200, 2, 64)
+    assert y[:, 0].isfinite().all() and y[:70, 1].isfinite().all() and y[70:, 1].isnan().all()
+    assert ST[0, 0].isfinite().all() and ST[0, 1].isnan().all()
 
 
 @pytest.mark.parametrize("dtype,B,T,H,G,N,P,more", SCAN)

@@ -17,6 +17,7 @@ def test_library_exports_every_declared_function():
     names = sorted(set(re.findall(r"^\s*(?:la_status|size_t)\s+(la_\w+)\s*\(", text, re.M)))
     assert names == sorted(["la_conv_fwd", "la_conv_bwd", "la_conv_step", "la_conv_bwd_workspace_bytes", "la_scan_fwd",
                             "la_scan_bwd", "la_scan_step", "la_scan_workspace_bytes", "la_scan_bwd_workspace_bytes",
+                            "la_scan_bwd_varlen_workspace_bytes",
                             "la_norm_fwd", "la_norm_bwd", "la_norm_bwd_workspace_bytes"])
     lib = la.load_library()
     for n in names:
@@ -47,6 +48,7 @@ def conv_fwd(cfg, **p):
     (dict(act=2), la.LA_ERR_INVALID_ARG, "act"), (dict(x_dtype=7), la.LA_ERR_INVALID_ARG, "x_dtype"),
     (dict(w_dtype=-1), la.LA_ERR_INVALID_ARG, "w_dtype"), (dict(ld_x=32), la.LA_ERR_INVALID_ARG, "shorter"),
     (dict(ld_y=68), la.LA_ERR_ALIGNMENT, "16 bytes"), (dict(B=1 << 20, T=1 << 20), la.LA_ERR_UNSUPPORTED, "elements"),
+    (dict(B=65536), la.LA_ERR_UNSUPPORTED, "65535"), (dict(T=(1 << 30) + 1), la.LA_ERR_UNSUPPORTED, "2^30"),
 ])
 def test_conv_refuses_configs(kw, status, word):
     refused(lambda: conv_fwd(conv(**kw)), status, word)
@@ -91,7 +93,9 @@ def scan_fwd(cfg, **p):
     (dict(out_dtype=2), la.LA_ERR_INVALID_ARG, "out_dtype"), (dict(ld_x=128), la.LA_ERR_INVALID_ARG, "shorter"),
     (dict(ld_b=132), la.LA_ERR_ALIGNMENT, "16 bytes"), (dict(ld_c=64), la.LA_ERR_INVALID_ARG, "shorter"),
     (dict(ld_dt=3), la.LA_ERR_INVALID_ARG, "ld_dt"), (dict(B=70000), la.LA_ERR_UNSUPPORTED, "65535"),
-    (dict(B=65535, H=65534), la.LA_ERR_UNSUPPORTED, "too many"),
+    (dict(B=65535, H=65534), la.LA_ERR_UNSUPPORTED, "too many"), (dict(T=(1 << 30) + 1), la.LA_ERR_UNSUPPORTED, "2^30"),
+    (dict(H=65534, d_v=192), la.LA_ERR_UNSUPPORTED, "2^23"), (dict(ld_x=(1 << 23) + 8), la.LA_ERR_UNSUPPORTED, "2^23"),
+    (dict(ld_c=(1 << 23) + 8), la.LA_ERR_UNSUPPORTED, "2^23"), (dict(ld_dt=(1 << 23) + 1), la.LA_ERR_UNSUPPORTED, "2^23"),
 ])
 def test_scan_refuses_configs(kw, status, word):
     refused(lambda: scan_fwd(scan(**kw)), status, word)
@@ -117,6 +121,32 @@ def test_scan_refuses_pointers():
     refused(lambda: la.la_scan_step(scan(), *[FAKE] * 5, None, None, FAKE, FAKE, stream=0), la.LA_ERR_INVALID_ARG, "T == 1")
     refused(lambda: la.la_scan_step(scan(T=1), *[FAKE] * 5, None, None, FAKE, FAKE, slots=FAKE, n_slots=-1, stream=0),
             la.LA_ERR_INVALID_ARG, "n_slots")
+
+
+def test_packed_workspaces_do_not_grow_with_the_sequences():
+    """64 sequences of one packing of 2^18 tokens: about the states of one sequence of them."""
+    one, many = scan(B=1, T=1 << 18), scan(B=64, T=1 << 18)
+    n1, n64 = la.la_scan_bwd_varlen_workspace_bytes(one), la.la_scan_bwd_varlen_workspace_bytes(many)
+    assert n1 <= n64 <= 1.02 * n1 and n64 <= la.la_scan_bwd_workspace_bytes(many)
+    # two FP32 states of 64 x 64 a head at each of 4096 + 65 slots, and 4 KB beside them
+    assert n64 <= (4096 + 65) * 4 * (2 * 64 * 64 * 4 + 4096)
+    assert la.la_conv_bwd_workspace_bytes(conv(B=4096, T=1 << 20, C=4096)) <= 256 << 20
+    args = [FAKE] * 5 + [None, None, None, FAKE, None, *[FAKE] * 5, None, None, None]
+    refused(lambda: la.la_scan_bwd(many, *args, FAKE, n64 - 1, cu_seqlens=FAKE, stream=0), la.LA_ERR_WORKSPACE, "workspace")
+
+
+def test_backward_refuses_what_its_grids_cannot_hold():
+    args = [FAKE] * 5 + [None, None, None, FAKE, None, *[FAKE] * 5, None, None, None, FAKE]
+    for kw, cu in ((dict(B=64, T=1 << 23), None), (dict(T=1 << 28), FAKE)):
+        refused(lambda: la.la_scan_bwd(scan(**kw), *args, 1 << 62, cu_seqlens=cu, stream=0), la.LA_ERR_UNSUPPORTED, "2^23")
+        assert la.la_scan_bwd_workspace_bytes(scan(**kw)) == 0
+
+
+def test_no_sequences_need_no_tensors():
+    """B = 0 with boundaries and a packed length."""
+    la.la_conv_fwd(conv(B=0), None, None, None, None, None, None, cu_seqlens=FAKE, stream=0)
+    la.la_scan_fwd(scan(B=0), None, None, None, None, None, None, None, None, None, None, None, 0, cu_seqlens=FAKE, stream=0)
+    assert la.la_conv_bwd_workspace_bytes(conv(B=0, T=4096)) == 0
 
 
 # -------------------------------------------------------------------------------------- norm
