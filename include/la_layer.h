@@ -24,6 +24,8 @@
  * each other at the same distance, and ld_* times the element size is a multiple of 16 bytes:
  * x, b and c of the scan can be the slices of one convolution output, and their gradients
  * the slices of one buffer.
+ *
+ * Outputs and gradients overlap neither inputs nor each other, but where a function says so.
  */
 #ifndef LA_LAYER_H
 #define LA_LAYER_H
@@ -140,11 +142,12 @@ la_status la_scan_step(const la_scan_config* cfg, const void* x, const void* dt,
  * and, with a quantizer, per group of `group` consecutive columns (0 = the whole row) the
  * codecs of la.h on n:  INT8 s = amax/127, code = clamp(rne(n/s), -127, 127);  E4M3 s =
  * amax/448, code = e4m3(n/s)  (s = 1 when amax == 0);  y is then the value the code stands
- * for, code * s.  A row with an infinity or NaN among its h gives NaN where the formula does;
- * its codes are unspecified.
+ * for, code * s (n / s within FP32's rounding of the middle between two codes may take either).
+ * A row with an infinity or NaN among its h gives NaN where the formula does; its codes are
+ * unspecified.
  */
 typedef struct la_norm_config {
-    int32_t rows, d;    /* d a multiple of 8 up to 16384 */
+    int32_t rows, d;    /* rows min(256, max(8, d / 4)) below 2^32; d a multiple of 8 up to 16384 */
     float eps;          /* >= 0 */
     int32_t qdq;        /* la_qdq: LA_QDQ_NONE, LA_QDQ_INT8_GROUP or LA_QDQ_E4M3_TILE (one row high) */
     int32_t group;      /* with a quantizer 0, 16, 32, 64 or 128, dividing d */

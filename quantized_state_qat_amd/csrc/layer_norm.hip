@@ -59,6 +59,16 @@ __device__ __forceinline__ float row_sum(float x, float* lds) {
     __syncthreads();
     return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
+// The same of doubles.
+template <int LANES>
+__device__ __forceinline__ double row_sum_wide(double x, double* lds) {
+#pragma unroll
+    for (int m = 1; m < (LANES < 64 ? LANES : 64); m <<= 1) x += __shfl_xor(x, m);
+    if constexpr (LANES <= 64) return x;
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
 template <int LANES>
 __device__ __forceinline__ float row_max(float x, float* lds) {
     if constexpr (LANES <= 64) return group_max_abs<LANES>(x);
@@ -93,13 +103,18 @@ struct NormFwd {
 template <class T, class O, int LANES, int CH, int QDQ>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(NormFwd p) {
     constexpr int RPW = 256 / LANES;  // rows a workgroup
+    // FP32 values of codes: half a code's step is far above FP32's rounding, so every operation is
+    // rounded as the formula has it (the squares summed in double), and a value near the middle
+    // between two codes goes where FP32 arithmetic puts it.
+    constexpr bool STEPWISE = QDQ != LA_QDQ_NONE && sizeof(O) == 4;
     __shared__ float lds[8];
+    __shared__ double wide[STEPWISE ? 4 : 1];
     const int l = threadIdx.x % LANES;
     const int row = blockIdx.x * RPW + threadIdx.x / LANES;
     if (LANES <= 64 && row >= p.rows) return;  // whole groups of lanes leave together
     const size_t base = static_cast<size_t>(row) * p.d;
     float h[CH][8];
-    float ss = 0.0f;
+    std::conditional_t<STEPWISE, double, float> ss = 0;
 #pragma unroll
     for (int c = 0; c < CH; c++) {
         const int col = (c * LANES + l) * kPiece;
@@ -125,9 +140,14 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormFwd p) {
             for (int e = 0; e < 8; e++) h[c][e] = 0.0f;
         }
 #pragma unroll
-        for (int e = 0; e < 8; e++) ss = __builtin_fmaf(h[c][e], h[c][e], ss);
+        for (int e = 0; e < 8; e++) {
+            if constexpr (STEPWISE) ss += h[c][e] * h[c][e];
+            else ss = __builtin_fmaf(h[c][e], h[c][e], ss);
+        }
     }
-    const float r = rsqrt_fine(row_sum<LANES>(ss, lds) / static_cast<float>(p.d) + p.eps);
+    float r;  // 1 / rms, or the rms
+    if constexpr (STEPWISE) r = sqrtf(static_cast<float>(row_sum_wide<LANES>(ss, wide) / p.d) + p.eps);
+    else r = rsqrt_fine(row_sum<LANES>(ss, lds) / static_cast<float>(p.d) + p.eps);
     float amax[CH];
 #pragma unroll
     for (int c = 0; c < CH; c++) {
@@ -138,7 +158,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormFwd p) {
             load_w(p.w, p.w_dtype, col, w);
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                h[c][e] = h[c][e] * r * w[e];
+                h[c][e] = (STEPWISE ? h[c][e] / r : h[c][e] * r) * w[e];
                 if (QDQ != LA_QDQ_NONE) amax[c] = fmaxf(amax[c], fabsf(h[c][e]));
             }
         }

@@ -157,6 +157,7 @@ def norm(**kw):
 @pytest.mark.parametrize("kw,status,word", [
     (dict(rows=-1), la.LA_ERR_INVALID_ARG, "size"), (dict(d=0), la.LA_ERR_INVALID_ARG, "size"),
     (dict(d=12), la.LA_ERR_UNSUPPORTED, "multiple of 8"), (dict(d=16392), la.LA_ERR_UNSUPPORTED, "16384"),
+    (dict(rows=1 << 24, d=4096), la.LA_ERR_UNSUPPORTED, "rows"), (dict(rows=1 << 29, d=8), la.LA_ERR_UNSUPPORTED, "rows"),
     (dict(eps=-1.0), la.LA_ERR_INVALID_ARG, "eps"), (dict(eps=float("nan")), la.LA_ERR_INVALID_ARG, "eps"),
     (dict(qdq=5), la.LA_ERR_INVALID_ARG, "qdq"), (dict(qdq=la.LA_QDQ_INT8_GROUP, group=8), la.LA_ERR_UNSUPPORTED, "group"),
     (dict(qdq=la.LA_QDQ_E4M3_TILE, group=64, d=96), la.LA_ERR_INVALID_ARG, "divide"),
