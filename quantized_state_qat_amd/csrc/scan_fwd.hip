@@ -1,55 +1,68 @@
-// Selective scan forward: a workgroup walks the 64-token chunks of one sequence for 64 value
-// columns of a head, the d_k x 64 state in its accumulators.
+// Selective scan forward: a workgroup walks the 64-token chunks of one sequence for 64 or 128
+// value columns, the states in its accumulators.
 //
-// Only the state's update is serial.  Eight waves, two roles: waves 0..3 bring chunk i + 1 into
-// LDS and form its M (and the decays of chunk i + 2, on the wave with one tile of M); waves
-// 4..7 (16 columns each) meanwhile form chunk i's output and update the state.  Two barriers a
-// chunk (staged | done) and two LDS buffers; the loads of chunk i + 3 are issued while chunk i is
-// in work.  With every wave doing every part in turn a chunk took 5.3 us, most of it waiting (one
-// wave a SIMD).
+// Only the states' update is serial.  Eight waves, two roles, two barriers a step; at step i
+//   waves 0..3   bring chunk i into LDS | form its M and the decays of chunk i + 1
+//   waves 4..7   (16 or 32 columns each) form M x and W x of chunk i - 1 | add the state's part,
+//                write the output and update the state
+// with two LDS buffers and the loads of chunk i + 2 issued at step i.  The operands formed in
+// FP32 (M, the state, W x) enter the products as two bf16 parts, 2^-17 of a value.  LDS and the
+// chain of reads, products and operand splits of waves 4..7 bound it, not memory: with d_k = 128
+// a chunk takes 2.7 us for 64 columns, 4.4 us for 128.  8 sequences of 4096 tokens, 16 heads,
+// d_v = 128: 180 us; 64 packed sequences, 40686 tokens in all: 265 us (334 with 64 columns a
+// workgroup).  Every wave doing every part in turn took 5.3 us a chunk of 64 columns; sixteen
+// waves in the same roles 5% more, and c's rows loaded from memory by waves 4..7 themselves 60%
+// more than this.
 //
 // Few heads and long sequences: the walk is cut into segments that run side by side.  A first
 // pass forms each segment's own contribution to the state from zero, a small kernel joins them
-// (S_in of every segment), and the full walk starts every segment from its S_in.
+// (S_in of every segment), and the full walk starts every segment from its S_in (32768 tokens,
+// 32 heads of d_v = 64: 64 + 10 + 147 us).
 #include "la_scan.hpp"
 
 namespace la {
 namespace {
 
-template <class T, int N, bool FULL>
-struct FwdLds {
+// CT: 64-column tiles a workgroup; HEADS: heads that they belong to (1, or CT heads of one tile each).
+template <class T, int N, int CT, int HEADS, bool FULL>
+struct FwdBuf {
     T b[kQ * lds_row<T>(N)];
     T c[FULL ? kQ * lds_row<T>(N) : 8];
-    T x[kQ * lds_row64<T>()];
-    T m[FULL ? Mat<T>::template parts<2> : 1][FULL ? kQ * lds_row64<T>() : 8];
+    T x[kQ * (CT == 2 ? lds_row<T>(128) : lds_row64<T>())];
 };
-// Two buffers where they fit (160 KB; not FP32 with d_k = 128: the roles then take turns), and
-// three of the decays, which are formed earlier.
-template <class T, int N, bool FULL>
-constexpr int kBufs = 2 * sizeof(FwdLds<T, N, FULL>) + 3 * sizeof(Decay) <= 160 * 1024 ? 2 : 1;
-template <class T, int N, bool FULL>
-constexpr size_t kFwdLds = kBufs<T, N, FULL> * sizeof(FwdLds<T, N, FULL>) + 3 * sizeof(Decay);
+template <class T, int N, int CT, int HEADS, bool FULL, int NB>
+struct FwdLds {
+    FwdBuf<T, N, CT, HEADS, FULL> buf[NB];
+    T m[FULL ? HEADS : 1][FULL ? Mat<T>::template parts<2> : 1][FULL ? kQ * lds_row64<T>() : 8];
+    Decay d[3][HEADS];  // formed a chunk earlier
+};
+// Two buffers where they fit (160 KB; not FP32 with d_k = 128: the roles then take turns).
+template <class T, int N, int CT, int HEADS, bool FULL>
+constexpr int kBufs = sizeof(FwdLds<T, N, CT, HEADS, FULL, 2>) <= 160 * 1024 ? 2 : 1;
+template <class T, int N, int CT, int HEADS, bool FULL>
+using FwdShared = FwdLds<T, N, CT, HEADS, FULL, kBufs<T, N, CT, HEADS, FULL>>;
 
 // FULL: outputs and S_T, from the segment's S_in (or S0).  Otherwise the segment's state from
 // zero into `local` and its decay into `decay`.
-template <class T, int N, bool FULL>
+template <class T, int N, int CT, int HEADS, bool FULL>
 __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0, const float* Sin, void* y, float* ST,
                                                        float* local, float* decay, int nseg, int segs) {
     using MT = Mat<T>;
-    constexpr int P2 = MT::template parts<2>, P3 = MT::template parts<3>;
-    constexpr int RB = lds_row<T>(N), RX = lds_row64<T>(), RM = lds_row64<T>();
+    constexpr int P2 = MT::template parts<2>;
+    constexpr int COLS = kPT * CT;
+    constexpr int RB = lds_row<T>(N), RX = CT == 2 ? lds_row<T>(128) : lds_row64<T>(), RM = lds_row64<T>();
     constexpr int KS = N / 32;  // contraction steps over the state's rows
-    constexpr int NB = kBufs<T, N, FULL>;
-    using Buf = FwdLds<T, N, FULL>;
+    constexpr int NB = kBufs<T, N, CT, HEADS, FULL>;
+    using Buf = FwdBuf<T, N, CT, HEADS, FULL>;
     extern __shared__ __align__(16) char raw_lds[];
-    Buf* const bufs = reinterpret_cast<Buf*>(raw_lds);
-    Decay* const decays = reinterpret_cast<Decay*>(raw_lds + NB * sizeof(Buf));
+    FwdShared<T, N, CT, HEADS, FULL>& shared = *reinterpret_cast<FwdShared<T, N, CT, HEADS, FULL>*>(raw_lds);
+    Buf* const bufs = shared.buf;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lm = lane & 15, g = lane >> 4;
 
-    const int tiles = p.dv / kPT;
+    const int tiles = HEADS == 1 ? p.dv / COLS : 1;
     uint32_t u = die_unit(blockIdx.x, gridDim.x);
-    const int tile = take(u, tiles), h = take(u, p.H), seg = take(u, segs);  // segs: segments of this launch
+    const int tile = take(u, tiles), h = take(u, p.H / HEADS) * HEADS, seg = take(u, segs);  // segs: segments of this launch
     const int bi = static_cast<int>(u);
     uint32_t hu = static_cast<uint32_t>(h);
     take(hu, p.H / p.G);
@@ -61,26 +74,30 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
     const int c0 = seg * cps;
     const int c1 = c0 + cps < nch ? c0 + cps : nch;
     if (c0 >= nch && !(nch == 0 && seg == 0)) return;
-    const float A = p.A ? p.A[h] : 0.0f;  // (no tokens: A may be missing)
-    const float Dh = FULL && p.D ? p.D[h] : 0.0f, bias = p.bias ? p.bias[h] : 0.0f;
+    float A[HEADS], Dh[HEADS], bias[HEADS];
+#pragma unroll
+    for (int q = 0; q < HEADS; q++) {
+        A[q] = p.A ? p.A[h + q] : 0.0f;  // (no tokens: A may be missing)
+        Dh[q] = FULL && p.D ? p.D[h + q] : 0.0f;
+        bias[q] = p.bias ? p.bias[h + q] : 0.0f;
+    }
 
     if (FULL) {  // the tiles above the diagonal that the products below read stay zero
-        for (int q = 0; q < NB; q++)
-            for (int i = threadIdx.x; i < P2 * kQ * RM; i += 512) (&bufs[q].m[0][0])[i] = T{};
+        for (int i = threadIdx.x; i < HEADS * P2 * kQ * RM; i += 512) (&shared.m[0][0][0])[i] = T{};
         __syncthreads();
     }
 
     if (wave < 4) {
         // ------------------------------------------------------------ chunks into LDS, and M
-        const T* xg = static_cast<const T*>(p.x) + static_cast<int64_t>(h) * p.dv + tile * kPT;
+        const T* xg = static_cast<const T*>(p.x) + static_cast<int64_t>(h) * p.dv + tile * COLS;
         const T* bg = static_cast<const T*>(p.b) + static_cast<int64_t>(grp) * p.dk;
         const T* cg = static_cast<const T*>(p.c) + static_cast<int64_t>(grp) * p.dk;
         struct None {};
         struct Ahead {
             Tile<T, N, 256> b;
             std::conditional_t<FULL, Tile<T, N, 256>, None> c;
-            Tile<T, kPT, 256> x;
-            DtAhead raw;
+            Tile<T, COLS, 256> x;
+            DtAhead raw[HEADS];
         };
         // two chunks ahead (FP32 tiles are twice the registers: one)
         constexpr int AH = sizeof(T) == 2 && NB == 2 ? 2 : 1;
@@ -91,64 +108,66 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
             const int live = sr.len - ch * kQ;
             r.b.load(bg + row0 * p.ld_b, p.ld_b, live, p.dk);
             if constexpr (FULL) r.c.load(cg + row0 * p.ld_c, p.ld_c, live, p.dk);
-            r.x.load(xg + row0 * p.ld_x, p.ld_x, live, kPT);
-            if (wave == 3) r.raw.fetch(p, row0, h, lane, live);
+            r.x.load(xg + row0 * p.ld_x, p.ld_x, live, COLS);
+            if (wave == 3)
+#pragma unroll
+                for (int q = 0; q < HEADS; q++) r.raw[q].fetch(p, row0, h + q, lane, live);
         };
-        double cum_seg = 0.0;
+        double cum_seg[HEADS] = {};
         auto decays_of = [&](int ch, const Ahead& r) {  // by one wave
-            cum_seg += make_decay(decays[(ch - c0) % 3], r.raw.value(p) + bias, p.softplus, sr.len - ch * kQ, A);
+#pragma unroll
+            for (int q = 0; q < HEADS; q++)
+                cum_seg[q] += make_decay(shared.d[(ch - c0) % 3][q], r.raw[q].value(p) + bias[q], p.softplus, sr.len - ch * kQ, A[q]);
         };
         auto stage = [&](Buf& lds, const Ahead& r) {
             r.b.store(lds.b, RB);
             if constexpr (FULL) r.c.store(lds.c, RB);
             r.x.store(lds.x, RX);
         };
-        // M^T tiles (ti, s_first ..): rows s, columns t; lane: t, four consecutive s.  D goes onto the diagonal.
-        auto pair_row = [&](Buf& lds, const Decay& d, int ti, int s_first, auto count) {
-            constexpr int C = decltype(count)::value;
-            typename MT::Frag bf[C][KS], cf[KS];
-            const int t = 16 * ti + lm;
+        // M^T tile (ti, si): rows s, columns t; lane: t, four consecutive s.  D goes onto the diagonal.
+        auto pair = [&](Buf& lds, const Decay* ds, int ti, int si) {
+            const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
+            const int t = 16 * ti + lm, s0 = 16 * si + 4 * g;
+            typename MT::Frag bf[KS], cf[KS];
 #pragma unroll
             for (int ks = 0; ks < KS; ks++) {
                 cf[ks] = MT::row8(lds.c + t * RB + 32 * ks + 8 * g);
-#pragma unroll
-                for (int q = 0; q < C; q++) bf[q][ks] = MT::row8(lds.b + (16 * (s_first + q) + lm) * RB + 32 * ks + 8 * g);
+                bf[ks] = MT::row8(lds.b + (16 * si + lm) * RB + 32 * ks + 8 * g);
             }
-            const float thi = d.hi[t], tlo = d.lo[t];
-            f4 shi[C], slo[C], sdl[C];
+            float thi[HEADS], tlo[HEADS];
+            f4 shi[HEADS], slo[HEADS], sdl[HEADS];
 #pragma unroll
-            for (int q = 0; q < C; q++) {
-                const int s0 = 16 * (s_first + q) + 4 * g;
-                shi[q] = *reinterpret_cast<const f4*>(d.hi + s0);
-                slo[q] = *reinterpret_cast<const f4*>(d.lo + s0);
-                sdl[q] = *reinterpret_cast<const f4*>(d.delta + s0);
+            for (int q = 0; q < HEADS; q++) {
+                thi[q] = ds[q].hi[t], tlo[q] = ds[q].lo[t];
+                shi[q] = *reinterpret_cast<const f4*>(ds[q].hi + s0);
+                slo[q] = *reinterpret_cast<const f4*>(ds[q].lo + s0);
+                sdl[q] = *reinterpret_cast<const f4*>(ds[q].delta + s0);
             }
             __builtin_amdgcn_sched_barrier(0);
-            f4 acc[C] = {};
+            f4 acc = {};
 #pragma unroll
-            for (int ks = 0; ks < KS; ks++)
+            for (int ks = 0; ks < KS; ks++) acc = MT::mma(bf[ks], cf[ks], acc);
 #pragma unroll
-                for (int q = 0; q < C; q++) acc[q] = MT::mma(bf[q][ks], cf[ks], acc[q]);
-#pragma unroll
-            for (int q = 0; q < C; q++) {
-                const int s0 = 16 * (s_first + q) + 4 * g;
+            for (int q = 0; q < HEADS; q++) {
                 float m[4];
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
-                    m[r] = acc[q][r] * (pair_decay(thi, tlo, shi[q][r], slo[q][r]) * sdl[q][r]);
-                    m[r] = s0 + r < t ? m[r] : s0 + r == t ? m[r] + Dh : 0.0f;
+                    m[r] = acc[r] * (pair_decay(thi[q], tlo[q], shi[q][r], slo[q][r]) * sdl[q][r]);
+                    if (si == ti) m[r] = s0 + r < t ? m[r] : s0 + r == t ? m[r] + Dh[q] : 0.0f;
                 }
-                MT::template put4<P2>(&lds.m[0][t * RM + s0], kQ * RM, m);
+                MT::template put4<P2>(&shared.m[q][0][t * RM + s0], kQ * RM, m);
             }
         };
-        auto pairs = [&](Buf& lds, const Decay& d) {  // the ten tiles; the wave with one also forms the decays
+        auto pairs = [&](Buf& lds, const Decay* d) {  // the ten tiles; the wave with one also forms the decays
             if constexpr (FULL) {
-                using std::integral_constant;
-                if (wave == 0) pair_row(lds, d, 3, 0, integral_constant<int, 3>{});
-                if (wave == 1) pair_row(lds, d, 2, 0, integral_constant<int, 3>{});
-                if (wave == 2) pair_row(lds, d, 1, 0, integral_constant<int, 2>{});
-                if (wave == 2) pair_row(lds, d, 3, 3, integral_constant<int, 1>{});
-                if (wave == 3) pair_row(lds, d, 0, 0, integral_constant<int, 1>{});
+                if (wave < 2) {
+                    for (int si = 0; si < 3; si++) pair(lds, d, 3 - wave, si);
+                } else if (wave == 2) {
+                    for (int si = 0; si < 2; si++) pair(lds, d, 1, si);
+                    pair(lds, d, 3, 3);
+                } else {
+                    pair(lds, d, 0, 0);
+                }
             }
         };
         fetch(c0, even);
@@ -163,7 +182,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
                 }
                 __syncthreads();
                 if constexpr (FULL) {
-                    if (ch < c1) pairs(lds, decays[(ch - c0) % 3]);
+                    if (ch < c1) pairs(lds, shared.d[(ch - c0) % 3]);
                     if (wave == 3 && ch + 1 < c1) decays_of(ch + 1, next);
                     __syncthreads();
                 }
@@ -184,43 +203,51 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
                 fetch(ch + 1, even);
                 __syncthreads();
                 if (FULL) {
-                    pairs(bufs[0], decays[(ch - c0) % 3]);
+                    pairs(bufs[0], shared.d[(ch - c0) % 3]);
                     __syncthreads();
                 }
                 __syncthreads();
             }
         }
         if (!FULL && threadIdx.x == 192 && tile == 0)
-            decay[(static_cast<size_t>(bi) * nseg + seg) * p.H + h] = static_cast<float>(exp2(cum_seg));
+#pragma unroll
+            for (int q = 0; q < HEADS; q++)
+                decay[(static_cast<size_t>(bi) * nseg + seg) * p.H + h + q] = static_cast<float>(exp2(cum_seg[q]));
         return;
     }
 
     // ---------------------------------------------------------------- outputs and the state
-    const int w0 = 16 * (wave - 4);                // this wave's columns of the tile
-    const int pcol = tile * kPT + w0 + lm;         // this lane's state column
-    f4 S[N / 16];
-    const size_t unit = (static_cast<size_t>(bi) * p.H + h) * p.dk * p.dv;
+    const int w0 = 16 * CT * (wave - 4);  // this wave's columns of the tile, 16 at a time
+    const int hh = HEADS == 1 ? 0 : (wave - 4) / 2;  // (two heads: 32 columns are half of one's)
+    const int hw = h + hh;
+    f4 S[CT][N / 16];                     // a lane: column w0 + 16 c + lm
+    const size_t unit = (static_cast<size_t>(bi) * p.H + hw) * p.dk * p.dv;
+    const int pcol = tile * COLS + w0 - kPT * hh + lm;
     const float* init = nullptr;
-    if (FULL) init = nseg > 1 && nch > 0 ? Sin + ((static_cast<size_t>(bi) * nseg + seg) * p.H + h) * p.dk * p.dv
+    if (FULL) init = nseg > 1 && nch > 0 ? Sin + ((static_cast<size_t>(bi) * nseg + seg) * p.H + hw) * p.dk * p.dv
                                          : (S0 ? S0 + unit : nullptr);
 #pragma unroll
-    for (int i = 0; i < N / 16; i++)
+    for (int c = 0; c < CT; c++)
 #pragma unroll
-        for (int r = 0; r < 4; r++) {
-            const int n = state_n(i, 4 * g + r);
-            S[i][r] = init && n < p.dk ? init[static_cast<size_t>(n) * p.dv + pcol] : 0.0f;
-        }
+        for (int i = 0; i < N / 16; i++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const int n = state_n(i, 4 * g + r);
+                S[c][i][r] = init && n < p.dk ? init[static_cast<size_t>(n) * p.dv + pcol + 16 * c] : 0.0f;
+            }
     // LDS reads are issued together ahead of the products that take them (the fences keep the
     // compiler from sinking each to its use, where its whole latency would be waited for), and
     // products on one accumulator are kept four apart.
     //
-    // What needs no state: W x, and M x as y^T (rows: columns w0 + 4 g + r of x; column: t).
-    auto stateless = [&](const Buf& lds, const Decay& d, f4 (&acc)[4], typename MT::Frag (&wx)[2][P3]) {
-        typename MT::Frag xT[2], mf[2][P2][4];  // x^T: column w0 + lm
+    // What needs no state: W x, and M x as y^T (rows: columns w0 + 16 c + 4 g + r of x; column: t).
+    auto stateless = [&](const Buf& lds, const Decay& d, f4 (&acc)[CT][4], typename MT::Frag (&wx)[CT][2][P2]) {
+        const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
+        typename MT::Frag xT[CT][2], mf[2][P2][4];  // x^T: column w0 + 16 c + lm
         float wt[2][8];
 #pragma unroll
         for (int k = 0; k < 2; k++) {
-            xT[k] = MT::col8(lds.x, RX, 32 * k, w0, lane);
+#pragma unroll
+            for (int c = 0; c < CT; c++) xT[c][k] = MT::col8(lds.x, RX, 32 * k, w0 + 16 * c, ln);
             get8(d.w + 32 * k + 8 * g, wt[k]);
         }
         if constexpr (FULL) {
@@ -229,92 +256,110 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
 #pragma unroll
                 for (int k = 0; k < P2; k++)
 #pragma unroll
-                    for (int i = 2 * ks; i < 4; i++) mf[ks][k][i] = MT::row8(&lds.m[k][(16 * i + lm) * RM + 32 * ks + 8 * g]);
+                    for (int i = 2 * ks; i < 4; i++) mf[ks][k][i] = MT::row8(&shared.m[hh][k][(16 * i + lm) * RM + 32 * ks + 8 * g]);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < 4; i++) acc[i] = f4{};
+            for (int c = 0; c < CT; c++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) acc[c][i] = f4{};
 #pragma unroll
             for (int ks = 0; ks < 2; ks++)
 #pragma unroll
                 for (int k = 0; k < P2; k++)
 #pragma unroll
-                    for (int i = 2 * ks; i < 4; i++) acc[i] = MT::mma(xT[ks], mf[ks][k][i], acc[i]);
+                    for (int c = 0; c < CT; c++)
+#pragma unroll
+                        for (int i = 2 * ks; i < 4; i++) acc[c][i] = MT::mma(xT[c][ks], mf[ks][k][i], acc[c][i]);
         }
 #pragma unroll
-        for (int k = 0; k < 2; k++) {
-            float v[8];
-            MT::widen8(xT[k], v);
+        for (int c = 0; c < CT; c++)
 #pragma unroll
-            for (int j = 0; j < 8; j++) v[j] *= wt[k][j];
-            MT::template split<P3>(v, wx[k]);
-        }
+            for (int k = 0; k < 2; k++) {
+                float v[8];
+                MT::widen8(xT[c][k], v);
+#pragma unroll
+                for (int j = 0; j < 8; j++) v[j] *= wt[k][j];
+                MT::template split<P2>(v, wx[c][k]);
+            }
     };
     const int es = p.out_dtype == LA_BF16 ? 2 : 4;
     const int64_t ld_y = static_cast<int64_t>(p.H) * p.dv;
-    constexpr int AHEAD = sizeof(T) == 2 ? KS : 1;  // contraction steps whose c rows are read together
-    auto output = [&](int ch, const Buf& lds, const Decay& d, const f4 (&acc)[4]) {
-        f4 y4[4] = {};
+    constexpr int AHEAD = sizeof(T) == 2 ? KS / CT : 1;  // contraction steps whose c rows are read together
+    auto output = [&](int ch, const Buf& lds, const Decay& d, const f4 (&acc)[CT][4]) {
+        const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
+        f4 y4[CT][4] = {};
         float head[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) head[i] = d.head[16 * i + lm];
 #pragma unroll
-        for (int k0 = 0; k0 < KS; k0 += AHEAD) {
-            typename MT::Frag cf[AHEAD][4];
+        for (int k0 = 0; k0 < KS; k0 += AHEAD > 0 ? AHEAD : 1) {
+            constexpr int A1 = AHEAD > 0 ? AHEAD : 1;
+            typename MT::Frag cf[A1][4];
 #pragma unroll
-            for (int ks = 0; ks < AHEAD; ks++)
+            for (int ks = 0; ks < A1; ks++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) cf[ks][i] = MT::row8(lds.c + (16 * i + lm) * RB + 32 * (k0 + ks) + 8 * g);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int ks = 0; ks < AHEAD; ks++) {
-                const int i0 = 2 * (k0 + ks);
-                typename MT::Frag Sp[P2];
-                const float v[8] = {S[i0][0], S[i0][1], S[i0][2], S[i0][3], S[i0 + 1][0], S[i0 + 1][1], S[i0 + 1][2], S[i0 + 1][3]};
-                MT::template split<P2>(v, Sp);
+            for (int ks = 0; ks < A1; ks++)
 #pragma unroll
-                for (int k = 0; k < P2; k++)
+                for (int c = 0; c < CT; c++) {
+                    const f4 &a = S[c][2 * (k0 + ks)], &b = S[c][2 * (k0 + ks) + 1];
+                    typename MT::Frag Sp[P2];
+                    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                    MT::template split<P2>(v, Sp);
 #pragma unroll
-                    for (int i = 0; i < 4; i++) y4[i] = MT::mma(Sp[k], cf[ks][i], y4[i]);
-            }
+                    for (int k = 0; k < P2; k++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) y4[c][i] = MT::mma(Sp[k], cf[ks][i], y4[c][i]);
+                }
         }
         // rows behind the sequence lie behind the buffer's end
         const int live = sr.len - ch * kQ < kQ ? sr.len - ch * kQ : kQ;
-        char* row0 = static_cast<char*>(y) + ((sr.begin + ch * static_cast<int64_t>(kQ)) * ld_y + static_cast<int64_t>(h) * p.dv + tile * kPT) * es;
+        char* row0 = static_cast<char*>(y) + ((sr.begin + ch * static_cast<int64_t>(kQ)) * ld_y + static_cast<int64_t>(h) * p.dv + tile * COLS) * es;
         const __amdgpu_buffer_rsrc_t ry = make_rsrc(row0, static_cast<size_t>(live) * ld_y * es);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
+        for (int c = 0; c < CT; c++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) y4[i][r] = __builtin_fmaf(y4[i][r], head[i], acc[i][r]);
-            const int off = ((16 * i + lm) * static_cast<int>(ld_y) + w0 + 4 * g) * es;
-            if (es == 2)
-                __builtin_amdgcn_raw_buffer_store_b64(uv2{pack16(y4[i][0], y4[i][1]), pack16(y4[i][2], y4[i][3])}, ry, off, 0, 0);
-            else
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uv4, y4[i]), ry, off, 0, 0);
-        }
+            for (int i = 0; i < 4; i++) {
+                f4 v;
+#pragma unroll
+                for (int r = 0; r < 4; r++) v[r] = __builtin_fmaf(y4[c][i][r], head[i], acc[c][i][r]);
+                const int off = ((16 * i + lm) * static_cast<int>(ld_y) + w0 + 16 * c + 4 * g) * es;
+                if (es == 2)
+                    __builtin_amdgcn_raw_buffer_store_b64(uv2{pack16(v[0], v[1]), pack16(v[2], v[3])}, ry, off, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uv4, v), ry, off, 0, 0);
+            }
     };
-    auto update = [&](const Buf& lds, const Decay& d, const typename MT::Frag (&wx)[2][P3]) {  // S = total S + B^T (W x)
+    auto update = [&](const Buf& lds, const Decay& d, const typename MT::Frag (&wx)[CT][2][P2]) {  // S = total S + B^T (W x)
+        const int ln = opaque(lane);
         const float total = d.total[0];
 #pragma unroll
         for (int k = 0; k < 2; k++) {
             typename MT::Frag bf[N / 16];
 #pragma unroll
-            for (int i = 0; i < N / 16; i++) bf[i] = MT::col8_state(lds.b, RB, 32 * k, i, lane);
+            for (int i = 0; i < N / 16; i++) bf[i] = MT::col8_state(lds.b, RB, 32 * k, i, ln);
             __builtin_amdgcn_sched_barrier(0);
             if (k == 0) {
 #pragma unroll
-                for (int i = 0; i < N / 16; i++) S[i] *= total;
+                for (int c = 0; c < CT; c++)
+#pragma unroll
+                    for (int i = 0; i < N / 16; i++) S[c][i] *= total;
             }
 #pragma unroll
-            for (int q = 0; q < P3; q++)
+            for (int q = 0; q < P2; q++)
 #pragma unroll
-                for (int i = 0; i < N / 16; i++) S[i] = MT::mma(bf[i], wx[k][q], S[i]);
+                for (int c = 0; c < CT; c++)
+#pragma unroll
+                    for (int i = 0; i < N / 16; i++) S[c][i] = MT::mma(bf[i], wx[c][k][q], S[c][i]);
         }
     };
     if constexpr (NB == 2) {
         auto step = [&](int ch, const Buf& lds) {  // beside the staging of chunk ch + 1 and its M
-            const Decay& d = decays[(ch - c0 + 3) % 3];
-            typename MT::Frag wx[2][P3];
-            f4 acc[4];
+            const Decay& d = shared.d[(ch - c0 + 3) % 3][hh];
+            typename MT::Frag wx[CT][2][P2];
+            f4 acc[CT][4];
             if (ch >= c0) stateless(lds, d, acc, wx);
             if constexpr (FULL) {
                 __syncthreads();
@@ -329,9 +374,9 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
         }
     } else {
         for (int ch = c0; ch < c1; ch++) {
-            const Decay& d = decays[(ch - c0) % 3];
-            typename MT::Frag wx[2][P3];
-            f4 acc[4];
+            const Decay& d = shared.d[(ch - c0) % 3][hh];
+            typename MT::Frag wx[CT][2][P2];
+            f4 acc[CT][4];
             __syncthreads();
             if (FULL) __syncthreads();
             stateless(bufs[0], d, acc, wx);
@@ -342,15 +387,17 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
     }
     float* out = nullptr;
     if (FULL) out = c1 == nch && ST ? ST + unit : nullptr;
-    else out = local + ((static_cast<size_t>(bi) * nseg + seg) * p.H + h) * p.dk * p.dv;
+    else out = local + ((static_cast<size_t>(bi) * nseg + seg) * p.H + hw) * p.dk * p.dv;
     if (!out) return;
 #pragma unroll
-    for (int i = 0; i < N / 16; i++)
+    for (int c = 0; c < CT; c++)
 #pragma unroll
-        for (int r = 0; r < 4; r++) {
-            const int n = state_n(i, 4 * g + r);
-            if (n < p.dk) out[static_cast<size_t>(n) * p.dv + pcol] = S[i][r];
-        }
+        for (int i = 0; i < N / 16; i++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                const int n = state_n(i, 4 * g + r);
+                if (n < p.dk) out[static_cast<size_t>(n) * p.dv + pcol + 16 * c] = S[c][i][r];
+            }
 }
 
 // The state entering every segment from the segments' own states, in place.
@@ -375,27 +422,44 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanP p, const float* S0
     }
 }
 
-// Segments of a sequence: one while the heads alone fill the chip (two workgroups a CU), else
-// enough for that, of at least four chunks each: the first pass costs about half a full walk,
-// so a cut pays from two to three segments on.
-int segments(const la_scan_config& c) {
+// Columns a workgroup and segments of a sequence.
+struct Walk {
+    int tiles, heads;  // 64-column tiles, and the heads that they belong to
+    int nseg;
+};
+// Segments: one while the heads alone fill the chip, else enough for that, of at least four
+// chunks each: the first pass costs about half a full walk, so that a cut of one-tile walks pays
+// from three segments on.
+//
+// One tile a workgroup, or two (a head's 128 columns, or two heads of one group), where b, c and
+// their products serve both, but half as many workgroups walk.  Two pay where they still fill
+// the chip (2048 tokens, 16 sequences of 16 heads, d_v = 128: 172 -> 144 us) or where the walk is
+// cut into segments either way (32768 tokens, 16 heads of 128: 237 -> 197 us; 32 of 64: 230 ->
+// 197); not for 256 tiles, where one a workgroup fills the chip without a cut (4096 tokens, 8
+// sequences of 16 heads: 182 against 205 us in two segments).
+Walk walk_of(const la_scan_config& c) {
     const int64_t groups = static_cast<int64_t>(c.B) * c.H * (c.d_v / kPT);
     const int64_t chunks = (c.T + kQ - 1) / kQ;
-    if (groups == 0) return 1;
-    int64_t n = 512 / groups;
-    if (n > chunks / 4) n = chunks / 4;
-    return n < 3 ? 1 : static_cast<int>(n);
+    if (groups == 0) return {1, 1, 1};
+    auto cut = [&](int64_t most) { return most < chunks / 4 ? most : chunks / 4; };
+    int64_t n = cut(512 / groups);
+    if (n < 3) n = 1;
+    const int heads = c.d_v % 128 == 0 ? 1 : c.d_v == 64 && (c.H / c.G) % 2 == 0 ? 2 : 0;
+    if (c.x_dtype == LA_BF16 && heads && (groups >= 512 || (n > 1 && groups * n >= 256))) {
+        n = cut(256 / (groups / 2));
+        return {2, heads, n < 2 ? 1 : static_cast<int>(n)};
+    }
+    return {1, 1, static_cast<int>(n)};
 }
 
 size_t local_bytes(const la_scan_config& c, int nseg) {
     return static_cast<size_t>(c.B) * nseg * c.H * c.d_k * c.d_v * sizeof(float);
 }
 
-template <class T, int N>
-hipError_t launch(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
+template <class T, int N, int CT, int HEADS>
+hipError_t launch_walk(const la_scan_config& c, const ScanArgs& a, int nseg, hipStream_t s) {
     const ScanP p = scan_params(c, a);
-    const int nseg = segments(c);
-    const int64_t groups = static_cast<int64_t>(c.B) * c.H * (c.d_v / kPT);
+    const int64_t groups = static_cast<int64_t>(c.B) * c.H * (c.d_v / kPT) / CT;
     float* local = reinterpret_cast<float*>(a.ws);
     float* decay = reinterpret_cast<float*>(a.ws + (nseg > 1 ? local_bytes(c, nseg) : 0));
     auto allow = [](auto& kernel, size_t bytes) {
@@ -404,26 +468,35 @@ hipError_t launch(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
     };
     hipError_t e;
     if (nseg > 1) {
-        constexpr size_t bytes = kFwdLds<T, N, false>;
-        e = allow(scan_fwd_kernel<T, N, false>, bytes);
+        constexpr size_t bytes = sizeof(FwdShared<T, N, CT, HEADS, false>);
+        e = allow(scan_fwd_kernel<T, N, CT, HEADS, false>, bytes);
         if (e != hipSuccess) return e;
-        scan_fwd_kernel<T, N, false><<<dim3(static_cast<unsigned>(groups * (nseg - 1))), 512, bytes, s>>>(
+        scan_fwd_kernel<T, N, CT, HEADS, false><<<dim3(static_cast<unsigned>(groups * (nseg - 1))), 512, bytes, s>>>(
             p, nullptr, nullptr, nullptr, nullptr, local, decay, nseg, nseg - 1);
         const int64_t items = static_cast<int64_t>(c.B) * c.H * (c.d_k * c.d_v / 4);
         scan_join_kernel<<<dim3(static_cast<unsigned>((items + 255) / 256)), 256, 0, s>>>(p, a.S0, local, decay, nseg);
     }
-    constexpr size_t bytes = kFwdLds<T, N, true>;
-    e = allow(scan_fwd_kernel<T, N, true>, bytes);
+    constexpr size_t bytes = sizeof(FwdShared<T, N, CT, HEADS, true>);
+    e = allow(scan_fwd_kernel<T, N, CT, HEADS, true>, bytes);
     if (e != hipSuccess) return e;
-    scan_fwd_kernel<T, N, true><<<dim3(static_cast<unsigned>(groups * nseg)), 512, bytes, s>>>(
+    scan_fwd_kernel<T, N, CT, HEADS, true><<<dim3(static_cast<unsigned>(groups * nseg)), 512, bytes, s>>>(
         p, a.S0, local, a.y, a.ST, nullptr, nullptr, nseg, nseg);
     return hipGetLastError();
+}
+
+template <class T, int N>
+hipError_t launch(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
+    const Walk w = walk_of(c);
+    if constexpr (sizeof(T) == 2) {
+        if (w.tiles == 2) return w.heads == 2 ? launch_walk<T, N, 2, 2>(c, a, w.nseg, s) : launch_walk<T, N, 2, 1>(c, a, w.nseg, s);
+    }
+    return launch_walk<T, N, 1, 1>(c, a, w.nseg, s);
 }
 
 }  // namespace
 
 size_t scan_fwd_workspace(const la_scan_config& c) {
-    const int nseg = segments(c);
+    const int nseg = walk_of(c).nseg;
     return nseg > 1 ? local_bytes(c, nseg) + static_cast<size_t>(c.B) * nseg * c.H * sizeof(float) : 0;
 }
 

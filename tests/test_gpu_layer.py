@@ -373,6 +373,17 @@ def test_scan_of_many_short_sequences(H):
     Scan(BF, 200, cu[-1] + 300, H, 1, 16, 64, cu=cu).check()
 
 
+@pytest.mark.parametrize("B,T,H,G,N,P,more", [
+    (32, 70, 16, 1, 32, 64, {}), (33, 65, 16, 2, 128, 64, {}), (16, 66, 16, 1, 64, 128, {}), (18, 130, 15, 5, 16, 128, {}),
+    (1, 4096, 16, 2, 16, 64, {}), (2, 4130, 4, 1, 128, 128, dict(cu=[0, 4100, 4125])), (2, 4200, 8, 1, 64, 64, dict(cu=[0, 0, 4200])),
+    (1, 4097, 18, 2, 32, 64, {}),
+])
+def test_scan_two_tiles_a_workgroup(B, T, H, G, N, P, more):
+    """Many heads, or few cut into many segments: a workgroup takes 128 columns of a head or two heads
+    of 64 (the last one: an odd number of heads a group, one tile again)."""
+    Scan(BF, B, T, H, G, N, P, **more).check(backward=False)
+
+
 def test_scan_nan_step_reaches_its_own_head_from_its_token_on():
     s = Scan(BF, 1, 200, 2, 1, 64, 64)
     s.dt[70, 1] = float("nan")
