@@ -5,19 +5,19 @@
 //   waves 0..3   bring chunk i into LDS | form its M and the decays of chunk i + 1
 //   waves 4..7   (16 or 32 columns each) form M x and W x of chunk i - 1 | add the state's part,
 //                write the output and update the state
-// with two LDS buffers and the loads of chunk i + 2 issued at step i.  The operands formed in
-// FP32 (M, the state, W x) enter the products as two bf16 parts, 2^-17 of a value.  LDS and the
-// chain of reads, products and operand splits of waves 4..7 bound it, not memory: with d_k = 128
-// a chunk takes 2.7 us for 64 columns, 4.4 us for 128.  8 sequences of 4096 tokens, 16 heads,
-// d_v = 128: 180 us; 64 packed sequences, 40686 tokens in all: 265 us (334 with 64 columns a
-// workgroup).  Every wave doing every part in turn took 5.3 us a chunk of 64 columns; sixteen
-// waves in the same roles 5% more, and c's rows loaded from memory by waves 4..7 themselves 60%
-// more than this.
+// with two LDS buffers and the loads of chunk i + 2 issued at step i.  M and the state enter the
+// products as two bf16 parts (2^-17 of a value, for a bf16 result), W x as three (exact: with two
+// the states' error against 64 bits was seven times that of FP32 arithmetic, for a tenth of the
+// time).  LDS and the chain of reads, products and operand splits of waves 4..7 bound it, not
+// memory: with d_k = 128 a chunk takes 2.6 us for 64 columns, 4.7 us for 128.  8 sequences of
+// 4096 tokens, 16 heads, d_v = 128: 166 us; 64 packed sequences, 40686 tokens in all: 261 us.
+// Every wave doing every part in turn took 5.3 us a chunk of 64 columns; sixteen waves in the
+// same roles 5% more, and c's rows loaded from memory by waves 4..7 themselves 60% more than this.
 //
 // Few heads and long sequences: the walk is cut into segments that run side by side.  A first
 // pass forms each segment's own contribution to the state from zero, a small kernel joins them
 // (S_in of every segment), and the full walk starts every segment from its S_in (32768 tokens,
-// 32 heads of d_v = 64: 64 + 10 + 147 us).
+// 32 heads of d_v = 64: 75 + 10 + 155 us by the profiler, 216 us by the clock).
 #include "la_scan.hpp"
 
 namespace la {
@@ -48,7 +48,7 @@ template <class T, int N, int CT, int HEADS, bool FULL>
 __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0, const float* Sin, void* y, float* ST,
                                                        float* local, float* decay, int nseg, int segs) {
     using MT = Mat<T>;
-    constexpr int P2 = MT::template parts<2>;
+    constexpr int P2 = MT::template parts<2>, P3 = MT::template parts<3>;
     constexpr int COLS = kPT * CT;
     constexpr int RB = lds_row<T>(N), RX = CT == 2 ? lds_row<T>(128) : lds_row64<T>(), RM = lds_row64<T>();
     constexpr int KS = N / 32;  // contraction steps over the state's rows
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
     // products on one accumulator are kept four apart.
     //
     // What needs no state: W x, and M x as y^T (rows: columns w0 + 16 c + 4 g + r of x; column: t).
-    auto stateless = [&](const Buf& lds, const Decay& d, f4 (&acc)[CT][4], typename MT::Frag (&wx)[CT][2][P2]) {
+    auto stateless = [&](const Buf& lds, const Decay& d, f4 (&acc)[CT][4], typename MT::Frag (&wx)[CT][2][P3]) {
         const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
         typename MT::Frag xT[CT][2], mf[2][P2][4];  // x^T: column w0 + 16 c + lm
         float wt[2][8];
@@ -279,12 +279,13 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
                 MT::widen8(xT[c][k], v);
 #pragma unroll
                 for (int j = 0; j < 8; j++) v[j] *= wt[k][j];
-                MT::template split<P2>(v, wx[c][k]);
+                MT::template split<P3>(v, wx[c][k]);
             }
     };
     const int es = p.out_dtype == LA_BF16 ? 2 : 4;
     const int64_t ld_y = static_cast<int64_t>(p.H) * p.dv;
-    constexpr int AHEAD = sizeof(T) == 2 ? KS / CT : 1;  // contraction steps whose c rows are read together
+    // contraction steps whose c rows are read together (two tiles leave registers for one)
+    constexpr int AHEAD = sizeof(T) == 2 && CT == 1 ? KS : 1;
     auto output = [&](int ch, const Buf& lds, const Decay& d, const f4 (&acc)[CT][4]) {
         const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
         f4 y4[CT][4] = {};
@@ -292,16 +293,15 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
 #pragma unroll
         for (int i = 0; i < 4; i++) head[i] = d.head[16 * i + lm];
 #pragma unroll
-        for (int k0 = 0; k0 < KS; k0 += AHEAD > 0 ? AHEAD : 1) {
-            constexpr int A1 = AHEAD > 0 ? AHEAD : 1;
-            typename MT::Frag cf[A1][4];
+        for (int k0 = 0; k0 < KS; k0 += AHEAD) {
+            typename MT::Frag cf[AHEAD][4];
 #pragma unroll
-            for (int ks = 0; ks < A1; ks++)
+            for (int ks = 0; ks < AHEAD; ks++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) cf[ks][i] = MT::row8(lds.c + (16 * i + lm) * RB + 32 * (k0 + ks) + 8 * g);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int ks = 0; ks < A1; ks++)
+            for (int ks = 0; ks < AHEAD; ks++)
 #pragma unroll
                 for (int c = 0; c < CT; c++) {
                     const f4 &a = S[c][2 * (k0 + ks)], &b = S[c][2 * (k0 + ks) + 1];
@@ -332,7 +332,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uv4, v), ry, off, 0, 0);
             }
     };
-    auto update = [&](const Buf& lds, const Decay& d, const typename MT::Frag (&wx)[CT][2][P2]) {  // S = total S + B^T (W x)
+    auto update = [&](const Buf& lds, const Decay& d, const typename MT::Frag (&wx)[CT][2][P3]) {  // S = total S + B^T (W x)
         const int ln = opaque(lane);
         const float total = d.total[0];
 #pragma unroll
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
                     for (int i = 0; i < N / 16; i++) S[c][i] *= total;
             }
 #pragma unroll
-            for (int q = 0; q < P2; q++)
+            for (int q = 0; q < P3; q++)
 #pragma unroll
                 for (int c = 0; c < CT; c++)
 #pragma unroll
@@ -358,7 +358,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
     if constexpr (NB == 2) {
         auto step = [&](int ch, const Buf& lds) {  // beside the staging of chunk ch + 1 and its M
             const Decay& d = shared.d[(ch - c0 + 3) % 3][hh];
-            typename MT::Frag wx[CT][2][P2];
+            typename MT::Frag wx[CT][2][P3];
             f4 acc[CT][4];
             if (ch >= c0) stateless(lds, d, acc, wx);
             if constexpr (FULL) {
@@ -375,7 +375,7 @@ __global__ __launch_bounds__(512) void scan_fwd_kernel(ScanP p, const float* S0,
     } else {
         for (int ch = c0; ch < c1; ch++) {
             const Decay& d = shared.d[(ch - c0) % 3][hh];
-            typename MT::Frag wx[CT][2][P2];
+            typename MT::Frag wx[CT][2][P3];
             f4 acc[CT][4];
             __syncthreads();
             if (FULL) __syncthreads();
@@ -433,10 +433,10 @@ struct Walk {
 //
 // One tile a workgroup, or two (a head's 128 columns, or two heads of one group), where b, c and
 // their products serve both, but half as many workgroups walk.  Two pay where they still fill
-// the chip (2048 tokens, 16 sequences of 16 heads, d_v = 128: 172 -> 144 us) or where the walk is
-// cut into segments either way (32768 tokens, 16 heads of 128: 237 -> 197 us; 32 of 64: 230 ->
-// 197); not for 256 tiles, where one a workgroup fills the chip without a cut (4096 tokens, 8
-// sequences of 16 heads: 182 against 205 us in two segments).
+// the chip (2048 tokens, 16 sequences of 16 heads, d_v = 128: 177 -> 135 us; 40686 packed tokens:
+// 337 -> 261) or where the walk is cut into segments either way (32768 tokens, 16 heads of 128:
+// 243 -> 206 us; 32 of 64: 244 -> 216); not for 256 tiles, where one a workgroup fills the chip
+// without a cut (4096 tokens, 8 sequences of 16 heads: 166 against 202 us in two segments).
 Walk walk_of(const la_scan_config& c) {
     const int64_t groups = static_cast<int64_t>(c.B) * c.H * (c.d_v / kPT);
     const int64_t chunks = (c.T + kQ - 1) / kQ;
