@@ -6,9 +6,9 @@
 //   waves 4..7   (16 or 32 columns each) form M x and W x of chunk i - 1 | add the state's part,
 //                write the output and update the state
 // with two LDS buffers and the loads of chunk i + 2 issued at step i.  M and the state enter the
-// products as two bf16 parts (2^-17 of a value, for a bf16 result), W x as three (exact: with two
-// the states' error against 64 bits was seven times that of FP32 arithmetic, for a tenth of the
-// time).  LDS and the chain of reads, products and operand splits of waves 4..7 bound it, not
+// products as two bf16 parts (2^-17 of a value, for a bf16 result), W x as three (exact; two
+// cost a tenth of the time less, but the final states were then further from their 64-bit values
+// than FP32 arithmetic's).  LDS and the chain of reads, products and operand splits of waves 4..7 bound it, not
 // memory: with d_k = 128 a chunk takes 2.6 us for 64 columns, 4.7 us for 128.  8 sequences of
 // 4096 tokens, 16 heads, d_v = 128: 166 us; 64 packed sequences, 40686 tokens in all: 261 us.
 // Every wave doing every part in turn took 5.3 us a chunk of 64 columns; sixteen waves in the
