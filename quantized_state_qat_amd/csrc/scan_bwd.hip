@@ -223,11 +223,12 @@ __global__ __launch_bounds__(256) void walk_join_kernel(ScanP p, const float* S0
     if (last) reinterpret_cast<fv4*>(last)[bh * per + e] = S;
 }
 
-// What the decays' gradients of one chunk and head are formed from.
+// What the decays' gradients of one chunk and head are formed from, added up in double: an error
+// of <S, dS> reaches all 64 tokens alike (with FP32 sums dA and ddt_bias were up to 2.5 times as
+// far from their 64-bit values as FP32 arithmetic token by token; so up to 1.0; 1% of the time).
 struct RateSums {
-    float r[kQ], c[kQ], inner[kQ];  // r_t, c_t, and c_t's part from dS
-    float sd, dd;                   // <S, dS>, sum of dy x
-    float pad[2];
+    double r[kQ], c[kQ], inner[kQ];  // r_t, c_t, and c_t's part from dS
+    double sd, dd;                   // <S, dS>, sum of dy x
 };
 
 template <class T, int N>
@@ -245,7 +246,8 @@ struct GradLds {
     // partial sums of the decays' gradients, by parity of the iteration (they are joined beside the next)
     float rt[2][10][16], ct[2][10][16];          // the pair tiles' row and column sums
     float ri[2][N / 16][kQ], ci[2][N / 16][kQ];  // sums over 16 state rows
-    float sd[2][8], dd[2][8];                    // the waves' <S, dS> and diagonals of dM
+    double sd[2][8];                             // the waves' <S, dS>
+    float dd[2][8];                              // and diagonals of dM
 };
 
 __device__ __forceinline__ void lower_tile_of(int k, int& ti, int& si) {
@@ -356,7 +358,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
     f4 dC[TI] = {}, dB[TI] = {};  // rows n, columns t (s)
 
     // kJoin: iteration it's partial sums, added up over a head's tiles; lane = token
-    float racc = 0.0f, cacc = 0.0f, iacc = 0.0f, sdacc = 0.0f, ddacc = 0.0f;
+    double racc = 0.0, cacc = 0.0, iacc = 0.0, sdacc = 0.0, ddacc = 0.0;
     auto join = [&](int it) {
         const int par = it & 1;
         const int tq = lane >> 4, tl = lane & 15;
@@ -366,7 +368,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
             racc += q <= tq ? rt : 0.0f;
             cacc += q >= tq ? ct : 0.0f;
         }
-        float inner = 0.0f;
+        double inner = 0.0;
 #pragma unroll 2
         for (int q = 0; q < NTL; q++) {  // (unrolled whole, its registers would spill others)
             racc += lds.ri[par][q][lane];
@@ -383,12 +385,12 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         o.r[lane] = racc;
         o.c[lane] = cacc;
         o.inner[lane] = iacc;
-        const float sd = group_sum<8>(sdacc), dd = group_sum<8>(ddacc);
+        const double sd = wave_last(wave_prefix(lane < 8 ? sdacc : 0.0)), dd = wave_last(wave_prefix(lane < 8 ? ddacc : 0.0));
         if (lane == 0) {
             o.sd = sd;
             o.dd = dd;
         }
-        racc = cacc = iacc = sdacc = ddacc = 0.0f;
+        racc = cacc = iacc = sdacc = ddacc = 0.0;
     };
 
     for (int it = 0; it < iters; it++) {
@@ -404,13 +406,13 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         ty.store(lds.dy, RX);
         td.store(lds.d);
         typename MT::Frag Sf[2][P3], dSf[2][P3];
-        float sd = 0.0f;
+        double sd = 0.0;
         {
         const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
 #pragma unroll
         for (int k = 0; k < 2; k++) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) sd = __builtin_fmaf(Sr[k][j], dSr[k][j], sd);
+            for (int j = 0; j < 8; j++) sd = __builtin_fma(static_cast<double>(Sr[k][j]), static_cast<double>(dSr[k][j]), sd);
             MT::template split<P3>(Sr[k], Sf[k]);
             MT::template split<P3>(dSr[k], dSf[k]);
             if constexpr (sizeof(T) == 2) {
@@ -421,7 +423,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                 }
             }
         }
-        sd = part == 0 ? wave_sum(sd) : 0.0f;
+        sd = part == 0 ? wave_last(wave_prefix(sd)) : 0.0;
         if (lane == 0) lds.sd[par][wave] = sd;
         }
         __syncthreads();
@@ -705,9 +707,9 @@ __global__ __launch_bounds__(256) void rates_kernel(ScanP p, const Decay* decays
     const int ch = at.ch, live = sr.len - ch * kQ;
     const Decay& d = decays[slot * p.H + h];
     const RateSums& m = sums[slot * p.H + h];
-    const float delta = d.delta[lane], c = m.c[lane];
-    double v = static_cast<double>(m.r[lane]) - static_cast<double>(delta) * c;
-    const float into = wave_sum(delta * m.inner[lane]);
+    const double delta = d.delta[lane], c = m.c[lane];
+    double v = m.r[lane] - delta * c;
+    const double into = wave_last(wave_prefix(delta * m.inner[lane]));
     if (lane == 63) v += static_cast<double>(d.total[0]) * m.sd + into;
     const double pre = wave_prefix(v);
     const double rate = wave_last(pre) - pre + v;  // the log decay's gradient
@@ -718,7 +720,7 @@ __global__ __launch_bounds__(256) void rates_kernel(ScanP p, const Decay* decays
     const float db = wave_sum(dz);
     if (lane == 0) {
         o[0] = da;
-        o[p.H] = m.dd;
+        o[p.H] = static_cast<float>(m.dd);
         o[2 * p.H] = db;
     }
 }
