@@ -217,12 +217,24 @@ __global__ __launch_bounds__(256) void walk_join_kernel(ScanP p, const float* S0
     const int nch = (sr.len + kQ - 1) / kQ;
     fv4 S = {};
     if (first) S = reinterpret_cast<const fv4*>(first)[bh * per + e];
-    for (int k = 0; k < nch; k++) {
-        const int64_t at = slot_of(p, bi, sr.begin, rev ? nch - 1 - k : k) * p.H + h;
-        fv4* l = reinterpret_cast<fv4*>(states) + at * per + e;
-        const fv4 own = *l;
-        *l = S;
-        S = S * decays[at].total[0] + own;
+    for (int k0 = 0; k0 < nch; k0 += 8) {  // eight chunks' loads in flight: only the sums are a chain
+        fv4 own[8];
+        float total[8];
+        fv4* l[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int k = k0 + j < nch ? k0 + j : nch - 1;
+            const int64_t at = slot_of(p, bi, sr.begin, rev ? nch - 1 - k : k) * p.H + h;
+            l[j] = reinterpret_cast<fv4*>(states) + at * per + e;
+            own[j] = *l[j];
+            total[j] = decays[at].total[0];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            if (k0 + j >= nch) break;
+            *l[j] = S;
+            S = S * total[j] + own[j];
+        }
     }
     if (last) reinterpret_cast<fv4*>(last)[bh * per + e] = S;
 }

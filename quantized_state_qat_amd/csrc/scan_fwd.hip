@@ -412,13 +412,26 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanP p, const float* S0
     const int cps = (nch + nseg - 1) / nseg;
     fv4 S = {};
     if (S0) S = reinterpret_cast<const fv4*>(S0)[bh * per + e];
-    for (int s = 0; s < nseg && s * cps < nch; s++) {
-        const size_t at = (static_cast<size_t>(bi) * nseg + s) * p.H + h;
-        fv4* l = reinterpret_cast<fv4*>(local) + at * per + e;
-        const bool more = (s + 1) * cps < nch;  // the last segment's own state is not formed
-        const fv4 own = more ? *l : fv4{};
-        *l = S;
-        if (more) S = S * decay[at] + own;
+    const int used = cps > 0 ? (nch + cps - 1) / cps : 0;  // the last segment's own state is not formed
+    for (int s0 = 0; s0 < used; s0 += 8) {                 // eight segments' loads in flight
+        fv4 own[8];
+        float dec[8];
+        fv4* l[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int s = s0 + j < used ? s0 + j : used - 1;
+            const size_t at = (static_cast<size_t>(bi) * nseg + s) * p.H + h;
+            l[j] = reinterpret_cast<fv4*>(local) + at * per + e;
+            const bool more = s + 1 < used;
+            own[j] = more ? *l[j] : fv4{};
+            dec[j] = more ? decay[at] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            if (s0 + j >= used) break;
+            *l[j] = S;
+            S = S * dec[j] + own[j];
+        }
     }
 }
 
