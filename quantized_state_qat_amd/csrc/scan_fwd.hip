@@ -440,9 +440,12 @@ struct Walk {
     int tiles, heads;  // 64-column tiles, and the heads that they belong to
     int nseg;
 };
-// Segments: one while the heads alone fill the chip, else enough for that, of at least four
-// chunks each: the first pass costs about half a full walk, so that a cut of one-tile walks pays
-// from three segments on.
+// Segments: one while the heads alone fill the chip, else enough for that: the first pass costs
+// about half a full walk, so that a cut of one-tile walks pays from three segments on.  A segment
+// has two chunks at least, or three of bf16 where there are few (whose walk costs little more
+// than the join: 1024 tokens, 16 heads of 128: 35-36 us with 3 or 4, 37 with 2; 700 tokens, 4
+// heads: 29 with 3, 31 with 2, 36 with 4; but 2048 tokens: 45 with 2, 48 with 4, and 1000 FP32
+// tokens, 8 heads: 31 against 39).
 //
 // One tile a workgroup, or two (a head's 128 columns, or two heads of one group), where b, c and
 // their products serve both, but half as many workgroups walk.  Two pay where they still fill
@@ -454,7 +457,8 @@ Walk walk_of(const la_scan_config& c) {
     const int64_t groups = static_cast<int64_t>(c.B) * c.H * (c.d_v / kPT);
     const int64_t chunks = (c.T + kQ - 1) / kQ;
     if (groups == 0) return {1, 1, 1};
-    auto cut = [&](int64_t most) { return most < chunks / 4 ? most : chunks / 4; };
+    const int least = c.x_dtype == LA_F32 || chunks >= 32 ? 2 : 3;
+    auto cut = [&](int64_t most) { return most < chunks / least ? most : chunks / least; };
     int64_t n = cut(512 / groups);
     if (n < 3) n = 1;
     const int heads = c.d_v % 128 == 0 ? 1 : c.d_v == 64 && (c.H / c.G) % 2 == 0 ? 2 : 0;
