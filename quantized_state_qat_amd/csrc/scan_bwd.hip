@@ -239,9 +239,10 @@ __global__ __launch_bounds__(256) void walk_join_kernel(ScanP p, const float* S0
     if (last) reinterpret_cast<fv4*>(last)[bh * per + e] = S;
 }
 
-// What the decays' gradients of one chunk and head are formed from, added up in double: an error
-// of <S, dS> reaches all 64 tokens alike (with FP32 sums dA and ddt_bias were up to 2.5 times as
-// far from their 64-bit values as FP32 arithmetic token by token; so up to 1.0; 1% of the time).
+// What the decays' gradients of one chunk and head are formed from: FP32 sums over a wave's part of
+// a row or column, joined in double (joined in FP32, dA and ddt_bias were up to 2.5 times as far
+// from their 64-bit values as the formulas in FP32 tensor operations; so up to 1.0, for 0.6% of
+// the time).
 struct RateSums {
     double r[kQ], c[kQ], inner[kQ];  // r_t, c_t, and c_t's part from dS
     double sd, dd;                   // <S, dS>, sum of dy x
@@ -262,8 +263,7 @@ struct GradLds {
     // partial sums of the decays' gradients, by parity of the iteration (they are joined beside the next)
     float rt[2][10][16], ct[2][10][16];          // the pair tiles' row and column sums
     float ri[2][N / 16][kQ], ci[2][N / 16][kQ];  // sums over 16 state rows
-    double sd[2][8];                             // the waves' <S, dS>
-    float dd[2][8];                              // and diagonals of dM
+    float sd[2][8], dd[2][8];                    // the waves' <S, dS> and diagonals of dM
 };
 
 __device__ __forceinline__ void lower_tile_of(int k, int& ti, int& si) {
@@ -423,13 +423,13 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         ty.store(lds.dy, RX);
         td.store(lds.d);
         typename MT::Frag Sf[2][P3], dSf[2][P3];
-        double sd = 0.0;
+        float sd = 0.0f;
         {
         const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
 #pragma unroll
         for (int k = 0; k < 2; k++) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) sd = __builtin_fma(static_cast<double>(Sr[k][j]), static_cast<double>(dSr[k][j]), sd);
+            for (int j = 0; j < 8; j++) sd = __builtin_fmaf(Sr[k][j], dSr[k][j], sd);
             MT::template split<P3>(Sr[k], Sf[k]);
             MT::template split<P3>(dSr[k], dSf[k]);
             if constexpr (sizeof(T) == 2) {
@@ -440,7 +440,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                 }
             }
         }
-        sd = part == 0 ? wave_last(wave_prefix(sd)) : 0.0;
+        sd = part == 0 ? wave_sum(sd) : 0.0f;
         if (lane == 0) lds.sd[par][wave] = sd;
         }
         __syncthreads();
