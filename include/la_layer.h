@@ -15,8 +15,8 @@
  * Packed sequences.  cu_seqlens == NULL: B sequences of T tokens, tensors [B][T][...].
  * Otherwise int32 [B + 1] in device memory, non-decreasing from 0 to at most T: sequence b is
  * tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of tensors [T][...], cfg->T the packed length.
- * Boundaries are clamped to [0, T] on the device; a sequence whose boundaries are out of order
- * is empty, and overlapping sequences are a caller error.  Tokens outside every sequence: their
+ * Boundaries are clamped to [0, T] on the device; decreasing ones are a caller error (results
+ * are then unspecified, nothing outside the tensors is touched).  Tokens outside every sequence: their
  * rows of forward outputs are left as they were, their gradients are zero.
  *
  * Row strides.  ld_* is the distance in elements between a tensor's rows of consecutive

@@ -384,6 +384,27 @@ def test_scan_two_tiles_a_workgroup(B, T, H, G, N, P, more):
     Scan(BF, B, T, H, G, N, P, **more).check(backward=False)
 
 
+@pytest.mark.parametrize("dtt,H", [(BF, 3), (BF, 4), (F32, 3)])
+def test_scan_steps_in_wider_rows(dtt, H):
+    """dt and ddt as the first columns of rows of 7 (bf16: rows that start in the middle of a word)."""
+    class Wide(Scan):
+        def __init__(self, *a, **k):
+            super().__init__(*a, **k)
+            wide = torch.full((self.tokens, 7), float("nan"), dtype=self.dtt, device="cuda")
+            wide[:, :H] = self.dt
+            self.dt, self.cfg.ld_dt = wide[:, :H], 7
+
+        def out_buffers(self):
+            buf, o = super().out_buffers()
+            self.wide = torch.full((self.tokens, 7), 9.0, dtype=self.dtt, device="cuda")
+            o["ddt"] = self.wide[:, :H]
+            return buf, o
+
+    s = Wide(BF, 2, 131, H, 1, 32, 64, dtt=dtt)
+    s.check()
+    assert (s.wide[:, H:] == 9).all()
+
+
 def test_scan_nan_step_reaches_its_own_head_from_its_token_on():
     s = Scan(BF, 1, 200, 2, 1, 64, 64)
     s.dt[70, 1] = float("nan")
@@ -468,6 +489,29 @@ def test_scan_step(B, H, G, N, P, dtype):
         pool2[1] = before[0]
         la.la_scan_step(cfg, x, dt, A, b, c, D, bias, pool2, y, slots=one, n_slots=B + 3)
         assert torch.equal(y2[0], y[0]) and torch.equal(pool2[1], st[0])
+
+
+@pytest.mark.parametrize("given,means", [([-5, 60, 400], [0, 60, 150]), ([0, 200, 300], [0, 150, 150])])
+def test_boundaries_are_clamped(given, means):
+    """Boundaries outside the packing are moved to its ends."""
+    T = 150
+    g = gen(3)
+    x, w, dy = draw(g, T, 64), draw(g, 64, 4, dtype=F32), draw(g, T, 64)
+    cc = la.ConvConfig(B=2, T=T, C=64, width=4)
+    s = Scan(BF, 2, T, 2, 1, 32, 64, cu=given)
+    results = []
+    for cu in (given, means):
+        y = torch.full_like(x, 5.0)
+        sT = torch.empty(2, 3, 64, dtype=BF, device="cuda")
+        dx, dw = torch.full_like(x, 5.0), torch.empty(64, 4, device="cuda")
+        n = la.la_conv_bwd_workspace_bytes(cc)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        la.la_conv_fwd(cc, x, w, None, None, y, sT, cu_seqlens=cu_tensor(cu))
+        la.la_conv_bwd(cc, x, w, None, None, dy, None, dx, dw, None, None, ws, n, cu_seqlens=cu_tensor(cu))
+        s.cu = cu
+        results.append([y, sT, dx, dw, *s.fwd(), *(t.clone() for t in s.bwd().values())])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
 
 
 # -------------------------------------------------------------------------------------- norm
