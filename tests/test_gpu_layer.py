@@ -759,3 +759,119 @@ def test_binding_refuses_layouts():
     la.la_conv_fwd(la.ConvConfig(B=2, T=8, C=64, width=4, ld_x=96), wide[..., 8:72], w, None, None, y)
     with pytest.raises(ValueError, match="GPU"):
         la.la_conv_fwd(cfg, x, w.cpu(), None, None, y)
+
+
+# ----------------------------------------------------------------------- offsets past 32 bits
+def zeros(*shape, dtype=BF):
+    return torch.zeros(*shape, dtype=dtype, device="cuda")
+
+
+def test_convolution_and_norm_past_32_bits():
+    """The last rows of tensors of more than 2^31 elements, the rest zeros: bit for bit what the
+    rows alone give."""
+    g = gen(11)
+    T, C, n = 935000, 2304, 200
+    assert T * C > 1 << 31
+    x, w = zeros(T, C), draw(g, C, 4, dtype=F32)
+    x[-n:] = draw(g, n, C)
+    y, sT = zeros(T, C), zeros(1, 3, C)
+    la.la_conv_fwd(la.ConvConfig(B=1, T=T, C=C, width=4), x, w, None, None, y, sT)
+    tail, small = x[-n:].clone(), la.ConvConfig(B=1, T=n, C=C, width=4)
+    yn, sn = zeros(n, C), zeros(1, 3, C)
+    la.la_conv_fwd(small, tail, w, None, None, yn, sn)
+    assert torch.equal(y[-n:], yn) and torch.equal(sT, sn)
+    dxs, dws = [], []
+    for cfg, xs in ((la.ConvConfig(B=1, T=T, C=C, width=4), x), (small, tail)):
+        b = la.la_conv_bwd_workspace_bytes(cfg)
+        ws = torch.empty(b, dtype=torch.uint8, device="cuda")
+        dx, dw = torch.empty_like(xs), zeros(C, 4, dtype=F32)
+        la.la_conv_bwd(cfg, xs, w, None, None, xs, None, dx, dw, None, None, ws, b)  # dy = x
+        dxs.append(dx[-n:].clone())
+        dws.append(dw)
+        del dx
+    assert torch.equal(*dxs)
+    # the weights' sums take other orders: each an FP32 sum of at most 200 nonzero terms
+    big = (tail.float().abs().amax(0) ** 2 * 1.1 * n * 2.0 ** -24 * n)[:, None]
+    assert ((dws[0] - dws[1]).abs() <= big).all()
+    del x, y
+    rows, d = 263000, 8192
+    assert rows * d > 1 << 31
+    x = zeros(rows, d)
+    x[-3:] = draw(g, 3, d)
+    y, codes, scales = zeros(rows, d), zeros(rows, d, dtype=torch.uint8), zeros(rows, d // 64, dtype=F32)
+    cfg = la.NormConfig(rows=rows, d=d, eps=1e-6, qdq=la.LA_QDQ_INT8_GROUP, group=64)
+    la.la_norm_fwd(cfg, x, None, None, x, y, codes, scales)
+    cfg.rows = 3
+    t, yt, ct, st = x[-3:].clone(), zeros(3, d), zeros(3, d, dtype=torch.uint8), zeros(3, d // 64, dtype=F32)
+    la.la_norm_fwd(cfg, t, None, None, t, yt, ct, st)
+    assert torch.equal(y[-3:], yt) and torch.equal(codes[-3:], ct) and torch.equal(scales[-3:], st)
+    assert not codes[0].any() and (scales[0] == 1).all()
+    cfg = la.NormConfig(rows=rows, d=d, eps=1e-6)
+    dx = torch.empty_like(x)
+    la.la_norm_bwd(cfg, x, None, y, None, dx, None, None, 0)
+    cfg.rows = 3
+    dt = torch.empty_like(t)
+    la.la_norm_bwd(cfg, t, None, yt, None, dt, None, None, 0)
+    assert torch.equal(dx[-3:], dt) and not dx[0].any()
+
+
+def test_scan_past_32_bits():
+    """A packing of more than 2^31 elements whose last sequence begins behind them."""
+    s = Scan(BF, 1, 200, 16, 1, 16, 128, states=False)
+    T = (1 << 31) // (s.H * s.P) + 300
+    def wide(t):  # noqa: E306
+        big = zeros(T, t.shape[1], dtype=t.dtype)
+        big[-200:] = t
+        return big
+    buf, dt, dy = wide(s.buf), wide(s.dt), wide(s.dy)
+    x, b, c = s.cut(buf)
+    cfg = la.ScanConfig(B=2, T=T, H=s.H, G=s.G, d_k=s.N, d_v=s.P, softplus=1, ld_x=s.ld, ld_b=s.ld, ld_c=s.ld)
+    cu = cu_tensor([0, T - 200, T])
+    n = max(la.la_scan_workspace_bytes(cfg), la.la_scan_bwd_varlen_workspace_bytes(cfg))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    y, ST = zeros(T, s.H * s.P), torch.empty(2, s.H, s.N, s.P, device="cuda")
+    la.la_scan_fwd(cfg, x, dt, s.A, b, c, s.D, s.bias, None, y, ST, ws, n, cu_seqlens=cu)
+    dbuf = torch.empty_like(buf)
+    dx, db, dc = s.cut(dbuf)
+    o = dict(ddt=torch.empty_like(dt), dA=zeros(s.H, dtype=F32), dD=zeros(s.H, dtype=F32), ddt_bias=zeros(s.H, dtype=F32))
+    la.la_scan_bwd(cfg, x, dt, s.A, b, c, s.D, s.bias, None, dy, None, dx, o["ddt"], o["dA"], db, dc, o["dD"], o["ddt_bias"],
+                   None, ws, n, cu_seqlens=cu)
+    w, m = s.reference(True)
+    share, once = 2.0 ** -14, 2.0 ** -8
+    close(y[-200:].reshape(w["y"].shape), w["y"], m["y"], share, "y")
+    close(ST[1:], w["S_T"], m["S_T"], share, "S_T")
+    for k, t in dict(dx=dx, db=db, dc=dc).items():
+        close(t[-200:].reshape(w[k].shape), w[k], m[k], share + once, k)
+    close(o["ddt"][-200:], w["ddt"], m["ddt"], share, "ddt")
+    for k in ("dA", "dD", "ddt_bias"):
+        close(o[k], w[k], m[k], share, k)
+    assert not y[0].any() and not ST[0].any() and not dx[0].any() and not o["ddt"][0].any()
+
+
+def test_state_pools_past_32_bits():
+    """A live slot behind 2^32 bytes (and 2^31 elements) of a pool."""
+    g = gen(12)
+    H, N, P, n = 8, 64, 64, 66000
+    assert (n - 1) * H * N * P > 1 << 31
+    x, dt, b, c = draw(g, 1, H * P), draw(g, 1, H), draw(g, 1, N), draw(g, 1, N)
+    A, S = -torch.rand(H, generator=g).cuda(), draw(g, 1, H, N, P, dtype=F32)
+    cfg = la.ScanConfig(B=1, T=1, H=H, G=1, d_k=N, d_v=P, softplus=1)
+    pool = zeros(n, H, N, P, dtype=F32)
+    pool[n - 1] = S[0]
+    y, yp = zeros(1, H * P), zeros(1, H * P)
+    slot = torch.tensor([n - 1], dtype=torch.int32, device="cuda")
+    la.la_scan_step(cfg, x, dt, A, b, c, None, None, pool, yp, slots=slot, n_slots=n)
+    la.la_scan_step(cfg, x, dt, A, b, c, None, None, S, y)
+    assert y.any() and torch.equal(y, yp) and torch.equal(pool[n - 1], S[0]) and not pool[:2].any()
+    del pool
+    C, W, n = 8192, 4, 90000
+    assert (n - 1) * (W - 1) * C > 1 << 31
+    x, w, st = draw(g, 1, C), draw(g, C, W, dtype=F32), draw(g, 1, W - 1, C)
+    cfg = la.ConvConfig(B=1, T=1, C=C, width=W)
+    pool = zeros(n, W - 1, C)
+    pool[n - 1] = st[0]
+    y, yp = zeros(1, C), zeros(1, C)
+    slot[0] = n - 1
+    la.la_conv_step(cfg, x, w, None, pool, yp, slots=slot, n_slots=n)
+    la.la_conv_step(cfg, x, w, None, st, y)
+    assert y.any() and torch.equal(y, yp) and torch.equal(pool[n - 1], st[0]) and not pool[:2].any()
