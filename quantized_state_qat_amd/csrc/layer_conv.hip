@@ -119,17 +119,18 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvGeom<T> g, const T* _
     Taps<E, W> taps;
     taps.load(w, bias, g.w_dtype, c0);
 
-    auto walk = [&](int64_t begin, int b, int p0, int p1) {  // positions p0 .. p1 - 1 of sequence b
+    uv4 rows[8];
+    auto fetch = [&](int64_t first, int n) {  // rows first .. first + n - 1 (up to eight)
+#pragma unroll
+        for (int k = 0; k < 8; k++) rows[k] = load16(x + (first + (k < n ? k : n - 1)) * g.ldx + c0);
+    };
+    // positions p0 .. p1 - 1 of sequence b, the first eight rows already fetched
+    auto walk = [&](int64_t begin, int b, int p0, int p1) {
         float win[W][E];  // rows p - (W - 1) .. p
 #pragma unroll
         for (int k = 0; k < W - 1; k++) widen(conv_row<T, W>(x, s0, begin, p0 - (W - 1) + k, b, g.C, g.ldx, c0), win[k + 1]);
         for (int p = p0; p < p1; p += 8) {
-            uv4 rows[8];
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const int q = p + k < p1 ? p + k : p1 - 1;
-                rows[k] = load16(x + (begin + q) * g.ldx + c0);
-            }
+            if (p > p0) fetch(begin + p, p1 - p);
 #pragma unroll
             for (int k = 0; k < 8; k++) {
                 if (p + k >= p1) break;
@@ -154,12 +155,14 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvGeom<T> g, const T* _
         const int b = static_cast<int>(tb / g.blocks);
         const int p0 = static_cast<int>(tb % g.blocks) * g.per;
         const int p1 = p0 + g.per < g.T_ ? p0 + g.per : g.T_;
+        fetch(static_cast<int64_t>(b) * g.T_ + p0, p1 - p0);
         walk(static_cast<int64_t>(b) * g.T_, b, p0, p1);
         return;
     }
     int t = static_cast<int>(tb) * g.per;
     const int t1 = g.T_ - t < g.per ? g.T_ : t + g.per;
-    while (t < t1) {
+    fetch(t, t1 - t);  // in flight behind the search for their sequence
+    for (const int t0 = t; t < t1;) {
         const int b = packed_find(g.cu, g.B, t);
         const Span sp = packed_span(g.cu, b, g.T_);
         if (t < sp.begin || t >= sp.end) {  // outside every sequence
@@ -167,6 +170,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvGeom<T> g, const T* _
             continue;
         }
         const int stop = t1 < sp.end ? t1 : sp.end;
+        if (t > t0) fetch(t, stop - t);
         walk(sp.begin, b, t - sp.begin, stop - sp.begin);
         t = stop;
     }
