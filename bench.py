@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import argparse
 import dataclasses
+import gc
 import hashlib
 import json
 import os
@@ -97,6 +98,7 @@ def bench_decode(steps, warmup, setup=None):
         la.la_decode_step(c, dev["q"], dev["k"], dev["v"], dev["g"], dev["beta"], states[i % 3], o,
                           stream=stream)
 
+    gc.collect()  # a collection among the timed launches would leave the GPU idle for 20 to 40 ms
     for i in range(warmup):
         step(i)
     torch.cuda.synchronize()
