@@ -119,7 +119,9 @@ size_t la_scan_workspace_bytes(const la_scan_config* cfg);
  * NULL).  db and dc are summed over the group's heads.  out_dtype must equal x_dtype.  A call
  * takes below 2^23 heads of 64-token chunks.  Workspace (the state and its gradient at every
  * 64th token, and more): at least la_scan_bwd_workspace_bytes(cfg) bytes; for packed sequences
- * la_scan_bwd_varlen_workspace_bytes(cfg), up to B times less, is enough. */
+ * la_scan_bwd_varlen_workspace_bytes(cfg), up to B times less, is enough.  A query returns 0 where
+ * the call itself would be refused: the first goes by B sequences of T tokens, the second by a
+ * packing of T tokens. */
 la_status la_scan_bwd(const la_scan_config* cfg, const int32_t* cu_seqlens, const void* x, const void* dt,
                       const float* A, const void* b, const void* c, const float* D, const float* dt_bias,
                       const float* S0, const void* dy, const float* dS_T, void* dx, void* ddt, float* dA, void* db,

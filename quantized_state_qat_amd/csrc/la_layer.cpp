@@ -127,6 +127,16 @@ la_status check_scan_bwd(const la_scan_config* c, bool packed) {
     return LA_OK;
 }
 
+// The bytes that la_scan_bwd asks for, of a config that passed the layout's check.  A dense call's
+// suffice for a packing too, where a packing of the config is taken at all: one of few or short
+// sequences has more chunk slots than they have chunks.
+size_t scan_bwd_need(const la_scan_config& c, bool packed) {
+    const size_t need = la::scan_bwd_workspace(c, packed);
+    if (packed || la::scan_bwd_slots(c, true) * c.H >= la::kMaxUnits) return need;
+    const size_t other = la::scan_bwd_workspace(c, true);
+    return need > other ? need : other;
+}
+
 la_status check_scan_inputs(const void* x, const void* dt, const float* A, const void* b, const void* c, const float* D,
                             const float* bias, bool work) {
     CHECK(check_ptr(x, "x", work));
@@ -255,15 +265,14 @@ la_status la_scan_fwd(const la_scan_config* cfg, const int32_t* cu_seqlens, cons
     return done(la::launch_scan_fwd(*cfg, a, static_cast<hipStream_t>(stream)), "la_scan_fwd launch");
 }
 
-size_t la_scan_bwd_workspace_bytes(const la_scan_config* cfg) {  // enough for either layout
-    if (check_scan_bwd(cfg, true) != LA_OK || check_scan_bwd(cfg, false) != LA_OK) return 0;
-    const size_t dense = la::scan_bwd_workspace(*cfg, false), packed = la::scan_bwd_workspace(*cfg, true);
-    return dense > packed ? dense : packed;
+size_t la_scan_bwd_workspace_bytes(const la_scan_config* cfg) {
+    if (check_scan_bwd(cfg, false) != LA_OK) return 0;
+    return scan_bwd_need(*cfg, false);
 }
 
 size_t la_scan_bwd_varlen_workspace_bytes(const la_scan_config* cfg) {
     if (check_scan_bwd(cfg, true) != LA_OK) return 0;
-    return la::scan_bwd_workspace(*cfg, true);
+    return scan_bwd_need(*cfg, true);
 }
 
 la_status la_scan_bwd(const la_scan_config* cfg, const int32_t* cu_seqlens, const void* x, const void* dt,
@@ -290,8 +299,7 @@ la_status la_scan_bwd(const la_scan_config* cfg, const int32_t* cu_seqlens, cons
     CHECK(check_ptr(ddt_bias, "ddt_bias", false));
     CHECK(check_ptr(dS0, "dS0", false));
     if (dS0 && dS0 == dS_T) return fail(LA_ERR_INVALID_ARG, "dS0 must not be dS_T");
-    CHECK(check_workspace(workspace, ws_bytes, cu_seqlens ? la_scan_bwd_varlen_workspace_bytes(cfg)
-                                                          : la_scan_bwd_workspace_bytes(cfg)));
+    CHECK(check_workspace(workspace, ws_bytes, scan_bwd_need(*cfg, cu_seqlens != nullptr)));
     if (cfg->H == 0) return ok();
     la::ScanArgs a;
     a.cu = cu_seqlens, a.x = x, a.dt = dt, a.A = A, a.b = b, a.c = c, a.D = D, a.bias = dt_bias, a.S0 = S0, a.dy = dy;

@@ -142,6 +142,19 @@ def test_backward_refuses_what_its_grids_cannot_hold():
         assert la.la_scan_bwd_workspace_bytes(scan(**kw)) == 0
 
 
+@pytest.mark.parametrize("kw", [dict(B=128, T=1, H=65535), dict(B=1, T=64 * 65535, H=128), dict(B=65535, T=1, H=128)])
+def test_backward_needs_its_workspace_where_only_the_dense_layout_fits(kw):
+    """B sequences of T tokens just below the limit on chunks, which a packing of them would pass."""
+    cfg = scan(G=1, d_k=16, **kw)
+    args = [FAKE] * 5 + [None, None, None, FAKE, None, *[FAKE] * 5, None, None, None]
+    states = 2 * cfg.B * -(-cfg.T // 64) * cfg.H * 16 * 64 * 4
+    n = la.la_scan_bwd_workspace_bytes(cfg)
+    assert n >= states and la.la_scan_bwd_varlen_workspace_bytes(cfg) == 0
+    for ws, given in ((None, 0), (FAKE, 0), (FAKE, n - 1)):
+        refused(lambda: la.la_scan_bwd(cfg, *args, ws, given, stream=0), la.LA_ERR_WORKSPACE, "workspace")
+    refused(lambda: la.la_scan_bwd(cfg, *args, FAKE, n, cu_seqlens=FAKE, stream=0), la.LA_ERR_UNSUPPORTED, "2^23")
+
+
 def test_no_sequences_need_no_tensors():
     """B = 0 with boundaries and a packed length."""
     la.la_conv_fwd(conv(B=0), None, None, None, None, None, None, cu_seqlens=FAKE, stream=0)
