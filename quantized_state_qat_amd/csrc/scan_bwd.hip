@@ -254,10 +254,10 @@ struct GradLds {
     T c[kQ * lds_row<T>(N)];
     T x[kQ * lds_row64<T>()];
     T dy[kQ * lds_row64<T>()];
-    // M[t][s] and dG[t][s].  bf16: rounded once.  Their share of dX, dB and dC then carries an error
-    // like the bf16 results' own rounding; the decays' gradients, in FP32, are formed before it.
-    T m[kQ * lds_row64<T>()];
-    T dg[kQ * lds_row64<T>()];
+    // M[t][s] and dG[t][s], as two bf16 parts: 2^-17 of a value for bf16 results (rounded to one,
+    // db and dc were 1.4 times as far from their 64-bit values as their own rounding leaves them)
+    T m[Mat<T>::template parts<2>][kQ * lds_row64<T>()];
+    T dg[Mat<T>::template parts<2>][kQ * lds_row64<T>()];
     T ds[sizeof(T) == 2 ? 2 : 1][sizeof(T) == 2 ? N * lds_row64<T>() : 8];  // dS (two bf16 parts); FP32 reads it from memory
     Decay d;
     // partial sums of the decays' gradients, by parity of the iteration (they are joined beside the next)
@@ -346,9 +346,9 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         t.store(lds.b, RB);
         t.load(static_cast<const T*>(p.c) + row0 * p.ld_c + static_cast<int64_t>(grp) * p.dk, p.ld_c, live, p.dk);
         t.store(lds.c, RB);
-        for (int i = threadIdx.x; i < kQ * RM; i += 512) {
-            lds.m[i] = T{};
-            lds.dg[i] = T{};
+        for (int i = threadIdx.x; i < P2 * kQ * RM; i += 512) {
+            (&lds.m[0][0])[i] = T{};
+            (&lds.dg[0][0])[i] = T{};
         }
     }
     __syncthreads();
@@ -481,8 +481,8 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                 pr = __builtin_fmaf(pc[r], dl, pr);
                 if (s == t) diag += acc[r];
             }
-            MT::template put4<1>(&lds.m[t * RM + s0], 0, m);
-            MT::template put4<1>(&lds.dg[t * RM + s0], 0, dg);
+            MT::template put4<P2>(&lds.m[0][t * RM + s0], kQ * RM, m);
+            MT::template put4<P2>(&lds.dg[0][t * RM + s0], kQ * RM, dg);
             pr = rows_sum(pr);
             if (g == 0) lds.rt[par][k][lm] = pr;
 #pragma unroll
@@ -533,12 +533,14 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                         for (int j = 0; j < 2; j++)
                             if (k1 + q < KS) acc[j] = MT::mma(dsT[q][k], bf[q][j], acc[j]);
             }
-            typename MT::Frag dyT[2], mf[2][2];
+            typename MT::Frag dyT[2], mf[2][P2][2];
 #pragma unroll
             for (int ks = 0; ks < 2; ks++) {
                 dyT[ks] = MT::col8(lds.dy, RX, 32 * ks, pc, ln);
 #pragma unroll
-                for (int j = 0; j < 2; j++) mf[ks][j] = MT::col8(lds.m, RM, 32 * ks, 32 * half + 16 * j, ln);
+                for (int k = 0; k < P2; k++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++) mf[ks][k][j] = MT::col8(lds.m[k], RM, 32 * ks, 32 * half + 16 * j, ln);
             }
             // (rows behind the sequence lie behind the buffer's end)
             const __amdgpu_buffer_rsrc_t rdx =
@@ -552,8 +554,10 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
 #pragma unroll
             for (int ks = 0; ks < 2; ks++)
 #pragma unroll
-                for (int j = 0; j < 2; j++)
-                    if (ks >= half) acc[j] = MT::mma(dyT[ks], mf[ks][j], acc[j]);  // (tokens before s: zero)
+                for (int k = 0; k < P2; k++)
+#pragma unroll
+                    for (int j = 0; j < 2; j++)
+                        if (ks >= half) acc[j] = MT::mma(dyT[ks], mf[ks][k][j], acc[j]);  // (tokens before s: zero)
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 const int s = 32 * half + 16 * j + lm;
@@ -577,13 +581,16 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
             for (int ii = 0; ii < TI; ii++) {
                 const int i = part * TI + ii, t = 16 * i + lm;
                 __builtin_amdgcn_sched_barrier(0);
-                typename MT::Frag yf[2], xf[2], gr[2], gc[2];
+                typename MT::Frag yf[2], xf[2], gr[2][P2], gc[2][P2];
 #pragma unroll
                 for (int ks = 0; ks < 2; ks++) {
                     yf[ks] = MT::row8(lds.dy + t * RX + 32 * ks + 8 * g);
                     xf[ks] = MT::row8(lds.x + t * RX + 32 * ks + 8 * g);
-                    gr[ks] = MT::row8(&lds.dg[t * RM + 32 * ks + 8 * g]);
-                    gc[ks] = MT::col8(lds.dg, RM, 32 * ks, 16 * i, ln);
+#pragma unroll
+                    for (int k = 0; k < P2; k++) {
+                        gr[ks][k] = MT::row8(&lds.dg[k][t * RM + 32 * ks + 8 * g]);
+                        gc[ks][k] = MT::col8(lds.dg[k], RM, 32 * ks, 16 * i, ln);
+                    }
                 }
                 float cv[4], bv[4];
                 MT::get4(lds.c + t * RB + n0 + 4 * g, cv);
@@ -599,10 +606,12 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                         b = MT::mma(dSf[ks][k], xf[ks], b);
                     }
 #pragma unroll
-                for (int ks = 0; ks < 2; ks++) {
-                    if (ks <= i / 2) dC[ii] = MT::mma(bT[ks], gr[ks], dC[ii]);
-                    if (ks >= i / 2) dB[ii] = MT::mma(cT[ks], gc[ks], dB[ii]);
-                }
+                for (int ks = 0; ks < 2; ks++)
+#pragma unroll
+                    for (int k = 0; k < P2; k++) {
+                        if (ks <= i / 2) dC[ii] = MT::mma(bT[ks], gr[ks][k], dC[ii]);
+                        if (ks >= i / 2) dB[ii] = MT::mma(cT[ks], gc[ks][k], dB[ii]);
+                    }
                 ri[ii] = ci[ii] = 0.0f;
 #pragma unroll
                 for (int r = 0; r < 4; r++) {

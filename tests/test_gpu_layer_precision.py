@@ -1,0 +1,45 @@
+"""How many bits the layer operators hold between their inputs and outputs, by path, against the
+64-bit forms (tests/layer_ref.py).
+
+The scan's inputs here are positive and its sequences short: every output is a sum of few positive
+terms, so an operand held in fewer bits than it should is not averaged away.  With T <= 5 tokens
+and d_k = 16 a sum has at most T + 16 = 21 terms, 21 x 2^-24 < 2^-19 of it; a step, its decays and
+their products with an operand are eight roundings or so more, 2^-21: 2^-18 with room for both.
+Where an operand is two bf16 parts (y, dx, db and dc of bf16 inputs; 2^-17 each): 2^-16.
+"""
+import numpy as np
+import pytest
+import torch
+
+import quantized_state_qat_amd as la
+from tests import layer_ref as R
+from tests.test_gpu_layer import BF, CODE, F32, Scan, close, draw, gen, np64
+
+pytestmark = pytest.mark.gpu
+
+
+class Positive(Scan):
+    def __init__(self, *a, **k):
+        super().__init__(*a, extra=0, **k)
+        for t in (self.buf, self.dy, self.D, self.S0, self.dST):
+            if t is not None:
+                t.abs_()
+
+
+@pytest.mark.parametrize("T", [1, 2, 5])
+@pytest.mark.parametrize("states", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_scan_holds_its_operands(dtype, T, states):
+    s = Positive(dtype, 3, T, 4, 2, 16, 64, states=states)
+    w, m = s.reference(True)
+    fine, parts = 2.0 ** -18, 2.0 ** -18 if dtype == F32 else 2.0 ** -16
+    o = s.bwd()
+    s.out = F32  # (the forward takes any output type)
+    s.cfg.out_dtype = CODE[F32]
+    y, ST = s.fwd()
+    close(y.reshape(w["y"].shape), w["y"], m["y"], parts, "y")
+    close(ST, w["S_T"], m["S_T"], fine, "S_T")
+    for k in ("dx", "db", "dc"):
+        close(o[k].reshape(w[k].shape), w[k], m[k], parts, k)
+    for k in ("dS0", "dD", "ddt", "dA", "ddt_bias"):
+        close(o[k].reshape(w[k].shape), w[k], m[k], fine, k)
