@@ -119,10 +119,10 @@ struct NormFwd {
 template <class T, class O, int LANES, int CH, int QDQ>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(NormFwd p) {
     constexpr int RPW = 256 / LANES;  // rows a workgroup
-    // FP32 values of codes: half a code's step is far above FP32's rounding, so every operation is
-    // rounded as the formula has it (the squares summed in double), and a value near the middle
-    // between two codes goes where FP32 arithmetic puts it.
-    constexpr bool STEPWISE = QDQ != LA_QDQ_NONE && sizeof(O) == 4;
+    // Codes: every operation is rounded as the formula has it (the squares summed in double), and a
+    // value near the middle between two codes goes where FP32 arithmetic puts it, whatever y's type
+    // and whether y is wanted at all.
+    constexpr bool STEPWISE = QDQ != LA_QDQ_NONE;
     __shared__ float lds[8];
     __shared__ double wide[STEPWISE ? 4 : 1];
     const int l = threadIdx.x % LANES;
@@ -162,8 +162,16 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormFwd p) {
         }
     }
     float r;  // 1 / rms, or the rms
-    if constexpr (STEPWISE) r = sqrtf(static_cast<float>(row_sum_wide<LANES>(ss, wide) / p.d) + p.eps);
-    else r = rsqrt_fine(row_sum<LANES>(ss, lds) / static_cast<float>(p.d) + p.eps);
+    [[maybe_unused]] float recip = 0.0f;  // RN(1 / r) as in int8_scale_recip, where its quotients are the exact ones
+    [[maybe_unused]] bool by_recip = false;
+    if constexpr (STEPWISE) {
+        r = sqrtf(static_cast<float>(row_sum_wide<LANES>(ss, wide) / p.d) + p.eps);
+        by_recip = r > 0x1p-60f && r < 0x1p60f;
+        const float e = __builtin_amdgcn_rcpf(r);
+        recip = __builtin_fmaf(__builtin_fmaf(-r, e, 1.0f), e, e);
+    } else {
+        r = rsqrt_fine(row_sum<LANES>(ss, lds) / static_cast<float>(p.d) + p.eps);
+    }
     float amax[CH];
 #pragma unroll
     for (int c = 0; c < CH; c++) {
@@ -174,7 +182,8 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormFwd p) {
             load_w(p.w, p.w_dtype, col, w);
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                h[c][e] = (STEPWISE ? h[c][e] / r : h[c][e] * r) * w[e];
+                if constexpr (STEPWISE) h[c][e] = (by_recip ? quot_rn_fast(h[c][e], r, recip) : h[c][e] / r) * w[e];
+                else h[c][e] = h[c][e] * r * w[e];
                 if (QDQ != LA_QDQ_NONE) amax[c] = fmaxf(amax[c], fabsf(h[c][e]));
             }
         }

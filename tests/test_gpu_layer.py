@@ -583,6 +583,27 @@ def test_norm(dtype, rows, d, kind, group, out, wt, residual):
     assert torch.equal(x2, ro) and torch.equal(y2, y)
 
 
+@pytest.mark.parametrize("kind,group", [("int8", 64), ("int8", 0), ("e4m3", 0), ("e4m3", 32)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 2048, 4096])
+def test_norm_codes_are_the_same_for_every_type_of_values(d, dtype, kind, group):
+    rows = 2000
+    g = gen(d)
+    x, res, w = draw(g, rows, d, dtype=dtype), draw(g, rows, d, dtype=dtype, scale=3.0), draw(g, d, dtype=F32)
+    qdq = la.LA_QDQ_INT8_GROUP if kind == "int8" else la.LA_QDQ_E4M3_TILE
+    got = []
+    for out in (F32, BF, None):
+        cfg = la.NormConfig(rows=rows, d=d, qdq=qdq, group=group, x_dtype=CODE[dtype], out_dtype=CODE[out or BF])
+        y = torch.empty(rows, d, dtype=out, device="cuda") if out else None
+        codes = torch.empty(rows, d, dtype=torch.int8 if kind == "int8" else torch.float8_e4m3fn, device="cuda")
+        scales = torch.empty(rows, d // (group or d), device="cuda")
+        la.la_norm_fwd(cfg, x, res, w, None, y, codes, scales)
+        got.append((codes.view(torch.uint8), scales, y))
+    for codes, scales, _ in got[1:]:
+        assert torch.equal(codes, got[0][0]) and torch.equal(scales, got[0][1])
+    assert torch.equal(got[0][2].to(BF), got[1][2])
+
+
 def test_norm_keeps_infinities_and_nan_in_their_rows():
     for qdq in (la.LA_QDQ_NONE, la.LA_QDQ_INT8_GROUP, la.LA_QDQ_E4M3_TILE):
         x = torch.ones(4, 256, dtype=BF, device="cuda")
