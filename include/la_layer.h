@@ -145,8 +145,10 @@ la_status la_scan_step(const la_scan_config* cfg, const void* x, const void* dt,
  * codecs of la.h on n:  INT8 s = amax/127, code = clamp(rne(n/s), -127, 127);  E4M3 s =
  * amax/448, code = e4m3(n/s)  (s = 1 when amax == 0);  y is then the value the code stands
  * for, code * s (n / s within FP32's rounding of the middle between two codes may take either).
- * A row with an infinity or NaN among its h gives NaN where the formula does; its codes are
- * unspecified.
+ * Codes and scales are the same for every out_dtype and without y.
+ * A row with an infinity or NaN among its h gives NaN where the formula does: in y, and with a
+ * quantizer in the scale and every y of a group that holds one.  Codes that stand for NaN are 0
+ * (INT8) or NaN (E4M3).
  */
 typedef struct la_norm_config {
     int32_t rows, d;    /* rows min(256, max(8, d / 4)) below 2^32; d a multiple of 8 up to 16384 */

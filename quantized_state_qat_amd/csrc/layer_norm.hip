@@ -51,6 +51,12 @@ __device__ __forceinline__ void load_w(const void* w, int dtype, int col, float 
     }
 }
 
+// The larger of a magnitude and |b|, a NaN above every number (fmaxf would drop it).
+__device__ __forceinline__ float larger_abs(float a, float b) {
+    const uint32_t u = __float_as_uint(a), v = __float_as_uint(b) & 0x7FFFFFFFu;
+    return __uint_as_float(u > v ? u : v);
+}
+
 // Sum over the row's lanes, the same bits in each of them.
 template <int LANES>
 __device__ __forceinline__ float row_sum(float x, float* lds) {
@@ -92,7 +98,7 @@ __device__ __forceinline__ float row_max(float x, float* lds) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) lds[4 + (threadIdx.x >> 6)] = x;
     __syncthreads();
-    return fmaxf(fmaxf(lds[4], lds[5]), fmaxf(lds[6], lds[7]));
+    return larger_abs(larger_abs(lds[4], lds[5]), larger_abs(lds[6], lds[7]));
 }
 
 // 1 / sqrt(m), correct to about an ulp: the hardware's estimate and one Newton step (skipped
@@ -184,7 +190,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormFwd p) {
             for (int e = 0; e < 8; e++) {
                 if constexpr (STEPWISE) h[c][e] = (by_recip ? quot_rn_fast(h[c][e], r, recip) : h[c][e] / r) * w[e];
                 else h[c][e] = h[c][e] * r * w[e];
-                if (QDQ != LA_QDQ_NONE) amax[c] = fmaxf(amax[c], fabsf(h[c][e]));
+                if (QDQ != LA_QDQ_NONE) amax[c] = larger_abs(amax[c], h[c][e]);
             }
         }
     }
@@ -192,7 +198,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormFwd p) {
         if (p.group == 0) {
             float m = 0.0f;
 #pragma unroll
-            for (int c = 0; c < CH; c++) m = fmaxf(m, amax[c]);
+            for (int c = 0; c < CH; c++) m = larger_abs(m, amax[c]);
             m = row_max<LANES>(m, lds);
 #pragma unroll
             for (int c = 0; c < CH; c++) amax[c] = m;
@@ -200,9 +206,9 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormFwd p) {
 #pragma unroll
             for (int c = 0; c < CH; c++) {
                 amax[c] = group_max_abs<2>(amax[c]);
-                if (p.group >= 32) amax[c] = fmaxf(amax[c], dpp<kDppXor2>(amax[c]));
-                if (p.group >= 64) amax[c] = fmaxf(amax[c], dpp<kDppHalfMirror>(amax[c]));
-                if (p.group >= 128) amax[c] = fmaxf(amax[c], dpp<kDppMirror>(amax[c]));
+                if (p.group >= 32) amax[c] = larger_abs(amax[c], dpp<kDppXor2>(amax[c]));
+                if (p.group >= 64) amax[c] = larger_abs(amax[c], dpp<kDppHalfMirror>(amax[c]));
+                if (p.group >= 128) amax[c] = larger_abs(amax[c], dpp<kDppMirror>(amax[c]));
             }
         }
         const int per_row = p.group ? p.d / p.group : 1;
@@ -212,16 +218,22 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormFwd p) {
             if (col >= p.d) continue;
             float s, y;
             uint32_t word[2] = {0, 0};
+            // a NaN in the group: its maximum, its scale and every value that its codes stand for
+            const bool none = amax[c] != amax[c];
             if constexpr (QDQ == LA_QDQ_INT8_GROUP) {
-                const bool fast = int8_scale_recip(amax[c], s, y);
+                bool fast = int8_scale_recip(amax[c], s, y);
+                if (none) s = amax[c], fast = false;
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
-                    const float q = fast ? int8_code_fast(h[c][e], s, y) : int8_code(h[c][e], s);
-                    word[e >> 2] |= (static_cast<uint32_t>(static_cast<int>(q)) & 0xFFu) << (8 * (e & 3));
+                    float q = fast ? int8_code_fast(h[c][e], s, y) : rintf(h[c][e] / s);
+                    const bool number = q == q;  // (of a quotient without one: code 0)
+                    if (!fast && number) q = fminf(fmaxf(q, -127.0f), 127.0f);
+                    word[e >> 2] |= (number ? static_cast<uint32_t>(static_cast<int>(q)) & 0xFFu : 0u) << (8 * (e & 3));
                     h[c][e] = q * s;
                 }
             } else {
-                const bool fast = e4m3_scale_recip(amax[c], s, y);
+                bool fast = e4m3_scale_recip(amax[c], s, y);
+                if (none) s = amax[c], fast = false;
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
                     float a = fast ? quot_rn_fast(h[c][e], s, y) : h[c][e] / s;

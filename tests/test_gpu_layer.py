@@ -616,6 +616,48 @@ def test_norm_keeps_infinities_and_nan_in_their_rows():
         assert torch.isnan(y[1]).all() and torch.isnan(y[2, 7])
 
 
+@pytest.mark.parametrize("kind", ["none", "int8", "e4m3"])
+@pytest.mark.parametrize("group", [0, 16, 64, 128])
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [256, 2048, 4096])
+def test_norm_infinities_and_nan_by_the_formula(d, dtype, out, group, kind):
+    """NaN exactly where torch's float64 formula has it: values, scales, codes."""
+    g = gen(d + group)
+    x, w = draw(g, 9, d, dtype=dtype), 1 + draw(g, d, dtype=F32, scale=0.1)
+    nan, inf = float("nan"), float("inf")
+    x[1, 3], x[2, d - 1], x[3, 0], x[4, 70], x[6, :] = nan, inf, -inf, nan, inf
+    x[7, 5], x[7, d // 2] = inf, nan
+    if dtype == F32:
+        w[130] = inf  # an infinite product: an infinite scale
+    qdq = {"none": la.LA_QDQ_NONE, "int8": la.LA_QDQ_INT8_GROUP, "e4m3": la.LA_QDQ_E4M3_TILE}[kind]
+    cfg = la.NormConfig(rows=9, d=d, eps=1e-5, qdq=qdq, group=group if kind != "none" else 0, x_dtype=CODE[dtype], out_dtype=CODE[out])
+    y = torch.empty(9, d, dtype=out, device="cuda")
+    codes = scales = None
+    width = cfg.group or d
+    if kind != "none":
+        codes = torch.empty(9, d, dtype=torch.int8 if kind == "int8" else torch.float8_e4m3fn, device="cuda")
+        scales = torch.empty(9, d // width, device="cuda")
+    la.la_norm_fwd(cfg, x, None, w, None, y, codes, scales)
+    h = x.double()
+    n = h / torch.sqrt((h * h).mean(1, keepdim=True) + 1e-5) * w.double()
+    if kind == "none":
+        assert torch.equal(y.isnan(), n.isnan()) and torch.equal(y.isinf(), n.isinf())
+        return
+    v = n.view(9, -1, width)
+    s = v.abs().amax(2, keepdim=True) / (127.0 if kind == "int8" else 448.0)  # (amax keeps NaN)
+    s = torch.where(s == 0, torch.ones_like(s), s)
+    q = v / s
+    q = torch.round(q).clamp(-127, 127) if kind == "int8" else q.clamp(-448, 448)
+    want, q = (q * s).view(9, d), q.view(9, d)
+    assert torch.equal(scales.isnan(), s[:, :, 0].isnan()) and torch.equal(scales.isinf(), s[:, :, 0].isinf())
+    assert torch.equal(y.isnan(), want.isnan()) and torch.equal(y.isinf(), want.isinf())
+    if kind == "int8":
+        assert not codes[q.isnan()].any()
+    else:
+        assert torch.equal(codes.float().isnan(), q.isnan())
+
+
 # ----------------------------------------------------------------------------- run together
 class Layer:
     """norm (8-bit) -> projection -> convolution -> scan -> projection, as a hybrid stack runs them."""
