@@ -17,7 +17,8 @@
  * tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of tensors [T][...], cfg->T the packed length.
  * Boundaries are clamped to [0, T] on the device; decreasing ones are a caller error (results
  * are then unspecified, nothing outside the tensors is touched).  Tokens outside every sequence: their
- * rows of forward outputs are left as they were, their gradients are zero.
+ * rows of forward outputs are left as they were, their gradients are zero (with B = 0 those of all
+ * T tokens, in the gradients that are not NULL).
  *
  * Row strides.  ld_* is the distance in elements between a tensor's rows of consecutive
  * tokens, 0 = packed tight.  The row's own elements are contiguous, rows of [B][T] follow

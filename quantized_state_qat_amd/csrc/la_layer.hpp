@@ -100,6 +100,9 @@ constexpr int64_t kMaxUnits = static_cast<int64_t>(1) << 23;
 hipError_t launch_reduce_parts(const float* part, int parts, int cols, float* out, int split, float* out2,
                                hipStream_t s);
 
+// Zeros to `width` elements of each of `rows` rows `ld` elements apart (out null: nothing).
+hipError_t launch_zero_rows(void* out, int dtype, int64_t rows, int64_t width, int64_t ld, hipStream_t s);
+
 // ------------------------------------------------------------------ device helpers
 typedef float fv4 __attribute__((ext_vector_type(4)));
 typedef uint32_t uv4 __attribute__((ext_vector_type(4)));

@@ -437,6 +437,12 @@ __global__ __launch_bounds__(1024) void reduce_parts_kernel(const float* __restr
     }
 }
 
+template <class T>
+__global__ __launch_bounds__(256) void zero_rows_kernel(T* out, int64_t n, int64_t width, int64_t ld) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
+        out[i / width * ld + i % width] = T{};
+}
+
 // Tokens a lane walks in the backward: 32 where that still gives every CU several workgroups,
 // fewer for short inputs.
 int conv_bwd_per(const la_conv_config& c) {
@@ -523,7 +529,9 @@ hipError_t launch_conv_bwd(const la_conv_config& c, const ConvArgs& a, hipStream
             conv_bwd_kernel<T, W, ACT><<<dim3(static_cast<unsigned>(gy + extra), (c.C / 4 + 31) / 32), 256, 0, s>>>(
                 g, static_cast<const T*>(a.x), a.w, a.bias, static_cast<const T*>(a.s0), static_cast<const T*>(a.dy),
                 static_cast<const T*>(a.dsT), static_cast<T*>(a.dx), a.part, nb.blocks, static_cast<T*>(a.ds0), gy);
-        const hipError_t e = hipGetLastError();
+        hipError_t e = hipGetLastError();
+        if (e == hipSuccess && c.B == 0 && a.cu)  // every token is outside every sequence
+            e = launch_zero_rows(a.dx, c.x_dtype, c.T, c.C, g.ldx, s);
         if (e != hipSuccess) return e;
         return launch_reduce_parts(a.part, static_cast<int>(gy), c.C * (W + 1), a.dw, c.C * W, a.dbias, s);
     });
@@ -545,6 +553,15 @@ hipError_t launch_reduce_parts(const float* part, int parts, int cols, float* ou
                                hipStream_t s) {
     if (cols == 0) return hipSuccess;
     reduce_parts_kernel<<<dim3((cols + 31) / 32), 1024, 0, s>>>(part, parts, cols, out, split, out2);
+    return hipGetLastError();
+}
+
+hipError_t launch_zero_rows(void* out, int dtype, int64_t rows, int64_t width, int64_t ld, hipStream_t s) {
+    const int64_t n = rows * width;
+    if (!out || n == 0) return hipSuccess;
+    const unsigned grid = static_cast<unsigned>(n < 65536 * 256 ? (n + 255) / 256 : 65536);
+    if (dtype == LA_BF16) zero_rows_kernel<<<grid, 256, 0, s>>>(static_cast<uint16_t*>(out), n, width, ld);
+    else zero_rows_kernel<<<grid, 256, 0, s>>>(static_cast<float*>(out), n, width, ld);
     return hipGetLastError();
 }
 

@@ -176,6 +176,16 @@ def test_conv_gradients_of_no_sequences():
     assert not dw.any() and not db.any()
 
 
+@pytest.mark.parametrize("dtype,T,C,ld", [(BF, 50, 64, 0), (F32, 3, 8, 16), (BF, 70000, 264, 272)])
+def test_conv_gradients_of_no_sequences_are_zero_rows(dtype, T, C, ld):
+    cfg = la.ConvConfig(B=0, T=T, C=C, width=4, x_dtype=CODE[dtype], ld_x=ld)
+    wide = torch.full((T, ld or C), 9.0, dtype=dtype, device="cuda")
+    dw, db = torch.full((C, 4), 3.0, device="cuda"), torch.full((C,), 3.0, device="cuda")
+    la.la_conv_bwd(cfg, None, torch.ones(C, 4, device="cuda"), None, None, None, None, wide[:, :C], dw, db, None, None, 0,
+                   cu_seqlens=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    assert not wide[:, :C].any() and (wide[:, C:] == 9).all() and not dw.any() and not db.any()
+
+
 @pytest.mark.parametrize("dtype,B,C,W,pool", [(BF, 5, 264, 4, True), (F32, 1, 8, 2, True), (BF, 3, 2312, 3, False)])
 def test_conv_step_continues_the_forward(dtype, B, C, W, pool):
     g = gen(B)
