@@ -117,11 +117,12 @@ size_t la_scan_workspace_bytes(const la_scan_config* cfg);
 
 /* Gradients for the upstream gradients dy and dS_T (NULL = zero): dx, ddt, db, dc laid out and
  * typed as their inputs; dA, dD, ddt_bias float [H] (dD and ddt_bias may be NULL); dS0 (may be
- * NULL).  db and dc are summed over the group's heads.  out_dtype must equal x_dtype.  A call
- * takes below 2^23 heads of 64-token chunks.  Workspace (the state and its gradient at every
- * 64th token, and more): at least la_scan_bwd_workspace_bytes(cfg) bytes; for packed sequences
- * la_scan_bwd_varlen_workspace_bytes(cfg), up to B times less, is enough.  A query returns 0 where
- * the call itself would be refused: the first goes by B sequences of T tokens, the second by a
+ * NULL).  db and dc are summed over the group's heads (H = 0: zero, where they are not NULL).
+ * out_dtype must equal x_dtype.  A call takes below 2^23 heads of 64-token chunks.  Workspace (the
+ * state and its gradient at every 64th token, and more): at least la_scan_bwd_workspace_bytes(cfg)
+ * bytes; for packed sequences la_scan_bwd_varlen_workspace_bytes(cfg), up to B times less, is
+ * enough.  A query returns 0 where the call has nothing to sum (B, T or H = 0) and where it would
+ * be refused: the first goes by B sequences of T tokens, the second by a
  * packing of T tokens. */
 la_status la_scan_bwd(const la_scan_config* cfg, const int32_t* cu_seqlens, const void* x, const void* dt,
                       const float* A, const void* b, const void* c, const float* D, const float* dt_bias,

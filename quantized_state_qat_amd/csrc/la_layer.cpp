@@ -131,6 +131,7 @@ la_status check_scan_bwd(const la_scan_config* c, bool packed) {
 // suffice for a packing too, where a packing of the config is taken at all: one of few or short
 // sequences has more chunk slots than they have chunks.
 size_t scan_bwd_need(const la_scan_config& c, bool packed) {
+    if (c.B == 0 || c.T == 0 || c.H == 0) return 0;  // (zeros only)
     const size_t need = la::scan_bwd_workspace(c, packed);
     if (packed || la::scan_bwd_slots(c, true) * c.H >= la::kMaxUnits) return need;
     const size_t other = la::scan_bwd_workspace(c, true);
@@ -300,7 +301,6 @@ la_status la_scan_bwd(const la_scan_config* cfg, const int32_t* cu_seqlens, cons
     CHECK(check_ptr(dS0, "dS0", false));
     if (dS0 && dS0 == dS_T) return fail(LA_ERR_INVALID_ARG, "dS0 must not be dS_T");
     CHECK(check_workspace(workspace, ws_bytes, scan_bwd_need(*cfg, cu_seqlens != nullptr)));
-    if (cfg->H == 0) return ok();
     la::ScanArgs a;
     a.cu = cu_seqlens, a.x = x, a.dt = dt, a.A = A, a.b = b, a.c = c, a.D = D, a.bias = dt_bias, a.S0 = S0, a.dy = dy;
     a.dST = dS_T, a.dx = dx, a.ddt = ddt, a.dA = dA, a.db = db, a.dc = dc, a.dD = dD, a.dbias = ddt_bias, a.dS0 = dS0;

@@ -856,9 +856,18 @@ size_t scan_bwd_workspace(const la_scan_config& c, bool packed) { return bwd_ws(
 int64_t scan_bwd_slots(const la_scan_config& c, bool packed) { return slot_count(c, packed); }
 
 hipError_t launch_scan_bwd(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
-    if (c.B == 0 || c.T == 0) {  // no tokens: the state's gradient passes through, the sums are zero
+    if (c.B == 0 || c.T == 0 || c.H == 0) {
+        // Nothing to sum: zeros, also for the tokens of a packing without sequences and for the
+        // groups of no heads; the state's gradient passes through.
+        const ScanP p = scan_params(c, a);
+        const int64_t rows = a.cu ? c.T : static_cast<int64_t>(c.B) * c.T;
+        for (const hipError_t e : {launch_zero_rows(a.dx, c.x_dtype, rows, static_cast<int64_t>(c.H) * c.d_v, p.ld_x, s),
+                                   launch_zero_rows(a.ddt, c.dt_dtype, rows, c.H, p.ld_dt, s),
+                                   launch_zero_rows(a.db, c.x_dtype, rows, static_cast<int64_t>(c.G) * c.d_k, p.ld_b, s),
+                                   launch_zero_rows(a.dc, c.x_dtype, rows, static_cast<int64_t>(c.G) * c.d_k, p.ld_c, s)})
+            if (e != hipSuccess) return e;
         for (float* o : {a.dA, a.dD, a.dbias})
-            if (o) copy_or_zero_kernel<<<dim3((c.H + 255) / 256), 256, 0, s>>>(nullptr, o, c.H);
+            if (o && c.H > 0) copy_or_zero_kernel<<<dim3((c.H + 255) / 256), 256, 0, s>>>(nullptr, o, c.H);
         const int64_t n = static_cast<int64_t>(c.B) * c.H * c.d_k * c.d_v;
         if (a.dS0 && n > 0) copy_or_zero_kernel<<<dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, s>>>(a.dST, a.dS0, n);
         return hipGetLastError();

@@ -458,6 +458,26 @@ def test_scan_without_tokens():
             assert not o["dx"].any() and not o["ddt"].any() and not o["db"].any() and not o["dc"].any()
 
 
+@pytest.mark.parametrize("dtype,B,T,H,G,cu", [(BF, 0, 70, 3, 1, [0]), (F32, 0, 300, 4, 2, [0]), (BF, 0, 1, 16, 1, [0]),
+                                              (BF, 2, 70, 0, 3, None), (F32, 2, 70, 0, 1, [0, 5, 60])])
+def test_scan_gradients_of_no_sequences_or_heads_are_zero(dtype, B, T, H, G, cu):
+    N, P = 32, 64
+    tokens = T if cu is not None else B * T
+    wx, wb = H * P, G * N
+    ld = wx + 2 * wb + 8
+    cfg = la.ScanConfig(B=B, T=T, H=H, G=G, d_k=N, d_v=P, x_dtype=CODE[dtype], dt_dtype=CODE[dtype], out_dtype=CODE[dtype],
+                        ld_x=ld, ld_b=ld, ld_c=ld, ld_dt=H + 5)
+    buf, ddt = (torch.full((tokens, w), 9.0, dtype=dtype, device="cuda") for w in (ld, H + 5))
+    sums = [torch.full((H,), 3.0, device="cuda") if H else None for _ in range(3)]
+    A = torch.ones(max(H, 1), device="cuda")
+    la.la_scan_bwd(cfg, None, None, A, None, None, None, None, None, None, None, buf[:, :wx] if H else None,
+                   ddt[:, :H] if H else None, sums[0], buf[:, wx:wx + wb], buf[:, wx + wb:wx + 2 * wb], sums[1], sums[2], None,
+                   None, 0, cu_seqlens=cu_tensor(cu))
+    assert not buf[:, :wx + 2 * wb].any() and (buf[:, wx + 2 * wb:] == 9).all()
+    assert not ddt[:, :H].any() and (ddt[:, H:] == 9).all()
+    assert not any(t is not None and t.any() for t in sums)
+
+
 @pytest.mark.parametrize("B,H,G,N,P,dtype", [(1, 2, 1, 16, 64, BF), (3, 4, 2, 32, 64, F32), (2, 3, 1, 64, 192, BF),
                                              (5, 16, 1, 128, 128, BF), (40, 16, 1, 64, 64, F32), (70, 16, 2, 16, 128, BF)])
 def test_scan_step(B, H, G, N, P, dtype):
