@@ -87,8 +87,8 @@ def _dtype(code):
 
 
 def _gpu(*tensors):
-    """The GPU of the first tensor among the arguments; None when it is on the host or all are
-    raw addresses."""
+    """The GPU of the first tensor among the arguments (all of a call's: any of them may be missing
+    or a raw address); None when it is on the host or there is none."""
     for t in tensors:
         if t is not None and t.__class__ is not int:
             return t.get_device() if t.is_cuda else None
@@ -182,7 +182,7 @@ def _tokens(cfg, cu_seqlens):
 def la_conv_fwd(cfg: ConvConfig, x, weight, bias, state0, y, state_T=None, cu_seqlens=None, stream=None) -> None:
     """y = act(causal depthwise convolution of state0 ++ x); state_T = its last rows."""
     lib = _library()
-    gpu = _gpu(x, weight, y)
+    gpu = _gpu(x, weight, y, bias, state0, state_T, cu_seqlens)
     xt, wt, n = _dtype(cfg.x_dtype), _dtype(cfg.w_dtype), _tokens(cfg, cu_seqlens)
     st = cfg.B * (cfg.width - 1) * cfg.C
     _call(gpu, stream, lib.la_conv_fwd, cfg,
@@ -200,7 +200,7 @@ def la_conv_bwd(cfg: ConvConfig, x, weight, bias, state0, dy, dstate_T, dx, dwei
                 ws_bytes: int, cu_seqlens=None, stream=None) -> None:
     """Gradients of la_conv_fwd (dweight and dbias float32)."""
     lib = _library()
-    gpu = _gpu(x, weight, dy, dx)
+    gpu = _gpu(x, weight, dy, dx, bias, state0, dstate_T, dweight, dbias, dstate0, workspace, cu_seqlens)
     xt, wt, n = _dtype(cfg.x_dtype), _dtype(cfg.w_dtype), _tokens(cfg, cu_seqlens)
     st, f32 = cfg.B * (cfg.width - 1) * cfg.C, _torch.float32
     _call(gpu, stream, lib.la_conv_bwd, cfg,
@@ -216,7 +216,7 @@ def la_conv_bwd(cfg: ConvConfig, x, weight, bias, state0, dy, dstate_T, dx, dwei
 def la_conv_step(cfg: ConvConfig, x, weight, bias, state, y, slots=None, n_slots: int = 0, stream=None) -> None:
     """One token; the state (or its slot of the pool) is shifted in place."""
     lib = _library()
-    gpu = _gpu(x, weight, state, y)
+    gpu = _gpu(x, weight, state, y, bias, slots)
     xt, wt = _dtype(cfg.x_dtype), _dtype(cfg.w_dtype)
     units = max(int(n_slots), 0) if slots is not None else cfg.B
     _call(gpu, stream, lib.la_conv_step, cfg,
@@ -242,7 +242,7 @@ def la_scan_fwd(cfg: ScanConfig, x, dt, A, b, c, D, dt_bias, S0, y, S_T, workspa
                 stream=None) -> None:
     """S <- exp(Delta A) S + Delta b x^T, y = S^T c + D x over every sequence."""
     lib = _library()
-    gpu = _gpu(x, dt, A, b, c, y)
+    gpu = _gpu(x, dt, A, b, c, y, D, dt_bias, S0, S_T, workspace, cu_seqlens)
     n, st, f32 = _tokens(cfg, cu_seqlens), cfg.B * cfg.H * cfg.d_k * cfg.d_v, _torch.float32
     _call(gpu, stream, lib.la_scan_fwd, cfg,
           _tight(gpu, cu_seqlens, "cu_seqlens", cfg.B + 1, _torch.int32),
@@ -264,7 +264,7 @@ def la_scan_bwd(cfg: ScanConfig, x, dt, A, b, c, D, dt_bias, S0, dy, dS_T, dx, d
                 workspace, ws_bytes: int, cu_seqlens=None, stream=None) -> None:
     """Gradients of la_scan_fwd."""
     lib = _library()
-    gpu = _gpu(x, dt, A, b, c, dy, dx)
+    gpu = _gpu(x, dt, A, b, c, dy, dx, D, dt_bias, S0, dS_T, ddt, dA, db, dc, dD, ddt_bias, dS0, workspace, cu_seqlens)
     n, st, f32 = _tokens(cfg, cu_seqlens), cfg.B * cfg.H * cfg.d_k * cfg.d_v, _torch.float32
     xt = _dtype(cfg.x_dtype)
     _call(gpu, stream, lib.la_scan_bwd, cfg,
@@ -281,7 +281,7 @@ def la_scan_bwd(cfg: ScanConfig, x, dt, A, b, c, D, dt_bias, S0, dy, dS_T, dx, d
 def la_scan_step(cfg: ScanConfig, x, dt, A, b, c, D, dt_bias, S, y, slots=None, n_slots: int = 0, stream=None) -> None:
     """One token; the state (or its slot of the pool) is advanced in place."""
     lib = _library()
-    gpu = _gpu(x, dt, A, b, c, S, y)
+    gpu = _gpu(x, dt, A, b, c, S, y, D, dt_bias, slots)
     units = max(int(n_slots), 0) if slots is not None else cfg.B
     _call(gpu, stream, lib.la_scan_step, cfg,
           *_scan_inputs(gpu, cfg, cfg.B, x, dt, A, b, c, D, dt_bias),
@@ -293,7 +293,7 @@ def la_scan_step(cfg: ScanConfig, x, dt, A, b, c, D, dt_bias, S, y, slots=None, 
 def la_norm_fwd(cfg: NormConfig, x, residual, weight, res_out, y, codes=None, scales=None, stream=None) -> None:
     """res_out = x + residual, y = its RMS norm, and with a quantizer its codes and scales."""
     lib = _library()
-    gpu = _gpu(x, residual, weight, res_out, y)
+    gpu = _gpu(x, residual, weight, res_out, y, codes, scales)
     n, xt, eight = cfg.rows * cfg.d, _dtype(cfg.x_dtype), _torch.uint8
     if codes is not None and codes.__class__ is not int and codes.dtype in (_torch.int8, _torch.float8_e4m3fn):
         eight = codes.dtype
@@ -311,7 +311,7 @@ def la_norm_bwd_workspace_bytes(cfg: NormConfig) -> int:
 def la_norm_bwd(cfg: NormConfig, h, weight, dy, dres, dx, dweight, workspace, ws_bytes: int, stream=None) -> None:
     """Gradients of la_norm_fwd from its res_out (straight through the codec)."""
     lib = _library()
-    gpu = _gpu(h, weight, dy, dres, dx)
+    gpu = _gpu(h, weight, dy, dres, dx, dweight, workspace)
     n, xt = cfg.rows * cfg.d, _dtype(cfg.x_dtype)
     _call(gpu, stream, lib.la_norm_bwd, cfg,
           _tight(gpu, h, "h", n, xt), _tight(gpu, weight, "weight", cfg.d, _dtype(cfg.w_dtype)),

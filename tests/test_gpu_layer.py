@@ -854,6 +854,25 @@ def test_binding_refuses_layouts():
         la.la_conv_fwd(cfg, x, w.cpu(), None, None, y)
 
 
+def test_binding_takes_tensors_after_addresses_and_nulls():
+    g = gen(4)
+    x, w, st, y = draw(g, 2, 64), draw(g, 64, 4, dtype=F32), draw(g, 2, 3, 64), torch.empty(2, 64, dtype=BF, device="cuda")
+    bias, want, first = draw(g, 64, dtype=F32), torch.empty_like(y), st.clone()
+    cfg = la.ConvConfig(B=2, T=1, C=64, width=4)
+    la.la_conv_step(cfg, x, w, bias, first, want)
+    la.la_conv_step(cfg, x.data_ptr(), w.data_ptr(), bias, st.data_ptr(), y.data_ptr())
+    assert torch.equal(y, want) and torch.equal(st, first)
+    nc = la.NormConfig(rows=2, d=64, qdq=la.LA_QDQ_INT8_GROUP)
+    scales, other = torch.empty(2, 1, device="cuda"), torch.empty(2, 1, device="cuda")
+    la.la_norm_fwd(nc, x, None, None, None, None, None, scales)
+    la.la_norm_fwd(nc, x.data_ptr(), None, None, None, None, None, other)
+    assert torch.equal(scales, other)
+    dST, dS0, dA = draw(g, 1, 2, 16, 64, dtype=F32), torch.empty(1, 2, 16, 64, device="cuda"), torch.ones(2, device="cuda")
+    la.la_scan_bwd(la.ScanConfig(B=1, T=0, H=2, G=1, d_k=16, d_v=64), None, None, None, None, None, None, None, None, None, dST,
+                   None, None, dA, None, None, None, None, dS0, None, 0)
+    assert torch.equal(dS0, dST) and not dA.any()
+
+
 # ----------------------------------------------------------------------- offsets past 32 bits
 def zeros(*shape, dtype=BF):
     return torch.zeros(*shape, dtype=dtype, device="cuda")
