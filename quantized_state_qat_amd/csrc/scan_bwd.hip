@@ -768,8 +768,8 @@ __global__ __launch_bounds__(256) void head_sums_kernel(ScanP p, const float* hp
 }
 
 __global__ __launch_bounds__(256) void copy_or_zero_kernel(const float* src, float* dst, int64_t n) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i < n) dst[i] = src ? src[i] : 0.0f;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256)
+        dst[i] = src ? src[i] : 0.0f;
 }
 
 // Slices of a group's heads: enough workgroups for two a CU.
@@ -869,7 +869,7 @@ hipError_t launch_scan_bwd(const la_scan_config& c, const ScanArgs& a, hipStream
         for (float* o : {a.dA, a.dD, a.dbias})
             if (o && c.H > 0) copy_or_zero_kernel<<<dim3((c.H + 255) / 256), 256, 0, s>>>(nullptr, o, c.H);
         const int64_t n = static_cast<int64_t>(c.B) * c.H * c.d_k * c.d_v;
-        if (a.dS0 && n > 0) copy_or_zero_kernel<<<dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, s>>>(a.dST, a.dS0, n);
+        if (a.dS0 && n > 0) copy_or_zero_kernel<<<dim3(static_cast<unsigned>(n < 65536 * 256 ? (n + 255) / 256 : 65536)), 256, 0, s>>>(a.dST, a.dS0, n);
         return hipGetLastError();
     }
     if (c.x_dtype == LA_BF16) {

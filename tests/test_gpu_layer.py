@@ -987,3 +987,16 @@ def test_state_pools_past_32_bits():
     la.la_conv_step(cfg, x, w, None, pool, yp, slots=slot, n_slots=n)
     la.la_conv_step(cfg, x, w, None, st, y)
     assert y.any() and torch.equal(y, yp) and torch.equal(pool[n - 1], st[0]) and not pool[:2].any()
+
+
+def test_scan_gradients_without_tokens_past_32_bits():
+    """T = 0: more than 2^32 elements of the states' gradient pass through."""
+    B, H, N, P = 4097, 64, 128, 128
+    assert B * H * N * P > 1 << 32
+    cfg = la.ScanConfig(B=B, T=0, H=H, G=1, d_k=N, d_v=P)
+    dST, dS0 = torch.ones(B, H, N, P, device="cuda"), zeros(B, H, N, P, dtype=F32)
+    dST[-1] = draw(gen(1), H, N, P, dtype=F32)
+    dA = torch.ones(H, device="cuda")
+    la.la_scan_bwd(cfg, None, None, None, None, None, None, None, None, None, dST, None, None, dA, None, None, None, None, dS0,
+                   None, 0)
+    assert torch.equal(dS0[-1], dST[-1]) and (dS0[:-1].amin(dim=(1, 2, 3)) == 1).all() and not dA.any()
