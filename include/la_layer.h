@@ -46,7 +46,9 @@ typedef enum { LA_ACT_NONE = 0, LA_ACT_SILU = 1 } la_act;
  * preceded by the W - 1 rows of its state, z = state0 ++ x,
  *     pre[t][c] = bias[c] + sum_{j < W} weight[c][j] z[t + j][c],   y = silu(pre) or pre,
  *     state_T   = the last W - 1 rows of z.
- * Sums are FP32.
+ * Sums are FP32.  B T C (packed: T C) may be up to 2^36 and B C up to 2^32, and, with the tokens'
+ * blocks of 16 n = B ceil(T / 16) (packed: ceil(T / 16)), (n + (W - 1) B) C up to 2^32 - 512
+ * pieces of 16 bytes.
  */
 typedef struct la_conv_config {
     int32_t B, T, C;  /* B up to 65535; T up to 2^30; C a multiple of 8 up to 2^20 */

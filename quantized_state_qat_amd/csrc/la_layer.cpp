@@ -78,10 +78,16 @@ la_status check_conv(const la_conv_config* c, bool step, bool packed) {
     CHECK(check_dtype(c->w_dtype, "w_dtype"));
     CHECK(check_ld(c->ld_x, c->C, c->x_dtype, "ld_x"));
     CHECK(check_ld(c->ld_y, c->C, c->x_dtype, "ld_y"));
-    // grids stay below 2^32 threads
     const int64_t tokens = packed ? c->T : static_cast<int64_t>(c->B) * c->T;
     if (tokens * c->C > (int64_t{1} << 36) || static_cast<int64_t>(c->B) * c->C > (int64_t{1} << 32))
         return fail(LA_ERR_UNSUPPORTED, "too many elements (B=%d T=%d C=%d)", c->B, c->T, c->C);
+    // The forward's grid stays below 2^32 threads (a larger one is cut short without an error): 16
+    // bytes of channels for 16 tokens and for every row of the final states, in two parts of whole
+    // workgroups of 256.
+    const int64_t lanes = c->C / (c->x_dtype == LA_BF16 ? 8 : 4);
+    const int64_t walks = (static_cast<int64_t>(c->T) + 15) / 16 * (packed ? 1 : c->B) + static_cast<int64_t>(c->width - 1) * c->B;
+    if (walks * lanes > (int64_t{1} << 32) - 512)
+        return fail(LA_ERR_UNSUPPORTED, "too many elements for a grid (B=%d T=%d C=%d)", c->B, c->T, c->C);
     if (c->B > 65535) return fail(LA_ERR_UNSUPPORTED, "B must be <= 65535 (B=%d)", c->B);
     return LA_OK;
 }

@@ -55,6 +55,14 @@ def test_conv_refuses_configs(kw, status, word):
     assert la.la_conv_bwd_workspace_bytes(conv(**kw)) == 0
 
 
+@pytest.mark.parametrize("kw", [dict(B=32768, T=1, C=131072), dict(B=65528, T=16, C=65544), dict(B=65535, T=17, C=61672)])
+def test_conv_refuses_grids_of_two_to_the_32(kw):
+    """Width 4: three rows of the final states and a walk for every 16 tokens, 16 bytes of channels each."""
+    cfg = conv(x_dtype=la.LA_F32, **kw)
+    assert cfg.B * (-(-cfg.T // 16) + 3) * (cfg.C // 4) > (1 << 32) - 512
+    refused(lambda: conv_fwd(cfg), la.LA_ERR_UNSUPPORTED, "elements")
+
+
 def test_conv_refuses_pointers():
     refused(lambda: conv_fwd(conv(), x=None), la.LA_ERR_INVALID_ARG, "x is NULL")
     refused(lambda: conv_fwd(conv(), weight=FAKE + 4), la.LA_ERR_ALIGNMENT, "weight")
