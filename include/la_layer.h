@@ -155,7 +155,7 @@ la_status la_scan_step(const la_scan_config* cfg, const void* x, const void* dt,
  * (INT8) or NaN (E4M3).
  */
 typedef struct la_norm_config {
-    int32_t rows, d;    /* rows min(256, max(8, d / 4)) below 2^32; d a multiple of 8 up to 16384 */
+    int32_t rows, d;    /* (rows + 31) min(256, max(8, d / 4)) below 2^32; d a multiple of 8 up to 16384 */
     float eps;          /* >= 0 */
     int32_t qdq;        /* la_qdq: LA_QDQ_NONE, LA_QDQ_INT8_GROUP or LA_QDQ_E4M3_TILE (one row high) */
     int32_t group;      /* with a quantizer 0, 16, 32, 64 or 128, dividing d */

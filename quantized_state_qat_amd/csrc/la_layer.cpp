@@ -161,9 +161,10 @@ la_status check_norm(const la_norm_config* c) {
     if (c->rows < 0 || c->d <= 0) return fail(LA_ERR_INVALID_ARG, "negative or zero size (rows=%d d=%d)", c->rows, c->d);
     if (c->d % 8 != 0 || c->d > 16384)
         return fail(LA_ERR_UNSUPPORTED, "d must be a multiple of 8 up to 16384 (d=%d)", c->d);
-    // a row has at most 256 lanes, or one for 4 columns: grids stay below 2^32 threads
+    // a row has at most 256 lanes, or one for 4 columns: grids, of whole workgroups of up to 32 rows,
+    // stay below 2^32 threads (a larger one is cut short without an error)
     const int64_t lanes = c->d / 4 < 8 ? 8 : c->d / 4 < 256 ? c->d / 4 : 256;
-    if (c->rows * lanes >= (int64_t{1} << 32)) return fail(LA_ERR_UNSUPPORTED, "too many rows (rows=%d d=%d)", c->rows, c->d);
+    if ((static_cast<int64_t>(c->rows) + 31) * lanes >= (int64_t{1} << 32)) return fail(LA_ERR_UNSUPPORTED, "too many rows (rows=%d d=%d)", c->rows, c->d);
     if (!(c->eps >= 0.0f)) return fail(LA_ERR_INVALID_ARG, "eps must be >= 0");
     CHECK(check_dtype(c->x_dtype, "x_dtype"));
     CHECK(check_dtype(c->w_dtype, "w_dtype"));

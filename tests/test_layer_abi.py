@@ -190,6 +190,13 @@ def test_norm_refuses_configs(kw, status, word):
     assert la.la_norm_bwd_workspace_bytes(norm(**kw)) == 0
 
 
+def test_norm_refuses_grids_of_two_to_the_32():
+    """d = 8: workgroups of 32 rows by 8 lanes."""
+    for rows in ((1 << 29) - 31, (1 << 29) - 1):
+        assert -(-rows // 32) * 256 == 1 << 32
+        refused(lambda: la.la_norm_fwd(norm(rows=rows, d=8), FAKE, None, None, FAKE, FAKE, stream=0), la.LA_ERR_UNSUPPORTED, "rows")
+
+
 def test_norm_refuses_pointers():
     refused(lambda: la.la_norm_fwd(norm(), None, None, None, FAKE, FAKE, stream=0), la.LA_ERR_INVALID_ARG, "x is NULL")
     refused(lambda: la.la_norm_fwd(norm(), FAKE, None, None, FAKE, FAKE, codes=FAKE, stream=0), la.LA_ERR_INVALID_ARG,
