@@ -6,10 +6,11 @@
 //     dX = M^T dY + diag(W) (B dS) + D dY          dS entering = exp(cum_end) dS + C^T diag(exp cum) dY
 //     dC = sum over heads of dG B + diag(exp cum) (dY S^T)
 //     dB = sum over heads of dG^T C + diag(W) (X dS^T)
-//     c_s = column sums of P + tail_s b_s^T dS x_s         (dDelta_s but for the decay's part)
+//     c_s = column sums of P + tail_s b_s^T dS x_s         (dDelta_s but for P_ss and the decay's part)
 //     r_t = row sums of P Delta + exp(cum_t) c_t^T S dy_t
-// cum_t enters the chunk's results as exp(cum_t) on the rows and exp(-cum_s) on the columns, so
-// its gradient is r_t - Delta_t c_t, plus for the last token exp(cum_end) <S, dS> + sum_s Delta_s
+// cum_t enters the chunk's results as exp(cum_t) on the rows and exp(-cum_s) on the columns (not P's
+// diagonal, which both sums leave out: its decay is 1, and its rounding would not cancel), so its
+// gradient is r_t - Delta_t c_t, plus for the last token exp(cum_end) <S, dS> + sum_s Delta_s
 // (c_s's part from dS); a log decay's gradient is the suffix sum of those (in double: the terms
 // cancel), and dDelta, dA follow from it.
 //
@@ -246,6 +247,7 @@ __global__ __launch_bounds__(256) void walk_join_kernel(ScanP p, const float* S0
 struct RateSums {
     double r[kQ], c[kQ], inner[kQ];  // r_t, c_t, and c_t's part from dS
     double sd, dd;                   // <S, dS>, sum of dy x
+    float diag[kQ];                  // P's diagonal
 };
 
 template <class T, int N>
@@ -264,6 +266,7 @@ struct GradLds {
     float rt[2][10][16], ct[2][10][16];          // the pair tiles' row and column sums
     float ri[2][N / 16][kQ], ci[2][N / 16][kQ];  // sums over 16 state rows
     float sd[2][8], dd[2][8];                    // the waves' <S, dS> and diagonals of dM
+    float pd[2][kQ];                             // P's diagonal
 };
 
 __device__ __forceinline__ void lower_tile_of(int k, int& ti, int& si) {
@@ -376,6 +379,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
 
     // kJoin: iteration it's partial sums, added up over a head's tiles; lane = token
     double racc = 0.0, cacc = 0.0, iacc = 0.0, sdacc = 0.0, ddacc = 0.0;
+    float pdacc = 0.0f;
     auto join = [&](int it) {
         const int par = it & 1;
         const int tq = lane >> 4, tl = lane & 15;
@@ -393,6 +397,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         }
         cacc += inner;
         iacc += inner;
+        pdacc += lds.pd[par][lane];
         // lane q: wave q's
         sdacc += lds.sd[par][lane & 7];
         ddacc += lds.dd[par][lane & 7];
@@ -402,12 +407,14 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         o.r[lane] = racc;
         o.c[lane] = cacc;
         o.inner[lane] = iacc;
+        o.diag[lane] = pdacc;
         const double sd = wave_last(wave_prefix(lane < 8 ? sdacc : 0.0)), dd = wave_last(wave_prefix(lane < 8 ? ddacc : 0.0));
         if (lane == 0) {
             o.sd = sd;
             o.dd = dd;
         }
         racc = cacc = iacc = sdacc = ddacc = 0.0;
+        pdacc = 0.0f;
     };
 
     for (int it = 0; it < iters; it++) {
@@ -477,9 +484,12 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                 const float gl = G[q][r] * L, dl = sdl[r];
                 m[r] = gl * dl;
                 dg[r] = L * dl * acc[r];
-                pc[r] = gl * acc[r];
+                pc[r] = s < t ? gl * acc[r] : 0.0f;
                 pr = __builtin_fmaf(pc[r], dl, pr);
-                if (s == t) diag += acc[r];
+                if (s == t) {
+                    diag += acc[r];
+                    lds.pd[par][t] = gl * acc[r];
+                }
             }
             MT::template put4<P2>(&lds.m[0][t * RM + s0], kQ * RM, m);
             MT::template put4<P2>(&lds.dg[0][t * RM + s0], kQ * RM, dg);
@@ -739,7 +749,7 @@ __global__ __launch_bounds__(256) void rates_kernel(ScanP p, const Decay* decays
     if (lane == 63) v += static_cast<double>(d.total[0]) * m.sd + into;
     const double pre = wave_prefix(v);
     const double rate = wave_last(pre) - pre + v;  // the log decay's gradient
-    const float dd = static_cast<float>(c + static_cast<double>(p.A[h]) * rate);
+    const float dd = static_cast<float>(c + static_cast<double>(m.diag[lane]) + static_cast<double>(p.A[h]) * rate);
     const float dz = lane < live ? (p.softplus ? dd * sigmoid_fine(d.z[lane]) : dd) : 0.0f;
     if (lane < live) store_elem(ddt, (sr.begin + static_cast<int64_t>(ch) * kQ + lane) * p.ld_dt + h, p.dt_dtype, dz);
     const float da = static_cast<float>(wave_last(wave_prefix(rate * delta)));

@@ -43,3 +43,22 @@ def test_scan_holds_its_operands(dtype, T, states):
         close(o[k].reshape(w[k].shape), w[k], m[k], parts, k)
     for k in ("dS0", "dD", "ddt", "dA", "ddt_bias"):
         close(o[k].reshape(w[k].shape), w[k], m[k], fine, k)
+
+
+@pytest.mark.parametrize("H,G,N,P", [(2, 1, 16, 64), (6, 2, 64, 192), (3, 3, 128, 128)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_first_tokens_decay_has_no_gradient_without_a_state(dtype, H, G, N, P):
+    """One token and no state: its decay multiplies zeros, so dA is zero and ddt the step's own share,
+    Delta's derivative times b.c x.dy.  Nothing of that product's rounding may reach dA."""
+    s = Scan(dtype, 40, 1, H, G, N, P, states=False, extra=0, rate=16.0)
+    o = s.bwd()
+    assert not o["dA"].any()
+    x, b, c, dy = (np64(t).reshape(40, n, -1) for t, n in ((s.x, H), (s.b, G), (s.c, G), (s.dy, H)))
+    of = np.arange(H) // (H // G)
+    z, _ = R.steps(np64(s.dt), np64(s.bias), 1)
+    sg = 1 / (1 + np.exp(-z))
+    want = (b * c).sum(2)[:, of] * (x * dy).sum(2) * sg
+    mag = np.abs(b * c).sum(2)[:, of] * np.abs(x * dy).sum(2) * sg
+    # two sums of at most 192 FP32 terms, a few roundings each
+    close(o["ddt"].reshape(want.shape), want, mag, 2.0 ** -16, "ddt")
+    close(o["ddt_bias"], want.sum(0), mag.sum(0), 2.0 ** -16, "ddt_bias")
