@@ -265,8 +265,8 @@ struct GradLds {
     // partial sums of the decays' gradients, by parity of the iteration (they are joined beside the next)
     float rt[2][10][16], ct[2][10][16];          // the pair tiles' row and column sums
     float ri[2][N / 16][kQ], ci[2][N / 16][kQ];  // sums over 16 state rows
-    float sd[2][8], dd[2][8];                    // the waves' <S, dS> and diagonals of dM
-    float pd[2][kQ];                             // P's diagonal
+    float sd[2][8];                              // the waves' <S, dS>
+    float pd[2][kQ], dd[2][kQ];                  // the diagonals of P and dM
 };
 
 __device__ __forceinline__ void lower_tile_of(int k, int& ti, int& si) {
@@ -398,9 +398,8 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         cacc += inner;
         iacc += inner;
         pdacc += lds.pd[par][lane];
-        // lane q: wave q's
-        sdacc += lds.sd[par][lane & 7];
-        ddacc += lds.dd[par][lane & 7];
+        ddacc += lds.dd[par][lane];
+        sdacc += lds.sd[par][lane & 7];  // lane q: wave q's
         uint32_t q = static_cast<uint32_t>(it);
         if (take(q, tiles) != tiles - 1) return;
         RateSums& o = sums[slot * p.H + h0 + q];
@@ -408,7 +407,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
         o.c[lane] = cacc;
         o.inner[lane] = iacc;
         o.diag[lane] = pdacc;
-        const double sd = wave_last(wave_prefix(lane < 8 ? sdacc : 0.0)), dd = wave_last(wave_prefix(lane < 8 ? ddacc : 0.0));
+        const double sd = wave_last(wave_prefix(lane < 8 ? sdacc : 0.0)), dd = wave_last(wave_prefix(ddacc));
         if (lane == 0) {
             o.sd = sd;
             o.dd = dd;
@@ -454,7 +453,6 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
 
         // ---- pairs: dM^T tiles (rows s, columns t)
         if (sizeof(T) == 2) fetch_state(next, Sin, Sr);  // (FP32: no registers to hold it so early)
-        float diag = 0.0f;
         {
         const int ln = opaque(lane), lm = ln & 15, g = ln >> 4;
 #pragma unroll
@@ -487,7 +485,7 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
                 pc[r] = s < t ? gl * acc[r] : 0.0f;
                 pr = __builtin_fmaf(pc[r], dl, pr);
                 if (s == t) {
-                    diag += acc[r];
+                    lds.dd[par][t] = acc[r];
                     lds.pd[par][t] = gl * acc[r];
                 }
             }
@@ -502,8 +500,6 @@ __global__ __launch_bounds__(512) void scan_grad_kernel(ScanP p, const T* dyr, c
             }
         }
         }
-        diag = wave_sum(diag);
-        if (lane == 0) lds.dd[par][wave] = diag;
         if (wave == kJoin && it > 0) join(it - 1);
         __syncthreads();
 
@@ -727,16 +723,16 @@ __global__ __launch_bounds__(256) void clear_outside_kernel(ScanP p, T* dx, void
 // The decays' gradients of every chunk, a wave each: the suffix sums of r_t - Delta_t c_t and what
 // the last token gets from the chunk's end, in double (the terms cancel); ddt, and the chunk's
 // share of dA, dD and ddt_bias to hp [slot][3][H].
-__global__ __launch_bounds__(256) void rates_kernel(ScanP p, const Decay* decays, const RateSums* sums, void* ddt, float* hp, uint32_t slots) {
+__global__ __launch_bounds__(256) void rates_kernel(ScanP p, const Decay* decays, const RateSums* sums, void* ddt, double* hp, uint32_t slots) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t su = blockIdx.x * 4u + wave;
     const int h = take(su, p.H);
     if (su >= slots) return;
     const int64_t slot = su;
-    float* o = hp + slot * 3 * p.H + h;
+    double* o = hp + slot * 3 * p.H + h;
     const ChunkAt at = chunk_at(p, su);
     if (!at.used) {
-        if (lane < 3) o[lane * p.H] = 0.0f;
+        if (lane < 3) o[lane * p.H] = 0.0;
         return;
     }
     const SeqRange sr = at.sr;
@@ -752,17 +748,16 @@ __global__ __launch_bounds__(256) void rates_kernel(ScanP p, const Decay* decays
     const float dd = static_cast<float>(c + static_cast<double>(m.diag[lane]) + static_cast<double>(p.A[h]) * rate);
     const float dz = lane < live ? (p.softplus ? dd * sigmoid_fine(d.z[lane]) : dd) : 0.0f;
     if (lane < live) store_elem(ddt, (sr.begin + static_cast<int64_t>(ch) * kQ + lane) * p.ld_dt + h, p.dt_dtype, dz);
-    const float da = static_cast<float>(wave_last(wave_prefix(rate * delta)));
-    const float db = wave_sum(dz);
+    const double da = wave_last(wave_prefix(rate * delta)), db = wave_last(wave_prefix(static_cast<double>(dz)));
     if (lane == 0) {
         o[0] = da;
-        o[p.H] = static_cast<float>(m.dd);
+        o[p.H] = m.dd;
         o[2 * p.H] = db;
     }
 }
 
 // The heads' dA, dD and ddt_bias over all chunks (a packing's unused slots hold zeros).
-__global__ __launch_bounds__(256) void head_sums_kernel(ScanP p, const float* hp, int64_t slots, float* dA, float* dD, float* dbias) {
+__global__ __launch_bounds__(256) void head_sums_kernel(ScanP p, const double* hp, int64_t slots, float* dA, float* dD, float* dbias) {
     __shared__ double red[256];
     const int h = blockIdx.x % p.H, which = blockIdx.x / p.H;
     double s = 0.0;
@@ -810,7 +805,7 @@ BwdWs bwd_ws(const la_scan_config& c, bool packed) {
     w.dbp = w.sums + up(static_cast<size_t>(slots) * c.H * sizeof(RateSums));
     w.dcp = w.dbp + bc;
     w.hp = w.dcp + bc;
-    w.total = w.hp + up(static_cast<size_t>(slots) * 3 * c.H * sizeof(float));
+    w.total = w.hp + up(static_cast<size_t>(slots) * 3 * c.H * sizeof(double));
     return w;
 }
 
@@ -823,7 +818,7 @@ hipError_t launch(const la_scan_config& c, const ScanArgs& a, hipStream_t s) {
     float* dS = reinterpret_cast<float*>(a.ws + w.dS);
     Decay* decays = reinterpret_cast<Decay*>(a.ws + w.decays);
     RateSums* sums = reinterpret_cast<RateSums*>(a.ws + w.sums);
-    float* hp = reinterpret_cast<float*>(a.ws + w.hp);
+    double* hp = reinterpret_cast<double*>(a.ws + w.hp);
     const int64_t rows = a.cu ? c.T : static_cast<int64_t>(c.B) * c.T;
     const int64_t slots = slot_count(c, packed), tiles = c.d_v / kPT;
     const int64_t groups = static_cast<int64_t>(c.B) * c.H * tiles, chunks = slots * c.H * tiles;

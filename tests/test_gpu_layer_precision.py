@@ -62,3 +62,18 @@ def test_first_tokens_decay_has_no_gradient_without_a_state(dtype, H, G, N, P):
     # two sums of at most 192 FP32 terms, a few roundings each
     close(o["ddt"].reshape(want.shape), want, mag, 2.0 ** -16, "ddt")
     close(o["ddt_bias"], want.sum(0), mag.sum(0), 2.0 ** -16, "ddt_bias")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_skip_gradient_is_summed_over_tokens_in_64_bits(dtype):
+    """dy.x of a chunk's 64 tokens: 2^24 for one of them and 1 for each other, which an FP32 sum over
+    the tokens loses (each by itself is exact); the sum of the exact values, rounded once."""
+    for big in (0, 17, 63):
+        s = Scan(dtype, 2, 130, 2, 1, 16, 64, extra=0)
+        x, dy = torch.zeros(260, 2, 64, device="cuda"), torch.zeros(260, 2, 64, device="cuda")
+        x[:, :, 5] = dy[:, :, 5] = 1.0
+        x[64 + big, :, 5] = dy[64 + big, :, 5] = 2.0 ** 12
+        s.x.copy_(x.reshape(260, -1))
+        s.dy.copy_(dy.reshape(260, -1))
+        want = float(np.float32(2.0 ** 24 + 259))
+        assert (s.bwd()["dD"] == want).all()
