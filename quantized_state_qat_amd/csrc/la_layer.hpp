@@ -94,7 +94,7 @@ int64_t scan_bwd_slots(const la_scan_config& c, bool packed);  // chunks of 64 t
 // Workgroups of a launch of 512 threads, and half of those of one of 256: a grid has below 2^32 threads.
 constexpr int64_t kMaxUnits = static_cast<int64_t>(1) << 23;
 
-// out[i] = sum over p < parts of part[p cols + i], p in order within each of 32 interleaved
+// out[i] = sum in double over p < parts of part[p cols + i], p in order within each of 32 interleaved
 // partial sums (a fixed order: the result does not depend on scheduling).  Columns from
 // `split` on go to out2 (may be null).
 hipError_t launch_reduce_parts(const float* part, int parts, int cols, float* out, int split, float* out2,

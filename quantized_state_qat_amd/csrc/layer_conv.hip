@@ -232,7 +232,8 @@ __device__ __forceinline__ void conv_bwd_state(const ConvGeom<T>& g, const T* x,
 // dx the part of dz behind the state, dstate0 the part before; dw[j] = sum_t dpre[t] z[t + j].
 // Work split as in the forward, 32 lanes of four channels by 8 token blocks a workgroup; each walk
 // goes W - 1 tokens past its block for dpre there.  dw and dbias are summed over a lane's walks in
-// registers, over the workgroup in LDS, and over workgroups by a second kernel: no atomics.
+// registers in FP32, and in double over the workgroup in LDS and over workgroups (whose sums are
+// FP32) by a second kernel: no atomics.
 template <class T, int W, int ACT>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* __restrict__ x, const void* w,
                                                        const void* bias, const T* __restrict__ s0,
@@ -365,13 +366,13 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* _
         const int tid = threadIdx.x;
         if (tid < 32 * E) {
             const int l = tid / E, e = tid % E, c = (blockIdx.y * 32 + l) * E + e;
-            float s = 0.0f;
+            double s = 0.0;
 #pragma unroll
             for (int k = 0; k < 8; k++) s += red[k][l][e];
             if (c < g.C) {
                 const size_t at = static_cast<size_t>(blockIdx.x) * g.C * (W + 1) + (j < W ? static_cast<size_t>(c) * W + j
                                                                                           : static_cast<size_t>(g.C) * W + c);
-                part[at] = s;
+                part[at] = static_cast<float>(s);
             }
         }
     }
@@ -418,10 +419,10 @@ __global__ __launch_bounds__(256) void conv_step_kernel(int B, int C, int ldx, i
 
 __global__ __launch_bounds__(1024) void reduce_parts_kernel(const float* __restrict__ part, int parts, int cols,
                                                             float* __restrict__ out, int split, float* __restrict__ out2) {
-    __shared__ float red[32][33];
+    __shared__ double red[32][33];
     const int l = threadIdx.x & 31, q = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + l;
-    float s = 0.0f;
+    double s = 0.0;
     if (col < cols) {
 #pragma unroll 4
         for (int p = q; p < parts; p += 32) s += part[static_cast<size_t>(p) * cols + col];
@@ -429,11 +430,11 @@ __global__ __launch_bounds__(1024) void reduce_parts_kernel(const float* __restr
     red[q][l] = s;
     __syncthreads();
     if (q == 0 && col < cols) {
-        s = 0.0f;
+        s = 0.0;
 #pragma unroll
         for (int k = 0; k < 32; k++) s += red[k][l];
-        if (col < split) out[col] = s;
-        else if (out2) out2[col - split] = s;
+        if (col < split) out[col] = static_cast<float>(s);
+        else if (out2) out2[col - split] = static_cast<float>(s);
     }
 }
 

@@ -263,8 +263,8 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormFwd p) {
 }
 
 // Backward: with r = rstd and g = dy w,  dx = dres + r (g - h r^2 mean(g h)),  dw = sum dy h r.
-// A workgroup walks rows a grid apart, dw's partial sums in registers; they are joined over the
-// workgroup's rows in LDS and over workgroups by a second kernel, in a fixed order.
+// A workgroup walks rows a grid apart, dw's partial sums in registers (FP32); they are joined in
+// double over the workgroup's rows in LDS and over workgroups by a second kernel, in a fixed order.
 struct NormBwd {
     int rows, d, w_dtype;
     float eps;
@@ -337,8 +337,11 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwd p) {
             __syncthreads();
             if (sub == 0) {
 #pragma unroll
-                for (int e = 0; e < 8; e++)
-                    for (int k = 1; k < RPW; k++) dw[c][e] += red[(k * LANES + l) * 8 + e];
+                for (int e = 0; e < 8; e++) {
+                    double s = dw[c][e];
+                    for (int k = 1; k < RPW; k++) s += red[(k * LANES + l) * 8 + e];
+                    dw[c][e] = static_cast<float>(s);
+                }
             }
         }
         if (sub == 0 && col < p.d) store8(p.part + static_cast<size_t>(blockIdx.x) * p.d + col, dw[c]);

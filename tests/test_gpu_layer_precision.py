@@ -77,3 +77,32 @@ def test_skip_gradient_is_summed_over_tokens_in_64_bits(dtype):
         s.dy.copy_(dy.reshape(260, -1))
         want = float(np.float32(2.0 ** 24 + 259))
         assert (s.bwd()["dD"] == want).all()
+
+
+def test_parameter_gradients_are_joined_in_64_bits():
+    """Sums over tokens or rows of one 2^24 and ones that FP32 additions to it would lose.  A lane's
+    own sum (32 tokens; the rows a grid apart) and a workgroup's are FP32 and rounded once: at most
+    half a step of 2 each for the workgroup that holds the 2^24, and the result's own rounding."""
+    T, C = 4096, 1024
+    dy = torch.zeros(T, C, dtype=BF, device="cuda")
+    dy[::32] = 1
+    dy[1024 + 32] = 2.0 ** 24
+    x, w = torch.ones(T, C, dtype=BF, device="cuda"), torch.ones(C, 2, device="cuda")
+    cfg = la.ConvConfig(B=1, T=T, C=C, width=2, act=la.LA_ACT_NONE)
+    n = la.la_conv_bwd_workspace_bytes(cfg)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    dx, dw, db = torch.empty_like(x), torch.empty(C, 2, device="cuda"), torch.empty(C, device="cuda")
+    la.la_conv_bwd(cfg, x, w, None, None, dy, None, dx, dw, db, None, ws, n)
+    want = 2.0 ** 24 + T // 32 - 1
+    for got, v in ((db, want), (dw[:, 1], want), (dw[:, 0], want - 1)):  # (the first token has none before it)
+        assert (got.double() - v).abs().max() <= 2, got.double() - v
+    for rows, d in ((2048, 64), (512, 512)):  # 32 rows and 4 a workgroup, one for a lane
+        h = torch.ones(rows, d, dtype=BF, device="cuda")
+        dy = torch.ones(rows, d, dtype=BF, device="cuda")
+        dy[100] = 2.0 ** 24
+        cfg = la.NormConfig(rows=rows, d=d, eps=0.0)
+        n = la.la_norm_bwd_workspace_bytes(cfg)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        dx, dw = torch.empty_like(h), torch.empty(d, device="cuda")
+        la.la_norm_bwd(cfg, h, None, dy, None, dx, dw, ws, n)
+        assert (dw.double() - (2.0 ** 24 + rows - 1)).abs().max() <= 2, dw
