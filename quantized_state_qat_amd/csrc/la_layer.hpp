@@ -169,11 +169,29 @@ __device__ __forceinline__ float exp_fine(float x) {
     return __builtin_fmaf(r, e * kLn2, r);
 }
 
-// 1 / (1 + exp(-x)) within |x| 2^-23 of itself: the hardware's exponential of the rounded product
-// and its reciprocal, no correction of either (the convolution is bound by its instructions where
-// memory keeps up; the result meets FP32 sums over tokens or a rounding to bf16 next).
+// 1 / (1 + exp(-x)) within (|x| + 2) 2^-23 of itself: the hardware's exponential of the rounded
+// product and its reciprocal, no correction of either (the bf16 convolution is bound by its
+// instructions where memory keeps up, and rounds the result to 2^-8).  0 from x = -89 down, where
+// the exponential is infinite.
 __device__ __forceinline__ float sigmoid_fine(float x) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504088896341f));
+}
+// The same within 4 2^-23 of itself, for results kept in FP32: the product with log2(e) in two parts
+// as in exp_fine and one Newton step for the reciprocal, each skipped where it would meet an infinity.
+__device__ __forceinline__ float sigmoid_full(float x) {
+    constexpr float kL2E = 1.44269502162933349609375f, kL2Elo = 1.925963033500011e-08f, kLn2 = 0.693147180559945309f;
+    const float t = x * -kL2E;
+    const float lo = __builtin_fmaf(x, -kL2Elo, __builtin_fmaf(x, -kL2E, -t));
+    const float r = __builtin_amdgcn_exp2f(t);
+    const float d = 1.0f + (fabsf(t) < 126.0f ? __builtin_fmaf(r, lo * kLn2, r) : r);
+    const float q = __builtin_amdgcn_rcpf(d);
+    return d < 0x1p126f ? __builtin_fmaf(__builtin_fmaf(-d, q, 1.0f), q, q) : q;
+}
+// By the type that holds the result.
+template <class T>
+__device__ __forceinline__ float sigmoid_for(float x) {
+    if constexpr (sizeof(T) == 4) return sigmoid_full(x);
+    else return sigmoid_fine(x);
 }
 
 // Sequence b of a packing, clamped to [0, T].

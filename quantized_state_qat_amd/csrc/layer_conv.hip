@@ -148,7 +148,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvGeom<T> g, const T* _
                     float s = taps.bias[e];
 #pragma unroll
                     for (int j = 0; j < W; j++) s = __builtin_fmaf(taps.w[j][e], win[j][e], s);
-                    out[e] = ACT == LA_ACT_SILU ? s * sigmoid_fine(s) : s;
+                    out[e] = ACT == LA_ACT_SILU ? s * sigmoid_for<T>(s) : s;
                 }
                 store16(y + (begin + p + k) * g.ldy + c0, narrow(out));
             }
@@ -210,7 +210,7 @@ __device__ __forceinline__ void conv_bwd_state(const ConvGeom<T>& g, const T* x,
 #pragma unroll
         for (int e = 0; e < E; e++) {
             if (ACT == LA_ACT_SILU) {
-                const float sg = sigmoid_fine(s[e]);
+                const float sg = sigmoid_for<T>(s[e]);
                 d[e] *= sg * __builtin_fmaf(s[e], 1.0f - sg, 1.0f);
             }
             dp[p][e] = p < len ? d[e] : 0.0f;
@@ -303,7 +303,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvGeom<T> g, const T* _
 #pragma unroll
                         for (int j = 0; j < W; j++) s = __builtin_fmaf(taps.w[j][e], win[j][e], s);
                         if (ACT == LA_ACT_SILU) {
-                            const float sg = sigmoid_fine(s);
+                            const float sg = sigmoid_for<T>(s);
                             d[e] *= sg * __builtin_fmaf(s, 1.0f - sg, 1.0f);
                         }
                         dp[W - 1][e] = inside ? d[e] : 0.0f;
@@ -410,7 +410,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(int B, int C, int ldx, i
     }
     if (ACT == LA_ACT_SILU) {
 #pragma unroll
-        for (int e = 0; e < E; e++) out[e] *= sigmoid_fine(out[e]);
+        for (int e = 0; e < E; e++) out[e] *= sigmoid_for<T>(out[e]);
     }
     store16(y + static_cast<int64_t>(b) * ldy + c0, narrow(out));
 #pragma unroll

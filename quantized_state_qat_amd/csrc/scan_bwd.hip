@@ -746,7 +746,7 @@ __global__ __launch_bounds__(256) void rates_kernel(ScanP p, const Decay* decays
     const double pre = wave_prefix(v);
     const double rate = wave_last(pre) - pre + v;  // the log decay's gradient
     const float dd = static_cast<float>(c + static_cast<double>(m.diag[lane]) + static_cast<double>(p.A[h]) * rate);
-    const float dz = lane < live ? (p.softplus ? dd * sigmoid_fine(d.z[lane]) : dd) : 0.0f;
+    const float dz = lane < live ? (p.softplus ? dd * sigmoid_full(d.z[lane]) : dd) : 0.0f;
     if (lane < live) store_elem(ddt, (sr.begin + static_cast<int64_t>(ch) * kQ + lane) * p.ld_dt + h, p.dt_dtype, dz);
     const double da = wave_last(wave_prefix(rate * delta)), db = wave_last(wave_prefix(static_cast<double>(dz)));
     if (lane == 0) {

@@ -106,3 +106,51 @@ def test_parameter_gradients_are_joined_in_64_bits():
         dx, dw = torch.empty_like(h), torch.empty(d, device="cuda")
         la.la_norm_bwd(cfg, h, None, dy, None, dx, dw, ws, n)
         assert (dw.double() - (2.0 ** 24 + rows - 1)).abs().max() <= 2, dw
+
+
+def test_sigmoids_of_fp32_results_hold_for_large_arguments():
+    """The convolution's SiLU and its derivative and the step's derivative, with FP32 results, over
+    +-80: a sigmoid within 4 x 2^-23 of itself and four roundings more, 2^-20 of the terms."""
+    n, C = 1024, 8
+    x = torch.linspace(-80, 80, n * C, device="cuda").view(n, C)
+    w = torch.zeros(C, 2, device="cuda")
+    w[:, 1] = 1
+    cfg = la.ConvConfig(B=1, T=n, C=C, width=2, x_dtype=CODE[F32])
+    y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w)
+    la.la_conv_fwd(cfg, x, w, None, None, y)
+    b = la.la_conv_bwd_workspace_bytes(cfg)
+    ws = torch.empty(b, dtype=torch.uint8, device="cuda")
+    la.la_conv_bwd(cfg, x, w, None, None, torch.ones_like(x), None, dx, dw, None, None, ws, b)
+    v = np64(x)
+    sg = 1 / (1 + np.exp(-v))
+    close(y, v * sg, np.abs(v * sg), 2.0 ** -20, "y")
+    close(dx, sg * (1 + v * (1 - sg)), sg * (1 + np.abs(v) * (1 - sg)), 2.0 ** -20, "dx")
+    st, ys = torch.zeros(n, 1, C, device="cuda"), torch.empty_like(y)
+    la.la_conv_step(la.ConvConfig(B=n, T=1, C=C, width=2, x_dtype=CODE[F32]), x, w, None, st, ys)
+    assert torch.equal(ys, y)
+    # the scan: one token of ones, b.c x.dy = 16 x 64 exactly
+    H = 512
+    dt = torch.linspace(-80, 80, H, device="cuda").view(1, H)
+    one = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    cfg = la.ScanConfig(B=1, T=1, H=H, G=1, d_k=16, d_v=64, x_dtype=CODE[F32], dt_dtype=CODE[F32], out_dtype=CODE[F32])
+    b = la.la_scan_bwd_workspace_bytes(cfg)
+    ws = torch.empty(b, dtype=torch.uint8, device="cuda")
+    ddt, dA = torch.empty_like(dt), one(H)
+    la.la_scan_bwd(cfg, one(1, H * 64), dt, -one(H), one(1, 16), one(1, 16), None, None, None, one(1, H * 64), None,
+                   one(1, H * 64), ddt, dA, one(1, 16), one(1, 16), None, None, None, ws, b)
+    want = 1024 / (1 + np.exp(-np64(dt)))
+    close(ddt, want, want, 2.0 ** -20, "ddt")
+
+
+def test_silu_at_infinities():
+    """silu(inf) = inf, silu(-inf) = NaN as z / (1 + exp(-z)) has it, and NaN stays."""
+    for dtype in (F32, BF):
+        x = torch.tensor([float("inf"), float("-inf"), float("nan"), 300.0, -300.0, 0.0, -89.5, 89.5], device="cuda").to(dtype)
+        w = torch.zeros(8, 2, device="cuda")
+        w[:, 1] = 1
+        y = torch.empty(1, 8, dtype=dtype, device="cuda")
+        la.la_conv_fwd(la.ConvConfig(B=1, T=1, C=8, width=2, x_dtype=CODE[dtype]), x.view(1, 8), w, None, None, y)
+        v = x.double()
+        want = (v / (1 + torch.exp(-v))).to(dtype)
+        assert torch.equal(y[0].isnan(), want.isnan())
+        torch.testing.assert_close(y[0], want, rtol=0, atol=1e-30, equal_nan=True)
