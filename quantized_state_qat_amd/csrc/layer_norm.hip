@@ -81,11 +81,34 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float* lds) {
     a = (lds[0] + lds[1]) + (lds[2] + lds[3]);
     b = (lds[4] + lds[5]) + (lds[6] + lds[7]);
 }
-// The sum of doubles.
+__device__ __forceinline__ double join64(uint32_t lo, uint32_t hi) {
+    return __builtin_bit_cast(double, static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_double(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    return join64(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, 0xF, 0xF, true),
+                  __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, 0xF, 0xF, true));
+}
+// The sum of doubles, by the exchanges of group_sum (by shuffles: 14.2 us against 12.7 for 40000 rows of 128).
 template <int LANES>
 __device__ __forceinline__ double row_sum_wide(double x, double* lds) {
-#pragma unroll
-    for (int m = 1; m < (LANES < 64 ? LANES : 64); m <<= 1) x += __shfl_xor(x, m);
+    if (LANES >= 2) x += dpp_double<kDppXor1>(x);
+    if (LANES >= 4) x += dpp_double<kDppXor2>(x);
+    if (LANES >= 8) x += dpp_double<kDppHalfMirror>(x);
+    if (LANES >= 16) x += dpp_double<kDppMirror>(x);
+    if (LANES >= 32) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, x);
+        const uint32_t a = static_cast<uint32_t>(u), b = static_cast<uint32_t>(u >> 32);
+        const auto lo = __builtin_amdgcn_permlane16_swap(a, a, false, false), hi = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+        x = join64(lo[0], hi[0]) + join64(lo[1], hi[1]);
+    }
+    if (LANES >= 64) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, x);
+        const uint32_t a = static_cast<uint32_t>(u), b = static_cast<uint32_t>(u >> 32);
+        const auto lo = __builtin_amdgcn_permlane32_swap(a, a, false, false), hi = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+        x = join64(lo[0], hi[0]) + join64(lo[1], hi[1]);
+    }
     if constexpr (LANES <= 64) return x;
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
     __syncthreads();
