@@ -76,9 +76,10 @@ def _library():
     lib = _la.load_library()
     if _torch is None:
         import torch
-        _torch, _types = torch, (torch.float32, torch.bfloat16)
+        _types = (torch.float32, torch.bfloat16)
         # (a stream object costs a microsecond a call, a fifth of a short one)
         _current = getattr(torch._C, "_cuda_getCurrentRawStream", lambda gpu: torch.cuda.current_stream(gpu).cuda_stream)
+        _torch = torch  # (last: another thread's call goes by it)
     return lib
 
 

@@ -2,6 +2,7 @@
 calls, and the binding's own checks."""
 import os
 import re
+import sys
 
 import pytest
 import torch
@@ -225,3 +226,26 @@ def test_binding_refuses_tensors():
         la.la_conv_fwd(conv(), host, FAKE, None, None, FAKE, stream=0)
     with pytest.raises(ValueError, match="weight must be a GPU tensor"):
         la.la_conv_fwd(conv(), FAKE, torch.zeros(64, 4), None, None, FAKE, stream=0)
+
+
+def test_binding_is_whole_once_it_looks_initialised(monkeypatch):
+    """What another thread's call sees between any two lines of the first call's initialisation."""
+    from quantized_state_qat_amd import layers
+    for name, value in (("_torch", None), ("_types", ()), ("_current", None)):
+        monkeypatch.setattr(layers, name, value)
+    lines = []
+
+    def trace(frame, event, arg):
+        if frame.f_code is not layers._library.__code__:
+            return None
+        lines.append(frame.f_lineno)
+        assert layers._torch is None or (len(layers._types) == 2 and callable(layers._current)), frame.f_lineno
+        return trace
+
+    before = sys.gettrace()
+    sys.settrace(trace)
+    try:
+        layers._library()
+    finally:
+        sys.settrace(before)
+    assert len(set(lines)) >= 6 and layers._torch is torch
