@@ -292,12 +292,13 @@ def la_scan_step(cfg: ScanConfig, x, dt, A, b, c, D, dt_bias, S, y, slots=None, 
 
 # -------------------------------------------------- RMS norm with the residual's addition
 def la_norm_fwd(cfg: NormConfig, x, residual, weight, res_out, y, codes=None, scales=None, stream=None) -> None:
-    """res_out = x + residual, y = its RMS norm, and with a quantizer its codes and scales."""
+    """res_out = x + residual, y = its RMS norm, and with a quantizer its codes (uint8, or int8 for
+    INT8 and float8_e4m3fn for E4M3) and scales."""
     lib = _library()
     gpu = _gpu(x, residual, weight, res_out, y, codes, scales)
     n, xt, eight = cfg.rows * cfg.d, _dtype(cfg.x_dtype), _torch.uint8
-    if codes is not None and codes.__class__ is not int and codes.dtype in (_torch.int8, _torch.float8_e4m3fn):
-        eight = codes.dtype
+    if codes is not None and codes.__class__ is not int and codes.dtype is not eight:  # or the codes' own type
+        eight = _torch.int8 if cfg.qdq == _la.LA_QDQ_INT8_GROUP else _torch.float8_e4m3fn
     _call(gpu, stream, lib.la_norm_fwd, cfg,
           _tight(gpu, x, "x", n, xt), _tight(gpu, residual, "residual", n, xt),
           _tight(gpu, weight, "weight", cfg.d, _dtype(cfg.w_dtype)), _tight(gpu, res_out, "res_out", n, xt),

@@ -854,6 +854,21 @@ def test_binding_refuses_layouts():
         la.la_conv_fwd(cfg, x, w.cpu(), None, None, y)
 
 
+@pytest.mark.parametrize("qdq,own,other", [(la.LA_QDQ_INT8_GROUP, torch.int8, torch.float8_e4m3fn),
+                                           (la.LA_QDQ_E4M3_TILE, torch.float8_e4m3fn, torch.int8)])
+def test_binding_takes_codes_of_the_quantizers_type(qdq, own, other):
+    x, cfg = draw(gen(3), 4, 64), la.NormConfig(rows=4, d=64, qdq=qdq)
+    got = []
+    for t in (own, torch.uint8):
+        codes = torch.empty(4, 64, dtype=t, device="cuda")
+        la.la_norm_fwd(cfg, x, None, None, None, None, codes)
+        got.append(codes.view(torch.uint8))
+    assert torch.equal(*got) and got[0].any()
+    for t in (other, torch.float8_e5m2, torch.bool, torch.float16):
+        with pytest.raises(ValueError, match="codes has dtype"):
+            la.la_norm_fwd(cfg, x, None, None, None, None, torch.empty(4, 64, dtype=t, device="cuda"))
+
+
 def test_binding_takes_tensors_after_addresses_and_nulls():
     g = gen(4)
     x, w, st, y = draw(g, 2, 64), draw(g, 64, 4, dtype=F32), draw(g, 2, 3, 64), torch.empty(2, 64, dtype=BF, device="cuda")
