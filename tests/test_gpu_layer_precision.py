@@ -154,3 +154,27 @@ def test_silu_at_infinities():
         want = (v / (1 + torch.exp(-v))).to(dtype)
         assert torch.equal(y[0].isnan(), want.isnan())
         torch.testing.assert_close(y[0], want, rtol=0, atol=1e-30, equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_rates_gradients_are_joined_in_64_bits(dtype):
+    """Steps of 1 and a rate of 0: dA is the sum of (t - s) P_ts with P_ts = dy_t x_s.  x is 2^26 for
+    token 0 and 1 for tokens 16 and 20, dy 2 for token 48 and -3 for token 32: the large terms cancel
+    (48 x 2 = 32 x 3) and leave 32 x 2 - 16 x 3 + 28 x 2 - 12 x 3 = 36.  Row 48's sum 2 (2^26 + 2) and
+    row 32's are not FP32 numbers; those of its 16 x 16 tiles are."""
+    T, H = 64, 2
+    x, dy, b = (torch.zeros(1, T, n, device="cuda") for n in (H * 64, H * 64, 16))
+    x[0, 0, 5::64], x[0, 16, 5::64], x[0, 20, 5::64] = 2.0 ** 26, 1, 1
+    dy[0, 48, 5::64], dy[0, 32, 5::64] = 2, -3
+    b[:, :, 3] = 1
+    x, dy, b = x.to(dtype), dy.to(dtype), b.to(dtype)
+    cfg = la.ScanConfig(B=1, T=T, H=H, G=1, d_k=16, d_v=64, softplus=0, x_dtype=CODE[dtype], dt_dtype=CODE[F32], out_dtype=CODE[dtype])
+    n = la.la_scan_bwd_workspace_bytes(cfg)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    dt, A = torch.ones(1, T, H, device="cuda"), torch.zeros(H, device="cuda")
+    ddt, dA = torch.empty_like(dt), torch.empty_like(A)
+    la.la_scan_bwd(cfg, x, dt, A, b, b, None, None, None, dy, None, torch.empty_like(x), ddt, dA, torch.empty_like(b),
+                   torch.empty_like(b), None, None, None, ws, n)
+    assert (dA == 36).all(), dA
+    # Delta_s: the column sums
+    assert (ddt[0, 0] == -2.0 ** 26).all() and (ddt[0, 16] == -1).all() and (ddt[0, 20] == -1).all() and not ddt[0, 21:].any()
