@@ -1015,3 +1015,24 @@ def test_scan_gradients_without_tokens_past_32_bits():
     la.la_scan_bwd(cfg, None, None, None, None, None, None, None, None, None, dST, None, None, dA, None, None, None, None, dS0,
                    None, 0)
     assert torch.equal(dS0[-1], dST[-1]) and (dS0[:-1].amin(dim=(1, 2, 3)) == 1).all() and not dA.any()
+
+
+@pytest.mark.parametrize("cu", [None, [0, 0, 0], [0, 1, 1]])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_conv_of_no_or_one_token_passes_its_states(dtype, cu):
+    """Sequences shorter than the state: its later rows move up, and their gradient comes back."""
+    g = gen(13)
+    T, C, W = cu[-1] if cu else 0, 40, 4
+    x, w, s0, dsT = draw(g, T, C, dtype=dtype), draw(g, C, W, dtype=F32), draw(g, 2, W - 1, C, dtype=dtype), draw(g, 2, W - 1, C, dtype=dtype)
+    cfg = la.ConvConfig(B=2, T=T, C=C, width=W, x_dtype=CODE[dtype])
+    y, sT, dx, ds0, dw = torch.empty_like(x), torch.empty_like(s0), torch.empty_like(x), torch.empty_like(s0), torch.ones(C, W, device="cuda")
+    la.la_conv_fwd(cfg, x, w, None, s0, y, sT, cu_seqlens=cu_tensor(cu))
+    n = la.la_conv_bwd_workspace_bytes(cfg)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+    la.la_conv_bwd(cfg, x, w, None, s0, torch.zeros_like(x), dsT, dx, dw, None, ds0, ws, n, cu_seqlens=cu_tensor(cu))
+    assert not dw.any() and torch.equal(sT[1], s0[1]) and torch.equal(ds0[1], dsT[1])
+    if T:
+        assert torch.equal(sT[0], torch.cat([s0[0, 1:], x])) and torch.equal(dx, dsT[0, 2:])
+        assert torch.equal(ds0[0, 1:], dsT[0, :2]) and not ds0[0, 0].any()
+    else:
+        assert torch.equal(sT, s0) and torch.equal(ds0, dsT)
