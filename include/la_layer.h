@@ -46,7 +46,7 @@ typedef enum { LA_ACT_NONE = 0, LA_ACT_SILU = 1 } la_act;
  * preceded by the W - 1 rows of its state, z = state0 ++ x,
  *     pre[t][c] = bias[c] + sum_{j < W} weight[c][j] z[t + j][c],   y = silu(pre) or pre,
  *     state_T   = the last W - 1 rows of z.
- * Sums are FP32.  B T C (packed: T C) may be up to 2^36 and B C up to 2^32, and, with the tokens'
+ * Sums are FP32 (dweight and dbias over a lane's tokens, joined in double).  B T C (packed: T C) may be up to 2^36 and B C up to 2^32, and, with the tokens'
  * blocks of 16 n = B ceil(T / 16) (packed: ceil(T / 16)), (n + (W - 1) B) C up to 2^32 - 512
  * pieces of 16 bytes.
  */
@@ -92,6 +92,9 @@ la_status la_conv_step(const la_conv_config* cfg, const void* x, const void* wei
  *     y_t     = S_t^T c_t + D_h x_t
  * The recurrence of la.h with the scalar gate g = Delta A, k = b, q = c and delta = Delta x.
  * Rates Delta A above zero grow the state; cumulated over 64 tokens they must stay below 88.
+ * Steps, decays, states and sums are FP32 or wider.  FP32 inputs meet FP32 products; with bf16 inputs
+ * y, dx, db and dc come from operands held to 2^-17 of a value (two bf16 parts), whatever their type,
+ * S_T, dS0 and the gradients of dt, A, D and dt_bias from exact ones.
  * An infinity or NaN in x reaches the outputs of its whole block of 64 tokens of the sequence
  * (earlier ones too), as one in dt, b or c those from its own token on, and every later one.
  */

@@ -6,11 +6,12 @@
 // row is read once (plus W - 1 rows at the walk's start, which its neighbour has just read);
 // the weights stay in registers.  A walk's first rows are fetched before anything else, ahead of
 // the search for their sequence in a packing (98 -> 83 us) and of the window, in the backward
-// always four tokens ahead (110 -> 105 us).
+// always four tokens ahead (5% less).
 //
-// bf16, C = 2304, W = 4, SiLU: 8 sequences of 4096 tokens forward 61 us (5.4 TB/s), backward 105 us
-// (4.9 TB/s, the vector units 63% busy) and 5 us for the parameters' sums; 40686 tokens in 64
-// packed sequences 83 us (5.0 TB/s); one token of 256 sequences 5.8 us, launch and latencies.
+// bf16, C = 2304, W = 4, SiLU: 8 sequences of 4096 tokens forward 61 us (5.4 TB/s), backward 107 us
+// (4.8 TB/s, the vector units 67% busy) and 5 us for the parameters' sums; 40686 tokens in 64
+// packed sequences 84 us (5.0 TB/s), their backward 162 us; one token of 256 sequences 5.6 us,
+// launch and latencies.
 #include "la_layer.hpp"
 
 namespace la {

@@ -7,8 +7,9 @@
 // CH pieces of 8 consecutive columns, the pieces of neighbouring lanes next to each other: 16
 // or 32 bytes a lane and access, and a codec's group of 16..128 columns is 2..16 neighbouring
 // lanes, whose maximum needs no LDS.  bf16: 40686 rows of 4096 to INT8 codes with a scale for 64
-// and their values 269 us (5.5 TB/s); 32768 rows of 2048 forward 99 us (5.4 TB/s), backward 115 us
-// (4.8 TB/s) and 4.8 us for the weight's sums; 256 rows of 2048 to E4M3 7.2 us, latencies.
+// and their values 270 us by the clock, 283 by the profiler (5.3 TB/s, the vector units 73% busy);
+// 32768 rows of 2048 forward 100 us (5.4 TB/s), backward 114 us (4.8 TB/s) and 5 us for the weight's
+// sums; 256 rows of 2048 to E4M3 7.8 us, latencies (64 of the chip's 256 CUs have rows).
 #include "la_layer.hpp"
 
 namespace la {

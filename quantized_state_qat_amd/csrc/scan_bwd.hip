@@ -14,8 +14,10 @@
 // (c_s's part from dS); a log decay's gradient is the suffix sum of those (in double: the terms
 // cancel), and dDelta, dA follow from it.
 //
-// 8 sequences of 4096 tokens, 16 heads, 128 x 128, bf16: decays 7 us, walks 330 us (0.35 GB read,
-// 1.09 GB written, 4.3 TB/s), gradients 405 us (1.38 GB read, 3.8 TB/s), rates 8 us, sums 5 us.
+// 8 sequences of 4096 tokens, 16 heads, 128 x 128, bf16 (the profiler's medians): decays 7 us, walks
+// 338 us (0.35 GB read, 1.09 GB written, 4.3 TB/s), gradients 462 us (1.38 GB read, 0.17 GB written,
+// 3.3 TB/s), rates 9 us, sums 5 us; one bf16 part for M and dG: 423 us.  64 packed sequences, 40686
+// tokens in all: 1141 us.
 // The FP32 states are 2.1 of those 2.8 GB.  Past the caches their stores and loads cost 4 to 6%.
 #include "la_scan.hpp"
 
@@ -241,9 +243,11 @@ __global__ __launch_bounds__(256) void walk_join_kernel(ScanP p, const float* S0
 }
 
 // What the decays' gradients of one chunk and head are formed from: FP32 sums over a wave's part of
-// a row or column, joined in double (joined in FP32, dA and ddt_bias of 8 x 4096 bf16 tokens and 16
-// heads were up to 2.5 times as far from their 64-bit values as the formulas in FP32 tensor
-// operations; so up to 1.0, for 0.6% of the time).
+// a row or column, joined in double for 0.6% of the time.  Against their 64-bit values, beside the same
+// formulas in FP32 tensor operations with sums over tokens in double: dA and ddt_bias of 8 x 4096
+// bf16 tokens and 16 heads 0.6 times as far (joined in FP32 up to 2.5 times); FP32 inputs, the means
+// over six seeds 0.3 to 0.8 times, ddt_bias of two heads 1.8 times, single seeds 0.1 to 8 times (few
+// sums, which nearly cancel).  dD 1.5 to 5 times: a token's 64 columns are added in FP32.
 struct RateSums {
     double r[kQ], c[kQ], inner[kQ];  // r_t, c_t, and c_t's part from dS
     double sd, dd;                   // <S, dS>, sum of dy x
@@ -278,7 +282,7 @@ __device__ __forceinline__ void lower_tile_of(int k, int& ti, int& si) {
 // columns an iteration.  Pairs: the ten lower tiles over the waves, and beside them the last
 // iteration's sums for the decays' gradients.  dX: a wave 16 columns by 32 tokens.  dC, dB: a
 // wave 16 state rows by all tokens (fewer rows than 128: by a part of them), kept in registers
-// over the heads.  Memory, LDS (conflicts in 17% of the cycles) and the vector units (41%) share
+// over the heads.  Memory, LDS (conflicts in 19% of the cycles) and the vector units (41%) share
 // the time: b^T and c^T, which do not change over the heads, stay in registers, and the next
 // iteration's loads are issued in three places.  dbp, dcp: FP32 partial sums of db and dc per
 // slice ([slice][row][G][dk]), or null where one slice holds the whole group.

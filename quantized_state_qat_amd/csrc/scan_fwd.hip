@@ -9,15 +9,16 @@
 // products as two bf16 parts (2^-17 of a value, for a bf16 result), W x as three (exact; two
 // cost a tenth of the time less, but the final states were then further from their 64-bit values
 // than FP32 arithmetic's).  LDS and the chain of reads, products and operand splits of waves 4..7 bound it, not
-// memory: with d_k = 128 a chunk takes 2.6 us for 64 columns, 4.7 us for 128.  8 sequences of
-// 4096 tokens, 16 heads, d_v = 128: 166 us; 64 packed sequences, 40686 tokens in all: 261 us.
+// memory: with d_k = 128 a chunk takes 2.8 us for 64 columns, 4.7 us for 128.  8 sequences of
+// 4096 tokens, 16 heads, d_v = 128: 182 us by the clock, 196 by the profiler; 64 packed sequences,
+// 40686 tokens in all: 245 to 262 us and 277.
 // Every wave doing every part in turn took 5.3 us a chunk of 64 columns; sixteen waves in the
 // same roles 5% more, and c's rows loaded from memory by waves 4..7 themselves 60% more than this.
 //
 // Few heads and long sequences: the walk is cut into segments that run side by side.  A first
 // pass forms each segment's own contribution to the state from zero, a small kernel joins them
 // (S_in of every segment), and the full walk starts every segment from its S_in (32768 tokens,
-// 32 heads of d_v = 64: 75 + 10 + 155 us by the profiler, 216 us by the clock).
+// 32 heads of d_v = 64: 80 + 8 + 168 us by the profiler, 214 to 219 us by the clock).
 #include "la_scan.hpp"
 
 namespace la {

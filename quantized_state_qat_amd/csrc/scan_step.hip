@@ -3,8 +3,8 @@
 //
 // Every state element is read and written once (8 N P bytes a head against 6 N P operations):
 // memory bound, the state's 16-byte accesses all issued before the first is used and passing the
-// caches by (256 sequences of 16 heads, 128 x 128, in shuffled slots: 104 us, 5.2 TB/s, against
-// 120 us through them).  A workgroup
+// caches by (256 sequences of 16 heads, 128 x 128, in shuffled slots: 110 us, 4.9 TB/s; through them
+// 15% more).  A workgroup
 // owns COLS columns of one head; a lane holds 4 columns of N COLS / 1024 rows, and y's sum over
 // rows is joined over the wave by lane exchanges and over the four waves in LDS.
 #include "la_layer.hpp"
