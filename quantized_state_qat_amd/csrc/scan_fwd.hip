@@ -8,7 +8,9 @@
 // with two LDS buffers and the loads of chunk i + 2 issued at step i.  M and the state enter the
 // products as two bf16 parts (2^-17 of a value, for a bf16 result), W x as three (exact; two
 // cost a tenth of the time less, but the final states were then further from their 64-bit values
-// than FP32 arithmetic's).  LDS and the chain of reads, products and operand splits of waves 4..7 bound it, not
+// than FP32 arithmetic's).  bf16 results lie 1.0e-4 from those of FP32 arithmetic, most of it from D x,
+// where D sits on M's diagonal, and as near to their 64-bit values (1.66e-3); D x added by itself
+// took that to 2.7e-5 and to the same 1.66e-3, for 3 to 7% more time.  LDS and the chain of reads, products and operand splits of waves 4..7 bound it, not
 // memory: with d_k = 128 a chunk takes 2.8 us for 64 columns, 4.7 us for 128.  8 sequences of
 // 4096 tokens, 16 heads, d_v = 128: 182 us by the clock, 196 by the profiler; 64 packed sequences,
 // 40686 tokens in all: 245 to 262 us and 277.
