@@ -209,9 +209,7 @@ def _own_linear(s, la):
     cfg = la.LinearConfig(M=M, N=N, K=K, x_dtype=code[t], out_dtype=code[t], w_dtype=la.LA_F32, dw_dtype=code[dwt])
     dev = s["xc"].device
     y = torch.empty(M, N, dtype=t, device=dev)
-    n = la.la_linear_workspace_bytes(cfg)
-    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    la.la_linear_fwd(cfg, s["xc"], s["xs"], s["wc"], s["ws"], s["bias"], y, ws, n)
+    la.la_linear_fwd(cfg, s["xc"], s["xs"], s["wc"], s["ws"], s["bias"], y)
     out = dict(y=y)
     if train:
         dx = torch.empty(M, K, dtype=t, device=dev)
@@ -262,8 +260,7 @@ def run(state):
     if own:
         import quantized_state_qat_amd as la
         return (_own_linear if linear else _own_gate)(state, la)
-    out = (_plain_linear if linear else _plain_gate)(state)
-    return out
+    return (_plain_linear if linear else _plain_gate)(state)
 
 
 # ------------------------------------------------------------------------------------- work
