@@ -124,6 +124,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.la_bwd_kernel_name.restype = ctypes.c_char_p
         lib.la_bwd_kernel_name.argtypes = [cp]
         layers.declare(lib)
+        projections.declare(lib)
         _lib = lib
     return _lib
 
@@ -465,3 +466,5 @@ from .layers import (LA_ACT_NONE, LA_ACT_SILU, ConvConfig, NormConfig, ScanConfi
                      la_norm_fwd, la_scan_bwd, la_scan_bwd_varlen_workspace_bytes, la_scan_bwd_workspace_bytes,
                      la_scan_fwd, la_scan_step,
                      la_scan_workspace_bytes)
+from . import projections  # noqa: E402
+from .projections import (LinearConfig, la_linear_bwd, la_linear_bwd_workspace_bytes, la_linear_fwd)  # noqa: E402,F401

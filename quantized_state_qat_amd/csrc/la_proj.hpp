@@ -1,0 +1,27 @@
+// Internal interface of the operators between two recurrences (matrix product of 8-bit codes, norms
+// around a block): the launchers behind la_proj.cpp.
+#pragma once
+
+#include "../../include/la_proj.h"
+#include "la_layer.hpp"
+
+namespace la {
+
+struct LinearArgs {
+    const int8_t* x = nullptr;
+    const float* xs = nullptr;
+    const int8_t* w = nullptr;
+    const float* ws = nullptr;
+    const void* bias = nullptr;
+    void* y = nullptr;
+    const void* dy = nullptr;
+    void* dx = nullptr;
+    void* dw = nullptr;
+    float* dbias = nullptr;
+    char* work = nullptr;
+};
+hipError_t launch_linear_fwd(const la_linear_config& c, const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_bwd(const la_linear_config& c, const LinearArgs& a, hipStream_t s);
+size_t linear_bwd_workspace(const la_linear_config& c);
+
+}  // namespace la

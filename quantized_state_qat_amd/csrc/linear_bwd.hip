@@ -1,0 +1,267 @@
+// Straight-through gradients of the product of 8-bit codes: dx = (dy s_w) c_w, dweight = (dy s_x)^T c_x.
+//
+// Both are products on the FP16 matrix cores: FP16 holds every code exactly, and dy times the scale,
+// brought to [2^14, 2^15) by a power of two for each row of the operand (scale_up), is off by at most
+// 2^-11 of itself in one part, for bf16 results, and 2^-22 in two, for FP32 ones (bf16 would be off by
+// 2^-8, as much as a bf16 result's own rounding).
+// The products sum over an index that is not contiguous in what the caller holds (channels of dx,
+// tokens of dweight), so a pass over dy and one over each matrix of codes lay the operands out first,
+// 128 bytes of the summed index at a time: they move 2 to 8 bytes an element once where the product
+// itself reads an operand many times over.
+#include "linear_gemm.hpp"
+
+namespace la {
+namespace {
+
+__device__ __forceinline__ uint32_t finite_abs(float v) {
+    const uint32_t u = __float_as_uint(v) & 0x7FFFFFFFu;
+    return u < 0x7F800000u ? u : 0;
+}
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// 8 elements of a row from column n on, zeros from N on.
+template <class T>
+__device__ __forceinline__ void load_part(const T* row, int n, int N, int wide, float (&v)[8]) {
+    if (wide && n + 8 <= N) {
+        if constexpr (sizeof(T) == 2) {
+            widen(load16(row + n), v);
+        } else {
+            float a[4], b[4];
+            widen(load16(row + n), a);
+            widen(load16(row + n + 4), b);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                v[e] = a[e];
+                v[4 + e] = b[e];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++) v[e] = n + e < N ? load_elem(row, n + e, sizeof(T) == 2 ? LA_BF16 : LA_F32) : 0.0f;
+    }
+}
+
+struct DyArgs {
+    const void* dy;
+    const float* xs;
+    const float* ws;
+    int M, N, wide;
+    int64_t ld;
+    uint32_t* rowmax;  // [M] of |dy s_w|, or null
+    uint32_t* colmax;  // [N] of |dy s_x|, or null
+    float* part;       // [ceil(M / 64)][N], or null
+    char* qx;          // [M][Npad] parts, or null
+    char* qw;          // [N][Mpad] parts, or null
+    int px, pw;        // parts
+};
+
+__global__ void clear_kernel(uint32_t* p, int64_t n) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i < n) p[i] = 0;
+}
+
+// Largest magnitudes of rows and columns (integer maxima: their order does not matter) and the sums
+// of 64 rows: a workgroup has 64 rows of 256 columns.
+template <class T>
+__global__ __launch_bounds__(256) void stats_kernel(DyArgs a) {
+    __shared__ float sum[8][256];
+    __shared__ uint32_t top[8][256];
+    const int across = (a.N + 255) / 256;
+    const int n0 = (blockIdx.x % across) * 256, m0 = (blockIdx.x / across) * 64;
+    const int c = (threadIdx.x & 31) * 8, ty = threadIdx.x >> 5, n = n0 + c;
+    float ws[8], cs[8] = {};
+    uint32_t cm[8] = {};
+#pragma unroll
+    for (int e = 0; e < 8; e++) ws[e] = a.rowmax && n + e < a.N ? a.ws[n + e] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+        const int m = m0 + ty + 8 * k;
+        float v[8] = {};
+        float xs = 0.0f;
+        if (m < a.M) {
+            load_part(static_cast<const T*>(a.dy) + m * a.ld, n, a.N, a.wide, v);
+            xs = a.colmax ? a.xs[m] : 0.0f;
+        }
+        uint32_t rm = 0;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            rm = umax(rm, finite_abs(v[e] * ws[e]));
+            cm[e] = umax(cm[e], finite_abs(v[e] * xs));
+            cs[e] += v[e];
+        }
+        rm = __float_as_uint(group_max_abs<32>(__uint_as_float(rm)));
+        if (a.rowmax && (threadIdx.x & 31) == 0 && rm) atomicMax(a.rowmax + m, rm);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        sum[ty][c + e] = cs[e];
+        top[ty][c + e] = cm[e];
+    }
+    __syncthreads();
+    const int col = n0 + threadIdx.x;
+    if (col >= a.N) return;
+    float s = 0.0f;
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+        s += sum[k][threadIdx.x];
+        m = umax(m, top[k][threadIdx.x]);
+    }
+    if (a.part) a.part[static_cast<int64_t>(blockIdx.x / across) * a.N + col] = s;
+    if (a.colmax && m) atomicMax(a.colmax + col, m);
+}
+
+__device__ __forceinline__ _Float16 low_part(float v, _Float16 hi) {
+    const float h = static_cast<float>(hi);
+    return fabsf(h) < 65536.0f ? static_cast<_Float16>(v - h) : static_cast<_Float16>(0.0f);  // (infinite and NaN: in hi)
+}
+
+// A part is 64 elements = 128 bytes of the summed index; a row holds chunk c's parts beside each other.
+__device__ __forceinline__ int64_t part_at(int chunk, int part, int parts) { return (static_cast<int64_t>(chunk) * parts + part) * 128; }
+
+// 64 x 64 of dy into both operands.
+template <class T>
+__global__ __launch_bounds__(256) void lay_dy_kernel(DyArgs a) {
+    __shared__ float tile[64][65];
+    const int across = (a.N + 63) / 64;
+    const int cn = blockIdx.x % across, cm = blockIdx.x / across;
+    const int n0 = cn * 64, m0 = cm * 64;
+    const int64_t rowx = part_at((a.N + 63) / 64, 0, a.px), roww = part_at((a.M + 63) / 64, 0, a.pw);
+    const int c = (threadIdx.x & 7) * 8;
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const int rr = (threadIdx.x >> 3) + 32 * k, m = m0 + rr, n = n0 + c;
+        float v[8] = {};
+        if (m < a.M) load_part(static_cast<const T*>(a.dy) + m * a.ld, n, a.N, a.wide, v);
+#pragma unroll
+        for (int e = 0; e < 8; e++) tile[rr][c + e] = v[e];
+        if (a.qx && m < a.M) {
+            const float up = scale_up(a.rowmax[m]);
+            hv8 hi, lo;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const float p = n + e < a.N ? v[e] * a.ws[n + e] * up : 0.0f;
+                hi[e] = static_cast<_Float16>(p);
+                lo[e] = low_part(p, hi[e]);
+            }
+            char* o = a.qx + m * rowx + part_at(cn, 0, a.px) + 2 * c;
+            *reinterpret_cast<hv8*>(o) = hi;
+            if (a.px == 2) *reinterpret_cast<hv8*>(o + 128) = lo;
+        }
+    }
+    if (!a.qw) return;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const int rr = (threadIdx.x >> 3) + 32 * k, n = n0 + rr;
+        if (n >= a.N) continue;
+        const float up = scale_up(a.colmax[n]);
+        hv8 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            const int m = m0 + c + e;
+            const float p = m < a.M ? tile[c + e][rr] * a.xs[m] * up : 0.0f;
+            hi[e] = static_cast<_Float16>(p);
+            lo[e] = low_part(p, hi[e]);
+        }
+        char* o = a.qw + n * roww + part_at(cm, 0, a.pw) + 2 * c;
+        *reinterpret_cast<hv8*>(o) = hi;
+        if (a.pw == 2) *reinterpret_cast<hv8*>(o + 128) = lo;
+    }
+}
+
+// Codes [R][C] (rows ld bytes apart, C a multiple of 16) to FP16 [C][Rpad]: 64 x 64 a workgroup.
+__global__ __launch_bounds__(256) void lay_codes_kernel(const int8_t* codes, int64_t ld, int R, int C, char* out) {
+    __shared__ __align__(16) int8_t tile[64][80];
+    const int across = (C + 63) / 64;
+    const int c0 = (blockIdx.x % across) * 64, cr = blockIdx.x / across, r0 = cr * 64;
+    {
+        const int rr = threadIdx.x >> 2, c = (threadIdx.x & 3) * 16;
+        uv4 v = {};
+        if (r0 + rr < R && c0 + c < C) v = load16(codes + (r0 + rr) * ld + c0 + c);
+        *reinterpret_cast<uv4*>(&tile[rr][c]) = v;
+    }
+    __syncthreads();
+    const int64_t row = part_at((R + 63) / 64, 0, 1);
+    const int c = (threadIdx.x & 7) * 8;
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const int rr = (threadIdx.x >> 3) + 32 * k;
+        if (c0 + rr >= C) continue;
+        hv8 h;
+#pragma unroll
+        for (int e = 0; e < 8; e++) h[e] = static_cast<_Float16>(tile[c + e][rr]);
+        *reinterpret_cast<hv8*>(out + (c0 + rr) * row + part_at(cr, 0, 1) + 2 * c) = h;
+    }
+}
+
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// What the workspace holds, in this order.
+struct Layout {
+    size_t rowmax, colmax, part, qx, qw, pw, px, end;  // offsets; pw: w's codes, px: x's
+    int parts_x, parts_w;
+};
+Layout layout(const la_linear_config& c) {
+    Layout l;
+    l.parts_x = c.x_dtype == LA_F32 ? 2 : 1, l.parts_w = c.dw_dtype == LA_F32 ? 2 : 1;
+    const size_t M = c.M, N = c.N, K = c.K, mc = (M + 63) / 64, nc = (N + 63) / 64;
+    size_t at = 0;
+    auto take = [&](size_t n) { const size_t p = at; at += up256(n); return p; };
+    l.rowmax = take(4 * M), l.colmax = take(4 * N), l.part = take(4 * mc * N);
+    l.qx = take(M * nc * 128 * l.parts_x), l.qw = take(N * mc * 128 * l.parts_w);
+    l.pw = take(K * nc * 128), l.px = take(K * mc * 128);
+    l.end = at;
+    return l;
+}
+
+}  // namespace
+
+size_t linear_bwd_workspace(const la_linear_config& c) { return layout(c).end; }
+
+hipError_t launch_linear_bwd(const la_linear_config& c, const LinearArgs& a, hipStream_t s) {
+    const Layout l = layout(c);
+    const int es = c.out_dtype == LA_BF16 ? 2 : 4;
+    DyArgs d{};
+    d.dy = a.dy, d.xs = a.xs, d.ws = a.ws, d.M = c.M, d.N = c.N, d.ld = c.ld_y ? c.ld_y : c.N;
+    d.wide = d.ld * es % 16 == 0;
+    d.rowmax = a.dx ? reinterpret_cast<uint32_t*>(a.work + l.rowmax) : nullptr;
+    d.colmax = a.dw ? reinterpret_cast<uint32_t*>(a.work + l.colmax) : nullptr;
+    d.part = a.dbias ? reinterpret_cast<float*>(a.work + l.part) : nullptr;
+    d.qx = a.dx ? a.work + l.qx : nullptr, d.qw = a.dw ? a.work + l.qw : nullptr;
+    d.px = l.parts_x, d.pw = l.parts_w;
+    const int64_t words = static_cast<int64_t>((l.part - l.rowmax) / 4);
+    const int64_t mc = (c.M + 63) / 64, nc = (c.N + 63) / 64, kc = (c.K + 63) / 64;
+    const auto blocks = [](int64_t n) { return dim3(static_cast<unsigned>(n)); };
+    if (words > 0) clear_kernel<<<blocks((words + 255) / 256), 256, 0, s>>>(reinterpret_cast<uint32_t*>(a.work + l.rowmax), words);
+    const bool work = c.M > 0 && c.N > 0;  // (otherwise the sums are empty: zeros)
+    if (!work) {
+    } else if (es == 2) stats_kernel<uint16_t><<<blocks(mc * ((c.N + 255) / 256)), 256, 0, s>>>(d);
+    else stats_kernel<float><<<blocks(mc * ((c.N + 255) / 256)), 256, 0, s>>>(d);
+    if (hipError_t e = hipGetLastError()) return e;
+    if (a.dbias && c.N > 0)
+        if (hipError_t e = launch_reduce_parts(d.part, static_cast<int>(mc), c.N, a.dbias, c.N, nullptr, s)) return e;
+    if (!a.dx && !a.dw) return hipSuccess;
+    if (!work) {
+    } else if (es == 2) lay_dy_kernel<uint16_t><<<blocks(mc * nc), 256, 0, s>>>(d);
+    else lay_dy_kernel<float><<<blocks(mc * nc), 256, 0, s>>>(d);
+    if (a.dx && c.M > 0) {
+        if (nc > 0) lay_codes_kernel<<<blocks(nc * kc), 256, 0, s>>>(a.w, c.K, c.N, c.K, a.work + l.pw);
+        GemmArgs g;
+        g.P = a.work + l.pw, g.ldP = nc * 128, g.I = c.K, g.kbytes = static_cast<int>(nc * 128);
+        g.Q = d.qx, g.ldQ = nc * 128 * d.px, g.J = c.M, g.shift = d.px - 1;
+        g.row = d.rowmax, g.out = a.dx, g.ldo = c.K, g.wide = 1;
+        if (hipError_t e = launch_gemm<_Float16, true>(g, c.x_dtype, s)) return e;
+    }
+    if (a.dw && c.N > 0) {
+        if (mc > 0) lay_codes_kernel<<<blocks(mc * kc), 256, 0, s>>>(a.x, c.ld_x ? c.ld_x : c.K, c.M, c.K, a.work + l.px);
+        GemmArgs g;
+        g.P = a.work + l.px, g.ldP = mc * 128, g.I = c.K, g.kbytes = static_cast<int>(mc * 128);
+        g.Q = d.qw, g.ldQ = mc * 128 * d.pw, g.J = c.N, g.shift = d.pw - 1;
+        g.row = d.colmax, g.out = a.dw, g.ldo = c.K, g.wide = 1;
+        if (hipError_t e = launch_gemm<_Float16, true>(g, c.dw_dtype, s)) return e;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace la
