@@ -65,6 +65,61 @@ la_status la_linear_bwd(const la_linear_config* cfg, const void* x_codes, const 
                         size_t ws_bytes, void* stream);
 size_t la_linear_bwd_workspace_bytes(const la_linear_config* cfg);
 
+/* ------------------------------------------- norms around a block, its gate and residual scale */
+
+typedef enum { LA_GATE_NONE = 0, LA_GATE_SILU = 1, LA_GATE_SIGMOID = 2 } la_out_gate;
+
+/*
+ * Per row of d columns, with act the gate's function and rms(v) = sqrt(mean(v^2) + eps):
+ *     u = x act(z)  (gate_first)  or  x
+ *     n = u / rms(u) * w_post  (post = 1; over each `head` columns, or over the row)  or  u
+ *     p = n  (gate_first or no gate)  or  n act(z)
+ *     t = residual + alpha p,      h = t rounded to x_dtype
+ *     v = h / rms(h) * w_pre  (pre = 1; over the row)  or  t
+ * and, with a quantizer, the codecs of la_norm_fwd on v: y is then the value that a code stands for.
+ * post alone is the gated output norm of a recurrence (silu: gated delta rule; sigmoid: per-channel
+ * gates; gate_first: state-space layers), post and pre the join of a block's output to the residual
+ * stream and the next block's norm; with neither, no gate and no residual, the codes are x's own.
+ * Everything is FP32 or wider but h (and y, dx, dz, dres at their types).  Codes and scales are the
+ * same for every out_dtype and without y.  NaN and infinities reach what the formula takes them to;
+ * codes that stand for NaN are as in la_norm_fwd.
+ */
+typedef struct la_gate_norm_config {
+    int32_t rows, d;    /* (rows + 31) min(256, max(8, d / 4)) below 2^32; d a multiple of 8 up to 16384 */
+    int32_t head;       /* columns of one norm after the block: 0 (the row), 16, 32, 64, 128, 256 or 512, dividing d */
+    float eps;          /* >= 0 */
+    int32_t gate;       /* la_out_gate */
+    int32_t gate_first; /* 0 | 1 */
+    int32_t post, pre;  /* 0 | 1 */
+    int32_t qdq;        /* la_qdq, as in la_norm_config */
+    int32_t group;      /* with a quantizer 0 (one scale a row), 16, 32, 64 or 128, dividing d */
+    int32_t x_dtype;    /* la_dtype of x, z, residual, h and their gradients */
+    int32_t w_dtype;    /* la_dtype of w_post, alpha and w_pre (their gradients are float32) */
+    int32_t out_dtype;  /* la_dtype of y and dy */
+    int32_t ld_x;       /* row stride of x and dx, a multiple of 16 bytes (0 = d) */
+    int32_t ld_z;       /* row stride of z and dz, a multiple of 16 bytes (0 = d) */
+} la_gate_norm_config;
+
+/* x [rows][d]; z [rows][d] with a gate, else NULL; w_post [head or d] (post) or NULL (ones); alpha [d] or
+ * NULL (ones); residual [rows][d] or NULL (zeros); w_pre [d] (pre) or NULL (ones); h and y [rows][d], codes
+ * (int8 or E4M3FN bits [rows][d]) and scales (float [rows][d / group]), each NULL where it is not wanted.
+ * h may be residual itself (updated in place); no other overlap. */
+la_status la_gate_norm_fwd(const la_gate_norm_config* cfg, const void* x, const void* z, const void* w_post, const void* alpha,
+                           const void* residual, const void* w_pre, void* h, void* y, void* codes, float* scales,
+                           void* stream);
+
+/* Gradients for the upstream gradients dy (of y; identity straight through the codec and h's rounding)
+ * and dh (of h; NULL = zero), from x, z and, with pre, the forward's h (else it may be NULL): dx; dz (with a
+ * gate; may be NULL); dres (may be NULL; may be dh itself); dw_post float [head or d] (post), dalpha float
+ * [d], dw_pre float [d] (pre), each may be NULL, summed in FP32 over a workgroup's rows and in double over
+ * workgroups and heads.  Workspace: at least la_gate_norm_bwd_workspace_bytes(cfg) bytes (needed for
+ * these three). */
+la_status la_gate_norm_bwd(const la_gate_norm_config* cfg, const void* x, const void* z, const void* w_post, const void* alpha,
+                           const void* h, const void* w_pre, const void* dy, const void* dh, void* dx, void* dz,
+                           void* dres, float* dw_post, float* dalpha, float* dw_pre, void* workspace, size_t ws_bytes,
+                           void* stream);
+size_t la_gate_norm_bwd_workspace_bytes(const la_gate_norm_config* cfg);
+
 #ifdef __cplusplus
 }
 #endif

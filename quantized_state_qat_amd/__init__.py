@@ -467,4 +467,6 @@ from .layers import (LA_ACT_NONE, LA_ACT_SILU, ConvConfig, NormConfig, ScanConfi
                      la_scan_fwd, la_scan_step,
                      la_scan_workspace_bytes)
 from . import projections  # noqa: E402
-from .projections import (LinearConfig, la_linear_bwd, la_linear_bwd_workspace_bytes, la_linear_fwd)  # noqa: E402,F401
+from .projections import (LA_GATE_NONE, LA_GATE_SIGMOID, LA_GATE_SILU, GateNormConfig, LinearConfig,  # noqa: E402,F401
+                          la_gate_norm_bwd, la_gate_norm_bwd_workspace_bytes, la_gate_norm_fwd, la_linear_bwd,
+                          la_linear_bwd_workspace_bytes, la_linear_fwd)

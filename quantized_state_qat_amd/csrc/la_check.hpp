@@ -59,4 +59,16 @@ la_status check_workspace(const void* ws, size_t given, size_t need) {
     return LA_OK;
 }
 
+// A row's codec: la_norm_config's qdq and group for rows of d columns.
+la_status check_codec(int qdq, int group, int d) {
+    if (qdq == LA_QDQ_NONE) return LA_OK;
+    if (qdq != LA_QDQ_INT8_GROUP && qdq != LA_QDQ_E4M3_TILE)
+        return fail(LA_ERR_INVALID_ARG, "unknown qdq mode %d", qdq);
+    if (group != 0 && group != 16 && group != 32 && group != 64 && group != 128)
+        return fail(LA_ERR_UNSUPPORTED, "group must be 0 (the row), 16, 32, 64 or 128 (group=%d)", group);
+    if (group != 0 && d % group != 0)
+        return fail(LA_ERR_INVALID_ARG, "group must divide d (d=%d group=%d)", d, group);
+    return LA_OK;
+}
+
 }  // namespace

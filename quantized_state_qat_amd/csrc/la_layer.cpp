@@ -116,14 +116,7 @@ la_status check_norm(const la_norm_config* c) {
     CHECK(check_dtype(c->x_dtype, "x_dtype"));
     CHECK(check_dtype(c->w_dtype, "w_dtype"));
     CHECK(check_dtype(c->out_dtype, "out_dtype"));
-    if (c->qdq == LA_QDQ_NONE) return LA_OK;
-    if (c->qdq != LA_QDQ_INT8_GROUP && c->qdq != LA_QDQ_E4M3_TILE)
-        return fail(LA_ERR_INVALID_ARG, "unknown qdq mode %d", c->qdq);
-    if (c->group != 0 && c->group != 16 && c->group != 32 && c->group != 64 && c->group != 128)
-        return fail(LA_ERR_UNSUPPORTED, "group must be 0 (the row), 16, 32, 64 or 128 (group=%d)", c->group);
-    if (c->group != 0 && c->d % c->group != 0)
-        return fail(LA_ERR_INVALID_ARG, "group must divide d (d=%d group=%d)", c->d, c->group);
-    return LA_OK;
+    return check_codec(c->qdq, c->group, c->d);
 }
 
 }  // namespace

@@ -24,4 +24,29 @@ hipError_t launch_linear_fwd(const la_linear_config& c, const LinearArgs& a, hip
 hipError_t launch_linear_bwd(const la_linear_config& c, const LinearArgs& a, hipStream_t s);
 size_t linear_bwd_workspace(const la_linear_config& c);
 
+struct GateArgs {
+    const void* x = nullptr;
+    const void* z = nullptr;
+    const void* w_post = nullptr;
+    const void* alpha = nullptr;
+    const void* res = nullptr;
+    const void* w_pre = nullptr;
+    void* h = nullptr;  // the backward's input
+    void* y = nullptr;
+    void* codes = nullptr;
+    float* scales = nullptr;
+    const void* dy = nullptr;
+    const void* dh = nullptr;
+    void* dx = nullptr;
+    void* dz = nullptr;
+    void* dres = nullptr;
+    float* dw_post = nullptr;
+    float* dalpha = nullptr;
+    float* dw_pre = nullptr;
+    float* part = nullptr;
+};
+hipError_t launch_gate_fwd(const la_gate_norm_config& c, const GateArgs& a, hipStream_t s);
+hipError_t launch_gate_bwd(const la_gate_norm_config& c, const GateArgs& a, hipStream_t s);
+size_t gate_bwd_workspace(const la_gate_norm_config& c);
+
 }  // namespace la

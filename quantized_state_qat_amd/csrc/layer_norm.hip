@@ -10,129 +10,10 @@
 // and their values 270 us by the clock, 283 by the profiler (5.3 TB/s, the vector units 73% busy);
 // 32768 rows of 2048 forward 100 us (5.4 TB/s), backward 114 us (4.8 TB/s) and 5 us for the weight's
 // sums; 256 rows of 2048 to E4M3 7.8 us, latencies (64 of the chip's 256 CUs have rows).
-#include "la_layer.hpp"
+#include "la_norm.hpp"
 
 namespace la {
 namespace {
-
-constexpr int kPiece = 8;
-
-template <class T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        widen(load16(p), v);
-    } else {
-        float a[4], b[4];
-        widen(load16(p), a);
-        widen(load16(p + 4), b);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-    }
-}
-template <class T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        store16(p, narrow(v));
-    } else {
-        store16(p, uv4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
-        store16(p + 4, uv4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
-    }
-}
-__device__ __forceinline__ void load_w(const void* w, int dtype, int col, float (&v)[8]) {
-    if (!w) {
-#pragma unroll
-        for (int e = 0; e < 8; e++) v[e] = 1.0f;
-    } else if (dtype == LA_BF16) {
-        load8(static_cast<const uint16_t*>(w) + col, v);
-    } else {
-        load8(static_cast<const float*>(w) + col, v);
-    }
-}
-
-// The larger of a magnitude and |b|, a NaN above every number (fmaxf would drop it).
-__device__ __forceinline__ float larger_abs(float a, float b) {
-    const uint32_t u = __float_as_uint(a), v = __float_as_uint(b) & 0x7FFFFFFFu;
-    return __uint_as_float(u > v ? u : v);
-}
-
-// Sum over the row's lanes, the same bits in each of them.
-template <int LANES>
-__device__ __forceinline__ float row_sum(float x, float* lds) {
-    if constexpr (LANES <= 64) return group_sum<LANES>(x);
-    x = group_sum<64>(x);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
-    __syncthreads();
-    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
-}
-// Two sums at once, by one barrier: `lds` is another eight words in the next call.
-template <int LANES>
-__device__ __forceinline__ void row_sums(float& a, float& b, float* lds) {
-    a = group_sum<(LANES < 64 ? LANES : 64)>(a);
-    b = group_sum<(LANES < 64 ? LANES : 64)>(b);
-    if constexpr (LANES <= 64) return;
-    if ((threadIdx.x & 63) == 0) {
-        lds[threadIdx.x >> 6] = a;
-        lds[4 + (threadIdx.x >> 6)] = b;
-    }
-    __syncthreads();
-    a = (lds[0] + lds[1]) + (lds[2] + lds[3]);
-    b = (lds[4] + lds[5]) + (lds[6] + lds[7]);
-}
-__device__ __forceinline__ double join64(uint32_t lo, uint32_t hi) {
-    return __builtin_bit_cast(double, static_cast<uint64_t>(lo) | (static_cast<uint64_t>(hi) << 32));
-}
-template <int CTRL>
-__device__ __forceinline__ double dpp_double(double x) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, x);
-    return join64(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, 0xF, 0xF, true),
-                  __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, 0xF, 0xF, true));
-}
-// The sum of doubles, by the exchanges of group_sum (by shuffles: 14.2 us against 12.7 for 40000 rows of 128).
-template <int LANES>
-__device__ __forceinline__ double row_sum_wide(double x, double* lds) {
-    if (LANES >= 2) x += dpp_double<kDppXor1>(x);
-    if (LANES >= 4) x += dpp_double<kDppXor2>(x);
-    if (LANES >= 8) x += dpp_double<kDppHalfMirror>(x);
-    if (LANES >= 16) x += dpp_double<kDppMirror>(x);
-    if (LANES >= 32) {
-        const uint64_t u = __builtin_bit_cast(uint64_t, x);
-        const uint32_t a = static_cast<uint32_t>(u), b = static_cast<uint32_t>(u >> 32);
-        const auto lo = __builtin_amdgcn_permlane16_swap(a, a, false, false), hi = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-        x = join64(lo[0], hi[0]) + join64(lo[1], hi[1]);
-    }
-    if (LANES >= 64) {
-        const uint64_t u = __builtin_bit_cast(uint64_t, x);
-        const uint32_t a = static_cast<uint32_t>(u), b = static_cast<uint32_t>(u >> 32);
-        const auto lo = __builtin_amdgcn_permlane32_swap(a, a, false, false), hi = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-        x = join64(lo[0], hi[0]) + join64(lo[1], hi[1]);
-    }
-    if constexpr (LANES <= 64) return x;
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
-    __syncthreads();
-    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
-}
-template <int LANES>
-__device__ __forceinline__ float row_max(float x, float* lds) {
-    if constexpr (LANES <= 64) return group_max_abs<LANES>(x);
-    x = group_max_abs<64>(x);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[4 + (threadIdx.x >> 6)] = x;
-    __syncthreads();
-    return larger_abs(larger_abs(lds[4], lds[5]), larger_abs(lds[6], lds[7]));
-}
-
-// 1 / sqrt(m), correct to about an ulp: the hardware's estimate and one Newton step (skipped
-// where the estimate is 0, infinite or NaN).
-__device__ __forceinline__ float rsqrt_fine(float m) {
-    const float r = __builtin_amdgcn_rsqf(m);
-    const float e = __builtin_fmaf(-m * r, r, 1.0f);
-    const float y = __builtin_fmaf(0.5f * r, e, r);
-    return (m > 1e-35f && m < 1e35f) ? y : 1.0f / sqrtf(m);
-}
 
 struct NormFwd {
     int rows, d, w_dtype, group;
@@ -218,65 +99,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormFwd p) {
             }
         }
     }
-    if constexpr (QDQ != LA_QDQ_NONE) {
-        if (p.group == 0) {
-            float m = 0.0f;
-#pragma unroll
-            for (int c = 0; c < CH; c++) m = larger_abs(m, amax[c]);
-            m = row_max<LANES>(m, lds);
-#pragma unroll
-            for (int c = 0; c < CH; c++) amax[c] = m;
-        } else {  // a row of LANES * 8 columns or more holds whole groups; in a shorter one a group may be the row
-#pragma unroll
-            for (int c = 0; c < CH; c++) {
-                amax[c] = group_max_abs<2>(amax[c]);
-                if (p.group >= 32) amax[c] = larger_abs(amax[c], dpp<kDppXor2>(amax[c]));
-                if (p.group >= 64) amax[c] = larger_abs(amax[c], dpp<kDppHalfMirror>(amax[c]));
-                if (p.group >= 128) amax[c] = larger_abs(amax[c], dpp<kDppMirror>(amax[c]));
-            }
-        }
-        const int per_row = p.group ? p.d / p.group : 1;
-#pragma unroll
-        for (int c = 0; c < CH; c++) {
-            const int col = (c * LANES + l) * kPiece;
-            if (col >= p.d) continue;
-            float s, y;
-            uint32_t word[2] = {0, 0};
-            // a NaN in the group: its maximum, its scale and every value that its codes stand for
-            const bool none = amax[c] != amax[c];
-            if constexpr (QDQ == LA_QDQ_INT8_GROUP) {
-                bool fast = int8_scale_recip(amax[c], s, y);
-                if (none) s = amax[c], fast = false;
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    float q = fast ? int8_code_fast(h[c][e], s, y) : rintf(h[c][e] / s);
-                    const bool number = q == q;  // (of a quotient without one: code 0)
-                    if (!fast && number) q = fminf(fmaxf(q, -127.0f), 127.0f);
-                    word[e >> 2] |= (number ? static_cast<uint32_t>(static_cast<int>(q)) & 0xFFu : 0u) << (8 * (e & 3));
-                    h[c][e] = q * s;
-                }
-            } else {
-                bool fast = e4m3_scale_recip(amax[c], s, y);
-                if (none) s = amax[c], fast = false;
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    float a = fast ? quot_rn_fast(h[c][e], s, y) : h[c][e] / s;
-                    float b = fast ? quot_rn_fast(h[c][e + 1], s, y) : h[c][e + 1] / s;
-                    a = a != a ? a : fminf(fmaxf(a, -448.0f), 448.0f);
-                    b = b != b ? b : fminf(fmaxf(b, -448.0f), 448.0f);
-                    const uint32_t k = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false)) & 0xFFFFu;
-                    word[e >> 2] |= k << (8 * (e & 3));
-                    h[c][e] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(k), 0) * s;
-                    h[c][e + 1] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(k), 1) * s;
-                }
-            }
-            if (p.codes) *reinterpret_cast<uv2*>(p.codes + base + col) = uv2{word[0], word[1]};
-            if (p.scales) {
-                if (p.group ? col % p.group == 0 : col == 0)
-                    p.scales[static_cast<size_t>(row) * per_row + (p.group ? col / p.group : 0)] = s;
-            }
-        }
-    }
+    if constexpr (QDQ != LA_QDQ_NONE) emit_codes<QDQ, LANES, CH>(CodeOut{p.d, p.group, p.codes, p.scales}, l, row, base, h, amax, lds);
     if (p.y) {
 #pragma unroll
         for (int c = 0; c < CH; c++) {

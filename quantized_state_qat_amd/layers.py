@@ -87,6 +87,13 @@ def _dtype(code):
     return _types[code] if code in (_F32, _BF16) else _types[_F32]  # (an unknown code is refused by the library)
 
 
+def _code_type(cfg, codes):
+    """The dtype that a tensor of codes must have: uint8, or the quantizer's own."""
+    if codes is None or codes.__class__ is int or codes.dtype is _torch.uint8:
+        return _torch.uint8
+    return _torch.int8 if cfg.qdq == _la.LA_QDQ_INT8_GROUP else _torch.float8_e4m3fn
+
+
 def _gpu(*tensors):
     """The GPU of the first tensor among the arguments (all of a call's: any of them may be missing
     or a raw address); None when it is on the host or there is none."""
@@ -296,13 +303,11 @@ def la_norm_fwd(cfg: NormConfig, x, residual, weight, res_out, y, codes=None, sc
     INT8 and float8_e4m3fn for E4M3) and scales."""
     lib = _library()
     gpu = _gpu(x, residual, weight, res_out, y, codes, scales)
-    n, xt, eight = cfg.rows * cfg.d, _dtype(cfg.x_dtype), _torch.uint8
-    if codes is not None and codes.__class__ is not int and codes.dtype is not eight:  # or the codes' own type
-        eight = _torch.int8 if cfg.qdq == _la.LA_QDQ_INT8_GROUP else _torch.float8_e4m3fn
+    n, xt = cfg.rows * cfg.d, _dtype(cfg.x_dtype)
     _call(gpu, stream, lib.la_norm_fwd, cfg,
           _tight(gpu, x, "x", n, xt), _tight(gpu, residual, "residual", n, xt),
           _tight(gpu, weight, "weight", cfg.d, _dtype(cfg.w_dtype)), _tight(gpu, res_out, "res_out", n, xt),
-          _tight(gpu, y, "y", n, _dtype(cfg.out_dtype)), _tight(gpu, codes, "codes", n, eight),
+          _tight(gpu, y, "y", n, _dtype(cfg.out_dtype)), _tight(gpu, codes, "codes", n, _code_type(cfg, codes)),
           _tight(gpu, scales, "scales", n // (cfg.group or cfg.d) if cfg.d > 0 else 0, _torch.float32))
 
 

@@ -87,3 +87,63 @@ def test_linear_binding_refuses_tensors():
     xc, xs = torch.zeros(8, 64, dtype=torch.int8), torch.zeros(8)
     with pytest.raises(ValueError, match="GPU tensor"):
         la.la_linear_fwd(cfg, xc, xs, FAKE, FAKE, None, FAKE, stream=0)
+
+
+# ---------------------------------------------------------------------- norms around a block
+def gate(**kw):
+    return la.GateNormConfig(**{**dict(rows=8, d=256, gate=la.LA_GATE_SILU, pre=1), **kw})
+
+
+FWD = dict(x=FAKE, z=FAKE, w_post=FAKE, alpha=FAKE, residual=FAKE, w_pre=FAKE, h=FAKE, y=FAKE, codes=None, scales=None)
+BWD = dict(x=FAKE, z=FAKE, w_post=FAKE, alpha=FAKE, h=FAKE, w_pre=FAKE, dy=FAKE, dh=FAKE, dx=FAKE, dz=FAKE, dres=FAKE,
+           dw_post=FAKE, dalpha=FAKE, dw_pre=FAKE)
+
+
+def gate_fwd(cfg, **p):
+    la.la_gate_norm_fwd(cfg, *{**FWD, **p}.values(), stream=0)
+
+
+def gate_bwd(cfg, space, n, **p):
+    la.la_gate_norm_bwd(cfg, *{**BWD, **p}.values(), space, n, stream=0)
+
+
+@pytest.mark.parametrize("kw,status,word", [
+    (dict(rows=-1), la.LA_ERR_INVALID_ARG, "size"), (dict(d=0), la.LA_ERR_INVALID_ARG, "size"),
+    (dict(d=100), la.LA_ERR_UNSUPPORTED, "multiple of 8"), (dict(d=16392), la.LA_ERR_UNSUPPORTED, "16384"),
+    (dict(rows=1 << 30, d=16384), la.LA_ERR_UNSUPPORTED, "too many rows"), (dict(head=8), la.LA_ERR_UNSUPPORTED, "head"),
+    (dict(head=48), la.LA_ERR_UNSUPPORTED, "head"), (dict(head=1024, d=1024), la.LA_ERR_UNSUPPORTED, "head"),
+    (dict(head=512), la.LA_ERR_INVALID_ARG, "divide"), (dict(eps=-1.0), la.LA_ERR_INVALID_ARG, "eps"),
+    (dict(eps=float("nan")), la.LA_ERR_INVALID_ARG, "eps"), (dict(gate=3), la.LA_ERR_INVALID_ARG, "gate"),
+    (dict(gate_first=2), la.LA_ERR_INVALID_ARG, "gate_first"), (dict(post=-1), la.LA_ERR_INVALID_ARG, "post"),
+    (dict(pre=2), la.LA_ERR_INVALID_ARG, "pre"), (dict(gate=0, gate_first=1), la.LA_ERR_INVALID_ARG, "needs a gate"),
+    (dict(x_dtype=2), la.LA_ERR_INVALID_ARG, "x_dtype"), (dict(w_dtype=2), la.LA_ERR_INVALID_ARG, "w_dtype"),
+    (dict(out_dtype=2), la.LA_ERR_INVALID_ARG, "out_dtype"), (dict(ld_x=248), la.LA_ERR_INVALID_ARG, "shorter"),
+    (dict(ld_z=260), la.LA_ERR_ALIGNMENT, "16 bytes"), (dict(qdq=3), la.LA_ERR_INVALID_ARG, "qdq"),
+    (dict(qdq=1, group=48), la.LA_ERR_UNSUPPORTED, "group"), (dict(qdq=1, group=128, d=192), la.LA_ERR_INVALID_ARG, "divide"),
+])
+def test_gate_norm_refuses_configs(kw, status, word):
+    refused(lambda: gate_fwd(gate(**kw)), status, word)
+    refused(lambda: gate_bwd(gate(**kw), FAKE, 1 << 40), status, word)
+    assert la.la_gate_norm_bwd_workspace_bytes(gate(**kw)) == 0
+
+
+def test_gate_norm_refuses_pointers():
+    for p in FWD:
+        refused(lambda: gate_fwd(gate(qdq=1), **{p: FAKE + 8}), la.LA_ERR_ALIGNMENT, "aligned")
+    n = la.la_gate_norm_bwd_workspace_bytes(gate())
+    for p in BWD:
+        refused(lambda: gate_bwd(gate(), FAKE, n, **{p: FAKE + 8}), la.LA_ERR_ALIGNMENT, "aligned")
+    for p in ("x", "z"):
+        refused(lambda: gate_fwd(gate(), **{p: None}), la.LA_ERR_INVALID_ARG, "is NULL")
+    for p in ("x", "z", "h", "dy", "dx"):
+        refused(lambda: gate_bwd(gate(), FAKE, n, **{p: None}), la.LA_ERR_INVALID_ARG, "is NULL")
+    refused(lambda: gate_fwd(gate(gate=0)), la.LA_ERR_INVALID_ARG, "z needs")
+    refused(lambda: gate_fwd(gate(post=0)), la.LA_ERR_INVALID_ARG, "w_post needs")
+    refused(lambda: gate_fwd(gate(pre=0)), la.LA_ERR_INVALID_ARG, "w_pre needs")
+    refused(lambda: gate_fwd(gate(), codes=FAKE), la.LA_ERR_INVALID_ARG, "quantizer")
+    refused(lambda: gate_bwd(gate(gate=0), FAKE, n, z=None), la.LA_ERR_INVALID_ARG, "dz needs")
+    refused(lambda: gate_bwd(gate(post=0), FAKE, n, w_post=None), la.LA_ERR_INVALID_ARG, "dw_post needs")
+    refused(lambda: gate_bwd(gate(pre=0), FAKE, n, w_pre=None), la.LA_ERR_INVALID_ARG, "dw_pre needs")
+    refused(lambda: gate_bwd(gate(), FAKE, n - 1), la.LA_ERR_WORKSPACE, "workspace")
+    refused(lambda: gate_bwd(gate(), None, n), la.LA_ERR_WORKSPACE, "workspace")
+    gate_fwd(gate(rows=0), **{k: None for k in FWD})
