@@ -26,11 +26,20 @@ FLAGS = [
     "-mllvm", "-amdgpu-mfma-vgpr-form=1",
     "-Wall", "-Wno-unused-function",
 ]
+# The products' 256 x 256 tiles take 256 accumulators a lane, which only the accumulator registers hold beside
+# the operands.
+WITHOUT = {"linear_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"], "linear_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+
+
+def _flags(src: str) -> list:
+    drop = WITHOUT.get(src, [])
+    at = next((i for i in range(len(FLAGS)) if drop and FLAGS[i:i + len(drop)] == drop), len(FLAGS))
+    return FLAGS[:at] + FLAGS[at + len(drop):]
 
 
 def _compile(src: str) -> str:
     obj = os.path.join(OUT, src + ".o")
-    cmd = [HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC, *_flags(src), "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stdout}\n{r.stderr}")

@@ -79,6 +79,9 @@ LINEAR = [
     (777, 305, 1040, F32, F32, F32, 0, 0, F32),
     (1030, 776, 144, BF, BF, BF, 0, 0, F32),
     (2000, 24, 512, F32, F32, F32, 0, 0, None),
+    (1500, 2001, 144, BF, BF, F32, 0, 0, F32),
+    (3000, 3100, 208, BF, F32, BF, 16, 4, F32),
+    (2900, 3333, 80, F32, BF, BF, 0, 0, None),
 ]
 
 
