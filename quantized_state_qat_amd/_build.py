@@ -26,8 +26,7 @@ FLAGS = [
     "-mllvm", "-amdgpu-mfma-vgpr-form=1",
     "-Wall", "-Wno-unused-function",
 ]
-# The products' 256 x 256 tiles take 256 accumulators a lane, which only the accumulator registers hold beside
-# the operands.
+# The products' tiles: accumulators in the accumulator registers, which leaves the others to the operands.
 WITHOUT = {"linear_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"], "linear_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 

@@ -36,72 +36,122 @@ struct GemmArgs {
     int wide = 0;     // rows of out are 16-byte aligned
 };
 
+typedef int iv16 __attribute__((ext_vector_type(16)));
+typedef float fv16 __attribute__((ext_vector_type(16)));
+
+// One matrix instruction: 32 x 32 results, 32 bytes of the summed index; lane l holds 16 of them,
+// 16 (l / 32) .. + 15, of row l % 32 of each operand.  (16 x 16 results over 64 bytes read the same LDS
+// for the same work in twice the instructions: 8192^3 in 8 bits 1975 against 2140 TOP/s, four waves.)
 template <class E>
 struct Mfma;
 template <>
 struct Mfma<int8_t> {
-    typedef iv4 Acc;
+    typedef iv16 Acc;
     static __device__ __forceinline__ Acc mul(uv4 a, uv4 b, Acc c) {
-        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(iv4, a), __builtin_bit_cast(iv4, b), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(iv4, a), __builtin_bit_cast(iv4, b), c, 0, 0, 0);
     }
 };
 template <>
 struct Mfma<_Float16> {
-    typedef fv4 Acc;
+    typedef fv16 Acc;
     static __device__ __forceinline__ Acc mul(uv4 a, uv4 b, Acc c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(hv8, a), __builtin_bit_cast(hv8, b), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(hv8, a), __builtin_bit_cast(hv8, b), c, 0, 0, 0);
     }
 };
 
-// Row of a 32-row slab of P that lane r of 16 holds in tile b of the slab's two: a lane's results in
-// the two tiles are then 8 consecutive columns of out, 8 (lane / 16) .. + 7 of the slab.
-__device__ __forceinline__ int slab_row(int r, int b) { return 8 * (r >> 2) + 4 * b + (r & 3); }
+// Row of a tile's 32 rows of P that lane r of 32 holds: results v of lane l are then columns
+// 16 (v / 8) + 8 (l / 32) + v % 8 of the tile (row 8 (v / 4) + 4 (l / 32) + v % 4 of the instruction is
+// result v of a lane).
+__device__ __forceinline__ int tile_row(int r) { return 16 * (r >> 4) + 8 * ((r >> 2) & 1) + 4 * ((r >> 3) & 1) + (r & 3); }
 
-// Results of TI x TJ tiles of 16 x 16 of a wave, whose first row of P is i0 and of Q j0.
+__device__ __forceinline__ void load_eight(const float* p, float (&v)[8]) {
+    float a[4], b[4];
+    widen(load16(p), a);
+    widen(load16(p + 4), b);
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        v[e] = a[e];
+        v[4 + e] = b[e];
+    }
+}
+
+// 128 bytes of 32 rows of out, on their way from a wave's registers to whole lines of memory.
+constexpr int kStoreLds = 4096;
+
+// Results of a wave's TI x TJ tiles, the first one's at column i0 and row j0 of out.  A lane's results are
+// 16 or 32 bytes of 32 different rows of out; where the tile lies inside, they go through the wave's LDS
+// (kStoreLds bytes) and leave as lines of 128 bytes.
 template <class O, bool BITS, int TI, int TJ, class Acc>
-__device__ __forceinline__ void store_tiles(const GemmArgs& a, int i0, int j0, const Acc (&acc)[TI][TJ]) {
-    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+__device__ __forceinline__ void store_tiles(const GemmArgs& a, int i0, int j0, const Acc (&acc)[TI][TJ], char* lds) {
+    const int lane = threadIdx.x & 63, r = lane & 31, q = lane >> 5;
+    constexpr int WIDE = TI * 32 * sizeof(O) < 128 ? TI * 32 : 128 / sizeof(O);  // columns of a pass
+    constexpr int LINE = WIDE * sizeof(O), PIECES = LINE / 16, ROWS = 64 / PIECES;  // rows of a store
+    const bool whole = a.wide && i0 + 32 * TI <= a.I;
     float rs[TJ];
 #pragma unroll
     for (int tj = 0; tj < TJ; tj++) {
-        const int j = j0 + 16 * tj + r;
+        const int j = j0 + 32 * tj + r;
         if constexpr (BITS) rs[tj] = j < a.J ? scale_back(static_cast<const uint32_t*>(a.row)[j]) : 0.0f;
         else rs[tj] = j < a.J ? static_cast<const float*>(a.row)[j] : 0.0f;
     }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (the kernel counts on it: every load before has landed)
 #pragma unroll
-    for (int u = 0; u < TI / 2; u++) {
-        const int i = i0 + 32 * u + 8 * q;
-        const bool whole = a.wide && i + 8 <= a.I;
-        float cs[8], bias[8];
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const bool in = i + e < a.I;
-            cs[e] = a.col && in ? a.col[i + e] : 1.0f;
-            bias[e] = a.bias && in ? load_elem(a.bias, i + e, a.bias_dtype) : 0.0f;
-        }
+    for (int pass = 0; pass < TI * 32 / WIDE; pass++) {
+        constexpr int EIGHTS = WIDE / 16;  // eights of columns that a lane has of a pass
 #pragma unroll
         for (int tj = 0; tj < TJ; tj++) {
-            const int j = j0 + 16 * tj + r;
-            if (j >= a.J) continue;
-            float v[8];
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                v[e] = static_cast<float>(acc[2 * u + (e >> 2)][tj][e & 3]) * rs[tj];
-                if (a.col) v[e] *= cs[e];
-                if (a.bias) v[e] += bias[e];
-            }
-            O* o = static_cast<O*>(a.out) + static_cast<int64_t>(j) * a.ldo + i;
-            if (whole) {
-                if constexpr (sizeof(O) == 2) {
-                    store16(o, narrow(v));
+            for (int k = 0; k < EIGHTS; k++) {
+                const int at = WIDE / 16 * pass + k, i = i0 + 16 * at + 8 * q;  // sixteens of columns from i0
+                float cs[8], bias[8];
+                if (i + 8 <= a.I) {
+                    if (a.col) load_eight(a.col + i, cs);
+                    if (a.bias) {
+                        if (a.bias_dtype == LA_BF16) widen(load16(static_cast<const uint16_t*>(a.bias) + i), bias);
+                        else load_eight(static_cast<const float*>(a.bias) + i, bias);
+                    }
                 } else {
-                    store16(o, uv4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
-                    store16(o + 4, uv4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])});
-                }
-            } else {
 #pragma unroll
-                for (int e = 0; e < 8; e++)
-                    if (i + e < a.I) store_elem(o, e, sizeof(O) == 2 ? LA_BF16 : LA_F32, v[e]);
+                    for (int e = 0; e < 8; e++) {
+                        const bool in = i + e < a.I;
+                        cs[e] = a.col && in ? a.col[i + e] : 1.0f;
+                        bias[e] = a.bias && in ? load_elem(a.bias, i + e, a.bias_dtype) : 0.0f;
+                    }
+                }
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    v[e] = static_cast<float>(acc[at / 2][tj][8 * (at % 2) + e]) * rs[tj];
+                    if (a.col) v[e] *= cs[e];
+                    if (a.bias) v[e] += bias[e];
+                }
+                if (whole) {
+                    constexpr int per = sizeof(O) / 2;  // pieces of 16 bytes
+                    const int piece = (2 * k + q) * per, x = r & (PIECES - 1);
+                    char* row = lds + r * LINE;
+                    if constexpr (sizeof(O) == 2) {
+                        *reinterpret_cast<uv4*>(row + 16 * (piece ^ x)) = narrow(v);
+                    } else {
+                        *reinterpret_cast<fv4*>(row + 16 * (piece ^ x)) = fv4{v[0], v[1], v[2], v[3]};
+                        *reinterpret_cast<fv4*>(row + 16 * ((piece + 1) ^ x)) = fv4{v[4], v[5], v[6], v[7]};
+                    }
+                } else {
+                    const int j = j0 + 32 * tj + r;
+                    O* o = static_cast<O*>(a.out) + static_cast<int64_t>(j) * a.ldo + i;
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+                        if (j < a.J && i + e < a.I) store_elem(o, e, sizeof(O) == 2 ? LA_BF16 : LA_F32, v[e]);
+                }
+            }
+            if (whole) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (one wave: its own writes, in order)
+#pragma unroll
+                for (int n = 0; n < 32 / ROWS; n++) {
+                    const int row = ROWS * n + lane / PIECES, piece = lane % PIECES, j = j0 + 32 * tj + row;
+                    const uv4 v = *reinterpret_cast<const uv4*>(lds + row * LINE + 16 * (piece ^ (row & (PIECES - 1))));
+                    if (j < a.J) store16(static_cast<O*>(a.out) + static_cast<int64_t>(j) * a.ldo + i0 + WIDE * pass + piece * (16 / sizeof(O)), v);
+                }
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             }
         }
     }
@@ -126,147 +176,158 @@ __device__ __forceinline__ TileAt tile_order(int tile, int across, int down) {
 
 constexpr uint32_t kOutside = 0x80000000u;  // an offset past every operand's buffer: such loads return zero
 
-// A wave's 32 x 32 results, operands from memory straight into registers.
-template <class E, class O, bool BITS>
-__global__ __launch_bounds__(256) void gemm_direct_kernel(GemmArgs a) {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-    const int across = (a.I + 63) / 64;
-    const int i0 = (blockIdx.x % across) * 64 + (wave & 1) * 32, j0 = (blockIdx.x / across) * 64 + (wave >> 1) * 32;
-    if (i0 >= a.I || j0 >= a.J) return;
-    const int ni = a.I - i0 < 32 ? a.I - i0 : 32, nj = a.J - j0 < 32 ? a.J - j0 : 32;
-    const int steps = ((a.kbytes + 127) >> 7) << a.shift;
-    const auto P = make_rsrc(a.P + i0 * a.ldP, (ni - 1) * a.ldP + a.kbytes);
-    const auto Q = make_rsrc(a.Q + j0 * a.ldQ, (nj - 1) * a.ldQ + (static_cast<int64_t>(a.kbytes) << a.shift));
-    uint32_t po[2], qo[2];
-#pragma unroll
-    for (int b = 0; b < 2; b++) {
-        po[b] = slab_row(r, b) * static_cast<uint32_t>(a.ldP) + 16 * q;
-        qo[b] = (16 * b + r) * static_cast<uint32_t>(a.ldQ) + 16 * q;
-    }
-    typename Mfma<E>::Acc acc[2][2] = {};
-    for (int t = 0; t < steps; t++) {
-        const int pk = (t >> a.shift) * 128, qk = t * 128;
-#pragma unroll
-        for (int half = 0; half < 2; half++) {
-            const bool in = pk + 64 * half + 16 * q < a.kbytes;  // past the row's end both operands are zero
-            uv4 p[2], x[2];
-#pragma unroll
-            for (int b = 0; b < 2; b++) {
-                p[b] = __builtin_bit_cast(uv4, __builtin_amdgcn_raw_buffer_load_b128(P, in ? po[b] + 64 * half : kOutside, pk, 0));
-                x[b] = __builtin_bit_cast(uv4, __builtin_amdgcn_raw_buffer_load_b128(Q, in ? qo[b] + 64 * half : kOutside, qk, 0));
-            }
-#pragma unroll
-            for (int ti = 0; ti < 2; ti++)
-#pragma unroll
-                for (int tj = 0; tj < 2; tj++) acc[ti][tj] = Mfma<E>::mul(p[ti], x[tj], acc[ti][tj]);
-        }
-    }
-    store_tiles<O, BITS, 2, 2>(a, i0, j0, acc);
-}
-
-// LDS offset of 16-byte piece `c` of 8 in row `row` of a tile with 128 bytes of each row: the piece is
-// exchanged by XOR with a number of the row, so that the 16 rows a wave reads at once lie in different
-// banks.  P's rows are read in slab_row order, Q's in their own.
-__device__ __forceinline__ int swizzle_p(int row) { return (row & 3) | ((row >> 1) & 4); }
-__device__ __forceinline__ int swizzle_q(int row) { return row & 7; }
+// LDS holds 128 bytes of every row of a tile; 16-byte piece c of 8 of row `row` lies at c ^ swizzle(row),
+// so that lanes that read the same piece of neighbouring rows at once reach different banks (no
+// conflicts counted; with row & 7 half of the reads' cycles were).
+__device__ __forceinline__ int swizzle(int row) { return (row >> 1) & 7; }
 
 // 16 bytes a lane from memory to LDS, at `lds` + 16 lane.
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, char* lds, uint32_t offset, uint32_t base) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, offset, base, 0, 0);
 }
 
-// 32 TI x 32 TJ results of a workgroup of four waves (2 x 2).  Two tiles of 128 bytes of every row in LDS:
-// while the waves multiply one, the next but one's loads go straight to LDS.  A tile is two halves of 64
-// bytes (one matrix instruction's depth): a half's operands are read from LDS while the half before is
-// multiplied, and once a tile's second half is in registers one barrier frees its LDS.
-template <class E, class O, bool BITS, int TI, int TJ, int MINW>
-__global__ __launch_bounds__(256, MINW) void gemm_tile_kernel(GemmArgs a, int across, int down) {
-    constexpr int BI = 32 * TI, BJ = 32 * TJ, STAGE = (BI + BJ) * 128;
-    __shared__ __align__(128) char lds[2 * STAGE];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-    const int tile = xcd_tile(blockIdx.x, across * down);
-    const TileAt at = tile_order(tile, across, down);
-    const int i0 = at.i * BI, j0 = at.j * BJ;
-    const int ni = a.I - i0 < BI ? a.I - i0 : BI, nj = a.J - j0 < BJ ? a.J - j0 : BJ;
+// WI x WJ waves with TI x TJ tiles of 32 x 32 each.  Two tiles of 128 bytes of every row in LDS: while the
+// waves multiply one, the next one's loads go straight to LDS.  A tile is two halves of 64 bytes (two
+// matrix instructions deep): a half's operands are read from LDS while the half before is multiplied,
+// and once a tile's second half is in registers one barrier frees its LDS for the loads of the next but
+// one.  The order of the two kinds of instructions is spelled out (the compiler bunches the reads: 8192^3
+// in 8 bits 2320 against 2380 TOP/s).  A workgroup takes tiles of out in turn, and the loads run on into
+// the next one, under the stores of the one before.
+template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int MINW>
+__global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs a, int across, int down) {
+    constexpr int NW = WI * WJ, BI = 32 * TI * WI, BJ = 32 * TJ * WJ, STAGE = (BI + BJ) * 128;
+    constexpr int LI = BI / (8 * NW), LJ = BJ / (8 * NW);  // loads a wave: 8 rows each
+    static_assert(BI % (8 * NW) == 0 && BJ % (8 * NW) == 0 && NW % 2 == 0);
+    __shared__ __align__(128) char lds[2 * STAGE + NW * kStoreLds];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 31, q = lane >> 5;
+    const int tiles = across * down;
     const int steps = ((a.kbytes + 127) >> 7) << a.shift;
-    const auto P = make_rsrc(a.P + i0 * a.ldP, (ni - 1) * a.ldP + a.kbytes);
-    const auto Q = make_rsrc(a.Q + j0 * a.ldQ, (nj - 1) * a.ldQ + (static_cast<int64_t>(a.kbytes) << a.shift));
-    // a wave loads 8 rows of 128 bytes at a time: rows 8 wave + 32 k + lane / 8; the piece that belongs at
-    // lane % 8 of the LDS row
-    const int lrow = 8 * wave + (lane >> 3);
-    uint32_t po[TI], qo[TJ];
-    int pc[2];
+    const int lrow = 8 * wave + (lane >> 3);  // and every 8 NW rows further: the swizzle is the same
+    const int piece = 16 * ((lane & 7) ^ swizzle(lrow));
+    uint32_t po[LI], qo[LJ];
 #pragma unroll
-    for (int k = 0; k < TI; k++) po[k] = (lrow + 32 * k) * static_cast<uint32_t>(a.ldP) + 16 * ((lane & 7) ^ swizzle_p(lrow + 32 * k));
+    for (int k = 0; k < LI; k++) po[k] = (lrow + 8 * NW * k) * static_cast<uint32_t>(a.ldP) + piece;
 #pragma unroll
-    for (int k = 0; k < TJ; k++) qo[k] = (lrow + 32 * k) * static_cast<uint32_t>(a.ldQ) + 16 * ((lane & 7) ^ swizzle_q(lrow + 32 * k));
-    pc[0] = 16 * ((lane & 7) ^ swizzle_p(lrow)), pc[1] = 16 * ((lane & 7) ^ swizzle_q(lrow));
-    auto issue = [&](int t) {
-        char* s = lds + (t & 1) * STAGE + wave * 1024;
-        const int pk = (t >> a.shift) * 128, qk = t * 128;
-        const bool inp = pk + pc[0] < a.kbytes, inq = pk + pc[1] < a.kbytes;  // past a row's end: zero
-#pragma unroll
-        for (int k = 0; k < TI; k++) load_to_lds(P, s + k * 4096, inp ? po[k] : kOutside, pk);
-#pragma unroll
-        for (int k = 0; k < TJ; k++) load_to_lds(Q, s + BI * 128 + k * 4096, inq ? qo[k] : kOutside, qk);
+    for (int k = 0; k < LJ; k++) qo[k] = (lrow + 8 * NW * k) * static_cast<uint32_t>(a.ldQ) + piece;
+    // where the loads are: step `at_k` of tile `at` (none left: at >= tiles), its operands' buffers
+    int at = blockIdx.x, at_k = 0;
+    __amdgpu_buffer_rsrc_t P, Q;
+    auto aim = [&] {
+        const TileAt t = tile_order(xcd_tile(at < tiles ? at : 0, tiles), across, down);
+        const int i0 = t.i * BI, j0 = t.j * BJ;
+        const int ni = a.I - i0 < BI ? a.I - i0 : BI, nj = a.J - j0 < BJ ? a.J - j0 : BJ;
+        P = make_rsrc(a.P + i0 * a.ldP, (ni - 1) * a.ldP + a.kbytes);
+        Q = make_rsrc(a.Q + j0 * a.ldQ, (nj - 1) * a.ldQ + (static_cast<int64_t>(a.kbytes) << a.shift));
     };
-    const int wi = (wave & 1) * 16 * TI, wj = (wave >> 1) * 16 * TJ;
-    const int prow = wi + slab_row(r, 0), qrow = wj + r;
-    const int pbase = prow * 128 + 16 * (q ^ swizzle_p(prow)), qbase = BI * 128 + qrow * 128 + 16 * (q ^ swizzle_q(qrow));
-    uv4 fp[2][TI], fq[2][TJ];
-    auto fetch = [&](int t, int half) {  // (the second half's pieces are 4 further: bit 6 of the offset)
-        const char* s = lds + (t & 1) * STAGE;
-        const char* sp = s + (pbase ^ (64 * half));
-        const char* sq = s + (qbase ^ (64 * half));
-#pragma unroll
-        for (int k = 0; k < TI; k++) fp[half][k] = *reinterpret_cast<const uv4*>(sp + (k >> 1) * 4096 + (k & 1) * 512);
-#pragma unroll
-        for (int k = 0; k < TJ; k++) fq[half][k] = *reinterpret_cast<const uv4*>(sq + k * 2048);
+    auto advance = [&] {
+        if (++at_k >= steps) {
+            at_k = 0;
+            at += gridDim.x;
+            aim();
+        }
     };
-    typename Mfma<E>::Acc acc[TI][TJ] = {};
+    // Past a row's end, and past the last tile, both operands are zero: bit 31 takes an offset outside (the
+    // scalar part of the address stays inside the buffer).
+    auto issue = [&](int stage) {
+        char* s = lds + stage * STAGE + wave * 1024;
+        const int qk = at_k * 128, pk = (at_k >> a.shift) * 128;
+        const uint32_t out = at < tiles && pk + piece < a.kbytes ? 0 : kOutside;
+#pragma unroll
+        for (int k = 0; k < LI; k++) load_to_lds(P, s + k * NW * 1024, po[k] | out, pk);
+#pragma unroll
+        for (int k = 0; k < LJ; k++) load_to_lds(Q, s + BI * 128 + k * NW * 1024, qo[k] | out, qk);
+    };
+    const int wi = (wave % WI) * 32 * TI, wj = (wave / WI) * 32 * TJ;
+    const int prow = wi + tile_row(r), qrow = wj + r;
+    const int pbase = prow * 128 + 16 * (q ^ swizzle(prow)), qbase = BI * 128 + qrow * 128 + 16 * (q ^ swizzle(qrow));
+    uv4 fp[2][2][TI], fq[2][2][TJ];
+    auto fetch = [&](int stage, int half) {  // (the pieces of instruction h of a half are 4 half + 2 h further)
+        const char* s = lds + stage * STAGE;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const char* sp = s + (pbase ^ (64 * half + 32 * h));
+            const char* sq = s + (qbase ^ (64 * half + 32 * h));
+#pragma unroll
+            for (int k = 0; k < TI; k++) fp[half][h][k] = *reinterpret_cast<const uv4*>(sp + k * 4096);
+#pragma unroll
+            for (int k = 0; k < TJ; k++) fq[half][h][k] = *reinterpret_cast<const uv4*>(sq + k * 4096);
+        }
+    };
+    typename Mfma<E>::Acc acc[TI][TJ];
     auto multiply = [&](int half) {
 #pragma unroll
-        for (int ti = 0; ti < TI; ti++)
+        for (int h = 0; h < 2; h++)
 #pragma unroll
-            for (int tj = 0; tj < TJ; tj++) acc[ti][tj] = Mfma<E>::mul(fp[half][ti], fq[half][tj], acc[ti][tj]);
+            for (int ti = 0; ti < TI; ti++)
+#pragma unroll
+                for (int tj = 0; tj < TJ; tj++) acc[ti][tj] = Mfma<E>::mul(fp[half][h][ti], fq[half][h][tj], acc[ti][tj]);
     };
-    // (loads past the last tile return zero, in LDS that nobody reads again: the loop has no branches)
+    // one LDS read (and, with LOADS, a share of the loads), then a share of the products, and so on
+    auto interleave = [&](auto loads) {
+        constexpr int reads = 2 * (TI + TJ), products = 2 * TI * TJ, share = products / reads;
+#pragma unroll
+        for (int k = 0; k < reads; k++) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if constexpr (decltype(loads)::value) __builtin_amdgcn_sched_group_barrier(0x20, (LI + LJ + reads - 1) / reads, 0);
+            if constexpr (share > 0) __builtin_amdgcn_sched_group_barrier(0x8, share, 0);
+        }
+        if constexpr (products > share * reads) __builtin_amdgcn_sched_group_barrier(0x8, products - share * reads, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    aim();
     issue(0);
+    advance();
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     issue(1);
+    advance();
     fetch(0, 0);
-    for (int t = 0; t < steps; t++) {
-        fetch(t, 1);
-        multiply(0);
-        // tile t is in registers and tile t + 1 in LDS, in every wave
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        issue(t + 2);
-        fetch(t + 1, 0);
-        multiply(1);
+    int stage = 0;
+    bool landed = false;  // the loads of the next step are known to have landed
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+#pragma unroll
+        for (int ti = 0; ti < TI; ti++)
+#pragma unroll
+            for (int tj = 0; tj < TJ; tj++) acc[ti][tj] = {};
+        for (int t = 0; t < steps; t++) {
+            fetch(stage, 1);
+            multiply(0);
+            interleave(std::false_type{});
+            // this step is in registers and the next one in LDS, in every wave
+            if (!landed) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            landed = false;
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            issue(stage);
+            fetch(stage ^ 1, 0);
+            multiply(1);
+            interleave(std::true_type{});
+            advance();
+            stage ^= 1;
+        }
+        const TileAt t = tile_order(xcd_tile(tile, tiles), across, down);
+        store_tiles<O, BITS, TI, TJ>(a, t.i * BI + wi, t.j * BJ + wj, acc, lds + 2 * STAGE + wave * kStoreLds);
+        landed = steps > 0;
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // no load may reach LDS after the workgroup
-    store_tiles<O, BITS, TI, TJ>(a, i0 + wi, j0 + wj, acc);
 }
 
-template <class E, class O, bool BITS, int TI, int TJ, int MINW>
+// PER: workgroups that a CU holds.
+template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int MINW, int PER>
 void launch_tiles(const GemmArgs& a, hipStream_t s) {
-    const int across = (a.I + 32 * TI - 1) / (32 * TI), down = (a.J + 32 * TJ - 1) / (32 * TJ);
-    gemm_tile_kernel<E, O, BITS, TI, TJ, MINW><<<static_cast<unsigned>(across * down), 256, 0, s>>>(a, across, down);
+    constexpr int BI = 32 * TI * WI, BJ = 32 * TJ * WJ;
+    const int across = (a.I + BI - 1) / BI, down = (a.J + BJ - 1) / BJ;
+    const int tiles = across * down, most = 256 * PER;
+    gemm_tile_kernel<E, O, BITS, WI, WJ, TI, TJ, MINW><<<static_cast<unsigned>(tiles < most ? tiles : most), 64 * WI * WJ, 0, s>>>(a, across, down);
 }
 
 template <class E, class O, bool BITS>
 void launch_any(const GemmArgs& a, hipStream_t s) {
-    const int64_t big = static_cast<int64_t>((a.I + 255) / 256) * ((a.J + 255) / 256);
-    if (big >= 128) {
-        launch_tiles<E, O, BITS, 8, 8, 1>(a, s);
-    } else if (static_cast<int64_t>((a.I + 127) / 128) * ((a.J + 127) / 128) >= 128) {
-        launch_tiles<E, O, BITS, 4, 4, 2>(a, s);
-    } else {
-        const unsigned grid = static_cast<unsigned>(((a.I + 63) / 64) * static_cast<int64_t>((a.J + 63) / 64));
-        gemm_direct_kernel<E, O, BITS><<<grid, 256, 0, s>>>(a);
-    }
+    const auto tiles = [&](int bi, int bj) { return static_cast<int64_t>((a.I + bi - 1) / bi) * ((a.J + bj - 1) / bj); };
+    if (tiles(256, 256) >= 128) launch_tiles<E, O, BITS, 2, 4, 4, 2, 2, 1>(a, s);
+    else if (tiles(128, 128) >= 128) launch_tiles<E, O, BITS, 2, 2, 2, 2, 2, 2>(a, s);
+    else launch_tiles<E, O, BITS, 2, 2, 1, 1, 4, 4>(a, s);
 }
 
 template <class E, bool BITS>
