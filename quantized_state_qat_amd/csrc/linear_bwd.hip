@@ -195,12 +195,32 @@ __global__ __launch_bounds__(256) void lay_codes_kernel(const int8_t* codes, int
     }
 }
 
+// out[j][i] = 2^.. (row j) times the sum over the parts of part[p][j][i], in order; 4 columns a lane.
+template <class O>
+__global__ __launch_bounds__(256) void join_kernel(const float* part, int parts, int I, int64_t n, const uint32_t* row, O* out) {
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (at >= n) return;
+    double s[4] = {};
+    for (int p = 0; p < parts; p++) {
+        const fv4 v = *reinterpret_cast<const fv4*>(part + p * n + at);
+#pragma unroll
+        for (int e = 0; e < 4; e++) s[e] += v[e];
+    }
+    const float k = scale_back(row[at / I]);
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) v[e] = static_cast<float>(s[e]) * k;
+    if constexpr (sizeof(O) == 2) *reinterpret_cast<uv2*>(out + at) = uv2{pack16(v[0], v[1]), pack16(v[2], v[3])};
+    else *reinterpret_cast<fv4*>(out + at) = fv4{v[0], v[1], v[2], v[3]};
+}
+
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // What the workspace holds, in this order.
 struct Layout {
-    size_t rowmax, colmax, part, qx, qw, pw, px, end;  // offsets; pw: w's codes, px: x's
-    int parts_x, parts_w;
+    size_t rowmax, colmax, part, qx, qw, pw, px, sums, end;  // offsets; pw: w's codes, px: x's
+    int parts_x, parts_w;  // of an operand
+    Cut dx, dw;            // the two products
 };
 Layout layout(const la_linear_config& c) {
     Layout l;
@@ -211,8 +231,30 @@ Layout layout(const la_linear_config& c) {
     l.rowmax = take(4 * M), l.colmax = take(4 * N), l.part = take(4 * mc * N);
     l.qx = take(M * nc * 128 * l.parts_x), l.qw = take(N * mc * 128 * l.parts_w);
     l.pw = take(K * nc * 128), l.px = take(K * mc * 128);
+    l.dx = cut_product(c.K, c.M, gemm_steps(nc * 128, l.parts_x - 1), 16);
+    l.dw = cut_product(c.K, c.N, gemm_steps(mc * 128, l.parts_w - 1), 16);
+    const size_t x = l.dx.parts > 1 ? l.dx.parts * M * K * 4 : 0, w = l.dw.parts > 1 ? l.dw.parts * N * K * 4 : 0;
+    l.sums = take(x > w ? x : w);  // (one product after the other)
     l.end = at;
     return l;
+}
+
+// One product, and the join of its parts.
+hipError_t product(GemmArgs& g, const Cut& cut, int out_dtype, float* sums, hipStream_t s) {
+    const int steps = gemm_steps(g.kbytes, g.shift);
+    g.parts = cut.parts;
+    g.part_steps = (steps + cut.parts - 1) / cut.parts;
+    if (cut.parts == 1)
+        return out_dtype == LA_BF16 ? launch_gemm<_Float16, uint16_t, true>(g, cut.tiling, s) : launch_gemm<_Float16, float, true>(g, cut.tiling, s);
+    const void* row = g.row;
+    void* out = g.out;
+    g.row = nullptr, g.out = sums;
+    if (hipError_t e = launch_gemm<_Float16, float, true>(g, cut.tiling, s)) return e;
+    const int64_t n = static_cast<int64_t>(g.I) * g.J;
+    const unsigned grid = static_cast<unsigned>((n / 4 + 255) / 256);
+    if (out_dtype == LA_BF16) join_kernel<<<grid, 256, 0, s>>>(sums, cut.parts, g.I, n, static_cast<const uint32_t*>(row), static_cast<uint16_t*>(out));
+    else join_kernel<<<grid, 256, 0, s>>>(sums, cut.parts, g.I, n, static_cast<const uint32_t*>(row), static_cast<float*>(out));
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -251,7 +293,7 @@ hipError_t launch_linear_bwd(const la_linear_config& c, const LinearArgs& a, hip
         g.P = a.work + l.pw, g.ldP = nc * 128, g.I = c.K, g.kbytes = static_cast<int>(nc * 128);
         g.Q = d.qx, g.ldQ = nc * 128 * d.px, g.J = c.M, g.shift = d.px - 1;
         g.row = d.rowmax, g.out = a.dx, g.ldo = c.K, g.wide = 1;
-        if (hipError_t e = launch_gemm<_Float16, true>(g, c.x_dtype, s)) return e;
+        if (hipError_t e = product(g, l.dx, c.x_dtype, reinterpret_cast<float*>(a.work + l.sums), s)) return e;
     }
     if (a.dw && c.N > 0) {
         if (mc > 0) lay_codes_kernel<<<blocks(mc * kc), 256, 0, s>>>(a.x, c.ld_x ? c.ld_x : c.K, c.M, c.K, a.work + l.px);
@@ -259,7 +301,7 @@ hipError_t launch_linear_bwd(const la_linear_config& c, const LinearArgs& a, hip
         g.P = a.work + l.px, g.ldP = mc * 128, g.I = c.K, g.kbytes = static_cast<int>(mc * 128);
         g.Q = d.qw, g.ldQ = mc * 128 * d.pw, g.J = c.N, g.shift = d.pw - 1;
         g.row = d.colmax, g.out = a.dw, g.ldo = c.K, g.wide = 1;
-        if (hipError_t e = launch_gemm<_Float16, true>(g, c.dw_dtype, s)) return e;
+        if (hipError_t e = product(g, l.dw, c.dw_dtype, reinterpret_cast<float*>(a.work + l.sums), s)) return e;
     }
     return hipGetLastError();
 }

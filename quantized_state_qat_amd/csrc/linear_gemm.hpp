@@ -27,7 +27,9 @@ struct GemmArgs {
     int I = 0, J = 0;
     int kbytes = 0;  // bytes of a row of P that are summed, a multiple of 16
     int shift = 0;   // Q holds 1 << shift parts of each 128 bytes of P, beside each other
-    const void* row = nullptr;   // [J]: float factors, or the largest magnitude's bits (scale_back)
+    int parts = 1;       // the sum is cut into this many, of part_steps x 128 bytes of Q each, part p's
+    int part_steps = 0;  // result J rows below part p - 1's
+    const void* row = nullptr;   // [J] or null: float factors, or the largest magnitude's bits (scale_back)
     const float* col = nullptr;  // [I] or null
     const void* bias = nullptr;  // [I] or null
     int bias_dtype = 0;
@@ -82,7 +84,7 @@ constexpr int kStoreLds = 4096;
 // 16 or 32 bytes of 32 different rows of out; where the tile lies inside, they go through the wave's LDS
 // (kStoreLds bytes) and leave as lines of 128 bytes.
 template <class O, bool BITS, int TI, int TJ, class Acc>
-__device__ __forceinline__ void store_tiles(const GemmArgs& a, int i0, int j0, const Acc (&acc)[TI][TJ], char* lds) {
+__device__ __forceinline__ void store_tiles(const GemmArgs& a, O* out, int i0, int j0, const Acc (&acc)[TI][TJ], char* lds) {
     const int lane = threadIdx.x & 63, r = lane & 31, q = lane >> 5;
     constexpr int WIDE = TI * 32 * sizeof(O) < 128 ? TI * 32 : 128 / sizeof(O);  // columns of a pass
     constexpr int LINE = WIDE * sizeof(O), PIECES = LINE / 16, ROWS = 64 / PIECES;  // rows of a store
@@ -91,8 +93,9 @@ __device__ __forceinline__ void store_tiles(const GemmArgs& a, int i0, int j0, c
 #pragma unroll
     for (int tj = 0; tj < TJ; tj++) {
         const int j = j0 + 32 * tj + r;
-        if constexpr (BITS) rs[tj] = j < a.J ? scale_back(static_cast<const uint32_t*>(a.row)[j]) : 0.0f;
-        else rs[tj] = j < a.J ? static_cast<const float*>(a.row)[j] : 0.0f;
+        if (!a.row || j >= a.J) rs[tj] = 1.0f;
+        else if constexpr (BITS) rs[tj] = scale_back(static_cast<const uint32_t*>(a.row)[j]);
+        else rs[tj] = static_cast<const float*>(a.row)[j];
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (the kernel counts on it: every load before has landed)
 #pragma unroll
@@ -137,7 +140,7 @@ __device__ __forceinline__ void store_tiles(const GemmArgs& a, int i0, int j0, c
                     }
                 } else {
                     const int j = j0 + 32 * tj + r;
-                    O* o = static_cast<O*>(a.out) + static_cast<int64_t>(j) * a.ldo + i;
+                    O* o = out + static_cast<int64_t>(j) * a.ldo + i;
 #pragma unroll
                     for (int e = 0; e < 8; e++)
                         if (j < a.J && i + e < a.I) store_elem(o, e, sizeof(O) == 2 ? LA_BF16 : LA_F32, v[e]);
@@ -149,7 +152,7 @@ __device__ __forceinline__ void store_tiles(const GemmArgs& a, int i0, int j0, c
                 for (int n = 0; n < 32 / ROWS; n++) {
                     const int row = ROWS * n + lane / PIECES, piece = lane % PIECES, j = j0 + 32 * tj + row;
                     const uv4 v = *reinterpret_cast<const uv4*>(lds + row * LINE + 16 * (piece ^ (row & (PIECES - 1))));
-                    if (j < a.J) store16(static_cast<O*>(a.out) + static_cast<int64_t>(j) * a.ldo + i0 + WIDE * pass + piece * (16 / sizeof(O)), v);
+                    if (j < a.J) store16(out + static_cast<int64_t>(j) * a.ldo + i0 + WIDE * pass + piece * (16 / sizeof(O)), v);
                 }
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             }
@@ -186,13 +189,12 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, char* lds,
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, offset, base, 0, 0);
 }
 
-// WI x WJ waves with TI x TJ tiles of 32 x 32 each.  Two tiles of 128 bytes of every row in LDS: while the
-// waves multiply one, the next one's loads go straight to LDS.  A tile is two halves of 64 bytes (two
-// matrix instructions deep): a half's operands are read from LDS while the half before is multiplied,
-// and once a tile's second half is in registers one barrier frees its LDS for the loads of the next but
-// one.  The order of the two kinds of instructions is spelled out (the compiler bunches the reads: 8192^3
-// in 8 bits 2320 against 2380 TOP/s).  A workgroup takes tiles of out in turn, and the loads run on into
-// the next one, under the stores of the one before.
+// WI x WJ waves with TI x TJ tiles of 32 x 32 each.  Two steps of 128 bytes of every row in LDS: while the
+// waves multiply one, the next one's loads go straight to LDS.  A step is four slices of one matrix
+// instruction's depth: a slice's operands are read from LDS while the slice before is multiplied, and
+// once a step's last slice is in registers one barrier frees its LDS for the loads of the next but one.
+// The order of reads, loads and products is spelled out (the compiler bunches the reads).  A workgroup
+// takes tiles of out in turn, and the loads run on into the next one, under the stores of the one before.
 template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int MINW>
 __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs a, int across, int down) {
     constexpr int NW = WI * WJ, BI = 32 * TI * WI, BJ = 32 * TJ * WJ, STAGE = (BI + BJ) * 128;
@@ -200,8 +202,7 @@ __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs 
     static_assert(BI % (8 * NW) == 0 && BJ % (8 * NW) == 0 && NW % 2 == 0);
     __shared__ __align__(128) char lds[2 * STAGE + NW * kStoreLds];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 31, q = lane >> 5;
-    const int tiles = across * down;
-    const int steps = ((a.kbytes + 127) >> 7) << a.shift;
+    const int tiles = across * down, units = tiles * a.parts, steps = a.part_steps;
     const int lrow = 8 * wave + (lane >> 3);  // and every 8 NW rows further: the swizzle is the same
     const int piece = 16 * ((lane & 7) ^ swizzle(lrow));
     uint32_t po[LI], qo[LJ];
@@ -209,11 +210,14 @@ __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs 
     for (int k = 0; k < LI; k++) po[k] = (lrow + 8 * NW * k) * static_cast<uint32_t>(a.ldP) + piece;
 #pragma unroll
     for (int k = 0; k < LJ; k++) qo[k] = (lrow + 8 * NW * k) * static_cast<uint32_t>(a.ldQ) + piece;
-    // where the loads are: step `at_k` of tile `at` (none left: at >= tiles), its operands' buffers
-    int at = blockIdx.x, at_k = 0;
+    // where the loads are: step `at_k` of unit `at`, a part of a tile (none left: at >= units), whose first
+    // step in the whole sum is k0, and its operands' buffers
+    int at = blockIdx.x, at_k = 0, k0 = 0;
     __amdgpu_buffer_rsrc_t P, Q;
     auto aim = [&] {
-        const TileAt t = tile_order(xcd_tile(at < tiles ? at : 0, tiles), across, down);
+        const int unit = xcd_tile(at < units ? at : 0, units);
+        const TileAt t = tile_order(unit % tiles, across, down);
+        k0 = unit / tiles * steps;
         const int i0 = t.i * BI, j0 = t.j * BJ;
         const int ni = a.I - i0 < BI ? a.I - i0 : BI, nj = a.J - j0 < BJ ? a.J - j0 : BJ;
         P = make_rsrc(a.P + i0 * a.ldP, (ni - 1) * a.ldP + a.kbytes);
@@ -230,8 +234,9 @@ __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs 
     // scalar part of the address stays inside the buffer).
     auto issue = [&](int stage) {
         char* s = lds + stage * STAGE + wave * 1024;
-        const int qk = at_k * 128, pk = (at_k >> a.shift) * 128;
-        const uint32_t out = at < tiles && pk + piece < a.kbytes ? 0 : kOutside;
+        int qk = (k0 + at_k) * 128, pk = ((k0 + at_k) >> a.shift) * 128;
+        const uint32_t out = at < units && pk + piece < a.kbytes ? 0 : kOutside;
+        if (pk >= a.kbytes) pk = qk = 0;
 #pragma unroll
         for (int k = 0; k < LI; k++) load_to_lds(P, s + k * NW * 1024, po[k] | out, pk);
 #pragma unroll
@@ -240,38 +245,38 @@ __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs 
     const int wi = (wave % WI) * 32 * TI, wj = (wave / WI) * 32 * TJ;
     const int prow = wi + tile_row(r), qrow = wj + r;
     const int pbase = prow * 128 + 16 * (q ^ swizzle(prow)), qbase = BI * 128 + qrow * 128 + 16 * (q ^ swizzle(qrow));
-    uv4 fp[2][2][TI], fq[2][2][TJ];
-    auto fetch = [&](int stage, int half) {  // (the pieces of instruction h of a half are 4 half + 2 h further)
-        const char* s = lds + stage * STAGE;
+    uv4 fp[2][TI], fq[2][TJ];
+    auto fetch = [&](int stage, int slice) {  // (the pieces of a slice are 2 further than those of the one before)
+        const char* sp = lds + stage * STAGE + (pbase ^ (32 * slice));
+        const char* sq = lds + stage * STAGE + (qbase ^ (32 * slice));
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const char* sp = s + (pbase ^ (64 * half + 32 * h));
-            const char* sq = s + (qbase ^ (64 * half + 32 * h));
+        for (int k = 0; k < TI; k++) fp[slice & 1][k] = *reinterpret_cast<const uv4*>(sp + k * 4096);
 #pragma unroll
-            for (int k = 0; k < TI; k++) fp[half][h][k] = *reinterpret_cast<const uv4*>(sp + k * 4096);
-#pragma unroll
-            for (int k = 0; k < TJ; k++) fq[half][h][k] = *reinterpret_cast<const uv4*>(sq + k * 4096);
-        }
+        for (int k = 0; k < TJ; k++) fq[slice & 1][k] = *reinterpret_cast<const uv4*>(sq + k * 4096);
     };
     typename Mfma<E>::Acc acc[TI][TJ];
-    auto multiply = [&](int half) {
+    auto multiply = [&](int slice) {
 #pragma unroll
-        for (int h = 0; h < 2; h++)
+        for (int ti = 0; ti < TI; ti++)
 #pragma unroll
-            for (int ti = 0; ti < TI; ti++)
-#pragma unroll
-                for (int tj = 0; tj < TJ; tj++) acc[ti][tj] = Mfma<E>::mul(fp[half][h][ti], fq[half][h][tj], acc[ti][tj]);
+            for (int tj = 0; tj < TJ; tj++) acc[ti][tj] = Mfma<E>::mul(fp[slice & 1][ti], fq[slice & 1][tj], acc[ti][tj]);
     };
-    // one LDS read (and, with LOADS, a share of the loads), then a share of the products, and so on
+    // Pairs of loads (none, or all of a step's) with a product each, then the LDS reads among the other products.
+    // (Loads to LDS keep their order with the reads behind them.)
     auto interleave = [&](auto loads) {
-        constexpr int reads = 2 * (TI + TJ), products = 2 * TI * TJ, share = products / reads;
+        constexpr int reads = TI + TJ, products = TI * TJ, with = decltype(loads)::value ? (LI + LJ) / 2 : 0;
+        constexpr int rest = products > with ? products - with : 0, bunch = rest > 0 ? (reads + rest - 1) / rest : 1;
 #pragma unroll
-        for (int k = 0; k < reads; k++) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            if constexpr (decltype(loads)::value) __builtin_amdgcn_sched_group_barrier(0x20, (LI + LJ + reads - 1) / reads, 0);
-            if constexpr (share > 0) __builtin_amdgcn_sched_group_barrier(0x8, share, 0);
+        for (int k = 0; k < with; k++) {
+            __builtin_amdgcn_sched_group_barrier(0x20, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
         }
-        if constexpr (products > share * reads) __builtin_amdgcn_sched_group_barrier(0x8, products - share * reads, 0);
+#pragma unroll
+        for (int k = 0; k < reads; k += bunch) {
+            __builtin_amdgcn_sched_group_barrier(0x100, bunch, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x8, products, 0);
         __builtin_amdgcn_sched_barrier(0);
     };
     aim();
@@ -284,15 +289,18 @@ __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs 
     fetch(0, 0);
     int stage = 0;
     bool landed = false;  // the loads of the next step are known to have landed
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    for (int id = blockIdx.x; id < units; id += gridDim.x) {
 #pragma unroll
         for (int ti = 0; ti < TI; ti++)
 #pragma unroll
             for (int tj = 0; tj < TJ; tj++) acc[ti][tj] = {};
-        for (int t = 0; t < steps; t++) {
-            fetch(stage, 1);
-            multiply(0);
-            interleave(std::false_type{});
+        for (int t = 0; t < steps; t++, stage ^= 1) {
+#pragma unroll
+            for (int k = 0; k < 3; k++) {
+                fetch(stage, k + 1);
+                multiply(k);
+                interleave(std::false_type{});
+            }
             // this step is in registers and the next one in LDS, in every wave
             if (!landed) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
             landed = false;
@@ -301,13 +309,14 @@ __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs 
             __builtin_amdgcn_sched_barrier(0);
             issue(stage);
             fetch(stage ^ 1, 0);
-            multiply(1);
+            multiply(3);
             interleave(std::true_type{});
             advance();
-            stage ^= 1;
         }
-        const TileAt t = tile_order(xcd_tile(tile, tiles), across, down);
-        store_tiles<O, BITS, TI, TJ>(a, t.i * BI + wi, t.j * BJ + wj, acc, lds + 2 * STAGE + wave * kStoreLds);
+        const int unit = xcd_tile(id, units);
+        const TileAt t = tile_order(unit % tiles, across, down);
+        O* out = static_cast<O*>(a.out) + unit / tiles * static_cast<int64_t>(a.J) * a.ldo;
+        store_tiles<O, BITS, TI, TJ>(a, out, t.i * BI + wi, t.j * BJ + wj, acc, lds + 2 * STAGE + wave * kStoreLds);
         landed = steps > 0;
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // no load may reach LDS after the workgroup
@@ -318,23 +327,50 @@ template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int MINW,
 void launch_tiles(const GemmArgs& a, hipStream_t s) {
     constexpr int BI = 32 * TI * WI, BJ = 32 * TJ * WJ;
     const int across = (a.I + BI - 1) / BI, down = (a.J + BJ - 1) / BJ;
-    const int tiles = across * down, most = 256 * PER;
-    gemm_tile_kernel<E, O, BITS, WI, WJ, TI, TJ, MINW><<<static_cast<unsigned>(tiles < most ? tiles : most), 64 * WI * WJ, 0, s>>>(a, across, down);
+    const int units = across * down * a.parts, most = 256 * PER;
+    gemm_tile_kernel<E, O, BITS, WI, WJ, TI, TJ, MINW>
+        <<<static_cast<unsigned>(units < most ? units : most), 64 * WI * WJ, 0, s>>>(a, across, down);
 }
+
+// The tiles that a product is cut into.
+enum Tiling { kTiles256, kTiles128, kTiles64 };
 
 template <class E, class O, bool BITS>
-void launch_any(const GemmArgs& a, hipStream_t s) {
-    const auto tiles = [&](int bi, int bj) { return static_cast<int64_t>((a.I + bi - 1) / bi) * ((a.J + bj - 1) / bj); };
-    if (tiles(256, 256) >= 128) launch_tiles<E, O, BITS, 2, 4, 4, 2, 2, 1>(a, s);
-    else if (tiles(128, 128) >= 128) launch_tiles<E, O, BITS, 2, 2, 2, 2, 2, 2>(a, s);
-    else launch_tiles<E, O, BITS, 2, 2, 1, 1, 4, 4>(a, s);
+hipError_t launch_gemm(const GemmArgs& a, Tiling t, hipStream_t s) {
+    if (t == kTiles256) launch_tiles<E, O, BITS, 2, 4, 4, 2, 2, 1>(a, s);
+    else if (t == kTiles128) launch_tiles<E, O, BITS, 2, 2, 2, 2, 2, 2>(a, s);
+    else launch_tiles<E, O, BITS, 2, 2, 1, 1, 4, 3>(a, s);
+    return hipGetLastError();
 }
 
-template <class E, bool BITS>
-hipError_t launch_gemm(const GemmArgs& a, int out_dtype, hipStream_t s) {
-    if (out_dtype == LA_BF16) launch_any<E, uint16_t, BITS>(a, s);
-    else launch_any<E, float, BITS>(a, s);
-    return hipGetLastError();
+inline int gemm_steps(int64_t kbytes, int shift) { return static_cast<int>((kbytes + 127) >> 7) << shift; }
+
+// The tiles and parts of a product of I x J results with `steps` steps, by what they would take in
+// microseconds: a launch's fixed time, and for every round of workgroups that the chip holds its steps,
+// which are slower the fuller it is; parts write their sums, and a second kernel reads them (4 TB/s).
+// Measured, us a step from a few workgroups to all: 256 x 256 1.1 to 1.75, 128 x 128 0.42 to 1.2 (two a CU),
+// 64 x 64 0.24 to 0.65 (three a CU).  256 tokens, 8192 channels, K = 2048 in 8 bits: 27, 13 and 10 us; 2048
+// tokens: 36, 40 and 75 us; 1552 x 512 results over 4096 in FP16: one part 81, 44 and 33 us, four 30, 16 and 19.
+struct Cut {
+    Tiling tiling;
+    int parts;
+};
+inline Cut cut_product(int64_t I, int64_t J, int steps, int most_parts) {
+    constexpr struct { int size, per; float fixed, few, full; } kinds[] = {
+        {256, 1, 7.0f, 1.1f, 1.75f}, {128, 2, 5.0f, 0.42f, 1.2f}, {64, 3, 3.5f, 0.24f, 0.65f}};
+    Cut best{kTiles256, 1};
+    float least = 0.0f;
+    for (int k = 0; k < 3; k++) {
+        for (int parts = 1; parts <= most_parts && (parts == 1 || steps / parts >= 4); parts *= 2) {
+            const auto& t = kinds[k];
+            const int64_t units = (I + t.size - 1) / t.size * ((J + t.size - 1) / t.size) * parts, slots = 256 * t.per;
+            const float each = static_cast<float>((steps + parts - 1) / parts), rest = static_cast<float>(units % slots) / slots;
+            float us = t.fixed + each * (static_cast<float>(units / slots) * t.full + (rest > 0.0f ? t.few + rest * (t.full - t.few) : 0.0f));
+            if (parts > 1) us += 4.0f + static_cast<float>(parts) * I * J * 8e-6f / 4.0f;
+            if ((k == 0 && parts == 1) || us < least) best = {static_cast<Tiling>(k), parts}, least = us;
+        }
+    }
+    return best;
 }
 
 }  // namespace la
