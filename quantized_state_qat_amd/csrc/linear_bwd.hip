@@ -19,22 +19,12 @@ __device__ __forceinline__ uint32_t finite_abs(float v) {
 }
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// 8 elements of a row from column n on, zeros from N on.
-template <class T>
-__device__ __forceinline__ void load_part(const T* row, int n, int N, int wide, float (&v)[8]) {
-    if (wide && n + 8 <= N) {
-        if constexpr (sizeof(T) == 2) {
-            widen(load16(row + n), v);
-        } else {
-            float a[4], b[4];
-            widen(load16(row + n), a);
-            widen(load16(row + n + 4), b);
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                v[e] = a[e];
-                v[4 + e] = b[e];
-            }
-        }
+// 8 elements of a row from column n on, zeros from N on.  FULL: all are there, 16-byte aligned.
+template <bool FULL, class T>
+__device__ __forceinline__ void load_part(const T* row, int n, int N, float (&v)[8]) {
+    if constexpr (FULL) {
+        if constexpr (sizeof(T) == 2) widen(load16(row + n), v);
+        else load_eight(row + n, v);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; e++) v[e] = n + e < N ? load_elem(row, n + e, sizeof(T) == 2 ? LA_BF16 : LA_F32) : 0.0f;
@@ -62,36 +52,46 @@ __global__ void clear_kernel(uint32_t* p, int64_t n) {
 
 // Largest magnitudes of rows and columns (integer maxima: their order does not matter) and the sums
 // of 64 rows: a workgroup has 64 rows of 256 columns.
+template <bool FULL, class T>
+__device__ __forceinline__ void stats_rows(const DyArgs& a, int m0, int n, int ty, float (&cs)[8], uint32_t (&cm)[8]) {
+    float ws[8] = {}, xs[8] = {}, v[8][8];
+    if (a.rowmax) load_part<FULL>(a.ws, n, a.N, ws);
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+        const int m = m0 + ty + 8 * k;
+        if (FULL || m < a.M) {
+            load_part<FULL>(static_cast<const T*>(a.dy) + m * a.ld, n, a.N, v[k]);
+            if (a.colmax) xs[k] = a.xs[m];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) v[k][e] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+        const int m = m0 + ty + 8 * k;
+        uint32_t rm = 0;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            rm = umax(rm, finite_abs(v[k][e] * ws[e]));
+            cm[e] = umax(cm[e], finite_abs(v[k][e] * xs[k]));
+            cs[e] += v[k][e];
+        }
+        rm = __float_as_uint(group_max_abs<32>(__uint_as_float(rm)));
+        if (a.rowmax && (threadIdx.x & 31) == 0 && rm) atomicMax(a.rowmax + m, rm);
+    }
+}
 template <class T>
 __global__ __launch_bounds__(256) void stats_kernel(DyArgs a) {
     __shared__ float sum[8][256];
     __shared__ uint32_t top[8][256];
     const int across = (a.N + 255) / 256;
     const int n0 = (blockIdx.x % across) * 256, m0 = (blockIdx.x / across) * 64;
-    const int c = (threadIdx.x & 31) * 8, ty = threadIdx.x >> 5, n = n0 + c;
-    float ws[8], cs[8] = {};
+    const int c = (threadIdx.x & 31) * 8, ty = threadIdx.x >> 5;
+    float cs[8] = {};
     uint32_t cm[8] = {};
-#pragma unroll
-    for (int e = 0; e < 8; e++) ws[e] = a.rowmax && n + e < a.N ? a.ws[n + e] : 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; k++) {
-        const int m = m0 + ty + 8 * k;
-        float v[8] = {};
-        float xs = 0.0f;
-        if (m < a.M) {
-            load_part(static_cast<const T*>(a.dy) + m * a.ld, n, a.N, a.wide, v);
-            xs = a.colmax ? a.xs[m] : 0.0f;
-        }
-        uint32_t rm = 0;
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            rm = umax(rm, finite_abs(v[e] * ws[e]));
-            cm[e] = umax(cm[e], finite_abs(v[e] * xs));
-            cs[e] += v[e];
-        }
-        rm = __float_as_uint(group_max_abs<32>(__uint_as_float(rm)));
-        if (a.rowmax && (threadIdx.x & 31) == 0 && rm) atomicMax(a.rowmax + m, rm);
-    }
+    if (a.wide && m0 + 64 <= a.M && n0 + 256 <= a.N) stats_rows<true, T>(a, m0, n0 + c, ty, cs, cm);
+    else stats_rows<false, T>(a, m0, n0 + c, ty, cs, cm);
 #pragma unroll
     for (int e = 0; e < 8; e++) {
         sum[ty][c + e] = cs[e];
@@ -111,42 +111,57 @@ __global__ __launch_bounds__(256) void stats_kernel(DyArgs a) {
     if (a.colmax && m) atomicMax(a.colmax + col, m);
 }
 
-__device__ __forceinline__ _Float16 low_part(float v, _Float16 hi) {
-    const float h = static_cast<float>(hi);
-    return fabsf(h) < 65536.0f ? static_cast<_Float16>(v - h) : static_cast<_Float16>(0.0f);  // (infinite and NaN: in hi)
-}
-
 // A part is 64 elements = 128 bytes of the summed index; a row holds chunk c's parts beside each other.
 __device__ __forceinline__ int64_t part_at(int chunk, int part, int parts) { return (static_cast<int64_t>(chunk) * parts + part) * 128; }
 
+// Eight scaled values as FP16, in one part or two.  The second is what the first leaves, which an infinity
+// leaves infinite: it meets the same codes.
+__device__ __forceinline__ void store_parts(char* o, const float (&v)[8], int parts) {
+    hv8 hi;
+#pragma unroll
+    for (int e = 0; e < 8; e++) hi[e] = static_cast<_Float16>(v[e]);
+    *reinterpret_cast<hv8*>(o) = hi;
+    if (parts == 2) {
+        hv8 lo;
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+            lo[e] = static_cast<_Float16>(v[e] - __builtin_amdgcn_fmed3f(static_cast<float>(hi[e]), -65504.0f, 65504.0f));
+        *reinterpret_cast<hv8*>(o + 128) = lo;
+    }
+}
+
 // 64 x 64 of dy into both operands.
-template <class T>
-__global__ __launch_bounds__(256) void lay_dy_kernel(DyArgs a) {
-    __shared__ float tile[64][65];
-    const int across = (a.N + 63) / 64;
-    const int cn = blockIdx.x % across, cm = blockIdx.x / across;
+template <bool FULL, class T>
+__device__ __forceinline__ void lay_dy(const DyArgs& a, int cm, int cn, T (&tile)[64][66]) {
     const int n0 = cn * 64, m0 = cm * 64;
     const int64_t rowx = part_at((a.N + 63) / 64, 0, a.px), roww = part_at((a.M + 63) / 64, 0, a.pw);
     const int c = (threadIdx.x & 7) * 8;
+    float ws[8], xs[8], v[2][8];
+    if (a.qx) load_part<FULL>(a.ws, n0 + c, a.N, ws);
+    if (a.qw) load_part<FULL>(a.xs, m0 + c, a.M, xs);
 #pragma unroll
     for (int k = 0; k < 2; k++) {
-        const int rr = (threadIdx.x >> 3) + 32 * k, m = m0 + rr, n = n0 + c;
-        float v[8] = {};
-        if (m < a.M) load_part(static_cast<const T*>(a.dy) + m * a.ld, n, a.N, a.wide, v);
+        const int m = m0 + (threadIdx.x >> 3) + 32 * k;
 #pragma unroll
-        for (int e = 0; e < 8; e++) tile[rr][c + e] = v[e];
-        if (a.qx && m < a.M) {
+        for (int e = 0; e < 8; e++) v[k][e] = 0.0f;
+        if (FULL || m < a.M) load_part<FULL>(static_cast<const T*>(a.dy) + m * a.ld, n0 + c, a.N, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const int rr = (threadIdx.x >> 3) + 32 * k, m = m0 + rr;
+        if constexpr (sizeof(T) == 2) {  // (the values as they were: their words)
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) *reinterpret_cast<uint32_t*>(&tile[rr][c + e]) = pack16(v[k][e], v[k][e + 1]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) tile[rr][c + e] = v[k][e];
+        }
+        if (a.qx && (FULL || m < a.M)) {
             const float up = scale_up(a.rowmax[m]);
-            hv8 hi, lo;
+            float p[8];
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const float p = n + e < a.N ? v[e] * a.ws[n + e] * up : 0.0f;
-                hi[e] = static_cast<_Float16>(p);
-                lo[e] = low_part(p, hi[e]);
-            }
-            char* o = a.qx + m * rowx + part_at(cn, 0, a.px) + 2 * c;
-            *reinterpret_cast<hv8*>(o) = hi;
-            if (a.px == 2) *reinterpret_cast<hv8*>(o + 128) = lo;
+            for (int e = 0; e < 8; e++) p[e] = v[k][e] * ws[e] * up;
+            store_parts(a.qx + m * rowx + part_at(cn, 0, a.px) + 2 * c, p, a.px);
         }
     }
     if (!a.qw) return;
@@ -154,20 +169,24 @@ __global__ __launch_bounds__(256) void lay_dy_kernel(DyArgs a) {
 #pragma unroll
     for (int k = 0; k < 2; k++) {
         const int rr = (threadIdx.x >> 3) + 32 * k, n = n0 + rr;
-        if (n >= a.N) continue;
+        if (!FULL && n >= a.N) continue;
         const float up = scale_up(a.colmax[n]);
-        hv8 hi, lo;
+        float p[8];
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const int m = m0 + c + e;
-            const float p = m < a.M ? tile[c + e][rr] * a.xs[m] * up : 0.0f;
-            hi[e] = static_cast<_Float16>(p);
-            lo[e] = low_part(p, hi[e]);
+            if constexpr (sizeof(T) == 2) p[e] = bf16_bits_to_f32(tile[c + e][rr]) * xs[e] * up;
+            else p[e] = tile[c + e][rr] * xs[e] * up;
         }
-        char* o = a.qw + n * roww + part_at(cm, 0, a.pw) + 2 * c;
-        *reinterpret_cast<hv8*>(o) = hi;
-        if (a.pw == 2) *reinterpret_cast<hv8*>(o + 128) = lo;
+        store_parts(a.qw + n * roww + part_at(cm, 0, a.pw) + 2 * c, p, a.pw);
     }
+}
+template <class T>
+__global__ __launch_bounds__(256) void lay_dy_kernel(DyArgs a) {
+    __shared__ T tile[64][66];
+    const int across = (a.N + 63) / 64;
+    const int cn = blockIdx.x % across, cm = blockIdx.x / across;
+    if (a.wide && cm * 64 + 64 <= a.M && cn * 64 + 64 <= a.N) lay_dy<true>(a, cm, cn, tile);
+    else lay_dy<false>(a, cm, cn, tile);
 }
 
 // Codes [R][C] (rows ld bytes apart, C a multiple of 16) to FP16 [C][Rpad]: 64 x 64 a workgroup.
