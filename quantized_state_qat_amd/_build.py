@@ -12,7 +12,7 @@ OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblaqat.so")
 SOURCES = ["la_api.cpp", "fwd.hip", "fwd_fast.hip", "fwd_wave.hip", "fwd_mfma.hip", "fwd_tok.hip", "decode.hip", "bwd.hip",
            "bwd_mfma.hip", "noalloc.hip", "chunk_fwd.hip", "chunk_bwd.hip", "la_layer.cpp", "layer_conv.hip", "layer_norm.hip",
-           "scan_step.hip", "scan_fwd.hip", "scan_bwd.hip", "la_proj.cpp", "linear_fwd.hip", "linear_bwd.hip", "gate_norm.hip"]
+           "scan_step.hip", "scan_fwd.hip", "scan_bwd.hip", "la_proj.cpp", "linear_fwd.hip", "linear_bwd.hip", "gate_norm.hip", "gate_bwd.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
