@@ -274,19 +274,17 @@ __global__ __launch_bounds__(256) void gate_fwd_kernel(GateFwd p) {
     }
 }
 
-// Lanes a row and pieces a lane: as in the residual norm, but that a few rows (one wave each would leave
-// SIMDs idle) take a workgroup each from 520 columns on.  PLACEHOLDER
+// Lanes a row and pieces a lane: one piece a lane up to 2048 columns (a wave with up to four pieces a lane, as
+// in the residual norm, took 189 us where a workgroup a row takes 149, of 40686 x 2048 joined and to INT8).
 template <class F>
-hipError_t by_width(int rows, int d, F&& f) {
+hipError_t by_width(int d, F&& f) {
     using std::integral_constant;
     const int pieces = d / kPiece;
-    if (rows <= 1024 && pieces > 64 && pieces <= 256) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     if (pieces <= 8) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
     if (pieces <= 16) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
     if (pieces <= 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
     if (pieces <= 64) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    if (pieces <= 128) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-    if (pieces <= 256) return f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    if (pieces <= 256) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     if (pieces <= 512) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
     if (pieces <= 1024) return f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
     return f(integral_constant<int, 256>{}, integral_constant<int, 8>{});
@@ -303,7 +301,7 @@ hipError_t launch_gate_fwd(const la_gate_norm_config& c, const GateArgs& a, hipS
                     c.ld_x ? c.ld_x : c.d, c.ld_z ? c.ld_z : c.d, a.x, a.z, a.w_post, a.alpha, a.res, a.w_pre, a.h, a.y,
                     static_cast<uint8_t*>(a.codes), a.scales};
     return by_type(c, [&](auto t) {
-        return by_width(c.rows, c.d, [&](auto lanes, auto ch) {
+        return by_width(c.d, [&](auto lanes, auto ch) {
             using T = decltype(t);
             constexpr int LANES = decltype(lanes)::value, CH = decltype(ch)::value;
             const unsigned grid = static_cast<unsigned>((c.rows + 256 / LANES - 1) / (256 / LANES));
