@@ -58,7 +58,7 @@ la_status la_linear_fwd(const la_linear_config* cfg, const void* x_codes, const 
  * (2^-22), both under a power of two for its row (for dweight its column): values 2^-29 of the row's
  * largest magnitude or smaller lose more.
  * The codes enter exactly.  Sums are FP32, joined in a fixed order; dbias is summed in double over
- * FP32 sums of 64 rows.  M and N up to 2^19.  Workspace: at least la_linear_bwd_workspace_bytes(cfg) bytes
+ * FP32 sums of 64 rows.  M and N up to 2^19, with below 2^23 tiles of 64 x 64.  Workspace: at least la_linear_bwd_workspace_bytes(cfg) bytes
  * (operands laid out for the products); 0 where there is nothing to sum or the call would be refused. */
 la_status la_linear_bwd(const la_linear_config* cfg, const void* x_codes, const float* x_scales, const void* w_codes,
                         const float* w_scales, const void* dy, void* dx, void* dweight, float* dbias, void* workspace,

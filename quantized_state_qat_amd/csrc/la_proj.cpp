@@ -30,8 +30,9 @@ la_status check_linear(const la_linear_config* c) {
 }
 la_status check_linear_bwd(const la_linear_config* c) {
     CHECK(check_linear(c));
-    if (c->M > (1 << 19) || c->N > (1 << 19))
-        return fail(LA_ERR_UNSUPPORTED, "the backward takes M and N up to 2^19 (M=%d N=%d)", c->M, c->N);
+    // (a launch lays out 64 x 64 of one or two operands a workgroup, beside the joins of dbias)
+    if (c->M > (1 << 19) || c->N > (1 << 19) || tiles64(c->M, c->N) >= (1 << 23))
+        return fail(LA_ERR_UNSUPPORTED, "the backward takes M and N up to 2^19, with below 2^23 tiles of 64 x 64 (M=%d N=%d)", c->M, c->N);
     return LA_OK;
 }
 

@@ -40,15 +40,11 @@ struct DyArgs {
     uint32_t* rowmax;  // [M] of |dy s_w|, or null
     uint32_t* colmax;  // [N] of |dy s_x|, or null
     float* part;       // [ceil(M / 64)][N], or null
+    float* dbias;      // [N], or null
     char* qx;          // [M][Npad] parts, or null
     char* qw;          // [N][Mpad] parts, or null
     int px, pw;        // parts
 };
-
-__global__ void clear_kernel(uint32_t* p, int64_t n) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i < n) p[i] = 0;
-}
 
 // Largest magnitudes of rows and columns (integer maxima: their order does not matter) and the sums
 // of 64 rows: a workgroup has 64 rows of 256 columns.
@@ -180,64 +176,116 @@ __device__ __forceinline__ void lay_dy(const DyArgs& a, int cm, int cn, T (&tile
         store_parts(a.qw + n * roww + part_at(cm, 0, a.pw) + 2 * c, p, a.pw);
     }
 }
+// The sums of the blocks of 64 rows, in double and in a fixed order: 32 columns a workgroup, eight interleaved sums.
+__device__ __forceinline__ void join_bias(const DyArgs& a, int block, double (&red)[8][32]) {
+    const int l = threadIdx.x & 31, q = threadIdx.x >> 5, n = block * 32 + l, blocks = (a.M + 63) / 64;
+    double s = 0.0;
+    if (n < a.N) {
+#pragma unroll 8
+        for (int p = q; p < blocks; p += 8) s += a.part[static_cast<int64_t>(p) * a.N + n];
+    }
+    red[q][l] = s;
+    __syncthreads();
+    if (q == 0 && n < a.N) {
+        s = 0.0;
+#pragma unroll
+        for (int k = 0; k < 8; k++) s += red[k][l];
+        a.dbias[n] = static_cast<float>(s);
+    }
+}
+
+// The first `bias` workgroups join dbias, the others lay out 64 x 64 of dy each.
 template <class T>
-__global__ __launch_bounds__(256) void lay_dy_kernel(DyArgs a) {
-    __shared__ T tile[64][66];
-    const int across = (a.N + 63) / 64;
-    const int cn = blockIdx.x % across, cm = blockIdx.x / across;
-    if (a.wide && cm * 64 + 64 <= a.M && cn * 64 + 64 <= a.N) lay_dy<true>(a, cm, cn, tile);
-    else lay_dy<false>(a, cm, cn, tile);
+__global__ __launch_bounds__(256) void lay_dy_kernel(DyArgs a, int bias) {
+    __shared__ union {
+        T tile[64][66];
+        double red[8][32];
+    } lds;
+    if (static_cast<int>(blockIdx.x) < bias) return join_bias(a, blockIdx.x, lds.red);
+    const int across = (a.N + 63) / 64, at = blockIdx.x - bias;
+    const int cn = at % across, cm = at / across;
+    if (a.wide && cm * 64 + 64 <= a.M && cn * 64 + 64 <= a.N) lay_dy<true>(a, cm, cn, lds.tile);
+    else lay_dy<false>(a, cm, cn, lds.tile);
 }
 
 // Codes [R][C] (rows ld bytes apart, C a multiple of 16) to FP16 [C][Rpad]: 64 x 64 a workgroup.
-__global__ __launch_bounds__(256) void lay_codes_kernel(const int8_t* codes, int64_t ld, int R, int C, char* out) {
-    __shared__ __align__(16) int8_t tile[64][80];
-    const int across = (C + 63) / 64;
-    const int c0 = (blockIdx.x % across) * 64, cr = blockIdx.x / across, r0 = cr * 64;
+struct Codes {
+    const int8_t* codes;
+    int64_t ld;
+    int R, C;
+    char* out;
+    int blocks;
+};
+__device__ __forceinline__ void lay_codes(const Codes& a, int block, int8_t (&tile)[64][80]) {
+    const int across = (a.C + 63) / 64;
+    const int c0 = (block % across) * 64, cr = block / across, r0 = cr * 64;
     {
         const int rr = threadIdx.x >> 2, c = (threadIdx.x & 3) * 16;
         uv4 v = {};
-        if (r0 + rr < R && c0 + c < C) v = load16(codes + (r0 + rr) * ld + c0 + c);
+        if (r0 + rr < a.R && c0 + c < a.C) v = load16(a.codes + (r0 + rr) * a.ld + c0 + c);
         *reinterpret_cast<uv4*>(&tile[rr][c]) = v;
     }
     __syncthreads();
-    const int64_t row = part_at((R + 63) / 64, 0, 1);
+    const int64_t row = part_at((a.R + 63) / 64, 0, 1);
     const int c = (threadIdx.x & 7) * 8;
 #pragma unroll
     for (int k = 0; k < 2; k++) {
         const int rr = (threadIdx.x >> 3) + 32 * k;
-        if (c0 + rr >= C) continue;
+        if (c0 + rr >= a.C) continue;
         hv8 h;
 #pragma unroll
         for (int e = 0; e < 8; e++) h[e] = static_cast<_Float16>(tile[c + e][rr]);
-        *reinterpret_cast<hv8*>(out + (c0 + rr) * row + part_at(cr, 0, 1) + 2 * c) = h;
+        *reinterpret_cast<hv8*>(a.out + (c0 + rr) * row + part_at(cr, 0, 1) + 2 * c) = h;
     }
 }
+// Both operands of codes, and zeros to what the maxima of dy go to.
+__global__ __launch_bounds__(256) void lay_codes_kernel(Codes x, Codes w, uint32_t* clear, int64_t words) {
+    __shared__ __align__(16) int8_t tile[64][80];
+    const int b = blockIdx.x;
+    if (b < x.blocks) return lay_codes(x, b, tile);
+    if (b < x.blocks + w.blocks) return lay_codes(w, b - x.blocks, tile);
+    const int64_t at = static_cast<int64_t>(b - x.blocks - w.blocks) * 1024 + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        if (at + 256 * k < words) clear[at + 256 * k] = 0;
+}
 
-// out[j][i] = 2^.. (row j) times the sum over the parts of part[p][j][i], in order; 4 columns a lane.
-template <class O>
-__global__ __launch_bounds__(256) void join_kernel(const float* part, int parts, int I, int64_t n, const uint32_t* row, O* out) {
-    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-    if (at >= n) return;
+// out[j][i] = scale_back(row j) times the sum over the parts of sums[p][j][i], in order; 4 columns a lane.
+struct Join {
+    const float* sums;
+    int parts, I, out_dtype;
+    int64_t n;  // I J
+    const uint32_t* row;
+    void* out;
+    int blocks;
+};
+__device__ __forceinline__ void join(const Join& a, int block) {
+    const int64_t at = (static_cast<int64_t>(block) * 256 + threadIdx.x) * 4;
+    if (at >= a.n) return;
     double s[4] = {};
-    for (int p = 0; p < parts; p++) {
-        const fv4 v = *reinterpret_cast<const fv4*>(part + p * n + at);
+    for (int p = 0; p < a.parts; p++) {
+        const fv4 v = *reinterpret_cast<const fv4*>(a.sums + p * a.n + at);
 #pragma unroll
         for (int e = 0; e < 4; e++) s[e] += v[e];
     }
-    const float k = scale_back(row[at / I]);
+    const float k = scale_back(a.row[at / a.I]);
     float v[4];
 #pragma unroll
     for (int e = 0; e < 4; e++) v[e] = static_cast<float>(s[e]) * k;
-    if constexpr (sizeof(O) == 2) *reinterpret_cast<uv2*>(out + at) = uv2{pack16(v[0], v[1]), pack16(v[2], v[3])};
-    else *reinterpret_cast<fv4*>(out + at) = fv4{v[0], v[1], v[2], v[3]};
+    if (a.out_dtype == LA_BF16) *reinterpret_cast<uv2*>(static_cast<uint16_t*>(a.out) + at) = uv2{pack16(v[0], v[1]), pack16(v[2], v[3])};
+    else *reinterpret_cast<fv4*>(static_cast<float*>(a.out) + at) = fv4{v[0], v[1], v[2], v[3]};
+}
+__global__ __launch_bounds__(256) void join_kernel(Join x, Join w) {
+    const int b = blockIdx.x;
+    if (b < x.blocks) join(x, b);
+    else join(w, b - x.blocks);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // What the workspace holds, in this order.
 struct Layout {
-    size_t rowmax, colmax, part, qx, qw, pw, px, sums, end;  // offsets; pw: w's codes, px: x's
+    size_t rowmax, colmax, part, qx, qw, pw, px, sums_x, sums_w, end;  // offsets; pw: w's codes, px: x's
     int parts_x, parts_w;  // of an operand
     Cut dx, dw;            // the two products
 };
@@ -250,30 +298,25 @@ Layout layout(const la_linear_config& c) {
     l.rowmax = take(4 * M), l.colmax = take(4 * N), l.part = take(4 * mc * N);
     l.qx = take(M * nc * 128 * l.parts_x), l.qw = take(N * mc * 128 * l.parts_w);
     l.pw = take(K * nc * 128), l.px = take(K * mc * 128);
-    l.dx = cut_product(c.K, c.M, gemm_steps(nc * 128, l.parts_x - 1), 16);
-    l.dw = cut_product(c.K, c.N, gemm_steps(mc * 128, l.parts_w - 1), 16);
-    const size_t x = l.dx.parts > 1 ? l.dx.parts * M * K * 4 : 0, w = l.dw.parts > 1 ? l.dw.parts * N * K * 4 : 0;
-    l.sums = take(x > w ? x : w);  // (one product after the other)
+    const auto most = [](size_t n) { return n <= (size_t{1} << 30) ? 16 : 1; };  // (the join's grid)
+    l.dx = cut_product(c.K, c.M, gemm_steps(nc * 128, l.parts_x - 1), most(M * K));
+    l.dw = cut_product(c.K, c.N, gemm_steps(mc * 128, l.parts_w - 1), most(N * K));
+    l.sums_x = take(l.dx.parts > 1 ? l.dx.parts * M * K * 4 : 0);
+    l.sums_w = take(l.dw.parts > 1 ? l.dw.parts * N * K * 4 : 0);
     l.end = at;
     return l;
 }
 
-// One product, and the join of its parts.
-hipError_t product(GemmArgs& g, const Cut& cut, int out_dtype, float* sums, hipStream_t s) {
-    const int steps = gemm_steps(g.kbytes, g.shift);
+// One product; parts of its sum go to `sums`, and are left to `join`.
+hipError_t product(GemmArgs& g, const Cut& cut, int out_dtype, float* sums, Join& join, hipStream_t s) {
     g.parts = cut.parts;
-    g.part_steps = (steps + cut.parts - 1) / cut.parts;
-    if (cut.parts == 1)
-        return out_dtype == LA_BF16 ? launch_gemm<_Float16, uint16_t, true>(g, cut.tiling, s) : launch_gemm<_Float16, float, true>(g, cut.tiling, s);
-    const void* row = g.row;
-    void* out = g.out;
-    g.row = nullptr, g.out = sums;
-    if (hipError_t e = launch_gemm<_Float16, float, true>(g, cut.tiling, s)) return e;
-    const int64_t n = static_cast<int64_t>(g.I) * g.J;
-    const unsigned grid = static_cast<unsigned>((n / 4 + 255) / 256);
-    if (out_dtype == LA_BF16) join_kernel<<<grid, 256, 0, s>>>(sums, cut.parts, g.I, n, static_cast<const uint32_t*>(row), static_cast<uint16_t*>(out));
-    else join_kernel<<<grid, 256, 0, s>>>(sums, cut.parts, g.I, n, static_cast<const uint32_t*>(row), static_cast<float*>(out));
-    return hipGetLastError();
+    g.part_steps = (gemm_steps(g.kbytes, g.shift) + cut.parts - 1) / cut.parts;
+    if (cut.parts > 1) {
+        const int64_t n = static_cast<int64_t>(g.I) * g.J;
+        join = {sums, cut.parts, g.I, out_dtype, n, static_cast<const uint32_t*>(g.row), g.out, static_cast<int>((n / 4 + 255) / 256)};
+        g.row = nullptr, g.out = sums, out_dtype = LA_F32;
+    }
+    return out_dtype == LA_BF16 ? launch_gemm<_Float16, uint16_t, true>(g, cut.tiling, s) : launch_gemm<_Float16, float, true>(g, cut.tiling, s);
 }
 
 }  // namespace
@@ -288,40 +331,42 @@ hipError_t launch_linear_bwd(const la_linear_config& c, const LinearArgs& a, hip
     d.wide = d.ld * es % 16 == 0;
     d.rowmax = a.dx ? reinterpret_cast<uint32_t*>(a.work + l.rowmax) : nullptr;
     d.colmax = a.dw ? reinterpret_cast<uint32_t*>(a.work + l.colmax) : nullptr;
-    d.part = a.dbias ? reinterpret_cast<float*>(a.work + l.part) : nullptr;
+    d.part = a.dbias ? reinterpret_cast<float*>(a.work + l.part) : nullptr, d.dbias = a.dbias;
     d.qx = a.dx ? a.work + l.qx : nullptr, d.qw = a.dw ? a.work + l.qw : nullptr;
     d.px = l.parts_x, d.pw = l.parts_w;
     const int64_t words = static_cast<int64_t>((l.part - l.rowmax) / 4);
     const int64_t mc = (c.M + 63) / 64, nc = (c.N + 63) / 64, kc = (c.K + 63) / 64;
-    const auto blocks = [](int64_t n) { return dim3(static_cast<unsigned>(n)); };
-    if (words > 0) clear_kernel<<<blocks((words + 255) / 256), 256, 0, s>>>(reinterpret_cast<uint32_t*>(a.work + l.rowmax), words);
-    const bool work = c.M > 0 && c.N > 0;  // (otherwise the sums are empty: zeros)
-    if (!work) {
-    } else if (es == 2) stats_kernel<uint16_t><<<blocks(mc * ((c.N + 255) / 256)), 256, 0, s>>>(d);
-    else stats_kernel<float><<<blocks(mc * ((c.N + 255) / 256)), 256, 0, s>>>(d);
+    const Codes x{a.x, c.ld_x ? c.ld_x : c.K, c.M, c.K, a.work + l.px, a.dw ? static_cast<int>(mc * kc) : 0};
+    const Codes w{a.w, c.K, c.N, c.K, a.work + l.pw, a.dx ? static_cast<int>(nc * kc) : 0};
+    const int64_t first = x.blocks + w.blocks + (words + 1023) / 1024;
+    if (first > 0) lay_codes_kernel<<<static_cast<unsigned>(first), 256, 0, s>>>(x, w, reinterpret_cast<uint32_t*>(a.work + l.rowmax), words);
+    // (without tokens or channels the sums are empty: zeros)
+    const int64_t stats = mc * ((c.N + 255) / 256), bias = a.dbias ? (c.N + 31) / 32 : 0, lay = bias + (a.dx || a.dw ? mc * nc : 0);
+    if (stats > 0) {
+        if (es == 2) stats_kernel<uint16_t><<<static_cast<unsigned>(stats), 256, 0, s>>>(d);
+        else stats_kernel<float><<<static_cast<unsigned>(stats), 256, 0, s>>>(d);
+    }
+    if (lay > 0) {
+        if (es == 2) lay_dy_kernel<uint16_t><<<static_cast<unsigned>(lay), 256, 0, s>>>(d, static_cast<int>(bias));
+        else lay_dy_kernel<float><<<static_cast<unsigned>(lay), 256, 0, s>>>(d, static_cast<int>(bias));
+    }
     if (hipError_t e = hipGetLastError()) return e;
-    if (a.dbias && c.N > 0)
-        if (hipError_t e = launch_reduce_parts(d.part, static_cast<int>(mc), c.N, a.dbias, c.N, nullptr, s)) return e;
-    if (!a.dx && !a.dw) return hipSuccess;
-    if (!work) {
-    } else if (es == 2) lay_dy_kernel<uint16_t><<<blocks(mc * nc), 256, 0, s>>>(d);
-    else lay_dy_kernel<float><<<blocks(mc * nc), 256, 0, s>>>(d);
+    Join jx{}, jw{};
     if (a.dx && c.M > 0) {
-        if (nc > 0) lay_codes_kernel<<<blocks(nc * kc), 256, 0, s>>>(a.w, c.K, c.N, c.K, a.work + l.pw);
         GemmArgs g;
         g.P = a.work + l.pw, g.ldP = nc * 128, g.I = c.K, g.kbytes = static_cast<int>(nc * 128);
         g.Q = d.qx, g.ldQ = nc * 128 * d.px, g.J = c.M, g.shift = d.px - 1;
         g.row = d.rowmax, g.out = a.dx, g.ldo = c.K, g.wide = 1;
-        if (hipError_t e = product(g, l.dx, c.x_dtype, reinterpret_cast<float*>(a.work + l.sums), s)) return e;
+        if (hipError_t e = product(g, l.dx, c.x_dtype, reinterpret_cast<float*>(a.work + l.sums_x), jx, s)) return e;
     }
     if (a.dw && c.N > 0) {
-        if (mc > 0) lay_codes_kernel<<<blocks(mc * kc), 256, 0, s>>>(a.x, c.ld_x ? c.ld_x : c.K, c.M, c.K, a.work + l.px);
         GemmArgs g;
         g.P = a.work + l.px, g.ldP = mc * 128, g.I = c.K, g.kbytes = static_cast<int>(mc * 128);
         g.Q = d.qw, g.ldQ = mc * 128 * d.pw, g.J = c.N, g.shift = d.pw - 1;
         g.row = d.colmax, g.out = a.dw, g.ldo = c.K, g.wide = 1;
-        if (hipError_t e = product(g, l.dw, c.dw_dtype, reinterpret_cast<float*>(a.work + l.sums), s)) return e;
+        if (hipError_t e = product(g, l.dw, c.dw_dtype, reinterpret_cast<float*>(a.work + l.sums_w), jw, s)) return e;
     }
+    if (jx.blocks + jw.blocks > 0) join_kernel<<<static_cast<unsigned>(jx.blocks + jw.blocks), 256, 0, s>>>(jx, jw);
     return hipGetLastError();
 }
 

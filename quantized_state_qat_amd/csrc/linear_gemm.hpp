@@ -189,18 +189,18 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, char* lds,
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, offset, base, 0, 0);
 }
 
-// WI x WJ waves with TI x TJ tiles of 32 x 32 each.  Two steps of 128 bytes of every row in LDS: while the
-// waves multiply one, the next one's loads go straight to LDS.  A step is four slices of one matrix
+// WI x WJ waves with TI x TJ tiles of 32 x 32 each.  NS steps of 128 bytes of every row in LDS: while the
+// waves multiply one, the next ones' loads go straight to LDS.  A step is four slices of one matrix
 // instruction's depth: a slice's operands are read from LDS while the slice before is multiplied, and
-// once a step's last slice is in registers one barrier frees its LDS for the loads of the next but one.
+// once a step's last slice is in registers one barrier frees its LDS for the loads of the step NS further.
 // The order of reads, loads and products is spelled out (the compiler bunches the reads).  A workgroup
 // takes tiles of out in turn, and the loads run on into the next one, under the stores of the one before.
-template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int MINW>
+template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int NS, int MINW>
 __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs a, int across, int down) {
     constexpr int NW = WI * WJ, BI = 32 * TI * WI, BJ = 32 * TJ * WJ, STAGE = (BI + BJ) * 128;
-    constexpr int LI = BI / (8 * NW), LJ = BJ / (8 * NW);  // loads a wave: 8 rows each
-    static_assert(BI % (8 * NW) == 0 && BJ % (8 * NW) == 0 && NW % 2 == 0);
-    __shared__ __align__(128) char lds[2 * STAGE + NW * kStoreLds];
+    constexpr int LI = BI / (8 * NW), LJ = BJ / (8 * NW);  // loads a wave and step: 8 rows each
+    static_assert(BI % (8 * NW) == 0 && BJ % (8 * NW) == 0 && NW % 2 == 0 && (NS & (NS - 1)) == 0);
+    __shared__ __align__(128) char lds[NS * STAGE + NW * kStoreLds];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 31, q = lane >> 5;
     const int tiles = across * down, units = tiles * a.parts, steps = a.part_steps;
     const int lrow = 8 * wave + (lane >> 3);  // and every 8 NW rows further: the swizzle is the same
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs 
     };
     const int wi = (wave % WI) * 32 * TI, wj = (wave / WI) * 32 * TJ;
     const int prow = wi + tile_row(r), qrow = wj + r;
-    const int pbase = prow * 128 + 16 * (q ^ swizzle(prow)), qbase = BI * 128 + qrow * 128 + 16 * (q ^ swizzle(qrow));
+    const int pbase = prow * 128 + 16 * (q ^ swizzle(prow)), qbase = (BI + qrow) * 128 + 16 * (q ^ swizzle(qrow));
     uv4 fp[2][TI], fq[2][TJ];
     auto fetch = [&](int stage, int slice) {  // (the pieces of a slice are 2 further than those of the one before)
         const char* sp = lds + stage * STAGE + (pbase ^ (32 * slice));
@@ -280,66 +280,70 @@ __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs 
         __builtin_amdgcn_sched_barrier(0);
     };
     aim();
-    issue(0);
-    advance();
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    issue(1);
-    advance();
+#pragma unroll
+    for (int k = 0; k < NS; k++) {
+        if (k == 1) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+        }
+        issue(k);
+        advance();
+    }
     fetch(0, 0);
     int stage = 0;
-    bool landed = false;  // the loads of the next step are known to have landed
+    int landed = 0;  // steps to come whose loads are known to have landed
     for (int id = blockIdx.x; id < units; id += gridDim.x) {
 #pragma unroll
-        for (int ti = 0; ti < TI; ti++)
-#pragma unroll
-            for (int tj = 0; tj < TJ; tj++) acc[ti][tj] = {};
-        for (int t = 0; t < steps; t++, stage ^= 1) {
+        for (int k = 0; k < TI * TJ; k++) acc[k / TJ][k % TJ] = {};
+        for (int t = 0; t < steps; t++) {
+            const int next = (stage + 1) & (NS - 1);
 #pragma unroll
             for (int k = 0; k < 3; k++) {
                 fetch(stage, k + 1);
                 multiply(k);
                 interleave(std::false_type{});
             }
-            // this step is in registers and the next one in LDS, in every wave
-            if (!landed) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            landed = false;
+            // this step is in registers and the next one in LDS, in every wave (the ones behind it may be on their way)
+            if (landed == 0) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * (LI + LJ)) : "memory");
+            else landed--;
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
             issue(stage);
-            fetch(stage ^ 1, 0);
+            fetch(next, 0);
             multiply(3);
             interleave(std::true_type{});
             advance();
+            stage = next;
         }
         const int unit = xcd_tile(id, units);
         const TileAt t = tile_order(unit % tiles, across, down);
         O* out = static_cast<O*>(a.out) + unit / tiles * static_cast<int64_t>(a.J) * a.ldo;
-        store_tiles<O, BITS, TI, TJ>(a, out, t.i * BI + wi, t.j * BJ + wj, acc, lds + 2 * STAGE + wave * kStoreLds);
-        landed = steps > 0;
+        store_tiles<O, BITS, TI, TJ>(a, out, t.i * BI + wi, t.j * BJ + wj, acc, lds + NS * STAGE + wave * kStoreLds);
+        landed = steps < NS - 1 ? steps : NS - 1;
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // no load may reach LDS after the workgroup
 }
 
 // PER: workgroups that a CU holds.
-template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int MINW, int PER>
+template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int NS, int MINW, int PER>
 void launch_tiles(const GemmArgs& a, hipStream_t s) {
     constexpr int BI = 32 * TI * WI, BJ = 32 * TJ * WJ;
     const int across = (a.I + BI - 1) / BI, down = (a.J + BJ - 1) / BJ;
     const int units = across * down * a.parts, most = 256 * PER;
-    gemm_tile_kernel<E, O, BITS, WI, WJ, TI, TJ, MINW>
+    gemm_tile_kernel<E, O, BITS, WI, WJ, TI, TJ, NS, MINW>
         <<<static_cast<unsigned>(units < most ? units : most), 64 * WI * WJ, 0, s>>>(a, across, down);
 }
 
-// The tiles that a product is cut into.
-enum Tiling { kTiles256, kTiles128, kTiles64 };
+// The tiles that a product is cut into (of 64 x 64 with two or four steps in LDS).
+enum Tiling { kTiles256, kTiles128, kTiles64, kTiles64Deep };
 
 template <class E, class O, bool BITS>
 hipError_t launch_gemm(const GemmArgs& a, Tiling t, hipStream_t s) {
-    if (t == kTiles256) launch_tiles<E, O, BITS, 2, 4, 4, 2, 2, 1>(a, s);
-    else if (t == kTiles128) launch_tiles<E, O, BITS, 2, 2, 2, 2, 2, 2>(a, s);
-    else launch_tiles<E, O, BITS, 2, 2, 1, 1, 4, 3>(a, s);
+    if (t == kTiles256) launch_tiles<E, O, BITS, 2, 4, 4, 2, 2, 2, 1>(a, s);
+    else if (t == kTiles128) launch_tiles<E, O, BITS, 2, 2, 2, 2, 2, 2, 2>(a, s);
+    else if (t == kTiles64) launch_tiles<E, O, BITS, 2, 2, 1, 1, 2, 4, 3>(a, s);
+    else launch_tiles<E, O, BITS, 2, 2, 1, 1, 4, 2, 2>(a, s);
     return hipGetLastError();
 }
 
@@ -357,10 +361,10 @@ struct Cut {
 };
 inline Cut cut_product(int64_t I, int64_t J, int steps, int most_parts) {
     constexpr struct { int size, per; float fixed, few, full; } kinds[] = {
-        {256, 1, 7.0f, 1.1f, 1.75f}, {128, 2, 5.0f, 0.42f, 1.2f}, {64, 3, 3.5f, 0.24f, 0.65f}};
+        {256, 1, 7.0f, 1.1f, 1.75f}, {128, 2, 5.0f, 0.42f, 1.2f}, {64, 3, 3.5f, 0.27f, 0.65f}, {64, 2, 3.5f, 0.25f, 0.47f}};
     Cut best{kTiles256, 1};
     float least = 0.0f;
-    for (int k = 0; k < 3; k++) {
+    for (int k = 0; k < 4; k++) {
         for (int parts = 1; parts <= most_parts && (parts == 1 || steps / parts >= 4); parts *= 2) {
             const auto& t = kinds[k];
             const int64_t units = (I + t.size - 1) / t.size * ((J + t.size - 1) / t.size) * parts, slots = 256 * t.per;

@@ -280,3 +280,307 @@ def test_gate_norm_bwd(k):
     dx2 = torch.empty(rows, cfg.ld_x or d, dtype=t, device="cuda")[:, :d]
     la.la_gate_norm_bwd(cfg, *args[:7], both, dx2, None, both, None, None, None, None, 0)
     assert torch.equal(dx2, dx) and (both is None or torch.equal(both, dres))
+
+
+def test_linear_extremes():
+    """The integer sum at its largest, scales of zero, infinity and NaN, all tokens' counts around the tiles."""
+    K = 65536
+    xc = torch.full((3, K), -128, dtype=torch.int8, device="cuda")
+    wc = torch.full((5, K), -128, dtype=torch.int8, device="cuda")
+    wc[1], wc[2, ::2] = 127, 0
+    xs, ws = torch.tensor([1.0, 0.0, 2.0 ** -30], device="cuda"), torch.ones(5, device="cuda")
+    y = torch.empty(3, 5, device="cuda")
+    la.la_linear_fwd(la.LinearConfig(M=3, N=5, K=K, out_dtype=la.LA_F32), xc, xs, wc, ws, None, y)
+    exact = (xc.cpu().long() @ wc.cpu().long().T).double() * xs.cpu().double()[:, None]
+    assert torch.equal(y.cpu(), exact.float())
+    for M in (3, 70, 130):
+        xc, xs = codes(gen(1), M, 64)
+        wc, ws = codes(gen(2), 200, 64)
+        clean = torch.empty(M, 200, device="cuda")
+        cfg = la.LinearConfig(M=M, N=200, K=64, out_dtype=la.LA_F32)
+        la.la_linear_fwd(cfg, xc, xs, wc, ws, None, clean)
+        xs[M - 1], ws[7], ws[8] = float("nan"), float("inf"), float("nan")
+        y = torch.empty_like(clean)
+        la.la_linear_fwd(cfg, xc, xs, wc, ws, None, y)
+        keep = [n for n in range(200) if n not in (7, 8)]
+        assert torch.equal(y[:M - 1][:, keep], clean[:M - 1][:, keep])  # nothing leaves its row or column
+        assert y[M - 1].isnan().all() and y[:, 8].isnan().all() and not y[:, 7].isfinite().any()
+
+
+@pytest.mark.parametrize("tx,tw", [(BF, BF), (F32, F32)])
+def test_linear_bwd_infinities_stay_in_their_rows(tx, tw):
+    M, N, K = 150, 140, 96
+    xc, xs = codes(gen(3), M, K)
+    wc, ws = codes(gen(4), N, K)
+    wc[wc == 0] = 1
+    xc[xc == 0] = 1
+    cfg = la.LinearConfig(M=M, N=N, K=K, out_dtype=la.LA_F32, x_dtype=CODE[tx], dw_dtype=CODE[tw])
+    n = la.la_linear_bwd_workspace_bytes(cfg)
+    ws_ = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def grads(dy):
+        out = torch.empty(M, K, dtype=tx, device="cuda"), torch.empty(N, K, dtype=tw, device="cuda"), torch.empty(N, device="cuda")
+        la.la_linear_bwd(cfg, xc, xs, wc, ws, dy, *out, ws_, n)
+        return out
+
+    dy = draw(gen(5), M, N, dtype=F32)
+    dy[20] = 0.0   # a token without a gradient
+    dy[:, 30] = 0.0
+    clean = grads(dy)
+    assert (clean[0][20] == 0).all() and (clean[1][30] == 0).all() and clean[2][30] == 0
+    dy[3, 5], dy[90, 100] = float("inf"), float("nan")
+    dx, dw, db = grads(dy)
+    rows, cols = [m for m in range(M) if m not in (3, 90)], [k for k in range(N) if k not in (5, 100)]
+    assert torch.equal(dx[rows], clean[0][rows]) and torch.equal(dw[cols], clean[1][cols]) and torch.equal(db[cols], clean[2][cols])
+    # one infinity times codes that are not zero is an infinity of their sign
+    assert torch.equal(dx[3].float(), torch.sign(wc[5].float()) * float("inf")) and torch.equal(dw[5].float(), torch.sign(xc[3].float()) * float("inf"))
+    assert dx[90].isnan().all() and dw[100].isnan().all() and db[5] == float("inf") and db[100].isnan()
+
+
+def test_linear_bwd_keeps_the_bits_of_its_type():
+    """Errors of the operands are independent: the 2-norm of a bf16 gradient's stays that of its own rounding
+    (2^-8 / sqrt(12) to 2^-8 / sqrt(3) of a value, a little less than 2^-9.2 on average over a binade; 2^-9 with
+    the operands' 2^-11), of an FP32 one's below 2^-20."""
+    M, N, K = 1000, 640, 528
+    xc, xs = codes(gen(6), M, K)
+    wc, ws = codes(gen(7), N, K)
+    dy = draw(gen(8), M, N, scale=1e-4) * torch.exp(draw(gen(9), M, 1, dtype=F32)).to(BF)
+    for tx, bound in ((BF, 2.0 ** -9), (F32, 2.0 ** -20)):
+        cfg = la.LinearConfig(M=M, N=N, K=K, x_dtype=CODE[tx], dw_dtype=CODE[tx])
+        n = la.la_linear_bwd_workspace_bytes(cfg)
+        dx, dw = torch.empty(M, K, dtype=tx, device="cuda"), torch.empty(N, K, dtype=tx, device="cuda")
+        la.la_linear_bwd(cfg, xc, xs, wc, ws, dy, dx, dw, None, torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+        for got, want in zip((dx, dw), R.linear_bwd(*[np64(v) for v in (xc, xs, wc, ws, dy)])):
+            assert np.linalg.norm(np64(got) - want) <= bound * np.linalg.norm(want)
+
+
+def test_linear_without_tokens_or_channels():
+    for M, N in ((0, 40), (40, 0)):
+        cfg = la.LinearConfig(M=M, N=N, K=64, out_dtype=la.LA_F32, x_dtype=la.LA_F32)
+        xc, xs = codes(gen(1), M, 64)
+        wc, ws = codes(gen(2), N, 64)
+        n = la.la_linear_bwd_workspace_bytes(cfg)
+        out = [torch.full(s, 7.0, device="cuda") for s in ((M, 64), (N, 64), (N,))]
+        la.la_linear_bwd(cfg, xc, xs, wc, ws, torch.empty(M, N, device="cuda"), *out, torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda"), n)
+        assert all((v == 0).all() for v in out)
+
+
+def test_linear_past_32_bits():
+    M, N, K, ld = (1 << 20) + 3, 4104, 16, 4112
+    xc = torch.zeros(M, ld, dtype=torch.int8, device="cuda")
+    xc[-200:, :K] = codes(gen(1), 200, K)[0]
+    wc, ws = codes(gen(2), N, K)
+    xs = torch.ones(M, device="cuda")
+    y = torch.empty(M, N, dtype=BF, device="cuda")
+    la.la_linear_fwd(la.LinearConfig(M=M, N=N, K=K, ld_x=ld), xc[:, :K], xs, wc, ws, None, y)
+    want = (xc[-200:, :K].float() @ wc.float().T * ws).to(BF)
+    assert torch.equal(y[-200:], want) and (y[0] == 0).all()
+    del y
+    # the backward: rows of dx and of the laid out operands past 2^32 elements
+    M, N, K = 1 << 19, 24, 8320
+    xc = torch.zeros(M, K, dtype=torch.int8, device="cuda")
+    xc[-64:] = codes(gen(3), 64, K)[0]
+    wc, ws = codes(gen(4), N, K)
+    dy = torch.zeros(M, N, device="cuda")
+    dy[-64:] = draw(gen(5), 64, N, dtype=F32)
+    xs = torch.full((M,), 0.01, device="cuda")
+    cfg = la.LinearConfig(M=M, N=N, K=K, out_dtype=la.LA_F32)
+    n = la.la_linear_bwd_workspace_bytes(cfg)
+    dx, dw = torch.empty(M, K, dtype=BF, device="cuda"), torch.empty(N, K, device="cuda")
+    la.la_linear_bwd(cfg, xc, xs, wc, ws, dy, dx, dw, None, torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+    args = [np64(xc[-64:]), np64(xs[-64:]), np64(wc), np64(ws), np64(dy[-64:])]
+    want, mag = R.linear_bwd(*args), R.linear_bwd(*[np.abs(a) for a in args])
+    close(dx[-64:], want[0], mag[0], 2.0 ** -11 + 25 * 2.0 ** -23, "dx")
+    close(dw, want[1], mag[1], 2.0 ** -22 + 65 * 2.0 ** -23, "dweight")
+    assert (dx[:64] == 0).all()
+
+
+def test_gate_norm_past_32_bits():
+    rows, d = (1 << 18) + 77, 16384
+    x = torch.zeros(rows, d, dtype=BF, device="cuda")
+    x[-3:] = draw(gen(1), 3, d)
+    w = draw(gen(2), d, dtype=F32)
+    codes_, scales = torch.empty(rows, d, dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    la.la_gate_norm_fwd(la.GateNormConfig(rows=rows, d=d, pre=0, qdq=la.LA_QDQ_INT8_GROUP), x, None, w, None, None, None, None, None, codes_, scales)
+    c3, s3 = torch.empty(3, d, dtype=torch.int8, device="cuda"), torch.empty(3, device="cuda")
+    la.la_gate_norm_fwd(la.GateNormConfig(rows=3, d=d, pre=0, qdq=la.LA_QDQ_INT8_GROUP), x[-3:], None, w, None, None, None, None, None, c3, s3)
+    assert torch.equal(codes_[-3:], c3) and torch.equal(scales[-3:], s3) and (codes_[:3] == 0).all() and (scales[:3] == 1).all()
+    dy = x  # (any values)
+    dx = torch.empty_like(x)
+    la.la_gate_norm_bwd(la.GateNormConfig(rows=rows, d=d), x, None, w, None, None, None, dy, None, dx, None, None, None, None, None, None, 0)
+    d3 = torch.empty_like(x[-3:])
+    la.la_gate_norm_bwd(la.GateNormConfig(rows=3, d=d), x[-3:], None, w, None, None, None, dy[-3:], None, d3, None, None, None, None, None, None, 0)
+    assert torch.equal(dx[-3:], d3) and (dx[:3] == 0).all()
+
+
+@pytest.mark.parametrize("d,head", [(64, 16), (520, 0), (2048, 128), (4096, 0), (16384, 0)])
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("codec", ["none", "int8", "e4m3"])
+def test_gate_norm_infinities_and_nan(d, head, t, codec):
+    """They stay in their row, reach its head or the row by the formula, and codes are defined."""
+    qdq = dict(none=la.LA_QDQ_NONE, int8=la.LA_QDQ_INT8_GROUP, e4m3=la.LA_QDQ_E4M3_TILE)[codec]
+    cfg = la.GateNormConfig(rows=5, d=d, head=head, gate=la.LA_GATE_SIGMOID, qdq=qdq, x_dtype=CODE[t], out_dtype=la.LA_F32)
+    x, z = draw(gen(1), 5, d, dtype=t), draw(gen(2), 5, d, dtype=t)
+    x[1] = 0.0
+    z[4, :3] = torch.tensor([float("inf"), float("-inf"), -200.0]).to(t)
+
+    def run():
+        y = torch.empty(5, d, device="cuda")
+        c = torch.empty(5, d, dtype=torch.uint8, device="cuda") if qdq else None
+        s = torch.empty(5, device="cuda") if qdq else None
+        la.la_gate_norm_fwd(cfg, x, z, None, None, None, None, None, y, c, s)
+        return y, c, s
+
+    clean = run()
+    assert clean[0].isfinite().all() and (clean[0][1] == 0).all() and (clean[0][4, 1:3] == 0).all()
+    x[2, 8], x[3, 8] = float("nan"), float("inf")
+    y, c, s = run()
+    for a, b in zip((y, c, s), clean):
+        assert a is None or all(torch.equal(a[r], b[r]) for r in (0, 1, 4))
+    assert y[2, 8].isnan() and y[3, 8].isnan()  # inf / rms(inf)
+    if codec != "none":
+        assert s[2].isnan() and s[3].isnan() and y[2].isnan().all() and ((c[2] == 0) if codec == "int8" else (c[2] & 0x7F) == 0x7F).all()  # (E4M3 has a NaN of each sign)
+    else:
+        width = head or d
+        assert y[2, :width].isnan().all() and (y[3, :8] == 0).all() and (width == d or y[2:4, width:].isfinite().all())
+
+
+# ------------------------------------------------------------------------------ used together
+def layer(s, cfgs):
+    """A layer from the recurrence's output to the next one's projected input: gated norm to codes, output
+    projection, join to the residual stream and codes, input projection."""
+    g, o, j, i = cfgs
+    la.la_gate_norm_fwd(g, s["o"], s["z"], s["w_o"], None, None, None, None, None, s["c0"], s["s0"])
+    la.la_linear_fwd(o, s["c0"], s["s0"], s["wo"][0], s["wo"][1], None, s["y0"])
+    la.la_gate_norm_fwd(j, s["y0"], None, s["w_post"], s["alpha"], s["res"], s["w_pre"], s["h"], None, s["c1"], s["s1"])
+    la.la_linear_fwd(i, s["c1"], s["s1"], s["wi"][0], s["wi"][1], None, s["y1"])
+
+
+def layer_case(rows, H=4, hd=64, model=512, out=776):
+    g = gen(11)
+    d = H * hd
+
+    def weight(n, k):
+        w = draw(g, n, k, scale=k ** -0.5)
+        c, s = torch.empty(n, k, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda")
+        la.la_gate_norm_fwd(la.GateNormConfig(rows=n, d=k, post=0, qdq=la.LA_QDQ_INT8_GROUP), w, None, None, None, None, None, None, None, c, s)
+        return c, s
+
+    e = lambda *shape, dtype=BF: torch.zeros(shape, dtype=dtype, device="cuda")  # noqa: E731
+    s = dict(o=draw(g, rows, d), z=draw(g, rows, d), w_o=draw(g, hd, dtype=F32, scale=0.1) + 1, wo=weight(model, d), wi=weight(out, model),
+             w_post=draw(g, model, dtype=F32, scale=0.1) + 1, alpha=draw(g, model, dtype=F32, scale=0.1) + 0.5, res=draw(g, rows, model, scale=2.0),
+             w_pre=draw(g, model, dtype=F32, scale=0.1) + 1, c0=e(rows, d, dtype=torch.int8), s0=e(rows, dtype=F32), y0=e(rows, model),
+             h=e(rows, model), c1=e(rows, model, dtype=torch.int8), s1=e(rows, dtype=F32), y1=e(rows, out))
+    cfgs = (la.GateNormConfig(rows=rows, d=d, head=hd, gate=la.LA_GATE_SILU, qdq=la.LA_QDQ_INT8_GROUP),
+            la.LinearConfig(M=rows, N=model, K=d),
+            la.GateNormConfig(rows=rows, d=model, pre=1, qdq=la.LA_QDQ_INT8_GROUP),
+            la.LinearConfig(M=rows, N=out, K=model))
+    return s, cfgs
+
+
+@pytest.mark.parametrize("rows", [1, 5, 300])
+def test_layer_in_8_bits(rows):
+    """Against the same path in 64 bits with its own rounding to codes: 8-bit steps of independent errors, each
+    1/254 of a row's largest value at most, about 1% of a result's root mean square in each of two products."""
+    s, cfgs = layer_case(rows)
+    layer(s, cfgs)
+    v = {k: np64(t) for k, t in s.items() if torch.is_tensor(t)}
+    wo, wi = [np64(c) * np64(sc)[:, None] for c, sc in (s["wo"], s["wi"])]
+    n0 = R.gate_norm_fwd(v["o"], v["z"], v["w_o"], None, None, None, 64, 1e-6, 1, 0, 1, 0)[1]
+    t, n1, _ = R.gate_norm_fwd(n0 @ wo.T, None, v["w_post"], v["alpha"], v["res"], v["w_pre"], 0, 1e-6, 0, 0, 1, 1)
+    for got, want, bound in (("h", t, 0.01), ("y1", n1 @ wi.T, 0.03)):
+        e = np.linalg.norm(v[got] - want) / np.linalg.norm(want)
+        assert e <= bound, (got, e)
+    # the pieces, from the codes that the GPU has
+    close(s["y0"], R.linear_fwd(v["c0"], v["s0"], np64(s["wo"][0]), np64(s["wo"][1]), None), np.abs(v["y0"]), 2.0 ** -22, "y0")
+    close(s["y1"], R.linear_fwd(v["c1"], v["s1"], np64(s["wi"][0]), np64(s["wi"][1]), None), np.abs(v["y1"]), 2.0 ** -22, "y1")
+
+
+def test_layer_captured_and_on_another_stream():
+    s, cfgs = layer_case(37)
+    layer(s, cfgs)
+    outs = ("c0", "s0", "y0", "h", "c1", "s1", "y1")
+    want = {k: s[k].clone() for k in outs}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for k in outs:
+        s[k].zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer(s, cfgs)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(s[k], want[k]) for k in outs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer(s, cfgs)
+    for r in range(3):
+        for k in outs:
+            s[k].zero_()
+        s["o"].mul_(2.0 if r == 1 else 1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {k: s[k].clone() for k in outs}
+        layer(s, cfgs)
+        assert all(torch.equal(s[k], got[k]) for k in outs), r
+
+
+@pytest.mark.parametrize("t", [BF, F32])
+def test_training_step_captured(t):
+    """Forward and backward of both operators in one graph, replayed with new gradients among eager work."""
+    M, N, K = 333, 264, 512
+    g = gen(21)
+    xc, xs = codes(g, M, K)
+    wc, ws = codes(g, N, K)
+    cfg = la.LinearConfig(M=M, N=N, K=K, out_dtype=CODE[t], x_dtype=CODE[t])
+    gate = la.GateNormConfig(rows=M, d=N, gate=la.LA_GATE_SILU, pre=1, x_dtype=CODE[t], out_dtype=CODE[t])
+    z, res, dv, dh = (draw(g, M, N, dtype=t) for _ in range(4))
+    wp, al, w2 = (draw(g, N, dtype=F32, scale=0.1) + 1 for _ in range(3))
+    n1, n2 = la.la_linear_bwd_workspace_bytes(cfg), la.la_gate_norm_bwd_workspace_bytes(gate)
+    ws1, ws2 = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in (n1, n2))
+    e = lambda *shape, dtype=t: torch.zeros(shape, dtype=dtype, device="cuda")  # noqa: E731
+    out = dict(y=e(M, N), h=e(M, N), v=e(M, N), dy=e(M, N), dz=e(M, N), dres=e(M, N), dwp=e(N, dtype=F32), dal=e(N, dtype=F32), dw2=e(N, dtype=F32),
+               dx=e(M, K), dw=e(N, K, dtype=F32), db=e(N, dtype=F32))
+
+    def step():
+        la.la_linear_fwd(cfg, xc, xs, wc, ws, None, out["y"])
+        la.la_gate_norm_fwd(gate, out["y"], z, wp, al, res, w2, out["h"], out["v"])
+        la.la_gate_norm_bwd(gate, out["y"], z, wp, al, out["h"], w2, dv, dh, out["dy"], out["dz"], out["dres"], out["dwp"], out["dal"], out["dw2"], ws2, n2)
+        la.la_linear_bwd(cfg, xc, xs, wc, ws, out["dy"], out["dx"], out["dw"], out["db"], ws1, n1)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for r in range(4):
+        dv.copy_(draw(gen(30 + r), M, N, dtype=t, scale=10.0 ** -r))
+        step()
+        torch.cuda.synchronize()
+        want = {k: v.clone() for k, v in out.items()}
+        for v in out.values():
+            v.fill_(float("nan"))
+        ws1.fill_(0xFF), ws2.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[k], want[k]) for k in out), r
+    assert all(v.isfinite().all() for v in out.values())
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    M, N, K = 700, 520, 272
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    cfg = la.LinearConfig(M=M, N=N, K=K, x_dtype=la.LA_F32)
+    n = la.la_linear_bwd_workspace_bytes(cfg)
+    cases = []
+    for k in range(2):
+        xc, xs = codes(gen(40 + k), M, K)
+        wc, ws = codes(gen(50 + k), N, K)
+        dy = draw(gen(60 + k), M, N)
+        outs = [[torch.empty(s, device="cuda") for s in ((M, K), (N, K), (N,))] for _ in range(2)]
+        cases.append((xc, xs, wc, ws, dy, outs, torch.empty(n, dtype=torch.uint8, device="cuda")))
+        la.la_linear_bwd(cfg, xc, xs, wc, ws, dy, *outs[0], cases[-1][-1], n)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, (xc, xs, wc, ws, dy, outs, space) in zip(streams, cases):
+            la.la_linear_bwd(cfg, xc, xs, wc, ws, dy, *outs[1], space, n, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for c in cases for a, b in zip(*c[5]))
