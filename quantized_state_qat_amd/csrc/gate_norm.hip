@@ -10,6 +10,12 @@
 namespace la {
 namespace {
 
+// The gate as its formula is rounded, operation by operation.
+__device__ __forceinline__ float gate_stepwise(float z, int gate) {
+    const float s = 1.0f / (1.0f + expf(-z));
+    return gate == LA_GATE_SILU ? (z < -89.0f ? 0.0f : z * s) : s;
+}
+
 struct GateFwd {
     int rows, d, head, gate, first, post, pre, group, w_dtype, out_dtype;
     float eps;
@@ -149,7 +155,10 @@ __global__ __launch_bounds__(256) void gate_fwd_kernel(GateFwd p) {
 #pragma unroll
         for (int c = 0; c < CH; c++)
 #pragma unroll
-            for (int e = 0; e < 8; e++) g[c][e] = gate_of<G>(g[c][e], p.gate);
+            for (int e = 0; e < 8; e++) {
+                if constexpr (STEPWISE) g[c][e] = gate_stepwise(g[c][e], p.gate);
+                else g[c][e] = gate_of<G>(g[c][e], p.gate);
+            }
         if (p.first) {
 #pragma unroll
             for (int c = 0; c < CH; c++)
