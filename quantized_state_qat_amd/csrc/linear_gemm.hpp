@@ -81,8 +81,8 @@ __device__ __forceinline__ void load_eight(const float* p, float (&v)[8]) {
 constexpr int kStoreLds = 4096;
 
 // Results of a wave's TI x TJ tiles, the first one's at column i0 and row j0 of out.  A lane's results are
-// 16 or 32 bytes of 32 different rows of out; where the tile lies inside, they go through the wave's LDS
-// (kStoreLds bytes) and leave as lines of 128 bytes.
+// 16 or 32 bytes of 32 different rows of out: they go through the wave's LDS (kStoreLds bytes) and leave
+// as lines of 128 bytes, by 16 bytes a lane inside aligned rows, else by elements.
 template <class O, bool BITS, int TI, int TJ, class Acc>
 __device__ __forceinline__ void store_tiles(const GemmArgs& a, O* out, int i0, int j0, const Acc (&acc)[TI][TJ], char* lds) {
     const int lane = threadIdx.x & 63, r = lane & 31, q = lane >> 5;
@@ -128,34 +128,34 @@ __device__ __forceinline__ void store_tiles(const GemmArgs& a, O* out, int i0, i
                     if (a.col) v[e] *= cs[e];
                     if (a.bias) v[e] += bias[e];
                 }
-                if (whole) {
-                    constexpr int per = sizeof(O) / 2;  // pieces of 16 bytes
-                    const int piece = (2 * k + q) * per, x = r & (PIECES - 1);
-                    char* row = lds + r * LINE;
-                    if constexpr (sizeof(O) == 2) {
-                        *reinterpret_cast<uv4*>(row + 16 * (piece ^ x)) = narrow(v);
-                    } else {
-                        *reinterpret_cast<fv4*>(row + 16 * (piece ^ x)) = fv4{v[0], v[1], v[2], v[3]};
-                        *reinterpret_cast<fv4*>(row + 16 * ((piece + 1) ^ x)) = fv4{v[4], v[5], v[6], v[7]};
-                    }
+                constexpr int per = sizeof(O) / 2;  // pieces of 16 bytes
+                const int piece = (2 * k + q) * per, x = r & (PIECES - 1);
+                char* row = lds + r * LINE;
+                if constexpr (sizeof(O) == 2) {
+                    *reinterpret_cast<uv4*>(row + 16 * (piece ^ x)) = narrow(v);
                 } else {
-                    const int j = j0 + 32 * tj + r;
-                    O* o = out + static_cast<int64_t>(j) * a.ldo + i;
-#pragma unroll
-                    for (int e = 0; e < 8; e++)
-                        if (j < a.J && i + e < a.I) store_elem(o, e, sizeof(O) == 2 ? LA_BF16 : LA_F32, v[e]);
+                    *reinterpret_cast<fv4*>(row + 16 * (piece ^ x)) = fv4{v[0], v[1], v[2], v[3]};
+                    *reinterpret_cast<fv4*>(row + 16 * ((piece + 1) ^ x)) = fv4{v[4], v[5], v[6], v[7]};
                 }
             }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (one wave: its own writes, in order)
             if (whole) {
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (one wave: its own writes, in order)
 #pragma unroll
                 for (int n = 0; n < 32 / ROWS; n++) {
                     const int row = ROWS * n + lane / PIECES, piece = lane % PIECES, j = j0 + 32 * tj + row;
                     const uv4 v = *reinterpret_cast<const uv4*>(lds + row * LINE + 16 * (piece ^ (row & (PIECES - 1))));
                     if (j < a.J) store16(out + static_cast<int64_t>(j) * a.ldo + i0 + WIDE * pass + piece * (16 / sizeof(O)), v);
                 }
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            } else {
+#pragma unroll
+                for (int n = 0; n < WIDE / 2; n++) {
+                    const int row = (64 * n + lane) / WIDE, col = (64 * n + lane) % WIDE, j = j0 + 32 * tj + row, i = i0 + WIDE * pass + col;
+                    const int at = col * static_cast<int>(sizeof(O));
+                    const O v = *reinterpret_cast<const O*>(lds + row * LINE + 16 * ((at >> 4) ^ (row & (PIECES - 1))) + (at & 15));
+                    if (j < a.J && i < a.I) out[static_cast<int64_t>(j) * a.ldo + i] = v;
+                }
             }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
     }
 }
