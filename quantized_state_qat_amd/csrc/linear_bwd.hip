@@ -287,7 +287,8 @@ size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 struct Layout {
     size_t rowmax, colmax, part, qx, qw, pw, px, sums_x, sums_w, end;  // offsets; pw: w's codes, px: x's
     int parts_x, parts_w;  // of an operand
-    Cut dx, dw;            // the two products
+    Cut dx, dw;            // the two products,
+    bool pair;             // which may share a launch
 };
 Layout layout(const la_linear_config& c) {
     Layout l;
@@ -299,24 +300,24 @@ Layout layout(const la_linear_config& c) {
     l.qx = take(M * nc * 128 * l.parts_x), l.qw = take(N * mc * 128 * l.parts_w);
     l.pw = take(K * nc * 128), l.px = take(K * mc * 128);
     const auto most = [](size_t n) { return n <= (size_t{1} << 30) ? 16 : 1; };  // (the join's grid)
-    l.dx = cut_product(c.K, c.M, gemm_steps(nc * 128, l.parts_x - 1), most(M * K));
-    l.dw = cut_product(c.K, c.N, gemm_steps(mc * 128, l.parts_w - 1), most(N * K));
+    const int steps_x = gemm_steps(nc * 128, l.parts_x - 1), steps_w = gemm_steps(mc * 128, l.parts_w - 1);
+    l.dx = cut_product(c.K, c.M, steps_x, most(M * K));
+    l.dw = cut_product(c.K, c.N, steps_w, most(N * K));
+    l.pair = cut_pair(c.K, c.M, steps_x, l.dx, c.K, c.N, steps_w, l.dw);
     l.sums_x = take(l.dx.parts > 1 ? l.dx.parts * M * K * 4 : 0);
     l.sums_w = take(l.dw.parts > 1 ? l.dw.parts * N * K * 4 : 0);
     l.end = at;
     return l;
 }
 
-// One product; parts of its sum go to `sums`, and are left to `join`.
-hipError_t product(GemmArgs& g, const Cut& cut, int out_dtype, float* sums, Join& join, hipStream_t s) {
+// Cuts a product's sum into parts, which go to `sums` and are left to `join`.
+void cut(GemmArgs& g, const Cut& cut, float* sums, Join& join) {
     g.parts = cut.parts;
     g.part_steps = (gemm_steps(g.kbytes, g.shift) + cut.parts - 1) / cut.parts;
-    if (cut.parts > 1) {
-        const int64_t n = static_cast<int64_t>(g.I) * g.J;
-        join = {sums, cut.parts, g.I, out_dtype, n, static_cast<const uint32_t*>(g.row), g.out, static_cast<int>((n / 4 + 255) / 256)};
-        g.row = nullptr, g.out = sums, out_dtype = LA_F32;
-    }
-    return out_dtype == LA_BF16 ? launch_gemm<_Float16, uint16_t, true>(g, cut.tiling, s) : launch_gemm<_Float16, float, true>(g, cut.tiling, s);
+    if (cut.parts == 1) return;
+    const int64_t n = static_cast<int64_t>(g.I) * g.J;
+    join = {sums, cut.parts, g.I, g.out_dtype, n, static_cast<const uint32_t*>(g.row), g.out, static_cast<int>((n / 4 + 255) / 256)};
+    g.row = nullptr, g.out = sums, g.out_dtype = LA_F32;
 }
 
 }  // namespace
@@ -351,20 +352,28 @@ hipError_t launch_linear_bwd(const la_linear_config& c, const LinearArgs& a, hip
         else lay_dy_kernel<float><<<static_cast<unsigned>(lay), 256, 0, s>>>(d, static_cast<int>(bias));
     }
     if (hipError_t e = hipGetLastError()) return e;
+    const bool dx = a.dx && c.M > 0, dw = a.dw && c.N > 0;
+    GemmArgs gx, gw;
     Join jx{}, jw{};
-    if (a.dx && c.M > 0) {
-        GemmArgs g;
-        g.P = a.work + l.pw, g.ldP = nc * 128, g.I = c.K, g.kbytes = static_cast<int>(nc * 128);
-        g.Q = d.qx, g.ldQ = nc * 128 * d.px, g.J = c.M, g.shift = d.px - 1;
-        g.row = d.rowmax, g.out = a.dx, g.ldo = c.K, g.wide = 1;
-        if (hipError_t e = product(g, l.dx, c.x_dtype, reinterpret_cast<float*>(a.work + l.sums_x), jx, s)) return e;
+    if (dx) {
+        gx.P = a.work + l.pw, gx.ldP = nc * 128, gx.I = c.K, gx.kbytes = static_cast<int>(nc * 128);
+        gx.Q = d.qx, gx.ldQ = nc * 128 * d.px, gx.J = c.M, gx.shift = d.px - 1;
+        gx.row = d.rowmax, gx.out = a.dx, gx.out_dtype = c.x_dtype, gx.ldo = c.K, gx.wide = 1;
+        cut(gx, l.dx, reinterpret_cast<float*>(a.work + l.sums_x), jx);
     }
-    if (a.dw && c.N > 0) {
-        GemmArgs g;
-        g.P = a.work + l.px, g.ldP = mc * 128, g.I = c.K, g.kbytes = static_cast<int>(mc * 128);
-        g.Q = d.qw, g.ldQ = mc * 128 * d.pw, g.J = c.N, g.shift = d.pw - 1;
-        g.row = d.colmax, g.out = a.dw, g.ldo = c.K, g.wide = 1;
-        if (hipError_t e = product(g, l.dw, c.dw_dtype, reinterpret_cast<float*>(a.work + l.sums_w), jw, s)) return e;
+    if (dw) {
+        gw.P = a.work + l.px, gw.ldP = mc * 128, gw.I = c.K, gw.kbytes = static_cast<int>(mc * 128);
+        gw.Q = d.qw, gw.ldQ = mc * 128 * d.pw, gw.J = c.N, gw.shift = d.pw - 1;
+        gw.row = d.colmax, gw.out = a.dw, gw.out_dtype = c.dw_dtype, gw.ldo = c.K, gw.wide = 1;
+        cut(gw, l.dw, reinterpret_cast<float*>(a.work + l.sums_w), jw);
+    }
+    if (dx && dw && l.pair) {
+        if (hipError_t e = launch_pair<_Float16, true>(gx, gw, l.dx.tiling, s)) return e;
+    } else {
+        if (dx)
+            if (hipError_t e = launch_gemm<_Float16, true>(gx, l.dx.tiling, s)) return e;
+        if (dw)
+            if (hipError_t e = launch_gemm<_Float16, true>(gw, l.dw.tiling, s)) return e;
     }
     if (jx.blocks + jw.blocks > 0) join_kernel<<<static_cast<unsigned>(jx.blocks + jw.blocks), 256, 0, s>>>(jx, jw);
     return hipGetLastError();

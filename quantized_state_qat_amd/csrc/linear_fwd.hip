@@ -77,7 +77,7 @@ hipError_t launch(const la_linear_config& c, GemmArgs& g, hipStream_t s) {
         return hipGetLastError();
     }
     g.part_steps = gemm_steps(g.kbytes, 0);
-    return launch_gemm<int8_t, O, false>(g, cut_product(c.N, c.M, g.part_steps, 1).tiling, s);
+    return launch_gemm<int8_t, false>(g, cut_product(c.N, c.M, g.part_steps, 1).tiling, s);
 }
 
 }  // namespace
@@ -88,7 +88,7 @@ hipError_t launch_linear_fwd(const la_linear_config& c, const LinearArgs& a, hip
     g.ldP = c.K, g.ldQ = c.ld_x ? c.ld_x : c.K;
     g.I = c.N, g.J = c.M, g.kbytes = c.K;
     g.row = a.xs, g.col = a.ws, g.bias = a.bias, g.bias_dtype = c.w_dtype;
-    g.out = a.y, g.ldo = c.ld_y ? c.ld_y : c.N;
+    g.out = a.y, g.out_dtype = c.out_dtype, g.ldo = c.ld_y ? c.ld_y : c.N;
     g.wide = g.ldo * (c.out_dtype == LA_BF16 ? 2 : 4) % 16 == 0;
     return c.out_dtype == LA_BF16 ? launch<uint16_t>(c, g, s) : launch<float>(c, g, s);
 }

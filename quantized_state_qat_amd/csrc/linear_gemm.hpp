@@ -34,6 +34,7 @@ struct GemmArgs {
     const void* bias = nullptr;  // [I] or null
     int bias_dtype = 0;
     void* out = nullptr;
+    int out_dtype = LA_F32;
     int64_t ldo = 0;  // elements
     int wide = 0;     // rows of out are 16-byte aligned
 };
@@ -83,7 +84,7 @@ constexpr int kStoreLds = 4096;
 // Results of a wave's TI x TJ tiles, the first one's at column i0 and row j0 of out.  A lane's results are
 // 16 or 32 bytes of 32 different rows of out: they go through the wave's LDS (kStoreLds bytes) and leave
 // as lines of 128 bytes, by 16 bytes a lane inside aligned rows, else by elements.
-template <class O, bool BITS, int TI, int TJ, class Acc>
+template <bool BITS, int TI, int TJ, class O, class Acc>
 __device__ __forceinline__ void store_tiles(const GemmArgs& a, O* out, int i0, int j0, const Acc (&acc)[TI][TJ], char* lds) {
     const int lane = threadIdx.x & 63, r = lane & 31, q = lane >> 5;
     constexpr int WIDE = TI * 32 * sizeof(O) < 128 ? TI * 32 : 128 / sizeof(O);  // columns of a pass
@@ -195,13 +196,15 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, char* lds,
 // once a step's last slice is in registers one barrier frees its LDS for the loads of the step NS further.
 // The order of reads, loads and products is spelled out (the compiler bunches the reads).  A workgroup
 // takes tiles of out in turn, and the loads run on into the next one, under the stores of the one before.
-template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int NS, int MINW>
-__global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs a, int across, int down) {
+// Of `blocks` workgroups on product a this is number `block`.  O: out's type, or void (a.out_dtype).
+template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int NS>
+__device__ __forceinline__ void gemm_units(const GemmArgs& a, int block, int blocks) {
     constexpr int NW = WI * WJ, BI = 32 * TI * WI, BJ = 32 * TJ * WJ, STAGE = (BI + BJ) * 128;
     constexpr int LI = BI / (8 * NW), LJ = BJ / (8 * NW);  // loads a wave and step: 8 rows each
     static_assert(BI % (8 * NW) == 0 && BJ % (8 * NW) == 0 && NW % 2 == 0 && (NS & (NS - 1)) == 0);
     __shared__ __align__(128) char lds[NS * STAGE + NW * kStoreLds];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 31, q = lane >> 5;
+    const int across = (a.I + BI - 1) / BI, down = (a.J + BJ - 1) / BJ;
     const int tiles = across * down, units = tiles * a.parts, steps = a.part_steps;
     const int lrow = 8 * wave + (lane >> 3);  // and every 8 NW rows further: the swizzle is the same
     const int piece = 16 * ((lane & 7) ^ swizzle(lrow));
@@ -212,7 +215,7 @@ __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs 
     for (int k = 0; k < LJ; k++) qo[k] = (lrow + 8 * NW * k) * static_cast<uint32_t>(a.ldQ) + piece;
     // where the loads are: step `at_k` of unit `at`, a part of a tile (none left: at >= units), whose first
     // step in the whole sum is k0, and its operands' buffers
-    int at = blockIdx.x, at_k = 0, k0 = 0;
+    int at = block, at_k = 0, k0 = 0;
     __amdgpu_buffer_rsrc_t P, Q;
     auto aim = [&] {
         const int unit = xcd_tile(at < units ? at : 0, units);
@@ -226,7 +229,7 @@ __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs 
     auto advance = [&] {
         if (++at_k >= steps) {
             at_k = 0;
-            at += gridDim.x;
+            at += blocks;
             aim();
         }
     };
@@ -292,7 +295,7 @@ __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs 
     fetch(0, 0);
     int stage = 0;
     int landed = 0;  // steps to come whose loads are known to have landed
-    for (int id = blockIdx.x; id < units; id += gridDim.x) {
+    for (int id = block; id < units; id += blocks) {
 #pragma unroll
         for (int k = 0; k < TI * TJ; k++) acc[k / TJ][k % TJ] = {};
         for (int t = 0; t < steps; t++) {
@@ -318,32 +321,61 @@ __global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs 
         }
         const int unit = xcd_tile(id, units);
         const TileAt t = tile_order(unit % tiles, across, down);
-        O* out = static_cast<O*>(a.out) + unit / tiles * static_cast<int64_t>(a.J) * a.ldo;
-        store_tiles<O, BITS, TI, TJ>(a, out, t.i * BI + wi, t.j * BJ + wj, acc, lds + NS * STAGE + wave * kStoreLds);
+        const int64_t part = unit / tiles * static_cast<int64_t>(a.J) * a.ldo;
+        char* const store = lds + NS * STAGE + wave * kStoreLds;
+        const int i0 = t.i * BI + wi, j0 = t.j * BJ + wj;
+        if constexpr (!std::is_void_v<O>) store_tiles<BITS, TI, TJ>(a, static_cast<O*>(a.out) + part, i0, j0, acc, store);
+        else if (a.out_dtype == LA_BF16) store_tiles<BITS, TI, TJ>(a, static_cast<uint16_t*>(a.out) + part, i0, j0, acc, store);
+        else store_tiles<BITS, TI, TJ>(a, static_cast<float*>(a.out) + part, i0, j0, acc, store);
         landed = steps < NS - 1 ? steps : NS - 1;
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");  // no load may reach LDS after the workgroup
 }
 
-// PER: workgroups that a CU holds.
-template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int NS, int MINW, int PER>
-void launch_tiles(const GemmArgs& a, hipStream_t s) {
-    constexpr int BI = 32 * TI * WI, BJ = 32 * TJ * WJ;
-    const int across = (a.I + BI - 1) / BI, down = (a.J + BJ - 1) / BJ;
-    const int units = across * down * a.parts, most = 256 * PER;
-    gemm_tile_kernel<E, O, BITS, WI, WJ, TI, TJ, NS, MINW>
-        <<<static_cast<unsigned>(units < most ? units : most), 64 * WI * WJ, 0, s>>>(a, across, down);
+template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int NS, int MINW>
+__global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_tile_kernel(GemmArgs a) {
+    gemm_units<E, O, BITS, WI, WJ, TI, TJ, NS>(a, blockIdx.x, gridDim.x);
+}
+// Two products side by side, the first one's workgroups before the second's.
+template <class E, bool BITS, int WI, int WJ, int TI, int TJ, int NS, int MINW>
+__global__ __launch_bounds__(64 * WI * WJ, MINW) void gemm_pair_kernel(GemmArgs a, GemmArgs b, int first) {
+    const bool one = static_cast<int>(blockIdx.x) < first;
+    const GemmArgs c = one ? a : b;
+    gemm_units<E, void, BITS, WI, WJ, TI, TJ, NS>(c, one ? blockIdx.x : blockIdx.x - first, one ? first : gridDim.x - first);
 }
 
-// The tiles that a product is cut into (of 64 x 64 with two or four steps in LDS).
+// The tiles that a product is cut into (of 64 x 64 with two or four steps in LDS), their size, and the workgroups
+// that a CU holds.
 enum Tiling { kTiles256, kTiles128, kTiles64, kTiles64Deep };
+constexpr int kTileSize[] = {256, 128, 64, 64}, kTilesPerCu[] = {1, 2, 3, 2};
+inline int64_t gemm_units_of(Tiling t, int64_t I, int64_t J, int parts) {
+    const int n = kTileSize[t];
+    return (I + n - 1) / n * ((J + n - 1) / n) * parts;
+}
 
-template <class E, class O, bool BITS>
+template <class E, bool BITS, int WI, int WJ, int TI, int TJ, int NS, int MINW>
+void launch_tiles(const GemmArgs& a, Tiling t, hipStream_t s) {
+    const int64_t units = gemm_units_of(t, a.I, a.J, a.parts), most = 256 * kTilesPerCu[t];
+    const unsigned grid = static_cast<unsigned>(units < most ? units : most);
+    if (a.out_dtype == LA_BF16) gemm_tile_kernel<E, uint16_t, BITS, WI, WJ, TI, TJ, NS, MINW><<<grid, 64 * WI * WJ, 0, s>>>(a);
+    else gemm_tile_kernel<E, float, BITS, WI, WJ, TI, TJ, NS, MINW><<<grid, 64 * WI * WJ, 0, s>>>(a);
+}
+template <class E, bool BITS>
 hipError_t launch_gemm(const GemmArgs& a, Tiling t, hipStream_t s) {
-    if (t == kTiles256) launch_tiles<E, O, BITS, 2, 4, 4, 2, 2, 2, 1>(a, s);
-    else if (t == kTiles128) launch_tiles<E, O, BITS, 2, 2, 2, 2, 2, 2, 2>(a, s);
-    else if (t == kTiles64) launch_tiles<E, O, BITS, 2, 2, 1, 1, 2, 4, 3>(a, s);
-    else launch_tiles<E, O, BITS, 2, 2, 1, 1, 4, 2, 2>(a, s);
+    if (t == kTiles256) launch_tiles<E, BITS, 2, 4, 4, 2, 2, 2>(a, t, s);
+    else if (t == kTiles128) launch_tiles<E, BITS, 2, 2, 2, 2, 2, 2>(a, t, s);
+    else if (t == kTiles64) launch_tiles<E, BITS, 2, 2, 1, 1, 2, 4>(a, t, s);
+    else launch_tiles<E, BITS, 2, 2, 1, 1, 4, 2>(a, t, s);
+    return hipGetLastError();
+}
+// Two products in one launch, a workgroup a unit.
+template <class E, bool BITS>
+hipError_t launch_pair(const GemmArgs& a, const GemmArgs& b, Tiling t, hipStream_t s) {
+    const int first = static_cast<int>(gemm_units_of(t, a.I, a.J, a.parts));
+    const unsigned grid = static_cast<unsigned>(first + gemm_units_of(t, b.I, b.J, b.parts));
+    if (t == kTiles128) gemm_pair_kernel<E, BITS, 2, 2, 2, 2, 2, 2><<<grid, 256, 0, s>>>(a, b, first);
+    else if (t == kTiles64) gemm_pair_kernel<E, BITS, 2, 2, 1, 1, 2, 4><<<grid, 256, 0, s>>>(a, b, first);
+    else gemm_pair_kernel<E, BITS, 2, 2, 1, 1, 4, 2><<<grid, 256, 0, s>>>(a, b, first);
     return hipGetLastError();
 }
 
@@ -358,23 +390,38 @@ inline int gemm_steps(int64_t kbytes, int shift) { return static_cast<int>((kbyt
 struct Cut {
     Tiling tiling;
     int parts;
+    float us;
 };
+inline float tiles_us(Tiling t, int64_t units, int steps) {
+    constexpr struct { float fixed, few, full; } kinds[] = {{7.0f, 1.1f, 1.75f}, {5.0f, 0.42f, 1.2f}, {3.5f, 0.27f, 0.65f}, {3.5f, 0.25f, 0.47f}};
+    const int64_t slots = 256 * kTilesPerCu[t];
+    const float rest = static_cast<float>(units % slots) / slots;
+    return kinds[t].fixed + steps * (static_cast<float>(units / slots) * kinds[t].full + (rest > 0.0f ? kinds[t].few + rest * (kinds[t].full - kinds[t].few) : 0.0f));
+}
 inline Cut cut_product(int64_t I, int64_t J, int steps, int most_parts) {
-    constexpr struct { int size, per; float fixed, few, full; } kinds[] = {
-        {256, 1, 7.0f, 1.1f, 1.75f}, {128, 2, 5.0f, 0.42f, 1.2f}, {64, 3, 3.5f, 0.27f, 0.65f}, {64, 2, 3.5f, 0.25f, 0.47f}};
-    Cut best{kTiles256, 1};
-    float least = 0.0f;
+    Cut best{kTiles256, 1, tiles_us(kTiles256, gemm_units_of(kTiles256, I, J, 1), steps)};
     for (int k = 0; k < 4; k++) {
+        const Tiling t = static_cast<Tiling>(k);
         for (int parts = 1; parts <= most_parts && (parts == 1 || steps / parts >= 4); parts *= 2) {
-            const auto& t = kinds[k];
-            const int64_t units = (I + t.size - 1) / t.size * ((J + t.size - 1) / t.size) * parts, slots = 256 * t.per;
-            const float each = static_cast<float>((steps + parts - 1) / parts), rest = static_cast<float>(units % slots) / slots;
-            float us = t.fixed + each * (static_cast<float>(units / slots) * t.full + (rest > 0.0f ? t.few + rest * (t.full - t.few) : 0.0f));
+            float us = tiles_us(t, gemm_units_of(t, I, J, parts), (steps + parts - 1) / parts);
             if (parts > 1) us += 4.0f + static_cast<float>(parts) * I * J * 8e-6f / 4.0f;
-            if ((k == 0 && parts == 1) || us < least) best = {static_cast<Tiling>(k), parts}, least = us;
+            if (us < best.us) best = {t, parts, us};
         }
     }
     return best;
+}
+// Two products in whole sums whose workgroups the chip holds at once, if one launch of them beats the two cuts:
+// both get its tiling.
+inline bool cut_pair(int64_t I0, int64_t J0, int steps0, Cut& c0, int64_t I1, int64_t J1, int steps1, Cut& c1) {
+    bool pair = false;
+    float least = c0.us + c1.us;
+    for (const Tiling t : {kTiles128, kTiles64, kTiles64Deep}) {
+        const int64_t units = gemm_units_of(t, I0, J0, 1) + gemm_units_of(t, I1, J1, 1);
+        if (units > 256 * kTilesPerCu[t]) continue;
+        const float us = tiles_us(t, units, steps0 > steps1 ? steps0 : steps1);
+        if (us < least) least = us, c0 = c1 = {t, 1, us}, pair = true;
+    }
+    return pair;
 }
 
 }  // namespace la
