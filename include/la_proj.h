@@ -56,10 +56,11 @@ la_status la_linear_fwd(const la_linear_config* cfg, const void* x_codes, const 
  * each may be NULL.  dy times the scales enters a gradient held in bf16 rounded to FP16's 11 bits (off
  * by at most 2^-11 of the value, an eighth of bf16's own rounding), one held in FP32 as two such parts
  * (2^-22), both under a power of two for its row (for dweight its column): values 2^-29 of the row's
- * largest magnitude or smaller lose more.
- * The codes enter exactly.  Sums are FP32, joined in a fixed order; dbias is summed in double over
- * FP32 sums of 64 rows.  M and N up to 2^19, with below 2^23 tiles of 64 x 64.  Workspace: at least la_linear_bwd_workspace_bytes(cfg) bytes
- * (operands laid out for the products); 0 where there is nothing to sum or the call would be refused. */
+ * largest magnitude or smaller lose more.  dy times a scale is formed in FP32, and must not overflow it.
+ * The codes enter exactly.  Sums are FP32, those of a sum's parts joined in double in a fixed order; dbias is
+ * summed in double over FP32 sums of 64 rows.  M and N up to 2^19, with below 2^23 tiles of 64 x 64.
+ * Workspace: at least la_linear_bwd_workspace_bytes(cfg) bytes (operands laid out for the products); a query
+ * returns 0 where there is nothing to sum and where the call would be refused. */
 la_status la_linear_bwd(const la_linear_config* cfg, const void* x_codes, const float* x_scales, const void* w_codes,
                         const float* w_scales, const void* dy, void* dx, void* dweight, float* dbias, void* workspace,
                         size_t ws_bytes, void* stream);
@@ -85,7 +86,8 @@ typedef enum { LA_GATE_NONE = 0, LA_GATE_SILU = 1, LA_GATE_SIGMOID = 2 } la_out_
  * codes that stand for NaN are as in la_norm_fwd.
  */
 typedef struct la_gate_norm_config {
-    int32_t rows, d;    /* (rows + 31) min(256, max(8, d / 4)) below 2^32; d a multiple of 8 up to 16384 */
+    int32_t rows, d;    /* d a multiple of 8 up to 16384; (rows + 31) L below 2^32, with L = 8, 16, 32 or 64 the
+                         * first that 8 L >= d holds for, 256 from d = 520 on */
     int32_t head;       /* columns of one norm after the block: 0 (the row), 16, 32, 64, 128, 256 or 512, dividing d */
     float eps;          /* >= 0 */
     int32_t gate;       /* la_out_gate */

@@ -127,6 +127,22 @@ def test_gate_norm_refuses_configs(kw, status, word):
     assert la.la_gate_norm_bwd_workspace_bytes(gate(**kw)) == 0
 
 
+@pytest.mark.parametrize("d,lanes", [(64, 8), (72, 16), (256, 32), (512, 64), (520, 256), (2048, 256), (16384, 256)])
+def test_gate_norm_refuses_grids_of_two_to_the_32(d, lanes):
+    """A row has that many threads, and a grid whole workgroups of 256."""
+    most = min((1 << 32) // lanes - 32, (1 << 31) - 1)
+    assert la.la_gate_norm_bwd_workspace_bytes(gate(rows=most, d=d)) > 0 and -(-most * lanes // 256) * 256 < 1 << 32
+    if most < (1 << 31) - 1:
+        refused(lambda: gate_fwd(gate(rows=most + 1, d=d)), la.LA_ERR_UNSUPPORTED, "too many rows")
+
+
+def test_linear_backward_refuses_grids():
+    cfg = linear(M=1 << 19, N=1 << 16)
+    assert la.la_linear_bwd_workspace_bytes(cfg) == 0
+    refused(lambda: linear_bwd(cfg, FAKE, 1 << 60), la.LA_ERR_UNSUPPORTED, "2^23")
+    assert la.la_linear_bwd_workspace_bytes(linear(M=1 << 19, N=(1 << 16) - 64, K=65536)) > 0
+
+
 def test_gate_norm_refuses_pointers():
     for p in FWD:
         refused(lambda: gate_fwd(gate(qdq=1), **{p: FAKE + 8}), la.LA_ERR_ALIGNMENT, "aligned")
