@@ -65,14 +65,15 @@ enum GateAt { kNoGate, kGateLast, kGateFirst };
 
 // Waves a SIMD that a kernel's registers leave room for, and workgroups a CU by them: all that a launch has are
 // resident.  32768 x 2048 bf16, forward and backward: three 291 us (row norms) and 228 (head norms and
-// gate), two 318 and 243, four, which spill, 426 and 296.
-constexpr int waves_for(int lanes) { return lanes <= 256 ? 3 : lanes == 512 ? 2 : 4; }
-constexpr int groups_for(int lanes) { return lanes <= 256 ? waves_for(lanes) : 1; }
+// gate), two 318 and 243, four, which spill, 426 and 296; gate and both norms: two 332 us, three, which
+// spill, 452.
+constexpr int waves_for(int lanes, bool full) { return lanes <= 256 ? (full ? 2 : 3) : lanes == 512 ? 2 : 4; }  // full: gate and both norms
+constexpr int groups_for(int lanes, bool full) { return lanes <= 256 ? waves_for(lanes, full) : 1; }
 
 // The loads of a workgroup's next row run under the sums of the one before: a row is five loads wide and
 // two barriers long.
 template <class T, int LANES, int CH, GateAt GATE, bool PRE>
-__global__ __launch_bounds__(LANES < 256 ? 256 : LANES, waves_for(LANES)) void gate_bwd_kernel(GateBwd p) {
+__global__ __launch_bounds__(LANES < 256 ? 256 : LANES, waves_for(LANES, GATE != kNoGate && PRE)) void gate_bwd_kernel(GateBwd p) {
     constexpr int THREADS = LANES < 256 ? 256 : LANES, RPW = THREADS / LANES, WAVES = THREADS / 64, CODE = Io<T>::kCode;
     constexpr bool AHEAD = CH == 1;  // (registers: two pieces a lane leave no room for a second row and the weights)
     __shared__ float lds[2][3][WAVES];
@@ -318,7 +319,7 @@ int bwd_groups(const la_gate_norm_config& c) {
     const int pieces = c.d / kPiece;
     const int lanes = pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : pieces <= 64 ? 64 : pieces <= 256 ? 256 : pieces <= 1024 ? 512 : 1024;
     const int rpw = lanes < 256 ? 256 / lanes : 1;
-    const int need = (c.rows + rpw - 1) / rpw, most = 256 * groups_for(lanes);
+    const int need = (c.rows + rpw - 1) / rpw, most = 256 * groups_for(lanes, c.gate != LA_GATE_NONE && c.pre);
     return need < most ? need : most;
 }
 
