@@ -86,8 +86,8 @@ typedef enum { LA_GATE_NONE = 0, LA_GATE_SILU = 1, LA_GATE_SIGMOID = 2 } la_out_
  * codes that stand for NaN are as in la_norm_fwd.
  */
 typedef struct la_gate_norm_config {
-    int32_t rows, d;    /* d a multiple of 8 up to 16384; (rows + 31) L below 2^32, with L = 8, 16, 32 or 64 the
-                         * first that 8 L >= d holds for, 256 from d = 520 on */
+    int32_t rows, d;    /* d a multiple of 8 up to 16384; (rows + 31) L below 2^32, with L the lanes of a row: 8, 16,
+                         * 32, 64, 128, 192, 256 or 384, the first that 8 L >= d holds for, 256 for longer rows */
     int32_t head;       /* columns of one norm after the block: 0 (the row), 16, 32, 64, 128, 256 or 512, dividing d */
     float eps;          /* >= 0 */
     int32_t gate;       /* la_out_gate */

@@ -67,14 +67,14 @@ enum GateAt { kNoGate, kGateLast, kGateFirst };
 // resident.  32768 x 2048 bf16, forward and backward: three 291 us (row norms) and 228 (head norms and
 // gate), two 318 and 243, four, which spill, 426 and 296; gate and both norms: two 332 us, three, which
 // spill, 452.
-constexpr int waves_for(int lanes, bool full) { return lanes <= 256 ? (full ? 2 : 3) : lanes == 512 ? 2 : 4; }  // full: gate and both norms
-constexpr int groups_for(int lanes, bool full) { return lanes <= 256 ? waves_for(lanes, full) : 1; }
+constexpr int waves_for(int lanes, bool full) { return lanes <= 384 ? (full ? 2 : 3) : lanes == 512 ? 2 : 4; }  // full: gate and both norms
+constexpr int groups_for(int lanes, bool full) { return lanes <= 64 ? waves_for(lanes, full) : 4 * waves_for(lanes, full) / (lanes / 64); }
 
 // The loads of a workgroup's next row run under the sums of the one before: a row is five loads wide and
 // two barriers long.
 template <class T, int LANES, int CH, GateAt GATE, bool PRE>
-__global__ __launch_bounds__(LANES < 256 ? 256 : LANES, waves_for(LANES, GATE != kNoGate && PRE)) void gate_bwd_kernel(GateBwd p) {
-    constexpr int THREADS = LANES < 256 ? 256 : LANES, RPW = THREADS / LANES, WAVES = THREADS / 64, CODE = Io<T>::kCode;
+__global__ __launch_bounds__(LANES <= 64 ? 256 : LANES, waves_for(LANES, GATE != kNoGate && PRE)) void gate_bwd_kernel(GateBwd p) {
+    constexpr int THREADS = LANES <= 64 ? 256 : LANES, RPW = THREADS / LANES, WAVES = THREADS / 64, CODE = Io<T>::kCode;
     constexpr bool AHEAD = CH == 1;  // (registers: two pieces a lane leave no room for a second row and the weights)
     __shared__ float lds[2][3][WAVES];
     __shared__ float red[THREADS * 8 * CH];
@@ -84,21 +84,32 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, waves_for(LANES, GATE !=
     const int head_lanes = p.head / kPiece;
     const bool whole = p.post && p.head == 0;
     int par = 0;
-    float w_post[CH][8], alpha[CH][8], w_pre[CH][8];
-    auto weights = [&] {
+    // the weights of a piece: kept where registers allow it, else read again
+    enum { kPost, kAlpha, kPre };
+    float kept[3][AHEAD ? CH : 1][8];
+    auto read_weight = [&](int which, int c, float (&w)[8]) {
+        const int col = (c * LANES + l) * kPiece;
+        const void* from = which == kPost ? p.w_post : which == kAlpha ? p.alpha : p.w_pre;
 #pragma unroll
-        for (int c = 0; c < CH; c++) {
-            const int col = (c * LANES + l) * kPiece;
+        for (int e = 0; e < 8; e++) w[e] = 1.0f;
+        if (from && col < p.d) load_w(from, p.w_dtype, which == kPost && p.head ? col & (p.head - 1) : col, w);
+    };
+    auto weight = [&](int which, int c, float (&w)[8]) {
+        if constexpr (AHEAD) {
 #pragma unroll
-            for (int e = 0; e < 8; e++) w_post[c][e] = alpha[c][e] = w_pre[c][e] = 1.0f;
-            if (col < p.d) {
-                if (p.w_post) load_w(p.w_post, p.w_dtype, p.head ? col & (p.head - 1) : col, w_post[c]);
-                if (p.alpha) load_w(p.alpha, p.w_dtype, col, alpha[c]);
-                if (PRE && p.w_pre) load_w(p.w_pre, p.w_dtype, col, w_pre[c]);
-            }
+            for (int e = 0; e < 8; e++) w[e] = kept[which][c][e];
+        } else {
+            read_weight(which, c, w);
         }
     };
-    if constexpr (AHEAD) weights();
+    if constexpr (AHEAD) {
+#pragma unroll
+        for (int c = 0; c < CH; c++) {
+            read_weight(kPost, c, kept[kPost][c]);
+            read_weight(kAlpha, c, kept[kAlpha][c]);
+            if constexpr (PRE) read_weight(kPre, c, kept[kPre][c]);
+        }
+    }
     struct Row {
         Raw x, z, h, dy, dh;
     } next[CH];
@@ -122,11 +133,8 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, waves_for(LANES, GATE !=
     if constexpr (AHEAD) fetch(row);
     for (; row < p.rows; row += stride) {
         const size_t base = static_cast<size_t>(row) * p.d;
-        if constexpr (!AHEAD) {
-            fetch(row);
-            weights();
-        }
-        float x[CH][8], z[CH][8], h[CH][8], dy[CH][8], up[CH][8], gate[CH][8], slope[CH][8];
+        if constexpr (!AHEAD) fetch(row);
+        float x[CH][8], z[CH][8], h[CH][8], dy[CH][8], up[CH][8], gates[2][AHEAD ? CH : 1][8];
 #pragma unroll
         for (int c = 0; c < CH; c++) {
             widen_raw(next[c].x, CODE, x[c]);
@@ -136,18 +144,27 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, waves_for(LANES, GATE !=
             widen_raw(next[c].dh, CODE, up[c]);
         }
         if constexpr (AHEAD) fetch(row + stride);
+        // the gate and its slope: kept, or formed again, as the weights
+        [[maybe_unused]] auto gate_at = [&](int c, int e, float& gate, float& slope) {
+            if constexpr (AHEAD) gate = gates[0][c][e], slope = gates[1][c][e];
+            else gate_both<T>(z[c][e], p.gate, gate, slope);
+        };
         float hh = 0.0f, gh = 0.0f, uu = 0.0f, us[CH];
 #pragma unroll
         for (int c = 0; c < CH; c++) {
             us[c] = 0.0f;
+            float w_pre[8];
+            if constexpr (PRE) weight(kPre, c, w_pre);
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                if constexpr (GATE != kNoGate) gate_both<T>(z[c][e], p.gate, gate[c][e], slope[c][e]);
-                const float u = GATE == kGateFirst ? x[c][e] * gate[c][e] : x[c][e];
+                [[maybe_unused]] float gate, slope;
+                if constexpr (GATE != kNoGate && (AHEAD || GATE == kGateFirst)) gate_both<T>(z[c][e], p.gate, gate, slope);
+                if constexpr (GATE != kNoGate && AHEAD) gates[0][c][e] = gate, gates[1][c][e] = slope;
+                const float u = GATE == kGateFirst ? x[c][e] * gate : x[c][e];
                 us[c] = __builtin_fmaf(u, u, us[c]);
                 if constexpr (PRE) {
                     hh = __builtin_fmaf(h[c][e], h[c][e], hh);
-                    gh = __builtin_fmaf(dy[c][e] * w_pre[c][e], h[c][e], gh);
+                    gh = __builtin_fmaf(dy[c][e] * w_pre[e], h[c][e], gh);
                 }
             }
             uu += us[c];
@@ -181,28 +198,33 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, waves_for(LANES, GATE !=
         for (int c = 0; c < CH; c++) {
             const int col = (c * LANES + l) * kPiece;
             r1[c] = !p.post ? 1.0f : rsqrt_fine((whole ? uu : sum_lanes(us[c], head_lanes)) * inv_n + p.eps);
-            float dz[8];
+            float dz[8], w_post[8], alpha[8], w_pre[8];
+            weight(kPost, c, w_post);
+            weight(kAlpha, c, alpha);
+            if constexpr (PRE) weight(kPre, c, w_pre);
             part[c] = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; e++) {
                 float t = up[c][e];
                 if constexpr (PRE) {
-                    t = __builtin_fmaf(r2, __builtin_fmaf(dy[c][e], w_pre[c][e], -h[c][e] * k2), t);
+                    t = __builtin_fmaf(r2, __builtin_fmaf(dy[c][e], w_pre[e], -h[c][e] * k2), t);
                     sum[2][c][e] = __builtin_fmaf(dy[c][e], h[c][e] * r2, sum[2][c][e]);
                 } else {
                     t += dy[c][e];
                 }
                 up[c][e] = t;
-                const float u = GATE == kGateFirst ? x[c][e] * gate[c][e] : x[c][e];
-                const float ur = u * r1[c], n = ur * w_post[c][e];
-                sum[1][c][e] = __builtin_fmaf(t, GATE == kGateLast ? n * gate[c][e] : n, sum[1][c][e]);
-                float g = t * alpha[c][e];
+                [[maybe_unused]] float gate, slope;
+                if constexpr (GATE != kNoGate) gate_at(c, e, gate, slope);
+                const float u = GATE == kGateFirst ? x[c][e] * gate : x[c][e];
+                const float ur = u * r1[c], n = ur * w_post[e];
+                sum[1][c][e] = __builtin_fmaf(t, GATE == kGateLast ? n * gate : n, sum[1][c][e]);
+                float g = t * alpha[e];
                 if constexpr (GATE == kGateLast) {
-                    dz[e] = g * n * slope[c][e];
-                    g *= gate[c][e];
+                    dz[e] = g * n * slope;
+                    g *= gate;
                 }
                 sum[0][c][e] = __builtin_fmaf(g, ur, sum[0][c][e]);
-                dy[c][e] = g * w_post[c][e];
+                dy[c][e] = g * w_post[e];
                 part[c] = __builtin_fmaf(dy[c][e], u, part[c]);
             }
             if (col < p.d) {
@@ -231,11 +253,13 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, waves_for(LANES, GATE !=
             float dz[8];
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                const float u = GATE == kGateFirst ? x[c][e] * gate[c][e] : x[c][e];
+                [[maybe_unused]] float gate, slope;
+                if constexpr (GATE == kGateFirst) gate_at(c, e, gate, slope);
+                const float u = GATE == kGateFirst ? x[c][e] * gate : x[c][e];
                 float g = r1[c] * __builtin_fmaf(-u, k1, dy[c][e]);
                 if constexpr (GATE == kGateFirst) {
-                    dz[e] = g * x[c][e] * slope[c][e];
-                    g *= gate[c][e];
+                    dz[e] = g * x[c][e] * slope;
+                    g *= gate;
                 }
                 dy[c][e] = g;
             }
@@ -288,18 +312,27 @@ __global__ __launch_bounds__(LANES < 256 ? 256 : LANES, waves_for(LANES, GATE !=
 }
 
 // The backward holds five rows: one piece a lane up to 4096 columns.
+int bwd_lanes(int d) {
+    const int pieces = d / kPiece;
+    return pieces <= 256 ? gate_lanes(d) : pieces <= 384 ? 384 : pieces <= 1024 ? 512 : 1024;
+}
 template <class F>
 hipError_t by_width_bwd(int d, F&& f) {
     using std::integral_constant;
-    const int pieces = d / kPiece;
-    if (pieces <= 8) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-    if (pieces <= 16) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-    if (pieces <= 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-    if (pieces <= 64) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    if (pieces <= 256) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-    if (pieces <= 512) return f(integral_constant<int, 512>{}, integral_constant<int, 1>{});
-    if (pieces <= 1024) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-    return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    constexpr integral_constant<int, 1> one;
+    constexpr integral_constant<int, 2> two;
+    switch (bwd_lanes(d)) {
+        case 8: return f(integral_constant<int, 8>{}, one);
+        case 16: return f(integral_constant<int, 16>{}, one);
+        case 32: return f(integral_constant<int, 32>{}, one);
+        case 64: return f(integral_constant<int, 64>{}, one);
+        case 128: return f(integral_constant<int, 128>{}, one);
+        case 192: return f(integral_constant<int, 192>{}, one);
+        case 256: return f(integral_constant<int, 256>{}, one);
+        case 384: return f(integral_constant<int, 384>{}, one);
+        case 1024: return f(integral_constant<int, 1024>{}, two);
+    }
+    return d / kPiece <= 512 ? f(integral_constant<int, 512>{}, one) : f(integral_constant<int, 512>{}, two);
 }
 template <class F>
 hipError_t by_type(const la_gate_norm_config& c, F&& f) {
@@ -316,9 +349,7 @@ hipError_t by_mode(const la_gate_norm_config& c, F&& f) {
 }
 
 int bwd_groups(const la_gate_norm_config& c) {
-    const int pieces = c.d / kPiece;
-    const int lanes = pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : pieces <= 64 ? 64 : pieces <= 256 ? 256 : pieces <= 1024 ? 512 : 1024;
-    const int rpw = lanes < 256 ? 256 / lanes : 1;
+    const int lanes = bwd_lanes(c.d), rpw = lanes <= 64 ? 256 / lanes : 1;
     const int need = (c.rows + rpw - 1) / rpw, most = 256 * groups_for(lanes, c.gate != LA_GATE_NONE && c.pre);
     return need < most ? need : most;
 }
@@ -369,7 +400,7 @@ hipError_t launch_gate_bwd(const la_gate_norm_config& c, const GateArgs& a, hipS
                 return by_width_bwd(c.d, [&](auto lanes, auto ch) {
                     constexpr int LANES = decltype(lanes)::value;
                     gate_bwd_kernel<decltype(t), LANES, decltype(ch)::value, decltype(gate)::value, decltype(pre)::value>
-                        <<<groups, LANES < 256 ? 256 : LANES, 0, s>>>(p);
+                        <<<groups, LANES <= 64 ? 256 : LANES, 0, s>>>(p);
                     return hipGetLastError();
                 });
             });

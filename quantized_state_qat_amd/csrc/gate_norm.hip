@@ -123,16 +123,16 @@ __device__ __forceinline__ void emit_codes_fast(const CodeOut& o, int l, int row
 }
 
 template <class T, int LANES, int CH, int QDQ>
-__global__ __launch_bounds__(256) void gate_fwd_kernel(GateFwd p) {
-    constexpr int RPW = 256 / LANES;
+__global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(GateFwd p) {
+    constexpr int RPW = LANES <= 64 ? 256 / LANES : 1;
     // What codes are formed from does not depend on y's type or on whether y is wanted.  Of FP32 rows every
     // operation is rounded as the formula has it and squares are summed in double, as in the residual norm; of
     // bf16 rows (whose own rounding is 2^-8) sums are FP32, norms by the reciprocal root and the gate within
     // (|z| + 2) 2^-23 (40686 x 4096 with 32 heads of 128 and silu: 289 us stepwise, 202 so).
     constexpr bool STEPWISE = QDQ != LA_QDQ_NONE && sizeof(T) == 4;
     typedef std::conditional_t<STEPWISE, double, float> S;
-    __shared__ S sums[2][4];
-    __shared__ float lds[8];
+    __shared__ S sums[2][LANES / 64 + 1];
+    __shared__ float lds[LANES / 64 + 1];
     const int l = threadIdx.x % LANES;
     const int row = blockIdx.x * RPW + threadIdx.x / LANES;
     if (LANES <= 64 && row >= p.rows) return;  // whole groups of lanes leave together
@@ -284,17 +284,24 @@ __global__ __launch_bounds__(256) void gate_fwd_kernel(GateFwd p) {
     }
 }
 
-// Lanes a row and pieces a lane: one piece a lane up to 2048 columns (a wave with up to four pieces a lane, as
-// in the residual norm, took 189 us where a workgroup a row takes 149, of 40686 x 2048 joined and to INT8).
+// Lanes a row (gate_lanes) and pieces a lane: one piece a lane as far as that goes (a wave with up to four
+// pieces a lane, as in the residual norm, took 189 us where a workgroup a row takes 149, of 40686 x 2048
+// joined and to INT8), two of 256 lanes and more from there on.
 template <class F>
 hipError_t by_width(int d, F&& f) {
     using std::integral_constant;
+    constexpr integral_constant<int, 1> one;
+    switch (gate_lanes(d)) {
+        case 8: return f(integral_constant<int, 8>{}, one);
+        case 16: return f(integral_constant<int, 16>{}, one);
+        case 32: return f(integral_constant<int, 32>{}, one);
+        case 64: return f(integral_constant<int, 64>{}, one);
+        case 128: return f(integral_constant<int, 128>{}, one);
+        case 192: return f(integral_constant<int, 192>{}, one);
+        case 384: return f(integral_constant<int, 384>{}, one);
+    }
     const int pieces = d / kPiece;
-    if (pieces <= 8) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-    if (pieces <= 16) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-    if (pieces <= 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-    if (pieces <= 64) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    if (pieces <= 256) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    if (pieces <= 256) return f(integral_constant<int, 256>{}, one);
     if (pieces <= 512) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
     if (pieces <= 1024) return f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
     return f(integral_constant<int, 256>{}, integral_constant<int, 8>{});
@@ -314,16 +321,17 @@ hipError_t launch_gate_fwd(const la_gate_norm_config& c, const GateArgs& a, hipS
         return by_width(c.d, [&](auto lanes, auto ch) {
             using T = decltype(t);
             constexpr int LANES = decltype(lanes)::value, CH = decltype(ch)::value;
-            const unsigned grid = static_cast<unsigned>((c.rows + 256 / LANES - 1) / (256 / LANES));
+            constexpr int threads = LANES <= 64 ? 256 : LANES, rows = threads / LANES;
+            const unsigned grid = static_cast<unsigned>((c.rows + rows - 1) / rows);
             switch (c.qdq) {
                 case LA_QDQ_INT8_GROUP:
-                    gate_fwd_kernel<T, LANES, CH, LA_QDQ_INT8_GROUP><<<grid, 256, 0, s>>>(p);
+                    gate_fwd_kernel<T, LANES, CH, LA_QDQ_INT8_GROUP><<<grid, threads, 0, s>>>(p);
                     break;
                 case LA_QDQ_E4M3_TILE:
-                    gate_fwd_kernel<T, LANES, CH, LA_QDQ_E4M3_TILE><<<grid, 256, 0, s>>>(p);
+                    gate_fwd_kernel<T, LANES, CH, LA_QDQ_E4M3_TILE><<<grid, threads, 0, s>>>(p);
                     break;
                 default:
-                    gate_fwd_kernel<T, LANES, CH, LA_QDQ_NONE><<<grid, 256, 0, s>>>(p);
+                    gate_fwd_kernel<T, LANES, CH, LA_QDQ_NONE><<<grid, threads, 0, s>>>(p);
             }
             return hipGetLastError();
         });

@@ -111,9 +111,12 @@ __device__ __forceinline__ float row_max(float x, float* lds) {
     if constexpr (LANES <= 64) return group_max_abs<LANES>(x);
     x = group_max_abs<64>(x);
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[4 + (threadIdx.x >> 6)] = x;
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
     __syncthreads();
-    return larger_abs(larger_abs(lds[4], lds[5]), larger_abs(lds[6], lds[7]));
+    x = lds[0];
+#pragma unroll
+    for (int k = 1; k < LANES / 64; k++) x = larger_abs(x, lds[k]);
+    return x;
 }
 
 // 1 / sqrt(m), correct to about an ulp: the hardware's estimate and one Newton step (skipped

@@ -42,9 +42,9 @@ la_status check_gate(const la_gate_norm_config* c) {
     if (c->rows < 0 || c->d <= 0) return fail(LA_ERR_INVALID_ARG, "negative or zero size (rows=%d d=%d)", c->rows, c->d);
     if (c->d % 8 != 0 || c->d > 16384)
         return fail(LA_ERR_UNSUPPORTED, "d must be a multiple of 8 up to 16384 (d=%d)", c->d);
-    // a row has 64 lanes at most, a workgroup from 520 columns on: grids, of whole workgroups of up to 32 rows,
-    // stay below 2^32 threads (a larger one is cut short without an error)
-    const int64_t lanes = c->d <= 64 ? 8 : c->d <= 128 ? 16 : c->d <= 256 ? 32 : c->d <= 512 ? 64 : 256;
+    // grids, of whole workgroups of up to 32 rows, stay below 2^32 threads (a larger one is cut short without
+    // an error)
+    const int64_t lanes = la::gate_lanes(c->d);
     if ((static_cast<int64_t>(c->rows) + 31) * lanes >= (int64_t{1} << 32)) return fail(LA_ERR_UNSUPPORTED, "too many rows (rows=%d d=%d)", c->rows, c->d);
     const bool power = c->head >= 16 && c->head <= 512 && (c->head & (c->head - 1)) == 0;
     if (c->head != 0 && !power)

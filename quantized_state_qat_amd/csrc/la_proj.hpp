@@ -45,6 +45,13 @@ struct GateArgs {
     float* dw_pre = nullptr;
     float* part = nullptr;
 };
+// Lanes that hold a row of the forward: pieces of 8 columns on 8 to 64 lanes of a wave, then a workgroup of whole
+// waves, with two pieces a lane and more from about 384 pieces on.
+inline int gate_lanes(int d) {
+    const int pieces = d / 8;
+    if (pieces <= 64) return pieces <= 8 ? 8 : pieces <= 16 ? 16 : pieces <= 32 ? 32 : 64;
+    return pieces <= 128 ? 128 : pieces <= 192 ? 192 : pieces <= 256 ? 256 : pieces <= 384 ? 384 : 256;
+}
 hipError_t launch_gate_fwd(const la_gate_norm_config& c, const GateArgs& a, hipStream_t s);
 hipError_t launch_gate_bwd(const la_gate_norm_config& c, const GateArgs& a, hipStream_t s);
 size_t gate_bwd_workspace(const la_gate_norm_config& c);

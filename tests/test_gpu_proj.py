@@ -162,6 +162,12 @@ GATE = [
     (BF, F32, F32, 12, 6144, 0, 2, 1, 1, 0, 1, 1, 0, 0),
     (F32, F32, F32, 1000, 512, 64, 1, 0, 1, 1, 1, 1, 0, 0),
     (F32, F32, F32, 11, 32, 32, 0, 0, 1, 0, 0, 0, 0, 0),
+    (BF, BF, F32, 21, 1024, 0, 1, 0, 1, 1, 1, 1, 0, 0),
+    (F32, F32, F32, 13, 1152, 128, 2, 0, 1, 1, 1, 1, 0, 0),
+    (BF, F32, F32, 19, 2304, 256, 1, 1, 1, 1, 1, 1, 8, 0),
+    (F32, F32, BF, 800, 2056, 0, 0, 0, 1, 1, 1, 1, 0, 0),
+    (BF, BF, F32, 10, 8192, 512, 1, 0, 1, 1, 1, 1, 0, 0),
+    (BF, BF, F32, 7, 10240, 0, 0, 0, 1, 1, 1, 1, 0, 0),
 ]
 
 

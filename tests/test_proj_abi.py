@@ -127,11 +127,11 @@ def test_gate_norm_refuses_configs(kw, status, word):
     assert la.la_gate_norm_bwd_workspace_bytes(gate(**kw)) == 0
 
 
-@pytest.mark.parametrize("d,lanes", [(64, 8), (72, 16), (256, 32), (512, 64), (520, 256), (2048, 256), (16384, 256)])
+@pytest.mark.parametrize("d,lanes", [(64, 8), (72, 16), (256, 32), (512, 64), (520, 128), (1032, 192), (2048, 256), (2304, 384), (16384, 256)])
 def test_gate_norm_refuses_grids_of_two_to_the_32(d, lanes):
-    """A row has that many threads, and a grid whole workgroups of 256."""
-    most = min((1 << 32) // lanes - 32, (1 << 31) - 1)
-    assert la.la_gate_norm_bwd_workspace_bytes(gate(rows=most, d=d)) > 0 and -(-most * lanes // 256) * 256 < 1 << 32
+    """A row has that many threads, and a grid whole workgroups of 256, or of the row's threads."""
+    most = min(((1 << 32) - 1) // lanes - 31, (1 << 31) - 1)  # (most + 31) lanes < 2^32
+    assert la.la_gate_norm_bwd_workspace_bytes(gate(rows=most, d=d)) > 0 and -(-most * lanes // max(lanes, 256)) * max(lanes, 256) < 1 << 32
     if most < (1 << 31) - 1:
         refused(lambda: gate_fwd(gate(rows=most + 1, d=d)), la.LA_ERR_UNSUPPORTED, "too many rows")
 
