@@ -8,7 +8,7 @@
 // tokens of dweight), so a pass over dy and one over each matrix of codes lay the operands out first,
 // 128 bytes of the summed index at a time: they move 2 to 8 bytes an element once where the product
 // itself reads an operand many times over.  32768 x 2048 x 2048 from bf16 dy to bf16 dx and FP32 dweight 930 us:
-// 33 + 94 + 43 laying out (4.5 to 6 TB/s: memory bound), 250 + 460 the products (1100 to 1190 TFLOP/s: power bound),
+// 40 + 94 + 39 laying out (3.3 to 5.7 TB/s: memory bound), 250 + 460 the products (1100 to 1190 TFLOP/s: power bound),
 // 14 joining dweight's four parts.
 #include "linear_gemm.hpp"
 
@@ -49,10 +49,13 @@ struct DyArgs {
 };
 
 // Largest magnitudes of rows and columns (integer maxima: their order does not matter) and the sums
-// of 64 rows: a workgroup has 64 rows of 256 columns, eight of each a lane, all loaded together (33 us for
-// 32768 x 2048 bf16, 4.1 TB/s).
+// of 64 rows: a workgroup has 64 rows of 256 columns, eight of each a lane, all loaded together.  Floating maxima
+// pass over NaN by themselves; where an infinity came up, the finite values' are taken in another pass.
+// 32768 x 2048 bf16 40 us (3.3 TB/s; 39 without the columns' atomics, 43 with every value looked at for
+// infinities).
 template <bool FULL, class T>
-__device__ __forceinline__ void stats_rows(const DyArgs& a, int m0, int n, int ty, float (&cs)[8], uint32_t (&cm)[8]) {
+__device__ __forceinline__ void stats_rows(const DyArgs& a, int m0, int n, int ty, float (&cs)[8], uint32_t (&cm)[8],
+                                           uint32_t (&rows)[64]) {
     float ws[8] = {}, xs[8] = {}, v[8][8];
     if (a.rowmax) load_part<FULL>(a.ws, n, a.N, ws);
 #pragma unroll
@@ -66,37 +69,62 @@ __device__ __forceinline__ void stats_rows(const DyArgs& a, int m0, int n, int t
             for (int e = 0; e < 8; e++) v[k][e] = 0.0f;
         }
     }
+    float rm[8] = {}, cf[8] = {}, top = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; k++) {
-        const int m = m0 + ty + 8 * k;
-        uint32_t rm = 0;
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            rm = umax(rm, finite_abs(v[k][e] * ws[e]));
-            cm[e] = umax(cm[e], finite_abs(v[k][e] * xs[k]));
+            rm[k] = fmaxf(rm[k], fabsf(v[k][e] * ws[e]));
+            cf[e] = fmaxf(cf[e], fabsf(v[k][e] * xs[k]));
             cs[e] += v[k][e];
         }
-        rm = __float_as_uint(group_max_abs<32>(__uint_as_float(rm)));
-        if (a.rowmax && (threadIdx.x & 31) == 0 && rm) atomicMax(a.rowmax + m, rm);
+        top = fmaxf(top, rm[k]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        cm[e] = __float_as_uint(cf[e]);
+        top = fmaxf(top, cf[e]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+        const uint32_t r = __float_as_uint(group_max_abs<32>(rm[k]));
+        if ((threadIdx.x & 31) == 0) rows[ty + 8 * k] = r;
+    }
+    if (!__any(top == __builtin_inff())) return;
+#pragma unroll
+    for (int e = 0; e < 8; e++) cm[e] = 0;
+#pragma unroll 1
+    for (int k = ty; k < 64 && m0 + k < a.M; k += 8) {
+        load_part<FULL>(static_cast<const T*>(a.dy) + (m0 + k) * a.ld, n, a.N, v[0]);
+        const float x = a.colmax ? a.xs[m0 + k] : 0.0f;
+        uint32_t r = 0;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            r = umax(r, finite_abs(v[0][e] * ws[e]));
+            cm[e] = umax(cm[e], finite_abs(v[0][e] * x));
+        }
+        r = __float_as_uint(group_max_abs<32>(__uint_as_float(r)));
+        if ((threadIdx.x & 31) == 0) rows[k] = r;
     }
 }
 template <class T>
 __global__ __launch_bounds__(256) void stats_kernel(DyArgs a) {
     __shared__ float sum[8][256];
-    __shared__ uint32_t top[8][256];
+    __shared__ uint32_t top[8][256], rows[64];
     const int across = (a.N + 255) / 256;
     const int n0 = (blockIdx.x % across) * 256, m0 = (blockIdx.x / across) * 64;
     const int c = (threadIdx.x & 31) * 8, ty = threadIdx.x >> 5;
     float cs[8] = {};
     uint32_t cm[8] = {};
-    if (a.wide && m0 + 64 <= a.M && n0 + 256 <= a.N) stats_rows<true, T>(a, m0, n0 + c, ty, cs, cm);
-    else stats_rows<false, T>(a, m0, n0 + c, ty, cs, cm);
+    if (a.wide && m0 + 64 <= a.M && n0 + 256 <= a.N) stats_rows<true, T>(a, m0, n0 + c, ty, cs, cm, rows);
+    else stats_rows<false, T>(a, m0, n0 + c, ty, cs, cm, rows);
 #pragma unroll
     for (int e = 0; e < 8; e++) {
         sum[ty][c + e] = cs[e];
         top[ty][c + e] = cm[e];
     }
     __syncthreads();
+    if (a.rowmax && threadIdx.x < 64 && rows[threadIdx.x]) atomicMax(a.rowmax + m0 + threadIdx.x, rows[threadIdx.x]);
     const int col = n0 + threadIdx.x;
     if (col >= a.N) return;
     float s = 0.0f;
@@ -213,7 +241,7 @@ __global__ __launch_bounds__(256) void lay_dy_kernel(DyArgs a, int bias) {
 }
 
 // Codes [R][C] (rows ld bytes apart, C a multiple of 16) to FP16, C rows of R in chunks of 64: 64 x 64 a
-// workgroup (43 us for 32768 x 2048, 4.9 TB/s; the bytes' reads across LDS rows conflict, under the stores).
+// workgroup (39 us for 32768 x 2048, 5.4 TB/s; 44 with the halves of a line on two dies).
 struct Codes {
     const int8_t* codes;
     int64_t ld;
@@ -221,14 +249,17 @@ struct Codes {
     char* out;
     int blocks;
 };
-__device__ __forceinline__ void lay_codes(const Codes& a, int block, int8_t (&tile)[64][80]) {
+__device__ __forceinline__ void lay_codes(const Codes& a, int block, int8_t (&tile)[64][68]) {
     const int across = (a.C + 63) / 64;
+    // (the halves of a line on one die, workgroups eight apart)
+    if ((block | 15) < a.blocks) block = (block & ~15) | (block & 7) << 1 | (block >> 3 & 1);
     const int c0 = (block % across) * 64, cr = block / across, r0 = cr * 64;
     {
         const int rr = threadIdx.x >> 2, c = (threadIdx.x & 3) * 16;
         uv4 v = {};
         if (r0 + rr < a.R && c0 + c < a.C) v = load16(a.codes + (r0 + rr) * a.ld + c0 + c);
-        *reinterpret_cast<uv4*>(&tile[rr][c]) = v;
+#pragma unroll
+        for (int e = 0; e < 4; e++) *reinterpret_cast<uint32_t*>(&tile[rr][c + 4 * e]) = v[e];
     }
     __syncthreads();
     const int64_t row = part_at((a.R + 63) / 64, 0, 1);
@@ -245,7 +276,7 @@ __device__ __forceinline__ void lay_codes(const Codes& a, int block, int8_t (&ti
 }
 // Both operands of codes, and zeros to what the maxima of dy go to.
 __global__ __launch_bounds__(256) void lay_codes_kernel(Codes x, Codes w, uint32_t* clear, int64_t words) {
-    __shared__ __align__(16) int8_t tile[64][80];
+    __shared__ __align__(16) int8_t tile[64][68];
     const int b = blockIdx.x;
     if (b < x.blocks) return lay_codes(x, b, tile);
     if (b < x.blocks + w.blocks) return lay_codes(w, b - x.blocks, tile);

@@ -590,3 +590,31 @@ def test_two_streams_with_workspaces_of_their_own():
             la.la_linear_bwd(cfg, xc, xs, wc, ws, dy, *outs[1], space, n, stream=st)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for c in cases for a, b in zip(*c[5]))
+
+
+@pytest.mark.parametrize("M,N", [(192, 512), (130, 520)])
+@pytest.mark.parametrize("t", [BF, F32])
+def test_linear_bwd_other_rows_beside_an_infinity(M, N, t):
+    """Largest magnitudes are the finite values' in whole blocks of rows and columns and in parts of them."""
+    K = 64
+    g = gen(11)
+    (xc, xs), (wc, ws) = codes(gen(3), M, K), codes(gen(4), N, K)
+    # (magnitudes over 2^40: a maximum lost or taken too high leaves nothing of the values)
+    dy = (draw(g, M, N, dtype=F32) * torch.exp2(torch.randint(-20, 21, (M, 1), generator=g).float()).cuda()).to(t)
+    dy[3, 5], dy[65, 300], dy[129, N - 1] = float("inf"), float("-inf"), float("nan")
+    cfg = la.LinearConfig(M=M, N=N, K=K, x_dtype=la.LA_F32, out_dtype=CODE[t], dw_dtype=la.LA_F32)
+    n = la.la_linear_bwd_workspace_bytes(cfg)
+    dx, dw, db = torch.empty(M, K, device="cuda"), torch.empty(N, K, device="cuda"), torch.empty(N, device="cuda")
+    la.la_linear_bwd(cfg, xc, xs, wc, ws, dy, dx, dw, db, torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+    rows, cols = [m for m in range(M) if m not in (3, 65, 129)], [c for c in range(N) if c not in (5, 300, N - 1)]
+    for a, bad in ((dx, (3, 65, 129)), (dw, (5, 300, N - 1))):
+        assert not any(a[i].isfinite().any() for i in bad)
+    held = dy.clone()
+    held[~held.isfinite()] = 0.0
+    args = [np64(xc), np64(xs), np64(wc), np64(ws), np64(held)]
+    want, mag = R.linear_bwd(*args), R.linear_bwd(*[np.abs(a) for a in args])
+    close(dx[rows], want[0][rows], mag[0][rows], 2.0 ** -22 + (N + 2) * 2.0 ** -23, "dx")
+    # a column's smaller rows: 2^-29 of its largest value
+    top = (np.abs(args[4]) * args[1][:, None]).max(0)[:, None] * np.abs(args[0]).sum(0) * 2.0 ** -29
+    close(dw[cols], want[1][cols], mag[1][cols] + top[cols], 2.0 ** -22 + (M + 2) * 2.0 ** -23, "dweight")
+    assert db[cols].isfinite().all() and not db[[5, 300, N - 1]].isfinite().any()
