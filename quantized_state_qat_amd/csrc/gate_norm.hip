@@ -5,7 +5,7 @@
 // Memory bound: one pass over the data, a row in the registers of 8 to 384 lanes between its loads, its
 // two norms and its outputs.  A head of 16 to 512 columns is 2 to 64 neighbouring lanes, whose sum needs no
 // LDS.  bf16 to INT8 codes and their values: 40686 rows of 32 heads of 128 with silu 202 us (5.8 TB/s, the vector
-// units 80% busy), the join of 40686 x 2048 149 us (5.0 TB/s); 32768 x 2048 without codes 72 and 85 us; 4 rows
+// units 80% busy), the join of 40686 x 2048 152 us (4.9 TB/s); 32768 x 2048 without codes 72 and 85 us; 4 rows
 // of 2048 3.5 us, latencies.
 #include "la_gate.hpp"
 
@@ -124,16 +124,22 @@ __device__ __forceinline__ void emit_codes_fast(const CodeOut& o, int l, int row
     }
 }
 
-template <class T, int LANES, int CH, int QDQ>
+template <class T, int LANES, int CH, int QDQ, bool FINE>
 __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(GateFwd p) {
     constexpr int RPW = LANES <= 64 ? 256 / LANES : 1;
     // What codes are formed from does not depend on y's type or on whether y is wanted.  Of FP32 rows every
-    // operation is rounded as the formula has it and squares are summed in double, as in the residual norm; of
-    // bf16 rows (whose own rounding is 2^-8) sums are FP32, norms by the reciprocal root and the gate within
-    // (|z| + 2) 2^-23 (40686 x 4096 with 32 heads of 128 and silu: 289 us stepwise, 202 so).
+    // operation is rounded as the formula has it and squares are summed in double, as in the residual norm
+    // (STEPWISE); of bf16 rows (whose own rounding is 2^-8) sums are FP32, norms by the reciprocal root and the gate
+    // within (|z| + 2) 2^-23 (40686 x 4096 with 32 heads of 128 and silu: 289 us stepwise, 202 so).  Where h is
+    // rounded before codes are formed, what leads to it is rounded stepwise too and a row's sum joined in double
+    // (FINE): a last bit there moves h by 2^-8 of itself where it falls on a tie, and with a row's largest element
+    // its scale (40686 x 2048: 530 of 83 million elements differ from the formula so rounded without it and 170, by
+    // the mean's last bit, with it; 149 and 152 us).
     constexpr bool STEPWISE = QDQ != LA_QDQ_NONE && sizeof(T) == 4;
-    typedef std::conditional_t<STEPWISE, double, float> S;
-    __shared__ S sums[2][LANES / 64 + 1];
+    typedef std::conditional_t<FINE, double, float> S;
+    typedef std::conditional_t<STEPWISE, double, float> S2;
+    __shared__ S sums[LANES / 64 + 1];
+    __shared__ S2 sums2[LANES / 64 + 1];
     __shared__ float lds[LANES / 64 + 1];
     const int l = threadIdx.x % LANES;
     const int row = blockIdx.x * RPW + threadIdx.x / LANES;
@@ -158,7 +164,7 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(Gat
         for (int c = 0; c < CH; c++)
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                if constexpr (STEPWISE) g[c][e] = gate_stepwise(g[c][e], p.gate);
+                if constexpr (FINE) g[c][e] = gate_stepwise(g[c][e], p.gate);
                 else g[c][e] = gate_of<T>(g[c][e], p.gate);
             }
         if (p.first) {
@@ -170,8 +176,8 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(Gat
     }
     const float inv_d = 1.0f / static_cast<float>(p.d), inv_head = 1.0f / static_cast<float>(p.head ? p.head : 1);
     // v / rms: stepwise by the correctly rounded quotient, else by the reciprocal root
-    auto unit = [](float (&v)[8], S sum, int n, [[maybe_unused]] float inv, float eps) {
-        if constexpr (STEPWISE) {
+    auto unit = [](auto fine, float (&v)[8], auto sum, int n, [[maybe_unused]] float inv, float eps) {
+        if constexpr (decltype(fine)::value) {
             const float rms = sqrtf(static_cast<float>(sum / n) + eps);
             const bool fast = rms > 0x1p-60f && rms < 0x1p60f;
             const float e0 = __builtin_amdgcn_rcpf(rms);
@@ -184,11 +190,11 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(Gat
             for (int e = 0; e < 8; e++) v[e] *= k;
         }
     };
-    auto squares = [](const float (&v)[8]) {
-        S s = 0;
+    auto squares = [](auto zero, const float (&v)[8]) {
+        auto s = zero;
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            if constexpr (STEPWISE) s += v[e] * v[e];
+            if constexpr (sizeof(s) == 8) s += v[e] * v[e];
             else s = __builtin_fmaf(v[e], v[e], s);
         }
         return s;
@@ -197,14 +203,14 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(Gat
         S row_ss = 0;
         if (p.head == 0) {
 #pragma unroll
-            for (int c = 0; c < CH; c++) row_ss += squares(t[c]);
-            row_ss = sum_row<LANES>(row_ss, sums[0]);
+            for (int c = 0; c < CH; c++) row_ss += squares(S2(0), t[c]);
+            row_ss = sum_row<LANES>(row_ss, sums);
         }
 #pragma unroll
         for (int c = 0; c < CH; c++) {
             const int col = (c * LANES + l) * kPiece;
-            const S ss = p.head ? sum_lanes(squares(t[c]), p.head / kPiece) : row_ss;
-            unit(t[c], ss, p.head ? p.head : p.d, p.head ? inv_head : inv_d, p.eps);
+            const S ss = p.head ? sum_lanes(squares(S(0), t[c]), p.head / kPiece) : row_ss;
+            unit(std::bool_constant<FINE>{}, t[c], ss, p.head ? p.head : p.d, p.head ? inv_head : inv_d, p.eps);
             float w[8];
             if (p.w_post && col < p.d) {
                 load_w(p.w_post, p.w_dtype, p.head ? col & (p.head - 1) : col, w);
@@ -213,7 +219,7 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(Gat
             }
         }
     }
-    S ss = 0;
+    S2 ss = 0;
 #pragma unroll
     for (int c = 0; c < CH; c++) {
         const int col = (c * LANES + l) * kPiece;
@@ -246,15 +252,15 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(Gat
                     t[c][e + 1] = hi16(u);
                 }
             }
-            ss += squares(t[c]);
+            ss += squares(S2(0), t[c]);
         }
     }
     if (p.pre) {
-        ss = sum_row<LANES>(ss, sums[1]);
+        ss = sum_row<LANES>(ss, sums2);
 #pragma unroll
         for (int c = 0; c < CH; c++) {
             const int col = (c * LANES + l) * kPiece;
-            unit(t[c], ss, p.d, inv_d, p.eps);
+            unit(std::bool_constant<STEPWISE>{}, t[c], ss, p.d, inv_d, p.eps);
             if (p.w_pre && col < p.d) {
                 float w[8];
                 load_w(p.w_pre, p.w_dtype, col, w);
@@ -325,15 +331,15 @@ hipError_t launch_gate_fwd(const la_gate_norm_config& c, const GateArgs& a, hipS
             constexpr int LANES = decltype(lanes)::value, CH = decltype(ch)::value;
             constexpr int threads = LANES <= 64 ? 256 : LANES, rows = threads / LANES;
             const unsigned grid = static_cast<unsigned>((c.rows + rows - 1) / rows);
+            auto launch = [&](auto qdq, auto fine) { gate_fwd_kernel<T, LANES, CH, decltype(qdq)::value, decltype(fine)::value><<<grid, threads, 0, s>>>(p); };
+            auto coded = [&](auto qdq) {
+                if (sizeof(T) == 4 || (c.pre && (c.post || c.gate))) launch(qdq, std::true_type{});
+                else if constexpr (sizeof(T) == 2) launch(qdq, std::false_type{});
+            };
             switch (c.qdq) {
-                case LA_QDQ_INT8_GROUP:
-                    gate_fwd_kernel<T, LANES, CH, LA_QDQ_INT8_GROUP><<<grid, threads, 0, s>>>(p);
-                    break;
-                case LA_QDQ_E4M3_TILE:
-                    gate_fwd_kernel<T, LANES, CH, LA_QDQ_E4M3_TILE><<<grid, threads, 0, s>>>(p);
-                    break;
-                default:
-                    gate_fwd_kernel<T, LANES, CH, LA_QDQ_NONE><<<grid, threads, 0, s>>>(p);
+                case LA_QDQ_INT8_GROUP: coded(std::integral_constant<int, LA_QDQ_INT8_GROUP>{}); break;
+                case LA_QDQ_E4M3_TILE: coded(std::integral_constant<int, LA_QDQ_E4M3_TILE>{}); break;
+                default: launch(std::integral_constant<int, LA_QDQ_NONE>{}, std::false_type{});
             }
             return hipGetLastError();
         });

@@ -618,3 +618,23 @@ def test_linear_bwd_other_rows_beside_an_infinity(M, N, t):
     top = (np.abs(args[4]) * args[1][:, None]).max(0)[:, None] * np.abs(args[0]).sum(0) * 2.0 ** -29
     close(dw[cols], want[1][cols], mag[1][cols] + top[cols], 2.0 ** -22 + (M + 2) * 2.0 ** -23, "dweight")
     assert db[cols].isfinite().all() and not db[[5, 300, N - 1]].isfinite().any()
+
+
+@pytest.mark.parametrize("d,head", [(64, 0), (512, 64), (520, 0), (2048, 0), (4096, 128), (16384, 0)])
+@pytest.mark.parametrize("codec", [la.LA_QDQ_INT8_GROUP, la.LA_QDQ_E4M3_TILE])
+def test_gate_norm_h_before_codes_is_rounded_stepwise(d, head, codec):
+    """With squares whose sums are exact in any order, h is the formula's in FP32, operation by operation."""
+    rows, g = 65, gen(12)
+    x = (torch.exp2(torch.randint(-2, 3, (rows, d), generator=g).float()) * (torch.randint(0, 2, (rows, d), generator=g) * 2 - 1)).cuda()
+    w, al = (draw(g, n, dtype=F32) for n in (head or d, d))
+    x, res = x.to(BF), draw(g, rows, d)
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    codes_, scales = torch.empty(rows, d, dtype=torch.uint8, device="cuda"), torch.empty(rows, device="cuda")
+    cfg = la.GateNormConfig(rows=rows, d=d, head=head, eps=2.0 ** -6, pre=1, qdq=codec)
+    la.la_gate_norm_fwd(cfg, x, None, w, al, res, None, h, y, codes_, scales)
+    f = x.float().cpu().unflatten(-1, (-1, head or d))
+    # the mean is rounded once (520 columns), and the root: 53 bits, 2 x 24 + 2 or more, round to FP32's own root
+    # (the vectorised FP32 root on the CPU is not it: 12 of 65 rows of 2048 a bit off)
+    rms = ((f.double() ** 2).mean(-1, keepdim=True).float() + 2.0 ** -6).double().sqrt().float()
+    p = ((f / rms) * w.cpu()).flatten(-2)
+    assert torch.equal(h.cpu(), (res.float().cpu() + al.cpu() * p).to(BF))
