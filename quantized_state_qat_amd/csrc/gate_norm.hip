@@ -5,7 +5,7 @@
 // Memory bound: one pass over the data, a row in the registers of 8 to 384 lanes between its loads, its
 // two norms and its outputs.  A head of 16 to 512 columns is 2 to 64 neighbouring lanes, whose sum needs no
 // LDS.  bf16 to INT8 codes and their values: 40686 rows of 32 heads of 128 with silu 202 us (5.8 TB/s, the vector
-// units 80% busy), the join of 40686 x 2048 152 us (4.9 TB/s); 32768 x 2048 without codes 72 and 85 us; 4 rows
+// units 80% busy), the join of 40686 x 2048 150 us (5.0 TB/s); 32768 x 2048 without codes 72 and 85 us; 4 rows
 // of 2048 3.5 us, latencies.
 #include "la_gate.hpp"
 
@@ -21,6 +21,7 @@ __device__ __forceinline__ float gate_stepwise(float z, int gate) {
 struct GateFwd {
     int rows, d, head, gate, first, post, pre, group, w_dtype, out_dtype;
     float eps;
+    double inv_d, inv_head;
     int64_t ld_x, ld_z;
     const void* x;
     const void* z;
@@ -134,7 +135,7 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(Gat
     // rounded before codes are formed, what leads to it is rounded stepwise too and a row's sum joined in double
     // (FINE): a last bit there moves h by 2^-8 of itself where it falls on a tie, and with a row's largest element
     // its scale (40686 x 2048: 530 of 83 million elements differ from the formula so rounded without it and 170, by
-    // the mean's last bit, with it; 149 and 152 us).
+    // the mean's last bit, with it; 149 and 150 us).
     constexpr bool STEPWISE = QDQ != LA_QDQ_NONE && sizeof(T) == 4;
     typedef std::conditional_t<FINE, double, float> S;
     typedef std::conditional_t<STEPWISE, double, float> S2;
@@ -176,9 +177,11 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(Gat
     }
     const float inv_d = 1.0f / static_cast<float>(p.d), inv_head = 1.0f / static_cast<float>(p.head ? p.head : 1);
     // v / rms: stepwise by the correctly rounded quotient, else by the reciprocal root
-    auto unit = [](auto fine, float (&v)[8], auto sum, int n, [[maybe_unused]] float inv, float eps) {
+    auto unit = [&p](auto fine, float (&v)[8], auto sum, int n, [[maybe_unused]] float inv, float eps) {
         if constexpr (decltype(fine)::value) {
-            const float rms = sqrtf(static_cast<float>(sum / n) + eps);
+            // (a double's quotient took 3 us of 152 here; its reciprocal's product rounds to the same FP32 value but
+            // within 2^-52 of a tie)
+            const float rms = sqrtf(static_cast<float>(sum * (n == p.d ? p.inv_d : p.inv_head)) + eps);
             const bool fast = rms > 0x1p-60f && rms < 0x1p60f;
             const float e0 = __builtin_amdgcn_rcpf(rms);
             const float recip = __builtin_fmaf(__builtin_fmaf(-rms, e0, 1.0f), e0, e0);
@@ -322,7 +325,7 @@ hipError_t by_type(const la_gate_norm_config& c, F&& f) {
 }  // namespace
 
 hipError_t launch_gate_fwd(const la_gate_norm_config& c, const GateArgs& a, hipStream_t s) {
-    const GateFwd p{c.rows, c.d, c.head, c.gate, c.gate_first, c.post, c.pre, c.group, c.w_dtype, c.out_dtype, c.eps,
+    const GateFwd p{c.rows, c.d, c.head, c.gate, c.gate_first, c.post, c.pre, c.group, c.w_dtype, c.out_dtype, c.eps, 1.0 / c.d, 1.0 / (c.head ? c.head : 1),
                     c.ld_x ? c.ld_x : c.d, c.ld_z ? c.ld_z : c.d, a.x, a.z, a.w_post, a.alpha, a.res, a.w_pre, a.h, a.y,
                     static_cast<uint8_t*>(a.codes), a.scales};
     return by_type(c, [&](auto t) {
