@@ -53,10 +53,10 @@ la_status la_linear_fwd(const la_linear_config* cfg, const void* x_codes, const 
 /* Gradients for the upstream gradient dy, straight through the codes' rounding, of the values
  * xhat = s_x c_x and what = s_w c_w that they stand for:
  *     dx = dy what ([M][K], tight),   dweight = dy^T xhat ([N][K]),   dbias = the sum of dy's rows (float [N]);
- * each may be NULL.  dy times the scales enters a gradient held in bf16 rounded to FP16's 11 bits (off
- * by at most 2^-11 of the value, an eighth of bf16's own rounding), one held in FP32 as two such parts
- * (2^-22), both under a power of two for its row (for dweight its column): values 2^-29 of the row's
- * largest magnitude or smaller lose more.  dy times a scale is formed in FP32, and must not overflow it.
+ * each may be NULL.  dy times the scales enters as two FP16 parts of 11 bits (off by at most 2^-22 of the
+ * value, whatever the gradient's type) under a power of two for its row (for dweight its column): of values
+ * below 2^-17 of the row's largest magnitude up to 2^-39 of that magnitude is lost.
+ * dy times a scale is formed in FP32, and must not overflow it.
  * The codes enter exactly.  Sums are FP32, those of a sum's parts joined in double in a fixed order; dbias is
  * summed in double over FP32 sums of 64 rows.  M and N up to 2^19, with below 2^23 tiles of 64 x 64.
  * Workspace: at least la_linear_bwd_workspace_bytes(cfg) bytes (operands laid out for the products); a query

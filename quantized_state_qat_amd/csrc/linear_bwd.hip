@@ -2,8 +2,8 @@
 //
 // Both are products on the FP16 matrix cores: FP16 holds every code exactly, and dy times the scale,
 // brought to [2^14, 2^15) by a power of two for each row of the operand (scale_up), is off by at most
-// 2^-11 of itself in one part, for bf16 results, and 2^-22 in two, for FP32 ones (bf16 would be off by
-// 2^-8, as much as a bf16 result's own rounding).
+// 2^-22 of itself in two parts.  (One part, off by 2^-11, halves the product's work, but a bf16 result
+// of terms that cancel shows it: such a gradient then differs from the formula's by more than its own rounding.)
 // The products sum over an index that is not contiguous in what the caller holds (channels of dx,
 // tokens of dweight), so a pass over dy and one over each matrix of codes lay the operands out first,
 // 128 bytes of the summed index at a time: they move 2 to 8 bytes an element once where the product
@@ -45,7 +45,6 @@ struct DyArgs {
     float* dbias;      // [N], or null
     char* qx;          // M rows of N in chunks of 64, or null
     char* qw;          // N rows of M, or null
-    int px, pw;        // parts
 };
 
 // Largest magnitudes of rows and columns (integer maxima: their order does not matter) and the sums
@@ -139,22 +138,20 @@ __global__ __launch_bounds__(256) void stats_kernel(DyArgs a) {
 }
 
 // A part is 64 elements = 128 bytes of the summed index; a row holds chunk c's parts beside each other.
+constexpr int kShift = 1, kParts = 1 << kShift;  // of dy times the scale
 __device__ __forceinline__ int64_t part_at(int chunk, int part, int parts) { return (static_cast<int64_t>(chunk) * parts + part) * 128; }
 
-// Eight scaled values as FP16, in one part or two.  The second is what the first leaves, which an infinity
+// Eight scaled values as FP16 in two parts.  The second is what the first leaves, which an infinity
 // leaves infinite: it meets the same codes.
-__device__ __forceinline__ void store_parts(char* o, const float (&v)[8], int parts) {
-    hv8 hi;
+__device__ __forceinline__ void store_parts(char* o, const float (&v)[8]) {
+    hv8 hi, lo;
 #pragma unroll
-    for (int e = 0; e < 8; e++) hi[e] = static_cast<_Float16>(v[e]);
-    *reinterpret_cast<hv8*>(o) = hi;
-    if (parts == 2) {
-        hv8 lo;
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-            lo[e] = static_cast<_Float16>(v[e] - __builtin_amdgcn_fmed3f(static_cast<float>(hi[e]), -65504.0f, 65504.0f));
-        *reinterpret_cast<hv8*>(o + 128) = lo;
+    for (int e = 0; e < 8; e++) {
+        hi[e] = static_cast<_Float16>(v[e]);
+        lo[e] = static_cast<_Float16>(v[e] - __builtin_amdgcn_fmed3f(static_cast<float>(hi[e]), -65504.0f, 65504.0f));
     }
+    *reinterpret_cast<hv8*>(o) = hi;
+    *reinterpret_cast<hv8*>(o + 128) = lo;
 }
 
 // 64 x 64 of dy into both operands: along the rows from registers, along the columns through LDS (94 us for
@@ -162,7 +159,7 @@ __device__ __forceinline__ void store_parts(char* o, const float (&v)[8], int pa
 template <bool FULL, class T>
 __device__ __forceinline__ void lay_dy(const DyArgs& a, int cm, int cn, T (&tile)[64][66]) {
     const int n0 = cn * 64, m0 = cm * 64;
-    const int64_t rowx = part_at((a.N + 63) / 64, 0, a.px), roww = part_at((a.M + 63) / 64, 0, a.pw);
+    const int64_t rowx = part_at((a.N + 63) / 64, 0, kParts), roww = part_at((a.M + 63) / 64, 0, kParts);
     const int c = (threadIdx.x & 7) * 8;
     float ws[8], xs[8], v[2][8];
     if (a.qx) load_part<FULL>(a.ws, n0 + c, a.N, ws);
@@ -189,7 +186,7 @@ __device__ __forceinline__ void lay_dy(const DyArgs& a, int cm, int cn, T (&tile
             float p[8];
 #pragma unroll
             for (int e = 0; e < 8; e++) p[e] = v[k][e] * ws[e] * up;
-            store_parts(a.qx + m * rowx + part_at(cn, 0, a.px) + 2 * c, p, a.px);
+            store_parts(a.qx + m * rowx + part_at(cn, 0, kParts) + 2 * c, p);
         }
     }
     if (!a.qw) return;
@@ -205,7 +202,7 @@ __device__ __forceinline__ void lay_dy(const DyArgs& a, int cm, int cn, T (&tile
             if constexpr (sizeof(T) == 2) p[e] = bf16_bits_to_f32(tile[c + e][rr]) * xs[e] * up;
             else p[e] = tile[c + e][rr] * xs[e] * up;
         }
-        store_parts(a.qw + n * roww + part_at(cm, 0, a.pw) + 2 * c, p, a.pw);
+        store_parts(a.qw + n * roww + part_at(cm, 0, kParts) + 2 * c, p);
     }
 }
 // The sums of the blocks of 64 rows, in double and in a fixed order: 32 columns a workgroup, eight interleaved sums.
@@ -322,21 +319,19 @@ size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 // What the workspace holds, in this order.
 struct Layout {
     size_t rowmax, colmax, part, qx, qw, pw, px, sums_x, sums_w, end;  // offsets; pw: w's codes, px: x's
-    int parts_x, parts_w;  // of an operand
     Cut dx, dw;            // the two products,
     bool pair;             // which may share a launch
 };
 Layout layout(const la_linear_config& c) {
     Layout l;
-    l.parts_x = c.x_dtype == LA_F32 ? 2 : 1, l.parts_w = c.dw_dtype == LA_F32 ? 2 : 1;
     const size_t M = c.M, N = c.N, K = c.K, mc = (M + 63) / 64, nc = (N + 63) / 64;
     size_t at = 0;
     auto take = [&](size_t n) { const size_t p = at; at += up256(n); return p; };
     l.rowmax = take(4 * M), l.colmax = take(4 * N), l.part = take(4 * mc * N);
-    l.qx = take(M * nc * 128 * l.parts_x), l.qw = take(N * mc * 128 * l.parts_w);
+    l.qx = take(M * nc * 128 * kParts), l.qw = take(N * mc * 128 * kParts);
     l.pw = take(K * nc * 128), l.px = take(K * mc * 128);
     const auto most = [](size_t n) { return n <= (size_t{1} << 30) ? 16 : 1; };  // (the join's grid)
-    const int steps_x = gemm_steps(nc * 128, l.parts_x - 1), steps_w = gemm_steps(mc * 128, l.parts_w - 1);
+    const int steps_x = gemm_steps(nc * 128, kShift), steps_w = gemm_steps(mc * 128, kShift);
     l.dx = cut_product(c.K, c.M, steps_x, most(M * K));
     l.dw = cut_product(c.K, c.N, steps_w, most(N * K));
     l.pair = cut_pair(c.K, c.M, steps_x, l.dx, c.K, c.N, steps_w, l.dw);
@@ -370,7 +365,6 @@ hipError_t launch_linear_bwd(const la_linear_config& c, const LinearArgs& a, hip
     d.colmax = a.dw ? reinterpret_cast<uint32_t*>(a.work + l.colmax) : nullptr;
     d.part = a.dbias ? reinterpret_cast<float*>(a.work + l.part) : nullptr, d.dbias = a.dbias;
     d.qx = a.dx ? a.work + l.qx : nullptr, d.qw = a.dw ? a.work + l.qw : nullptr;
-    d.px = l.parts_x, d.pw = l.parts_w;
     const int64_t words = static_cast<int64_t>((l.part - l.rowmax) / 4);
     const int64_t mc = (c.M + 63) / 64, nc = (c.N + 63) / 64, kc = (c.K + 63) / 64;
     const Codes x{a.x, c.ld_x ? c.ld_x : c.K, c.M, c.K, a.work + l.px, a.dw ? static_cast<int>(mc * kc) : 0};
@@ -393,13 +387,13 @@ hipError_t launch_linear_bwd(const la_linear_config& c, const LinearArgs& a, hip
     Join jx{}, jw{};
     if (dx) {
         gx.P = a.work + l.pw, gx.ldP = nc * 128, gx.I = c.K, gx.kbytes = static_cast<int>(nc * 128);
-        gx.Q = d.qx, gx.ldQ = nc * 128 * d.px, gx.J = c.M, gx.shift = d.px - 1;
+        gx.Q = d.qx, gx.ldQ = nc * 128 * kParts, gx.J = c.M, gx.shift = kShift;
         gx.row = d.rowmax, gx.out = a.dx, gx.out_dtype = c.x_dtype, gx.ldo = c.K, gx.wide = 1;
         cut(gx, l.dx, reinterpret_cast<float*>(a.work + l.sums_x), jx);
     }
     if (dw) {
         gw.P = a.work + l.px, gw.ldP = mc * 128, gw.I = c.K, gw.kbytes = static_cast<int>(mc * 128);
-        gw.Q = d.qw, gw.ldQ = mc * 128 * d.pw, gw.J = c.N, gw.shift = d.pw - 1;
+        gw.Q = d.qw, gw.ldQ = mc * 128 * kParts, gw.J = c.N, gw.shift = kShift;
         gw.row = d.colmax, gw.out = a.dw, gw.out_dtype = c.dw_dtype, gw.ldo = c.K, gw.wide = 1;
         cut(gw, l.dw, reinterpret_cast<float*>(a.work + l.sums_w), jw);
     }
