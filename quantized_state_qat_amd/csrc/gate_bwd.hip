@@ -257,7 +257,8 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES, waves_for(LANES, GATE !=
                 [[maybe_unused]] float gate, slope;
                 if constexpr (GATE == kGateFirst) gate_at(c, e, gate, slope);
                 const float u = GATE == kGateFirst ? x[c][e] * gate : x[c][e];
-                float g = r1[c] * __builtin_fmaf(-u, k1, dy[c][e]);
+                // (without the norm there is no u in it: an infinite one would leave NaN)
+                float g = p.post ? r1[c] * __builtin_fmaf(-u, k1, dy[c][e]) : dy[c][e];
                 if constexpr (GATE == kGateFirst) {
                     dz[e] = g * x[c][e] * slope;
                     g *= gate;

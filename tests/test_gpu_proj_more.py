@@ -67,3 +67,63 @@ def test_gradients_keep_22_bits_of_dy_under_every_type(M, N, K, t, tx, tw):
     want, mag = R.linear_bwd(*args), R.linear_bwd(*[np.abs(v) for v in args])
     for name, terms, o, w, m in zip(("dx", "dweight"), (N, M), got, want, mag):
         close(o, w, m, 2.0 ** -22 + 2.0 ** -23 + terms * 2.0 ** -23, name)
+
+
+# ---------------------------------------------------------------------- norms around a block
+def gate_gradients(cfg, s, dy, dh, t):
+    """The backward's outputs by name, s the forward's arguments."""
+    rows, d = dy.shape
+    nan = lambda *shape, dtype=F32: torch.full(shape, float("nan"), dtype=dtype, device="cuda")  # noqa: E731
+    h = nan(rows, d, dtype=t)
+    la.la_gate_norm_fwd(cfg, *s.values(), h, None)
+    out = dict(dx=nan(rows, d, dtype=t), dz=nan(rows, d, dtype=t) if cfg.gate else None, dres=nan(rows, d, dtype=t),
+               dw_post=nan(cfg.head or d) if cfg.post else None, dalpha=nan(d), dw_pre=nan(d) if cfg.pre else None)
+    n = la.la_gate_norm_bwd_workspace_bytes(cfg)
+    la.la_gate_norm_bwd(cfg, s["x"], s["z"], s["w_post"], s["alpha"], h if cfg.pre else None, s["w_pre"], dy, dh, *out.values(),
+                        torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda"), n)
+    return h, out
+
+
+@pytest.mark.parametrize("t,d,head", [(BF, 64, 16), (F32, 512, 0), (F32, 520, 0), (BF, 2048, 128), (F32, 5120, 0), (BF, 10240, 512)])
+@pytest.mark.parametrize("act,first", [(0, 0), (1, 0), (2, 1)])
+@pytest.mark.parametrize("post", [0, 1])
+@pytest.mark.parametrize("pre", [0, 1])
+def test_gate_norm_bwd_infinities_and_nan(t, d, head, act, first, post, pre):
+    """They go where the formula takes them: without the norm after the block to their own element and not
+    beyond, with it to their head or row, with the next norm to the row; never to another row."""
+    rows, g = 5, gen(3)
+    head = head if post else 0
+    s = dict(x=draw(g, rows, d, dtype=t), z=draw(g, rows, d, dtype=t) if act else None, w_post=draw(g, head or d, dtype=F32) if post else None,
+             alpha=draw(g, d, dtype=F32), residual=draw(g, rows, d, dtype=t), w_pre=draw(g, d, dtype=F32) if pre else None)
+    dy, dh = draw(g, rows, d, dtype=t), draw(g, rows, d, dtype=t)
+    cfg = la.GateNormConfig(rows=rows, d=d, head=head, eps=1e-5, gate=act, gate_first=first, post=post, pre=pre, x_dtype=CODE[t], out_dtype=CODE[t])
+    clean = gate_gradients(cfg, s, dy, dh, t)[1]
+    bad = {1: (8, float("inf")), 2: (d - 1, float("nan")), 3: (9, float("-inf"))}
+    for r, (c, v) in bad.items():
+        s["x"][r, c] = v
+    h, out = gate_gradients(cfg, s, dy, dh, t)
+    for name in ("dx", "dz", "dres"):
+        if out[name] is not None:
+            assert torch.equal(out[name][[0, 4]], clean[name][[0, 4]]), name
+    if post:
+        width = head or d
+        for r, (c, _) in bad.items():
+            at = c // width * width
+            assert out["dx"][r, at:at + width].isnan().all()
+            if not pre:
+                keep = [k for k in range(d) if not at <= k < at + width]
+                assert torch.equal(out["dx"][r, keep], clean["dx"][r, keep])
+        return
+    if pre:
+        assert all(out["dx"][r].isnan().all() for r in bad)
+        return
+    with np.errstate(invalid="ignore"):
+        keep = R.gate_norm_fwd(*[None if v is None else np64(v) for v in s.values()], 0, 1e-5, act, first, 0, 0)[2]
+        want = R.gate_norm_bwd(np64(s["x"]), keep, np64(dy), np64(dh), first, 0, 0)
+    for name, w in zip(("dx", "dz", "dres"), want):
+        if out[name] is None:
+            continue
+        assert np.array_equal(np.isnan(w), np.isnan(np64(out[name]))), name  # (a gate of NaN times x: no NaN in z here)
+        fine = np.isfinite(w)
+        assert np.array_equal(w[~fine & ~np.isnan(w)], np64(out[name])[~fine & ~np.isnan(w)]), name
+        assert torch.equal(out[name][torch.from_numpy(fine).cuda()], clean[name][torch.from_numpy(fine).cuda()]), name
