@@ -351,11 +351,20 @@ void cut(GemmArgs& g, const Cut& cut, float* sums, Join& join) {
     g.row = nullptr, g.out = sums, g.out_dtype = LA_F32;
 }
 
+// Without tokens or channels every sum is empty: zeros, and no operand is looked at (the call may have none).
+bool no_sums(const la_linear_config& c) { return c.M == 0 || c.N == 0; }
+
 }  // namespace
 
-size_t linear_bwd_workspace(const la_linear_config& c) { return layout(c).end; }
+size_t linear_bwd_workspace(const la_linear_config& c) { return no_sums(c) ? 0 : layout(c).end; }
 
 hipError_t launch_linear_bwd(const la_linear_config& c, const LinearArgs& a, hipStream_t s) {
+    if (no_sums(c)) {
+        for (const hipError_t e : {launch_zero_rows(a.dx, c.x_dtype, c.M, c.K, c.K, s), launch_zero_rows(a.dw, c.dw_dtype, c.N, c.K, c.K, s),
+                                   launch_zero_rows(a.dbias, LA_F32, 1, c.N, c.N, s)})
+            if (e != hipSuccess) return e;
+        return hipSuccess;
+    }
     const Layout l = layout(c);
     const int es = c.out_dtype == LA_BF16 ? 2 : 4;
     DyArgs d{};
@@ -370,19 +379,17 @@ hipError_t launch_linear_bwd(const la_linear_config& c, const LinearArgs& a, hip
     const Codes x{a.x, c.ld_x ? c.ld_x : c.K, c.M, c.K, a.work + l.px, a.dw ? static_cast<int>(mc * kc) : 0};
     const Codes w{a.w, c.K, c.N, c.K, a.work + l.pw, a.dx ? static_cast<int>(nc * kc) : 0};
     const int64_t first = x.blocks + w.blocks + (words + 1023) / 1024;
-    if (first > 0) lay_codes_kernel<<<static_cast<unsigned>(first), 256, 0, s>>>(x, w, reinterpret_cast<uint32_t*>(a.work + l.rowmax), words);
-    // (without tokens or channels the sums are empty: zeros)
+    lay_codes_kernel<<<static_cast<unsigned>(first), 256, 0, s>>>(x, w, reinterpret_cast<uint32_t*>(a.work + l.rowmax), words);
     const int64_t stats = mc * ((c.N + 255) / 256), bias = a.dbias ? (c.N + 31) / 32 : 0, lay = bias + (a.dx || a.dw ? mc * nc : 0);
-    if (stats > 0) {
-        if (es == 2) stats_kernel<uint16_t><<<static_cast<unsigned>(stats), 256, 0, s>>>(d);
-        else stats_kernel<float><<<static_cast<unsigned>(stats), 256, 0, s>>>(d);
-    }
-    if (lay > 0) {
-        if (es == 2) lay_dy_kernel<uint16_t><<<static_cast<unsigned>(lay), 256, 0, s>>>(d, static_cast<int>(bias));
-        else lay_dy_kernel<float><<<static_cast<unsigned>(lay), 256, 0, s>>>(d, static_cast<int>(bias));
+    if (es == 2) {
+        stats_kernel<uint16_t><<<static_cast<unsigned>(stats), 256, 0, s>>>(d);
+        lay_dy_kernel<uint16_t><<<static_cast<unsigned>(lay), 256, 0, s>>>(d, static_cast<int>(bias));
+    } else {
+        stats_kernel<float><<<static_cast<unsigned>(stats), 256, 0, s>>>(d);
+        lay_dy_kernel<float><<<static_cast<unsigned>(lay), 256, 0, s>>>(d, static_cast<int>(bias));
     }
     if (hipError_t e = hipGetLastError()) return e;
-    const bool dx = a.dx && c.M > 0, dw = a.dw && c.N > 0;
+    const bool dx = a.dx, dw = a.dw;
     GemmArgs gx, gw;
     Join jx{}, jw{};
     if (dx) {

@@ -69,6 +69,17 @@ def test_gradients_keep_22_bits_of_dy_under_every_type(M, N, K, t, tx, tw):
         close(o, w, m, 2.0 ** -22 + 2.0 ** -23 + terms * 2.0 ** -23, name)
 
 
+@pytest.mark.parametrize("tx,tw", [(BF, F32), (F32, BF)])
+def test_gradients_of_empty_sums_look_at_no_operand(tx, tw):
+    """Zeros, without codes, scales, dy or a workspace, and for the empty gradient's address too."""
+    spare = torch.full((64,), 7.0, device="cuda")
+    for M, N, K in ((0, 200, 272), (3000, 0, 80), (0, 1, 16), (1, 0, 2048)):
+        out = [torch.full(s, 7.0, dtype=t, device="cuda") for s, t in (((M, K), tx), ((N, K), tw), ((N,), F32))]
+        cfg = la.LinearConfig(M=M, N=N, K=K, x_dtype=CODE[tx], dw_dtype=CODE[tw])
+        la.la_linear_bwd(cfg, None, None, None, None, None, *[v if v.numel() else spare.data_ptr() for v in out], None, 0)
+        assert all((v == 0).all() for v in out) and (spare == 7.0).all()
+
+
 # ---------------------------------------------------------------------- norms around a block
 def gate_gradients(cfg, s, dy, dh, t):
     """The backward's outputs by name, s the forward's arguments."""

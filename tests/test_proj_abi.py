@@ -82,6 +82,14 @@ def test_linear_refuses_pointers():
         refused(lambda: linear_bwd(linear(**kw), FAKE, 1 << 50), la.LA_ERR_UNSUPPORTED, "2^19")
 
 
+def test_linear_backward_without_tokens_or_channels_needs_nothing():
+    """Nothing to sum: no workspace, so no operand is laid out for the products, whose codes may be NULL."""
+    for kw in (dict(M=0), dict(N=0), dict(M=0, N=0), dict(M=0, N=1 << 19, K=65536), dict(N=0, M=1 << 19)):
+        assert la.la_linear_bwd_workspace_bytes(linear(**kw)) == 0
+        linear_bwd(linear(**kw), None, 0, xc=None, xs=None, wc=None, ws=None, dy=None, dx=None, dw=None)
+    assert la.la_linear_bwd_workspace_bytes(linear(M=1, N=1, K=16)) > 0
+
+
 def test_linear_binding_refuses_tensors():
     cfg = linear()
     xc, xs = torch.zeros(8, 64, dtype=torch.int8), torch.zeros(8)
