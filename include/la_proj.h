@@ -77,7 +77,9 @@ typedef enum { LA_GATE_NONE = 0, LA_GATE_SILU = 1, LA_GATE_SIGMOID = 2 } la_out_
  *     p = n  (gate_first or no gate)  or  n act(z)
  *     t = residual + alpha p,      h = t rounded to x_dtype
  *     v = h / rms(h) * w_pre  (pre = 1; over the row)  or  t
- * and, with a quantizer, the codecs of la_norm_fwd on v: y is then the value that a code stands for.
+ * and, with a quantizer, the codecs of la_norm_fwd on v: y is then the value that a code stands for.  (v of
+ * bf16 rows comes from FP32 sums and reciprocal roots, la_norm_fwd's from sums of doubles and quotients: of the
+ * formula that both have, post = 0 and pre = 1, codes may differ by one where v is a tie but for its last bits.)
  * post alone is the gated output norm of a recurrence (silu: gated delta rule; sigmoid: per-channel
  * gates; gate_first: state-space layers), post and pre the join of a block's output to the residual
  * stream and the next block's norm; with neither, no gate and no residual, the codes are x's own.

@@ -4,8 +4,8 @@
 //     v = h / rms(h) * w_pre  or t,     and 8-bit codes of v,
 // Memory bound: one pass over the data, a row in the registers of 8 to 384 lanes between its loads, its
 // two norms and its outputs.  A head of 16 to 512 columns is 2 to 64 neighbouring lanes, whose sum needs no
-// LDS.  bf16 to INT8 codes and their values: 40686 rows of 32 heads of 128 with silu 202 us (5.8 TB/s, the vector
-// units 80% busy), the join of 40686 x 2048 150 us (5.0 TB/s); 32768 x 2048 without codes 72 and 85 us; 4 rows
+// LDS.  bf16 to INT8 codes and their values: 40686 rows of 32 heads of 128 with silu 215 us (5.4 TB/s), the join of
+// 40686 x 2048 157 us (4.8 TB/s): by the vector units as much as by memory; 32768 x 2048 without codes 72 and 85 us; 4 rows
 // of 2048 3.5 us, latencies.
 #include "la_gate.hpp"
 
@@ -40,102 +40,19 @@ __device__ __forceinline__ void store_as(void* p, int dtype, size_t at, const fl
     else store8(static_cast<float*>(p) + at, v);
 }
 
-// Codes of bf16 rows, by the reciprocal of the scale: x / s is off by 2^-23 of itself before it is rounded to
-// a code (the FP32 rows' codes, and the residual norm's, come from the correctly rounded quotient, which
-// takes four more operations a value).  INT8: adding 1.5 x 2^23 rounds to the integer and leaves it in the
-// low byte.
-template <int QDQ, int LANES, int CH>
-__device__ __forceinline__ void emit_codes_fast(const CodeOut& o, int l, int row, size_t base, float (&h)[CH][8], float (&amax)[CH], float* lds) {
-    if (o.group == 0) {
-        float m = 0.0f;
-#pragma unroll
-        for (int c = 0; c < CH; c++) m = larger_abs(m, amax[c]);
-        m = row_max<LANES>(m, lds);
-#pragma unroll
-        for (int c = 0; c < CH; c++) amax[c] = m;
-    } else {  // a row of LANES * 8 columns or more holds whole groups; in a shorter one a group may be the row
-#pragma unroll
-        for (int c = 0; c < CH; c++) {
-            amax[c] = group_max_abs<2>(amax[c]);
-            if (o.group >= 32) amax[c] = larger_abs(amax[c], dpp<kDppXor2>(amax[c]));
-            if (o.group >= 64) amax[c] = larger_abs(amax[c], dpp<kDppHalfMirror>(amax[c]));
-            if (o.group >= 128) amax[c] = larger_abs(amax[c], dpp<kDppMirror>(amax[c]));
-        }
-    }
-    const int per_row = o.group ? o.d / o.group : 1;
-#pragma unroll
-    for (int c = 0; c < CH; c++) {
-        const int col = (c * LANES + l) * kPiece;
-        if (col >= o.d) continue;
-        float s, y;
-        uint32_t word[2] = {0, 0};
-        bool fast = QDQ == LA_QDQ_INT8_GROUP ? int8_scale_recip(amax[c], s, y) : e4m3_scale_recip(amax[c], s, y);
-        if (!(amax[c] < __builtin_inff())) {  // (an infinity or a NaN in the group)
-            s = amax[c];
-            fast = false;
-        }
-        if (fast) {
-            if constexpr (QDQ == LA_QDQ_INT8_GROUP) {
-                constexpr float kRound = 12582912.0f;
-                uint32_t q[8];
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    const float t = __builtin_fmaf(h[c][e], y, kRound);
-                    q[e] = __float_as_uint(t);
-                    h[c][e] = (t - kRound) * s;
-                }
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    const uint32_t lo = __builtin_amdgcn_perm(q[4 * k + 1], q[4 * k], 0x0c0c0400u);
-                    const uint32_t hi = __builtin_amdgcn_perm(q[4 * k + 3], q[4 * k + 2], 0x04000c0cu);
-                    word[k] = lo | hi;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float a = fminf(fmaxf(h[c][e] * y, -448.0f), 448.0f), b = fminf(fmaxf(h[c][e + 1] * y, -448.0f), 448.0f);
-                    const uint32_t k = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false)) & 0xFFFFu;
-                    word[e >> 2] |= k << (8 * (e & 3));
-                    h[c][e] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(k), 0) * s;
-                    h[c][e + 1] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(k), 1) * s;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const float x = h[c][e] / s;
-                const bool number = x == x;  // (of a quotient without one: code 0, or E4M3's NaN)
-                if constexpr (QDQ == LA_QDQ_INT8_GROUP) {
-                    const float q = number ? fminf(fmaxf(rintf(x), -127.0f), 127.0f) : x;
-                    word[e >> 2] |= (number ? static_cast<uint32_t>(static_cast<int>(q)) & 0xFFu : 0u) << (8 * (e & 3));
-                    h[c][e] = q * s;
-                } else {
-                    const float a = number ? fminf(fmaxf(x, -448.0f), 448.0f) : x;
-                    const uint32_t k = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(a, a, 0, false)) & 0xFFu;
-                    word[e >> 2] |= k << (8 * (e & 3));
-                    h[c][e] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(k), 0) * s;
-                }
-            }
-        }
-        if (o.codes) *reinterpret_cast<uv2*>(o.codes + base + col) = uv2{word[0], word[1]};
-        if (o.scales) {
-            if (o.group ? col % o.group == 0 : col == 0)
-                o.scales[static_cast<size_t>(row) * per_row + (o.group ? col / o.group : 0)] = s;
-        }
-    }
-}
-
 template <class T, int LANES, int CH, int QDQ, bool FINE>
 __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(GateFwd p) {
     constexpr int RPW = LANES <= 64 ? 256 / LANES : 1;
     // What codes are formed from does not depend on y's type or on whether y is wanted.  Of FP32 rows every
     // operation is rounded as the formula has it and squares are summed in double, as in the residual norm
     // (STEPWISE); of bf16 rows (whose own rounding is 2^-8) sums are FP32, norms by the reciprocal root and the gate
-    // within (|z| + 2) 2^-23 (40686 x 4096 with 32 heads of 128 and silu: 289 us stepwise, 202 so).  Where h is
+    // within (|z| + 2) 2^-23 (40686 x 4096 with 32 heads of 128 and silu: 289 us stepwise, 215 so).  Codes are those of
+    // the correctly rounded quotient in both (by the product with the scale's reciprocal, which may take a near tie
+    // to the other side, bf16 rows took 200 us, and the join of 40686 x 2048 150 for 157).  Where h is
     // rounded before codes are formed, what leads to it is rounded stepwise too and a row's sum joined in double
     // (FINE): a last bit there moves h by 2^-8 of itself where it falls on a tie, and with a row's largest element
     // its scale (40686 x 2048: 530 of 83 million elements differ from the formula so rounded without it and 170, by
-    // the mean's last bit, with it; 149 and 150 us).
+    // the mean's last bit, with it; it takes about 1 us).
     constexpr bool STEPWISE = QDQ != LA_QDQ_NONE && sizeof(T) == 4;
     typedef std::conditional_t<FINE, double, float> S;
     typedef std::conditional_t<STEPWISE, double, float> S2;
@@ -283,8 +200,7 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(Gat
             }
         }
         const CodeOut o{p.d, p.group, p.codes, p.scales};
-        if constexpr (STEPWISE) emit_codes<QDQ, LANES, CH>(o, l, row, base, t, amax, lds);
-        else emit_codes_fast<QDQ, LANES, CH>(o, l, row, base, t, amax, lds);
+        emit_codes<QDQ, LANES, CH>(o, l, row, base, t, amax, lds);
     }
     if (p.y) {
 #pragma unroll

@@ -138,3 +138,54 @@ def test_gate_norm_bwd_infinities_and_nan(t, d, head, act, first, post, pre):
         fine = np.isfinite(w)
         assert np.array_equal(w[~fine & ~np.isnan(w)], np64(out[name])[~fine & ~np.isnan(w)]), name
         assert torch.equal(out[name][torch.from_numpy(fine).cuda()], clean[name][torch.from_numpy(fine).cuda()]), name
+
+
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("codec", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,group", [(2048, 0), (512, 64), (4096, 128)])
+def test_codes_of_a_row_are_the_codec_of_its_values(t, codec, d, group):
+    """Without norms v is x itself: s = max / 127 (448) and code = rne(v / s), quotients rounded to FP32 as written,
+    so every code is known (8 million values, some of them within 2^-23 of a tie)."""
+    rows = (1 << 23) // d
+    x = draw(gen(5), rows, d, dtype=t)
+    cfg = la.GateNormConfig(rows=rows, d=d, post=0, qdq=la.LA_QDQ_INT8_GROUP if codec == "int8" else la.LA_QDQ_E4M3_TILE, group=group, x_dtype=CODE[t])
+    c = torch.empty(rows, d, dtype=torch.int8 if codec == "int8" else torch.float8_e4m3fn, device="cuda")
+    s = torch.empty(rows, d // (group or d), device="cuda")
+    la.la_gate_norm_fwd(cfg, x, None, None, None, None, None, None, None, c, s)
+    v = x.float().cpu().unflatten(1, (-1, group or d))
+    scale = v.abs().amax(2) / (127.0 if codec == "int8" else 448.0)
+    assert torch.equal(s.cpu(), scale)
+    q = (v / scale[:, :, None]).flatten(1)
+    if codec == "int8":
+        assert torch.equal(c.cpu(), torch.round(q).to(torch.int8))
+    else:  # (a zero's sign aside)
+        assert torch.equal(c.cpu().float(), q.clamp(-448, 448).to(torch.float8_e4m3fn).float())
+
+
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("codec", ["int8", "e4m3"])
+def test_codes_beside_the_residual_norm_s(t, codec):
+    """The formula that both operators have, residual, norm and codes: h is the same, a scale within what the
+    norms may be off by (2^-17, as the tolerances of the forward), and a code moves to its neighbour only where its
+    quotient lies as near to the middle between the two."""
+    rows, d = 1024, 2048
+    g = gen(6)
+    x, res, w = draw(g, rows, d, dtype=t), draw(g, rows, d, dtype=t, scale=3.0), draw(g, d, dtype=F32, scale=0.2) + 1
+    qdq, top = (la.LA_QDQ_INT8_GROUP, 127) if codec == "int8" else (la.LA_QDQ_E4M3_TILE, 448)
+    new = lambda dtype, *shape: torch.empty(*shape, dtype=dtype, device="cuda")  # noqa: E731
+    ct = torch.int8 if codec == "int8" else torch.float8_e4m3fn
+    h1, h2, c1, c2, s1, s2 = new(t, rows, d), new(t, rows, d), new(ct, rows, d), new(ct, rows, d), new(F32, rows), new(F32, rows)
+    la.la_norm_fwd(la.NormConfig(rows=rows, d=d, eps=1e-6, qdq=qdq, group=0, x_dtype=CODE[t]), x, res, w, h1, None, c1, s1)
+    la.la_gate_norm_fwd(la.GateNormConfig(rows=rows, d=d, eps=1e-6, post=0, pre=1, qdq=qdq, x_dtype=CODE[t]), x, None, None, None, res, w, h2, None, c2, s2)
+    assert torch.equal(h1, h2)
+    a, b = np64(s1), np64(s2)
+    assert (np.abs(a - b) <= 2.0 ** -17 * a).all()
+    h = np64(h1)
+    q = h / np.sqrt((h ** 2).mean(1, keepdims=True) + 1e-6) * np64(w) / a[:, None]
+    k1, k2 = np64(c1.float()), np64(c2.float())
+    off = k1 != k2
+    # either code is a nearest one of a quotient that far away
+    step = 1.0 if codec == "int8" else np.exp2(np.maximum(np.floor(np.log2(np.maximum(np.abs(q), 2.0 ** -20))), -6) - 3)
+    assert (np.abs(k1 - k2)[off] <= 2.0001 * np.broadcast_to(step, q.shape)[off]).all()
+    assert (np.abs(np.abs(k1 - q) - np.abs(k2 - q))[off] <= 2 * 2.0 ** -16 * np.abs(q)[off]).all()
+    assert off.mean() <= 2.0 ** -16 * top * 4
