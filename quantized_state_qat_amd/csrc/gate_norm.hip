@@ -49,10 +49,10 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(Gat
     // within (|z| + 2) 2^-23 (40686 x 4096 with 32 heads of 128 and silu: 289 us stepwise, 215 so).  Codes are those of
     // the correctly rounded quotient in both (by the product with the scale's reciprocal, which may take a near tie
     // to the other side, bf16 rows took 200 us, and the join of 40686 x 2048 150 for 157).  Where h is
-    // rounded before codes are formed, what leads to it is rounded stepwise too and a row's sum joined in double
-    // (FINE): a last bit there moves h by 2^-8 of itself where it falls on a tie, and with a row's largest element
-    // its scale (40686 x 2048: 530 of 83 million elements differ from the formula so rounded without it and 170, by
-    // the mean's last bit, with it; it takes about 1 us).
+    // rounded before the next norm, what leads to it is rounded stepwise too and a row's sum joined in double
+    // (FINE), with codes and without: a last bit there moves h by 2^-8 of itself where it falls on a tie, and with a
+    // row's largest element its scale (40686 x 2048: 530 of 83 million elements differ from the formula so rounded
+    // without it and 170, by the mean's last bit, with it; it takes about 1 us).
     constexpr bool STEPWISE = QDQ != LA_QDQ_NONE && sizeof(T) == 4;
     typedef std::conditional_t<FINE, double, float> S;
     typedef std::conditional_t<STEPWISE, double, float> S2;
@@ -251,14 +251,17 @@ hipError_t launch_gate_fwd(const la_gate_norm_config& c, const GateArgs& a, hipS
             constexpr int threads = LANES <= 64 ? 256 : LANES, rows = threads / LANES;
             const unsigned grid = static_cast<unsigned>((c.rows + rows - 1) / rows);
             auto launch = [&](auto qdq, auto fine) { gate_fwd_kernel<T, LANES, CH, decltype(qdq)::value, decltype(fine)::value><<<grid, threads, 0, s>>>(p); };
+            // (h of FP32 rows is not rounded: there only codes ask for every operation as the formula has it)
+            const bool rounded = sizeof(T) == 2 && c.pre && (c.post || c.gate);
             auto coded = [&](auto qdq) {
-                if (sizeof(T) == 4 || (c.pre && (c.post || c.gate))) launch(qdq, std::true_type{});
-                else if constexpr (sizeof(T) == 2) launch(qdq, std::false_type{});
+                if constexpr (sizeof(T) == 4) launch(qdq, std::bool_constant<decltype(qdq)::value != LA_QDQ_NONE>{});
+                else if (rounded) launch(qdq, std::true_type{});
+                else launch(qdq, std::false_type{});
             };
             switch (c.qdq) {
                 case LA_QDQ_INT8_GROUP: coded(std::integral_constant<int, LA_QDQ_INT8_GROUP>{}); break;
                 case LA_QDQ_E4M3_TILE: coded(std::integral_constant<int, LA_QDQ_E4M3_TILE>{}); break;
-                default: launch(std::integral_constant<int, LA_QDQ_NONE>{}, std::false_type{});
+                default: coded(std::integral_constant<int, LA_QDQ_NONE>{});
             }
             return hipGetLastError();
         });

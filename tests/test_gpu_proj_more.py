@@ -189,3 +189,25 @@ def test_codes_beside_the_residual_norm_s(t, codec):
     assert (np.abs(k1 - k2)[off] <= 2.0001 * np.broadcast_to(step, q.shape)[off]).all()
     assert (np.abs(np.abs(k1 - q) - np.abs(k2 - q))[off] <= 2 * 2.0 ** -16 * np.abs(q)[off]).all()
     assert off.mean() <= 2.0 ** -16 * top * 4
+
+
+@pytest.mark.parametrize("d,head", [(64, 16), (512, 64), (520, 0), (2048, 128), (4096, 0), (16384, 0)])
+def test_h_without_codes_is_rounded_stepwise(d, head):
+    """As in front of codes: with squares whose sums are exact in any order, h is the formula's in FP32, operation by
+    operation, and h of any values is the same with codes and without."""
+    rows, g = 65, gen(7)
+    x = (torch.exp2(torch.randint(-2, 3, (rows, d), generator=g).float()) * (torch.randint(0, 2, (rows, d), generator=g) * 2 - 1)).cuda().to(BF)
+    w, al, res = draw(g, head or d, dtype=F32), draw(g, d, dtype=F32), draw(g, rows, d)
+    h = torch.empty_like(x)
+    cfg = la.GateNormConfig(rows=rows, d=d, head=head, eps=2.0 ** -6, pre=1)
+    la.la_gate_norm_fwd(cfg, x, None, w, al, res, None, h, None)
+    f = x.float().cpu().unflatten(-1, (-1, head or d))
+    rms = ((f.double() ** 2).mean(-1, keepdim=True).float() + 2.0 ** -6).double().sqrt().float()
+    p = ((f / rms) * w.cpu()).flatten(-2)
+    assert torch.equal(h.cpu(), (res.float().cpu() + al.cpu() * p).to(BF))
+    x, z, hs = draw(g, 4096, d), draw(g, 4096, d), []
+    for qdq in (0, la.LA_QDQ_INT8_GROUP):
+        hs.append(torch.empty_like(x))
+        cfg = la.GateNormConfig(rows=4096, d=d, head=head, gate=la.LA_GATE_SILU, pre=1, qdq=qdq)
+        la.la_gate_norm_fwd(cfg, x, z, w, al, None, None, hs[-1], None)
+    assert torch.equal(*hs)
