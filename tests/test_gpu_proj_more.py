@@ -8,7 +8,7 @@ import torch
 
 import quantized_state_qat_amd as la
 from tests import proj_ref as R
-from tests.test_gpu_proj import BF, CODE, F32, close, codes, draw, gen, np64, wider
+from tests.test_gpu_proj import BF, CODE, F32, close, codes, draw, gen, np64, two_norm, wider
 
 pytestmark = pytest.mark.gpu
 
@@ -211,3 +211,61 @@ def test_h_without_codes_is_rounded_stepwise(d, head):
         cfg = la.GateNormConfig(rows=4096, d=d, head=head, gate=la.LA_GATE_SILU, pre=1, qdq=qdq)
         la.la_gate_norm_fwd(cfg, x, z, w, al, None, None, hs[-1], None)
     assert torch.equal(*hs)
+
+
+# The backward's workgroups walk rows a grid apart: 256 x 1 to 256 x 3 workgroups of a row, or of 4 to 32 rows up
+# to 512 columns.  Each case has two whole rounds of them and a part of a third.
+# type, rows, d, head, gate, first, post, pre, residual
+WALKS = [
+    (F32, 36001, 64, 16, 2, 0, 1, 1, 1),
+    (BF, 52000, 64, 0, 1, 0, 1, 0, 0),
+    (F32, 26003, 128, 128, 0, 0, 1, 1, 1),
+    (BF, 9001, 256, 256, 1, 1, 1, 1, 0),
+    (F32, 4500, 512, 64, 1, 0, 1, 1, 1),
+    (F32, 6200, 512, 0, 0, 0, 0, 1, 1),
+    (BF, 3500, 1024, 0, 0, 0, 1, 1, 1),
+    (F32, 1300, 1152, 0, 1, 1, 1, 1, 1),
+    (BF, 1700, 2048, 128, 2, 0, 1, 0, 0),
+    (F32, 1701, 2048, 0, 0, 0, 0, 1, 1),
+    (F32, 1100, 2048, 0, 1, 0, 1, 1, 1),
+    (BF, 1100, 2304, 0, 0, 0, 1, 0, 1),
+    (F32, 600, 4096, 32, 1, 0, 1, 1, 0),
+    (BF, 600, 8192, 512, 1, 1, 1, 1, 1),
+    (F32, 600, 8192, 0, 2, 0, 1, 1, 1),
+    (F32, 530, 10240, 0, 0, 0, 1, 1, 1),
+    (BF, 530, 16384, 64, 1, 0, 1, 1, 1),
+]
+
+
+@pytest.mark.parametrize("k", range(len(WALKS)))
+def test_gate_norm_bwd_of_many_rows_a_workgroup(k):
+    """Every row and the parameters' sums against 64 bits.  Tolerances as in test_gpu_proj.py; a lane's share of a
+    sum is three rows, and up to 32 of them are joined in double."""
+    t, rows, d, head, act, first, post, pre, res = WALKS[k]
+    g = gen(700 + k)
+    s = dict(x=draw(g, rows, d, dtype=t), z=draw(g, rows, d, dtype=t) if act else None,
+             w_post=draw(g, head or d, dtype=F32, scale=0.2) + 1 if post else None, alpha=draw(g, d, dtype=F32, scale=0.5),
+             residual=draw(g, rows, d, dtype=t, scale=2.0) if res else None, w_pre=draw(g, d, dtype=F32, scale=0.2) + 1 if pre else None)
+    dy, dh = draw(g, rows, d, dtype=t), draw(g, rows, d, dtype=t) if res else None
+    cfg = la.GateNormConfig(rows=rows, d=d, head=head, eps=1e-5, gate=act, gate_first=first, post=post, pre=pre, x_dtype=CODE[t], out_dtype=CODE[t])
+    h, out = gate_gradients(cfg, s, dy, dh, t)
+    sums = {n: np.zeros(out[n].numel()) for n in ("dw_post", "dalpha", "dw_pre") if out[n] is not None}
+    mags = {n: np.zeros_like(v) for n, v in sums.items()}
+    step = max(1, (1 << 22) // d)
+    for a in range(0, rows, step):
+        cut = slice(a, a + step)
+        part = {n: None if v is None else np64(v[cut] if n in ("x", "z", "residual") else v) for n, v in s.items()}
+        keep = R.gate_norm_fwd(*part.values(), head, 1e-5, act, first, post, pre, np64(h[cut]) if pre else None)[2]
+        args = (part["x"], keep, np64(dy[cut]), None if dh is None else np64(dh[cut]), first, post, pre)
+        want, mag = R.gate_norm_bwd(*args), R.gate_norm_bwd(*args, mag=True)
+        for name, w, m in zip(out, want, mag):
+            if name in sums:
+                sums[name] += w
+                mags[name] += m
+            elif out[name] is not None:
+                close(out[name][cut], w, m, 2.0 ** -15, name)
+                two_norm(out[name][cut], w, 2.0 ** -20 * max(1.0, np.linalg.norm(m) / np.linalg.norm(w)), name)
+    for name, w in sums.items():
+        close(out[name], w, mags[name], 2.0 ** -15, name)
+        # (independent errors of many rows: their share of a sum shrinks with the root of its terms)
+        assert np.linalg.norm(np64(out[name]) - w) <= 2.0 ** -20 * np.linalg.norm(mags[name]), name
