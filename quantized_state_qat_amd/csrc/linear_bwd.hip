@@ -138,7 +138,7 @@ __global__ __launch_bounds__(256) void stats_kernel(DyArgs a) {
 }
 
 // A part is 64 elements = 128 bytes of the summed index; a row holds chunk c's parts beside each other.
-constexpr int kShift = 1, kParts = 1 << kShift;  // of dy times the scale
+constexpr int kParts = 1 << kShift;  // of dy times the scale
 __device__ __forceinline__ int64_t part_at(int chunk, int part, int parts) { return (static_cast<int64_t>(chunk) * parts + part) * 128; }
 
 // Eight scaled values as FP16 in two parts.  The second is what the first leaves, which an infinity
@@ -330,11 +330,8 @@ Layout layout(const la_linear_config& c) {
     l.rowmax = take(4 * M), l.colmax = take(4 * N), l.part = take(4 * mc * N);
     l.qx = take(M * nc * 128 * kParts), l.qw = take(N * mc * 128 * kParts);
     l.pw = take(K * nc * 128), l.px = take(K * mc * 128);
-    const auto most = [](size_t n) { return n <= (size_t{1} << 30) ? 16 : 1; };  // (the join's grid)
-    const int steps_x = gemm_steps(nc * 128, kShift), steps_w = gemm_steps(mc * 128, kShift);
-    l.dx = cut_product(c.K, c.M, steps_x, most(M * K));
-    l.dw = cut_product(c.K, c.N, steps_w, most(N * K));
-    l.pair = cut_pair(c.K, c.M, steps_x, l.dx, c.K, c.N, steps_w, l.dw);
+    const GradientCuts cuts = cut_gradients(c.M, c.N, c.K);
+    l.dx = cuts.dx, l.dw = cuts.dw, l.pair = cuts.pair;
     l.sums_x = take(l.dx.parts > 1 ? l.dx.parts * M * K * 4 : 0);
     l.sums_w = take(l.dw.parts > 1 ? l.dw.parts * N * K * 4 : 0);
     l.end = at;

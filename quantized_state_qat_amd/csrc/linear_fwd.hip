@@ -62,14 +62,9 @@ __global__ __launch_bounds__(512) void skinny_kernel(GemmArgs a) {
     }
 }
 
-// The workgroups of the few tokens' kernel read all tokens' codes for 16 channels, tiles of 64 x 64 for 64.
-// us, that kernel and the tiles: 32 tokens, N = 8192, K = 2048 9.2 and 7.5, N = 2048 5.5 and 7.5, K = 8192
-// 13 and 20; 64 tokens 12 and 7.7, 6.9 and 7.6, 21 and 20.
-int few_tokens(const la_linear_config& c) { return c.N <= 4096 ? (c.K <= 4096 ? 64 : 32) : 16; }
-
 template <class O>
 hipError_t launch(const la_linear_config& c, GemmArgs& g, hipStream_t s) {
-    if (c.M <= few_tokens(c)) {
+    if (c.M <= few_tokens(c.N, c.K)) {
         const unsigned grid = static_cast<unsigned>((c.N + 15) / 16);
         if (c.M <= 16) skinny_kernel<O, 1><<<grid, 512, 0, s>>>(g);
         else if (c.M <= 32) skinny_kernel<O, 2><<<grid, 512, 0, s>>>(g);
@@ -77,7 +72,7 @@ hipError_t launch(const la_linear_config& c, GemmArgs& g, hipStream_t s) {
         return hipGetLastError();
     }
     g.part_steps = gemm_steps(g.kbytes, 0);
-    return launch_gemm<int8_t, false>(g, cut_product(c.N, c.M, g.part_steps, 1).tiling, s);
+    return launch_gemm<int8_t, false>(g, cut_forward(c.M, c.N, c.K).tiling, s);
 }
 
 }  // namespace

@@ -8,6 +8,7 @@ import torch
 
 import quantized_state_qat_amd as la
 from tests import proj_ref as R
+from tests.proj_tiles import FORWARD, GRADIENTS
 from tests.test_gpu_proj import BF, CODE, F32, close, codes, draw, gen, np64, two_norm, wider
 
 pytestmark = pytest.mark.gpu
@@ -78,6 +79,48 @@ def test_gradients_of_empty_sums_look_at_no_operand(tx, tw):
         cfg = la.LinearConfig(M=M, N=N, K=K, x_dtype=CODE[tx], dw_dtype=CODE[tw])
         la.la_linear_bwd(cfg, None, None, None, None, None, *[v if v.numel() else spare.data_ptr() for v in out], None, 0)
         assert all((v == 0).all() for v in out) and (spare == 7.0).all()
+
+
+# Every way of cutting the products (proj_tiles.py says which shape takes which), on operands without a zero block.
+@pytest.mark.parametrize("M,N,K", [c[:3] for c in FORWARD])
+@pytest.mark.parametrize("t", [BF, F32])
+def test_forward_of_every_tiling(M, N, K, t):
+    """Bit for bit: the sum is exact, its conversion, two products and an addition are rounded as written."""
+    g = gen(M + N + K)
+    (xc, xs), (wc, ws) = codes(g, M, K), codes(g, N, K)
+    bias = draw(g, N, dtype=F32)
+    whole, y = wider(g, M, N, 3, t, fill=7.0)
+    la.la_linear_fwd(la.LinearConfig(M=M, N=N, K=K, out_dtype=CODE[t], ld_y=N + 3), xc, xs, wc, ws, bias, y)
+    exact = torch.mm(xc.double(), wc.double().t().contiguous())
+    assert torch.equal(y, (exact.float() * xs[:, None] * ws + bias).to(t))
+    assert (whole[:, N:] == 7.0).all()
+    tight = torch.full((M, N), float("nan"), dtype=t, device="cuda")
+    la.la_linear_fwd(la.LinearConfig(M=M, N=N, K=K, out_dtype=CODE[t]), xc, xs, wc, ws, None, tight)
+    assert torch.equal(tight, (exact.float() * xs[:, None] * ws).to(t))
+
+
+@pytest.mark.parametrize("M,N,K,dx,dw", [c[:5] for c in GRADIENTS])
+@pytest.mark.parametrize("t", [BF, F32])
+def test_gradients_of_every_tiling(M, N, K, dx, dw, t):
+    """Against 64-bit products on the GPU.  Beside each element's bound the 2-norm of what a result is off by: operands 2^-22 + 2^-23,
+    a part's sum of n terms is n / 8 additions (16 products each, of two parts), each off by 2^-23 of a partial sum that grows
+    to the result, its own rounding (2^-24, or 2^-9 on average for bf16)."""
+    g = gen(M + N + K)
+    (xc, xs), (wc, ws) = codes(g, M, K), codes(g, N, K)
+    dy = draw(g, M, N, dtype=t) * torch.exp2(torch.randint(-8, 9, (M, 1), generator=g).float()).cuda().to(t)
+    cfg = la.LinearConfig(M=M, N=N, K=K, x_dtype=CODE[t], out_dtype=CODE[t], dw_dtype=CODE[t])
+    got = gradients(cfg, xc, xs, wc, ws, dy, t, t)
+    d, x, w = dy.double(), xc.double() * xs.double()[:, None], wc.double() * ws.double()[:, None]
+    half = 2.0 ** -8 if t is BF else 2.0 ** -24
+    for name, o, a, b, n, parts in (("dx", got[0], d, w, N, dx[1]), ("dweight", got[1], d.t().contiguous(), x, M, dw[1])):
+        want, mag = torch.mm(a, b), torch.mm(a.abs(), b.abs())
+        off = (o.double() - want).abs()
+        assert (off <= half * 1.01 * want.abs() + (2.0 ** -22 + 2.0 ** -23 + n * 2.0 ** -23) * mag).all(), name
+        bound = 2.0 ** -22 + 2.0 ** -23 + n / parts / 8 * 2.0 ** -23 + half / 2
+        assert off.norm() <= bound * want.norm(), (name, float(off.norm() / want.norm()), bound)
+    # dbias: at most 64 terms in FP32, the rest in double
+    off = (got[2].double() - d.sum(0)).abs()
+    assert (off <= 2.0 ** -24 * d.sum(0).abs() + 64 * 2.0 ** -24 * d.abs().sum(0)).all()
 
 
 # ---------------------------------------------------------------------- norms around a block
