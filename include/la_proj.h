@@ -115,9 +115,8 @@ la_status la_gate_norm_fwd(const la_gate_norm_config* cfg, const void* x, const 
 /* Gradients for the upstream gradients dy (of y; identity straight through the codec and h's rounding)
  * and dh (of h; NULL = zero), from x, z and, with pre, the forward's h (else it may be NULL): dx; dz (with a
  * gate; may be NULL); dres (may be NULL; may be dh itself); dw_post float [head or d] (post), dalpha float
- * [d], dw_pre float [d] (pre), each may be NULL, summed in FP32 over a workgroup's rows and in double over
- * workgroups and heads.  Workspace: at least la_gate_norm_bwd_workspace_bytes(cfg) bytes (needed for
- * these three). */
+ * [d], dw_pre float [d] (pre), each may be NULL, summed in FP32 over at most 128 rows and beyond in double.
+ * Workspace: at least la_gate_norm_bwd_workspace_bytes(cfg) bytes (needed for these three). */
 la_status la_gate_norm_bwd(const la_gate_norm_config* cfg, const void* x, const void* z, const void* w_post, const void* alpha,
                            const void* h, const void* w_pre, const void* dy, const void* dh, void* dx, void* dz,
                            void* dres, float* dw_post, float* dalpha, float* dw_pre, void* workspace, size_t ws_bytes,

@@ -7,8 +7,8 @@
 //     dw_post = sum G u r1,    G <- r1 (G w_post - u r1^2 mean(G w_post u))
 //     dz      = G x act'(z),   G <- G act(z)                     (gate first)
 //     dx      = G,             dw_pre = sum dy h r2.
-// A workgroup walks rows a grid apart; the parameters' partial sums stay in registers (FP32, over its
-// rows), are joined in double over the workgroup's rows in LDS and over workgroups by a second kernel.
+// A workgroup walks up to 128 rows a grid apart; the parameters' partial sums stay in registers (FP32, over its
+// rows), are joined in double over the workgroup's groups of lanes in LDS and over workgroups by a second kernel.
 #include "la_gate.hpp"
 
 namespace la {
@@ -350,10 +350,14 @@ hipError_t by_mode(const la_gate_norm_config& c, F&& f) {
     return gate(integral_constant<GateAt, kGateFirst>{});
 }
 
+// A workgroup walks at most this many rows (each of its groups of lanes): what their FP32 sums may lose.
+constexpr int kWalk = 128;
+
+// Workgroups: all that are resident, or whole rounds of those where they would walk further.
 int bwd_groups(const la_gate_norm_config& c) {
     const int lanes = bwd_lanes(c.d), rpw = lanes <= 64 ? 256 / lanes : 1;
     const int need = (c.rows + rpw - 1) / rpw, most = 256 * groups_for(lanes, c.gate != LA_GATE_NONE && c.pre);
-    return need < most ? need : most;
+    return need < most ? need : (need + most * kWalk - 1) / (most * kWalk) * most;
 }
 
 // The parameters' sums over the workgroups, in double and in a fixed order: 32 columns a workgroup, 32

@@ -312,3 +312,18 @@ def test_gate_norm_bwd_of_many_rows_a_workgroup(k):
         close(out[name], w, mags[name], 2.0 ** -15, name)
         # (independent errors of many rows: their share of a sum shrinks with the root of its terms)
         assert np.linalg.norm(np64(out[name]) - w) <= 2.0 ** -20 * np.linalg.norm(mags[name]), name
+
+
+def test_parameter_sums_over_many_rows_are_not_all_fp32():
+    """Behind 2^24 in the first rows, ones are lost in FP32 sums: of at most 128 rows, 2^-17 of the sum."""
+    rows, d = 1 << 16, 8192
+    x = torch.ones(rows, d, dtype=BF, device="cuda")
+    dy = torch.ones(rows, d, dtype=BF, device="cuda")
+    dy[:256] = 2.0 ** 24
+    cfg = la.GateNormConfig(rows=rows, d=d, post=0)
+    n = la.la_gate_norm_bwd_workspace_bytes(cfg)
+    dalpha = torch.empty(d, device="cuda")
+    la.la_gate_norm_bwd(cfg, x, None, None, None, None, None, dy, None, torch.empty_like(x), None, None, None, dalpha, None,
+                        torch.empty(n, dtype=torch.uint8, device="cuda"), n)
+    want = 256 * 2.0 ** 24 + rows - 256
+    assert ((dalpha.double() - want).abs() <= (2.0 ** -17 + 2.0 ** -24) * want).all()

@@ -151,6 +151,17 @@ def test_linear_backward_refuses_grids():
     assert la.la_linear_bwd_workspace_bytes(linear(M=1 << 19, N=(1 << 16) - 64, K=65536)) > 0
 
 
+@pytest.mark.parametrize("d,rpw", [(8, 32), (64, 32), (128, 16), (256, 8), (512, 4), (520, 1), (2048, 1), (4096, 1), (16384, 1)])
+@pytest.mark.parametrize("kw", [dict(), dict(gate=0), dict(pre=0)])
+def test_gate_norm_backward_sums_128_rows_at_most(d, rpw, kw):
+    """The workspace has three rows of sums a workgroup, which walks rows of its own that many at a time."""
+    for rows in (1, 77, 5000, 32768, 1 << 20, (1 << 23) + 5):
+        groups = la.la_gate_norm_bwd_workspace_bytes(gate(rows=rows, d=d, **kw)) / (12 * d)
+        assert groups == int(groups) and groups * rpw * 128 >= rows
+        assert groups * rpw < rows + rpw  # none without rows
+        assert groups * rpw * 64 < rows or groups <= 1536  # (several rounds of resident workgroups are of more rows than half of that)
+
+
 def test_gate_norm_refuses_pointers():
     for p in FWD:
         refused(lambda: gate_fwd(gate(qdq=1), **{p: FAKE + 8}), la.LA_ERR_ALIGNMENT, "aligned")
