@@ -52,7 +52,7 @@ __device__ __forceinline__ void gate_both(float z, int gate, float& g, float& sl
         slope = z < -89.0f ? 0.0f : s * (1.0f + z * (1.0f - s));
     } else {
         g = s;
-        slope = s * (1.0f - s);
+        slope = s * sigmoid_for<T>(-z);  // (1 - s keeps 24 - 1.44 z bits of what is left at large z)
     }
 }
 

@@ -327,3 +327,25 @@ def test_parameter_sums_over_many_rows_are_not_all_fp32():
                         torch.empty(n, dtype=torch.uint8, device="cuda"), n)
     want = 256 * 2.0 ** 24 + rows - 256
     assert ((dalpha.double() - want).abs() <= (2.0 ** -17 + 2.0 ** -24) * want).all()
+
+
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("act", [1, 2])
+@pytest.mark.parametrize("first", [0, 1])
+def test_gates_far_from_zero(t, act, first):
+    """The gate's derivative keeps its bits where the gate is all but open or shut: dz within 2^-15 of the magnitude as
+    near zero, z over -60 to 60."""
+    rows, d, g = 64, 512, gen(8)
+    s = dict(x=draw(g, rows, d, dtype=t), z=torch.linspace(-60, 60, rows * d, device="cuda")[torch.randperm(rows * d, generator=g).cuda()].view(rows, d).to(t),
+             w_post=None, alpha=None, residual=None, w_pre=None)
+    dy = draw(g, rows, d, dtype=t)
+    cfg = la.GateNormConfig(rows=rows, d=d, eps=1e-5, gate=act, gate_first=first, post=0, x_dtype=CODE[t], out_dtype=CODE[t])
+    out = gate_gradients(cfg, s, dy, None, t)[1]
+    keep = R.gate_norm_fwd(np64(s["x"]), np64(s["z"]), None, None, None, None, 0, 1e-5, act, first, 0, 0)[2]
+    if act == 2:  # (64 bits lose 1 - s too, from z = 37 on all of it: the same by both sigmoids)
+        z = np64(s["z"])
+        keep["slope"] = keep["terms"] = 1 / (1 + np.exp(-z)) / (1 + np.exp(z))
+    args = (np64(s["x"]), keep, np64(dy), None, first, 0, 0)
+    want, mag = R.gate_norm_bwd(*args), R.gate_norm_bwd(*args, mag=True)
+    for name, w, m in zip(("dx", "dz"), want, mag):
+        close(out[name], w, m, 2.0 ** -15, name)
