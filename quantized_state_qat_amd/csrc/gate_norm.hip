@@ -4,8 +4,8 @@
 //     v = h / rms(h) * w_pre  or t,     and 8-bit codes of v,
 // Memory bound: one pass over the data, a row in the registers of 8 to 384 lanes between its loads, its
 // two norms and its outputs.  A head of 16 to 512 columns is 2 to 64 neighbouring lanes, whose sum needs no
-// LDS.  bf16 to INT8 codes and their values: 40686 rows of 32 heads of 128 with silu 215 us (5.4 TB/s), the join of
-// 40686 x 2048 157 us (4.8 TB/s): by the vector units as much as by memory; 32768 x 2048 without codes 72 and 85 us; 4 rows
+// LDS.  bf16 to INT8 codes and their values: 40686 rows of 32 heads of 128 with silu 206 us (5.6 TB/s), the join of
+// 40686 x 2048 154 us (4.9 TB/s): by the vector units as much as by memory; 32768 x 2048 without codes 72 and 85 us; 4 rows
 // of 2048 3.5 us, latencies.
 #include "la_gate.hpp"
 
@@ -46,9 +46,9 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void gate_fwd_kernel(Gat
     // What codes are formed from does not depend on y's type or on whether y is wanted.  Of FP32 rows every
     // operation is rounded as the formula has it and squares are summed in double, as in the residual norm
     // (STEPWISE); of bf16 rows (whose own rounding is 2^-8) sums are FP32, norms by the reciprocal root and the gate
-    // within (|z| + 2) 2^-23 (40686 x 4096 with 32 heads of 128 and silu: 289 us stepwise, 215 so).  Codes are those of
+    // within (|z| + 2) 2^-23 (40686 x 4096 with 32 heads of 128 and silu: 289 us stepwise, 206 so).  Codes are those of
     // the correctly rounded quotient in both (by the product with the scale's reciprocal, which may take a near tie
-    // to the other side, bf16 rows took 200 us, and the join of 40686 x 2048 150 for 157).  Where h is
+    // to the other side, bf16 rows took 200 us, and the join of 40686 x 2048 150 for 154).  Where h is
     // rounded before the next norm, what leads to it is rounded stepwise too and a row's sum joined in double
     // (FINE), with codes and without: a last bit there moves h by 2^-8 of itself where it falls on a tie, and with a
     // row's largest element its scale (40686 x 2048: 530 of 83 million elements differ from the formula so rounded

@@ -164,30 +164,46 @@ __device__ __forceinline__ void emit_codes(const CodeOut& o, int l, int row, siz
         uint32_t word[2] = {0, 0};
         // a NaN in the group: its maximum, its scale and every value that its codes stand for
         const bool none = amax[c] != amax[c];
-        if constexpr (QDQ == LA_QDQ_INT8_GROUP) {
-            bool fast = int8_scale_recip(amax[c], s, y);
-            if (none) s = amax[c], fast = false;
+        bool fast = QDQ == LA_QDQ_INT8_GROUP ? int8_scale_recip(amax[c], s, y) : e4m3_scale_recip(amax[c], s, y);
+        if (none) s = amax[c], fast = false;
+        if (fast) {  // numbers, whose quotients no code's range leaves
+            if constexpr (QDQ == LA_QDQ_INT8_GROUP) {
+                uint32_t q[8];
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                float q = fast ? int8_code_fast(h[c][e], s, y) : rintf(h[c][e] / s);
-                const bool number = q == q;  // (of a quotient without one: code 0)
-                if (!fast && number) q = fminf(fmaxf(q, -127.0f), 127.0f);
-                word[e >> 2] |= (number ? static_cast<uint32_t>(static_cast<int>(q)) & 0xFFu : 0u) << (8 * (e & 3));
-                h[c][e] = q * s;
+                for (int e = 0; e < 8; e++) {
+                    const float r = int8_code_fast(h[c][e], s, y);
+                    q[e] = __float_as_uint(r + 12582912.0f);  // (1.5 x 2^23: the integer in the low byte)
+                    h[c][e] = r * s;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; k++)
+                    word[k] = __builtin_amdgcn_perm(q[4 * k + 1], q[4 * k], 0x0c0c0400u) | __builtin_amdgcn_perm(q[4 * k + 3], q[4 * k + 2], 0x04000c0cu);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float a = fminf(fmaxf(quot_rn_fast(h[c][e], s, y), -448.0f), 448.0f);
+                    const float b = fminf(fmaxf(quot_rn_fast(h[c][e + 1], s, y), -448.0f), 448.0f);
+                    const uint32_t k = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false)) & 0xFFFFu;
+                    word[e >> 2] |= k << (8 * (e & 3));
+                    h[c][e] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(k), 0) * s;
+                    h[c][e + 1] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(k), 1) * s;
+                }
             }
         } else {
-            bool fast = e4m3_scale_recip(amax[c], s, y);
-            if (none) s = amax[c], fast = false;
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                float a = fast ? quot_rn_fast(h[c][e], s, y) : h[c][e] / s;
-                float b = fast ? quot_rn_fast(h[c][e + 1], s, y) : h[c][e + 1] / s;
-                a = a != a ? a : fminf(fmaxf(a, -448.0f), 448.0f);
-                b = b != b ? b : fminf(fmaxf(b, -448.0f), 448.0f);
-                const uint32_t k = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false)) & 0xFFFFu;
-                word[e >> 2] |= k << (8 * (e & 3));
-                h[c][e] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(k), 0) * s;
-                h[c][e + 1] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(k), 1) * s;
+            for (int e = 0; e < 8; e++) {
+                const float x = h[c][e] / s;
+                const bool number = x == x;  // (of a quotient without one: code 0, or E4M3's NaN)
+                if constexpr (QDQ == LA_QDQ_INT8_GROUP) {
+                    const float q = number ? fminf(fmaxf(rintf(x), -127.0f), 127.0f) : x;
+                    word[e >> 2] |= (number ? static_cast<uint32_t>(static_cast<int>(q)) & 0xFFu : 0u) << (8 * (e & 3));
+                    h[c][e] = q * s;
+                } else {
+                    const float a = number ? fminf(fmaxf(x, -448.0f), 448.0f) : x;
+                    const uint32_t k = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(a, a, 0, false)) & 0xFFu;
+                    word[e >> 2] |= k << (8 * (e & 3));
+                    h[c][e] = __builtin_amdgcn_cvt_f32_fp8(static_cast<int>(k), 0) * s;
+                }
             }
         }
         if (o.codes) *reinterpret_cast<uv2*>(o.codes + base + col) = uv2{word[0], word[1]};
