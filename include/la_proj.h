@@ -41,7 +41,7 @@ typedef struct la_linear_config {
     int32_t out_dtype;  /* la_dtype of y and dy */
     int32_t w_dtype;    /* la_dtype of bias (its gradient is float32) */
     int32_t dw_dtype;   /* la_dtype of dweight */
-    int32_t ld_x;       /* row stride of x_codes, a multiple of 16 (0 = K) */
+    int32_t ld_x;       /* row stride of x_codes, a multiple of 16 up to 2^22 (0 = K) */
     int32_t ld_y;       /* row stride of y and dy, any value >= N (0 = N) */
 } la_linear_config;
 
@@ -56,11 +56,12 @@ la_status la_linear_fwd(const la_linear_config* cfg, const void* x_codes, const 
  * each may be NULL.  dy times the scales enters as two FP16 parts of 11 bits (off by at most 2^-22 of the
  * value, whatever the gradient's type) under a power of two for its row (for dweight its column): of values
  * below 2^-17 of the row's largest magnitude up to 2^-39 of that magnitude is lost.
- * dy times a scale is formed in FP32, and must not overflow it.
- * The codes enter exactly.  Sums are FP32, those of a sum's parts joined in double in a fixed order; dbias is
- * summed in double over FP32 sums of 64 rows.  M and N up to 2^19, with below 2^23 tiles of 64 x 64.
- * Workspace: at least la_linear_bwd_workspace_bytes(cfg) bytes (operands laid out for the products); a query
- * returns 0 where there is nothing to sum and where the call would be refused. */
+ * dy times a scale is formed in FP32, and must not overflow it.  The codes enter exactly.  Sums are
+ * FP32, those of a sum's parts joined in double in a fixed order; dbias is summed in double over FP32 sums of
+ * 64 rows.  M and N up to 2^19, with below 2^23 tiles of 64 x 64.  Workspace: at least
+ * la_linear_bwd_workspace_bytes(cfg) bytes (operands laid out for both products, whichever gradients are wanted:
+ * each is the same, bit for bit, alone and with the others); a query returns 0 where there is nothing to sum
+ * and where the call would be refused. */
 la_status la_linear_bwd(const la_linear_config* cfg, const void* x_codes, const float* x_scales, const void* w_codes,
                         const float* w_scales, const void* dy, void* dx, void* dweight, float* dbias, void* workspace,
                         size_t ws_bytes, void* stream);

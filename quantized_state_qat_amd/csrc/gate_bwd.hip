@@ -66,13 +66,15 @@ enum GateAt { kNoGate, kGateLast, kGateFirst };
 // Waves a SIMD that a kernel's registers leave room for, and workgroups a CU by them: all that a launch has are
 // resident.  32768 x 2048 bf16, forward and backward: three 291 us (row norms) and 228 (head norms and
 // gate), two 318 and 243, four, which spill, 426 and 296; gate and both norms: two 332 us, three, which
-// spill, 452.
+// spill, 452.  Some spill all the same: gate and both norms of up to 64 columns (80 registers, with 32 groups of
+// lanes to join) and of 4097 to 8192 (6 with the gate last, 46 to 49 first); beyond 8192 columns all do (42 to 224).
 constexpr int waves_for(int lanes, bool full) { return lanes <= 384 ? (full ? 2 : 3) : lanes == 512 ? 2 : 4; }  // full: gate and both norms
 constexpr int groups_for(int lanes, bool full) { return lanes <= 64 ? waves_for(lanes, full) : 4 * waves_for(lanes, full) / (lanes / 64); }
 
 // The loads of a workgroup's next row run under the sums of the one before: a row is five loads wide and
-// two barriers long.  32768 x 2048 bf16: row norms and residual 160 us (5.1 TB/s), head norms and gate 120 us
-// (5.5 TB/s): memory bound.
+// two barriers long.  32768 x 2048 bf16: row norms and residual 160 us (5.1 TB/s), head norms and gate 130 us
+// (5.1 TB/s): memory bound.  Wide rows, both norms without a gate, with all they write: 8192 rows of 6144 171 us
+// and of 8192 190, 4096 rows of 16384 680.
 template <class T, int LANES, int CH, GateAt GATE, bool PRE>
 __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES, waves_for(LANES, GATE != kNoGate && PRE)) void gate_bwd_kernel(GateBwd p) {
     constexpr int THREADS = LANES <= 64 ? 256 : LANES, RPW = THREADS / LANES, WAVES = THREADS / 64, CODE = Io<T>::kCode;

@@ -7,9 +7,9 @@
 // The products sum over an index that is not contiguous in what the caller holds (channels of dx,
 // tokens of dweight), so a pass over dy and one over each matrix of codes lay the operands out first,
 // 128 bytes of the summed index at a time: they move 2 to 8 bytes an element once where the product
-// itself reads an operand many times over.  32768 x 2048 x 2048 from bf16 dy to bf16 dx and FP32 dweight 930 us:
-// 40 + 94 + 39 laying out (3.3 to 5.7 TB/s: memory bound), 250 + 460 the products (1100 to 1190 TFLOP/s: power bound),
-// 14 joining dweight's four parts.
+// itself reads an operand many times over.  32768 x 2048 x 2048 from bf16 dy to bf16 dx and FP32 dweight 1145 to
+// 1160 us: 41 + 41 + 112 laying out (3.5 to 6.0 TB/s: memory bound), 500 to 530 and 470 to 510 the products (1040 to
+// 1170 TFLOP/s by the clock that a card's power leaves), 15 joining dweight's four parts.
 #include "linear_gemm.hpp"
 
 namespace la {
@@ -154,8 +154,8 @@ __device__ __forceinline__ void store_parts(char* o, const float (&v)[8]) {
     *reinterpret_cast<hv8*>(o + 128) = lo;
 }
 
-// 64 x 64 of dy into both operands: along the rows from registers, along the columns through LDS (94 us for
-// 32768 x 2048 bf16 into one part and two, 540 MB, 5.7 TB/s).
+// 64 x 64 of dy into both operands: along the rows from registers, along the columns through LDS (110 us for
+// 32768 x 2048 bf16, 678 MB, 6.0 TB/s).
 template <bool FULL, class T>
 __device__ __forceinline__ void lay_dy(const DyArgs& a, int cm, int cn, T (&tile)[64][66]) {
     const int n0 = cn * 64, m0 = cm * 64;
@@ -238,7 +238,8 @@ __global__ __launch_bounds__(256) void lay_dy_kernel(DyArgs a, int bias) {
 }
 
 // Codes [R][C] (rows ld bytes apart, C a multiple of 16) to FP16, C rows of R in chunks of 64: 64 x 64 a
-// workgroup (39 us for 32768 x 2048, 5.4 TB/s; 44 with the halves of a line on two dies).
+// workgroup (36 to 41 us for 32768 x 2048, 5.3 TB/s, a tenth of the
+// cycles in LDS conflicts; 44 with the halves of a line on two dies).
 struct Codes {
     const int8_t* codes;
     int64_t ld;

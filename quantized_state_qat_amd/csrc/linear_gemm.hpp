@@ -197,10 +197,10 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t r, char* lds,
 // once a step's last slice is in registers one barrier frees its LDS for the loads of the step NS further.
 // The order of reads, loads and products is spelled out (the compiler bunches the reads).  A workgroup
 // takes tiles of out in turn, and the loads run on into the next one, under the stores of the one before
-// (32768 x 2048 x 2048 in 8 bits: a launch of all tiles 208 us, this 192, with whole lines stored 142).
-// 256 x 256 tiles are bound by power: 8192^3 in 8 bits 463 us (2370 TOP/s) with the matrix cores 67% busy at
+// (32768 x 2048 x 2048 in 8 bits: a launch of all tiles 208 us, this 192, with whole lines stored 140).
+// 256 x 256 tiles are bound by power: 8192^3 in 8 bits 463 to 473 us (2320 to 2370 TOP/s) with the matrix cores 67% busy at
 // 1.65 GHz, where these instructions alone, from registers, reach 3250 on the same kind of numbers.  64 x 64 ones are
-// bound by LDS traffic and latency: 256 tokens, K = 2048, N = 8192 10 us, the matrix cores 10% busy.
+// bound by LDS traffic and latency: 256 tokens, K = 2048, N = 8192 11 us, the matrix cores 9% busy.
 // Of `blocks` workgroups on product a this is number `block`.  O: out's type, or void (a.out_dtype).
 template <class E, class O, bool BITS, int WI, int WJ, int TI, int TJ, int NS>
 __device__ __forceinline__ void gemm_units(const GemmArgs& a, int block, int blocks) {
